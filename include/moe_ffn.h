@@ -401,7 +401,8 @@ const char *moe_ffn_stage_name(int path, int stage);
 /*
  * Device fault word: bit flags that kernels set when a bounded device-side
  * wait gives up (instead of hanging): bits 0-7 the grouped GEMMs, 8-15 the
- * fused decode kernel, 16-23 the backward pass's weight-gradient GEMMs.
+ * fused decode kernel, 16-23 the backward pass's weight-gradient GEMMs,
+ * 24-31 the orthogonalisation's products (moe_block.h).
  * Reads the current device's word
  * synchronously into *flags and, if clear != 0, resets it.  Returns MOE_OK,
  * or MOE_ERR_CUDA if the read fails.  A non-zero word means some call since

@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         unsigned long long tag_cap, unsigned long long *__restrict__ flags,
                         unsigned long long epoch_salt, int32_t *__restrict__ idx_out, float *__restrict__ w_out,
                         float *__restrict__ out, int32_t *__restrict__ exchange_out, uint64_t wait_ns,
-                        int mode, RouterArgs ra, MxArgs mx)
+                        int mode, RouterArgs ra, MxArgs mx, Routing rt)
 {
     static_assert(!(ROUTER && MX), "the router projection is built for BF16 weights only");
     extern __shared__ __align__(128) uint8_t sm[];
@@ -597,7 +597,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The tokens' logits and x rows, which every CTA reads first, fetched
     // into L2 while the previous launch drains (whole 16-byte pieces only)
     if ((mode & kPrefetchInputs) && threadIdx.x == 0 && blockIdx.x < 2) {
-        const uint32_t n = blockIdx.x == 0 ? (ROUTER ? 0u : (uint32_t)(T * E * 4) & ~15u) : (uint32_t)(T * H * 2);
+        const uint32_t n = blockIdx.x == 0 ? (ROUTER || rt.idx ? 0u : (uint32_t)(T * E * 4) & ~15u)
+                                           : (uint32_t)(T * H * 2);
         if (n) ptx::bulk_prefetch_l2(blockIdx.x == 0 ? (const void *)logits : (const void *)x, n);
     }
     ptx::griddep_wait();
@@ -691,8 +692,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         int e;
         float wt;
         if (t == 0 && lane == 0) MOE_TL(56);
-        route_token_warp<ROUTER>(logits + (int64_t)t * E, E, k, reinterpret_cast<float *>(sm) + (size_t)t * E, e,
-                                 wt);
+        if (!ROUTER && rt.idx)  // the caller's routing
+            take_routing_warp(rt.idx + (int64_t)t * k, rt.w + (int64_t)t * k, E, k, e, wt);
+        else
+            route_token_warp<ROUTER>(logits + (int64_t)t * E, E, k, reinterpret_cast<float *>(sm) + (size_t)t * E, e,
+                                     wt);
 #ifdef MOE_FUSED_TIMELINE
         if (t == 0 && lane == 0 && wt != -1.0f) MOE_TL(57);
 #endif
@@ -1315,9 +1319,9 @@ cudaError_t launch_decode_fused(const void *x, const float *logits, const void *
                                 unsigned long long tag_cap, unsigned long long *flags, int32_t *idx_out, float *w_out,
                                 float *out, int32_t *exchange_out, unsigned long long wait_ns, int skip_arrival,
                                 const FusedRouter *router, const FusedMx *mxw, bool prefetch_inputs,
-                                cudaStream_t s)
+                                cudaStream_t s, const Routing *routing)
 {
-    if (router && mxw) return cudaErrorInvalidValue;  // no such instantiation
+    if (router && (mxw || routing)) return cudaErrorInvalidValue;  // no such instantiation
     const Plan p = plan_for(T, H, I, k, n_sm, mxw != nullptr);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)n_sm);
@@ -1353,7 +1357,8 @@ cudaError_t launch_decode_fused(const void *x, const float *logits, const void *
     return cudaLaunchKernelEx(&cfg, kern, (const uint16_t *)x, logits, (const uint16_t *)wgu, (const uint16_t *)wd, T,
                               H, I, E, k, p.slots, p.slot_bytes, p.rpc, p.rps, p.nh_max, p.act_in_smem, act, act_tag,
                               tag_cap, flags, epoch_salt(), idx_out, w_out, out, exchange_out, (uint64_t)wait_ns,
-                              (skip_arrival ? kSkipArrival : 0) | (prefetch_inputs ? kPrefetchInputs : 0), ra, ma);
+                              (skip_arrival ? kSkipArrival : 0) | (prefetch_inputs ? kPrefetchInputs : 0), ra, ma,
+                              routing ? *routing : Routing{});
 }
 
 cudaError_t read_decode_fused_fault_word(uint32_t *flags, bool clear)

@@ -424,6 +424,23 @@ __global__ void __launch_bounds__(256) dlogits_kernel(const float *__restrict__ 
     if (lane < k) row[ej] = wj * (dw - S);
 }
 
+// The routing weights' gradient where the caller passed the routing: the
+// same sums, 0 for a dropped slot (whose expert is not the caller's).
+__global__ void __launch_bounds__(256) routed_dw_kernel(const float *__restrict__ dwp, const int32_t *__restrict__ pos,
+                                                        const int32_t *__restrict__ idx_in,
+                                                        const int32_t *__restrict__ idx, int64_t slots, int groups,
+                                                        float *__restrict__ dw)
+{
+    const int64_t a = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (a >= slots) return;
+    float v = 0.0f;
+    if (__ldg(idx_in + a) == __ldg(idx + a)) {
+        const float *p = dwp + (int64_t)__ldg(pos + a) * groups;
+        for (int g = 0; g < groups; ++g) v += __ldg(p + g);
+    }
+    dw[a] = v;
+}
+
 template <int KIND>
 cudaError_t set_wgrad_smem()
 {
@@ -537,6 +554,14 @@ cudaError_t launch_zero_untouched(const int32_t *counts, int E, int H, int I, fl
     zero_untouched_kernel<<<8 * n_sm, 256, 0, s>>>(counts, E, reinterpret_cast<float4 *>(dwgu),
                                                    (int64_t)2 * I * H / 4, reinterpret_cast<float4 *>(dwd),
                                                    (int64_t)H * I / 4);
+    return cudaPeekAtLastError();
+}
+
+cudaError_t launch_routed_dw(const float *dwp, const int32_t *pos, const int32_t *idx_in, const int32_t *idx, int T,
+                             int k, int I, float *dw, cudaStream_t s)
+{
+    const int64_t slots = (int64_t)T * k;
+    routed_dw_kernel<<<(unsigned)ceil_div(slots, 256), 256, 0, s>>>(dwp, pos, idx_in, idx, slots, I / 32, dw);
     return cudaPeekAtLastError();
 }
 

@@ -19,6 +19,12 @@ struct FusedMx {
 // Bytes per scale row for rows of K elements: K / 32 scales padded to 16.
 constexpr int mx_scale_bytes(int K) { return (K / 32 + 15) / 16 * 16; }
 
+// A routing that the caller passes instead of logits: [T, k] each.
+struct Routing {
+    const int32_t *idx;
+    const float *w;
+};
+
 // routing.cu
 cudaError_t routing_init_device();
 // tag_size (nullable): the fused decode kernel's size word in a workspace
@@ -87,6 +93,8 @@ struct FusedRouter {
     unsigned long long *ltag;
     float *logits_out;
 };
+// routing (nullable): the caller's routing instead of logits (then not read);
+// not together with router.
 // mxw (nullable): MXFP8 expert weights (FusedMx) instead of wgu/wd (then
 // not read); not together with router.  prefetch_inputs: fetch x and the
 // logits into L2 while the previous launch drains (device memory only).
@@ -95,7 +103,7 @@ cudaError_t launch_decode_fused(const void *x, const float *logits, const void *
                                 unsigned long long tag_cap, unsigned long long *flags, int32_t *idx_out, float *w_out,
                                 float *out, int32_t *exchange_out, unsigned long long wait_ns, int skip_arrival,
                                 const FusedRouter *router, const FusedMx *mxw, bool prefetch_inputs,
-                                cudaStream_t s);
+                                cudaStream_t s, const Routing *routing = nullptr);
 constexpr unsigned long long kDecodeFusedWaitNs = 2000000000ull;  // default bound of its waits
 
 // moe_ffn_api.cu: an identifier of the calling thread's current CUDA
@@ -175,5 +183,63 @@ cudaError_t launch_zero_untouched(const int32_t *counts, int E, int H, int I, fl
                                   cudaStream_t s);
 cudaError_t launch_dlogits(const float *dwp, const int32_t *pos, const int32_t *idx, const float *w, int T, int E,
                            int k, int I, float *dlogits, cudaStream_t s);
+
+
+// ---------------------------------------------------------------- the operators around the experts
+// moe_ffn_api.cu: the current device's SM count and the pairs of CTAs that
+// the orthogonalisation's products can hold at once, after the per-device
+// set-up; a MOE_* status
+int device_info(int *n_sm, int *pairs);
+
+// rms_norm.cu.  x_f32, res_f32 ...: FP32, else BF16
+constexpr int kNormGradParts = 512;  // most blocks (rows of partial sums) of the gradient
+bool norm_supported(int64_t H);
+int norm_grad_parts(int64_t T);
+cudaError_t launch_norm(const void *x, bool x_f32, const void *residual, bool res_f32, const float *weight, float eps,
+                        int64_t T, int H, void *h_out, void *y, void *codes, void *scales, int n_sm, cudaStream_t s);
+// partial: [norm_grad_parts(T)][H]
+cudaError_t launch_norm_grad(const void *h, bool h_f32, const float *weight, const void *dy, bool dy_f32,
+                             const void *dres, float eps, int64_t T, int H, void *dh, float *dweight, float *partial,
+                             int n_sm, cudaStream_t s);
+
+// gate.cu
+struct GateCall {
+    const float *logits, *bias;  // bias nullable
+    int64_t T;
+    int E, k, groups, topk_groups;
+    bool sigmoid, renorm;
+    float scale;
+    int32_t *idx;
+    float *w;
+    int32_t *counts;  // nullable
+};
+cudaError_t launch_gate(const GateCall &c, int n_sm, cudaStream_t s);
+cudaError_t launch_gate_grad(const float *logits, const int32_t *idx, const float *dw, int64_t T, int E, int k,
+                             bool sigmoid, bool renorm, float scale, float *dlogits, int n_sm, cudaStream_t s);
+
+// routing.cu: the caller's routing as the layer's own (dropped slots
+// replaced, route_block.cuh); tag_size, tag_cap as for launch_router
+cudaError_t launch_take_routing(const int32_t *idx_in, const float *w_in, int T, int E, int k, int32_t *idx, float *w,
+                                unsigned long long *tag_size, unsigned long long tag_cap, cudaStream_t s);
+// MXFP8 rows [T, H] (codes, scales) widened to BF16
+cudaError_t launch_mx_widen(const void *codes, const void *scales, int T, int H, void *x, int n_sm, cudaStream_t s);
+// grouped_bwd.cu: dw [T, k] from the q GEMM's partial sums; 0 where idx_in
+// differs from the routing that ran (a dropped slot)
+cudaError_t launch_routed_dw(const float *dwp, const int32_t *pos, const int32_t *idx_in, const int32_t *idx, int T,
+                             int k, int I, float *dw, cudaStream_t s);
+
+// orthogonalize.cu
+struct OrthoCall {
+    const void *g;
+    bool g_f32;
+    int64_t B, M, N;
+    int steps;
+    float a, b, c, eps, out_scale;
+    void *out;
+};
+cudaError_t ortho_init_device(int *pairs);
+cudaError_t read_ortho_fault_word(uint32_t *flags, bool clear);
+size_t ortho_workspace_bytes(int64_t B, int64_t M, int64_t N);
+cudaError_t launch_orthogonalize(const OrthoCall &c, void *workspace, int pairs, cudaStream_t s);
 
 }  // namespace moe

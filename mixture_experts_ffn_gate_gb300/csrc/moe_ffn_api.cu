@@ -4,6 +4,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "moe_block.h"
 #include "moe_ffn.h"
 
 namespace {
@@ -137,6 +138,7 @@ struct DeviceInfo {
     bool ready = false;
     unsigned long long ctx = 0;
     int n_sm = 0;
+    int pairs = 0;  // pairs of CTAs that the orthogonalisation's products hold at once
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mutex;
@@ -156,6 +158,7 @@ int device_setup(DeviceInfo **info)
         if (moe::decode_fused_init_device() != cudaSuccess) return MOE_ERR_CUDA;
         if (moe::gemm_init_device() != cudaSuccess) return MOE_ERR_CUDA;
         if (moe::bwd_init_device() != cudaSuccess) return MOE_ERR_CUDA;
+        if (moe::ortho_init_device(&d.pairs) != cudaSuccess || d.pairs < 1) return MOE_ERR_CUDA;
         // the attribute calls above created the context if there was none
         d.ctx = moe::current_context_id();
         d.ready = true;
@@ -215,10 +218,12 @@ struct Stages {
 // logits_out, nullable).  mx (nullable): MXFP8 expert weights instead of
 // wgu/wd; such calls take the decode kernels only.  host_inputs: x and the
 // logits are page-locked host memory read in place (not prefetched to L2).
+// routing (nullable): the caller's routing instead of logits.
 int run_forward(const void *x, const float *logits, const void *wgu, const void *wd, const Shape &s, float *out,
                 char *ws, const Layout &L, bool keep_state, int32_t *idx_out, float *w_out, moe_ffn_opts *opts,
                 cudaStream_t stream, const void *wr = nullptr, const float *rbias = nullptr,
-                float *logits_out = nullptr, const moe::FusedMx *mx = nullptr, bool host_inputs = false)
+                float *logits_out = nullptr, const moe::FusedMx *mx = nullptr, bool host_inputs = false,
+                const moe::Routing *routing = nullptr)
 {
     DeviceInfo *dev = nullptr;
     int st = device_setup(&dev);
@@ -265,7 +270,7 @@ int run_forward(const void *x, const float *logits, const void *wgu, const void 
             x, logits, wgu, wd, T, H, I, E, k, dev->n_sm, (float *)(ws + L.act),
             keep_state ? (unsigned long long *)(ws + L.act_tag) : nullptr, L.tag_cap,
             (unsigned long long *)(ws + L.flags), idx_out, w_out, out, opts ? opts->exchange_out : nullptr, wait_ns,
-            opts ? opts->test_skip_arrival : 0, wr ? &fr : nullptr, mx, !host_inputs, stream)));
+            opts ? opts->test_skip_arrival : 0, wr ? &fr : nullptr, mx, !host_inputs, stream, routing)));
         if (opts) {
             opts->n_stages = stg.n;
             opts->path_taken = path;
@@ -279,7 +284,10 @@ int run_forward(const void *x, const float *logits, const void *wgu, const void 
         logits = (const float *)(ws + L.rlog);
         MOE_TRY(moe::launch_router_gemv(x, wr, rbias, T, H, E, (float *)(ws + L.rlog), logits_out, stream));
     }
-    MOE_TRY(stg.done(moe::launch_router(logits, T, E, k, idx, w, idx_out, w_out, tag_size, L.tag_cap, stream)));
+    MOE_TRY(stg.done(routing ? moe::launch_take_routing(routing->idx, routing->w, T, E, k, idx, w, tag_size, L.tag_cap,
+                                                        stream)
+                             : moe::launch_router(logits, T, E, k, idx, w, idx_out, w_out, tag_size, L.tag_cap,
+                                                  stream)));
     if (path == MOE_PATH_DECODE) {
         auto *act = (float *)(ws + L.act);
         MOE_TRY(stg.done(moe::launch_sort(idx, n_assign, E, moe::kGemmChunkMax, offs, perm, pos, uexp, ucount,
@@ -371,9 +379,12 @@ BwdLayout make_bwd_layout(const Shape &s)
 // the workspace from moe_ffn_forward_train (moe_ffn_backward_train).  Both
 // route and sort: everything that indexes memory is this call's own, so a
 // state from another call can give wrong values but no stray access.
+// routing (nullable): the caller's routing instead of logits; dlogits is
+// then dtopk_w [T, k].
 int run_backward(const void *x, const float *logits, const void *wgu, const void *wd, const float *dout,
                  const Shape &s, float *dx, float *dlogits, float *dwgu, float *dwd, char *ws, const BwdLayout &L,
-                 moe_ffn_opts *opts, cudaStream_t stream, bool recompute = true)
+                 moe_ffn_opts *opts, cudaStream_t stream, bool recompute = true,
+                 const moe::Routing *routing = nullptr)
 {
     DeviceInfo *dev = nullptr;
     int st = device_setup(&dev);
@@ -398,7 +409,8 @@ int run_backward(const void *x, const float *logits, const void *wgu, const void
 
     Stages stg{opts ? opts->stage_events : nullptr, stream};
     MOE_TRY(stg.begin());
-    MOE_TRY(stg.done(moe::launch_router(logits, T, E, k, idx, w, nullptr, nullptr, tag_size, 0, stream)));
+    MOE_TRY(stg.done(routing ? moe::launch_take_routing(routing->idx, routing->w, T, E, k, idx, w, tag_size, 0, stream)
+                             : moe::launch_router(logits, T, E, k, idx, w, nullptr, nullptr, tag_size, 0, stream)));
     MOE_TRY(stg.done(moe::launch_sort(idx, T * k, E, moe::kGemmChunkMax, offs, perm, pos, (int32_t *)(ws + L.uexp),
                                       (int32_t *)(ws + L.ucount), chunks, nchunks, stream, 16, counts)));
     MOE_TRY(stg.done(moe::launch_bwd_prep(x, dout, w, perm, offs, rows, E, H, k, ws + L.xs, ws + L.ds_hi,
@@ -417,7 +429,8 @@ int run_backward(const void *x, const float *logits, const void *wgu, const void
                                             rows, H, I, E, dwd, ctas, stream)));
     MOE_TRY(stg.done(moe::launch_wgrad_gate_up(ws + L.dgu_hi, ws + L.dgu_lo, ws + L.xs, offs, counts, rows, H, I, E,
                                                dwgu, ctas, stream)));
-    MOE_TRY(stg.done(moe::launch_dlogits(dwp, pos, idx, w, T, E, k, I, dlogits, stream)));
+    MOE_TRY(stg.done(routing ? moe::launch_routed_dw(dwp, pos, routing->idx, idx, T, k, I, dlogits, stream)
+                             : moe::launch_dlogits(dwp, pos, idx, w, T, E, k, I, dlogits, stream)));
     if (opts) {
         opts->n_stages = stg.n;
         opts->path_taken = recompute ? MOE_PATH_BACKWARD : MOE_PATH_TRAIN_BACKWARD;
@@ -432,7 +445,8 @@ int run_backward(const void *x, const float *logits, const void *wgu, const void
 // rows in z.  The kernels and their per-element order are the grouped
 // forward's, so out has the same bits as a grouped moe_ffn_forward_ex call.
 int run_forward_train(const void *x, const float *logits, const void *wgu, const void *wd, const Shape &s,
-                      float *out, char *ws, const BwdLayout &L, moe_ffn_opts *opts, cudaStream_t stream)
+                      float *out, char *ws, const BwdLayout &L, moe_ffn_opts *opts, cudaStream_t stream,
+                      const moe::Routing *routing = nullptr)
 {
     DeviceInfo *dev = nullptr;
     int st = device_setup(&dev);
@@ -453,7 +467,8 @@ int run_forward_train(const void *x, const float *logits, const void *wgu, const
 
     Stages stg{opts ? opts->stage_events : nullptr, stream};
     MOE_TRY(stg.begin());
-    MOE_TRY(stg.done(moe::launch_router(logits, T, E, k, idx, w, nullptr, nullptr, tag_size, 0, stream)));
+    MOE_TRY(stg.done(routing ? moe::launch_take_routing(routing->idx, routing->w, T, E, k, idx, w, tag_size, 0, stream)
+                             : moe::launch_router(logits, T, E, k, idx, w, nullptr, nullptr, tag_size, 0, stream)));
     MOE_TRY(stg.done(moe::launch_sort(idx, T * k, E, moe::kGemmChunkMax, offs, perm, pos, (int32_t *)(ws + L.uexp),
                                       (int32_t *)(ws + L.ucount), chunks, nchunks, stream, 16, counts)));
     MOE_TRY(stg.done(moe::launch_gemm_gate_up_keep(x, perm, k, wgu, chunks, nchunks, offs, rows, H, I, E,
@@ -472,6 +487,16 @@ int run_forward_train(const void *x, const float *logits, const void *wgu, const
 }  // namespace
 
 namespace moe {
+
+int device_info(int *n_sm, int *pairs)
+{
+    DeviceInfo *d = nullptr;
+    const int st = device_setup(&d);
+    if (st != MOE_OK) return st;
+    *n_sm = d->n_sm;
+    *pairs = d->pairs;
+    return MOE_OK;
+}
 
 unsigned long long current_context_id()
 {
@@ -858,6 +883,109 @@ int moe_ffn_backward_train(const void *x_bf16, const float *router_logits_f32, c
                         dw_gate_up_f32, dw_down_f32, (char *)state, L, opts, stream, false);
 }
 
+// ---------------------------------------------------------------- a routing that the caller passes
+size_t moe_ffn_routed_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k)
+{
+    Shape s{T, H, I, E, k};
+    if (check_shape(s) != MOE_OK) return 0;
+    return make_layout(s).total + align256((size_t)(T * H * 2));  // the last region: MXFP8 tokens widened
+}
+
+int moe_ffn_forward_routed(const void *x, const void *x_scale, const int32_t *topk_idx, const float *topk_w_f32,
+                           const void *w_gate_up, const void *w_gate_up_scale, const void *w_down,
+                           const void *w_down_scale, int64_t T, int64_t H, int64_t I, int64_t E, int64_t k,
+                           float *out_f32, void *workspace, size_t workspace_bytes, moe_ffn_opts *opts,
+                           cudaStream_t stream)
+{
+    Shape s{T, H, I, E, k};
+    int st = check_shape(s);
+    if (st != MOE_OK) return st;
+    st = check_opts(opts);
+    if (st != MOE_OK) return st;
+    if (opts) {
+        opts->n_stages = 0;
+        opts->path_taken = 0;
+    }
+    if (T == 0) return MOE_OK;
+    if (!x || !topk_idx || !topk_w_f32 || !w_gate_up || !w_down || !out_f32) return MOE_ERR_INVALID_ARG;
+    if ((w_gate_up_scale == nullptr) != (w_down_scale == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(x_scale) || !aligned16(topk_idx) || !aligned16(topk_w_f32) ||
+        !aligned16(w_gate_up) || !aligned16(w_gate_up_scale) || !aligned16(w_down) || !aligned16(w_down_scale) ||
+        !aligned16(out_f32))
+        return MOE_ERR_INVALID_ARG;
+    if (!workspace || ((uintptr_t)workspace & 255)) return MOE_ERR_INVALID_ARG;
+    const Layout L = make_layout(s);
+    if (workspace_bytes < (x_scale ? moe_ffn_routed_workspace_bytes(T, H, I, E, k) : L.total))
+        return MOE_ERR_WORKSPACE_TOO_SMALL;
+    const moe::FusedMx mx{w_gate_up, w_gate_up_scale, w_down, w_down_scale};
+    const bool mxw = w_gate_up_scale != nullptr;
+    if (mxw && opts && opts->path == MOE_PATH_DECODE && T > kMxMaxTokens) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (x_scale) {
+        DeviceInfo *dev = nullptr;
+        st = device_setup(&dev);
+        if (st != MOE_OK) return st;
+        void *wide = (char *)workspace + L.total;
+        MOE_TRY(moe::launch_mx_widen(x, x_scale, (int)T, (int)H, wide, dev->n_sm, stream));
+        x = wide;
+    }
+    const moe::Routing routing{topk_idx, topk_w_f32};
+    return run_forward(x, nullptr, w_gate_up, w_down, s, out_f32, (char *)workspace, L, true, nullptr, nullptr, opts,
+                       stream, nullptr, nullptr, nullptr, mxw ? &mx : nullptr, false, &routing);
+}
+
+int moe_ffn_backward_routed(const void *x_bf16, const int32_t *topk_idx, const float *topk_w_f32,
+                            const void *w_gate_up_bf16, const void *w_down_bf16, const float *dout_f32, int64_t T,
+                            int64_t H, int64_t I, int64_t E, int64_t k, float *dx_f32, float *dtopk_w_f32,
+                            float *dw_gate_up_f32, float *dw_down_f32, void *workspace, size_t workspace_bytes,
+                            int from_state, moe_ffn_opts *opts, cudaStream_t stream)
+{
+    Shape s{T, H, I, E, k};
+    BwdLayout L;
+    int st = check_train_call(s, opts, w_gate_up_bf16, w_down_bf16, workspace, workspace_bytes, &L);
+    if (st != MOE_OK) return st;
+    if (!dw_gate_up_f32 || !dw_down_f32 || !aligned16(dw_gate_up_f32) || !aligned16(dw_down_f32))
+        return MOE_ERR_INVALID_ARG;
+    if (T > 0) {
+        if (!x_bf16 || !topk_idx || !topk_w_f32 || !dout_f32 || !dx_f32 || !dtopk_w_f32) return MOE_ERR_INVALID_ARG;
+        if (!aligned16(x_bf16) || !aligned16(topk_idx) || !aligned16(topk_w_f32) || !aligned16(dout_f32) ||
+            !aligned16(dx_f32) || !aligned16(dtopk_w_f32))
+            return MOE_ERR_INVALID_ARG;
+    }
+    // the first check that asks the CUDA runtime (the TMA encoder)
+    if (!moe::gemm_supported((int)H, (int)I, (int)E)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) {
+        if (cudaMemsetAsync(dw_gate_up_f32, 0, (size_t)(E * 2 * I * H) * 4, stream) != cudaSuccess ||
+            cudaMemsetAsync(dw_down_f32, 0, (size_t)(E * H * I) * 4, stream) != cudaSuccess)
+            return MOE_ERR_CUDA;
+        return MOE_OK;
+    }
+    const moe::Routing routing{topk_idx, topk_w_f32};
+    return run_backward(x_bf16, nullptr, w_gate_up_bf16, w_down_bf16, dout_f32, s, dx_f32, dtopk_w_f32, dw_gate_up_f32,
+                        dw_down_f32, (char *)workspace, L, opts, stream, from_state == 0, &routing);
+}
+
+int moe_ffn_forward_routed_train(const void *x_bf16, const int32_t *topk_idx, const float *topk_w_f32,
+                                 const void *w_gate_up_bf16, const void *w_down_bf16, int64_t T, int64_t H, int64_t I,
+                                 int64_t E, int64_t k, float *out_f32, void *state, size_t state_bytes,
+                                 moe_ffn_opts *opts, cudaStream_t stream)
+{
+    Shape s{T, H, I, E, k};
+    BwdLayout L;
+    int st = check_train_call(s, opts, w_gate_up_bf16, w_down_bf16, state, state_bytes, &L);
+    if (st != MOE_OK) return st;
+    if (T > 0) {
+        if (!x_bf16 || !topk_idx || !topk_w_f32 || !out_f32) return MOE_ERR_INVALID_ARG;
+        if (!aligned16(x_bf16) || !aligned16(topk_idx) || !aligned16(topk_w_f32) || !aligned16(out_f32))
+            return MOE_ERR_INVALID_ARG;
+    }
+    // the first check that asks the CUDA runtime (the TMA encoder)
+    if (!moe::gemm_supported((int)H, (int)I, (int)E)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return MOE_OK;
+    const moe::Routing routing{topk_idx, topk_w_f32};
+    return run_forward_train(x_bf16, nullptr, w_gate_up_bf16, w_down_bf16, s, out_f32, (char *)state, L, opts, stream,
+                             &routing);
+}
+
 const char *moe_ffn_status_string(int status)
 {
     switch (status) {
@@ -893,12 +1021,14 @@ const char *moe_ffn_stage_name(int path, int stage)
 int moe_ffn_device_faults(uint32_t *flags, int clear)
 {
     if (!flags) return MOE_ERR_INVALID_ARG;
-    uint32_t gemm = 0, decode = 0, wgrad = 0;
+    uint32_t gemm = 0, decode = 0, wgrad = 0, ortho = 0;
     if (moe::read_fault_word(&gemm, clear != 0) != cudaSuccess) return MOE_ERR_CUDA;
     if (moe::read_decode_fused_fault_word(&decode, clear != 0) != cudaSuccess) return MOE_ERR_CUDA;
     if (moe::read_bwd_fault_word(&wgrad, clear != 0) != cudaSuccess) return MOE_ERR_CUDA;
-    // bits 0-7: grouped GEMMs, 8-15: fused decode, 16-23: weight-gradient GEMMs
-    *flags = gemm | (decode << 8) | (wgrad << 16);
+    if (moe::read_ortho_fault_word(&ortho, clear != 0) != cudaSuccess) return MOE_ERR_CUDA;
+    // bits 0-7: grouped GEMMs, 8-15: fused decode, 16-23: weight-gradient
+    // GEMMs, 24-31: the orthogonalisation's products
+    *flags = gemm | (decode << 8) | (wgrad << 16) | (ortho << 24);
     return MOE_OK;
 }
 

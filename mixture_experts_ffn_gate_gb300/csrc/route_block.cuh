@@ -1,5 +1,5 @@
 // route_block.cuh -- top-k selection and softmax weights for one token,
-// computed by one warp.  Used by the router kernel and by the fused decode
+// computed by one warp, or taken from the caller.  Used by the router kernel and by the fused decode
 // kernel, which routes its tokens itself; both give the same bits.
 #pragma once
 
@@ -142,6 +142,34 @@ __device__ __forceinline__ void route_token_warp(const float *__restrict__ l, in
     float s = ex;
     for (int o = k <= 8 ? 4 : k <= 16 ? 8 : 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     w_j = lane < k ? ex / s : 0.0f;
+}
+
+// A routing that the caller passes, for one token by one warp: lane j < k
+// gets slot j's expert and weight.  The layer's kernels need k distinct
+// experts in [0, E): a slot whose index is outside, or repeats an earlier
+// slot's, is dropped, i.e. takes the lowest expert that no other slot has,
+// with weight 0.
+__device__ __forceinline__ void take_routing_warp(const int32_t *__restrict__ idx, const float *__restrict__ w, int E,
+                                                  int k, int &sel_j, float &w_j)
+{
+    const int lane = threadIdx.x & 31;
+    const int e = lane < k ? __ldg(idx + lane) : -1;
+    const unsigned lower = (1u << lane) - 1u;
+    const unsigned same = __match_any_sync(0xffffffffu, e);
+    const bool used = lane < k && e >= 0 && e < E && (same & lower) == 0;
+    sel_j = used ? e : 0;
+    w_j = used ? __ldg(w + lane) : 0.0f;
+    const unsigned dropped = __ballot_sync(0xffffffffu, lane < k && !used);
+    if (dropped) {
+        // k <= E: there are at least as many free experts as dropped slots
+        int next = 0;
+        const int want = __popc(dropped), place = __popc(dropped & lower);
+        for (int c = 0; c < E && next < want; ++c)
+            if (!__any_sync(0xffffffffu, used && e == c)) {
+                if ((dropped >> lane & 1) && place == next) sel_j = c;
+                ++next;
+            }
+    }
 }
 
 // The router projection sum_h x[h] * w[h] + bias, rounded once to FP32,

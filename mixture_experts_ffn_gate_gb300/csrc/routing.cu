@@ -49,6 +49,53 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_kernel(const float *
     }
 }
 
+// The caller's routing in the place of the router's (take_routing_warp), and
+// the same care for the fused decode kernel's state.
+__global__ void __launch_bounds__(32 * kRouterWarps) take_routing_kernel(const int32_t *__restrict__ idx_in,
+                                                                         const float *__restrict__ w_in, int T, int E,
+                                                                         int k, int32_t *__restrict__ idx,
+                                                                         float *__restrict__ w,
+                                                                         unsigned long long *__restrict__ tag_size,
+                                                                         unsigned long long tag_cap)
+{
+    if (tag_size && blockIdx.x == 0 && threadIdx.x == 0 && *tag_size > tag_cap) *tag_size = tag_cap;
+    const int t = blockIdx.x * kRouterWarps + (threadIdx.x >> 5), j = threadIdx.x & 31;
+    if (t >= T) return;
+    int e;
+    float wt;
+    take_routing_warp(idx_in + (int64_t)t * k, w_in + (int64_t)t * k, E, k, e, wt);
+    if (j < k) {
+        idx[(int64_t)t * k + j] = e;
+        w[(int64_t)t * k + j] = wt;
+    }
+}
+
+// ---------------------------------------------------------------- MXFP8 tokens
+// x [T, H] BF16 from E4M3 codes and E8M0 scales, exactly (a value outside
+// BF16's range rounds as BF16 does): 16 codes, half a scale block, per step.
+__global__ void __launch_bounds__(256) mx_widen_kernel(const uint8_t *__restrict__ codes,
+                                                       const uint8_t *__restrict__ scales, int64_t pieces, int H,
+                                                       int scale_stride, uint16_t *__restrict__ x)
+{
+    const int per_row = H / 16;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / per_row;
+        const int c = (int)(i - t * per_row);
+        const uint4 v = ld_nc16(codes + i * 16);
+        const uint32_t s = __ldg(scales + t * scale_stride + c / 2);
+        // the scale 255 is NaN; mx_f32_scale leaves it infinite
+        const float f = s == 255u ? __uint_as_float(0x7fc00000u) : mx_f32_scale(s);
+        uint4 a, b;
+        e4m3x4_to_bf16x2_f32(v.x, f, a.x, a.y);
+        e4m3x4_to_bf16x2_f32(v.y, f, a.z, a.w);
+        e4m3x4_to_bf16x2_f32(v.z, f, b.x, b.y);
+        e4m3x4_to_bf16x2_f32(v.w, f, b.z, b.w);
+        uint4 *dst = reinterpret_cast<uint4 *>(x + i * 16);
+        dst[0] = a;
+        dst[1] = b;
+    }
+}
+
 // ---------------------------------------------------------------- router projection
 // logits[t, e] = round_f32(sum_h x[t, h] * W_r[e, h] + b[e]), one warp per
 // logit (router_logit_warp), for calls that pass the router weights instead
@@ -230,6 +277,24 @@ cudaError_t launch_router(const float *logits, int T, int E, int k, int32_t *idx
 {
     router_kernel<<<(unsigned)ceil_div(T, kRouterWarps), 32 * kRouterWarps, (size_t)kRouterWarps * E * 4, s>>>(
         logits, T, E, k, idx, w, idx_copy, w_copy, tag_size, tag_cap);
+    return cudaPeekAtLastError();
+}
+
+cudaError_t launch_take_routing(const int32_t *idx_in, const float *w_in, int T, int E, int k, int32_t *idx, float *w,
+                                unsigned long long *tag_size, unsigned long long tag_cap, cudaStream_t s)
+{
+    take_routing_kernel<<<(unsigned)ceil_div(T, kRouterWarps), 32 * kRouterWarps, 0, s>>>(idx_in, w_in, T, E, k, idx, w,
+                                                                                         tag_size, tag_cap);
+    return cudaPeekAtLastError();
+}
+
+cudaError_t launch_mx_widen(const void *codes, const void *scales, int T, int H, void *x, int n_sm, cudaStream_t s)
+{
+    const int64_t pieces = (int64_t)T * (H / 16);
+    const int64_t blocks = ceil_div(pieces, 256);
+    const int grid = (int)(blocks < (int64_t)n_sm * 8 ? blocks : (int64_t)n_sm * 8);
+    mx_widen_kernel<<<grid, 256, 0, s>>>((const uint8_t *)codes, (const uint8_t *)scales, pieces, H, mx_scale_bytes(H),
+                                         (uint16_t *)x);
     return cudaPeekAtLastError();
 }
 

@@ -37,7 +37,12 @@ EXPORTED = ["moe_ffn_forward", "moe_ffn_workspace_bytes", "moe_ffn_forward_ex",
             "moe_ffn_stage_name", "moe_ffn_device_faults", "moe_ffn_forward_noalloc",
             "moe_ffn_router_workspace_bytes", "moe_ffn_forward_router", "moe_ffn_forward_mxfp8",
             "moe_ffn_backward_workspace_bytes", "moe_ffn_backward", "moe_ffn_train_state_bytes",
-            "moe_ffn_forward_train", "moe_ffn_backward_train"]
+            "moe_ffn_forward_train", "moe_ffn_backward_train",
+            # moe_block.h, bound in moe_block.py
+            "moe_rms_norm_forward", "moe_rms_norm_backward_workspace_bytes", "moe_rms_norm_backward",
+            "moe_gate_forward", "moe_gate_backward", "moe_ffn_routed_workspace_bytes", "moe_ffn_forward_routed",
+            "moe_ffn_backward_routed", "moe_ffn_forward_routed_train", "moe_orthogonalize_workspace_bytes",
+            "moe_orthogonalize"]
 
 # Size of the library's fixed scratch array used by moe_ffn_forward_noalloc.
 MOE_FFN_NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -126,6 +131,8 @@ def lib():
                       L.moe_ffn_forward_mxfp8, L.moe_ffn_backward, L.moe_ffn_forward_train,
                       L.moe_ffn_backward_train):
                 f.restype = i32
+            from . import moe_block
+            moe_block.declare(L)
             if hasattr(L, "moe_ffn_debug_fused_timeline"):   # instrumented build only
                 L.moe_ffn_debug_fused_timeline.argtypes = [vp, i32]
                 L.moe_ffn_debug_fused_timeline.restype = i32
