@@ -35,6 +35,17 @@
 // Every output element is one MMA chain over K in a fixed order, so results
 // do not depend on the grid size or on which CTA ran which tile.
 //
+// The calls that take the routing from the caller run instances that cut K
+// into segments of kSegSteps stages (SEG): the MMAs of a segment start a new
+// accumulator, and the epilogue adds the segments in FP32 registers, in
+// order.  The tensor cores' own additions round toward zero, which shrinks a
+// chain of K / 16 of them by about 1.2e-8 K / 16 of its value: measured
+// against FP64 at H = 4096, I = 1536, 1.1e-5 with one chain and %SEGERR% with
+// segments of 256.  The drains are small beside the weight stream that bounds
+// these kernels, so the segments cost %SEGCOST%.  An epilogue warp keeps the
+// sums of one 32-row x 64-column block, so SEG has four epilogue warps per
+// weight tile, and gate_up two tiles per item instead of four (five stages).
+//
 // One persistent CTA per SM: warp 0 issues TMA loads into a ring of smem
 // stages, warp 1 issues tcgen05.mma into one of two TMEM accumulators,
 // warps 2-5 drain the other accumulator (tcgen05.ld) and store.  gate_up
@@ -94,7 +105,9 @@ enum : int {
     kGateUpSave = 7, // kGateUp that also keeps g and u in FP32 (the training forward)
 };
 
-template <int KIND>
+constexpr int kSegSteps = 4;  // SEG: K stages per accumulator, 256 elements
+
+template <int KIND, bool SEG = false>
 struct Cfg {
     // MXFP8 weights: the producer loads E4M3 code tiles, converter warps
     // write them as exact BF16 (each 32-element block times its E8M0
@@ -107,15 +120,20 @@ struct Cfg {
     // epilogue warps: q's SwiGLU backward reads and writes several arrays
     // per element, so two warps share each TMEM lane quarter (one 32-column
     // block each) to drain its single accumulator set sooner
-    static constexpr int EPI_WARPS = KIND == kBwdQ ? 8 : 4;
+    // (SEG: a warp per lane quarter of each weight tile)
+    static constexpr int MT_SEG = GATE_UP || KIND == kBwdQ ? 2 : 3;
+    static constexpr int EPI_WARPS = SEG ? 4 * MT_SEG : KIND == kBwdQ ? 8 : 4;
     static constexpr int CONV_WARPS = MX ? 8 : 0;
-    static constexpr int FIRST_CONV = 2 + EPI_WARPS + (GATE_UP ? 3 : 0);  // after the x-row loaders
+    static constexpr int STAGES = KIND == kBwdQ ? 4 : SEG && GATE_UP ? 5 : 3;
+    static constexpr int FIRST_LOADER = 2 + EPI_WARPS;                          // gate_up: the x-row loaders,
+    static constexpr int FIRST_CONV = FIRST_LOADER + (GATE_UP ? STAGES : 0);  // one per stage
+    static_assert(!(SEG && MX), "the segments are built for BF16 weights only");
     static constexpr int THREADS = 32 * (FIRST_CONV + CONV_WARPS);
     // weight tiles per item (they share one token tile); q takes two, so
     // that its accumulators fit twice (its long epilogue then overlaps the
     // next item's MMAs) and I's 128-row tiles split evenly
     // (MX: two, so that the code tiles fit beside three stages)
-    static constexpr int MT = MX ? 2 : GATE_UP ? 4 : KIND == kBwdQ ? 2 : 3;
+    static constexpr int MT = SEG ? MT_SEG : MX ? 2 : GATE_UP ? 4 : KIND == kBwdQ ? 2 : 3;
     // accumulator columns per weight tile: the chunk's tokens (gate_up), or
     // its hi rows then its lo rows (down, q, dx); gate_up and q double-buffer
     // them so the epilogue of one item overlaps the MMAs of the next, down
@@ -130,7 +148,6 @@ struct Cfg {
                                       : TMEM_COLS <= 256 ? 256
                                                          : 512;
     static_assert(TMEM_COLS <= 512, "accumulators exceed TMEM");
-    static constexpr int STAGES = KIND == kBwdQ ? 4 : 3;
     static constexpr int A_TILE = BM * BK * 2;                            // 16 KB per weight tile
     static constexpr int A_BYTES = MT * A_TILE;
     static constexpr int B_TILE = NMAX * BK * 2;                          // 8 KB per operand
@@ -140,7 +157,7 @@ struct Cfg {
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + CODE_BYTES;
     static constexpr int BAR_BYTES = 256;
     static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + BAR_BYTES;
-    static_assert(THREADS == (GATE_UP && !MX ? kThreadsGateUp : THREADS), "gate_up keeps 288 threads");
+    static_assert(THREADS == (GATE_UP && !MX && !SEG ? kThreadsGateUp : THREADS), "gate_up keeps 288 threads");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -280,8 +297,8 @@ __device__ __forceinline__ void bwd_q_columns(const uint32_t (&r)[32], int ncols
     if (lane < ncols && c0 + lane < n) b.dwp[(int64_t)(p0 + c0 + lane) * (I / 32) + grp] = sum;
 }
 
-template <int KIND>
-__global__ void __launch_bounds__(Cfg<KIND>::THREADS, 1)
+template <int KIND, bool SEG = false>
+__global__ void __launch_bounds__(Cfg<KIND, SEG>::THREADS, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0s,
                         const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1s,
                         const __grid_constant__ CUtensorMap tmB1, const GemmArgs args)
@@ -299,7 +316,7 @@ __global__ void __launch_bounds__(Cfg<KIND>::THREADS, 1)
     // <= 16 rows.  gate_up leaves the B maps unread.
     // MX (gate_up, down): tmA is the same view of the E4M3 codes (uint8,
     // no swizzle: 64-byte rows), its box a tile's codes.
-    using C = Cfg<KIND>;
+    using C = Cfg<KIND, SEG>;
     constexpr bool GATE_UP = C::GATE_UP;
     constexpr bool A_MN = C::A_MN;
     constexpr bool MX = C::MX;
@@ -445,26 +462,41 @@ __global__ void __launch_bounds__(Cfg<KIND>::THREADS, 1)
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
-            int li = 0;
+            int li = 0;  // accumulator sets filled: one per item (SEG: per segment)
             Item nxt = blockIdx.x < total ? decode_item(blockIdx.x, args) : Item{};
-            for (int i = blockIdx.x; i < total && !*abort_flag; i += gridDim.x, ++li) {
+            for (int i = blockIdx.x; i < total && !*abort_flag; i += gridDim.x) {
                 const Item it = nxt;
                 if (i + (int)gridDim.x < total) nxt = decode_item(i + gridDim.x, args);
                 // down: N spans the hi box and the lo rows that matter
                 const int box = it.n <= SMALL_ROWS ? SMALL_ROWS : NMAX;
                 const uint32_t idesc =
                     ptx::idesc_bf16_f32_mn(BM, GATE_UP ? pad16(it.n) : box + pad16(it.n), A_MN, false);
-                const int acc = C::ACC_BUFS == 2 ? (li & 1) : 0;
-                const uint32_t aph = C::ACC_BUFS == 2 ? (li >> 1) & 1 : li & 1;
-                if (!ptx::mbar_wait_bounded(tempty + acc, aph ^ 1, abort_flag, kWaitLimitNs)) {
-                    if (!*abort_flag) raise_fault(FAULT_GEMM_MMA);
-                    *abort_flag = 1;
-                    break;
-                }
-                ptx::tc_fence_after();
-                const uint32_t d = tmem + acc * MT * C::TILE_COLS;
+                int acc = 0;
+                uint32_t d = 0;
                 bool ok = true;
+                // the next free accumulator set
+                auto take_set = [&] {
+                    acc = C::ACC_BUFS == 2 ? (li & 1) : 0;
+                    const uint32_t aph = C::ACC_BUFS == 2 ? (li >> 1) & 1 : li & 1;
+                    ++li;
+                    if (!ptx::mbar_wait_bounded(tempty + acc, aph ^ 1, abort_flag, kWaitLimitNs)) {
+                        if (!*abort_flag) raise_fault(FAULT_GEMM_MMA);
+                        *abort_flag = 1;
+                        return false;
+                    }
+                    ptx::tc_fence_after();
+                    d = tmem + acc * MT * C::TILE_COLS;
+                    return true;
+                };
+                if (!SEG && !take_set()) break;
                 for (int kb = 0; kb < KB; ++kb) {
+                    if (SEG && kb % kSegSteps == 0) {
+                        if (kb) ptx::mma_commit(tfull + acc);
+                        if (!take_set()) {
+                            ok = false;
+                            break;
+                        }
+                    }
                     if (!ptx::mbar_wait_bounded(full + stage, phase, abort_flag, kWaitLimitNs)) {
                         if (!*abort_flag) raise_fault(FAULT_GEMM_MMA);
                         *abort_flag = 1;
@@ -484,7 +516,7 @@ __global__ void __launch_bounds__(Cfg<KIND>::THREADS, 1)
                             // second 64-wide MN block a box (8 KB) on
                             const uint64_t ad = A_MN ? ptx::sw128_desc_mn(a_addr + t * C::A_TILE + k * 2048, C::A_TILE / 2)
                                                      : ptx::sw128_desc(a_addr + t * C::A_TILE + k * 32);
-                            ptx::mma_bf16(d + t * C::TILE_COLS, ad, bd, idesc, (kb | k) != 0);
+                            ptx::mma_bf16(d + t * C::TILE_COLS, ad, bd, idesc, ((SEG ? kb % kSegSteps : kb) | k) != 0);
                         }
                     }
                     ptx::mma_commit(empty + stage);
@@ -579,15 +611,15 @@ __global__ void __launch_bounds__(Cfg<KIND>::THREADS, 1)
                 }
             }
         }
-    } else if (GATE_UP && warp >= 6) {
+    } else if (GATE_UP && warp >= C::FIRST_LOADER) {
         // ------------------------------------- x-row loaders (gate_up only)
-        // Warp 6 + sl fills ring stage sl: the CTA's K steps n = sl, sl +
+        // Warp FIRST_LOADER + sl fills ring stage sl: the CTA's K steps n = sl, sl +
         // STAGES, ... over its items in the producer's order (item i = block
         // + j * grid, K steps in order; stage n % STAGES, phase (n / STAGES)
         // & 1).  Lane l copies rows l and l + 32 of the chunk, 128 bytes per
         // row, piece q of row r at (q ^ (r & 7)) * 16; rows past the chunk
         // are not loaded (the MMA's columns for them are never stored).
-        const int sl = warp - 6;
+        const int sl = warp - C::FIRST_LOADER;
         uint32_t swz[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) swz[q] = (uint32_t)((q ^ (lane & 7)) << 4);
@@ -639,19 +671,111 @@ __global__ void __launch_bounds__(Cfg<KIND>::THREADS, 1)
         // q: warps 2-5 take the chunk's 32-column blocks 0, 2, ..., warps 6-9 blocks 1, 3, ...
         const int c_first = C::EPI_WARPS == 8 ? 32 * ((warp - 2) >> 2) : 0;
         constexpr int c_step = C::EPI_WARPS == 8 ? 64 : 32;
+        // what becomes of 32 columns (sorted rows it.p0 + c0 + j) of the
+        // warp's 32 weight rows of a tile
+        auto emit = [&](const uint32_t (&r)[32], const Item &it, int tile, int c0) {
+                            if constexpr (KIND == kGateUpRaw) {
+                                const int neuron = tile * 64 + 16 * q + (lane & 15);
+                                float *dst = reinterpret_cast<float *>(lane < 16 ? args.out0 : args.out1);
+            #pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    if (c0 + j < it.n) dst[(int64_t)(it.p0 + c0 + j) * args.I + neuron] = __uint_as_float(r[j]);
+                            } else if constexpr (KIND == kBwdQ) {
+                                bwd_q_columns(r, it.n > SMALL_ROWS ? 32 : SMALL_ROWS, it.p0, it.n, c0, tile * BM + 32 * q + lane,
+                                              tile * 4 + q, args, lane);
+                            } else if constexpr (KIND == kGateUp || KIND == kGateUpMx || KIND == kGateUpSave) {
+                                const int neuron = tile * 64 + 16 * q + (lane & 15);
+                                __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(lane < 16 ? args.out0 : args.out1);
+                                float *keep = lane < 16 ? args.g_keep : args.u_keep;   // kGateUpSave: g (lanes 0-15), u
+            #pragma unroll
+                                for (int j = 0; j < 32; ++j) {
+                                    const float v = __uint_as_float(r[j]);
+                                    const float o = __shfl_xor_sync(0xffffffffu, v, 16);
+                                    const float a = lane < 16 ? swiglu(v, o) : swiglu(o, v);
+                                    const __nv_bfloat16 hi = __float2bfloat16_rn(a);
+                                    const __nv_bfloat16 lo = __float2bfloat16_rn(a - __bfloat162float(hi));
+                                    if (c0 + j < it.n) {
+                                        const int64_t at = (int64_t)(it.p0 + c0 + j) * args.I + neuron;
+                                        dst[at] = lane < 16 ? hi : lo;
+                                        if constexpr (KIND == kGateUpSave) keep[at] = v;
+                                    }
+                                }
+                            } else {
+                                const int h = tile * BM + 32 * q + lane;
+                                float *z = reinterpret_cast<float *>(args.out0);
+                                if (h < args.H) {
+            #pragma unroll
+                                    for (int j = 0; j < 32; ++j)
+                                        if (c0 + j < it.n) z[(int64_t)(it.p0 + c0 + j) * args.H + h] = __uint_as_float(r[j]);
+                                }
+                            }
+        };
+        // a set of accumulators that the MMAs have filled
+        auto wait_set = [&](int acc, uint32_t aph) {
+            if (!ptx::mbar_wait_bounded(tfull + acc, aph, abort_flag, kWaitLimitNs)) {
+                if (!*abort_flag) raise_fault(FAULT_GEMM_EPILOGUE);
+                *abort_flag = 1;
+                return false;
+            }
+            ptx::tc_fence_after();
+            return true;
+        };
         int li = 0;
         Item nxt = blockIdx.x < total ? decode_item(blockIdx.x, args) : Item{};
+        if constexpr (SEG) {
+            const int t = (warp - 2) >> 2;  // the warp's tile of an item
+            bool ok = true;
+            for (int i = blockIdx.x; i < total && ok; i += gridDim.x) {
+                const Item it = nxt;
+                if (i + (int)gridDim.x < total) nxt = decode_item(i + gridDim.x, args);
+                const int tile = it.m * MT + t;
+                // (q: nothing to do either where the warp's 32 neurons lie past I)
+                const bool mine = tile < args.tiles && !(KIND == kBwdQ && tile * BM + 32 * q >= args.I);
+                uint32_t sum[2][32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) sum[0][j] = sum[1][j] = 0u;
+                auto add = [&](uint32_t (&to)[32], uint32_t taddr) {
+                    uint32_t r[32];
+                    ptx::tmem_ld32(taddr, r);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) to[j] = __float_as_uint(__uint_as_float(to[j]) + __uint_as_float(r[j]));
+                };
+                for (int kb = 0; kb < KB; kb += kSegSteps, ++li) {
+                    const int acc = C::ACC_BUFS == 2 ? (li & 1) : 0;
+                    ok = __all_sync(0xffffffffu, wait_set(acc, C::ACC_BUFS == 2 ? (li >> 1) & 1 : li & 1));
+                    if (!ok) break;
+                    if (mine) {
+                        const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (acc * MT + t) * C::TILE_COLS;
+                        add(sum[0], tbase);
+                        if (it.n > 32) add(sum[1], tbase + 32);
+                        if (!GATE_UP && it.n > SMALL_ROWS) {  // the lo rows' columns
+                            add(sum[0], tbase + NMAX);
+                            if (it.n > 32) add(sum[1], tbase + NMAX + 32);
+                        }
+                    }
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(tempty + acc);
+                }
+                if (!ok) break;
+                if (!mine) continue;
+                if (!GATE_UP && it.n <= SMALL_ROWS) {  // lo from column 16
+#pragma unroll
+                    for (int j = 0; j < SMALL_ROWS; ++j)
+                        sum[0][j] =
+                            __float_as_uint(__uint_as_float(sum[0][j]) + __uint_as_float(sum[0][SMALL_ROWS + j]));
+                }
+                emit(sum[0], it, tile, 0);
+                if (it.n > 32) emit(sum[1], it, tile, 32);
+            }
+        } else {
         for (int i = blockIdx.x; i < total; i += gridDim.x, ++li) {
             const Item it = nxt;
             if (i + (int)gridDim.x < total) nxt = decode_item(i + gridDim.x, args);
             const int acc = C::ACC_BUFS == 2 ? (li & 1) : 0;
             const uint32_t aph = C::ACC_BUFS == 2 ? (li >> 1) & 1 : li & 1;
-            if (!ptx::mbar_wait_bounded(tfull + acc, aph, abort_flag, kWaitLimitNs)) {
-                if (!*abort_flag) raise_fault(FAULT_GEMM_EPILOGUE);
-                *abort_flag = 1;
-                break;
-            }
-            ptx::tc_fence_after();
+            if (!wait_set(acc, aph)) break;
             for (int t = 0; t < MT && it.m * MT + t < args.tiles; ++t) {
             const int tile = it.m * MT + t;
             // q: a warp whose 32 neurons lie past I has nothing to do
@@ -679,46 +803,13 @@ __global__ void __launch_bounds__(Cfg<KIND>::THREADS, 1)
                 } else {
                     ptx::tmem_wait_ld();
                 }
-                if constexpr (KIND == kGateUpRaw) {
-                    const int neuron = tile * 64 + 16 * q + (lane & 15);
-                    float *dst = reinterpret_cast<float *>(lane < 16 ? args.out0 : args.out1);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (c0 + j < it.n) dst[(int64_t)(it.p0 + c0 + j) * args.I + neuron] = __uint_as_float(r[j]);
-                } else if constexpr (KIND == kBwdQ) {
-                    bwd_q_columns(r, it.n > SMALL_ROWS ? 32 : SMALL_ROWS, it.p0, it.n, c0, tile * BM + 32 * q + lane,
-                                  tile * 4 + q, args, lane);
-                } else if constexpr (KIND == kGateUp || KIND == kGateUpMx || KIND == kGateUpSave) {
-                    const int neuron = tile * 64 + 16 * q + (lane & 15);
-                    __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(lane < 16 ? args.out0 : args.out1);
-                    float *keep = lane < 16 ? args.g_keep : args.u_keep;   // kGateUpSave: g (lanes 0-15), u
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float v = __uint_as_float(r[j]);
-                        const float o = __shfl_xor_sync(0xffffffffu, v, 16);
-                        const float a = lane < 16 ? swiglu(v, o) : swiglu(o, v);
-                        const __nv_bfloat16 hi = __float2bfloat16_rn(a);
-                        const __nv_bfloat16 lo = __float2bfloat16_rn(a - __bfloat162float(hi));
-                        if (c0 + j < it.n) {
-                            const int64_t at = (int64_t)(it.p0 + c0 + j) * args.I + neuron;
-                            dst[at] = lane < 16 ? hi : lo;
-                            if constexpr (KIND == kGateUpSave) keep[at] = v;
-                        }
-                    }
-                } else {
-                    const int h = tile * BM + 32 * q + lane;
-                    float *z = reinterpret_cast<float *>(args.out0);
-                    if (h < args.H) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (c0 + j < it.n) z[(int64_t)(it.p0 + c0 + j) * args.H + h] = __uint_as_float(r[j]);
-                    }
-                }
+                emit(r, it, tile, c0);
             }
             }
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(tempty + acc);
+        }
         }
     }
 
@@ -838,11 +929,11 @@ int grid_for(int ctas, int n_assign, int m_tiles, int E)
 
 }  // namespace
 
-template <int KIND>
+template <int KIND, bool SEG = false>
 cudaError_t set_smem()
 {
-    return cudaFuncSetAttribute(grouped_gemm_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Cfg<KIND>::SMEM);
+    return cudaFuncSetAttribute(grouped_gemm_kernel<KIND, SEG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Cfg<KIND, SEG>::SMEM);
 }
 
 cudaError_t gemm_init_device()
@@ -855,6 +946,12 @@ cudaError_t gemm_init_device()
     if (e == cudaSuccess) e = set_smem<kGateUpMx>();
     if (e == cudaSuccess) e = set_smem<kDownMx>();
     if (e == cudaSuccess) e = set_smem<kGateUpSave>();
+    if (e == cudaSuccess) e = set_smem<kGateUp, true>();
+    if (e == cudaSuccess) e = set_smem<kDown, true>();
+    if (e == cudaSuccess) e = set_smem<kGateUpRaw, true>();
+    if (e == cudaSuccess) e = set_smem<kBwdQ, true>();
+    if (e == cudaSuccess) e = set_smem<kBwdDx, true>();
+    if (e == cudaSuccess) e = set_smem<kGateUpSave, true>();
     return e;
 }
 
@@ -867,13 +964,13 @@ bool gemm_supported(int H, int I, int E)
 
 namespace {
 
-template <int KIND>
+template <int KIND, bool SEG>
 cudaError_t gate_up_like(const void *x, const int32_t *perm, int k, const void *wgu, const int4 *chunks,
                          const int32_t *nchunks, const int32_t *offs, int n_assign, int H, int I, int E, void *out0,
                          void *out1, int ctas, cudaStream_t s, float *g_keep = nullptr, float *u_keep = nullptr)
 {
     CUtensorMap tA;
-    constexpr int MT = Cfg<KIND>::MT;
+    constexpr int MT = Cfg<KIND, SEG>::MT;
     // groups of 16 neurons per box: MT tiles of 4, but never more than the tensor has
     const uint32_t groups = (uint32_t)(4 * MT < I / 16 ? 4 * MT : I / 16);
     cudaError_t e = make_gate_up_map(&tA, wgu, E, I, H, groups);
@@ -883,8 +980,9 @@ cudaError_t gate_up_like(const void *x, const int32_t *perm, int k, const void *
     a.g_keep = g_keep;
     a.u_keep = u_keep;
     // the token rows come from x through the loader warps: the B maps are not read
-    grouped_gemm_kernel<KIND><<<grid_for(ctas, n_assign, a.m_tiles, E), Cfg<KIND>::THREADS, Cfg<KIND>::SMEM, s>>>(
-        tA, tA, tA, tA, tA, a);
+    grouped_gemm_kernel<KIND, SEG>
+        <<<grid_for(ctas, n_assign, a.m_tiles, E), Cfg<KIND, SEG>::THREADS, Cfg<KIND, SEG>::SMEM, s>>>(tA, tA, tA, tA,
+                                                                                                     tA, a);
     return cudaPeekAtLastError();
 }
 
@@ -915,17 +1013,18 @@ cudaError_t make_mn_map(CUtensorMap *map, const void *base, uint64_t d0, uint64_
 }
 
 // q and dx: M (the weight side) of size m_size in tiles of 128, K = k_size.
-template <int KIND>
+template <int KIND, bool SEG>
 cudaError_t launch_mn(const CUtensorMap &tA, const CUtensorMap (&tB)[4], const int4 *chunks, const int32_t *nchunks,
                       const int32_t *offs, int n_rows, int H, int I, int E, int m_size, int k_size, void *out0,
                       const BwdQArgs &q, int ctas, cudaStream_t s)
 {
-    constexpr int MT = Cfg<KIND>::MT;
+    constexpr int MT = Cfg<KIND, SEG>::MT;
     const int tiles = (m_size + BM - 1) / BM;
     GemmArgs a{chunks, nchunks, offs, H, I, k_size, (tiles + MT - 1) / MT, tiles, MT * BM * BK * 2, out0, nullptr,
                nullptr, nullptr, 0, q};
-    grouped_gemm_kernel<KIND><<<grid_for(ctas, n_rows, a.m_tiles, E), Cfg<KIND>::THREADS, Cfg<KIND>::SMEM, s>>>(
-        tA, tB[0], tB[1], tB[2], tB[3], a);
+    grouped_gemm_kernel<KIND, SEG>
+        <<<grid_for(ctas, n_rows, a.m_tiles, E), Cfg<KIND, SEG>::THREADS, Cfg<KIND, SEG>::SMEM, s>>>(
+            tA, tB[0], tB[1], tB[2], tB[3], a);
     return cudaPeekAtLastError();
 }
 
@@ -933,9 +1032,10 @@ cudaError_t launch_mn(const CUtensorMap &tA, const CUtensorMap (&tB)[4], const i
 
 cudaError_t launch_gemm_gate_up(const void *x, const int32_t *perm, int k, const void *wgu, const int4 *chunks,
                                 const int32_t *nchunks, const int32_t *offs, int n_assign, int H, int I, int E,
-                                void *act_hi, void *act_lo, int ctas, cudaStream_t s)
+                                void *act_hi, void *act_lo, int ctas, cudaStream_t s, bool seg)
 {
-    return gate_up_like<kGateUp>(x, perm, k, wgu, chunks, nchunks, offs, n_assign, H, I, E, act_hi, act_lo, ctas, s);
+    auto f = seg ? gate_up_like<kGateUp, true> : gate_up_like<kGateUp, false>;
+    return f(x, perm, k, wgu, chunks, nchunks, offs, n_assign, H, I, E, act_hi, act_lo, ctas, s, nullptr, nullptr);
 }
 
 cudaError_t launch_gemm_gate_up_mx(const void *x, const int32_t *perm, int k, const void *gq, const void *gs,
@@ -973,22 +1073,24 @@ cudaError_t launch_gemm_down_mx(const void *act_hi, const void *act_lo, const vo
 
 cudaError_t launch_gemm_gate_up_raw(const void *x, const int32_t *perm, int k, const void *wgu, const int4 *chunks,
                                     const int32_t *nchunks, const int32_t *offs, int n_rows, int H, int I, int E,
-                                    float *g, float *u, int ctas, cudaStream_t s)
+                                    float *g, float *u, int ctas, cudaStream_t s, bool seg)
 {
-    return gate_up_like<kGateUpRaw>(x, perm, k, wgu, chunks, nchunks, offs, n_rows, H, I, E, g, u, ctas, s);
+    auto f = seg ? gate_up_like<kGateUpRaw, true> : gate_up_like<kGateUpRaw, false>;
+    return f(x, perm, k, wgu, chunks, nchunks, offs, n_rows, H, I, E, g, u, ctas, s, nullptr, nullptr);
 }
 
 cudaError_t launch_gemm_gate_up_keep(const void *x, const int32_t *perm, int k, const void *wgu, const int4 *chunks,
                                      const int32_t *nchunks, const int32_t *offs, int n_rows, int H, int I, int E,
-                                     void *act_hi, void *act_lo, float *g, float *u, int ctas, cudaStream_t s)
+                                     void *act_hi, void *act_lo, float *g, float *u, int ctas, cudaStream_t s,
+                                     bool seg)
 {
-    return gate_up_like<kGateUpSave>(x, perm, k, wgu, chunks, nchunks, offs, n_rows, H, I, E, act_hi, act_lo, ctas, s,
-                                     g, u);
+    auto f = seg ? gate_up_like<kGateUpSave, true> : gate_up_like<kGateUpSave, false>;
+    return f(x, perm, k, wgu, chunks, nchunks, offs, n_rows, H, I, E, act_hi, act_lo, ctas, s, g, u);
 }
 
 cudaError_t launch_bwd_q(const void *ds_hi, const void *ds_lo, const void *wd, const int4 *chunks,
                          const int32_t *nchunks, const int32_t *offs, int n_rows, int H, int I, int E,
-                         const BwdQOut &o, int ctas, cudaStream_t s)
+                         const BwdQOut &o, int ctas, cudaStream_t s, bool seg)
 {
     CUtensorMap tA, tB[4];
     cudaError_t e = make_mn_map(&tA, wd, I, H, E);
@@ -996,25 +1098,28 @@ cudaError_t launch_bwd_q(const void *ds_hi, const void *ds_lo, const void *wd, c
     if (e != cudaSuccess) return e;
     const BwdQArgs q{o.g, o.u, o.w_s, (__nv_bfloat16 *)o.dgu_hi, (__nv_bfloat16 *)o.dgu_lo,
                      (__nv_bfloat16 *)o.wa_hi, (__nv_bfloat16 *)o.wa_lo, o.dwp};
-    return launch_mn<kBwdQ>(tA, tB, chunks, nchunks, offs, n_rows, H, I, E, I, H, nullptr, q, ctas, s);
+    auto f = seg ? launch_mn<kBwdQ, true> : launch_mn<kBwdQ, false>;
+    return f(tA, tB, chunks, nchunks, offs, n_rows, H, I, E, I, H, nullptr, q, ctas, s);
 }
 
 cudaError_t launch_bwd_dx(const void *dgu_hi, const void *dgu_lo, const void *wgu, const int4 *chunks,
                           const int32_t *nchunks, const int32_t *offs, int n_rows, int H, int I, int E, float *z,
-                          int ctas, cudaStream_t s)
+                          int ctas, cudaStream_t s, bool seg)
 {
     CUtensorMap tA, tB[4];
     cudaError_t e = make_mn_map(&tA, wgu, H, 2 * (uint64_t)I, E);
     if (e == cudaSuccess) e = make_pair_maps(tB, dgu_hi, dgu_lo, n_rows, 2 * (uint64_t)I);
     if (e != cudaSuccess) return e;
-    return launch_mn<kBwdDx>(tA, tB, chunks, nchunks, offs, n_rows, H, I, E, H, 2 * I, z, BwdQArgs{}, ctas, s);
+    auto f = seg ? launch_mn<kBwdDx, true> : launch_mn<kBwdDx, false>;
+    return f(tA, tB, chunks, nchunks, offs, n_rows, H, I, E, H, 2 * I, z, BwdQArgs{}, ctas, s);
 }
 
 cudaError_t launch_gemm_down(const void *act_hi, const void *act_lo, const void *wd, const int4 *chunks,
                              const int32_t *nchunks, const int32_t *offs, int n_assign, int H, int I, int E, float *z,
-                             int ctas, cudaStream_t s)
+                             int ctas, cudaStream_t s, bool seg)
 {
     CUtensorMap tA, tB0s, tB0, tB1s, tB1;
+    static_assert(Cfg<kDown>::MT == Cfg<kDown, true>::MT, "one item list for both");
     constexpr int MT = Cfg<kDown>::MT;
     cudaError_t e = make_down_map(&tA, wd, E, H, I);
     if (e == cudaSuccess) e = make_map(&tB0s, act_hi, n_assign, I, SMALL_ROWS);
@@ -1025,8 +1130,12 @@ cudaError_t launch_gemm_down(const void *act_hi, const void *act_lo, const void 
     const int tiles = (H + BM - 1) / BM;
     GemmArgs a{chunks, nchunks, offs, H, I, I, (tiles + MT - 1) / MT, tiles, MT * BM * BK * 2, z, nullptr, nullptr,
                nullptr, 0};
-    grouped_gemm_kernel<kDown><<<grid_for(ctas, n_assign, a.m_tiles, E), kThreads, Cfg<kDown>::SMEM, s>>>(
-        tA, tB0s, tB0, tB1s, tB1, a);
+    const int grid = grid_for(ctas, n_assign, a.m_tiles, E);
+    if (seg)
+        grouped_gemm_kernel<kDown, true><<<grid, Cfg<kDown, true>::THREADS, Cfg<kDown, true>::SMEM, s>>>(
+            tA, tB0s, tB0, tB1s, tB1, a);
+    else
+        grouped_gemm_kernel<kDown><<<grid, kThreads, Cfg<kDown>::SMEM, s>>>(tA, tB0s, tB0, tB1s, tB1, a);
     return cudaPeekAtLastError();
 }
 

@@ -112,16 +112,18 @@ constexpr unsigned long long kDecodeFusedWaitNs = 2000000000ull;  // default bou
 unsigned long long current_context_id();
 
 // grouped_gemm.cu
+// seg: the instances that add segments of K in FP32 (the calls that take the
+// routing from the caller)
 cudaError_t gemm_init_device();
 bool gemm_supported(int H, int I, int E);
 // gate_up reads the chunk's token rows from x [T, H] by perm (row p of the
 // sorted order is token perm[p] / k)
 cudaError_t launch_gemm_gate_up(const void *x, const int32_t *perm, int k, const void *wgu, const int4 *chunks,
                                 const int32_t *nchunks, const int32_t *offs, int n_assign, int H, int I, int E,
-                                void *act_hi, void *act_lo, int ctas, cudaStream_t s);
+                                void *act_hi, void *act_lo, int ctas, cudaStream_t s, bool seg = false);
 cudaError_t launch_gemm_down(const void *act_hi, const void *act_lo, const void *wd, const int4 *chunks,
                              const int32_t *nchunks, const int32_t *offs, int n_assign, int H, int I, int E, float *z,
-                             int ctas, cudaStream_t s);
+                             int ctas, cudaStream_t s, bool seg = false);
 cudaError_t read_fault_word(uint32_t *flags, bool clear);
 // The same two GEMMs with MXFP8 weights: E4M3 codes gq [E, 2I, H] / dq
 // [E, H, I] and E8M0 scales gs [E, 2I, mx_scale_bytes(H)] / ds [E, H,
@@ -138,12 +140,13 @@ cudaError_t launch_gemm_down_mx(const void *act_hi, const void *act_lo, const vo
 // gate_up_raw: g = W_gate x, u = W_up x [rows][I] FP32.
 cudaError_t launch_gemm_gate_up_raw(const void *x, const int32_t *perm, int k, const void *wgu, const int4 *chunks,
                                     const int32_t *nchunks, const int32_t *offs, int n_rows, int H, int I, int E,
-                                    float *g, float *u, int ctas, cudaStream_t s);
+                                    float *g, float *u, int ctas, cudaStream_t s, bool seg = false);
 // The forward gate_up GEMM (act as a BF16 hi/lo pair) that also keeps g and
 // u [n_rows][I] in FP32 for a later backward pass (the training forward).
 cudaError_t launch_gemm_gate_up_keep(const void *x, const int32_t *perm, int k, const void *wgu, const int4 *chunks,
                                      const int32_t *nchunks, const int32_t *offs, int n_rows, int H, int I, int E,
-                                     void *act_hi, void *act_lo, float *g, float *u, int ctas, cudaStream_t s);
+                                     void *act_hi, void *act_lo, float *g, float *u, int ctas, cudaStream_t s,
+                                     bool seg = false);
 // q = W_down^T dout (dout as ds_hi + ds_lo [rows][H]) and the SwiGLU
 // backward: in g, u, w_s; out dgu_hi/lo [rows][2I], wa_hi/lo [rows][I]
 // (BF16 pairs) and dwp [rows][I/32] (partial sums of act . q)
@@ -154,11 +157,11 @@ struct BwdQOut {
 };
 cudaError_t launch_bwd_q(const void *ds_hi, const void *ds_lo, const void *wd, const int4 *chunks,
                          const int32_t *nchunks, const int32_t *offs, int n_rows, int H, int I, int E,
-                         const BwdQOut &o, int ctas, cudaStream_t s);
+                         const BwdQOut &o, int ctas, cudaStream_t s, bool seg = false);
 // z [rows][H] = W_gate_up^T (dgu_hi + dgu_lo)
 cudaError_t launch_bwd_dx(const void *dgu_hi, const void *dgu_lo, const void *wgu, const int4 *chunks,
                           const int32_t *nchunks, const int32_t *offs, int n_rows, int H, int I, int E, float *z,
-                          int ctas, cudaStream_t s);
+                          int ctas, cudaStream_t s, bool seg = false);
 
 // grouped_bwd.cu
 cudaError_t bwd_init_device();

@@ -309,9 +309,9 @@ int run_forward(const void *x, const float *logits, const void *wgu, const void 
                                                       n_assign, H, I, E, z, gemm_ctas, stream)));
         } else {
             MOE_TRY(stg.done(moe::launch_gemm_gate_up(x, perm, k, wgu, chunks, nchunks, offs, n_assign, H, I, E,
-                                                      act_hi, act_lo, gemm_ctas, stream)));
+                                                      act_hi, act_lo, gemm_ctas, stream, routing != nullptr)));
             MOE_TRY(stg.done(moe::launch_gemm_down(act_hi, act_lo, wd, chunks, nchunks, offs, n_assign, H, I, E, z,
-                                                   gemm_ctas, stream)));
+                                                   gemm_ctas, stream, routing != nullptr)));
         }
         MOE_TRY(stg.done(moe::launch_combine(z, w, pos, T, H, k, out, dev->n_sm, stream)));
     }
@@ -392,6 +392,7 @@ int run_backward(const void *x, const float *logits, const void *wgu, const void
     const int T = (int)s.T, H = (int)s.H, I = (int)s.I, E = (int)s.E, k = (int)s.k;
     const int rows = (int)L.rows;
     const int ctas = (opts && opts->gemm_ctas) ? opts->gemm_ctas : dev->n_sm;
+    const bool seg = routing != nullptr;
     auto *idx = (int32_t *)(ws + L.idx);
     auto *w = (float *)(ws + L.w);
     auto *offs = (int32_t *)(ws + L.offs);
@@ -417,12 +418,12 @@ int run_backward(const void *x, const float *logits, const void *wgu, const void
                                           ws + L.ds_lo, w_s, dev->n_sm, stream)));
     if (recompute)
         MOE_TRY(stg.done(moe::launch_gemm_gate_up_raw(x, perm, k, wgu, chunks, nchunks, offs, rows, H, I, E, g, u,
-                                                      ctas, stream)));
+                                                      ctas, stream, seg)));
     const moe::BwdQOut qo{g, u, w_s, ws + L.dgu_hi, ws + L.dgu_lo, ws + L.wa_hi, ws + L.wa_lo, dwp};
     MOE_TRY(stg.done(moe::launch_bwd_q(ws + L.ds_hi, ws + L.ds_lo, wd, chunks, nchunks, offs, rows, H, I, E, qo, ctas,
-                                       stream)));
+                                       stream, seg)));
     MOE_TRY(stg.done(moe::launch_bwd_dx(ws + L.dgu_hi, ws + L.dgu_lo, wgu, chunks, nchunks, offs, rows, H, I, E, z,
-                                        ctas, stream)));
+                                        ctas, stream, seg)));
     MOE_TRY(stg.done(moe::launch_combine(z, nullptr, pos, T, H, k, dx, dev->n_sm, stream)));
     MOE_TRY(stg.done(moe::launch_zero_untouched(counts, E, H, I, dwgu, dwd, dev->n_sm, stream)));
     MOE_TRY(stg.done(moe::launch_wgrad_down(ws + L.ds_hi, ws + L.ds_lo, ws + L.wa_hi, ws + L.wa_lo, offs, counts,
@@ -454,6 +455,7 @@ int run_forward_train(const void *x, const float *logits, const void *wgu, const
     const int T = (int)s.T, H = (int)s.H, I = (int)s.I, E = (int)s.E, k = (int)s.k;
     const int rows = (int)L.rows;
     const int ctas = (opts && opts->gemm_ctas) ? opts->gemm_ctas : dev->n_sm;
+    const bool seg = routing != nullptr;
     auto *idx = (int32_t *)(ws + L.idx);
     auto *w = (float *)(ws + L.w);
     auto *offs = (int32_t *)(ws + L.offs);
@@ -473,9 +475,9 @@ int run_forward_train(const void *x, const float *logits, const void *wgu, const
                                       (int32_t *)(ws + L.ucount), chunks, nchunks, stream, 16, counts)));
     MOE_TRY(stg.done(moe::launch_gemm_gate_up_keep(x, perm, k, wgu, chunks, nchunks, offs, rows, H, I, E,
                                                    ws + L.wa_hi, ws + L.wa_lo, (float *)(ws + L.g),
-                                                   (float *)(ws + L.u), ctas, stream)));
+                                                   (float *)(ws + L.u), ctas, stream, seg)));
     MOE_TRY(stg.done(moe::launch_gemm_down(ws + L.wa_hi, ws + L.wa_lo, wd, chunks, nchunks, offs, rows, H, I, E, z,
-                                           ctas, stream)));
+                                           ctas, stream, seg)));
     MOE_TRY(stg.done(moe::launch_combine(z, w, pos, T, H, k, out, dev->n_sm, stream)));
     if (opts) {
         opts->n_stages = stg.n;
