@@ -54,7 +54,9 @@ int check_gate(int64_t T, int64_t E, int64_t k, const moe_gate_opts *o, Gate *g)
 bool ortho_shape(int64_t B, int64_t M, int64_t N)
 {
     return B >= 0 && B <= 65535 && M >= 1 && N >= 1 && M <= 32768 && N <= 32768 &&
-           B <= ((int64_t)1 << 40) / (M * N);
+           B <= ((int64_t)1 << 40) / (M * N) &&
+           // the list of tiles, 3 products and 32 steps, is indexed in 32 bits
+           B * ((M + 127) / 128) * ((N + 127) / 128) <= ((int64_t)1 << 24);
 }
 
 }  // namespace

@@ -6,10 +6,10 @@
 //   gram     A  = X X^T                    [m, m]
 //   poly     Bm = b A + c A A              [m, m]
 //   apply    X  = a X + Bm X               [m, n]
-// Each is one launch over the whole batch.  A and Bm are symmetric: only the
-// tiles on and above the diagonal are computed, the others written as their
-// mirror images, which takes a step from 4 m^2 n + 2 m^3 operations to
-// 3 m^2 n + m^3 (and the diagonal tiles' other halves).
+// A and Bm are symmetric: only the tiles on and above the diagonal are
+// computed, the others written as their mirror images, which takes a step
+// from 4 m^2 n + 2 m^3 operations to 3 m^2 n + m^3 (and the diagonal tiles'
+// other halves).
 //
 // Numbers.  BF16 operands lose too much here (a polynomial whose slope at
 // zero is 3.4 raises the rounding noise of the small singular values with
@@ -33,6 +33,18 @@
 // The epilogue moves its operands and results through shared memory by TMA
 // (32 x 64 blocks), the mirror images by plain stores (a warp's 32 lanes are
 // 32 consecutive elements of a mirrored row).
+//
+// One launch.  All steps are one cooperative launch of one pair per two SMs:
+// the tiles of all products form a list (step by step, gram, poly, apply,
+// matrix by matrix), pair p takes tiles p, p + pairs, ...  A matrix's tiles
+// of one product need all of its tiles of the one before: every epilogue
+// warp adds one to the matrix's counter when its part of a tile has been
+// written, and the loads of a later tile wait for the count.  A waiting tile
+// only needs tiles that come before it in the list, and every pair is
+// resident, so the list moves on; with several matrices the tail of one
+// product is filled by the next one's first tiles, where a launch per
+// product left pairs idle (16 matrices of 1536 x 2048: 4.4 and 10.1 waves
+// rounded up to 5 and 11).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -64,6 +76,8 @@ constexpr int kEpiWarps = 8;
 constexpr int BLOCK = 32 * 64 * 2;        // one staged 32 x 64 FP16 block
 constexpr uint64_t kWaitNs = 2000000000ull;
 
+constexpr uint32_t kWarpsPerTile = 2 * kEpiWarps;  // that count a tile as done
+
 enum : int { kGram = 0, kPoly = 1, kApply = 2, kLast = 3 };  // kLast: the last step's apply, into the output
 
 template <int BN>
@@ -76,17 +90,34 @@ struct Cfg {
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
+// The tensor maps over X (two hi buffers, used in turn, and lo), A and Bm:
+// left operands (K-major, box 64 x 128 rows), right ones (K-major, box 64 x
+// BN / 2 rows; X's columns, MN-major, box 64 x 64 rows) and the epilogue's
+// blocks (64 x 32 rows).
+struct OrthoMaps {
+    CUtensorMap x_left[2], x_right[2], x_cols[2], x_blk[2], lo_blk, a_left, a_right, a_blk, b_left, b_blk;
+};
+
 struct OrthoArgs {
-    int m, n, batch;       // X is [batch][m][n]
-    int rows, cols, depth; // of the product: rows x cols, K = depth
-    int row_tiles, col_tiles, tiles;  // tiles of one matrix (symmetric: on and above the diagonal)
-    float ca, cb, cc;      // the step's coefficients, powers of two folded in
-    __half *mirror;        // kGram, kPoly: the output, for the mirror images
-    int64_t mirror_pitch, mirror_matrix;  // elements per row, per matrix
-    __nv_bfloat16 *out;    // kLast
-    int out_cols;          // the caller's N
-    int transposed;        // kLast: out is [n][m]
-    float out_scale;
+    int m, n, batch, steps;  // X is [batch][m][n]
+    int group;               // matrices per group: a group's steps all come before the next group's
+    int row_tiles, sym_cols, x_cols;  // tiles of 256 rows, of BN columns of A and of X
+    int sym_tiles, x_tiles;  // per matrix: of a symmetric product (on and above the diagonal), of apply
+    // the factors of the epilogues, powers of two folded in: gram A = g acc;
+    // poly Bm = pb A + pc acc; apply X = xa X + xc acc; last: times out_scale
+    float g, pb, pc, xa, xc, out_scale;
+    __half *a, *bm;          // for the mirror images
+    int64_t pitch;           // elements per row of A and Bm
+    __nv_bfloat16 *out;
+    int out_cols;            // the caller's N
+    int transposed;          // out is [n][m]
+    uint32_t *done;          // [batch] the counters, zero before the launch
+};
+
+// A tile of the list.
+struct Tile {
+    int b, step, kind, r0, c0;  // matrix, step, product, first row and column
+    uint32_t need;              // the matrix's count that it waits for
 };
 
 // ------------------------------------------------------------ cluster and pair forms
@@ -206,20 +237,256 @@ __device__ __forceinline__ float2 half_unpair(uint32_t v)
     return __half22float2(*reinterpret_cast<const __half2 *>(&v));
 }
 
-// tmL, tmR: the left (K-major, box 64 x 128 rows) and right operand (K-major,
-// box 64 x BN / 2 rows; apply: MN-major, box 64 x 64 rows).  tmIn, tmInLo:
-// the epilogue's operands (poly: A; apply: X hi and lo), tmOut, tmOutLo: the
-// results (gram: A, poly: Bm, apply: X hi and lo), boxes of 64 x 32 rows.
-template <int KIND, int BN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    ortho_gemm_kernel(const __grid_constant__ CUtensorMap tmL, const __grid_constant__ CUtensorMap tmR,
-                      const __grid_constant__ CUtensorMap tmIn, const __grid_constant__ CUtensorMap tmInLo,
-                      const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmOutLo,
-                      const OrthoArgs args)
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t *p)
 {
-    using C = Cfg<BN>;
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+
+// Waits (bounded) until a matrix's count has reached `need`; what was counted
+// may then be read by TMA.
+__device__ __forceinline__ bool wait_count(const uint32_t *done, uint32_t need, const volatile int *abort)
+{
+    if (need == 0) return true;
+    if (ld_acquire(done) < need) {
+        const uint64_t t0 = ptx::globaltimer_ns();
+        while (ld_acquire(done) < need) {
+            if (*abort || ptx::globaltimer_ns() - t0 > kWaitNs) return false;
+            __nanosleep(100);
+        }
+    }
+    asm volatile("fence.proxy.async;" ::: "memory");
+    return true;
+}
+
+// Counts this warp's part of a tile, whose stores (TMA by lane 0, plain ones
+// by all lanes) are complete afterwards.  Whole warp.
+__device__ __forceinline__ void count_done(uint32_t *done, int lane)
+{
+    asm volatile("fence.proxy.async;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+        ptx::bulk_wait_all();
+        asm volatile("fence.proxy.async;" ::: "memory");
+        ptx::fence_acq_rel_gpu();
+        asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(done), "r"(1u) : "memory");
+    }
+}
+
+template <int BN>
+__device__ __forceinline__ Tile decode_tile(int i, const OrthoArgs &a)
+{
+    const int per_step = 2 * a.sym_tiles + a.x_tiles;  // of one matrix
+    const int per_group = per_step * a.steps * a.group;
+    const int grp = i / per_group;
+    i -= grp * per_group;
+    const int size = min(a.group, a.batch - grp * a.group);
+    Tile t;
+    t.step = i / (per_step * size);
+    i -= t.step * per_step * size;
+    const int sym = a.sym_tiles * size;
+    t.kind = i < sym ? kGram : i < 2 * sym ? kPoly : t.step + 1 < a.steps ? kApply : kLast;
+    i -= t.kind == kGram ? 0 : t.kind == kPoly ? sym : 2 * sym;
+    const int tiles = t.kind <= kPoly ? a.sym_tiles : a.x_tiles;
+    const int b = i / tiles;
+    i -= b * tiles;
+    t.b = grp * a.group + b;
+    t.need = kWarpsPerTile * (uint32_t)(t.step * per_step + (t.kind == kGram   ? 0
+                                                             : t.kind == kPoly ? a.sym_tiles
+                                                                               : 2 * a.sym_tiles));
+    if (t.kind <= kPoly) {
+        // row tile rt has the column tiles from the one that holds its first
+        // row's diagonal on
+        int rt = 0;
+        for (;; ++rt) {
+            const int from = rt * 256 / BN, here = a.sym_cols - from;
+            if (i < here) {
+                i += from;
+                break;
+            }
+            i -= here;
+        }
+        t.r0 = rt * 256;
+        t.c0 = i * BN;
+    } else {
+        // down the rows first: neighbouring pairs share the right operand
+        const int ct = i / a.row_tiles;
+        t.r0 = (i - ct * a.row_tiles) * 256;
+        t.c0 = ct * BN;
+    }
+    return t;
+}
+
+// What an epilogue warp carries along.
+struct Epilogue {
+    uint8_t *st, *st_lo;   // its staging blocks
+    uint64_t *bar;         // of the blocks' loads
+    uint32_t load_phase;
+    int q, half, lane;
+    uint32_t rank, tmem;
+};
+
+// One tile's epilogue for one warp: lane quarter q (rows r0 + 128 rank + 32 q
+// ..), columns half * BN / 2 ... in blocks of 64.  Lane l holds row l of a
+// block; its 16-byte piece j is at (j ^ (l % 8)) * 16 of the row's 128 bytes
+// in the staging buffer (the tensor maps' swizzle).  Returns false when a
+// wait gave up.
+template <int KIND, int BN>
+__device__ __forceinline__ bool epilogue(const Tile &t, const OrthoMaps &maps, const OrthoArgs &args, Epilogue &ep,
+                                         uint64_t *tfull, uint32_t tfull_phase, uint32_t acc_tmem, bool ready,
+                                         volatile int *abort_flag)
+{
     constexpr bool SYM = KIND == kGram || KIND == kPoly;
     constexpr bool PAIR_IN = KIND == kApply || KIND == kLast;
+    const int lane = ep.lane, x = t.step & 1;
+    const int rows = args.m, cols = SYM ? args.m : args.n;
+    const int row0 = t.r0 + 128 * (int)ep.rank + 32 * ep.q, row = row0 + lane;
+    const bool mirrored = SYM && t.r0 + 256 <= t.c0;  // wholly above the diagonal's tiles
+    uint8_t *const st = ep.st, *const st_lo = ep.st_lo;
+    bool have = false, failed = false;
+#pragma unroll 1
+    for (int blk = 0; blk < BN / 128; ++blk) {
+        const int cb = ep.half * (BN / 2) + 64 * blk, col0 = t.c0 + cb;
+        const bool in = ready && row0 < rows && col0 < cols;
+        // the block's own operands, while the products run
+        if (in && KIND != kGram) {
+            if (lane == 0) {
+                ptx::bulk_wait_group_read<0>();  // the buffers' last stores have read them
+                ptx::mbar_arrive_expect_tx(ep.bar, (PAIR_IN ? 2 : 1) * BLOCK);
+                ptx::tma_load_3d(st, PAIR_IN ? &maps.x_blk[x] : &maps.a_blk, col0, row0, t.b, ep.bar);
+                if (PAIR_IN) ptx::tma_load_3d(st_lo, &maps.lo_blk, col0, row0, t.b, ep.bar);
+            }
+            __syncwarp();
+        }
+        if (!have) {
+            have = true;
+            failed = !ready || *abort_flag || !wait_cluster(tfull, tfull_phase, abort_flag);
+            failed = __any_sync(0xffffffffu, failed);
+            ptx::tc_fence_after();
+        }
+        if (in && KIND != kGram) {
+            const int keep = 0;
+            const bool got = ptx::mbar_wait_bounded(ep.bar, ep.load_phase, &keep, kWaitNs);
+            ep.load_phase ^= 1;
+            failed = __any_sync(0xffffffffu, failed || !got);
+        }
+        if (failed) return false;
+        if (!in) continue;
+        if (KIND == kGram) {
+            if (lane == 0) ptx::bulk_wait_group_read<0>();
+            __syncwarp();
+        }
+        const uint32_t taddr = acc_tmem + ((uint32_t)(32 * ep.q) << 16) + cb;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t r[32];
+            ptx::tmem_ld32(taddr + 32 * h, r);
+            ptx::tmem_wait_ld();
+            float v[32];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int at = lane * 128 + (((4 * h + j) ^ (lane & 7)) << 4);
+                uint4 *p = reinterpret_cast<uint4 *>(st + at), *p_lo = reinterpret_cast<uint4 *>(st_lo + at);
+                uint32_t in_w[4] = {0, 0, 0, 0}, lo_w[4] = {0, 0, 0, 0}, o[4], o_lo[4];
+                if (KIND != kGram) {
+                    const uint4 w = *p;
+                    in_w[0] = w.x, in_w[1] = w.y, in_w[2] = w.z, in_w[3] = w.w;
+                }
+                if (PAIR_IN) {
+                    const uint4 w = *p_lo;
+                    lo_w[0] = w.x, lo_w[1] = w.y, lo_w[2] = w.z, lo_w[3] = w.w;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = 8 * j + 2 * e;
+                    const float a0 = __uint_as_float(r[c]), a1 = __uint_as_float(r[c + 1]);
+                    float v0, v1;
+                    if (KIND == kGram) {
+                        v0 = a0 * args.g, v1 = a1 * args.g;
+                    } else if (KIND == kPoly) {
+                        const float2 y = half_unpair(in_w[e]);
+                        v0 = fmaf(args.pc, a0, args.pb * y.x), v1 = fmaf(args.pc, a1, args.pb * y.y);
+                    } else {
+                        const float2 y = half_unpair(in_w[e]), z = half_unpair(lo_w[e]);
+                        v0 = fmaf(args.xc, a0, args.xa * (y.x + z.x));
+                        v1 = fmaf(args.xc, a1, args.xa * (y.y + z.y));
+                    }
+                    if (KIND == kLast) v0 *= args.out_scale, v1 *= args.out_scale;
+                    v[c] = v0, v[c + 1] = v1;
+                    if (KIND == kLast) {
+                        const __nv_bfloat162 z = __floats2bfloat162_rn(v0, v1);
+                        o[e] = *reinterpret_cast<const uint32_t *>(&z);
+                    } else {
+                        o[e] = half_pair(v0, v1);
+                    }
+                    if (KIND == kApply) {
+                        const float2 hi = half_unpair(o[e]);
+                        o_lo[e] = half_pair(v0 - hi.x, v1 - hi.y);
+                    }
+                }
+                *p = make_uint4(o[0], o[1], o[2], o[3]);
+                if (KIND == kApply) *p_lo = make_uint4(o_lo[0], o_lo[1], o_lo[2], o_lo[3]);
+            }
+            const int c = col0 + 32 * h;
+            if (mirrored && row < rows) {
+                __half *dst = (KIND == kGram ? args.a : args.bm) + (int64_t)t.b * args.m * args.pitch + row;
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (c + e < cols) dst[(c + e) * args.pitch] = __float2half_rn(v[e]);
+            }
+            if (KIND == kLast && args.transposed && row < rows) {
+                __nv_bfloat16 *dst = args.out + (int64_t)t.b * rows * cols + row;
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (c + e < cols) dst[(int64_t)(c + e) * args.out_cols] = __float2bfloat16_rn(v[e]);
+            }
+        }
+        if (KIND == kLast) {
+            // the caller's rows have any pitch: from the staging buffer, a
+            // row's 64 elements at a time, two per lane
+            __syncwarp();
+            if (!args.transposed) {
+                const int c = col0 + 2 * lane;
+                __nv_bfloat16 *dst = args.out + (int64_t)t.b * rows * cols + c;
+                for (int rr = 0; rr < 32 && row0 + rr < rows; ++rr) {
+                    const uint32_t w = *reinterpret_cast<const uint32_t *>(
+                        st + rr * 128 + (((lane >> 2) ^ (rr & 7)) << 4) + (lane & 3) * 4);
+                    __nv_bfloat16 *d = dst + (int64_t)(row0 + rr) * args.out_cols;
+                    const __nv_bfloat162 z = *reinterpret_cast<const __nv_bfloat162 *>(&w);
+                    if (args.out_cols % 2 == 0) {
+                        if (c < cols) *reinterpret_cast<__nv_bfloat162 *>(d) = z;
+                    } else {
+                        if (c < cols) d[0] = z.x;
+                        if (c + 1 < cols) d[1] = z.y;
+                    }
+                }
+            }
+            // the next block's TMA load overwrites what the warp has read
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+        } else {
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                // rows and columns past the matrix are not written by the stores
+                ptx::tma_store_3d(KIND == kGram   ? &maps.a_blk
+                                  : KIND == kPoly ? &maps.b_blk
+                                                  : &maps.x_blk[x ^ 1],
+                                  st, col0, row0, t.b);
+                if (KIND == kApply) ptx::tma_store_3d(&maps.lo_blk, st_lo, col0, row0, t.b);
+                ptx::bulk_commit_group();
+            }
+        }
+    }
+    return true;
+}
+
+template <int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    ortho_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant__ OrthoArgs args)
+{
+    using C = Cfg<BN>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *staging = smem + C::STAGES * C::STAGE_BYTES;
@@ -234,7 +501,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
-    ptx::griddep_launch_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
             ptx::mbar_init(full + s, 1);
@@ -242,16 +508,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(tfull + b, 1);
-            ptx::mbar_init(tempty + b, 2 * kEpiWarps);
+            ptx::mbar_init(tempty + b, kWarpsPerTile);
         }
         ptx::mbar_init(drain, 1);
         for (int w = 0; w < kEpiWarps; ++w) ptx::mbar_init(loaded + w, 1);
         *abort_flag = 0;
         ptx::fence_barrier_init();
-        ptx::prefetch_tensormap(&tmL);
-        ptx::prefetch_tensormap(&tmR);
-        if (KIND != kGram) ptx::prefetch_tensormap(&tmIn);
-        if (KIND != kLast) ptx::prefetch_tensormap(&tmOut);
     }
     __syncwarp();
     if (warp == 1) pair_tmem_alloc(tmem_slot, 2 * BN);
@@ -259,47 +521,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     cluster_sync();  // barriers initialised and TMEM allocated in both CTAs
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    ptx::griddep_wait();  // the previous launch's results, its plain stores too
-    asm volatile("fence.proxy.async;" ::: "memory");
 
-    const int clusters = gridDim.x / 2, first = blockIdx.x / 2;
-    const int total = args.tiles * args.batch;
-    const int ksteps = (args.depth + BK - 1) / BK;
-    // tile i: its matrix, first row and first column
-    auto decode = [&](int i, int &b, int &r0, int &c0) {
-        b = i / args.tiles;
-        int rem = i - b * args.tiles;
-        if (SYM) {
-            // row tile rt has the column tiles from the one that holds its
-            // first row's diagonal on
-            int rt = 0;
-            for (;; ++rt) {
-                const int from = rt * 256 / BN, here = args.col_tiles - from;
-                if (rem < here) {
-                    rem += from;
-                    break;
-                }
-                rem -= here;
-            }
-            r0 = rt * 256;
-            c0 = rem * BN;
-        } else {
-            // down the rows first: neighbouring clusters share the right operand
-            const int ct = rem / args.row_tiles;
-            r0 = (rem - ct * args.row_tiles) * 256;
-            c0 = ct * BN;
-        }
-    };
+    const int pairs = gridDim.x / 2, first = blockIdx.x / 2;
+    const int total = args.batch * args.steps * (2 * args.sym_tiles + args.x_tiles);
 
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
-            for (int i = first; i < total && !*abort_flag; i += clusters) {
-                int b, r0, c0;
-                decode(i, b, r0, c0);
-                const int row = r0 + 128 * (int)rank, col = c0 + BN / 2 * (int)rank;
+            for (int i = first; i < total && !*abort_flag; i += pairs) {
+                const Tile t = decode_tile<BN>(i, args);
+                const bool apply = t.kind >= kApply;
+                const int x = t.step & 1;
+                const CUtensorMap *left = t.kind == kGram   ? &maps.x_left[x]
+                                          : t.kind == kPoly ? &maps.a_left
+                                                            : &maps.b_left;
+                const CUtensorMap *right = t.kind == kGram   ? &maps.x_right[x]
+                                           : t.kind == kPoly ? &maps.a_right
+                                                             : &maps.x_cols[x];
+                const int ksteps = ((t.kind == kGram ? args.n : args.m) + BK - 1) / BK;
+                const int row = t.r0 + 128 * (int)rank, col = t.c0 + BN / 2 * (int)rank;
+                if (!wait_count(args.done + t.b, t.need, abort_flag)) {
+                    if (!*abort_flag) raise(FAULT_GEMM_PRODUCER);
+                    *abort_flag = 1;
+                    break;
+                }
                 for (int ks = 0; ks < ksteps; ++ks) {
                     if (!wait_cluster(empty + stage, phase ^ 1, abort_flag)) {
                         if (!*abort_flag) raise(FAULT_GEMM_PRODUCER);
@@ -311,13 +558,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (rank == 0) ptx::mbar_arrive_expect_tx(full + stage, 2 * C::STAGE_BYTES);
                     uint8_t *l = smem + stage * C::STAGE_BYTES;
                     uint8_t *r = l + A_BYTES;
-                    pair_load_3d(l, &tmL, ks * BK, row, b, bar);
-                    if (PAIR_IN) {
+                    pair_load_3d(l, left, ks * BK, row, t.b, bar);
+                    if (apply) {
 #pragma unroll
                         for (int h = 0; h < BN / 128; ++h)
-                            pair_load_3d(r + h * (64 * BK * 2), &tmR, col + 64 * h, ks * BK, b, bar);
+                            pair_load_3d(r + h * (64 * BK * 2), right, col + 64 * h, ks * BK, t.b, bar);
                     } else {
-                        pair_load_3d(r, &tmR, ks * BK, col, b, bar);
+                        pair_load_3d(r, right, ks * BK, col, t.b, bar);
                     }
                     if (++stage == C::STAGES) {
                         stage = 0;
@@ -337,8 +584,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int stage = 0;
             uint32_t phase = 0;
             int li = 0;
-            constexpr uint32_t idesc = idesc_f16(BN, PAIR_IN);
-            for (int i = first; i < total && !*abort_flag; i += clusters, ++li) {
+            for (int i = first; i < total && !*abort_flag; i += pairs, ++li) {
+                const Tile t = decode_tile<BN>(i, args);
+                const bool apply = t.kind >= kApply;
+                const int ksteps = ((t.kind == kGram ? args.n : args.m) + BK - 1) / BK;
+                const uint32_t idesc = idesc_f16(BN, apply);
                 const int acc = li & 1;
                 if (!wait_cluster(tempty + acc, ((li >> 1) & 1) ^ 1, abort_flag)) {
                     if (!*abort_flag) raise(FAULT_GEMM_MMA);
@@ -361,7 +611,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int k = 0; k < BK / 16; ++k)
                         pair_mma(d, ptx::sw128_desc(l + k * 32),
-                                 PAIR_IN ? ptx::sw128_desc_mn(r + k * 2048, 64 * BK * 2) : ptx::sw128_desc(r + k * 32),
+                                 apply ? ptx::sw128_desc_mn(r + k * 2048, 64 * BK * 2) : ptx::sw128_desc(r + k * 32),
                                  idesc, (ks | k) != 0);
                     pair_commit(empty + stage);
                     if (++stage == C::STAGES) {
@@ -378,166 +628,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else {
         // ---------------------------------------------------- epilogue
-        // warps 2..9: TMEM lane quarter warp % 4 (rows r0 + 128 rank + 32 q
-        // ..), columns half * BN / 2 ... in blocks of 64.  Lane l holds row l
-        // of a block; its 16-byte piece j is at (j ^ (l % 8)) * 16 of the
-        // row's 128 bytes in the staging buffer (the tensor maps' swizzle).
-        const int q = warp & 3, half = (warp - 2) >> 2;
-        uint8_t *st = staging + (warp - 2) * 2 * BLOCK, *st_lo = st + BLOCK;
-        uint64_t *bar = loaded + (warp - 2);
-        uint32_t load_phase = 0;
+        Epilogue ep;
+        ep.st = staging + (warp - 2) * 2 * BLOCK;
+        ep.st_lo = ep.st + BLOCK;
+        ep.bar = loaded + (warp - 2);
+        ep.load_phase = 0;
+        ep.q = warp & 3;
+        ep.half = (warp - 2) >> 2;
+        ep.lane = lane;
+        ep.rank = rank;
+        ep.tmem = tmem;
         int li = 0;
-        for (int i = first; i < total; i += clusters, ++li) {
-            int b, r0, c0;
-            decode(i, b, r0, c0);
-            const int row0 = r0 + 128 * (int)rank + 32 * q, row = row0 + lane;
-            const bool mirrored = SYM && r0 + 256 <= c0;  // a tile wholly above the diagonal's tiles
+        for (int i = first; i < total; i += pairs, ++li) {
+            const Tile t = decode_tile<BN>(i, args);
             const int acc = li & 1;
-            bool have = false, failed = false;
-#pragma unroll 1
-            for (int blk = 0; blk < BN / 128; ++blk) {
-                const int cb = half * (BN / 2) + 64 * blk, col0 = c0 + cb;
-                const bool in = row0 < args.rows && col0 < args.cols;
-                // the block's own operands, while the products run
-                if (in && KIND != kGram) {
-                    if (lane == 0) {
-                        ptx::bulk_wait_group_read<0>();  // the buffers' last stores have read them
-                        ptx::mbar_arrive_expect_tx(bar, (PAIR_IN ? 2 : 1) * BLOCK);
-                        ptx::tma_load_3d(st, &tmIn, col0, row0, b, bar);
-                        if (PAIR_IN) ptx::tma_load_3d(st_lo, &tmInLo, col0, row0, b, bar);
-                    }
-                    __syncwarp();
-                }
-                if (!have) {
-                    have = true;
-                    if (*abort_flag || !wait_cluster(tfull + acc, (li >> 1) & 1, abort_flag)) {
-                        if (!*abort_flag) raise(FAULT_GEMM_EPILOGUE);
-                        *abort_flag = 1;
-                        failed = true;
-                    }
-                    failed = __any_sync(0xffffffffu, failed);
-                    ptx::tc_fence_after();
-                }
-                if (in && KIND != kGram) {
-                    const int keep = 0;
-                    if (!ptx::mbar_wait_bounded(bar, load_phase, &keep, kWaitNs)) {
-                        if (!*abort_flag) raise(FAULT_GEMM_EPILOGUE);
-                        *abort_flag = 1;
-                        failed = true;
-                    }
-                    load_phase ^= 1;
-                    failed = __any_sync(0xffffffffu, failed);
-                }
-                if (failed) break;
-                if (!in) continue;
-                if (KIND == kGram) {
-                    if (lane == 0) ptx::bulk_wait_group_read<0>();
-                    __syncwarp();
-                }
-                const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + acc * BN + cb;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t r[32];
-                    ptx::tmem_ld32(taddr + 32 * h, r);
-                    ptx::tmem_wait_ld();
-                    float v[32];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int at = lane * 128 + (((4 * h + j) ^ (lane & 7)) << 4);
-                        uint4 *p = reinterpret_cast<uint4 *>(st + at), *p_lo = reinterpret_cast<uint4 *>(st_lo + at);
-                        uint32_t in_w[4] = {0, 0, 0, 0}, lo_w[4] = {0, 0, 0, 0}, o[4], o_lo[4];
-                        if (KIND != kGram) {
-                            const uint4 w = *p;
-                            in_w[0] = w.x, in_w[1] = w.y, in_w[2] = w.z, in_w[3] = w.w;
-                        }
-                        if (PAIR_IN) {
-                            const uint4 w = *p_lo;
-                            lo_w[0] = w.x, lo_w[1] = w.y, lo_w[2] = w.z, lo_w[3] = w.w;
-                        }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int c = 8 * j + 2 * e;
-                            const float a0 = __uint_as_float(r[c]), a1 = __uint_as_float(r[c + 1]);
-                            float v0, v1;
-                            if (KIND == kGram) {
-                                v0 = a0 * args.cc, v1 = a1 * args.cc;
-                            } else if (KIND == kPoly) {
-                                const float2 x = half_unpair(in_w[e]);
-                                v0 = fmaf(args.cc, a0, args.cb * x.x), v1 = fmaf(args.cc, a1, args.cb * x.y);
-                            } else {
-                                const float2 x = half_unpair(in_w[e]), y = half_unpair(lo_w[e]);
-                                v0 = fmaf(args.cc, a0, args.ca * (x.x + y.x));
-                                v1 = fmaf(args.cc, a1, args.ca * (x.y + y.y));
-                            }
-                            v[c] = v0, v[c + 1] = v1;
-                            if (KIND == kLast) {
-                                const __nv_bfloat162 z = __floats2bfloat162_rn(v0 * args.out_scale, v1 * args.out_scale);
-                                o[e] = *reinterpret_cast<const uint32_t *>(&z);
-                            } else {
-                                o[e] = half_pair(v0, v1);
-                            }
-                            if (KIND == kApply) {
-                                const float2 hi = half_unpair(o[e]);
-                                o_lo[e] = half_pair(v0 - hi.x, v1 - hi.y);
-                            }
-                        }
-                        *p = make_uint4(o[0], o[1], o[2], o[3]);
-                        if (KIND == kApply) *p_lo = make_uint4(o_lo[0], o_lo[1], o_lo[2], o_lo[3]);
-                    }
-                    if (mirrored && row < args.rows) {
-                        __half *dst = args.mirror + b * args.mirror_matrix + row;
-                        const int c = col0 + 32 * h;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (c + e < args.cols) dst[(c + e) * args.mirror_pitch] = __float2half_rn(v[e]);
-                    }
-                    if (KIND == kLast && args.transposed && row < args.rows) {
-                        __nv_bfloat16 *dst = args.out + (int64_t)b * args.rows * args.cols + row;
-                        const int c = col0 + 32 * h;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (c + e < args.cols)
-                                dst[(int64_t)(c + e) * args.out_cols] = __float2bfloat16_rn(v[e] * args.out_scale);
-                    }
-                }
-                if (KIND == kLast) {
-                    // the caller's rows have any pitch: from the staging buffer,
-                    // a row's 64 elements at a time, two per lane
-                    __syncwarp();
-                    if (!args.transposed) {
-                        const int c = col0 + 2 * lane;
-                        __nv_bfloat16 *dst = args.out + (int64_t)b * args.rows * args.cols + c;
-                        for (int rr = 0; rr < 32 && row0 + rr < args.rows; ++rr) {
-                            const uint32_t w = *reinterpret_cast<const uint32_t *>(
-                                st + rr * 128 + (((lane >> 2) ^ (rr & 7)) << 4) + (lane & 3) * 4);
-                            __nv_bfloat16 *d = dst + (int64_t)(row0 + rr) * args.out_cols;
-                            const __nv_bfloat162 z = *reinterpret_cast<const __nv_bfloat162 *>(&w);
-                            if (args.out_cols % 2 == 0) {
-                                if (c < args.cols) *reinterpret_cast<__nv_bfloat162 *>(d) = z;
-                            } else {
-                                if (c < args.cols) d[0] = z.x;
-                                if (c + 1 < args.cols) d[1] = z.y;
-                            }
-                        }
-                    }
-                    // the next block's TMA load overwrites what the warp has read
-                    ptx::fence_proxy_async_smem();
-                    __syncwarp();
-                } else {
-                    ptx::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        // rows and columns past the matrix are not written by the stores
-                        ptx::tma_store_3d(&tmOut, st, col0, row0, b);
-                        if (KIND == kApply) ptx::tma_store_3d(&tmOutLo, st_lo, col0, row0, b);
-                        ptx::bulk_commit_group();
-                    }
-                }
+            const uint32_t ph = (li >> 1) & 1, at = tmem + acc * BN;
+            // the tile's own operands are complete (gram has none)
+            bool ready = true;
+            if (t.kind != kGram) {
+                if (lane == 0) ready = wait_count(args.done + t.b, t.need, abort_flag);
+                ready = __shfl_sync(0xffffffffu, ready, 0);
             }
-            if (failed) break;
+            bool ok;
+            if (t.kind == kGram)
+                ok = epilogue<kGram, BN>(t, maps, args, ep, tfull + acc, ph, at, ready, abort_flag);
+            else if (t.kind == kPoly)
+                ok = epilogue<kPoly, BN>(t, maps, args, ep, tfull + acc, ph, at, ready, abort_flag);
+            else if (t.kind == kApply)
+                ok = epilogue<kApply, BN>(t, maps, args, ep, tfull + acc, ph, at, ready, abort_flag);
+            else
+                ok = epilogue<kLast, BN>(t, maps, args, ep, tfull + acc, ph, at, ready, abort_flag);
+            if (!ok) {
+                if (lane == 0) {
+                    if (!*abort_flag) raise(FAULT_GEMM_EPILOGUE);
+                    *abort_flag = 1;
+                }
+                break;
+            }
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_cluster(map_to(ptx::smem_u32(tempty + acc), 0));
+            count_done(args.done + t.b, lane);
         }
         if (lane == 0) ptx::bulk_wait_all();
         __syncwarp();
@@ -553,41 +684,141 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- the input
 constexpr int kMaxParts = 64;
+// G is read twice, for its norm and to be scaled: matrices are taken in turns
+// of at most this many bytes, so that the second read comes from L2.
+constexpr int64_t kTurnBytes = 48 << 20;
+
+// 8 consecutive elements, 16-byte aligned (BF16) or 32 (FP32)
+__device__ __forceinline__ void load8(const float *p, float (&v)[8])
+{
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8])
+{
+    unpack8(__ldg(reinterpret_cast<const uint4 *>(p)), v);
+}
 
 // partial[b][p]: the sum of squares of a slice of matrix b.
 template <typename T>
 __global__ void __launch_bounds__(256) ortho_norm_kernel(const T *__restrict__ g, int64_t count,
-                                                         float *__restrict__ partial)
+                                                         float *__restrict__ partial, uint32_t *__restrict__ done)
 {
     __shared__ float sums[8];
-    const T *p = g + (int64_t)blockIdx.y * count;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    const int64_t stride = (int64_t)gridDim.x * 256;
-    int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    for (; i + 3 * stride < count; i += 4 * stride) {
+    const int b = blockIdx.y;
+    const T *p = g + (int64_t)b * count;
+    float s[8] = {};
+    const int64_t stride = (int64_t)gridDim.x * 256, start = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (count % 8 == 0) {
+        const int64_t n = count / 8;
+        auto add = [&](const float(&v)[8]) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float v = (float)p[i + q * stride];
-            s[q] = fmaf(v, v, s[q]);
+            for (int q = 0; q < 8; ++q) s[q] = fmaf(v[q], v[q], s[q]);
+        };
+        int64_t i = start;
+        for (; i + 3 * stride < n; i += 4 * stride) {  // four loads in flight
+            float v[4][8];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) load8(p + 8 * (i + u * stride), v[u]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) add(v[u]);
+        }
+        for (; i < n; i += stride) {
+            float v[8];
+            load8(p + 8 * i, v);
+            add(v);
+        }
+    } else {
+        for (int64_t i = start; i < count; i += stride) {
+            const float v = (float)p[i];
+            s[0] = fmaf(v, v, s[0]);
         }
     }
-    for (; i < count; i += stride) {
-        const float v = (float)p[i];
-        s[0] = fmaf(v, v, s[0]);
-    }
-    const float t = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
+    const float t = warp_sum(((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7])));
     if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = t;
     __syncthreads();
     if (threadIdx.x == 0) {
         float v = 0.0f;
 #pragma unroll
         for (int q = 0; q < 8; ++q) v += sums[q];
-        partial[blockIdx.y * kMaxParts + blockIdx.x] = v;
+        partial[b * kMaxParts + blockIdx.x] = v;
+        if (blockIdx.x == 0) done[b] = 0;  // for the products that follow
     }
 }
 
-// X hi and lo [b][m][pitch] from g [b][M][N], in 32 x 32 tiles (transposed
-// through shared memory where the matrix is tall).
+// 2^kXBits / (||G|| + eps) of a matrix from its partial sums.  Whole warp.
+__device__ __forceinline__ float input_factor(const float *partial, int parts, float eps)
+{
+    const int lane = threadIdx.x & 31;
+    float s = lane < parts ? __ldg(partial + lane) : 0.0f;
+    if (lane + 32 < parts) s += __ldg(partial + lane + 32);
+    static_assert(kMaxParts == 64, "two partial sums per lane");
+    return (float)(1 << kXBits) / (sqrtf(warp_sum(s)) + eps);
+}
+
+__device__ __forceinline__ void split8(const float (&v)[8], __half *hi, __half *lo)
+{
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        h[q] = half_pair(v[2 * q], v[2 * q + 1]);
+        const float2 f = half_unpair(h[q]);
+        l[q] = half_pair(v[2 * q] - f.x, v[2 * q + 1] - f.y);
+    }
+    *reinterpret_cast<uint4 *>(hi) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4 *>(lo) = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// X hi and lo [b][m][pitch] from g [b][M][N]: M and N multiples of 8.  WIDE:
+// the rows of X are those of g.  Else a block transposes 64 x 64 elements
+// through shared memory.
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(256) ortho_split8_kernel(const T *__restrict__ g, int M, int N,
+                                                           const float *__restrict__ partial, int parts, float eps,
+                                                           __half *__restrict__ hi, __half *__restrict__ lo)
+{
+    const int b = blockIdx.z;
+    const float f = input_factor(partial + b * kMaxParts, parts, eps);
+    const int64_t base = (int64_t)b * M * N;
+    if constexpr (WIDE) {
+        const int64_t n = (int64_t)M * N / 8, stride = (int64_t)gridDim.x * 256;
+        for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += stride) {
+            float v[8];
+            load8(g + base + 8 * i, v);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] *= f;
+            split8(v, hi + base + 8 * i, lo + base + 8 * i);
+        }
+    } else {
+        __shared__ float tile[64][65];
+        const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;  // in g
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int e = threadIdx.x + 256 * u, y = e >> 3, c = (e & 7) * 8;
+            if (r0 + y < M && c0 + c < N) {
+                float v[8];
+                load8(g + base + (int64_t)(r0 + y) * N + c0 + c, v);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) tile[y][c + q] = v[q] * f;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int e = threadIdx.x + 256 * u, y = e >> 3, c = (e & 7) * 8;  // row c0 + y of X
+            if (c0 + y < N && r0 + c < M) {
+                float v[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[q] = tile[c + q][y];
+                const int64_t at = base + (int64_t)(c0 + y) * M + r0 + c;
+                split8(v, hi + at, lo + at);
+            }
+        }
+    }
+}
+
+// The same for any M and N, in 32 x 32 tiles (X's rows have `pitch` elements).
 template <typename T>
 __global__ void __launch_bounds__(256) ortho_split_kernel(const T *__restrict__ g, int M, int N,
                                                           const float *__restrict__ partial, int parts, float eps,
@@ -596,9 +827,7 @@ __global__ void __launch_bounds__(256) ortho_split_kernel(const T *__restrict__ 
 {
     __shared__ float tile[32][33];
     const int b = blockIdx.z, tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    float ss = 0.0f;
-    for (int p = 0; p < parts; ++p) ss += __ldg(partial + b * kMaxParts + p);
-    const float f = (float)(1 << kXBits) / (sqrtf(ss) + eps);
+    const float f = input_factor(partial + b * kMaxParts, parts, eps);
     const int m = tall ? N : M;
     const T *src = g + (int64_t)b * M * N;
     const int64_t base = (int64_t)b * m * pitch;
@@ -662,41 +891,8 @@ cudaError_t make_map(CUtensorMap *map, const __half *base, int64_t batch, int64_
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int KIND, int BN>
-cudaError_t launch_gemm(const CUtensorMap &l, const CUtensorMap &r, const CUtensorMap &in, const CUtensorMap &in_lo,
-                        const CUtensorMap &out, const CUtensorMap &out_lo, OrthoArgs a, int pairs, cudaStream_t s)
-{
-    a.row_tiles = (a.rows + 255) / 256;
-    a.col_tiles = (a.cols + BN - 1) / BN;
-    if (KIND == kGram || KIND == kPoly) {
-        a.tiles = 0;
-        for (int rt = 0; rt < a.row_tiles; ++rt) a.tiles += a.col_tiles - rt * 256 / BN;
-    } else {
-        a.tiles = a.row_tiles * a.col_tiles;
-    }
-    const int64_t total = (int64_t)a.tiles * a.batch;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * (total < pairs ? total : pairs)));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Cfg<BN>::SMEM;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, ortho_gemm_kernel<KIND, BN>, l, r, in, in_lo, out, out_lo, a);
-}
-
-template <int KIND, int BN>
-cudaError_t set_smem()
-{
-    return cudaFuncSetAttribute(ortho_gemm_kernel<KIND, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Cfg<BN>::SMEM);
-}
-
 struct Region {
-    size_t partial, hi[2], lo, a, bm, total;
+    size_t partial, done, hi[2], lo, a, bm, total;
     int64_t m, n, x_pitch, a_pitch;
 };
 
@@ -714,6 +910,7 @@ Region layout(int64_t B, int64_t M, int64_t N)
         return at;
     };
     L.partial = take((size_t)B * kMaxParts * 4);
+    L.done = take((size_t)B * 4);
     const size_t x = (size_t)(B * L.m * L.x_pitch) * 2, a = (size_t)(B * L.m * L.a_pitch) * 2;
     L.hi[0] = take(x);
     L.hi[1] = take(x);
@@ -729,63 +926,94 @@ cudaError_t run_steps(const OrthoCall &c, char *ws, const Region &L, int pairs, 
 {
     auto *lo = (__half *)(ws + L.lo), *A = (__half *)(ws + L.a), *Bm = (__half *)(ws + L.bm);
     __half *hi[2] = {(__half *)(ws + L.hi[0]), (__half *)(ws + L.hi[1])};
-    const int64_t B = c.B;
-    CUtensorMap x_left[2], x_right[2], x_cols[2], x_blk[2], lo_blk, a_left, a_right, a_blk, b_left, b_blk;
+    OrthoMaps t;
     cudaError_t e = cudaSuccess;
-    auto map = [&](CUtensorMap *t, const __half *p, int64_t cols, int64_t pitch, int box_rows) {
-        if (e == cudaSuccess) e = make_map(t, p, B, L.m, cols, pitch, box_rows);
+    auto map = [&](CUtensorMap *m, const __half *p, int64_t cols, int64_t pitch, int box_rows) {
+        if (e == cudaSuccess) e = make_map(m, p, c.B, L.m, cols, pitch, box_rows);
     };
     for (int i = 0; i < 2; ++i) {
-        map(&x_left[i], hi[i], L.n, L.x_pitch, 128);
-        map(&x_right[i], hi[i], L.n, L.x_pitch, BN / 2);
-        map(&x_cols[i], hi[i], L.n, L.x_pitch, 64);
-        map(&x_blk[i], hi[i], L.n, L.x_pitch, 32);
+        map(&t.x_left[i], hi[i], L.n, L.x_pitch, 128);
+        map(&t.x_right[i], hi[i], L.n, L.x_pitch, BN / 2);
+        map(&t.x_cols[i], hi[i], L.n, L.x_pitch, 64);
+        map(&t.x_blk[i], hi[i], L.n, L.x_pitch, 32);
     }
-    map(&lo_blk, lo, L.n, L.x_pitch, 32);
-    map(&a_left, A, L.m, L.a_pitch, 128);
-    map(&a_right, A, L.m, L.a_pitch, BN / 2);
-    map(&a_blk, A, L.m, L.a_pitch, 32);
-    map(&b_left, Bm, L.m, L.a_pitch, 128);
-    map(&b_blk, Bm, L.m, L.a_pitch, 32);
+    map(&t.lo_blk, lo, L.n, L.x_pitch, 32);
+    map(&t.a_left, A, L.m, L.a_pitch, 128);
+    map(&t.a_right, A, L.m, L.a_pitch, BN / 2);
+    map(&t.a_blk, A, L.m, L.a_pitch, 32);
+    map(&t.b_left, Bm, L.m, L.a_pitch, 128);
+    map(&t.b_blk, Bm, L.m, L.a_pitch, 32);
     if (e != cudaSuccess) return e;
 
-    OrthoArgs base{};
-    base.m = (int)L.m;
-    base.n = (int)L.n;
-    base.batch = (int)B;
     auto pow2 = [](int p) { return ldexpf(1.0f, p); };
-    for (int i = 0; i < c.steps; ++i) {
-        const int x = i & 1, y = x ^ 1;
-        OrthoArgs a = base;
-        a.rows = a.cols = (int)L.m;
-        a.depth = (int)L.n;
-        a.cc = pow2(kABits - 2 * kXBits);
-        a.mirror = A;
-        a.mirror_pitch = L.a_pitch;
-        a.mirror_matrix = L.m * L.a_pitch;
-        e = launch_gemm<kGram, BN>(x_left[x], x_right[x], a_blk, a_blk, a_blk, a_blk, a, pairs, s);
-        if (e != cudaSuccess) return e;
-        a.depth = (int)L.m;
-        a.cb = c.b * pow2(kBBits - kABits);
-        a.cc = c.c * pow2(kBBits - 2 * kABits);
-        a.mirror = Bm;
-        e = launch_gemm<kPoly, BN>(a_left, a_right, a_blk, a_blk, b_blk, b_blk, a, pairs, s);
-        if (e != cudaSuccess) return e;
-        a = base;
-        a.rows = (int)L.m;
-        a.cols = (int)L.n;
-        a.depth = (int)L.m;
-        a.ca = c.a;
-        a.cc = pow2(-kBBits);
-        if (i + 1 < c.steps) {
-            e = launch_gemm<kApply, BN>(b_left, x_cols[x], x_blk[x], lo_blk, x_blk[y], lo_blk, a, pairs, s);
-        } else {
-            a.out = (__nv_bfloat16 *)c.out;
-            a.out_cols = (int)c.N;
-            a.transposed = c.M > c.N;
-            a.out_scale = c.out_scale * pow2(-kXBits);
-            e = launch_gemm<kLast, BN>(b_left, x_cols[x], x_blk[x], lo_blk, x_blk[y], lo_blk, a, pairs, s);
-        }
+    OrthoArgs a{};
+    a.m = (int)L.m;
+    a.n = (int)L.n;
+    a.batch = (int)c.B;
+    a.steps = c.steps;
+    a.group = a.batch;
+    a.row_tiles = (a.m + 255) / 256;
+    a.sym_cols = (a.m + BN - 1) / BN;
+    a.x_cols = (a.n + BN - 1) / BN;
+    for (int rt = 0; rt < a.row_tiles; ++rt) a.sym_tiles += a.sym_cols - rt * 256 / BN;
+    a.x_tiles = a.row_tiles * a.x_cols;
+    a.g = pow2(kABits - 2 * kXBits);
+    a.pb = c.b * pow2(kBBits - kABits);
+    a.pc = c.c * pow2(kBBits - 2 * kABits);
+    a.xa = c.a;
+    a.xc = pow2(-kBBits);
+    a.out_scale = c.out_scale * pow2(-kXBits);
+    a.a = A;
+    a.bm = Bm;
+    a.pitch = L.a_pitch;
+    a.out = (__nv_bfloat16 *)c.out;
+    a.out_cols = (int)c.N;
+    a.transposed = c.M > c.N;
+    a.done = (uint32_t *)(ws + L.done);
+    // the most tiles that can run at once: one product's of the whole batch
+    const int64_t at_once = (int64_t)a.batch * (a.x_tiles > a.sym_tiles ? a.x_tiles : a.sym_tiles);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * (at_once < pairs ? at_once : pairs)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Cfg<BN>::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;  // tiles wait for tiles: every pair has to be resident
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, ortho_kernel<BN>, t, a);
+}
+
+template <typename T>
+cudaError_t launch_input(const OrthoCall &c, const Region &L, float *partial, uint32_t *done, __half *hi, __half *lo,
+                         cudaStream_t s)
+{
+    const int64_t count = c.M * c.N;
+    const int64_t slices = ceil_div(count, 8192);
+    const int parts = (int)(slices < kMaxParts ? slices : kMaxParts);
+    const bool tall = c.M > c.N, by8 = c.M % 8 == 0 && c.N % 8 == 0;
+    const int64_t fit = kTurnBytes / (count * (int64_t)sizeof(T));
+    const int64_t turn = fit < 1 ? 1 : fit < c.B ? fit : c.B;
+    for (int64_t b = 0; b < c.B; b += turn) {
+        const unsigned n = (unsigned)(c.B - b < turn ? c.B - b : turn);
+        const T *g = (const T *)c.g + b * count;
+        float *part = partial + b * kMaxParts;
+        const int64_t at = b * L.m * L.x_pitch;
+        ortho_norm_kernel<<<dim3(parts, n), 256, 0, s>>>(g, count, part, done + b);
+        const int M = (int)c.M, N = (int)c.N;
+        if (by8 && !tall)
+            ortho_split8_kernel<T, true>
+                <<<dim3((unsigned)ceil_div(count, 8 * 256 * 4), 1, n), 256, 0, s>>>(g, M, N, part, parts, c.eps,
+                                                                                    hi + at, lo + at);
+        else if (by8)
+            ortho_split8_kernel<T, false>
+                <<<dim3((unsigned)ceil_div(N, 64), (unsigned)ceil_div(M, 64), n), 256, 0, s>>>(g, M, N, part, parts,
+                                                                                               c.eps, hi + at, lo + at);
+        else
+            ortho_split_kernel<<<dim3((unsigned)ceil_div(N, 32), (unsigned)ceil_div(M, 32), n), 256, 0, s>>>(
+                g, M, N, part, parts, c.eps, tall, L.x_pitch, hi + at, lo + at);
+        const cudaError_t e = cudaPeekAtLastError();
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -797,14 +1025,10 @@ size_t ortho_workspace_bytes(int64_t B, int64_t M, int64_t N) { return layout(B,
 
 cudaError_t ortho_init_device(int *pairs)
 {
-    cudaError_t e = set_smem<kGram, 256>();
-    if (e == cudaSuccess) e = set_smem<kPoly, 256>();
-    if (e == cudaSuccess) e = set_smem<kApply, 256>();
-    if (e == cudaSuccess) e = set_smem<kLast, 256>();
-    if (e == cudaSuccess) e = set_smem<kGram, 128>();
-    if (e == cudaSuccess) e = set_smem<kPoly, 128>();
-    if (e == cudaSuccess) e = set_smem<kApply, 128>();
-    if (e == cudaSuccess) e = set_smem<kLast, 128>();
+    cudaError_t e = cudaFuncSetAttribute(ortho_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Cfg<256>::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(ortho_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<128>::SMEM);
     if (e != cudaSuccess) return e;
     // the pairs of CTAs that the device can hold at once
     cudaLaunchConfig_t cfg = {};
@@ -817,7 +1041,7 @@ cudaError_t ortho_init_device(int *pairs)
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaOccupancyMaxActiveClusters(pairs, ortho_gemm_kernel<kApply, 256>, &cfg);
+    return cudaOccupancyMaxActiveClusters(pairs, ortho_kernel<256>, &cfg);
 }
 
 cudaError_t launch_orthogonalize(const OrthoCall &c, void *workspace, int pairs, cudaStream_t s)
@@ -826,21 +1050,9 @@ cudaError_t launch_orthogonalize(const OrthoCall &c, void *workspace, int pairs,
     char *ws = (char *)workspace;
     auto *partial = (float *)(ws + L.partial);
     auto *hi = (__half *)(ws + L.hi[0]), *lo = (__half *)(ws + L.lo);
-    const int64_t count = c.M * c.N;
-    const int64_t slices = ceil_div(count, 4096);
-    const int parts = (int)(slices < kMaxParts ? slices : kMaxParts);
-    const dim3 tiles((unsigned)ceil_div(c.N, 32), (unsigned)ceil_div(c.M, 32), (unsigned)c.B);
-    const bool tall = c.M > c.N;
-    if (c.g_f32) {
-        ortho_norm_kernel<<<dim3(parts, (unsigned)c.B), 256, 0, s>>>((const float *)c.g, count, partial);
-        ortho_split_kernel<<<tiles, 256, 0, s>>>((const float *)c.g, (int)c.M, (int)c.N, partial, parts, c.eps, tall,
-                                                 L.x_pitch, hi, lo);
-    } else {
-        ortho_norm_kernel<<<dim3(parts, (unsigned)c.B), 256, 0, s>>>((const __nv_bfloat16 *)c.g, count, partial);
-        ortho_split_kernel<<<tiles, 256, 0, s>>>((const __nv_bfloat16 *)c.g, (int)c.M, (int)c.N, partial, parts, c.eps,
-                                                 tall, L.x_pitch, hi, lo);
-    }
-    cudaError_t e = cudaPeekAtLastError();
+    auto *done = (uint32_t *)(ws + L.done);
+    const cudaError_t e = c.g_f32 ? launch_input<float>(c, L, partial, done, hi, lo, s)
+                                  : launch_input<__nv_bfloat16>(c, L, partial, done, hi, lo, s);
     if (e != cudaSuccess) return e;
     // 256-wide tiles feed the tensor cores best; where they leave pairs of
     // CTAs without one, 128-wide tiles are twice as many
