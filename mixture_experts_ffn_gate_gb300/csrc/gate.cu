@@ -7,15 +7,17 @@
 //   with a bias the sum of the two largest), of them the k largest c
 //   w_j = scale s_j (/ sum of the chosen s)
 //
-// One warp per token.  Lane q owns the kPer consecutive experts q kPer ...,
-// as 32-bit keys in the order of c (logit_key; 0 below every value marks what
-// cannot be chosen).  A round of the selection is one warp maximum of the
-// lanes' largest keys (redux); on equal keys the lowest lane that has it, and
-// its first expert, is the lowest index, so 32-bit keys are enough (the
-// router of the expert layer, whose lanes own experts 32 apart, needs 64).
+// One warp per token.  Lane q owns the PER consecutive experts q PER ..., as
+// 32-bit keys in the order of c, and sorts its (at most) 8 largest once (a
+// sorting network on key and index); the list waits in shared memory, its
+// head in registers.  A round of the selection is one warp maximum of the
+// heads (redux); on equal keys the lowest lane that has it holds the lowest
+// index, so the 32-bit keys decide (the router of the expert layer, whose
+// lanes own experts 32 apart, compares 64 bits), and that lane pops its list.
 //
 // The bytes (4 E per token in, 8 k out) would take 2.6 us for 16384 tokens of
-// 256 experts at the copy rate; the instructions of the k rounds bound it.
+// 256 experts at the copy rate; the instructions bound it (the scores' exp
+// and division, the sort, k rounds).
 #include <type_traits>
 
 #include "common.cuh"
@@ -29,7 +31,8 @@ namespace {
 constexpr int kGateWarps = 8;
 // up to this many tokens run as one block, which owns the counts (no zeroing
 // before it, no atomics to global memory)
-constexpr int kGateOneBlock = 16;
+constexpr int kGateOneBlock = kGateWarps;
+constexpr int kList = 8;  // sorted keys per lane
 
 struct GateArgs {
     const float *logits, *bias;
@@ -41,6 +44,27 @@ struct GateArgs {
     float *w;
     int32_t *counts;
 };
+
+// logit_key in three instructions: adding +0 turns -0 into +0 and every NaN
+// into the one positive NaN that the GPU's FP32 additions give.
+__device__ __forceinline__ uint32_t gate_key(float f)
+{
+    const int b = __float_as_int(__fadd_rn(f, 0.0f));
+    return (uint32_t)(b ^ ((b >> 31) | (int)0x80000000));
+}
+
+// The 8 largest of two descending lists, into `list`: the larger of each
+// list[q], x[7 - q] pair form a bitonic sequence, sorted by half-cleaners.
+__device__ __forceinline__ void merge8_desc(unsigned long long (&list)[8], const unsigned long long (&x)[8])
+{
+#pragma unroll
+    for (int q = 0; q < 8; ++q) list[q] = list[q] > x[7 - q] ? list[q] : x[7 - q];
+#pragma unroll
+    for (int d = 4; d >= 1; d >>= 1)
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (!(q & d)) key_order(list[q], list[q + d]);
+}
 
 __device__ __forceinline__ float sigmoid_of(float l) { return 1.0f / (1.0f + expf(-l)); }
 
@@ -98,10 +122,12 @@ __device__ __forceinline__ void top2_merge(uint32_t &m1, uint32_t &m2, uint32_t 
 }
 
 template <int PER>
-__global__ void __launch_bounds__(32 * kGateOneBlock) gate_kernel(const GateArgs a)
+__global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
 {
     constexpr bool AHEAD = PER <= 12;  // the next token's logits are loaded before this one's are used
     extern __shared__ int32_t hist[];  // [E], with counts
+    __shared__ unsigned long long lists[kGateWarps][kList][32];
+    __shared__ unsigned long long chosen[kGateWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int E = a.E, k = a.k, e0 = lane * PER;
     if (a.counts) {
@@ -124,7 +150,7 @@ __global__ void __launch_bounds__(32 * kGateOneBlock) gate_kernel(const GateArgs
         if (!a.sigmoid && (a.bias || !a.renorm)) {
             uint32_t m = 0;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) m = max(m, logit_key(l[i]));
+            for (int i = 0; i < PER; ++i) m = max(m, gate_key(l[i]));
             top = key_logit(__reduce_max_sync(0xffffffffu, m));
             total = 0.0f;
 #pragma unroll
@@ -132,97 +158,126 @@ __global__ void __launch_bounds__(32 * kGateOneBlock) gate_kernel(const GateArgs
             total = warp_sum(total);
         }
         uint32_t key[PER];
+        if (!a.bias) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            float c = l[i];
-            if (a.bias && e0 + i < E) {
-                const float s = a.sigmoid ? sigmoid_of(c) : total > 0.0f ? exp_below(c, top) / total : 0.0f;
-                c = s + __ldg(a.bias + e0 + i);
+            for (int i = 0; i < PER; ++i) key[i] = e0 + i < E ? gate_key(l[i]) : 0u;
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                float s;
+                if (a.sigmoid)
+                    s = sigmoid_of(l[i]);
+                else
+                    s = total > 0.0f ? exp_below(l[i], top) / total : 0.0f;
+                key[i] = e0 + i < E ? gate_key(s + __ldg(a.bias + e0 + i)) : 0u;
             }
-            key[i] = e0 + i < E ? logit_key(c) : 0u;
         }
-        if (a.groups > 1) {
-            // lane g: the rank of group g as a key
-            uint32_t rank = 0;
-            const int size = a.group_size, lanes = size / PER;
-            const bool whole = lanes * PER == size && (lanes & (lanes - 1)) == 0 && lanes > 0;
-            if (whole) {  // a group is a power of two of neighbouring lanes
-                uint32_t m1 = 0, m2 = 0;
-#pragma unroll
-                for (int i = 0; i < PER; ++i) top2_merge(m1, m2, key[i], 0u);
-                for (int o = 1; o < lanes; o <<= 1)
-                    top2_merge(m1, m2, __shfl_xor_sync(0xffffffffu, m1, o), __shfl_xor_sync(0xffffffffu, m2, o));
-                const uint32_t r = a.bias && size > 1 ? logit_key(key_logit(m1) + key_logit(m2)) : m1;
-                rank = __shfl_sync(0xffffffffu, r, (lane * lanes) & 31);
-            } else {
-                for (int g = 0; g < a.groups; ++g) {
-                    uint32_t m1 = 0, m2 = 0;
-#pragma unroll
-                    for (int i = 0; i < PER; ++i)
-                        if (e0 + i >= g * size && e0 + i < (g + 1) * size) top2_merge(m1, m2, key[i], 0u);
-                    const uint32_t g1 = __reduce_max_sync(0xffffffffu, m1);
-                    const int owner = __ffs(__ballot_sync(0xffffffffu, m1 == g1)) - 1;
-                    const uint32_t g2 = __reduce_max_sync(0xffffffffu, lane == owner ? m2 : m1);
-                    if (lane == g) rank = a.bias && size > 1 ? logit_key(key_logit(g1) + key_logit(g2)) : g1;
-                }
-            }
-            if (lane >= a.groups) rank = 0;
-            uint32_t kept = 0;
+        // groups that are a power of two of neighbouring lanes are ranked
+        // from the lanes' lists, others from the keys
+        const int size = a.group_size, lanes = size / PER;
+        const bool whole = lanes * PER == size && (lanes & (lanes - 1)) == 0;
+        uint32_t kept = 0;
+        auto keep_best = [&](uint32_t rank) {  // lane g holds the rank of group g
             for (int r = 0; r < a.topk_groups; ++r) {
-                const uint32_t m = __reduce_max_sync(0xffffffffu, rank);
-                const int g = __ffs(__ballot_sync(0xffffffffu, rank == m && lane < a.groups && !(kept >> lane & 1))) - 1;
+                const uint32_t m = __reduce_max_sync(0xffffffffu, lane < a.groups ? rank : 0u);
+                const int g = __ffs(__ballot_sync(0xffffffffu, rank == m && lane < a.groups)) - 1;
                 kept |= 1u << g;
                 if (lane == g) rank = 0;
             }
-            if (whole) {
-                if (!(kept >> (lane / lanes) & 1))
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) key[i] = 0;
-            } else {
+        };
+        auto rank_of = [&](uint32_t m1, uint32_t m2) {
+            return a.bias && size > 1 ? gate_key(key_logit(m1) + key_logit(m2)) : m1;
+        };
+        if (a.groups > 1 && !whole) {
+            uint32_t rank = 0;
+            for (int g = 0; g < a.groups; ++g) {
+                uint32_t m1 = 0, m2 = 0;
 #pragma unroll
                 for (int i = 0; i < PER; ++i)
-                    if (e0 + i < E && !(kept >> ((unsigned)(e0 + i) / (unsigned)size) & 1)) key[i] = 0;
+                    if (e0 + i >= g * size && e0 + i < (g + 1) * size) top2_merge(m1, m2, key[i], 0u);
+                const uint32_t g1 = __reduce_max_sync(0xffffffffu, m1);
+                const int owner = __ffs(__ballot_sync(0xffffffffu, m1 == g1)) - 1;
+                const uint32_t g2 = __reduce_max_sync(0xffffffffu, lane == owner ? m2 : m1);
+                if (lane == g) rank = rank_of(g1, g2);
+            }
+            keep_best(rank);
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (e0 + i < E && !(kept >> ((unsigned)(e0 + i) / (unsigned)size) & 1)) key[i] = 0;
+        }
+        // the lane's list: (key, ~index), so that the lower index is the larger
+        unsigned long long list[kList];
+#pragma unroll
+        for (int c = 0; c < (PER + 7) / 8; ++c) {
+            unsigned long long x[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const int i = 8 * c + q;
+                x[q] = i < PER && key[i < PER ? i : 0]
+                           ? ((unsigned long long)key[i < PER ? i : 0] << 32) | (uint32_t)~(uint32_t)(e0 + i)
+                           : 0ull;
+            }
+            if (PER == 2)
+                key_order(x[0], x[1]);
+            else if (PER > 2)
+                sort8_desc(x);
+            if (c == 0) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) list[q] = x[q];
+            } else {
+                merge8_desc(list, x);
             }
         }
-        // k rounds; lane j keeps the j-th choice
-        uint32_t best = 0;
+        unsigned long long head = list[0];
+        if (a.groups > 1 && whole) {
+            uint32_t m1 = (uint32_t)(list[0] >> 32), m2 = (uint32_t)(list[1] >> 32);
+            for (int o = 1; o < lanes; o <<= 1)
+                top2_merge(m1, m2, __shfl_xor_sync(0xffffffffu, m1, o), __shfl_xor_sync(0xffffffffu, m2, o));
+            keep_best(__shfl_sync(0xffffffffu, rank_of(m1, m2), (lane * lanes) & 31));
+            if (!(kept >> (lane / lanes) & 1)) head = 0;
+        }
 #pragma unroll
-        for (int i = 0; i < PER; ++i) best = max(best, key[i]);
-        uint32_t mine = 0, first = 0;
-        int sel = 0;
+        for (int q = 1; q < (PER < kList ? PER : kList); ++q) lists[warp][q][lane] = list[q];
+        // k rounds (the experts that stay are at least k, so no round comes to
+        // a head of 0)
+        int next = 1;
         for (int r = 0; r < k; ++r) {
-            const uint32_t m = __reduce_max_sync(0xffffffffu, best);
-            const int owner = __ffs(__ballot_sync(0xffffffffu, best == m)) - 1;
-            int i_first = 0;
-#pragma unroll
-            for (int i = PER - 1; i >= 0; --i)
-                if (key[i] == m) i_first = i;
-            const int e = __shfl_sync(0xffffffffu, e0 + i_first, owner);
-            if (r == 0) first = m;
-            if (lane == r) {
-                sel = e;
-                mine = m;
-            }
+            const uint32_t m = __reduce_max_sync(0xffffffffu, (uint32_t)(head >> 32));
+            const int owner = __ffs(__ballot_sync(0xffffffffu, (uint32_t)(head >> 32) == m)) - 1;
             if (lane == owner) {
-                best = 0;
+                chosen[warp][r] = head;
+                if (next < (PER < kList ? PER : kList)) {
+                    head = lists[warp][next++][lane];
+                } else {
+                    // the list is used up: the largest key below the last one
+                    const unsigned long long last = head;
+                    head = 0;
+                    if (PER > kList)
 #pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    if (i == i_first) key[i] = 0;
-                    best = max(best, key[i]);
+                        for (int i = 0; i < PER; ++i) {
+                            const unsigned long long x =
+                                ((unsigned long long)key[i] << 32) | (uint32_t)~(uint32_t)(e0 + i);
+                            if (key[i] && x < last && x > head) head = x;
+                        }
                 }
             }
         }
+        __syncwarp();
         float s = 0.0f;
+        int sel = 0;
         if (lane < k) {
+            const unsigned long long mine = chosen[warp][lane];
+            sel = (int)~(uint32_t)mine;
             // without a bias the key is the logit's
-            const float lj = a.bias ? __ldg(a.logits + t * E + sel) : key_logit(mine);
+            const float lj = a.bias ? __ldg(a.logits + t * E + sel) : key_logit((uint32_t)(mine >> 32));
             if (a.sigmoid)
                 s = sigmoid_of(lj);
             else if (a.renorm)
-                s = exp_below(lj, a.bias ? top : key_logit(first));
+                s = exp_below(lj, a.bias ? top : key_logit((uint32_t)(chosen[warp][0] >> 32)));
             else
                 s = total > 0.0f || total != total ? exp_below(lj, top) / total : 0.0f;
         }
+        __syncwarp();  // the lists and choices are read before the next token's
         if (a.renorm) {
             const float sum = warp_sum(s);
             s = sum == 0.0f ? 0.0f : s / sum;
@@ -281,7 +336,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_grad_kernel(const float 
             load_logits<PER>(row, E, v);
             uint32_t m = 0;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) m = max(m, logit_key(v[i]));
+            for (int i = 0; i < PER; ++i) m = max(m, gate_key(v[i]));
             const float top = key_logit(__reduce_max_sync(0xffffffffu, m));
             float total = 0.0f;
 #pragma unroll
@@ -300,14 +355,16 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_grad_kernel(const float 
             if (sigmoid) {
                 p = used ? sigmoid_of(l) : 0.0f;
             } else {
-                const float top = key_logit(__reduce_max_sync(0xffffffffu, used ? logit_key(l) : 0u));
+                const float top = key_logit(__reduce_max_sync(0xffffffffu, used ? gate_key(l) : 0u));
                 p = used ? exp_below(l, top) : 0.0f;
             }
             float ds = d;
             if (renorm) {
                 const float total = warp_sum(p);
-                const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-                ds = (d - warp_sum(used ? d * p : 0.0f) * inv) * inv;
+                // one chosen expert has the share 1 exactly and no gradient
+                const float share = total == 0.0f ? 0.0f : p / total;
+                const float mean = warp_sum(used ? d * share : 0.0f);
+                ds = total == 0.0f ? 0.0f : (d - mean) / total;
             }
             // softmax: the factor p_j of the scores' gradient, sums cancelled
             mine = sigmoid ? ds * p * (1.0f - p) : ds * p;
@@ -344,7 +401,7 @@ cudaError_t launch_gate(const GateCall &c, int n_sm, cudaStream_t s)
     if (c.T > kGateOneBlock) {
         warps = kGateWarps;
         const int64_t blocks = ceil_div(c.T, kGateWarps);
-        grid = (int)(blocks < (int64_t)n_sm * 6 ? blocks : (int64_t)n_sm * 6);
+        grid = (int)(blocks < (int64_t)n_sm * 4 ? blocks : (int64_t)n_sm * 4);
         if (c.counts) {
             cudaError_t e = cudaMemsetAsync(c.counts, 0, (size_t)c.E * 4, s);
             if (e != cudaSuccess) return e;

@@ -214,28 +214,68 @@ struct NormGradArgs {
     float *partial;  // [gridDim.x][H]
 };
 
+// A piece of a row as it was loaded, VEC elements: half the registers for
+// BF16 while it waits.
+template <typename T, int VEC>
+struct Raw {
+    static constexpr int kWords = VEC * (int)sizeof(T) > 4 ? VEC * (int)sizeof(T) / 4 : 1;
+    uint32_t v[kWords];
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) v[i] = 0;
+    }
+    template <bool NC>
+    __device__ __forceinline__ void load(const T *p)
+    {
+        if constexpr (VEC == 8) {
+#pragma unroll
+            for (int i = 0; i < kWords; i += 4) {
+                const void *at = reinterpret_cast<const uint32_t *>(p) + i;
+                const uint4 w = NC ? ld_nc16(at) : *reinterpret_cast<const uint4 *>(at);
+                v[i] = w.x, v[i + 1] = w.y, v[i + 2] = w.z, v[i + 3] = w.w;
+            }
+        } else if constexpr (sizeof(T) == 4) {
+            v[0] = *reinterpret_cast<const uint32_t *>(p);
+        } else {
+            v[0] = (uint32_t)*reinterpret_cast<const uint16_t *>(p) << 16;
+        }
+    }
+    __device__ __forceinline__ float get(int q) const
+    {
+        if constexpr (sizeof(T) == 4 || VEC == 1)
+            return __uint_as_float(v[sizeof(T) == 4 ? q : 0]);
+        else
+            return q & 1 ? bf16hi(v[q / 2]) : bf16lo(v[q / 2]);
+    }
+};
+
 // Backward.  A block walks rows blockIdx.x, blockIdx.x + gridDim.x, ... and
-// keeps its columns' sums of dy n in registers; AHEAD loads the next row's h
-// and dy before it reduces this one's.
+// keeps its columns' sums of dy n in registers; AHEAD loads the next row
+// before it reduces this one, so a block of up to 512 threads always has a
+// whole row (48 KB at H = 6144) on its way.
 template <typename HT, typename GT, int VEC, bool AHEAD>
-__global__ void __launch_bounds__(AHEAD ? 512 : 1024) norm_grad_kernel(const NormGradArgs a)
+__global__ void __launch_bounds__(AHEAD ? 512 : 1024, 1) norm_grad_kernel(const NormGradArgs a)
 {
     constexpr int NV = kEpt / VEC;
     __shared__ float part[2][2][32];
     const int H = a.H;
+    struct Row {
+        Raw<HT, VEC> h[NV], dres[NV];
+        Raw<GT, VEC> dy[NV];
+    };
     float w[NV][VEC], dw[NV][VEC];
-    float h[NV][VEC], dy[NV][VEC];
     auto column = [&](int c) { return (c * (int)blockDim.x + (int)threadIdx.x) * VEC; };
-    auto fetch = [&](int64_t t, float(&hv)[NV][VEC], float(&gv)[NV][VEC]) {
+    auto fetch = [&](int64_t t, Row &r) {
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
             const int i = column(c);
+            r.h[c].zero(), r.dy[c].zero(), r.dres[c].zero();
             if (i < H && t < a.T) {
-                load_row<VEC>((const HT *)a.h + t * H + i, hv[c]);
-                load_row<VEC>((const GT *)a.dy + t * H + i, gv[c]);
-            } else {
-#pragma unroll
-                for (int q = 0; q < VEC; ++q) hv[c][q] = gv[c][q] = 0.0f;
+                r.h[c].template load<true>((const HT *)a.h + t * H + i);
+                r.dy[c].template load<true>((const GT *)a.dy + t * H + i);
+                // dh may take the place of dres: plain loads
+                if (a.dres) r.dres[c].template load<false>((const HT *)a.dres + t * H + i);
             }
         }
     };
@@ -246,52 +286,37 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024) norm_grad_kernel(const Nor
         for (int q = 0; q < VEC; ++q) w[c][q] = dw[c][q] = 0.0f;
         if (i < H) load_row<VEC>(a.weight + i, w[c]);
     }
-    if (AHEAD) fetch(blockIdx.x, h, dy);
+    Row r;
+    if (AHEAD) fetch(blockIdx.x, r);
     int turn = 0;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
-        float hn[NV][VEC], dyn[NV][VEC];
-        if (AHEAD)
-            fetch(t + gridDim.x, hn, dyn);
-        else
-            fetch(t, h, dy);
-        float dres[NV][VEC];
-#pragma unroll
-        for (int c = 0; c < NV; ++c) {
-            const int i = column(c);
-            if (a.dres && i < H) {
-                load_row_rw<VEC>((const HT *)a.dres + t * H + i, dres[c]);
-            } else {
-#pragma unroll
-                for (int q = 0; q < VEC; ++q) dres[c][q] = 0.0f;
-            }
-        }
+        Row next;
+        fetch(AHEAD ? t + gridDim.x : t, AHEAD ? next : r);
         float s[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int c = 0; c < NV; ++c)
 #pragma unroll
             for (int q = 0; q < VEC; ++q) {
-                s[0] = fmaf(h[c][q], h[c][q], s[0]);
-                s[1] = fmaf(dy[c][q] * w[c][q], h[c][q], s[1]);
+                const float h = r.h[c].get(q);
+                s[0] = fmaf(h, h, s[0]);
+                s[1] = fmaf(r.dy[c].get(q) * w[c][q], h, s[1]);
             }
         block_sum(s, part[turn]);
-        const float r = 1.0f / sqrtf(fmaf(s[0], a.inv_h, a.eps));
-        const float m = s[1] * a.inv_h * r * r;  // n mean(g n) = h m
+        const float inv = 1.0f / sqrtf(fmaf(s[0], a.inv_h, a.eps));
+        const float m = s[1] * a.inv_h * inv * inv;  // n mean(g n) = h m
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
             const int i = column(c);
             float o[VEC];
 #pragma unroll
             for (int q = 0; q < VEC; ++q) {
-                dw[c][q] = fmaf(dy[c][q], h[c][q] * r, dw[c][q]);
-                o[q] = fmaf(r, dy[c][q] * w[c][q] - h[c][q] * m, dres[c][q]);
+                const float h = r.h[c].get(q), dy = r.dy[c].get(q);
+                dw[c][q] = fmaf(dy, h * inv, dw[c][q]);
+                o[q] = fmaf(inv, dy * w[c][q] - h * m, r.dres[c].get(q));
             }
             if (i < H) store_row<VEC>((HT *)a.dh + t * H + i, o);
         }
-        if (AHEAD)
-#pragma unroll
-            for (int c = 0; c < NV; ++c)
-#pragma unroll
-                for (int q = 0; q < VEC; ++q) h[c][q] = hn[c][q], dy[c][q] = dyn[c][q];
+        if (AHEAD) r = next;
     }
 #pragma unroll
     for (int c = 0; c < NV; ++c) {

@@ -9,6 +9,7 @@ fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
@@ -52,12 +53,19 @@ def declare(L):
         f.argtypes, f.restype = [i64] * n, sz
 
 
+# A call of one token takes a few microseconds on the GPU, so the wrappers keep
+# their own part short: one test per tensor, the raw stream, no lock.
+def _lib():
+    return _m._lib or _m.lib()
+
+
 def _is(t, shape, dtype, name):
     """t is a contiguous CUDA tensor of this shape and type."""
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
 
 
 def _type(t, name):
@@ -65,6 +73,19 @@ def _type(t, name):
     if code is None:
         raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
     return code
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream(stream, device):
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _m._stream(stream)
+
+
+def _check(status, what):
+    if status:
+        raise MoeFfnError(status, what)
 
 
 def _workspace(n, device, what):
@@ -117,9 +138,9 @@ def moe_rms_norm_forward(x, weight, residual=None, eps: float = 1e-6, bf16: bool
             scales = torch.empty((T, Sh), dtype=torch.uint8, device=dev)
         _is(codes, (T, H), torch.uint8, "codes")
         _is(scales, (T, Sh), torch.uint8, "scales")
-    p = _m._ptr
-    _m._check(_m.lib().moe_rms_norm_forward(p(x), xt, p(residual), rt, p(weight), eps, T, H, p(h), p(y), p(codes),
-                                            p(scales), _m._stream(stream)), "moe_rms_norm_forward")
+    p = _ptr
+    _check(_lib().moe_rms_norm_forward(p(x), xt, p(residual), rt, p(weight), eps, T, H, p(h), p(y), p(codes),
+                                      p(scales), _stream(stream, dev)), "moe_rms_norm_forward")
     return NormOutput(y, h, codes, scales)
 
 
@@ -153,10 +174,10 @@ def moe_rms_norm_backward(h, weight, dy, dres=None, eps: float = 1e-6, dh=None, 
         _is(dweight, (H,), torch.float32, "dweight")
     if workspace is None:
         workspace = new_rms_norm_backward_workspace(T, H, device=h.device)
-    p = _m._ptr
-    _m._check(_m.lib().moe_rms_norm_backward(p(h), ht, p(weight), p(dy), gt, p(dres), eps, T, H, p(dh), p(dweight),
-                                             p(workspace), _size(workspace), _m._stream(stream)),
-              "moe_rms_norm_backward")
+    p = _ptr
+    _check(_lib().moe_rms_norm_backward(p(h), ht, p(weight), p(dy), gt, p(dres), eps, T, H, p(dh), p(dweight),
+                                        p(workspace), _size(workspace), _stream(stream, h.device)),
+           "moe_rms_norm_backward")
     return dh, dweight
 
 
@@ -167,12 +188,13 @@ class GateOutput(NamedTuple):
     counts: torch.Tensor | None     # int32 [E]
 
 
+@functools.lru_cache(maxsize=64)
 def _gate_opts(score, renormalize, scale, groups=1, topk_groups=1):
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
     if scale == 0.0:
         raise ValueError("scale must not be 0")  # 0 means 1 in the C struct
-    return moe_gate_opts(_SCORES[score], groups, topk_groups, int(renormalize), scale)
+    return ctypes.byref(moe_gate_opts(_SCORES[score], groups, topk_groups, int(renormalize), scale))
 
 
 def moe_gate_forward(logits, k: int, bias=None, score: str = "softmax", groups: int = 1, topk_groups: int = 1,
@@ -199,9 +221,9 @@ def moe_gate_forward(logits, k: int, bias=None, score: str = "softmax", groups: 
     elif counts is not None:
         _is(counts, (E,), torch.int32, "counts")
     o = _gate_opts(score, renormalize, scale, groups, topk_groups)
-    p = _m._ptr
-    _m._check(_m.lib().moe_gate_forward(p(logits), p(bias), T, E, k, ctypes.byref(o), p(topk_idx), p(topk_w),
-                                        p(counts), _m._stream(stream)), "moe_gate_forward")
+    p = _ptr
+    _check(_lib().moe_gate_forward(p(logits), p(bias), T, E, k, o, p(topk_idx), p(topk_w), p(counts),
+                                   _stream(stream, dev)), "moe_gate_forward")
     return GateOutput(topk_idx, topk_w, counts)
 
 
@@ -220,9 +242,9 @@ def moe_gate_backward(logits, topk_idx, dtopk_w, score: str = "softmax", renorma
     else:
         _is(dlogits, (T, E), torch.float32, "dlogits")
     o = _gate_opts(score, renormalize, scale)
-    p = _m._ptr
-    _m._check(_m.lib().moe_gate_backward(p(logits), p(topk_idx), p(dtopk_w), T, E, k, ctypes.byref(o), p(dlogits),
-                                         _m._stream(stream)), "moe_gate_backward")
+    p = _ptr
+    _check(_lib().moe_gate_backward(p(logits), p(topk_idx), p(dtopk_w), T, E, k, o, p(dlogits),
+                                    _stream(stream, logits.device)), "moe_gate_backward")
     return dlogits
 
 
@@ -282,11 +304,11 @@ def moe_ffn_forward_routed(x, topk_idx, topk_w, w_gate_up, w_down, x_scale=None,
     out = _new(out, (T, H), "out", x.device)
     if workspace is None:
         workspace = new_routed_workspace(T, H, I, E, k, device=x.device)
-    p = _m._ptr
-    _m._check(_m.lib().moe_ffn_forward_routed(
+    p = _ptr
+    _check(_lib().moe_ffn_forward_routed(
         p(x), p(x_scale), p(topk_idx), p(topk_w), p(w_gate_up), p(w_gate_up_scale), p(w_down), p(w_down_scale), T, H,
         I, E, k, p(out), p(workspace), _size(workspace), None if opts is None else ctypes.byref(opts),
-        _m._stream(stream)), "moe_ffn_forward_routed")
+        _stream(stream, x.device)), "moe_ffn_forward_routed")
     return out
 
 
@@ -298,10 +320,10 @@ def moe_ffn_forward_routed_train(x, topk_idx, topk_w, w_gate_up, w_down, state, 
     k = _routing(topk_idx, topk_w, T)
     _is(x, (T, H), torch.bfloat16, "x")
     out = _new(out, (T, H), "out", x.device)
-    p = _m._ptr
-    _m._check(_m.lib().moe_ffn_forward_routed_train(
+    p = _ptr
+    _check(_lib().moe_ffn_forward_routed_train(
         p(x), p(topk_idx), p(topk_w), p(w_gate_up), p(w_down), T, H, I, E, k, p(out), p(state), _size(state),
-        None if opts is None else ctypes.byref(opts), _m._stream(stream)), "moe_ffn_forward_routed_train")
+        None if opts is None else ctypes.byref(opts), _stream(stream, x.device)), "moe_ffn_forward_routed_train")
     return out
 
 
@@ -326,11 +348,11 @@ def moe_ffn_backward_routed(x, topk_idx, topk_w, w_gate_up, w_down, dout, dx=Non
     ws = state if state is not None else workspace
     if ws is None:
         ws = _m.new_backward_workspace(T, H, I, E, k, device=dev)
-    p = _m._ptr
-    _m._check(_m.lib().moe_ffn_backward_routed(
+    p = _ptr
+    _check(_lib().moe_ffn_backward_routed(
         p(x), p(topk_idx), p(topk_w), p(w_gate_up), p(w_down), p(dout), T, H, I, E, k, p(dx), p(dtopk_w),
         p(dw_gate_up), p(dw_down), p(ws), _size(ws), int(state is not None),
-        None if opts is None else ctypes.byref(opts), _m._stream(stream)), "moe_ffn_backward_routed")
+        None if opts is None else ctypes.byref(opts), _stream(stream, x.device)), "moe_ffn_backward_routed")
     return dx, dtopk_w, dw_gate_up, dw_down
 
 
@@ -358,7 +380,7 @@ def moe_orthogonalize(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
     if workspace is None:
         workspace = new_orthogonalize_workspace(B, M, N, device=g.device) if B else g.new_empty(0)
     a, b, c = coefficients
-    p = _m._ptr
-    _m._check(_m.lib().moe_orthogonalize(p(g), gt, B, M, N, steps, a, b, c, eps, out_scale, p(out), p(workspace),
-                                         _size(workspace), _m._stream(stream)), "moe_orthogonalize")
+    p = _ptr
+    _check(_lib().moe_orthogonalize(p(g), gt, B, M, N, steps, a, b, c, eps, out_scale, p(out), p(workspace),
+                                    _size(workspace), _stream(stream, g.device)), "moe_orthogonalize")
     return out
