@@ -7,20 +7,23 @@
 //   poly     Bm = b A + c A A              [m, m]
 //   apply    X  = a X + Bm X               [m, n]
 // A and Bm are symmetric: only the tiles on and above the diagonal are
-// computed, the others written as their mirror images, which takes a step
-// from 4 m^2 n + 2 m^3 operations to 3 m^2 n + m^3 (and the diagonal tiles'
-// other halves).
+// computed and stored, and what lies below it is read from its mirror image
+// (as an MN-major operand instead of a K-major one), which takes a step from
+// 4 m^2 n + 2 m^3 operations to 3 m^2 n + m^3 (and the diagonal tiles' other
+// halves).
 //
 // Numbers.  BF16 operands lose too much here (a polynomial whose slope at
 // zero is 3.4 raises the rounding noise of the small singular values with
 // them: 1e-2 after five steps, up to 0.2 for a matrix of low rank plus
 // noise).  FP16 has three more bits at the same rate, and its range is
 // enough because every singular value is at most about 1.2: the stored X is
-// 2^10 X, A 2^14 A, Bm 2^11 Bm.  X between steps is a pair hi + lo, so that
-// a X, the part that carries the singular directions from step to step, is
-// exact to about 22 bits; the products read hi.  In 64-bit simulations of
-// these roundings the result is within 8e-4 (low rank, power-law spectra) to
-// 2.6e-3 (Gaussian) of the exact one, and a single FP16 X within 2e-2.
+// 2^10 X, A 2^14 A, Bm 2^11 Bm.  X between steps is a pair: hi in FP16 and lo
+// = X - hi in E4M3 (times 2^14), so that a X, the part that carries the
+// singular directions from step to step, has about 15 bits; the products
+// read hi.  In 64-bit simulations of these roundings the result is within
+// %SIMLO% (low rank, power-law spectra) to %SIMGAUSS% (Gaussian) of the exact one
+// (an FP16 lo: 8e-4 and 2.6e-3, for twice the bytes), and a single FP16 X
+// within 2e-2.
 //
 // The products.  A pair of CTAs (a cluster of two) computes a 256 x BN tile
 // with tcgen05.mma.cta_group::2: each CTA loads its 128 rows of the left and
@@ -31,15 +34,16 @@
 // TMEM accumulators, warps 2-9 of each CTA drain the other one.  The right
 // operand of `apply`, X read down its columns, is taken as MN-major tiles.
 // The epilogue moves its operands and results through shared memory by TMA
-// (32 x 64 blocks), the mirror images by plain stores (a warp's 32 lanes are
-// 32 consecutive elements of a mirrored row).
+// (32 x 64 blocks).
 //
 // One launch.  All steps are one cooperative launch of one pair per two SMs:
 // the tiles of all products form a list (step by step, gram, poly, apply,
 // matrix by matrix), pair p takes tiles p, p + pairs, ...  A matrix's tiles
-// of one product need all of its tiles of the one before: every epilogue
-// warp adds one to the matrix's counter when its part of a tile has been
-// written, and the loads of a later tile wait for the count.  A waiting tile
+// of one product need all of its tiles of the one before: each CTA adds one
+// to the matrix's counter when its half of a tile has been written (the last
+// of its epilogue warps does, so that a tile costs one fence to the GPU's
+// scope; one per warp cost more than the products), and the loads of a later
+// tile wait for the count.  A waiting tile
 // only needs tiles that come before it in the list, and every pair is
 // resident, so the list moves on; with several matrices the tail of one
 // product is filled by the next one's first tiles, where a launch per
@@ -67,16 +71,18 @@ cudaError_t read_ortho_fault_word(uint32_t *flags, bool clear)
 
 namespace {
 
-constexpr int kXBits = 10, kABits = 14, kBBits = 11;  // the powers of two that X, A and Bm are stored with
+// the powers of two that X, A, Bm and X's lo part (beside X's own) are stored with
+constexpr int kXBits = 10, kABits = 14, kBBits = 11;
+constexpr float kLoScale = 16384.0f, kLoInv = 1.0f / 16384.0f;
 
 constexpr int BK = 64;                    // K per stage: 128 bytes of FP16, the swizzle's width
 constexpr int A_BYTES = 128 * BK * 2;     // one CTA's left operand of a stage
-constexpr int kThreads = 320;
 constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr int BLOCK = 32 * 64 * 2;        // one staged 32 x 64 FP16 block
+constexpr int LO_BLOCK = 32 * 64;         // and its E4M3 part
+constexpr int kSlots = 4;                 // tiles that the producer and the epilogue can be apart, and one more
 constexpr uint64_t kWaitNs = 2000000000ull;
-
-constexpr uint32_t kWarpsPerTile = 2 * kEpiWarps;  // that count a tile as done
 
 enum : int { kGram = 0, kPoly = 1, kApply = 2, kLast = 3 };  // kLast: the last step's apply, into the output
 
@@ -85,29 +91,27 @@ struct Cfg {
     static constexpr int B_BYTES = BN / 2 * BK * 2;  // one CTA's right operand of a stage
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int STAGES = BN == 256 ? 5 : 6;
-    static constexpr int STAGING = kEpiWarps * 2 * BLOCK;
+    static constexpr int STAGING = kEpiWarps * (BLOCK + LO_BLOCK);
     static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + STAGING + 512;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
 // The tensor maps over X (two hi buffers, used in turn, and lo), A and Bm:
 // left operands (K-major, box 64 x 128 rows), right ones (K-major, box 64 x
-// BN / 2 rows; X's columns, MN-major, box 64 x 64 rows) and the epilogue's
-// blocks (64 x 32 rows).
+// BN / 2 rows), MN-major ones (box 64 x 64 rows) and the epilogue's blocks
+// (64 x 32 rows).
 struct OrthoMaps {
-    CUtensorMap x_left[2], x_right[2], x_cols[2], x_blk[2], lo_blk, a_left, a_right, a_blk, b_left, b_blk;
+    CUtensorMap x_left[2], x_right[2], x_cols[2], x_blk[2], lo_blk, a_left, a_right, a_cols, a_blk, b_left, b_cols,
+        b_blk;
 };
 
 struct OrthoArgs {
     int m, n, batch, steps;  // X is [batch][m][n]
-    int group;               // matrices per group: a group's steps all come before the next group's
     int row_tiles, sym_cols, x_cols;  // tiles of 256 rows, of BN columns of A and of X
     int sym_tiles, x_tiles;  // per matrix: of a symmetric product (on and above the diagonal), of apply
     // the factors of the epilogues, powers of two folded in: gram A = g acc;
     // poly Bm = pb A + pc acc; apply X = xa X + xc acc; last: times out_scale
     float g, pb, pc, xa, xc, out_scale;
-    __half *a, *bm;          // for the mirror images
-    int64_t pitch;           // elements per row of A and Bm
     __nv_bfloat16 *out;
     int out_cols;            // the caller's N
     int transposed;          // out is [n][m]
@@ -217,11 +221,11 @@ __device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// Instruction descriptor, kind::f16: D = F32, A = B = F16, shape 256 x N, B
-// MN-major or not.
-__host__ __device__ constexpr uint32_t idesc_f16(uint32_t N, bool b_mn)
+// Instruction descriptor, kind::f16: D = F32, A = B = F16, shape 256 x N, A
+// and B MN-major or not.
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t N, bool a_mn, bool b_mn)
 {
-    return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((256u >> 4) << 24);
+    return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((256u >> 4) << 24);
 }
 
 __device__ __forceinline__ void raise(uint32_t bit) { atomicOr(&g_ortho_fault_word, bit); }
@@ -230,6 +234,12 @@ __device__ __forceinline__ uint32_t half_pair(float lo, float hi)
 {
     const __half2 p = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+// The E4M3 codes of X's lo part of two elements.
+__device__ __forceinline__ uint32_t lo_code(float lo0, float lo1)
+{
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo0 * kLoScale, lo1 * kLoScale), __NV_SATFINITE, __NV_E4M3);
 }
 
 __device__ __forceinline__ float2 half_unpair(uint32_t v)
@@ -252,47 +262,29 @@ __device__ __forceinline__ bool wait_count(const uint32_t *done, uint32_t need, 
     if (ld_acquire(done) < need) {
         const uint64_t t0 = ptx::globaltimer_ns();
         while (ld_acquire(done) < need) {
-            if (*abort || ptx::globaltimer_ns() - t0 > kWaitNs) return false;
-            __nanosleep(100);
+            const uint64_t t = ptx::globaltimer_ns() - t0;
+            if (*abort || t > kWaitNs) return false;
+            if (t > 5000) __nanosleep(200);
         }
     }
     asm volatile("fence.proxy.async;" ::: "memory");
     return true;
 }
 
-// Counts this warp's part of a tile, whose stores (TMA by lane 0, plain ones
-// by all lanes) are complete afterwards.  Whole warp.
-__device__ __forceinline__ void count_done(uint32_t *done, int lane)
-{
-    asm volatile("fence.proxy.async;" ::: "memory");
-    __syncwarp();
-    if (lane == 0) {
-        ptx::bulk_wait_all();
-        asm volatile("fence.proxy.async;" ::: "memory");
-        ptx::fence_acq_rel_gpu();
-        asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(done), "r"(1u) : "memory");
-    }
-}
-
 template <int BN>
 __device__ __forceinline__ Tile decode_tile(int i, const OrthoArgs &a)
 {
     const int per_step = 2 * a.sym_tiles + a.x_tiles;  // of one matrix
-    const int per_group = per_step * a.steps * a.group;
-    const int grp = i / per_group;
-    i -= grp * per_group;
-    const int size = min(a.group, a.batch - grp * a.group);
     Tile t;
-    t.step = i / (per_step * size);
-    i -= t.step * per_step * size;
-    const int sym = a.sym_tiles * size;
+    t.step = i / (per_step * a.batch);
+    i -= t.step * per_step * a.batch;
+    const int sym = a.sym_tiles * a.batch;
     t.kind = i < sym ? kGram : i < 2 * sym ? kPoly : t.step + 1 < a.steps ? kApply : kLast;
     i -= t.kind == kGram ? 0 : t.kind == kPoly ? sym : 2 * sym;
     const int tiles = t.kind <= kPoly ? a.sym_tiles : a.x_tiles;
-    const int b = i / tiles;
-    i -= b * tiles;
-    t.b = grp * a.group + b;
-    t.need = kWarpsPerTile * (uint32_t)(t.step * per_step + (t.kind == kGram   ? 0
+    t.b = i / tiles;
+    i -= t.b * tiles;
+    t.need = 2u * (uint32_t)(t.step * per_step + (t.kind == kGram   ? 0
                                                              : t.kind == kPoly ? a.sym_tiles
                                                                                : 2 * a.sym_tiles));
     if (t.kind <= kPoly) {
@@ -318,56 +310,95 @@ __device__ __forceinline__ Tile decode_tile(int i, const OrthoArgs &a)
     return t;
 }
 
+// Which K steps of a tile's operands are read as MN-major tiles: those before
+// left_mn, right_mn.  A and Bm hold their 256 x 256 tiles on and above the
+// diagonal, so columns before the row tile's diagonal come from the mirror
+// image; X's columns are MN-major all the way.
+struct Sides {
+    int left_mn, right_mn;
+};
+
+template <int BN>
+__device__ __forceinline__ Sides sides_of(const Tile &t)
+{
+    return {t.kind == kGram ? 0 : t.r0 / BK, t.kind == kGram ? 0 : t.kind == kPoly ? (t.c0 & ~255) / BK : 1 << 30};
+}
+
 // What an epilogue warp carries along.
 struct Epilogue {
     uint8_t *st, *st_lo;   // its staging blocks
     uint64_t *bar;         // of the blocks' loads
     uint32_t load_phase;
     int q, half, lane;
-    uint32_t rank, tmem;
+    uint32_t rank;
+    uint32_t *stored;      // [kSlots] in shared memory: warps whose part of a tile is written
+    uint32_t *pending;     // lane 0: the counter of a tile that it has not reported yet,
+    int pending_slot;      // and its slot
+
+    // Reports this warp's part of its last tile once its stores are
+    // complete; the last of the CTA's warps counts the CTA's half.  Lane 0.
+    __device__ __forceinline__ void flush()
+    {
+        if (!pending) return;
+        ptx::bulk_wait_all();
+        __threadfence_block();
+        if (atomicAdd(stored + pending_slot, 1u) == kEpiWarps - 1) {
+            stored[pending_slot] = 0;
+            ptx::fence_acq_rel_gpu();
+            asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(pending), "r"(1u) : "memory");
+        }
+        pending = nullptr;
+    }
 };
 
 // One tile's epilogue for one warp: lane quarter q (rows r0 + 128 rank + 32 q
 // ..), columns half * BN / 2 ... in blocks of 64.  Lane l holds row l of a
 // block; its 16-byte piece j is at (j ^ (l % 8)) * 16 of the row's 128 bytes
-// in the staging buffer (the tensor maps' swizzle).  Returns false when a
-// wait gave up.
+// in the staging buffer, and of lo's 64 bytes at (j ^ (l / 2 % 4)) * 16 (the
+// tensor maps' 128- and 64-byte swizzles).  The warp reports its previous
+// tile while this tile's first loads are on their way; before any wait that
+// may need that tile it reports first.  Returns false when a wait gave up.
 template <int KIND, int BN>
 __device__ __forceinline__ bool epilogue(const Tile &t, const OrthoMaps &maps, const OrthoArgs &args, Epilogue &ep,
-                                         uint64_t *tfull, uint32_t tfull_phase, uint32_t acc_tmem, bool ready,
-                                         volatile int *abort_flag)
+                                         uint64_t *ready, uint32_t ready_phase, uint64_t *tfull, uint32_t tfull_phase,
+                                         uint32_t acc_tmem, volatile int *abort_flag)
 {
     constexpr bool SYM = KIND == kGram || KIND == kPoly;
     constexpr bool PAIR_IN = KIND == kApply || KIND == kLast;
     const int lane = ep.lane, x = t.step & 1;
     const int rows = args.m, cols = SYM ? args.m : args.n;
     const int row0 = t.r0 + 128 * (int)ep.rank + 32 * ep.q, row = row0 + lane;
-    const bool mirrored = SYM && t.r0 + 256 <= t.c0;  // wholly above the diagonal's tiles
     uint8_t *const st = ep.st, *const st_lo = ep.st_lo;
-    bool have = false, failed = false;
+    bool failed = false;
 #pragma unroll 1
     for (int blk = 0; blk < BN / 128; ++blk) {
         const int cb = ep.half * (BN / 2) + 64 * blk, col0 = t.c0 + cb;
-        const bool in = ready && row0 < rows && col0 < cols;
-        // the block's own operands, while the products run
-        if (in && KIND != kGram) {
-            if (lane == 0) {
-                ptx::bulk_wait_group_read<0>();  // the buffers' last stores have read them
-                ptx::mbar_arrive_expect_tx(ep.bar, (PAIR_IN ? 2 : 1) * BLOCK);
-                ptx::tma_load_3d(st, PAIR_IN ? &maps.x_blk[x] : &maps.a_blk, col0, row0, t.b, ep.bar);
-                if (PAIR_IN) ptx::tma_load_3d(st_lo, &maps.lo_blk, col0, row0, t.b, ep.bar);
+        const bool in = row0 < rows && col0 < cols;
+        if (lane == 0) {
+            // the block's own operands, while the products run
+            if (KIND != kGram) {
+                if (blk == 0 && !ptx::mbar_try_wait(ready, ready_phase)) {
+                    ep.flush();
+                    failed = !ptx::mbar_wait_bounded(ready, ready_phase, abort_flag, kWaitNs);
+                }
+                if (in && !failed) {
+                    ptx::bulk_wait_group_read<0>();  // the buffers' last stores have read them
+                    ptx::mbar_arrive_expect_tx(ep.bar, BLOCK + (PAIR_IN ? LO_BLOCK : 0));
+                    ptx::tma_load_3d(st, PAIR_IN ? &maps.x_blk[x] : &maps.a_blk, col0, row0, t.b, ep.bar);
+                    if (PAIR_IN) ptx::tma_load_3d(st_lo, &maps.lo_blk, col0, row0, t.b, ep.bar);
+                }
             }
-            __syncwarp();
+            ep.flush();
         }
-        if (!have) {
-            have = true;
-            failed = !ready || *abort_flag || !wait_cluster(tfull, tfull_phase, abort_flag);
+        failed = __any_sync(0xffffffffu, failed);
+        if (blk == 0) {
+            failed = failed || *abort_flag || !wait_cluster(tfull, tfull_phase, abort_flag);
             failed = __any_sync(0xffffffffu, failed);
             ptx::tc_fence_after();
         }
         if (in && KIND != kGram) {
             const int keep = 0;
-            const bool got = ptx::mbar_wait_bounded(ep.bar, ep.load_phase, &keep, kWaitNs);
+            const bool got = failed || ptx::mbar_wait_bounded(ep.bar, ep.load_phase, &keep, kWaitNs);
             ep.load_phase ^= 1;
             failed = __any_sync(0xffffffffu, failed || !got);
         }
@@ -383,19 +414,24 @@ __device__ __forceinline__ bool epilogue(const Tile &t, const OrthoMaps &maps, c
             uint32_t r[32];
             ptx::tmem_ld32(taddr + 32 * h, r);
             ptx::tmem_wait_ld();
-            float v[32];
+            uint32_t lo_w[8];  // 32 codes
+            uint4 *p_lo[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                p_lo[j] = reinterpret_cast<uint4 *>(st_lo + lane * 64 + (((2 * h + j) ^ (lane >> 1 & 3)) << 4));
+                if (PAIR_IN) {
+                    const uint4 w = *p_lo[j];
+                    lo_w[4 * j] = w.x, lo_w[4 * j + 1] = w.y, lo_w[4 * j + 2] = w.z, lo_w[4 * j + 3] = w.w;
+                }
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int at = lane * 128 + (((4 * h + j) ^ (lane & 7)) << 4);
-                uint4 *p = reinterpret_cast<uint4 *>(st + at), *p_lo = reinterpret_cast<uint4 *>(st_lo + at);
-                uint32_t in_w[4] = {0, 0, 0, 0}, lo_w[4] = {0, 0, 0, 0}, o[4], o_lo[4];
+                uint4 *p = reinterpret_cast<uint4 *>(st + lane * 128 + (((4 * h + j) ^ (lane & 7)) << 4));
+                uint32_t in_w[4] = {0, 0, 0, 0}, o[4];
+                float last[8];
                 if (KIND != kGram) {
                     const uint4 w = *p;
                     in_w[0] = w.x, in_w[1] = w.y, in_w[2] = w.z, in_w[3] = w.w;
-                }
-                if (PAIR_IN) {
-                    const uint4 w = *p_lo;
-                    lo_w[0] = w.x, lo_w[1] = w.y, lo_w[2] = w.z, lo_w[3] = w.w;
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -408,13 +444,15 @@ __device__ __forceinline__ bool epilogue(const Tile &t, const OrthoMaps &maps, c
                         const float2 y = half_unpair(in_w[e]);
                         v0 = fmaf(args.pc, a0, args.pb * y.x), v1 = fmaf(args.pc, a1, args.pb * y.y);
                     } else {
-                        const float2 y = half_unpair(in_w[e]), z = half_unpair(lo_w[e]);
-                        v0 = fmaf(args.xc, a0, args.xa * (y.x + z.x));
-                        v1 = fmaf(args.xc, a1, args.xa * (y.y + z.y));
+                        const float2 y = half_unpair(in_w[e]);
+                        const uint32_t code = lo_w[2 * j + e / 2] >> (16 * (e & 1));
+                        const float2 z = __half22float2(
+                            __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)code, __NV_E4M3)));
+                        v0 = fmaf(args.xc, a0, args.xa * fmaf(z.x, kLoInv, y.x));
+                        v1 = fmaf(args.xc, a1, args.xa * fmaf(z.y, kLoInv, y.y));
                     }
-                    if (KIND == kLast) v0 *= args.out_scale, v1 *= args.out_scale;
-                    v[c] = v0, v[c + 1] = v1;
                     if (KIND == kLast) {
+                        last[2 * e] = v0 *= args.out_scale, last[2 * e + 1] = v1 *= args.out_scale;
                         const __nv_bfloat162 z = __floats2bfloat162_rn(v0, v1);
                         o[e] = *reinterpret_cast<const uint32_t *>(&z);
                     } else {
@@ -422,25 +460,24 @@ __device__ __forceinline__ bool epilogue(const Tile &t, const OrthoMaps &maps, c
                     }
                     if (KIND == kApply) {
                         const float2 hi = half_unpair(o[e]);
-                        o_lo[e] = half_pair(v0 - hi.x, v1 - hi.y);
+                        const uint32_t code = lo_code(v0 - hi.x, v1 - hi.y);
+                        uint32_t &w = lo_w[2 * j + e / 2];
+                        w = e & 1 ? (w & 0xffffu) | (code << 16) : (w & 0xffff0000u) | code;
                     }
                 }
                 *p = make_uint4(o[0], o[1], o[2], o[3]);
-                if (KIND == kApply) *p_lo = make_uint4(o_lo[0], o_lo[1], o_lo[2], o_lo[3]);
-            }
-            const int c = col0 + 32 * h;
-            if (mirrored && row < rows) {
-                __half *dst = (KIND == kGram ? args.a : args.bm) + (int64_t)t.b * args.m * args.pitch + row;
+                if (KIND == kLast && args.transposed && row < rows) {
+                    const int c = col0 + 32 * h + 8 * j;
+                    __nv_bfloat16 *dst = args.out + (int64_t)t.b * rows * cols + row;
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (c + e < cols) dst[(c + e) * args.pitch] = __float2half_rn(v[e]);
+                    for (int e = 0; e < 8; ++e)
+                        if (c + e < cols) dst[(int64_t)(c + e) * args.out_cols] = __float2bfloat16_rn(last[e]);
+                }
             }
-            if (KIND == kLast && args.transposed && row < rows) {
-                __nv_bfloat16 *dst = args.out + (int64_t)t.b * rows * cols + row;
+            if (KIND == kApply)
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (c + e < cols) dst[(int64_t)(c + e) * args.out_cols] = __float2bfloat16_rn(v[e]);
-            }
+                for (int j = 0; j < 2; ++j)
+                    *p_lo[j] = make_uint4(lo_w[4 * j], lo_w[4 * j + 1], lo_w[4 * j + 2], lo_w[4 * j + 3]);
         }
         if (KIND == kLast) {
             // the caller's rows have any pitch: from the staging buffer, a
@@ -495,8 +532,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint64_t *tfull = empty + C::STAGES;
     uint64_t *tempty = tfull + 2;
     uint64_t *drain = tempty + 2;
-    uint64_t *loaded = drain + 1;  // [kEpiWarps]: an epilogue warp's operand blocks
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(loaded + kEpiWarps);
+    uint64_t *loaded = drain + 1;           // [kEpiWarps]: an epilogue warp's operand blocks
+    uint64_t *ready = loaded + kEpiWarps;   // [kSlots]: the tile's operands are complete
+    uint32_t *stored = reinterpret_cast<uint32_t *>(ready + kSlots);  // [kSlots]
+    uint32_t *tmem_slot = stored + kSlots;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -508,10 +547,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(tfull + b, 1);
-            ptx::mbar_init(tempty + b, kWarpsPerTile);
+            ptx::mbar_init(tempty + b, 2 * kEpiWarps);
         }
         ptx::mbar_init(drain, 1);
         for (int w = 0; w < kEpiWarps; ++w) ptx::mbar_init(loaded + w, 1);
+        for (int w = 0; w < kSlots; ++w) {
+            ptx::mbar_init(ready + w, 1);
+            stored[w] = 0;
+        }
         *abort_flag = 0;
         ptx::fence_barrier_init();
     }
@@ -530,23 +573,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             int stage = 0;
             uint32_t phase = 0;
-            for (int i = first; i < total && !*abort_flag; i += pairs) {
+            int li = 0;
+            for (int i = first; i < total && !*abort_flag; i += pairs, ++li) {
                 const Tile t = decode_tile<BN>(i, args);
-                const bool apply = t.kind >= kApply;
                 const int x = t.step & 1;
+                const int ksteps = ((t.kind == kGram ? args.n : args.m) + BK - 1) / BK;
+                const int row = t.r0 + 128 * (int)rank, col = t.c0 + BN / 2 * (int)rank;
+                const Sides sides = sides_of<BN>(t);
                 const CUtensorMap *left = t.kind == kGram   ? &maps.x_left[x]
                                           : t.kind == kPoly ? &maps.a_left
                                                             : &maps.b_left;
-                const CUtensorMap *right = t.kind == kGram   ? &maps.x_right[x]
-                                           : t.kind == kPoly ? &maps.a_right
-                                                             : &maps.x_cols[x];
-                const int ksteps = ((t.kind == kGram ? args.n : args.m) + BK - 1) / BK;
-                const int row = t.r0 + 128 * (int)rank, col = t.c0 + BN / 2 * (int)rank;
+                const CUtensorMap *left_mn = t.kind == kPoly ? &maps.a_cols : &maps.b_cols;
+                const CUtensorMap *right = t.kind == kGram ? &maps.x_right[x] : &maps.a_right;
+                const CUtensorMap *right_mn = t.kind == kPoly ? &maps.a_cols : &maps.x_cols[x];
                 if (!wait_count(args.done + t.b, t.need, abort_flag)) {
                     if (!*abort_flag) raise(FAULT_GEMM_PRODUCER);
                     *abort_flag = 1;
                     break;
                 }
+                ptx::mbar_arrive(ready + li % kSlots);
                 for (int ks = 0; ks < ksteps; ++ks) {
                     if (!wait_cluster(empty + stage, phase ^ 1, abort_flag)) {
                         if (!*abort_flag) raise(FAULT_GEMM_PRODUCER);
@@ -558,11 +603,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (rank == 0) ptx::mbar_arrive_expect_tx(full + stage, 2 * C::STAGE_BYTES);
                     uint8_t *l = smem + stage * C::STAGE_BYTES;
                     uint8_t *r = l + A_BYTES;
-                    pair_load_3d(l, left, ks * BK, row, t.b, bar);
-                    if (apply) {
+                    if (ks < sides.left_mn) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            pair_load_3d(l + h * (64 * BK * 2), left_mn, row + 64 * h, ks * BK, t.b, bar);
+                    } else {
+                        pair_load_3d(l, left, ks * BK, row, t.b, bar);
+                    }
+                    if (ks < sides.right_mn) {
 #pragma unroll
                         for (int h = 0; h < BN / 128; ++h)
-                            pair_load_3d(r + h * (64 * BK * 2), right, col + 64 * h, ks * BK, t.b, bar);
+                            pair_load_3d(r + h * (64 * BK * 2), right_mn, col + 64 * h, ks * BK, t.b, bar);
                     } else {
                         pair_load_3d(r, right, ks * BK, col, t.b, bar);
                     }
@@ -586,9 +637,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int li = 0;
             for (int i = first; i < total && !*abort_flag; i += pairs, ++li) {
                 const Tile t = decode_tile<BN>(i, args);
-                const bool apply = t.kind >= kApply;
                 const int ksteps = ((t.kind == kGram ? args.n : args.m) + BK - 1) / BK;
-                const uint32_t idesc = idesc_f16(BN, apply);
+                const Sides sides = sides_of<BN>(t);
                 const int acc = li & 1;
                 if (!wait_cluster(tempty + acc, ((li >> 1) & 1) ^ 1, abort_flag)) {
                     if (!*abort_flag) raise(FAULT_GEMM_MMA);
@@ -608,11 +658,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     ptx::tc_fence_after();
                     const uint32_t l = ptx::smem_u32(smem + stage * C::STAGE_BYTES);
                     const uint32_t r = l + A_BYTES;
+                    // K-major: a K step of 16 is 32 bytes along the rows; MN-major:
+                    // 16 rows of 128 bytes, the next 64 of M or N a box on
+                    const bool l_mn = ks < sides.left_mn, r_mn = ks < sides.right_mn;
+                    const uint32_t idesc = idesc_f16(BN, l_mn, r_mn);
+                    uint64_t ld = l_mn ? ptx::sw128_desc_mn(l, 64 * BK * 2) : ptx::sw128_desc(l);
+                    uint64_t rd = r_mn ? ptx::sw128_desc_mn(r, 64 * BK * 2) : ptx::sw128_desc(r);
+                    const uint64_t l_step = l_mn ? 2048 >> 4 : 32 >> 4, r_step = r_mn ? 2048 >> 4 : 32 >> 4;
 #pragma unroll
-                    for (int k = 0; k < BK / 16; ++k)
-                        pair_mma(d, ptx::sw128_desc(l + k * 32),
-                                 apply ? ptx::sw128_desc_mn(r + k * 2048, 64 * BK * 2) : ptx::sw128_desc(r + k * 32),
-                                 idesc, (ks | k) != 0);
+                    for (int k = 0; k < BK / 16; ++k) pair_mma(d, ld + k * l_step, rd + k * r_step, idesc, (ks | k) != 0);
                     pair_commit(empty + stage);
                     if (++stage == C::STAGES) {
                         stage = 0;
@@ -629,35 +683,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else {
         // ---------------------------------------------------- epilogue
         Epilogue ep;
-        ep.st = staging + (warp - 2) * 2 * BLOCK;
-        ep.st_lo = ep.st + BLOCK;
+        ep.st = staging + (warp - 2) * BLOCK;
+        ep.st_lo = staging + kEpiWarps * BLOCK + (warp - 2) * LO_BLOCK;
         ep.bar = loaded + (warp - 2);
         ep.load_phase = 0;
         ep.q = warp & 3;
         ep.half = (warp - 2) >> 2;
         ep.lane = lane;
         ep.rank = rank;
-        ep.tmem = tmem;
+        ep.stored = stored;
+        ep.pending = nullptr;
         int li = 0;
         for (int i = first; i < total; i += pairs, ++li) {
             const Tile t = decode_tile<BN>(i, args);
             const int acc = li & 1;
             const uint32_t ph = (li >> 1) & 1, at = tmem + acc * BN;
-            // the tile's own operands are complete (gram has none)
-            bool ready = true;
-            if (t.kind != kGram) {
-                if (lane == 0) ready = wait_count(args.done + t.b, t.need, abort_flag);
-                ready = __shfl_sync(0xffffffffu, ready, 0);
-            }
+            uint64_t *rd = ready + li % kSlots;
+            const uint32_t rph = (li / kSlots) & 1;
             bool ok;
             if (t.kind == kGram)
-                ok = epilogue<kGram, BN>(t, maps, args, ep, tfull + acc, ph, at, ready, abort_flag);
+                ok = epilogue<kGram, BN>(t, maps, args, ep, rd, rph, tfull + acc, ph, at, abort_flag);
             else if (t.kind == kPoly)
-                ok = epilogue<kPoly, BN>(t, maps, args, ep, tfull + acc, ph, at, ready, abort_flag);
+                ok = epilogue<kPoly, BN>(t, maps, args, ep, rd, rph, tfull + acc, ph, at, abort_flag);
             else if (t.kind == kApply)
-                ok = epilogue<kApply, BN>(t, maps, args, ep, tfull + acc, ph, at, ready, abort_flag);
+                ok = epilogue<kApply, BN>(t, maps, args, ep, rd, rph, tfull + acc, ph, at, abort_flag);
             else
-                ok = epilogue<kLast, BN>(t, maps, args, ep, tfull + acc, ph, at, ready, abort_flag);
+                ok = epilogue<kLast, BN>(t, maps, args, ep, rd, rph, tfull + acc, ph, at, abort_flag);
             if (!ok) {
                 if (lane == 0) {
                     if (!*abort_flag) raise(FAULT_GEMM_EPILOGUE);
@@ -667,9 +718,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_cluster(map_to(ptx::smem_u32(tempty + acc), 0));
-            count_done(args.done + t.b, lane);
+            if (lane == 0) {
+                arrive_cluster(map_to(ptx::smem_u32(tempty + acc), 0));
+                ep.pending = args.done + t.b;
+                ep.pending_slot = li % kSlots;
+            }
         }
+        if (lane == 0) ep.flush();
         if (lane == 0) ptx::bulk_wait_all();
         __syncwarp();
     }
@@ -757,26 +812,26 @@ __device__ __forceinline__ float input_factor(const float *partial, int parts, f
     return (float)(1 << kXBits) / (sqrtf(warp_sum(s)) + eps);
 }
 
-__device__ __forceinline__ void split8(const float (&v)[8], __half *hi, __half *lo)
+__device__ __forceinline__ void split8(const float (&v)[8], __half *hi, uint8_t *lo)
 {
-    uint32_t h[4], l[4];
+    uint32_t h[4], l[2] = {0, 0};
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         h[q] = half_pair(v[2 * q], v[2 * q + 1]);
         const float2 f = half_unpair(h[q]);
-        l[q] = half_pair(v[2 * q] - f.x, v[2 * q + 1] - f.y);
+        l[q / 2] |= lo_code(v[2 * q] - f.x, v[2 * q + 1] - f.y) << (16 * (q & 1));
     }
     *reinterpret_cast<uint4 *>(hi) = make_uint4(h[0], h[1], h[2], h[3]);
-    *reinterpret_cast<uint4 *>(lo) = make_uint4(l[0], l[1], l[2], l[3]);
+    *reinterpret_cast<uint2 *>(lo) = make_uint2(l[0], l[1]);
 }
 
-// X hi and lo [b][m][pitch] from g [b][M][N]: M and N multiples of 8.  WIDE:
+// X hi and lo [b][m][pitch] from g [b][M][N]: M and N multiples of 16.  WIDE:
 // the rows of X are those of g.  Else a block transposes 64 x 64 elements
 // through shared memory.
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(256) ortho_split8_kernel(const T *__restrict__ g, int M, int N,
                                                            const float *__restrict__ partial, int parts, float eps,
-                                                           __half *__restrict__ hi, __half *__restrict__ lo)
+                                                           __half *__restrict__ hi, uint8_t *__restrict__ lo)
 {
     const int b = blockIdx.z;
     const float f = input_factor(partial + b * kMaxParts, parts, eps);
@@ -823,7 +878,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) ortho_split_kernel(const T *__restrict__ g, int M, int N,
                                                           const float *__restrict__ partial, int parts, float eps,
                                                           bool tall, int64_t pitch, __half *__restrict__ hi,
-                                                          __half *__restrict__ lo)
+                                                          uint8_t *__restrict__ lo)
 {
     __shared__ float tile[32][33];
     const int b = blockIdx.z, tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
@@ -835,7 +890,7 @@ __global__ void __launch_bounds__(256) ortho_split_kernel(const T *__restrict__ 
     auto put = [&](int r, int c, float v) {
         const __half h = __float2half_rn(v);
         hi[base + r * pitch + c] = h;
-        lo[base + r * pitch + c] = __float2half_rn(v - __half2float(h));
+        lo[base + r * pitch + c] = (uint8_t)lo_code(v - __half2float(h), 0.0f);
     };
     for (int y = ty; y < 32; y += 8) {
         const int r = r0 + y, c = c0 + tx;
@@ -874,20 +929,22 @@ EncodeFn encoder()
     return fn;
 }
 
-// [batch][rows][cols] FP16 with `pitch` elements per row, boxes of 64
-// columns (128 bytes, 128-byte swizzle) x box_rows rows
-cudaError_t make_map(CUtensorMap *map, const __half *base, int64_t batch, int64_t rows, int64_t cols, int64_t pitch,
-                     int box_rows)
+// [batch][rows][cols] with `pitch` elements per row, FP16 or bytes, boxes of
+// 64 columns x box_rows rows, swizzled over the box's row (128 or 64 bytes)
+cudaError_t make_map(CUtensorMap *map, const void *base, bool bytes, int64_t batch, int64_t rows, int64_t cols,
+                     int64_t pitch, int box_rows)
 {
     EncodeFn enc = encoder();
     if (!enc) return cudaErrorNotSupported;
+    const int size = bytes ? 1 : 2;
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
-    const cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)(pitch * rows) * 2};
+    const cuuint64_t strides[2] = {(cuuint64_t)pitch * size, (cuuint64_t)(pitch * rows) * size};
     const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half *>(base), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUtensorMapSwizzle swizzle = bytes ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    CUresult r = enc(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                     const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -901,7 +958,7 @@ Region layout(int64_t B, int64_t M, int64_t N)
     Region L{};
     L.m = M < N ? M : N;
     L.n = M < N ? N : M;
-    L.x_pitch = round_up(L.n, 8);  // rows start on 16 bytes
+    L.x_pitch = round_up(L.n, 16);  // rows of hi and lo start on 16 bytes
     L.a_pitch = round_up(L.m, 8);
     size_t o = 0;
     auto take = [&](size_t bytes) {
@@ -914,7 +971,7 @@ Region layout(int64_t B, int64_t M, int64_t N)
     const size_t x = (size_t)(B * L.m * L.x_pitch) * 2, a = (size_t)(B * L.m * L.a_pitch) * 2;
     L.hi[0] = take(x);
     L.hi[1] = take(x);
-    L.lo = take(x);
+    L.lo = take(x / 2);
     L.a = take(a);
     L.bm = take(a);
     L.total = o;
@@ -924,12 +981,12 @@ Region layout(int64_t B, int64_t M, int64_t N)
 template <int BN>
 cudaError_t run_steps(const OrthoCall &c, char *ws, const Region &L, int pairs, cudaStream_t s)
 {
-    auto *lo = (__half *)(ws + L.lo), *A = (__half *)(ws + L.a), *Bm = (__half *)(ws + L.bm);
+    auto *A = (__half *)(ws + L.a), *Bm = (__half *)(ws + L.bm);
     __half *hi[2] = {(__half *)(ws + L.hi[0]), (__half *)(ws + L.hi[1])};
     OrthoMaps t;
     cudaError_t e = cudaSuccess;
     auto map = [&](CUtensorMap *m, const __half *p, int64_t cols, int64_t pitch, int box_rows) {
-        if (e == cudaSuccess) e = make_map(m, p, c.B, L.m, cols, pitch, box_rows);
+        if (e == cudaSuccess) e = make_map(m, p, false, c.B, L.m, cols, pitch, box_rows);
     };
     for (int i = 0; i < 2; ++i) {
         map(&t.x_left[i], hi[i], L.n, L.x_pitch, 128);
@@ -937,11 +994,13 @@ cudaError_t run_steps(const OrthoCall &c, char *ws, const Region &L, int pairs, 
         map(&t.x_cols[i], hi[i], L.n, L.x_pitch, 64);
         map(&t.x_blk[i], hi[i], L.n, L.x_pitch, 32);
     }
-    map(&t.lo_blk, lo, L.n, L.x_pitch, 32);
+    if (e == cudaSuccess) e = make_map(&t.lo_blk, ws + L.lo, true, c.B, L.m, L.n, L.x_pitch, 32);
     map(&t.a_left, A, L.m, L.a_pitch, 128);
     map(&t.a_right, A, L.m, L.a_pitch, BN / 2);
+    map(&t.a_cols, A, L.m, L.a_pitch, 64);
     map(&t.a_blk, A, L.m, L.a_pitch, 32);
     map(&t.b_left, Bm, L.m, L.a_pitch, 128);
+    map(&t.b_cols, Bm, L.m, L.a_pitch, 64);
     map(&t.b_blk, Bm, L.m, L.a_pitch, 32);
     if (e != cudaSuccess) return e;
 
@@ -951,7 +1010,6 @@ cudaError_t run_steps(const OrthoCall &c, char *ws, const Region &L, int pairs, 
     a.n = (int)L.n;
     a.batch = (int)c.B;
     a.steps = c.steps;
-    a.group = a.batch;
     a.row_tiles = (a.m + 255) / 256;
     a.sym_cols = (a.m + BN - 1) / BN;
     a.x_cols = (a.n + BN - 1) / BN;
@@ -963,9 +1021,6 @@ cudaError_t run_steps(const OrthoCall &c, char *ws, const Region &L, int pairs, 
     a.xa = c.a;
     a.xc = pow2(-kBBits);
     a.out_scale = c.out_scale * pow2(-kXBits);
-    a.a = A;
-    a.bm = Bm;
-    a.pitch = L.a_pitch;
     a.out = (__nv_bfloat16 *)c.out;
     a.out_cols = (int)c.N;
     a.transposed = c.M > c.N;
@@ -986,13 +1041,13 @@ cudaError_t run_steps(const OrthoCall &c, char *ws, const Region &L, int pairs, 
 }
 
 template <typename T>
-cudaError_t launch_input(const OrthoCall &c, const Region &L, float *partial, uint32_t *done, __half *hi, __half *lo,
+cudaError_t launch_input(const OrthoCall &c, const Region &L, float *partial, uint32_t *done, __half *hi, uint8_t *lo,
                          cudaStream_t s)
 {
     const int64_t count = c.M * c.N;
     const int64_t slices = ceil_div(count, 8192);
     const int parts = (int)(slices < kMaxParts ? slices : kMaxParts);
-    const bool tall = c.M > c.N, by8 = c.M % 8 == 0 && c.N % 8 == 0;
+    const bool tall = c.M > c.N, by16 = c.M % 16 == 0 && c.N % 16 == 0;
     const int64_t fit = kTurnBytes / (count * (int64_t)sizeof(T));
     const int64_t turn = fit < 1 ? 1 : fit < c.B ? fit : c.B;
     for (int64_t b = 0; b < c.B; b += turn) {
@@ -1002,11 +1057,11 @@ cudaError_t launch_input(const OrthoCall &c, const Region &L, float *partial, ui
         const int64_t at = b * L.m * L.x_pitch;
         ortho_norm_kernel<<<dim3(parts, n), 256, 0, s>>>(g, count, part, done + b);
         const int M = (int)c.M, N = (int)c.N;
-        if (by8 && !tall)
+        if (by16 && !tall)
             ortho_split8_kernel<T, true>
                 <<<dim3((unsigned)ceil_div(count, 8 * 256 * 4), 1, n), 256, 0, s>>>(g, M, N, part, parts, c.eps,
                                                                                     hi + at, lo + at);
-        else if (by8)
+        else if (by16)
             ortho_split8_kernel<T, false>
                 <<<dim3((unsigned)ceil_div(N, 64), (unsigned)ceil_div(M, 64), n), 256, 0, s>>>(g, M, N, part, parts,
                                                                                                c.eps, hi + at, lo + at);
@@ -1049,7 +1104,8 @@ cudaError_t launch_orthogonalize(const OrthoCall &c, void *workspace, int pairs,
     const Region L = layout(c.B, c.M, c.N);
     char *ws = (char *)workspace;
     auto *partial = (float *)(ws + L.partial);
-    auto *hi = (__half *)(ws + L.hi[0]), *lo = (__half *)(ws + L.lo);
+    auto *hi = (__half *)(ws + L.hi[0]);
+    auto *lo = (uint8_t *)(ws + L.lo);
     auto *done = (uint32_t *)(ws + L.done);
     const cudaError_t e = c.g_f32 ? launch_input<float>(c, L, partial, done, hi, lo, s)
                                   : launch_input<__nv_bfloat16>(c, L, partial, done, hi, lo, s);
