@@ -214,10 +214,10 @@ int moe_ffn_forward_routed_train(const void *x_bf16, const int32_t *topk_idx,
  *   g       [B,M,N], g_type
  *   out_bf16 [B,M,N]; scaled by out_scale before it is rounded
  * The products run on the tensor cores with FP16 operands and FP32 sums.  X
- * is kept between steps as an FP16 pair hi + lo (about 22 significant bits),
- * of which the products read hi; A and b A + c A A are rounded to FP16.
- * Relative error of out in the 2-norm: below 4e-3 for the usual
- * coefficients, most of it out's own rounding to BF16.
+ * is kept between steps as a pair of FP16 values (about 22 significant bits),
+ * of which the products read the high one; A and b A + c A A are rounded to
+ * FP16.  Relative error in the 2-norm for the usual coefficients: up to 2e-3
+ * before out's rounding to BF16, and 1.7e-3 from that.
  * A matrix of zeros gives zeros; a NaN or an infinity spreads over its whole
  * matrix and no other.  Squares are summed in FP32: entries below about
  * 1e-19 count as zero in the norm.

@@ -17,13 +17,14 @@
 // them: 1e-2 after five steps, up to 0.2 for a matrix of low rank plus
 // noise).  FP16 has three more bits at the same rate, and its range is
 // enough because every singular value is at most about 1.2: the stored X is
-// 2^10 X, A 2^14 A, Bm 2^11 Bm.  X between steps is a pair: hi in FP16 and lo
-// = X - hi in E4M3 (times 2^14), so that a X, the part that carries the
-// singular directions from step to step, has about 15 bits; the products
-// read hi.  In 64-bit simulations of these roundings the result is within
-// %SIMLO% (low rank, power-law spectra) to %SIMGAUSS% (Gaussian) of the exact one
-// (an FP16 lo: 8e-4 and 2.6e-3, for twice the bytes), and a single FP16 X
-// within 2e-2.
+// 2^10 X, A 2^14 A, Bm 2^11 Bm.  X between steps is a pair of FP16 values,
+// hi and lo = 2^12 (X - hi), so that a X, the part that carries the singular
+// directions from step to step, has about 22 bits; the products read hi.  In
+// 64-bit simulations of these roundings the result, before its rounding to
+// BF16, is within 2e-4 (rank one, as an expert's gradient from one token) to
+// 2e-3 (small Gaussian matrices) of the exact one.  A single FP16 X is 2e-2
+// off for a matrix of low rank, and a lo part of 8 bits (E4M3) 3.5e-3 to
+// 2e-2 for one of rank one.
 //
 // The products.  A pair of CTAs (a cluster of two) computes a 256 x BN tile
 // with tcgen05.mma.cta_group::2: each CTA loads its 128 rows of the left and
@@ -73,14 +74,13 @@ namespace {
 
 // the powers of two that X, A, Bm and X's lo part (beside X's own) are stored with
 constexpr int kXBits = 10, kABits = 14, kBBits = 11;
-constexpr float kLoScale = 16384.0f, kLoInv = 1.0f / 16384.0f;
+constexpr float kLoScale = 4096.0f, kLoInv = 1.0f / 4096.0f;
 
 constexpr int BK = 64;                    // K per stage: 128 bytes of FP16, the swizzle's width
 constexpr int A_BYTES = 128 * BK * 2;     // one CTA's left operand of a stage
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr int BLOCK = 32 * 64 * 2;        // one staged 32 x 64 FP16 block
-constexpr int LO_BLOCK = 32 * 64;         // and its E4M3 part
 constexpr int kSlots = 4;                 // tiles that the producer and the epilogue can be apart, and one more
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -91,7 +91,7 @@ struct Cfg {
     static constexpr int B_BYTES = BN / 2 * BK * 2;  // one CTA's right operand of a stage
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int STAGES = BN == 256 ? 5 : 6;
-    static constexpr int STAGING = kEpiWarps * (BLOCK + LO_BLOCK);
+    static constexpr int STAGING = kEpiWarps * 2 * BLOCK;
     static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + STAGING + 512;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -236,12 +236,6 @@ __device__ __forceinline__ uint32_t half_pair(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&p);
 }
 
-// The E4M3 codes of X's lo part of two elements.
-__device__ __forceinline__ uint32_t lo_code(float lo0, float lo1)
-{
-    return __nv_cvt_float2_to_fp8x2(make_float2(lo0 * kLoScale, lo1 * kLoScale), __NV_SATFINITE, __NV_E4M3);
-}
-
 __device__ __forceinline__ float2 half_unpair(uint32_t v)
 {
     return __half22float2(*reinterpret_cast<const __half2 *>(&v));
@@ -354,8 +348,7 @@ struct Epilogue {
 // One tile's epilogue for one warp: lane quarter q (rows r0 + 128 rank + 32 q
 // ..), columns half * BN / 2 ... in blocks of 64.  Lane l holds row l of a
 // block; its 16-byte piece j is at (j ^ (l % 8)) * 16 of the row's 128 bytes
-// in the staging buffer, and of lo's 64 bytes at (j ^ (l / 2 % 4)) * 16 (the
-// tensor maps' 128- and 64-byte swizzles).  The warp reports its previous
+// in the staging buffer (the tensor maps' swizzle).  The warp reports its previous
 // tile while this tile's first loads are on their way; before any wait that
 // may need that tile it reports first.  Returns false when a wait gave up.
 template <int KIND, int BN>
@@ -383,7 +376,7 @@ __device__ __forceinline__ bool epilogue(const Tile &t, const OrthoMaps &maps, c
                 }
                 if (in && !failed) {
                     ptx::bulk_wait_group_read<0>();  // the buffers' last stores have read them
-                    ptx::mbar_arrive_expect_tx(ep.bar, BLOCK + (PAIR_IN ? LO_BLOCK : 0));
+                    ptx::mbar_arrive_expect_tx(ep.bar, (PAIR_IN ? 2 : 1) * BLOCK);
                     ptx::tma_load_3d(st, PAIR_IN ? &maps.x_blk[x] : &maps.a_blk, col0, row0, t.b, ep.bar);
                     if (PAIR_IN) ptx::tma_load_3d(st_lo, &maps.lo_blk, col0, row0, t.b, ep.bar);
                 }
@@ -414,24 +407,19 @@ __device__ __forceinline__ bool epilogue(const Tile &t, const OrthoMaps &maps, c
             uint32_t r[32];
             ptx::tmem_ld32(taddr + 32 * h, r);
             ptx::tmem_wait_ld();
-            uint32_t lo_w[8];  // 32 codes
-            uint4 *p_lo[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                p_lo[j] = reinterpret_cast<uint4 *>(st_lo + lane * 64 + (((2 * h + j) ^ (lane >> 1 & 3)) << 4));
-                if (PAIR_IN) {
-                    const uint4 w = *p_lo[j];
-                    lo_w[4 * j] = w.x, lo_w[4 * j + 1] = w.y, lo_w[4 * j + 2] = w.z, lo_w[4 * j + 3] = w.w;
-                }
-            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                uint4 *p = reinterpret_cast<uint4 *>(st + lane * 128 + (((4 * h + j) ^ (lane & 7)) << 4));
-                uint32_t in_w[4] = {0, 0, 0, 0}, o[4];
+                const int at = lane * 128 + (((4 * h + j) ^ (lane & 7)) << 4);
+                uint4 *p = reinterpret_cast<uint4 *>(st + at), *p_lo = reinterpret_cast<uint4 *>(st_lo + at);
+                uint32_t in_w[4] = {0, 0, 0, 0}, lo_w[4] = {0, 0, 0, 0}, o[4], o_lo[4];
                 float last[8];
                 if (KIND != kGram) {
                     const uint4 w = *p;
                     in_w[0] = w.x, in_w[1] = w.y, in_w[2] = w.z, in_w[3] = w.w;
+                }
+                if (PAIR_IN) {
+                    const uint4 w = *p_lo;
+                    lo_w[0] = w.x, lo_w[1] = w.y, lo_w[2] = w.z, lo_w[3] = w.w;
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -444,10 +432,7 @@ __device__ __forceinline__ bool epilogue(const Tile &t, const OrthoMaps &maps, c
                         const float2 y = half_unpair(in_w[e]);
                         v0 = fmaf(args.pc, a0, args.pb * y.x), v1 = fmaf(args.pc, a1, args.pb * y.y);
                     } else {
-                        const float2 y = half_unpair(in_w[e]);
-                        const uint32_t code = lo_w[2 * j + e / 2] >> (16 * (e & 1));
-                        const float2 z = __half22float2(
-                            __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)code, __NV_E4M3)));
+                        const float2 y = half_unpair(in_w[e]), z = half_unpair(lo_w[e]);
                         v0 = fmaf(args.xc, a0, args.xa * fmaf(z.x, kLoInv, y.x));
                         v1 = fmaf(args.xc, a1, args.xa * fmaf(z.y, kLoInv, y.y));
                     }
@@ -460,12 +445,11 @@ __device__ __forceinline__ bool epilogue(const Tile &t, const OrthoMaps &maps, c
                     }
                     if (KIND == kApply) {
                         const float2 hi = half_unpair(o[e]);
-                        const uint32_t code = lo_code(v0 - hi.x, v1 - hi.y);
-                        uint32_t &w = lo_w[2 * j + e / 2];
-                        w = e & 1 ? (w & 0xffffu) | (code << 16) : (w & 0xffff0000u) | code;
+                        o_lo[e] = half_pair((v0 - hi.x) * kLoScale, (v1 - hi.y) * kLoScale);
                     }
                 }
                 *p = make_uint4(o[0], o[1], o[2], o[3]);
+                if (KIND == kApply) *p_lo = make_uint4(o_lo[0], o_lo[1], o_lo[2], o_lo[3]);
                 if (KIND == kLast && args.transposed && row < rows) {
                     const int c = col0 + 32 * h + 8 * j;
                     __nv_bfloat16 *dst = args.out + (int64_t)t.b * rows * cols + row;
@@ -474,10 +458,6 @@ __device__ __forceinline__ bool epilogue(const Tile &t, const OrthoMaps &maps, c
                         if (c + e < cols) dst[(int64_t)(c + e) * args.out_cols] = __float2bfloat16_rn(last[e]);
                 }
             }
-            if (KIND == kApply)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    *p_lo[j] = make_uint4(lo_w[4 * j], lo_w[4 * j + 1], lo_w[4 * j + 2], lo_w[4 * j + 3]);
         }
         if (KIND == kLast) {
             // the caller's rows have any pitch: from the staging buffer, a
@@ -683,8 +663,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else {
         // ---------------------------------------------------- epilogue
         Epilogue ep;
-        ep.st = staging + (warp - 2) * BLOCK;
-        ep.st_lo = staging + kEpiWarps * BLOCK + (warp - 2) * LO_BLOCK;
+        ep.st = staging + (warp - 2) * 2 * BLOCK;
+        ep.st_lo = ep.st + BLOCK;
         ep.bar = loaded + (warp - 2);
         ep.load_phase = 0;
         ep.q = warp & 3;
@@ -812,26 +792,26 @@ __device__ __forceinline__ float input_factor(const float *partial, int parts, f
     return (float)(1 << kXBits) / (sqrtf(warp_sum(s)) + eps);
 }
 
-__device__ __forceinline__ void split8(const float (&v)[8], __half *hi, uint8_t *lo)
+__device__ __forceinline__ void split8(const float (&v)[8], __half *hi, __half *lo)
 {
-    uint32_t h[4], l[2] = {0, 0};
+    uint32_t h[4], l[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         h[q] = half_pair(v[2 * q], v[2 * q + 1]);
         const float2 f = half_unpair(h[q]);
-        l[q / 2] |= lo_code(v[2 * q] - f.x, v[2 * q + 1] - f.y) << (16 * (q & 1));
+        l[q] = half_pair((v[2 * q] - f.x) * kLoScale, (v[2 * q + 1] - f.y) * kLoScale);
     }
     *reinterpret_cast<uint4 *>(hi) = make_uint4(h[0], h[1], h[2], h[3]);
-    *reinterpret_cast<uint2 *>(lo) = make_uint2(l[0], l[1]);
+    *reinterpret_cast<uint4 *>(lo) = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-// X hi and lo [b][m][pitch] from g [b][M][N]: M and N multiples of 16.  WIDE:
+// X hi and lo [b][m][pitch] from g [b][M][N]: M and N multiples of 8.  WIDE:
 // the rows of X are those of g.  Else a block transposes 64 x 64 elements
 // through shared memory.
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(256) ortho_split8_kernel(const T *__restrict__ g, int M, int N,
                                                            const float *__restrict__ partial, int parts, float eps,
-                                                           __half *__restrict__ hi, uint8_t *__restrict__ lo)
+                                                           __half *__restrict__ hi, __half *__restrict__ lo)
 {
     const int b = blockIdx.z;
     const float f = input_factor(partial + b * kMaxParts, parts, eps);
@@ -878,7 +858,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) ortho_split_kernel(const T *__restrict__ g, int M, int N,
                                                           const float *__restrict__ partial, int parts, float eps,
                                                           bool tall, int64_t pitch, __half *__restrict__ hi,
-                                                          uint8_t *__restrict__ lo)
+                                                          __half *__restrict__ lo)
 {
     __shared__ float tile[32][33];
     const int b = blockIdx.z, tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
@@ -890,7 +870,7 @@ __global__ void __launch_bounds__(256) ortho_split_kernel(const T *__restrict__ 
     auto put = [&](int r, int c, float v) {
         const __half h = __float2half_rn(v);
         hi[base + r * pitch + c] = h;
-        lo[base + r * pitch + c] = (uint8_t)lo_code(v - __half2float(h), 0.0f);
+        lo[base + r * pitch + c] = __float2half_rn((v - __half2float(h)) * kLoScale);
     };
     for (int y = ty; y < 32; y += 8) {
         const int r = r0 + y, c = c0 + tx;
@@ -929,22 +909,20 @@ EncodeFn encoder()
     return fn;
 }
 
-// [batch][rows][cols] with `pitch` elements per row, FP16 or bytes, boxes of
-// 64 columns x box_rows rows, swizzled over the box's row (128 or 64 bytes)
-cudaError_t make_map(CUtensorMap *map, const void *base, bool bytes, int64_t batch, int64_t rows, int64_t cols,
-                     int64_t pitch, int box_rows)
+// [batch][rows][cols] FP16 with `pitch` elements per row, boxes of 64
+// columns (128 bytes, 128-byte swizzle) x box_rows rows
+cudaError_t make_map(CUtensorMap *map, const __half *base, int64_t batch, int64_t rows, int64_t cols, int64_t pitch,
+                     int box_rows)
 {
     EncodeFn enc = encoder();
     if (!enc) return cudaErrorNotSupported;
-    const int size = bytes ? 1 : 2;
     const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
-    const cuuint64_t strides[2] = {(cuuint64_t)pitch * size, (cuuint64_t)(pitch * rows) * size};
+    const cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)(pitch * rows) * 2};
     const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
-    const CUtensorMapSwizzle swizzle = bytes ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
-    CUresult r = enc(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
-                     const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half *>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -958,7 +936,7 @@ Region layout(int64_t B, int64_t M, int64_t N)
     Region L{};
     L.m = M < N ? M : N;
     L.n = M < N ? N : M;
-    L.x_pitch = round_up(L.n, 16);  // rows of hi and lo start on 16 bytes
+    L.x_pitch = round_up(L.n, 8);  // rows start on 16 bytes
     L.a_pitch = round_up(L.m, 8);
     size_t o = 0;
     auto take = [&](size_t bytes) {
@@ -971,7 +949,7 @@ Region layout(int64_t B, int64_t M, int64_t N)
     const size_t x = (size_t)(B * L.m * L.x_pitch) * 2, a = (size_t)(B * L.m * L.a_pitch) * 2;
     L.hi[0] = take(x);
     L.hi[1] = take(x);
-    L.lo = take(x / 2);
+    L.lo = take(x);
     L.a = take(a);
     L.bm = take(a);
     L.total = o;
@@ -986,7 +964,7 @@ cudaError_t run_steps(const OrthoCall &c, char *ws, const Region &L, int pairs, 
     OrthoMaps t;
     cudaError_t e = cudaSuccess;
     auto map = [&](CUtensorMap *m, const __half *p, int64_t cols, int64_t pitch, int box_rows) {
-        if (e == cudaSuccess) e = make_map(m, p, false, c.B, L.m, cols, pitch, box_rows);
+        if (e == cudaSuccess) e = make_map(m, p, c.B, L.m, cols, pitch, box_rows);
     };
     for (int i = 0; i < 2; ++i) {
         map(&t.x_left[i], hi[i], L.n, L.x_pitch, 128);
@@ -994,7 +972,7 @@ cudaError_t run_steps(const OrthoCall &c, char *ws, const Region &L, int pairs, 
         map(&t.x_cols[i], hi[i], L.n, L.x_pitch, 64);
         map(&t.x_blk[i], hi[i], L.n, L.x_pitch, 32);
     }
-    if (e == cudaSuccess) e = make_map(&t.lo_blk, ws + L.lo, true, c.B, L.m, L.n, L.x_pitch, 32);
+    map(&t.lo_blk, (const __half *)(ws + L.lo), L.n, L.x_pitch, 32);
     map(&t.a_left, A, L.m, L.a_pitch, 128);
     map(&t.a_right, A, L.m, L.a_pitch, BN / 2);
     map(&t.a_cols, A, L.m, L.a_pitch, 64);
@@ -1041,13 +1019,13 @@ cudaError_t run_steps(const OrthoCall &c, char *ws, const Region &L, int pairs, 
 }
 
 template <typename T>
-cudaError_t launch_input(const OrthoCall &c, const Region &L, float *partial, uint32_t *done, __half *hi, uint8_t *lo,
+cudaError_t launch_input(const OrthoCall &c, const Region &L, float *partial, uint32_t *done, __half *hi, __half *lo,
                          cudaStream_t s)
 {
     const int64_t count = c.M * c.N;
     const int64_t slices = ceil_div(count, 8192);
     const int parts = (int)(slices < kMaxParts ? slices : kMaxParts);
-    const bool tall = c.M > c.N, by16 = c.M % 16 == 0 && c.N % 16 == 0;
+    const bool tall = c.M > c.N, by8 = c.M % 8 == 0 && c.N % 8 == 0;
     const int64_t fit = kTurnBytes / (count * (int64_t)sizeof(T));
     const int64_t turn = fit < 1 ? 1 : fit < c.B ? fit : c.B;
     for (int64_t b = 0; b < c.B; b += turn) {
@@ -1057,11 +1035,11 @@ cudaError_t launch_input(const OrthoCall &c, const Region &L, float *partial, ui
         const int64_t at = b * L.m * L.x_pitch;
         ortho_norm_kernel<<<dim3(parts, n), 256, 0, s>>>(g, count, part, done + b);
         const int M = (int)c.M, N = (int)c.N;
-        if (by16 && !tall)
+        if (by8 && !tall)
             ortho_split8_kernel<T, true>
                 <<<dim3((unsigned)ceil_div(count, 8 * 256 * 4), 1, n), 256, 0, s>>>(g, M, N, part, parts, c.eps,
                                                                                     hi + at, lo + at);
-        else if (by16)
+        else if (by8)
             ortho_split8_kernel<T, false>
                 <<<dim3((unsigned)ceil_div(N, 64), (unsigned)ceil_div(M, 64), n), 256, 0, s>>>(g, M, N, part, parts,
                                                                                                c.eps, hi + at, lo + at);
@@ -1105,7 +1083,7 @@ cudaError_t launch_orthogonalize(const OrthoCall &c, void *workspace, int pairs,
     char *ws = (char *)workspace;
     auto *partial = (float *)(ws + L.partial);
     auto *hi = (__half *)(ws + L.hi[0]);
-    auto *lo = (uint8_t *)(ws + L.lo);
+    auto *lo = (__half *)(ws + L.lo);
     auto *done = (uint32_t *)(ws + L.done);
     const cudaError_t e = c.g_f32 ? launch_input<float>(c, L, partial, done, hi, lo, s)
                                   : launch_input<__nv_bfloat16>(c, L, partial, done, hi, lo, s);
