@@ -165,6 +165,12 @@ int moe_gate_backward(const float *logits_f32, const int32_t *topk_idx,
  * A slot whose index is outside [0, E), or that repeats the index of an
  * earlier slot of its token, is dropped: an expert that the token does not
  * use takes its place with weight 0.  So -1 marks an unused slot.
+ * Arithmetic with BF16 weights: FP32 sums (on the grouped path in segments of
+ * 256 products, added in order) and FP32 intermediates, which the tensor-core
+ * products take as three BF16 terms (24 bits): closer to the definition than
+ * moe_ffn_forward_ex's grouped path (two terms, one chain), not bit-identical
+ * to it.  The decode path, and the calls with MXFP8 weights, give
+ * moe_ffn_forward_ex's and moe_ffn_forward_mxfp8's bits for the same routing.
  */
 size_t moe_ffn_routed_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k);
 int moe_ffn_forward_routed(const void *x, const void *x_scale, const int32_t *topk_idx,
@@ -177,13 +183,15 @@ int moe_ffn_forward_routed(const void *x, const void *x_scale, const int32_t *to
 /*
  * Its gradients for BF16 x and weights: moe_ffn_backward's dx, dW_gate_up and
  * dW_down, and dtopk_w_f32 [T,k] = dL/dtopk_w (a dropped slot's is 0) in the
- * place of the logits' gradient.  workspace: at least
- * moe_ffn_backward_workspace_bytes, and required; the rules are
- * moe_ffn_backward's.  from_state != 0: the workspace is the state that
+ * place of the logits' gradient, with the same arithmetic as above.  workspace:
+ * at least moe_ffn_routed_backward_workspace_bytes, and required; the rules
+ * are moe_ffn_backward's.  from_state != 0: the workspace is the state that
  * moe_ffn_forward_routed_train left for the same x, routing, weights and
  * shape, and g and u are read from it instead of computed again (same bits).
  * T == 0 zeroes the two weight gradients.
  */
+size_t moe_ffn_routed_backward_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E,
+                                               int64_t k);
 int moe_ffn_backward_routed(const void *x_bf16, const int32_t *topk_idx,
                             const float *topk_w_f32, const void *w_gate_up_bf16,
                             const void *w_down_bf16, const float *dout_f32, int64_t T,
@@ -194,7 +202,7 @@ int moe_ffn_backward_routed(const void *x_bf16, const int32_t *topk_idx,
 
 /*
  * The forward pass that keeps g and u for it in `state` (at least
- * moe_ffn_train_state_bytes), as moe_ffn_forward_train does.
+ * moe_ffn_routed_backward_workspace_bytes), as moe_ffn_forward_train does.
  */
 int moe_ffn_forward_routed_train(const void *x_bf16, const int32_t *topk_idx,
                                  const float *topk_w_f32, const void *w_gate_up_bf16,

@@ -24,6 +24,12 @@
 //                   of the product)
 //       dW_gate_up: A = dgu_hi/lo [rows][2I], B = x_s [rows][H]
 //                   (hi.x + lo.x; x is exact in BF16)
+//     With three terms per operand (TRIPLE: the calls that take the routing
+//     from the caller) the products down to 2^-16 of the first are taken:
+//     hi.hi + hi.lo + lo.hi + hi.lo2 + lo.lo + lo2.hi, and hi.x + lo.x +
+//     lo2.x; 16 rows per K step and, for dW_down, 128 output columns make
+//     room for four stages.  Error against FP64 (512 tokens, 32 rows per
+//     expert): 4.5e-6 with two terms, %WGERR% with three.
 //     One item is one 128 x 256 output tile of one expert; K is the
 //     expert's rows in steps of 32 (the MMA's K steps of 16 stop at the
 //     16-row padding, whose rows are zero).  Both operands are MN-major:
@@ -72,9 +78,8 @@ cudaError_t read_bwd_fault_word(uint32_t *flags, bool clear)
 namespace {
 
 constexpr int WBM = 128;               // output rows per tile (MMA M)
-constexpr int WNB = 256;               // output columns per tile (MMA N)
-constexpr int WK = 32;                 // rows per K step (TMA box height)
-constexpr int BOX = 64 * WK * 2;       // one 64-element x 32-row BF16 box: 4 KB
+constexpr int kTileCols = 256;         // output columns per tile (MMA N)
+constexpr int kRowsPerStep = 32;       // rows per K step (TMA box height)
 constexpr int kWThreads = 320;         // producer, MMA issuer, 8 epilogue warps
 constexpr int kEpiWarps = 8;
 constexpr int OUT_BLOCK = 32 * 32 * 4;  // one staged 32 x 32 FP32 output block: 4 KB
@@ -83,15 +88,19 @@ constexpr uint64_t kDrainNs = 200000000ull;
 
 enum : int { kDwDown = 0, kDwGateUp = 1 };
 
-template <int KIND>
+template <int KIND, bool TRIPLE = false>
 struct WCfg {
-    static constexpr bool B_PAIR = KIND == kDwDown;      // B is a hi/lo pair (wa); else x_s
-    static constexpr int A_HALF = (WBM / 64) * BOX;      // 16 KB: the tile's rows of A_hi (or A_lo)
-    static constexpr int B_HALF = (WNB / 64) * BOX;      // 32 KB
-    static constexpr int A_BYTES = 2 * A_HALF;
-    static constexpr int B_BYTES = (B_PAIR ? 2 : 1) * B_HALF;
+    static constexpr bool B_PAIR = KIND == kDwDown;      // B is in terms (wa); else x_s
+    static constexpr int A_TERMS = TRIPLE ? 3 : 2, B_TERMS = B_PAIR ? A_TERMS : 1;
+    static constexpr int WK = TRIPLE ? 16 : kRowsPerStep;     // rows per K step
+    static constexpr int WNB = TRIPLE && B_PAIR ? 128 : kTileCols;
+    static constexpr int BOX = 64 * WK * 2;              // one 64-element x WK-row box
+    static constexpr int A_HALF = (WBM / 64) * BOX;      // the tile's rows of one term: 16 KB (TRIPLE: 4)
+    static constexpr int B_HALF = (WNB / 64) * BOX;      // 32 KB (TRIPLE: 4, x_s 8)
+    static constexpr int A_BYTES = A_TERMS * A_HALF;
+    static constexpr int B_BYTES = B_TERMS * B_HALF;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES = B_PAIR ? 4 : 5;
+    static constexpr int STAGES = TRIPLE ? 7 : B_PAIR ? 4 : 5;
     // one staged block per epilogue warp: the shared memory serves the
     // operand stages better (measured: two blocks per warp and one stage
     // fewer, 2.62 / 5.00 ms at T = 2048; one block, 2.53 / 4.92 ms)
@@ -109,14 +118,17 @@ struct WArgs {
 
 __device__ __forceinline__ void raise(uint32_t bit) { atomicOr(&g_bwd_fault_word, bit); }
 
-template <int KIND>
+template <int KIND, bool TRIPLE = false>
 __global__ void __launch_bounds__(kWThreads, 1)
     wgrad_kernel(const __grid_constant__ CUtensorMap tmAh, const __grid_constant__ CUtensorMap tmAl,
-                 const __grid_constant__ CUtensorMap tmBh, const __grid_constant__ CUtensorMap tmBl,
+                 const __grid_constant__ CUtensorMap tmAl2, const __grid_constant__ CUtensorMap tmBh,
+                 const __grid_constant__ CUtensorMap tmBl, const __grid_constant__ CUtensorMap tmBl2,
                  const __grid_constant__ CUtensorMap tmOut, const WArgs args)
 {
+    // tmAl2, tmBl2: the third terms (TRIPLE).
     // tmOut: the gradient [E][M][N] FP32, box 32 x 32 x 1, 128-byte swizzle
-    using C = WCfg<KIND>;
+    using C = WCfg<KIND, TRIPLE>;
+    constexpr int WK = C::WK, WNB = C::WNB, BOX = C::BOX;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *staging = smem + C::STAGES * C::STAGE_BYTES;
@@ -145,6 +157,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
         ptx::prefetch_tensormap(&tmAl);
         ptx::prefetch_tensormap(&tmBh);
         if (C::B_PAIR) ptx::prefetch_tensormap(&tmBl);
+        if (TRIPLE) ptx::prefetch_tensormap(&tmAl2);
+        if (TRIPLE && C::B_PAIR) ptx::prefetch_tensormap(&tmBl2);
         ptx::prefetch_tensormap(&tmOut);
     }
     if (warp == 1) {
@@ -194,11 +208,15 @@ __global__ void __launch_bounds__(kWThreads, 1)
                     for (int h = 0; h < WBM / 64; ++h) {
                         ptx::tma_load_2d(a + h * BOX, &tmAh, m0 + 64 * h, r, full + stage);
                         ptx::tma_load_2d(a + C::A_HALF + h * BOX, &tmAl, m0 + 64 * h, r, full + stage);
+                        if (TRIPLE)
+                            ptx::tma_load_2d(a + 2 * C::A_HALF + h * BOX, &tmAl2, m0 + 64 * h, r, full + stage);
                     }
 #pragma unroll
                     for (int h = 0; h < WNB / 64; ++h) {
                         ptx::tma_load_2d(b + h * BOX, &tmBh, n0 + 64 * h, r, full + stage);
                         if (C::B_PAIR) ptx::tma_load_2d(b + C::B_HALF + h * BOX, &tmBl, n0 + 64 * h, r, full + stage);
+                        if (TRIPLE && C::B_PAIR)
+                            ptx::tma_load_2d(b + 2 * C::B_HALF + h * BOX, &tmBl2, n0 + 64 * h, r, full + stage);
                     }
                     if (++stage == C::STAGES) {
                         stage = 0;
@@ -254,6 +272,16 @@ __global__ void __launch_bounds__(kWThreads, 1)
                             ptx::mma_bf16(d, ah, bl, idesc, 1);
                         }
                         ptx::mma_bf16(d, al, bh, idesc, 1);
+                        if (TRIPLE) {
+                            const uint64_t al2 = ptx::sw128_desc_mn(a_addr + 2 * C::A_HALF + k * 2048, BOX);
+                            if (C::B_PAIR) {
+                                const uint64_t bl = ptx::sw128_desc_mn(b_addr + C::B_HALF + k * 2048, BOX);
+                                const uint64_t bl2 = ptx::sw128_desc_mn(b_addr + 2 * C::B_HALF + k * 2048, BOX);
+                                ptx::mma_bf16(d, ah, bl2, idesc, 1);
+                                ptx::mma_bf16(d, al, bl, idesc, 1);
+                            }
+                            ptx::mma_bf16(d, al2, bh, idesc, 1);
+                        }
                     }
                     ptx::mma_commit(empty + stage);
                     if (++stage == C::STAGES) {
@@ -336,7 +364,8 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint16_t *__restric
                                                        const int32_t *__restrict__ perm,
                                                        const int32_t *__restrict__ offs, int E, int H, int k,
                                                        uint16_t *__restrict__ xs, __nv_bfloat16 *__restrict__ ds_hi,
-                                                       __nv_bfloat16 *__restrict__ ds_lo, float *__restrict__ w_s)
+                                                       __nv_bfloat16 *__restrict__ ds_lo,
+                                                       __nv_bfloat16 *__restrict__ ds_lo2, float *__restrict__ w_s)
 {
     const int n_rows = __ldg(offs + E);
     for (int r = blockIdx.x; r < n_rows; r += gridDim.x) {
@@ -355,14 +384,17 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint16_t *__restric
                 d[4] = d1.x, d[5] = d1.y, d[6] = d1.z, d[7] = d1.w;
             }
             reinterpret_cast<uint4 *>(xs + (int64_t)r * H)[c] = xv;
-            __align__(16) __nv_bfloat16 hi[8], lo[8];
+            __align__(16) __nv_bfloat16 hi[8], lo[8], lo2[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 hi[j] = __float2bfloat16_rn(d[j]);
-                lo[j] = __float2bfloat16_rn(d[j] - __bfloat162float(hi[j]));
+                const float r1 = d[j] - __bfloat162float(hi[j]);
+                lo[j] = __float2bfloat16_rn(r1);
+                lo2[j] = __float2bfloat16_rn(r1 - __bfloat162float(lo[j]));
             }
             reinterpret_cast<uint4 *>(ds_hi + (int64_t)r * H)[c] = *reinterpret_cast<const uint4 *>(hi);
             reinterpret_cast<uint4 *>(ds_lo + (int64_t)r * H)[c] = *reinterpret_cast<const uint4 *>(lo);
+            if (ds_lo2) reinterpret_cast<uint4 *>(ds_lo2 + (int64_t)r * H)[c] = *reinterpret_cast<const uint4 *>(lo2);
         }
     }
 }
@@ -389,10 +421,16 @@ __global__ void __launch_bounds__(256) zero_untouched_kernel(const int32_t *__re
         }
         for (; i < n; i += stride) p[i] = z;
     };
-    for (int e = 0; e < E; ++e) {
-        if (__ldg(counts + e) != 0) continue;
-        fill(dwgu + (int64_t)e * gu4, gu4);
-        fill(dwd + (int64_t)e * d4, d4);
+    // 32 experts' counts at a time: one load after the other took 24 us for
+    // 128 experts with nothing to fill
+    const int lane = threadIdx.x & 31;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+        unsigned none = __ballot_sync(0xffffffffu, e0 + lane < E && __ldg(counts + min(e0 + lane, E - 1)) == 0);
+        for (; none; none &= none - 1) {
+            const int e = e0 + __ffs(none) - 1;
+            fill(dwgu + (int64_t)e * gu4, gu4);
+            fill(dwd + (int64_t)e * d4, d4);
+        }
     }
 }
 
@@ -441,10 +479,11 @@ __global__ void __launch_bounds__(256) routed_dw_kernel(const float *__restrict_
     dw[a] = v;
 }
 
-template <int KIND>
+template <int KIND, bool TRIPLE>
 cudaError_t set_wgrad_smem()
 {
-    return cudaFuncSetAttribute(wgrad_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, WCfg<KIND>::SMEM);
+    return cudaFuncSetAttribute(wgrad_kernel<KIND, TRIPLE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                WCfg<KIND, TRIPLE>::SMEM);
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -465,14 +504,14 @@ EncodeTiledFn wencoder()
     return fn;
 }
 
-// [rows][cols] BF16, box 64 columns (128 bytes, 128-byte swizzle) x 64 rows
-cudaError_t make_rows_map(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols)
+// [rows][cols] BF16, box 64 columns (128 bytes, 128-byte swizzle) x wk rows
+cudaError_t make_rows_map(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, int wk)
 {
     EncodeTiledFn enc = wencoder();
     if (!enc) return cudaErrorNotSupported;
     const cuuint64_t dims[2] = {cols, rows};
     const cuuint64_t strides[1] = {cols * 2};
-    const cuuint32_t box[2] = {64, WK};
+    const cuuint32_t box[2] = {64, (cuuint32_t)wk};
     const cuuint32_t estr[2] = {1, 1};
     CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -496,21 +535,25 @@ cudaError_t make_out_map(CUtensorMap *map, float *base, uint64_t E, uint64_t M, 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int KIND>
-cudaError_t launch_wgrad(const void *ah, const void *al, const void *bh, const void *bl, const int32_t *offs,
+// a, b: the operands' terms hi, lo, lo2 (lo2, and b's lo, may be null)
+template <int KIND, bool TRIPLE>
+cudaError_t launch_wgrad(const void *const (&a)[3], const void *const (&b)[3], const int32_t *offs,
                          const int32_t *counts, int n_rows, int M, int N, int E, float *out, int ctas, cudaStream_t s)
 {
-    CUtensorMap tAh, tAl, tBh, tBl, tOut;
-    cudaError_t e = make_rows_map(&tAh, ah, n_rows, M);
-    if (e == cudaSuccess) e = make_rows_map(&tAl, al, n_rows, M);
-    if (e == cudaSuccess) e = make_rows_map(&tBh, bh, n_rows, N);
-    if (e == cudaSuccess) e = make_rows_map(&tBl, bl ? bl : bh, n_rows, N);
+    using C = WCfg<KIND, TRIPLE>;
+    CUtensorMap tA[3], tB[3], tOut;
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < 3 && e == cudaSuccess; ++i) {
+        e = make_rows_map(&tA[i], a[i] ? a[i] : a[0], n_rows, M, C::WK);
+        if (e == cudaSuccess) e = make_rows_map(&tB[i], b[i] ? b[i] : b[0], n_rows, N, C::WK);
+    }
     if (e == cudaSuccess) e = make_out_map(&tOut, out, E, M, N);
     if (e != cudaSuccess) return e;
-    const WArgs a{offs, counts, M, N, E, (M + WBM - 1) / WBM, (N + WNB - 1) / WNB};
-    const int64_t items = (int64_t)E * a.m_tiles * a.n_tiles;
+    const WArgs args{offs, counts, M, N, E, (M + WBM - 1) / WBM, (N + C::WNB - 1) / C::WNB};
+    const int64_t items = (int64_t)E * args.m_tiles * args.n_tiles;
     const int grid = (int)(items < ctas ? items : ctas);
-    wgrad_kernel<KIND><<<grid, kWThreads, WCfg<KIND>::SMEM, s>>>(tAh, tAl, tBh, tBl, tOut, a);
+    wgrad_kernel<KIND, TRIPLE>
+        <<<grid, kWThreads, C::SMEM, s>>>(tA[0], tA[1], tA[2], tB[0], tB[1], tB[2], tOut, args);
     return cudaPeekAtLastError();
 }
 
@@ -518,33 +561,38 @@ cudaError_t launch_wgrad(const void *ah, const void *al, const void *bh, const v
 
 cudaError_t bwd_init_device()
 {
-    cudaError_t e = set_wgrad_smem<kDwDown>();
-    if (e == cudaSuccess) e = set_wgrad_smem<kDwGateUp>();
+    cudaError_t e = set_wgrad_smem<kDwDown, false>();
+    if (e == cudaSuccess) e = set_wgrad_smem<kDwGateUp, false>();
+    if (e == cudaSuccess) e = set_wgrad_smem<kDwDown, true>();
+    if (e == cudaSuccess) e = set_wgrad_smem<kDwGateUp, true>();
     return e;
 }
 
 cudaError_t launch_bwd_prep(const void *x, const float *dout, const float *w, const int32_t *perm,
                             const int32_t *offs, int n_rows_max, int E, int H, int k, void *xs, void *ds_hi,
-                            void *ds_lo, float *w_s, int n_sm, cudaStream_t s)
+                            void *ds_lo, float *w_s, int n_sm, cudaStream_t s, void *ds_lo2)
 {
     const int grid = n_rows_max < 8 * n_sm ? (n_rows_max > 0 ? n_rows_max : 1) : 8 * n_sm;
     bwd_prep_kernel<<<grid, 256, 0, s>>>((const uint16_t *)x, dout, w, perm, offs, E, H, k, (uint16_t *)xs,
-                                         (__nv_bfloat16 *)ds_hi, (__nv_bfloat16 *)ds_lo, w_s);
+                                         (__nv_bfloat16 *)ds_hi, (__nv_bfloat16 *)ds_lo, (__nv_bfloat16 *)ds_lo2,
+                                         w_s);
     return cudaPeekAtLastError();
 }
 
 cudaError_t launch_wgrad_down(const void *ds_hi, const void *ds_lo, const void *wa_hi, const void *wa_lo,
                               const int32_t *offs, const int32_t *counts, int n_rows, int H, int I, int E,
-                              float *dwd, int ctas, cudaStream_t s)
+                              float *dwd, int ctas, cudaStream_t s, const void *ds_lo2, const void *wa_lo2)
 {
-    return launch_wgrad<kDwDown>(ds_hi, ds_lo, wa_hi, wa_lo, offs, counts, n_rows, H, I, E, dwd, ctas, s);
+    auto f = ds_lo2 ? launch_wgrad<kDwDown, true> : launch_wgrad<kDwDown, false>;
+    return f({ds_hi, ds_lo, ds_lo2}, {wa_hi, wa_lo, wa_lo2}, offs, counts, n_rows, H, I, E, dwd, ctas, s);
 }
 
 cudaError_t launch_wgrad_gate_up(const void *dgu_hi, const void *dgu_lo, const void *xs, const int32_t *offs,
                                  const int32_t *counts, int n_rows, int H, int I, int E, float *dwgu, int ctas,
-                                 cudaStream_t s)
+                                 cudaStream_t s, const void *dgu_lo2)
 {
-    return launch_wgrad<kDwGateUp>(dgu_hi, dgu_lo, xs, nullptr, offs, counts, n_rows, 2 * I, H, E, dwgu, ctas, s);
+    auto f = dgu_lo2 ? launch_wgrad<kDwGateUp, true> : launch_wgrad<kDwGateUp, false>;
+    return f({dgu_hi, dgu_lo, dgu_lo2}, {xs, nullptr, nullptr}, offs, counts, n_rows, 2 * I, H, E, dwgu, ctas, s);
 }
 
 cudaError_t launch_zero_untouched(const int32_t *counts, int E, int H, int I, float *dwgu, float *dwd, int n_sm,

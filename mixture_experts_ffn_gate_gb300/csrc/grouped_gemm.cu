@@ -35,16 +35,19 @@
 // Every output element is one MMA chain over K in a fixed order, so results
 // do not depend on the grid size or on which CTA ran which tile.
 //
-// The calls that take the routing from the caller run instances that cut K
-// into segments of kSegSteps stages (SEG): the MMAs of a segment start a new
-// accumulator, and the epilogue adds the segments in FP32 registers, in
-// order.  The tensor cores' own additions round toward zero, which shrinks a
-// chain of K / 16 of them by about 1.2e-8 K / 16 of its value: measured
-// against FP64 at H = 4096, I = 1536, 1.1e-5 with one chain and %SEGERR% with
-// segments of 256.  The drains are small beside the weight stream that bounds
-// these kernels, so the segments cost %SEGCOST%.  An epilogue warp keeps the
-// sums of one 32-row x 64-column block, so SEG has four epilogue warps per
-// weight tile, and gate_up two tiles per item instead of four (five stages).
+// The calls that take the routing from the caller run instances with two
+// differences (SEG):
+//   - K is cut into segments of kSegSteps stages: the MMAs of a segment start
+//     a new accumulator, and the epilogue adds the segments in FP32 registers,
+//     in order.  The tensor cores' own additions round toward zero, which
+//     shrinks a chain of K / 16 of them with its length.
+//   - an FP32 operand is three BF16 terms hi + lo + lo2 (24 bits), not two.
+// Measured against FP64 at H = 4096, I = 1536: 1.1e-5 with one chain and two
+// terms, 2.6e-6 with segments of 256 and two, %SEGERR% with both.  The drains
+// and the third term are small beside the weight stream that bounds these
+// kernels (733 us with segments, %SEGTIME% with both, 64 tokens).  An epilogue
+// warp keeps the sums of one 32-row x 64-column block, so SEG has four
+// epilogue warps per weight tile, and two tiles per item.
 //
 // One persistent CTA per SM: warp 0 issues TMA loads into a ring of smem
 // stages, warp 1 issues tcgen05.mma into one of two TMEM accumulators,
@@ -121,10 +124,10 @@ struct Cfg {
     // per element, so two warps share each TMEM lane quarter (one 32-column
     // block each) to drain its single accumulator set sooner
     // (SEG: a warp per lane quarter of each weight tile)
-    static constexpr int MT_SEG = GATE_UP || KIND == kBwdQ ? 2 : 3;
+    static constexpr int MT_SEG = 2;
     static constexpr int EPI_WARPS = SEG ? 4 * MT_SEG : KIND == kBwdQ ? 8 : 4;
     static constexpr int CONV_WARPS = MX ? 8 : 0;
-    static constexpr int STAGES = KIND == kBwdQ ? 4 : SEG && GATE_UP ? 5 : 3;
+    static constexpr int STAGES = SEG ? (GATE_UP ? 5 : 4) : KIND == kBwdQ ? 4 : 3;
     static constexpr int FIRST_LOADER = 2 + EPI_WARPS;                          // gate_up: the x-row loaders,
     static constexpr int FIRST_CONV = FIRST_LOADER + (GATE_UP ? STAGES : 0);  // one per stage
     static_assert(!(SEG && MX), "the segments are built for BF16 weights only");
@@ -135,11 +138,13 @@ struct Cfg {
     // (MX: two, so that the code tiles fit beside three stages)
     static constexpr int MT = SEG ? MT_SEG : MX ? 2 : GATE_UP ? 4 : KIND == kBwdQ ? 2 : 3;
     // accumulator columns per weight tile: the chunk's tokens (gate_up), or
-    // its hi rows then its lo rows (down, q, dx); gate_up and q double-buffer
-    // them so the epilogue of one item overlaps the MMAs of the next, down
-    // and dx (three tiles of 128 columns) have room for one set
-    static constexpr int TILE_COLS = GATE_UP ? ACC_COLS : 2 * ACC_COLS;
-    static constexpr int ACC_BUFS = GATE_UP || KIND == kBwdQ || MX ? 2 : 1;
+    // its rows' TERMS parts one after the other (down, q, dx); gate_up and q
+    // double-buffer them so the epilogue of one item overlaps the MMAs of the
+    // next, down and dx (three tiles of 128 columns) have room for one set, as
+    // have the three terms of SEG (whose sums leave TMEM after each segment)
+    static constexpr int TERMS = GATE_UP ? 1 : SEG ? 3 : 2;
+    static constexpr int TILE_COLS = TERMS * ACC_COLS;
+    static constexpr int ACC_BUFS = GATE_UP || MX || (KIND == kBwdQ && !SEG) ? 2 : 1;
     static constexpr int TMEM_COLS = ACC_BUFS * MT * TILE_COLS;
     // tcgen05.alloc takes a power of two of at least 32 columns
     static constexpr int TMEM_ALLOC = TMEM_COLS <= 32    ? 32
@@ -151,7 +156,7 @@ struct Cfg {
     static constexpr int A_TILE = BM * BK * 2;                            // 16 KB per weight tile
     static constexpr int A_BYTES = MT * A_TILE;
     static constexpr int B_TILE = NMAX * BK * 2;                          // 8 KB per operand
-    static constexpr int B_BYTES = B_TILE * (GATE_UP ? 1 : 2);            // x | act_hi + act_lo
+    static constexpr int B_BYTES = B_TILE * TERMS;                        // x | act_hi + act_lo (+ act_lo2)
     static constexpr int CODE_TILE = BM * BK;                             // 8 KB of E4M3 codes per tile
     static constexpr int CODE_BYTES = MX ? MT * CODE_TILE : 0;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + CODE_BYTES;
@@ -170,6 +175,7 @@ struct BwdQArgs {
     const float *g, *u, *w_s;
     __nv_bfloat16 *dgu_hi, *dgu_lo, *wa_hi, *wa_lo;
     float *dwp;
+    __nv_bfloat16 *dgu_lo2, *wa_lo2;  // SEG
 };
 
 struct GemmArgs {
@@ -189,6 +195,7 @@ struct GemmArgs {
     const uint8_t *scales;  // MX: the E8M0 scales [E][rows][scale_row] of the weight
     int scale_row;          // bytes per scale row (K / 32 padded to 16)
     float *g_keep, *u_keep; // kGateUpSave: g and u [rows][I] FP32 besides act
+    __nv_bfloat16 *act_lo2; // SEG: act's third term
 };
 
 struct Item {
@@ -219,6 +226,18 @@ __device__ __forceinline__ void store_pair(__nv_bfloat16 *hi, __nv_bfloat16 *lo,
     lo[at] = __float2bfloat16_rn(v - __bfloat162float(h));
 }
 
+// Three BF16 terms of an FP32 value.
+__device__ __forceinline__ void store_terms(__nv_bfloat16 *hi, __nv_bfloat16 *lo, __nv_bfloat16 *lo2, int64_t at,
+                                            float v)
+{
+    const __nv_bfloat16 h = __float2bfloat16_rn(v);
+    const float r = v - __bfloat162float(h);
+    const __nv_bfloat16 l = __float2bfloat16_rn(r);
+    hi[at] = h;
+    lo[at] = l;
+    lo2[at] = __float2bfloat16_rn(r - __bfloat162float(l));
+}
+
 // After this, lane l holds the sum over the warp's 32 lanes of v[l] (a
 // 32 x 32 transpose-and-add in 31 shuffles, in a fixed order): each round
 // a lane keeps one half of its remaining columns and adds its partner's
@@ -242,9 +261,10 @@ __device__ __forceinline__ float warp_column_sums(float (&v)[32], int lane)
 // j) of neuron i, whose q = W_down[e]^T dout_t values are r[j]:
 //   s = sigmoid(g), a = g s u, da = w q,
 //   dg = da u s (1 + g (1 - s)), du = da g s,
-// stored as BF16 pairs (dgu rows: dg at i, du at I + i; wa = w a), zeros in
+// stored as BF16 pairs (SEG: three terms; dgu rows: dg at i, du at I + i; wa = w a), zeros in
 // the expert's pad rows; and act . q summed over the warp's 32 neurons
 // into dwp[row][grp].
+template <bool SEG>
 __device__ __forceinline__ void bwd_q_columns(const uint32_t (&r)[32], int ncols, int p0, int n, int c0, int i,
                                               int grp, const GemmArgs &args, int lane)
 {
@@ -287,9 +307,15 @@ __device__ __forceinline__ void bwd_q_columns(const uint32_t (&r)[32], int ncols
                     wa = w * a;
                     prod[j] = a * qv;
                 }
-                store_pair(b.dgu_hi, b.dgu_lo, row * 2 * I + i, dg);
-                store_pair(b.dgu_hi, b.dgu_lo, row * 2 * I + I + i, du);
-                store_pair(b.wa_hi, b.wa_lo, row * I + i, wa);
+                if constexpr (SEG) {
+                    store_terms(b.dgu_hi, b.dgu_lo, b.dgu_lo2, row * 2 * I + i, dg);
+                    store_terms(b.dgu_hi, b.dgu_lo, b.dgu_lo2, row * 2 * I + I + i, du);
+                    store_terms(b.wa_hi, b.wa_lo, b.wa_lo2, row * I + i, wa);
+                } else {
+                    store_pair(b.dgu_hi, b.dgu_lo, row * 2 * I + i, dg);
+                    store_pair(b.dgu_hi, b.dgu_lo, row * 2 * I + I + i, du);
+                    store_pair(b.wa_hi, b.wa_lo, row * I + i, wa);
+                }
             }
         }
     }
@@ -301,7 +327,8 @@ template <int KIND, bool SEG = false>
 __global__ void __launch_bounds__(Cfg<KIND, SEG>::THREADS, 1)
     grouped_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0s,
                         const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1s,
-                        const __grid_constant__ CUtensorMap tmB1, const GemmArgs args)
+                        const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmB2s,
+                        const __grid_constant__ CUtensorMap tmB2, const GemmArgs args)
 {
     // tmA: gate_up -- 5-D view of W_gu [E][2][I/16][16][H] (dims innermost
     //      first: H, 16 rows, gate|up, row group, expert) whose {64,16,2,4,1}
@@ -313,7 +340,7 @@ __global__ void __launch_bounds__(Cfg<KIND, SEG>::THREADS, 1)
     //      two boxes (dims h0.., h0+64..) per tile and K step.
     // tmB0/tmB1 (down, q, dx): the chunk's hi/lo rows (act, dout or dgu),
     // box 64 x NMAX; tmB0s/tmB1s: the same with a 16-row box, for chunks of
-    // <= 16 rows.  gate_up leaves the B maps unread.
+    // <= 16 rows; tmB2/tmB2s: SEG's third term.  gate_up leaves the B maps unread.
     // MX (gate_up, down): tmA is the same view of the E4M3 codes (uint8,
     // no swizzle: 64-byte rows), its box a tile's codes.
     using C = Cfg<KIND, SEG>;
@@ -384,7 +411,7 @@ __global__ void __launch_bounds__(Cfg<KIND, SEG>::THREADS, 1)
                 if (i + (int)gridDim.x < total) nxt = decode_item(i + gridDim.x, args);  // loads overlap this item
                 const bool small = it.n <= SMALL_ROWS;
                 // gate_up: the weight box only (the x rows come from the loader warps)
-                const uint32_t bytes = args.a_bytes + (GATE_UP ? 0 : (small ? SMALL_ROWS : NMAX) * BK * 2 * 2);
+                const uint32_t bytes = args.a_bytes + (GATE_UP ? 0 : (small ? SMALL_ROWS : NMAX) * BK * 2 * C::TERMS);
                 uint64_t *const land = MX ? cfull : full;  // where the TMA copies complete
                 for (int kb = 0; kb < KB; ++kb) {
                     if (!ptx::mbar_wait_bounded(empty + stage, phase ^ 1, abort_flag, kWaitLimitNs)) {
@@ -443,6 +470,9 @@ __global__ void __launch_bounds__(Cfg<KIND, SEG>::THREADS, 1)
                         ptx::tma_load_2d(b, small ? &tmB0s : &tmB0, k0, it.p0, land + stage);
                         ptx::tma_load_2d(b + (small ? SMALL_ROWS : NMAX) * BK * 2, small ? &tmB1s : &tmB1, k0, it.p0,
                                          land + stage);
+                        if (SEG)
+                            ptx::tma_load_2d(b + 2 * (small ? SMALL_ROWS : NMAX) * BK * 2, small ? &tmB2s : &tmB2, k0,
+                                             it.p0, land + stage);
                     }
                     if (++stage == C::STAGES) {
                         stage = 0;
@@ -467,10 +497,10 @@ __global__ void __launch_bounds__(Cfg<KIND, SEG>::THREADS, 1)
             for (int i = blockIdx.x; i < total && !*abort_flag; i += gridDim.x) {
                 const Item it = nxt;
                 if (i + (int)gridDim.x < total) nxt = decode_item(i + gridDim.x, args);
-                // down: N spans the hi box and the lo rows that matter
+                // down: N spans the first terms' boxes and the last one's rows that matter
                 const int box = it.n <= SMALL_ROWS ? SMALL_ROWS : NMAX;
                 const uint32_t idesc =
-                    ptx::idesc_bf16_f32_mn(BM, GATE_UP ? pad16(it.n) : box + pad16(it.n), A_MN, false);
+                    ptx::idesc_bf16_f32_mn(BM, (C::TERMS - 1) * box + pad16(it.n), A_MN, false);
                 int acc = 0;
                 uint32_t d = 0;
                 bool ok = true;
@@ -681,7 +711,7 @@ __global__ void __launch_bounds__(Cfg<KIND, SEG>::THREADS, 1)
                                 for (int j = 0; j < 32; ++j)
                                     if (c0 + j < it.n) dst[(int64_t)(it.p0 + c0 + j) * args.I + neuron] = __uint_as_float(r[j]);
                             } else if constexpr (KIND == kBwdQ) {
-                                bwd_q_columns(r, it.n > SMALL_ROWS ? 32 : SMALL_ROWS, it.p0, it.n, c0, tile * BM + 32 * q + lane,
+                                bwd_q_columns<SEG>(r, it.n > SMALL_ROWS ? 32 : SMALL_ROWS, it.p0, it.n, c0, tile * BM + 32 * q + lane,
                                               tile * 4 + q, args, lane);
                             } else if constexpr (KIND == kGateUp || KIND == kGateUpMx || KIND == kGateUpSave) {
                                 const int neuron = tile * 64 + 16 * q + (lane & 15);
@@ -698,6 +728,9 @@ __global__ void __launch_bounds__(Cfg<KIND, SEG>::THREADS, 1)
                                         const int64_t at = (int64_t)(it.p0 + c0 + j) * args.I + neuron;
                                         dst[at] = lane < 16 ? hi : lo;
                                         if constexpr (KIND == kGateUpSave) keep[at] = v;
+                                        if constexpr (SEG)
+                                            if (lane < 16)
+                                                args.act_lo2[at] = __float2bfloat16_rn((a - __bfloat162float(hi)) - __bfloat162float(lo));
                                     }
                                 }
                             } else {
@@ -747,11 +780,17 @@ __global__ void __launch_bounds__(Cfg<KIND, SEG>::THREADS, 1)
                     if (!ok) break;
                     if (mine) {
                         const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (acc * MT + t) * C::TILE_COLS;
-                        add(sum[0], tbase);
-                        if (it.n > 32) add(sum[1], tbase + 32);
-                        if (!GATE_UP && it.n > SMALL_ROWS) {  // the lo rows' columns
-                            add(sum[0], tbase + NMAX);
-                            if (it.n > 32) add(sum[1], tbase + NMAX + 32);
+                        if (GATE_UP || it.n > SMALL_ROWS) {
+                            // the terms' columns, NMAX apart
+#pragma unroll
+                            for (int p = 0; p < C::TERMS; ++p) {
+                                add(sum[0], tbase + p * NMAX);
+                                if (it.n > 32) add(sum[1], tbase + p * NMAX + 32);
+                            }
+                        } else {
+                            // 16 columns apart: two terms, then the third
+                            add(sum[0], tbase);
+                            add(sum[1], tbase + 32);
                         }
                     }
                     ptx::tc_fence_before();
@@ -760,11 +799,12 @@ __global__ void __launch_bounds__(Cfg<KIND, SEG>::THREADS, 1)
                 }
                 if (!ok) break;
                 if (!mine) continue;
-                if (!GATE_UP && it.n <= SMALL_ROWS) {  // lo from column 16
+                if (!GATE_UP && it.n <= SMALL_ROWS) {
 #pragma unroll
                     for (int j = 0; j < SMALL_ROWS; ++j)
-                        sum[0][j] =
-                            __float_as_uint(__uint_as_float(sum[0][j]) + __uint_as_float(sum[0][SMALL_ROWS + j]));
+                        sum[0][j] = __float_as_uint(
+                            __uint_as_float(sum[0][j]) +
+                            (__uint_as_float(sum[0][SMALL_ROWS + j]) + __uint_as_float(sum[1][j])));
                 }
                 emit(sum[0], it, tile, 0);
                 if (it.n > 32) emit(sum[1], it, tile, 32);
@@ -967,7 +1007,7 @@ namespace {
 template <int KIND, bool SEG>
 cudaError_t gate_up_like(const void *x, const int32_t *perm, int k, const void *wgu, const int4 *chunks,
                          const int32_t *nchunks, const int32_t *offs, int n_assign, int H, int I, int E, void *out0,
-                         void *out1, int ctas, cudaStream_t s, float *g_keep = nullptr, float *u_keep = nullptr)
+                         void *out1, int ctas, cudaStream_t s, float *g_keep, float *u_keep, void *act_lo2)
 {
     CUtensorMap tA;
     constexpr int MT = Cfg<KIND, SEG>::MT;
@@ -979,20 +1019,25 @@ cudaError_t gate_up_like(const void *x, const int32_t *perm, int k, const void *
                out1, (const uint16_t *)x, perm, k};
     a.g_keep = g_keep;
     a.u_keep = u_keep;
+    a.act_lo2 = (__nv_bfloat16 *)act_lo2;
     // the token rows come from x through the loader warps: the B maps are not read
     grouped_gemm_kernel<KIND, SEG>
-        <<<grid_for(ctas, n_assign, a.m_tiles, E), Cfg<KIND, SEG>::THREADS, Cfg<KIND, SEG>::SMEM, s>>>(tA, tA, tA, tA,
-                                                                                                     tA, a);
+        <<<grid_for(ctas, n_assign, a.m_tiles, E), Cfg<KIND, SEG>::THREADS, Cfg<KIND, SEG>::SMEM, s>>>(tA, tA, tA, tA, tA,
+                                                                                                     tA, tA, a);
     return cudaPeekAtLastError();
 }
 
-// The B maps of a hi/lo operand pair [rows][cols]: NMAX- and 16-row boxes.
-cudaError_t make_pair_maps(CUtensorMap (&m)[4], const void *hi, const void *lo, uint64_t rows, uint64_t cols)
+// The B maps of an operand's terms [rows][cols]: 16- and NMAX-row boxes of
+// hi, lo and (nullable) lo2.
+cudaError_t make_term_maps(CUtensorMap (&m)[6], const void *hi, const void *lo, const void *lo2, uint64_t rows,
+                           uint64_t cols)
 {
-    cudaError_t e = make_map(&m[0], hi, rows, cols, SMALL_ROWS);
-    if (e == cudaSuccess) e = make_map(&m[1], hi, rows, cols, NMAX);
-    if (e == cudaSuccess) e = make_map(&m[2], lo, rows, cols, SMALL_ROWS);
-    if (e == cudaSuccess) e = make_map(&m[3], lo, rows, cols, NMAX);
+    const void *term[3] = {hi, lo, lo2 ? lo2 : lo};
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < 3 && e == cudaSuccess; ++i) {
+        e = make_map(&m[2 * i], term[i], rows, cols, SMALL_ROWS);
+        if (e == cudaSuccess) e = make_map(&m[2 * i + 1], term[i], rows, cols, NMAX);
+    }
     return e;
 }
 
@@ -1012,9 +1057,9 @@ cudaError_t make_mn_map(CUtensorMap *map, const void *base, uint64_t d0, uint64_
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// q and dx: M (the weight side) of size m_size in tiles of 128, K = k_size.
+// down, q and dx: M (the weight side) of size m_size in tiles of 128, K = k_size.
 template <int KIND, bool SEG>
-cudaError_t launch_mn(const CUtensorMap &tA, const CUtensorMap (&tB)[4], const int4 *chunks, const int32_t *nchunks,
+cudaError_t launch_mn(const CUtensorMap &tA, const CUtensorMap (&tB)[6], const int4 *chunks, const int32_t *nchunks,
                       const int32_t *offs, int n_rows, int H, int I, int E, int m_size, int k_size, void *out0,
                       const BwdQArgs &q, int ctas, cudaStream_t s)
 {
@@ -1024,7 +1069,7 @@ cudaError_t launch_mn(const CUtensorMap &tA, const CUtensorMap (&tB)[4], const i
                nullptr, nullptr, 0, q};
     grouped_gemm_kernel<KIND, SEG>
         <<<grid_for(ctas, n_rows, a.m_tiles, E), Cfg<KIND, SEG>::THREADS, Cfg<KIND, SEG>::SMEM, s>>>(
-            tA, tB[0], tB[1], tB[2], tB[3], a);
+            tA, tB[0], tB[1], tB[2], tB[3], tB[4], tB[5], a);
     return cudaPeekAtLastError();
 }
 
@@ -1032,10 +1077,11 @@ cudaError_t launch_mn(const CUtensorMap &tA, const CUtensorMap (&tB)[4], const i
 
 cudaError_t launch_gemm_gate_up(const void *x, const int32_t *perm, int k, const void *wgu, const int4 *chunks,
                                 const int32_t *nchunks, const int32_t *offs, int n_assign, int H, int I, int E,
-                                void *act_hi, void *act_lo, int ctas, cudaStream_t s, bool seg)
+                                void *act_hi, void *act_lo, int ctas, cudaStream_t s, void *act_lo2)
 {
-    auto f = seg ? gate_up_like<kGateUp, true> : gate_up_like<kGateUp, false>;
-    return f(x, perm, k, wgu, chunks, nchunks, offs, n_assign, H, I, E, act_hi, act_lo, ctas, s, nullptr, nullptr);
+    auto f = act_lo2 ? gate_up_like<kGateUp, true> : gate_up_like<kGateUp, false>;
+    return f(x, perm, k, wgu, chunks, nchunks, offs, n_assign, H, I, E, act_hi, act_lo, ctas, s, nullptr, nullptr,
+             act_lo2);
 }
 
 cudaError_t launch_gemm_gate_up_mx(const void *x, const int32_t *perm, int k, const void *gq, const void *gs,
@@ -1050,7 +1096,7 @@ cudaError_t launch_gemm_gate_up_mx(const void *x, const int32_t *perm, int k, co
     GemmArgs a{chunks, nchunks, offs, H, I, H, (I / 64 + MT - 1) / MT, I / 64, (int)groups * 32 * BK, act_hi, act_lo,
                (const uint16_t *)x, perm, k, BwdQArgs{}, (const uint8_t *)gs, mx_scale_bytes(H)};
     grouped_gemm_kernel<kGateUpMx><<<grid_for(ctas, n_assign, a.m_tiles, E), Cfg<kGateUpMx>::THREADS,
-                                     Cfg<kGateUpMx>::SMEM, s>>>(tA, tA, tA, tA, tA, a);
+                                     Cfg<kGateUpMx>::SMEM, s>>>(tA, tA, tA, tA, tA, tA, tA, a);
     return cudaPeekAtLastError();
 }
 
@@ -1058,16 +1104,16 @@ cudaError_t launch_gemm_down_mx(const void *act_hi, const void *act_lo, const vo
                                 const int4 *chunks, const int32_t *nchunks, const int32_t *offs, int n_assign, int H,
                                 int I, int E, float *z, int ctas, cudaStream_t s)
 {
-    CUtensorMap tA, tB[4];
+    CUtensorMap tA, tB[6];
     constexpr int MT = Cfg<kDownMx>::MT;
     cudaError_t e = make_down_code_map(&tA, dq, E, H, I);
-    if (e == cudaSuccess) e = make_pair_maps(tB, act_hi, act_lo, n_assign, I);
+    if (e == cudaSuccess) e = make_term_maps(tB, act_hi, act_lo, nullptr, n_assign, I);
     if (e != cudaSuccess) return e;
     const int tiles = (H + BM - 1) / BM;
     GemmArgs a{chunks, nchunks, offs, H, I, I, (tiles + MT - 1) / MT, tiles, MT * Cfg<kDownMx>::CODE_TILE, z, nullptr,
                nullptr, nullptr, 0, BwdQArgs{}, (const uint8_t *)ds, mx_scale_bytes(I)};
     grouped_gemm_kernel<kDownMx><<<grid_for(ctas, n_assign, a.m_tiles, E), Cfg<kDownMx>::THREADS,
-                                   Cfg<kDownMx>::SMEM, s>>>(tA, tB[0], tB[1], tB[2], tB[3], a);
+                                   Cfg<kDownMx>::SMEM, s>>>(tA, tB[0], tB[1], tB[2], tB[3], tB[4], tB[5], a);
     return cudaPeekAtLastError();
 }
 
@@ -1076,67 +1122,55 @@ cudaError_t launch_gemm_gate_up_raw(const void *x, const int32_t *perm, int k, c
                                     float *g, float *u, int ctas, cudaStream_t s, bool seg)
 {
     auto f = seg ? gate_up_like<kGateUpRaw, true> : gate_up_like<kGateUpRaw, false>;
-    return f(x, perm, k, wgu, chunks, nchunks, offs, n_rows, H, I, E, g, u, ctas, s, nullptr, nullptr);
+    return f(x, perm, k, wgu, chunks, nchunks, offs, n_rows, H, I, E, g, u, ctas, s, nullptr, nullptr, nullptr);
 }
 
 cudaError_t launch_gemm_gate_up_keep(const void *x, const int32_t *perm, int k, const void *wgu, const int4 *chunks,
                                      const int32_t *nchunks, const int32_t *offs, int n_rows, int H, int I, int E,
                                      void *act_hi, void *act_lo, float *g, float *u, int ctas, cudaStream_t s,
-                                     bool seg)
+                                     void *act_lo2)
 {
-    auto f = seg ? gate_up_like<kGateUpSave, true> : gate_up_like<kGateUpSave, false>;
-    return f(x, perm, k, wgu, chunks, nchunks, offs, n_rows, H, I, E, act_hi, act_lo, ctas, s, g, u);
+    auto f = act_lo2 ? gate_up_like<kGateUpSave, true> : gate_up_like<kGateUpSave, false>;
+    return f(x, perm, k, wgu, chunks, nchunks, offs, n_rows, H, I, E, act_hi, act_lo, ctas, s, g, u, act_lo2);
 }
 
 cudaError_t launch_bwd_q(const void *ds_hi, const void *ds_lo, const void *wd, const int4 *chunks,
                          const int32_t *nchunks, const int32_t *offs, int n_rows, int H, int I, int E,
-                         const BwdQOut &o, int ctas, cudaStream_t s, bool seg)
+                         const BwdQOut &o, int ctas, cudaStream_t s, const void *ds_lo2)
 {
-    CUtensorMap tA, tB[4];
+    CUtensorMap tA, tB[6];
     cudaError_t e = make_mn_map(&tA, wd, I, H, E);
-    if (e == cudaSuccess) e = make_pair_maps(tB, ds_hi, ds_lo, n_rows, H);
+    if (e == cudaSuccess) e = make_term_maps(tB, ds_hi, ds_lo, ds_lo2, n_rows, H);
     if (e != cudaSuccess) return e;
     const BwdQArgs q{o.g, o.u, o.w_s, (__nv_bfloat16 *)o.dgu_hi, (__nv_bfloat16 *)o.dgu_lo,
-                     (__nv_bfloat16 *)o.wa_hi, (__nv_bfloat16 *)o.wa_lo, o.dwp};
-    auto f = seg ? launch_mn<kBwdQ, true> : launch_mn<kBwdQ, false>;
+                     (__nv_bfloat16 *)o.wa_hi, (__nv_bfloat16 *)o.wa_lo, o.dwp,
+                     (__nv_bfloat16 *)o.dgu_lo2, (__nv_bfloat16 *)o.wa_lo2};
+    auto f = ds_lo2 ? launch_mn<kBwdQ, true> : launch_mn<kBwdQ, false>;
     return f(tA, tB, chunks, nchunks, offs, n_rows, H, I, E, I, H, nullptr, q, ctas, s);
 }
 
 cudaError_t launch_bwd_dx(const void *dgu_hi, const void *dgu_lo, const void *wgu, const int4 *chunks,
                           const int32_t *nchunks, const int32_t *offs, int n_rows, int H, int I, int E, float *z,
-                          int ctas, cudaStream_t s, bool seg)
+                          int ctas, cudaStream_t s, const void *dgu_lo2)
 {
-    CUtensorMap tA, tB[4];
+    CUtensorMap tA, tB[6];
     cudaError_t e = make_mn_map(&tA, wgu, H, 2 * (uint64_t)I, E);
-    if (e == cudaSuccess) e = make_pair_maps(tB, dgu_hi, dgu_lo, n_rows, 2 * (uint64_t)I);
+    if (e == cudaSuccess) e = make_term_maps(tB, dgu_hi, dgu_lo, dgu_lo2, n_rows, 2 * (uint64_t)I);
     if (e != cudaSuccess) return e;
-    auto f = seg ? launch_mn<kBwdDx, true> : launch_mn<kBwdDx, false>;
+    auto f = dgu_lo2 ? launch_mn<kBwdDx, true> : launch_mn<kBwdDx, false>;
     return f(tA, tB, chunks, nchunks, offs, n_rows, H, I, E, H, 2 * I, z, BwdQArgs{}, ctas, s);
 }
 
 cudaError_t launch_gemm_down(const void *act_hi, const void *act_lo, const void *wd, const int4 *chunks,
                              const int32_t *nchunks, const int32_t *offs, int n_assign, int H, int I, int E, float *z,
-                             int ctas, cudaStream_t s, bool seg)
+                             int ctas, cudaStream_t s, const void *act_lo2)
 {
-    CUtensorMap tA, tB0s, tB0, tB1s, tB1;
-    static_assert(Cfg<kDown>::MT == Cfg<kDown, true>::MT, "one item list for both");
-    constexpr int MT = Cfg<kDown>::MT;
+    CUtensorMap tA, tB[6];
     cudaError_t e = make_down_map(&tA, wd, E, H, I);
-    if (e == cudaSuccess) e = make_map(&tB0s, act_hi, n_assign, I, SMALL_ROWS);
-    if (e == cudaSuccess) e = make_map(&tB0, act_hi, n_assign, I, NMAX);
-    if (e == cudaSuccess) e = make_map(&tB1s, act_lo, n_assign, I, SMALL_ROWS);
-    if (e == cudaSuccess) e = make_map(&tB1, act_lo, n_assign, I, NMAX);
+    if (e == cudaSuccess) e = make_term_maps(tB, act_hi, act_lo, act_lo2, n_assign, I);
     if (e != cudaSuccess) return e;
-    const int tiles = (H + BM - 1) / BM;
-    GemmArgs a{chunks, nchunks, offs, H, I, I, (tiles + MT - 1) / MT, tiles, MT * BM * BK * 2, z, nullptr, nullptr,
-               nullptr, 0};
-    const int grid = grid_for(ctas, n_assign, a.m_tiles, E);
-    if (seg)
-        grouped_gemm_kernel<kDown, true><<<grid, Cfg<kDown, true>::THREADS, Cfg<kDown, true>::SMEM, s>>>(
-            tA, tB0s, tB0, tB1s, tB1, a);
-    else
-        grouped_gemm_kernel<kDown><<<grid, kThreads, Cfg<kDown>::SMEM, s>>>(tA, tB0s, tB0, tB1s, tB1, a);
-    return cudaPeekAtLastError();
+    auto f = act_lo2 ? launch_mn<kDown, true> : launch_mn<kDown, false>;
+    return f(tA, tB, chunks, nchunks, offs, n_assign, H, I, E, H, I, z, BwdQArgs{}, ctas, s);
 }
 
 }  // namespace moe

@@ -112,18 +112,19 @@ constexpr unsigned long long kDecodeFusedWaitNs = 2000000000ull;  // default bou
 unsigned long long current_context_id();
 
 // grouped_gemm.cu
-// seg: the instances that add segments of K in FP32 (the calls that take the
-// routing from the caller)
+// seg, or a third term (lo2) of an operand or a result: the instances that add
+// segments of K in FP32 and take FP32 operands as three BF16 terms (the calls
+// that take the routing from the caller)
 cudaError_t gemm_init_device();
 bool gemm_supported(int H, int I, int E);
 // gate_up reads the chunk's token rows from x [T, H] by perm (row p of the
 // sorted order is token perm[p] / k)
 cudaError_t launch_gemm_gate_up(const void *x, const int32_t *perm, int k, const void *wgu, const int4 *chunks,
                                 const int32_t *nchunks, const int32_t *offs, int n_assign, int H, int I, int E,
-                                void *act_hi, void *act_lo, int ctas, cudaStream_t s, bool seg = false);
+                                void *act_hi, void *act_lo, int ctas, cudaStream_t s, void *act_lo2 = nullptr);
 cudaError_t launch_gemm_down(const void *act_hi, const void *act_lo, const void *wd, const int4 *chunks,
                              const int32_t *nchunks, const int32_t *offs, int n_assign, int H, int I, int E, float *z,
-                             int ctas, cudaStream_t s, bool seg = false);
+                             int ctas, cudaStream_t s, const void *act_lo2 = nullptr);
 cudaError_t read_fault_word(uint32_t *flags, bool clear);
 // The same two GEMMs with MXFP8 weights: E4M3 codes gq [E, 2I, H] / dq
 // [E, H, I] and E8M0 scales gs [E, 2I, mx_scale_bytes(H)] / ds [E, H,
@@ -146,7 +147,7 @@ cudaError_t launch_gemm_gate_up_raw(const void *x, const int32_t *perm, int k, c
 cudaError_t launch_gemm_gate_up_keep(const void *x, const int32_t *perm, int k, const void *wgu, const int4 *chunks,
                                      const int32_t *nchunks, const int32_t *offs, int n_rows, int H, int I, int E,
                                      void *act_hi, void *act_lo, float *g, float *u, int ctas, cudaStream_t s,
-                                     bool seg = false);
+                                     void *act_lo2 = nullptr);
 // q = W_down^T dout (dout as ds_hi + ds_lo [rows][H]) and the SwiGLU
 // backward: in g, u, w_s; out dgu_hi/lo [rows][2I], wa_hi/lo [rows][I]
 // (BF16 pairs) and dwp [rows][I/32] (partial sums of act . q)
@@ -154,14 +155,15 @@ struct BwdQOut {
     const float *g, *u, *w_s;
     void *dgu_hi, *dgu_lo, *wa_hi, *wa_lo;
     float *dwp;
+    void *dgu_lo2, *wa_lo2;  // with ds_lo2
 };
 cudaError_t launch_bwd_q(const void *ds_hi, const void *ds_lo, const void *wd, const int4 *chunks,
                          const int32_t *nchunks, const int32_t *offs, int n_rows, int H, int I, int E,
-                         const BwdQOut &o, int ctas, cudaStream_t s, bool seg = false);
+                         const BwdQOut &o, int ctas, cudaStream_t s, const void *ds_lo2 = nullptr);
 // z [rows][H] = W_gate_up^T (dgu_hi + dgu_lo)
 cudaError_t launch_bwd_dx(const void *dgu_hi, const void *dgu_lo, const void *wgu, const int4 *chunks,
                           const int32_t *nchunks, const int32_t *offs, int n_rows, int H, int I, int E, float *z,
-                          int ctas, cudaStream_t s, bool seg = false);
+                          int ctas, cudaStream_t s, const void *dgu_lo2 = nullptr);
 
 // grouped_bwd.cu
 cudaError_t bwd_init_device();
@@ -170,15 +172,16 @@ cudaError_t read_bwd_fault_word(uint32_t *flags, bool clear);
 // routing weight; zeros in pad rows
 cudaError_t launch_bwd_prep(const void *x, const float *dout, const float *w, const int32_t *perm,
                             const int32_t *offs, int n_rows_max, int E, int H, int k, void *xs, void *ds_hi,
-                            void *ds_lo, float *w_s, int n_sm, cudaStream_t s);
+                            void *ds_lo, float *w_s, int n_sm, cudaStream_t s, void *ds_lo2 = nullptr);
 // dW_down [E][H][I] = sum_r ds[r] (x) wa[r] over each expert's rows
 cudaError_t launch_wgrad_down(const void *ds_hi, const void *ds_lo, const void *wa_hi, const void *wa_lo,
                               const int32_t *offs, const int32_t *counts, int n_rows, int H, int I, int E,
-                              float *dwd, int ctas, cudaStream_t s);
+                              float *dwd, int ctas, cudaStream_t s, const void *ds_lo2 = nullptr,
+                              const void *wa_lo2 = nullptr);
 // dW_gate_up [E][2I][H] = sum_r dgu[r] (x) xs[r]
 cudaError_t launch_wgrad_gate_up(const void *dgu_hi, const void *dgu_lo, const void *xs, const int32_t *offs,
                                  const int32_t *counts, int n_rows, int H, int I, int E, float *dwgu, int ctas,
-                                 cudaStream_t s);
+                                 cudaStream_t s, const void *dgu_lo2 = nullptr);
 // dlogits [T][E] from dwp (I/32 partial sums per row), pos, idx, w
 // Zeroes dW_gate_up[e] and dW_down[e] of every expert with counts[e] == 0
 // (the weight-gradient kernels skip those experts).

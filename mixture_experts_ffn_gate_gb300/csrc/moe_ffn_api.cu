@@ -49,6 +49,9 @@ struct Layout {
     // than the fused decode kernel) and the fused kernel's tagged logit words
     // (copies of [T*E] words of 16 bytes), after everything else
     size_t rlog, rtag, router_total;
+    // calls that pass the routing: act's third term (grouped path) and MXFP8
+    // tokens widened to BF16 [T, H]; over the router's regions
+    size_t act_lo2, wide, routed_total;
 };
 
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
@@ -91,6 +94,10 @@ Layout make_layout(const Shape &s)
     L.rlog = take((size_t)(s.T * s.E) * 4);
     L.rtag = take((size_t)(s.T * s.E) * 16 * moe::kDecodeFusedLogitCopies);
     L.router_total = o;
+    o = L.total;
+    L.act_lo2 = take(n * (size_t)s.I * 2);
+    L.wide = take((size_t)(s.T * s.H) * 2);
+    L.routed_total = o;
     return L;
 }
 
@@ -309,9 +316,10 @@ int run_forward(const void *x, const float *logits, const void *wgu, const void 
                                                       n_assign, H, I, E, z, gemm_ctas, stream)));
         } else {
             MOE_TRY(stg.done(moe::launch_gemm_gate_up(x, perm, k, wgu, chunks, nchunks, offs, n_assign, H, I, E,
-                                                      act_hi, act_lo, gemm_ctas, stream, routing != nullptr)));
+                                                      act_hi, act_lo, gemm_ctas, stream,
+                                                      routing ? ws + L.act_lo2 : nullptr)));
             MOE_TRY(stg.done(moe::launch_gemm_down(act_hi, act_lo, wd, chunks, nchunks, offs, n_assign, H, I, E, z,
-                                                   gemm_ctas, stream, routing != nullptr)));
+                                                   gemm_ctas, stream, routing ? ws + L.act_lo2 : nullptr)));
         }
         MOE_TRY(stg.done(moe::launch_combine(z, w, pos, T, H, k, out, dev->n_sm, stream)));
     }
@@ -333,6 +341,8 @@ int run_forward(const void *x, const float *logits, const void *wgu, const void 
 struct BwdLayout {
     size_t flags, idx, w, offs, perm, pos, uexp, ucount, chunks, nchunks, counts;
     size_t xs, ds_hi, ds_lo, w_s, g, u, dgu_hi, dgu_lo, wa_hi, wa_lo, dwp, z, total;
+    // the third terms of the calls that take the routing, after everything else
+    size_t ds_lo2, dgu_lo2, wa_lo2, routed_total;
     int64_t rows;
 };
 
@@ -372,6 +382,10 @@ BwdLayout make_bwd_layout(const Shape &s)
     L.dwp = take(R * (size_t)(s.I / 32) * 4);
     L.z = take(R * (size_t)s.H * 4);
     L.total = o;
+    L.ds_lo2 = take(R * (size_t)s.H * 2);
+    L.dgu_lo2 = take(R * (size_t)s.I * 4);
+    L.wa_lo2 = take(R * (size_t)s.I * 2);
+    L.routed_total = o;
     return L;
 }
 
@@ -414,22 +428,25 @@ int run_backward(const void *x, const float *logits, const void *wgu, const void
                              : moe::launch_router(logits, T, E, k, idx, w, nullptr, nullptr, tag_size, 0, stream)));
     MOE_TRY(stg.done(moe::launch_sort(idx, T * k, E, moe::kGemmChunkMax, offs, perm, pos, (int32_t *)(ws + L.uexp),
                                       (int32_t *)(ws + L.ucount), chunks, nchunks, stream, 16, counts)));
+    void *const ds_lo2 = seg ? ws + L.ds_lo2 : nullptr, *const dgu_lo2 = seg ? ws + L.dgu_lo2 : nullptr;
+    void *const wa_lo2 = seg ? ws + L.wa_lo2 : nullptr;
     MOE_TRY(stg.done(moe::launch_bwd_prep(x, dout, w, perm, offs, rows, E, H, k, ws + L.xs, ws + L.ds_hi,
-                                          ws + L.ds_lo, w_s, dev->n_sm, stream)));
+                                          ws + L.ds_lo, w_s, dev->n_sm, stream, ds_lo2)));
     if (recompute)
         MOE_TRY(stg.done(moe::launch_gemm_gate_up_raw(x, perm, k, wgu, chunks, nchunks, offs, rows, H, I, E, g, u,
                                                       ctas, stream, seg)));
-    const moe::BwdQOut qo{g, u, w_s, ws + L.dgu_hi, ws + L.dgu_lo, ws + L.wa_hi, ws + L.wa_lo, dwp};
+    const moe::BwdQOut qo{g, u, w_s, ws + L.dgu_hi, ws + L.dgu_lo, ws + L.wa_hi, ws + L.wa_lo, dwp,
+                          dgu_lo2, wa_lo2};
     MOE_TRY(stg.done(moe::launch_bwd_q(ws + L.ds_hi, ws + L.ds_lo, wd, chunks, nchunks, offs, rows, H, I, E, qo, ctas,
-                                       stream, seg)));
+                                       stream, ds_lo2)));
     MOE_TRY(stg.done(moe::launch_bwd_dx(ws + L.dgu_hi, ws + L.dgu_lo, wgu, chunks, nchunks, offs, rows, H, I, E, z,
-                                        ctas, stream, seg)));
+                                        ctas, stream, dgu_lo2)));
     MOE_TRY(stg.done(moe::launch_combine(z, nullptr, pos, T, H, k, dx, dev->n_sm, stream)));
     MOE_TRY(stg.done(moe::launch_zero_untouched(counts, E, H, I, dwgu, dwd, dev->n_sm, stream)));
     MOE_TRY(stg.done(moe::launch_wgrad_down(ws + L.ds_hi, ws + L.ds_lo, ws + L.wa_hi, ws + L.wa_lo, offs, counts,
-                                            rows, H, I, E, dwd, ctas, stream)));
+                                            rows, H, I, E, dwd, ctas, stream, ds_lo2, wa_lo2)));
     MOE_TRY(stg.done(moe::launch_wgrad_gate_up(ws + L.dgu_hi, ws + L.dgu_lo, ws + L.xs, offs, counts, rows, H, I, E,
-                                               dwgu, ctas, stream)));
+                                               dwgu, ctas, stream, dgu_lo2)));
     MOE_TRY(stg.done(routing ? moe::launch_routed_dw(dwp, pos, routing->idx, idx, T, k, I, dlogits, stream)
                              : moe::launch_dlogits(dwp, pos, idx, w, T, E, k, I, dlogits, stream)));
     if (opts) {
@@ -455,7 +472,7 @@ int run_forward_train(const void *x, const float *logits, const void *wgu, const
     const int T = (int)s.T, H = (int)s.H, I = (int)s.I, E = (int)s.E, k = (int)s.k;
     const int rows = (int)L.rows;
     const int ctas = (opts && opts->gemm_ctas) ? opts->gemm_ctas : dev->n_sm;
-    const bool seg = routing != nullptr;
+    void *const act_lo2 = routing ? ws + L.wa_lo2 : nullptr;
     auto *idx = (int32_t *)(ws + L.idx);
     auto *w = (float *)(ws + L.w);
     auto *offs = (int32_t *)(ws + L.offs);
@@ -475,9 +492,9 @@ int run_forward_train(const void *x, const float *logits, const void *wgu, const
                                       (int32_t *)(ws + L.ucount), chunks, nchunks, stream, 16, counts)));
     MOE_TRY(stg.done(moe::launch_gemm_gate_up_keep(x, perm, k, wgu, chunks, nchunks, offs, rows, H, I, E,
                                                    ws + L.wa_hi, ws + L.wa_lo, (float *)(ws + L.g),
-                                                   (float *)(ws + L.u), ctas, stream, seg)));
+                                                   (float *)(ws + L.u), ctas, stream, act_lo2)));
     MOE_TRY(stg.done(moe::launch_gemm_down(ws + L.wa_hi, ws + L.wa_lo, wd, chunks, nchunks, offs, rows, H, I, E, z,
-                                           ctas, stream, seg)));
+                                           ctas, stream, act_lo2)));
     MOE_TRY(stg.done(moe::launch_combine(z, w, pos, T, H, k, out, dev->n_sm, stream)));
     if (opts) {
         opts->n_stages = stg.n;
@@ -890,7 +907,14 @@ size_t moe_ffn_routed_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E
 {
     Shape s{T, H, I, E, k};
     if (check_shape(s) != MOE_OK) return 0;
-    return make_layout(s).total + align256((size_t)(T * H * 2));  // the last region: MXFP8 tokens widened
+    return make_layout(s).routed_total;
+}
+
+size_t moe_ffn_routed_backward_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int64_t k)
+{
+    Shape s{T, H, I, E, k};
+    if (check_shape(s) != MOE_OK) return 0;
+    return make_bwd_layout(s).routed_total;
 }
 
 int moe_ffn_forward_routed(const void *x, const void *x_scale, const int32_t *topk_idx, const float *topk_w_f32,
@@ -917,8 +941,7 @@ int moe_ffn_forward_routed(const void *x, const void *x_scale, const int32_t *to
         return MOE_ERR_INVALID_ARG;
     if (!workspace || ((uintptr_t)workspace & 255)) return MOE_ERR_INVALID_ARG;
     const Layout L = make_layout(s);
-    if (workspace_bytes < (x_scale ? moe_ffn_routed_workspace_bytes(T, H, I, E, k) : L.total))
-        return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (workspace_bytes < L.routed_total) return MOE_ERR_WORKSPACE_TOO_SMALL;
     const moe::FusedMx mx{w_gate_up, w_gate_up_scale, w_down, w_down_scale};
     const bool mxw = w_gate_up_scale != nullptr;
     if (mxw && opts && opts->path == MOE_PATH_DECODE && T > kMxMaxTokens) return MOE_ERR_UNSUPPORTED_SHAPE;
@@ -926,7 +949,7 @@ int moe_ffn_forward_routed(const void *x, const void *x_scale, const int32_t *to
         DeviceInfo *dev = nullptr;
         st = device_setup(&dev);
         if (st != MOE_OK) return st;
-        void *wide = (char *)workspace + L.total;
+        void *wide = (char *)workspace + L.wide;
         MOE_TRY(moe::launch_mx_widen(x, x_scale, (int)T, (int)H, wide, dev->n_sm, stream));
         x = wide;
     }
@@ -945,6 +968,7 @@ int moe_ffn_backward_routed(const void *x_bf16, const int32_t *topk_idx, const f
     BwdLayout L;
     int st = check_train_call(s, opts, w_gate_up_bf16, w_down_bf16, workspace, workspace_bytes, &L);
     if (st != MOE_OK) return st;
+    if (T > 0 && workspace_bytes < L.routed_total) return MOE_ERR_WORKSPACE_TOO_SMALL;
     if (!dw_gate_up_f32 || !dw_down_f32 || !aligned16(dw_gate_up_f32) || !aligned16(dw_down_f32))
         return MOE_ERR_INVALID_ARG;
     if (T > 0) {
@@ -975,6 +999,7 @@ int moe_ffn_forward_routed_train(const void *x_bf16, const int32_t *topk_idx, co
     BwdLayout L;
     int st = check_train_call(s, opts, w_gate_up_bf16, w_down_bf16, state, state_bytes, &L);
     if (st != MOE_OK) return st;
+    if (T > 0 && state_bytes < L.routed_total) return MOE_ERR_WORKSPACE_TOO_SMALL;
     if (T > 0) {
         if (!x_bf16 || !topk_idx || !topk_w_f32 || !out_f32) return MOE_ERR_INVALID_ARG;
         if (!aligned16(x_bf16) || !aligned16(topk_idx) || !aligned16(topk_w_f32) || !aligned16(out_f32))

@@ -48,6 +48,7 @@ def declare(L):
         f = getattr(L, name)
         f.argtypes, f.restype = args, i32
     for name, n in (("moe_rms_norm_backward_workspace_bytes", 2), ("moe_ffn_routed_workspace_bytes", 5),
+                    ("moe_ffn_routed_backward_workspace_bytes", 5),
                     ("moe_orthogonalize_workspace_bytes", 3)):
         f = getattr(L, name)
         f.argtypes, f.restype = [i64] * n, sz
@@ -253,12 +254,14 @@ def moe_ffn_routed_workspace_bytes(T, H, I, E, k) -> int:
     return int(_m.lib().moe_ffn_routed_workspace_bytes(T, H, I, E, k))
 
 
-def new_routed_workspace(T, H, I, E, k, device="cuda"):
-    """A workspace for moe_ffn_forward_routed (state bytes zeroed); without
-    MXFP8 tokens moe_ffn.new_workspace's is enough."""
-    ws = _workspace(moe_ffn_routed_workspace_bytes(T, H, I, E, k), device, "workspace size")
-    ws[:_m.MOE_FFN_WORKSPACE_STATE_BYTES].zero_()
-    return ws
+def moe_ffn_routed_backward_workspace_bytes(T, H, I, E, k) -> int:
+    return int(_m.lib().moe_ffn_routed_backward_workspace_bytes(T, H, I, E, k))
+
+
+# Their workspaces and the training pair's state: moe_ffn's, which are as
+# large as these calls need.
+new_routed_workspace = _m.new_workspace
+new_routed_backward_workspace = _m.new_backward_workspace
 
 
 def _routing(topk_idx, topk_w, T):

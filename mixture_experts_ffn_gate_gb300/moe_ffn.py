@@ -41,7 +41,7 @@ EXPORTED = ["moe_ffn_forward", "moe_ffn_workspace_bytes", "moe_ffn_forward_ex",
             # moe_block.h, bound in moe_block.py
             "moe_rms_norm_forward", "moe_rms_norm_backward_workspace_bytes", "moe_rms_norm_backward",
             "moe_gate_forward", "moe_gate_backward", "moe_ffn_routed_workspace_bytes", "moe_ffn_forward_routed",
-            "moe_ffn_backward_routed", "moe_ffn_forward_routed_train", "moe_orthogonalize_workspace_bytes",
+            "moe_ffn_routed_backward_workspace_bytes", "moe_ffn_backward_routed", "moe_ffn_forward_routed_train", "moe_orthogonalize_workspace_bytes",
             "moe_orthogonalize"]
 
 # Size of the library's fixed scratch array used by moe_ffn_forward_noalloc.
@@ -232,11 +232,12 @@ def moe_ffn_forward_noalloc(x, logits, w_gate_up, w_down, k: int, out=None, stre
 
 
 def new_workspace(T, H, I, E, k, device="cuda", host=False):
-    """A workspace tensor big enough for this shape (256-byte aligned).
+    """A workspace tensor big enough for this shape (256-byte aligned),
+    moe_block.moe_ffn_forward_routed's too unless it is for the host entry.
 
     Its state bytes are zeroed: torch's caching allocator may hand out
     memory that served as another workspace and then held other data."""
-    n = (moe_ffn_host_workspace_bytes if host else moe_ffn_workspace_bytes)(T, H, I, E, k)
+    n = moe_ffn_host_workspace_bytes(T, H, I, E, k) if host else lib().moe_ffn_routed_workspace_bytes(T, H, I, E, k)
     if n == 0:
         raise MoeFfnError(MOE_ERR_UNSUPPORTED_SHAPE, "workspace size")
     ws = torch.empty(n, dtype=torch.uint8, device=device)
@@ -380,9 +381,9 @@ def moe_ffn_backward_workspace_bytes(T, H, I, E, k) -> int:
 
 
 def new_backward_workspace(T, H, I, E, k, device="cuda"):
-    """A workspace for moe_ffn_backward (state bytes zeroed, so that forward
-    calls may share it)."""
-    n = moe_ffn_backward_workspace_bytes(T, H, I, E, k)
+    """A workspace for moe_ffn_backward and moe_block.moe_ffn_backward_routed
+    (state bytes zeroed, so that forward calls may share it)."""
+    n = lib().moe_ffn_routed_backward_workspace_bytes(T, H, I, E, k)
     if n == 0:
         raise MoeFfnError(MOE_ERR_UNSUPPORTED_SHAPE, "workspace size")
     ws = torch.empty(n, dtype=torch.uint8, device=device)
@@ -430,8 +431,8 @@ def moe_ffn_train_state_bytes(T, H, I, E, k) -> int:
 
 def new_train_state(T, H, I, E, k, device="cuda"):
     """A state buffer for the training pair (moe_ffn_forward_train, then
-    moe_ffn_backward_train)."""
-    n = moe_ffn_train_state_bytes(T, H, I, E, k)
+    moe_ffn_backward_train; or moe_block's routed pair)."""
+    n = lib().moe_ffn_routed_backward_workspace_bytes(T, H, I, E, k)
     if n == 0:
         raise MoeFfnError(MOE_ERR_UNSUPPORTED_SHAPE, "state size")
     st = torch.empty(n, dtype=torch.uint8, device=device)
