@@ -26,7 +26,8 @@
 // off for a matrix of low rank, and a lo part of 8 bits (E4M3) 3.5e-3 to
 // 2e-2 for one of rank one.
 //
-// The products.  A pair of CTAs (a cluster of two) computes a 256 x BN tile
+// The products.  A pair of CTAs (a cluster of two) computes a 256 x BN tile,
+// BN = 256 or, where the pairs outnumber a product's tiles of 128, 128,
 // with tcgen05.mma.cta_group::2: each CTA loads its 128 rows of the left and
 // its BN / 2 rows of the right operand, so a byte of shared memory feeds
 // twice the work of a single CTA's tile.  Warp 0 of each CTA loads a ring of
@@ -86,9 +87,11 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 
 enum : int { kGram = 0, kPoly = 1, kApply = 2, kLast = 3 };  // kLast: the last step's apply, into the output
 
-template <int BN>
+// BN of the symmetric products and of apply.
+template <int BS, int BX>
 struct Cfg {
-    static constexpr int B_BYTES = BN / 2 * BK * 2;  // one CTA's right operand of a stage
+    static constexpr int BN = BS > BX ? BS : BX;
+    static constexpr int B_BYTES = BN / 2 * BK * 2;  // one CTA's right operand of a stage, at most
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int STAGES = BN == 256 ? 5 : 6;
     static constexpr int STAGING = kEpiWarps * 2 * BLOCK;
@@ -98,7 +101,7 @@ struct Cfg {
 
 // The tensor maps over X (two hi buffers, used in turn, and lo), A and Bm:
 // left operands (K-major, box 64 x 128 rows), right ones (K-major, box 64 x
-// BN / 2 rows), MN-major ones (box 64 x 64 rows) and the epilogue's blocks
+// BS / 2 rows), MN-major ones (box 64 x 64 rows) and the epilogue's blocks
 // (64 x 32 rows).
 struct OrthoMaps {
     CUtensorMap x_left[2], x_right[2], x_cols[2], x_blk[2], lo_blk, a_left, a_right, a_cols, a_blk, b_left, b_cols,
@@ -107,7 +110,7 @@ struct OrthoMaps {
 
 struct OrthoArgs {
     int m, n, batch, steps;  // X is [batch][m][n]
-    int row_tiles, sym_cols, x_cols;  // tiles of 256 rows, of BN columns of A and of X
+    int row_tiles, sym_cols, x_cols;  // tiles of 256 rows, of BS columns of A and BX of X
     int sym_tiles, x_tiles;  // per matrix: of a symmetric product (on and above the diagonal), of apply
     // the factors of the epilogues, powers of two folded in: gram A = g acc;
     // poly Bm = pb A + pc acc; apply X = xa X + xc acc; last: times out_scale
@@ -145,31 +148,38 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// An arrival on a barrier of either CTA that passes on TMEM alone (ordered by
+// the tcgen05 fences): a release at the cluster's scope would wait for all of
+// the thread's stores, 1.2 us per tile.
 __device__ __forceinline__ void arrive_cluster(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
+// Whether the phase is complete, without a wait (try_wait may suspend the
+// thread for a microsecond or more before it says no).
+__device__ __forceinline__ bool test_wait(uint64_t *bar, uint32_t parity)
 {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(ptx::smem_u32(bar)), "r"(parity), "n"(ptx::kSuspendNs)
+        : "r"(ptx::smem_u32(bar)), "r"(parity)
         : "memory");
     return ok != 0;
 }
 
-// mbar_wait_bounded for a barrier that the other CTA arrives on.
-__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, const volatile int *abort)
+// ptx::mbar_wait_bounded, the first try with the suspend-time hint too: the
+// waits here are short, and reading the clock after a failed try cost 5% of
+// the large batches' time.
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, const volatile int *abort)
 {
-    if (try_wait_cluster(bar, parity)) return true;
+    if (ptx::mbar_try_wait_sleep(bar, parity)) return true;
     const uint64_t t0 = ptx::globaltimer_ns();
     for (;;) {
-        if (try_wait_cluster(bar, parity)) return true;
+        if (ptx::mbar_try_wait_sleep(bar, parity)) return true;
         if (*abort) return false;
         if (ptx::globaltimer_ns() - t0 > kWaitNs) return false;
     }
@@ -265,7 +275,7 @@ __device__ __forceinline__ bool wait_count(const uint32_t *done, uint32_t need, 
     return true;
 }
 
-template <int BN>
+template <int BS, int BX>
 __device__ __forceinline__ Tile decode_tile(int i, const OrthoArgs &a)
 {
     const int per_step = 2 * a.sym_tiles + a.x_tiles;  // of one matrix
@@ -286,7 +296,7 @@ __device__ __forceinline__ Tile decode_tile(int i, const OrthoArgs &a)
         // row's diagonal on
         int rt = 0;
         for (;; ++rt) {
-            const int from = rt * 256 / BN, here = a.sym_cols - from;
+            const int from = rt * 256 / BS, here = a.sym_cols - from;
             if (i < here) {
                 i += from;
                 break;
@@ -294,12 +304,12 @@ __device__ __forceinline__ Tile decode_tile(int i, const OrthoArgs &a)
             i -= here;
         }
         t.r0 = rt * 256;
-        t.c0 = i * BN;
+        t.c0 = i * BS;
     } else {
         // down the rows first: neighbouring pairs share the right operand
         const int ct = i / a.row_tiles;
         t.r0 = (i - ct * a.row_tiles) * 256;
-        t.c0 = ct * BN;
+        t.c0 = ct * BX;
     }
     return t;
 }
@@ -312,7 +322,6 @@ struct Sides {
     int left_mn, right_mn;
 };
 
-template <int BN>
 __device__ __forceinline__ Sides sides_of(const Tile &t)
 {
     return {t.kind == kGram ? 0 : t.r0 / BK, t.kind == kGram ? 0 : t.kind == kPoly ? (t.c0 & ~255) / BK : 1 << 30};
@@ -339,7 +348,7 @@ struct Epilogue {
         if (atomicAdd(stored + pending_slot, 1u) == kEpiWarps - 1) {
             stored[pending_slot] = 0;
             ptx::fence_acq_rel_gpu();
-            asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(pending), "r"(1u) : "memory");
+            asm volatile("red.relaxed.gpu.global.add.u32 [%0], %1;" ::"l"(pending), "r"(1u) : "memory");
         }
         pending = nullptr;
     }
@@ -370,9 +379,9 @@ __device__ __forceinline__ bool epilogue(const Tile &t, const OrthoMaps &maps, c
         if (lane == 0) {
             // the block's own operands, while the products run
             if (KIND != kGram) {
-                if (blk == 0 && !ptx::mbar_try_wait(ready, ready_phase)) {
+                if (blk == 0 && !test_wait(ready, ready_phase)) {
                     ep.flush();
-                    failed = !ptx::mbar_wait_bounded(ready, ready_phase, abort_flag, kWaitNs);
+                    failed = !wait_bar(ready, ready_phase, abort_flag);
                 }
                 if (in && !failed) {
                     ptx::bulk_wait_group_read<0>();  // the buffers' last stores have read them
@@ -385,13 +394,13 @@ __device__ __forceinline__ bool epilogue(const Tile &t, const OrthoMaps &maps, c
         }
         failed = __any_sync(0xffffffffu, failed);
         if (blk == 0) {
-            failed = failed || *abort_flag || !wait_cluster(tfull, tfull_phase, abort_flag);
+            failed = failed || *abort_flag || !wait_bar(tfull, tfull_phase, abort_flag);
             failed = __any_sync(0xffffffffu, failed);
             ptx::tc_fence_after();
         }
         if (in && KIND != kGram) {
             const int keep = 0;
-            const bool got = failed || ptx::mbar_wait_bounded(ep.bar, ep.load_phase, &keep, kWaitNs);
+            const bool got = failed || wait_bar(ep.bar, ep.load_phase, &keep);
             ep.load_phase ^= 1;
             failed = __any_sync(0xffffffffu, failed || !got);
         }
@@ -499,11 +508,12 @@ __device__ __forceinline__ bool epilogue(const Tile &t, const OrthoMaps &maps, c
     return true;
 }
 
-template <int BN>
+template <int BS, int BX>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ortho_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant__ OrthoArgs args)
 {
-    using C = Cfg<BN>;
+    using C = Cfg<BS, BX>;
+    constexpr int BN = C::BN;  // TMEM columns per accumulator
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *staging = smem + C::STAGES * C::STAGE_BYTES;
@@ -555,11 +565,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t phase = 0;
             int li = 0;
             for (int i = first; i < total && !*abort_flag; i += pairs, ++li) {
-                const Tile t = decode_tile<BN>(i, args);
+                const Tile t = decode_tile<BS, BX>(i, args);
                 const int x = t.step & 1;
                 const int ksteps = ((t.kind == kGram ? args.n : args.m) + BK - 1) / BK;
-                const int row = t.r0 + 128 * (int)rank, col = t.c0 + BN / 2 * (int)rank;
-                const Sides sides = sides_of<BN>(t);
+                const int bn = t.kind <= kPoly ? BS : BX;
+                const int row = t.r0 + 128 * (int)rank, col = t.c0 + bn / 2 * (int)rank;
+                const uint32_t bytes = 2 * (A_BYTES + bn / 2 * BK * 2);  // of both CTAs
+                const Sides sides = sides_of(t);
                 const CUtensorMap *left = t.kind == kGram   ? &maps.x_left[x]
                                           : t.kind == kPoly ? &maps.a_left
                                                             : &maps.b_left;
@@ -573,14 +585,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 ptx::mbar_arrive(ready + li % kSlots);
                 for (int ks = 0; ks < ksteps; ++ks) {
-                    if (!wait_cluster(empty + stage, phase ^ 1, abort_flag)) {
+                    if (!wait_bar(empty + stage, phase ^ 1, abort_flag)) {
                         if (!*abort_flag) raise(FAULT_GEMM_PRODUCER);
                         *abort_flag = 1;
                         break;
                     }
                     // both CTAs' bytes complete on the first CTA's barrier
                     const uint32_t bar = map_to(ptx::smem_u32(full + stage), 0);
-                    if (rank == 0) ptx::mbar_arrive_expect_tx(full + stage, 2 * C::STAGE_BYTES);
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(full + stage, bytes);
                     uint8_t *l = smem + stage * C::STAGE_BYTES;
                     uint8_t *r = l + A_BYTES;
                     if (ks < sides.left_mn) {
@@ -591,8 +603,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         pair_load_3d(l, left, ks * BK, row, t.b, bar);
                     }
                     if (ks < sides.right_mn) {
-#pragma unroll
-                        for (int h = 0; h < BN / 128; ++h)
+                        for (int h = 0; h < bn / 128; ++h)
                             pair_load_3d(r + h * (64 * BK * 2), right_mn, col + 64 * h, ks * BK, t.b, bar);
                     } else {
                         pair_load_3d(r, right, ks * BK, col, t.b, bar);
@@ -616,11 +627,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t phase = 0;
             int li = 0;
             for (int i = first; i < total && !*abort_flag; i += pairs, ++li) {
-                const Tile t = decode_tile<BN>(i, args);
+                const Tile t = decode_tile<BS, BX>(i, args);
                 const int ksteps = ((t.kind == kGram ? args.n : args.m) + BK - 1) / BK;
-                const Sides sides = sides_of<BN>(t);
+                const Sides sides = sides_of(t);
                 const int acc = li & 1;
-                if (!wait_cluster(tempty + acc, ((li >> 1) & 1) ^ 1, abort_flag)) {
+                if (!wait_bar(tempty + acc, ((li >> 1) & 1) ^ 1, abort_flag)) {
                     if (!*abort_flag) raise(FAULT_GEMM_MMA);
                     *abort_flag = 1;
                     break;
@@ -629,7 +640,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 const uint32_t d = tmem + acc * BN;
                 bool ok = true;
                 for (int ks = 0; ks < ksteps; ++ks) {
-                    if (!wait_cluster(full + stage, phase, abort_flag)) {
+                    if (!wait_bar(full + stage, phase, abort_flag)) {
                         if (!*abort_flag) raise(FAULT_GEMM_MMA);
                         *abort_flag = 1;
                         ok = false;
@@ -641,7 +652,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     // K-major: a K step of 16 is 32 bytes along the rows; MN-major:
                     // 16 rows of 128 bytes, the next 64 of M or N a box on
                     const bool l_mn = ks < sides.left_mn, r_mn = ks < sides.right_mn;
-                    const uint32_t idesc = idesc_f16(BN, l_mn, r_mn);
+                    const uint32_t idesc = idesc_f16(t.kind <= kPoly ? BS : BX, l_mn, r_mn);
                     uint64_t ld = l_mn ? ptx::sw128_desc_mn(l, 64 * BK * 2) : ptx::sw128_desc(l);
                     uint64_t rd = r_mn ? ptx::sw128_desc_mn(r, 64 * BK * 2) : ptx::sw128_desc(r);
                     const uint64_t l_step = l_mn ? 2048 >> 4 : 32 >> 4, r_step = r_mn ? 2048 >> 4 : 32 >> 4;
@@ -658,7 +669,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             // the drain barrier of both CTAs; this CTA's says that all is done
             pair_commit(drain);
-            wait_cluster(drain, 0, abort_flag);
+            wait_bar(drain, 0, abort_flag);
         }
     } else {
         // ---------------------------------------------------- epilogue
@@ -675,20 +686,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ep.pending = nullptr;
         int li = 0;
         for (int i = first; i < total; i += pairs, ++li) {
-            const Tile t = decode_tile<BN>(i, args);
+            const Tile t = decode_tile<BS, BX>(i, args);
             const int acc = li & 1;
             const uint32_t ph = (li >> 1) & 1, at = tmem + acc * BN;
             uint64_t *rd = ready + li % kSlots;
             const uint32_t rph = (li / kSlots) & 1;
             bool ok;
             if (t.kind == kGram)
-                ok = epilogue<kGram, BN>(t, maps, args, ep, rd, rph, tfull + acc, ph, at, abort_flag);
+                ok = epilogue<kGram, BS>(t, maps, args, ep, rd, rph, tfull + acc, ph, at, abort_flag);
             else if (t.kind == kPoly)
-                ok = epilogue<kPoly, BN>(t, maps, args, ep, rd, rph, tfull + acc, ph, at, abort_flag);
+                ok = epilogue<kPoly, BS>(t, maps, args, ep, rd, rph, tfull + acc, ph, at, abort_flag);
             else if (t.kind == kApply)
-                ok = epilogue<kApply, BN>(t, maps, args, ep, rd, rph, tfull + acc, ph, at, abort_flag);
+                ok = epilogue<kApply, BX>(t, maps, args, ep, rd, rph, tfull + acc, ph, at, abort_flag);
             else
-                ok = epilogue<kLast, BN>(t, maps, args, ep, rd, rph, tfull + acc, ph, at, abort_flag);
+                ok = epilogue<kLast, BX>(t, maps, args, ep, rd, rph, tfull + acc, ph, at, abort_flag);
             if (!ok) {
                 if (lane == 0) {
                     if (!*abort_flag) raise(FAULT_GEMM_EPILOGUE);
@@ -956,7 +967,15 @@ Region layout(int64_t B, int64_t M, int64_t N)
     return L;
 }
 
-template <int BN>
+int sym_tiles(int64_t m, int bn)
+{
+    const int cols = (int)ceil_div(m, bn);
+    int n = 0;
+    for (int rt = 0; rt < ceil_div(m, 256); ++rt) n += cols - rt * 256 / bn;
+    return n;
+}
+
+template <int BS, int BX>
 cudaError_t run_steps(const OrthoCall &c, char *ws, const Region &L, int pairs, cudaStream_t s)
 {
     auto *A = (__half *)(ws + L.a), *Bm = (__half *)(ws + L.bm);
@@ -968,13 +987,13 @@ cudaError_t run_steps(const OrthoCall &c, char *ws, const Region &L, int pairs, 
     };
     for (int i = 0; i < 2; ++i) {
         map(&t.x_left[i], hi[i], L.n, L.x_pitch, 128);
-        map(&t.x_right[i], hi[i], L.n, L.x_pitch, BN / 2);
+        map(&t.x_right[i], hi[i], L.n, L.x_pitch, BS / 2);
         map(&t.x_cols[i], hi[i], L.n, L.x_pitch, 64);
         map(&t.x_blk[i], hi[i], L.n, L.x_pitch, 32);
     }
     map(&t.lo_blk, (const __half *)(ws + L.lo), L.n, L.x_pitch, 32);
     map(&t.a_left, A, L.m, L.a_pitch, 128);
-    map(&t.a_right, A, L.m, L.a_pitch, BN / 2);
+    map(&t.a_right, A, L.m, L.a_pitch, BS / 2);
     map(&t.a_cols, A, L.m, L.a_pitch, 64);
     map(&t.a_blk, A, L.m, L.a_pitch, 32);
     map(&t.b_left, Bm, L.m, L.a_pitch, 128);
@@ -989,9 +1008,9 @@ cudaError_t run_steps(const OrthoCall &c, char *ws, const Region &L, int pairs, 
     a.batch = (int)c.B;
     a.steps = c.steps;
     a.row_tiles = (a.m + 255) / 256;
-    a.sym_cols = (a.m + BN - 1) / BN;
-    a.x_cols = (a.n + BN - 1) / BN;
-    for (int rt = 0; rt < a.row_tiles; ++rt) a.sym_tiles += a.sym_cols - rt * 256 / BN;
+    a.sym_cols = (a.m + BS - 1) / BS;
+    a.x_cols = (a.n + BX - 1) / BX;
+    a.sym_tiles = sym_tiles(L.m, BS);
     a.x_tiles = a.row_tiles * a.x_cols;
     a.g = pow2(kABits - 2 * kXBits);
     a.pb = c.b * pow2(kBBits - kABits);
@@ -1008,14 +1027,14 @@ cudaError_t run_steps(const OrthoCall &c, char *ws, const Region &L, int pairs, 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * (at_once < pairs ? at_once : pairs)));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Cfg<BN>::SMEM;
+    cfg.dynamicSmemBytes = Cfg<BS, BX>::SMEM;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;  // tiles wait for tiles: every pair has to be resident
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, ortho_kernel<BN>, t, a);
+    return cudaLaunchKernelEx(&cfg, ortho_kernel<BS, BX>, t, a);
 }
 
 template <typename T>
@@ -1058,23 +1077,27 @@ size_t ortho_workspace_bytes(int64_t B, int64_t M, int64_t N) { return layout(B,
 
 cudaError_t ortho_init_device(int *pairs)
 {
-    cudaError_t e = cudaFuncSetAttribute(ortho_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Cfg<256>::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(ortho_kernel<256, 256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Cfg<256, 256>::SMEM);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(ortho_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<128>::SMEM);
+        e = cudaFuncSetAttribute(ortho_kernel<128, 256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Cfg<128, 256>::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(ortho_kernel<128, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Cfg<128, 128>::SMEM);
     if (e != cudaSuccess) return e;
     // the pairs of CTAs that the device can hold at once
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Cfg<256>::SMEM;
+    cfg.dynamicSmemBytes = Cfg<256, 256>::SMEM;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaOccupancyMaxActiveClusters(pairs, ortho_kernel<256>, &cfg);
+    return cudaOccupancyMaxActiveClusters(pairs, ortho_kernel<256, 256>, &cfg);
 }
 
 cudaError_t launch_orthogonalize(const OrthoCall &c, void *workspace, int pairs, cudaStream_t s)
@@ -1088,11 +1111,19 @@ cudaError_t launch_orthogonalize(const OrthoCall &c, void *workspace, int pairs,
     const cudaError_t e = c.g_f32 ? launch_input<float>(c, L, partial, done, hi, lo, s)
                                   : launch_input<__nv_bfloat16>(c, L, partial, done, hi, lo, s);
     if (e != cudaSuccess) return e;
-    // 256-wide tiles feed the tensor cores best; where they leave pairs of
-    // CTAs without one, 128-wide tiles are twice as many
-    const int64_t rt = ceil_div(L.m, 256);
-    const bool wide = c.B * (rt * (rt + 1) / 2) >= pairs;
-    return wide ? run_steps<256>(c, ws, L, pairs, s) : run_steps<128>(c, ws, L, pairs, s);
+    // 256-wide tiles feed the tensor cores best (a byte of shared memory does a
+    // third more work); 128-wide ones are twice as many and take their turn
+    // where the pairs outnumber them, or nearly so in a batch, whose matrices
+    // fill the last wave.  Measured, us for 256 / 256, 128 / 256, 128 / 128
+    // (symmetric products / apply): 1 x 1536 x 2048 220, 197, 225 (42 and 96
+    // tiles of 128 for 76 pairs); 1 x 1000 x 1000 204, 176, 156 (20, 32);
+    // 2 x 1536 x 2048 249, 253, 277 (84, 192); 40 x 256 x 256 113, 105, 95
+    // (80, 80); 6 x 768 x 2048 218, 204, 231 (72, 288)
+    auto fit = [&](int64_t tiles) { return c.B == 1 ? tiles <= pairs : 12 * c.B * tiles <= 13 * pairs; };
+    const bool sym128 = fit(sym_tiles(L.m, 128));
+    const bool x128 = fit(ceil_div(L.m, 256) * ceil_div(L.n, 128));
+    if (!sym128) return run_steps<256, 256>(c, ws, L, pairs, s);
+    return x128 ? run_steps<128, 128>(c, ws, L, pairs, s) : run_steps<128, 256>(c, ws, L, pairs, s);
 }
 
 }  // namespace moe
