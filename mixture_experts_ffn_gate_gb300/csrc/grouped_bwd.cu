@@ -27,9 +27,13 @@
 //     With three terms per operand (TRIPLE: the calls that take the routing
 //     from the caller) the products down to 2^-16 of the first are taken:
 //     hi.hi + hi.lo + lo.hi + hi.lo2 + lo.lo + lo2.hi, and hi.x + lo.x +
-//     lo2.x; 16 rows per K step and, for dW_down, 128 output columns make
-//     room for four stages.  Error against FP64 (512 tokens, 32 rows per
-//     expert): 4.5e-6 with two terms, %WGERR% with three.
+//     lo2.x; 16 rows per K step make room for the third terms.  The tensor
+//     cores add toward zero, at the accumulator's magnitude, so an expert with
+//     more than kLongRows rows keeps the products below hi.hi in an
+//     accumulator of their own (both TMEM sets, added in the epilogue): the
+//     large one's chain is then rows / 16 long, not six times that (315 rows:
+//     2.7e-6 in one, 8.2e-7 in two).  Error against FP64 (512 tokens, 32 rows per
+//     expert): 4.5e-6 with two terms, 8.3e-7 with three.
 //     One item is one 128 x 256 output tile of one expert; K is the
 //     expert's rows in steps of 32 (the MMA's K steps of 16 stop at the
 //     16-row padding, whose rows are zero).  Both operands are MN-major:
@@ -83,6 +87,7 @@ constexpr int kRowsPerStep = 32;       // rows per K step (TMA box height)
 constexpr int kWThreads = 320;         // producer, MMA issuer, 8 epilogue warps
 constexpr int kEpiWarps = 8;
 constexpr int OUT_BLOCK = 32 * 32 * 4;  // one staged 32 x 32 FP32 output block: 4 KB
+constexpr int kLongRows = 64;           // TRIPLE: experts with more rows take two accumulators
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint64_t kDrainNs = 200000000ull;
 
@@ -93,14 +98,14 @@ struct WCfg {
     static constexpr bool B_PAIR = KIND == kDwDown;      // B is in terms (wa); else x_s
     static constexpr int A_TERMS = TRIPLE ? 3 : 2, B_TERMS = B_PAIR ? A_TERMS : 1;
     static constexpr int WK = TRIPLE ? 16 : kRowsPerStep;     // rows per K step
-    static constexpr int WNB = TRIPLE && B_PAIR ? 128 : kTileCols;
+    static constexpr int WNB = kTileCols;
     static constexpr int BOX = 64 * WK * 2;              // one 64-element x WK-row box
     static constexpr int A_HALF = (WBM / 64) * BOX;      // the tile's rows of one term: 16 KB (TRIPLE: 4)
     static constexpr int B_HALF = (WNB / 64) * BOX;      // 32 KB (TRIPLE: 4, x_s 8)
     static constexpr int A_BYTES = A_TERMS * A_HALF;
     static constexpr int B_BYTES = B_TERMS * B_HALF;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES = TRIPLE ? 7 : B_PAIR ? 4 : 5;
+    static constexpr int STAGES = TRIPLE ? (B_PAIR ? 5 : 7) : B_PAIR ? 4 : 5;
     // one staged block per epilogue warp: the shared memory serves the
     // operand stages better (measured: two blocks per warp and one stage
     // fewer, 2.62 / 5.00 ms at T = 2048; one block, 2.53 / 4.92 ms)
@@ -241,16 +246,23 @@ __global__ void __launch_bounds__(kWThreads, 1)
                 if (rows == 0) continue;
                 const int acc = li & 1;
                 const uint32_t aph = (li >> 1) & 1;
+                const bool two = TRIPLE && rows > kLongRows;
                 ++li;
-                if (!ptx::mbar_wait_bounded(tempty + acc, aph ^ 1, abort_flag, kWaitNs)) {
+                bool ok = ptx::mbar_wait_bounded(tempty + acc, aph ^ 1, abort_flag, kWaitNs);
+                if (ok && two) {
+                    ok = ptx::mbar_wait_bounded(tempty + (li & 1), ((li >> 1) & 1) ^ 1, abort_flag, kWaitNs);
+                    ++li;
+                }
+                if (!ok) {
                     if (!*abort_flag) raise(FAULT_GEMM_MMA);
                     *abort_flag = 1;
                     break;
                 }
                 ptx::tc_fence_after();
                 const uint32_t d = tmem + acc * WNB;
+                // where the smaller products go, and whether the first of them adds
+                const uint32_t ds = two ? tmem + (acc ^ 1) * WNB : d;
                 const int padded = (rows + 15) & ~15;
-                bool ok = true;
                 for (int kr = 0; kr < rows; kr += WK) {
                     if (!ptx::mbar_wait_bounded(full + stage, phase, abort_flag, kWaitNs)) {
                         if (!*abort_flag) raise(FAULT_GEMM_MMA);
@@ -269,18 +281,18 @@ __global__ void __launch_bounds__(kWThreads, 1)
                         ptx::mma_bf16(d, ah, bh, idesc, (kr | k) != 0);
                         if (C::B_PAIR) {
                             const uint64_t bl = ptx::sw128_desc_mn(b_addr + C::B_HALF + k * 2048, BOX);
-                            ptx::mma_bf16(d, ah, bl, idesc, 1);
+                            ptx::mma_bf16(ds, ah, bl, idesc, !two || (kr | k) != 0);
                         }
-                        ptx::mma_bf16(d, al, bh, idesc, 1);
+                        ptx::mma_bf16(ds, al, bh, idesc, C::B_PAIR || !two || (kr | k) != 0);
                         if (TRIPLE) {
                             const uint64_t al2 = ptx::sw128_desc_mn(a_addr + 2 * C::A_HALF + k * 2048, BOX);
                             if (C::B_PAIR) {
                                 const uint64_t bl = ptx::sw128_desc_mn(b_addr + C::B_HALF + k * 2048, BOX);
                                 const uint64_t bl2 = ptx::sw128_desc_mn(b_addr + 2 * C::B_HALF + k * 2048, BOX);
-                                ptx::mma_bf16(d, ah, bl2, idesc, 1);
-                                ptx::mma_bf16(d, al, bl, idesc, 1);
+                                ptx::mma_bf16(ds, ah, bl2, idesc, 1);
+                                ptx::mma_bf16(ds, al, bl, idesc, 1);
                             }
-                            ptx::mma_bf16(d, al2, bh, idesc, 1);
+                            ptx::mma_bf16(ds, al2, bh, idesc, 1);
                         }
                     }
                     ptx::mma_commit(empty + stage);
@@ -291,6 +303,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
                 }
                 if (!ok) break;
                 ptx::mma_commit(tfull + acc);
+                if (two) ptx::mma_commit(tfull + (acc ^ 1));
             }
             ptx::mma_commit(drain);
             ptx::mbar_wait_bounded(drain, 0, abort_flag, kDrainNs);
@@ -328,8 +341,12 @@ __global__ void __launch_bounds__(kWThreads, 1)
             if (rows == 0) continue;   // nothing selected this expert: zero_untouched_kernel wrote its zeros
             const int acc = li & 1;
             const uint32_t aph = (li >> 1) & 1;
+            const bool two = TRIPLE && rows > kLongRows;
             ++li;
-            if (*abort_flag || !ptx::mbar_wait_bounded(tfull + acc, aph, abort_flag, kWaitNs)) {
+            bool got = !*abort_flag && ptx::mbar_wait_bounded(tfull + acc, aph, abort_flag, kWaitNs);
+            if (got && two) got = ptx::mbar_wait_bounded(tfull + (acc ^ 1), (li >> 1) & 1, abort_flag, kWaitNs);
+            if (two) ++li;
+            if (!got) {
                 if (!*abort_flag) raise(FAULT_GEMM_EPILOGUE);
                 *abort_flag = 1;
                 break;
@@ -339,13 +356,23 @@ __global__ void __launch_bounds__(kWThreads, 1)
             for (int c0 = half * (WNB / 2); c0 < (half + 1) * (WNB / 2); c0 += 32) {
                 uint32_t r[32];
                 ptx::tmem_ld32(tbase + c0, r);
+                if (two) {
+                    uint32_t r2[32];
+                    ptx::tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + (acc ^ 1) * WNB + c0, r2);
+                    ptx::tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(r2[j]));
+                }
                 ptx::tmem_wait_ld();
                 // N is a multiple of 64, so a 32-column block is all in or all out
                 if (rows_in && n0 + c0 < args.N) put_block(r, e, row0, n0 + c0);
             }
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(tempty + acc);
+            if (lane == 0) {
+                ptx::mbar_arrive(tempty + acc);
+                if (two) ptx::mbar_arrive(tempty + (acc ^ 1));
+            }
         }
         if (lane == 0) ptx::bulk_wait_all();   // the last stores have left shared memory and landed
         __syncwarp();

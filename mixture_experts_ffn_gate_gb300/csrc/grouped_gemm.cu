@@ -43,9 +43,9 @@
 //     shrinks a chain of K / 16 of them with its length.
 //   - an FP32 operand is three BF16 terms hi + lo + lo2 (24 bits), not two.
 // Measured against FP64 at H = 4096, I = 1536: 1.1e-5 with one chain and two
-// terms, 2.6e-6 with segments of 256 and two, %SEGERR% with both.  The drains
+// terms, 2.6e-6 with segments of 256 and two, 7.4e-7 with both.  The drains
 // and the third term are small beside the weight stream that bounds these
-// kernels (733 us with segments, %SEGTIME% with both, 64 tokens).  An epilogue
+// kernels (733 us with segments, 737 us with both, 64 tokens).  An epilogue
 // warp keeps the sums of one 32-row x 64-column block, so SEG has four
 // epilogue warps per weight tile, and two tiles per item.
 //
@@ -227,8 +227,7 @@ __device__ __forceinline__ void store_pair(__nv_bfloat16 *hi, __nv_bfloat16 *lo,
 }
 
 // Three BF16 terms of an FP32 value.
-__device__ __forceinline__ void store_terms(__nv_bfloat16 *hi, __nv_bfloat16 *lo, __nv_bfloat16 *lo2, int64_t at,
-                                            float v)
+__device__ __forceinline__ void store_terms(__nv_bfloat16 *hi, __nv_bfloat16 *lo, __nv_bfloat16 *lo2, int at, float v)
 {
     const __nv_bfloat16 h = __float2bfloat16_rn(v);
     const float r = v - __bfloat162float(h);
@@ -261,10 +260,9 @@ __device__ __forceinline__ float warp_column_sums(float (&v)[32], int lane)
 // j) of neuron i, whose q = W_down[e]^T dout_t values are r[j]:
 //   s = sigmoid(g), a = g s u, da = w q,
 //   dg = da u s (1 + g (1 - s)), du = da g s,
-// stored as BF16 pairs (SEG: three terms; dgu rows: dg at i, du at I + i; wa = w a), zeros in
+// stored as BF16 pairs (dgu rows: dg at i, du at I + i; wa = w a), zeros in
 // the expert's pad rows; and act . q summed over the warp's 32 neurons
 // into dwp[row][grp].
-template <bool SEG>
 __device__ __forceinline__ void bwd_q_columns(const uint32_t (&r)[32], int ncols, int p0, int n, int c0, int i,
                                               int grp, const GemmArgs &args, int lane)
 {
@@ -307,20 +305,77 @@ __device__ __forceinline__ void bwd_q_columns(const uint32_t (&r)[32], int ncols
                     wa = w * a;
                     prod[j] = a * qv;
                 }
-                if constexpr (SEG) {
-                    store_terms(b.dgu_hi, b.dgu_lo, b.dgu_lo2, row * 2 * I + i, dg);
-                    store_terms(b.dgu_hi, b.dgu_lo, b.dgu_lo2, row * 2 * I + I + i, du);
-                    store_terms(b.wa_hi, b.wa_lo, b.wa_lo2, row * I + i, wa);
-                } else {
-                    store_pair(b.dgu_hi, b.dgu_lo, row * 2 * I + i, dg);
-                    store_pair(b.dgu_hi, b.dgu_lo, row * 2 * I + I + i, du);
-                    store_pair(b.wa_hi, b.wa_lo, row * I + i, wa);
-                }
+                store_pair(b.dgu_hi, b.dgu_lo, row * 2 * I + i, dg);
+                store_pair(b.dgu_hi, b.dgu_lo, row * 2 * I + I + i, du);
+                store_pair(b.wa_hi, b.wa_lo, row * I + i, wa);
             }
         }
     }
     const float sum = warp_column_sums(prod, lane);
     if (lane < ncols && c0 + lane < n) b.dwp[(int64_t)(p0 + c0 + lane) * (I / 32) + grp] = sum;
+}
+
+// The same with three terms per value (SEG), eight columns at a time: the
+// warp also holds the item's 64 sums, and with all 32 columns' operands in
+// registers beside them the loads went one after the other (q took 170 us
+// instead of 145 at 512 tokens, H = 2048, I = 768, E = 128).  The next
+// eight columns' loads are issued before this one's stores.
+__device__ __forceinline__ void bwd_q_columns_terms(const uint32_t (&r)[32], int p0, int n, int c0, int i, int grp,
+                                                    const GemmArgs &args, int lane)
+{
+    const int I = args.I, npad = pad16(n);
+    const BwdQArgs &b = args.q;
+    // the block's first row; the rest are 32-bit offsets from it
+    const int64_t at = (int64_t)(p0 + c0) * I + i, at2 = at + (int64_t)(p0 + c0) * I;
+    const float *const g0 = b.g + at, *const u0 = b.u + at, *const w0 = b.w_s + p0 + c0;
+    __nv_bfloat16 *const d_hi = b.dgu_hi + at2, *const d_lo = b.dgu_lo + at2, *const d_lo2 = b.dgu_lo2 + at2;
+    __nv_bfloat16 *const a_hi = b.wa_hi + at, *const a_lo = b.wa_lo + at, *const a_lo2 = b.wa_lo2 + at;
+    float gv[2][8], uv[2][8], wv[2][8];
+    auto load = [&](int h, int buf) {
+#pragma unroll
+        for (int jj = 0; jj < 8; ++jj) {
+            const int j = 8 * h + jj;
+            const bool live = c0 + j < n;
+            gv[buf][jj] = live ? __ldg(g0 + j * I) : 0.0f;
+            uv[buf][jj] = live ? __ldg(u0 + j * I) : 0.0f;
+            wv[buf][jj] = live ? __ldg(w0 + j) : 0.0f;
+        }
+    };
+    load(0, 0);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        if (c0 + 8 * h >= npad) break;
+        if (h < 3) load(h + 1, (h + 1) & 1);
+        float prod[8];
+#pragma unroll
+        for (int jj = 0; jj < 8; ++jj) {
+            const int col = c0 + 8 * h + jj;
+            prod[jj] = 0.0f;
+            if (col < npad) {
+                float dg = 0.0f, du = 0.0f, wa = 0.0f;
+                if (col < n) {
+                    const float qv = __uint_as_float(r[8 * h + jj]);
+                    const float g = gv[h & 1][jj], u = uv[h & 1][jj], w = wv[h & 1][jj];
+                    const float sg = 1.0f / (1.0f + expf(-g));
+                    const float silu = g * sg;
+                    const float a = silu * u;
+                    const float da = w * qv;
+                    dg = da * u * (sg * (1.0f + g * (1.0f - sg)));
+                    du = da * silu;
+                    wa = w * a;
+                    prod[jj] = a * qv;
+                }
+                const int j = 8 * h + jj;
+                store_terms(d_hi, d_lo, d_lo2, j * 2 * I, dg);
+                store_terms(d_hi, d_lo, d_lo2, j * 2 * I + I, du);
+                store_terms(a_hi, a_lo, a_lo2, j * I, wa);
+            }
+        }
+        // the sum of column s ends in lanes 4 s ..
+        const float sum = warp_sum_split<8>(prod, lane);
+        const int col = c0 + 8 * h + (lane >> 2);
+        if ((lane & 3) == 0 && col < n) b.dwp[(int64_t)(p0 + col) * (I / 32) + grp] = sum;
+    }
 }
 
 template <int KIND, bool SEG = false>
@@ -711,8 +766,11 @@ __global__ void __launch_bounds__(Cfg<KIND, SEG>::THREADS, 1)
                                 for (int j = 0; j < 32; ++j)
                                     if (c0 + j < it.n) dst[(int64_t)(it.p0 + c0 + j) * args.I + neuron] = __uint_as_float(r[j]);
                             } else if constexpr (KIND == kBwdQ) {
-                                bwd_q_columns<SEG>(r, it.n > SMALL_ROWS ? 32 : SMALL_ROWS, it.p0, it.n, c0, tile * BM + 32 * q + lane,
-                                              tile * 4 + q, args, lane);
+                if constexpr (SEG)
+                    bwd_q_columns_terms(r, it.p0, it.n, c0, tile * BM + 32 * q + lane, tile * 4 + q, args, lane);
+                else
+                    bwd_q_columns(r, it.n > SMALL_ROWS ? 32 : SMALL_ROWS, it.p0, it.n, c0, tile * BM + 32 * q + lane,
+                                  tile * 4 + q, args, lane);
                             } else if constexpr (KIND == kGateUp || KIND == kGateUpMx || KIND == kGateUpSave) {
                                 const int neuron = tile * 64 + 16 * q + (lane & 15);
                                 __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(lane < 16 ? args.out0 : args.out1);

@@ -730,9 +730,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- the input
 constexpr int kMaxParts = 64;
-// G is read twice, for its norm and to be scaled: matrices are taken in turns
-// of at most this many bytes, so that the second read comes from L2.
-constexpr int64_t kTurnBytes = 48 << 20;
+// G is read twice, for its norm and to be scaled, both bound by memory (16
+// matrices of 1536 x 2048 in FP32: 34 and 66 us).  Taking the matrices in
+// turns that fit L2 costs more in short launches than it saves (128 us).
 
 // 8 consecutive elements, 16-byte aligned (BF16) or 32 (FP32)
 __device__ __forceinline__ void load8(const float *p, float (&v)[8])
@@ -1045,30 +1045,20 @@ cudaError_t launch_input(const OrthoCall &c, const Region &L, float *partial, ui
     const int64_t slices = ceil_div(count, 8192);
     const int parts = (int)(slices < kMaxParts ? slices : kMaxParts);
     const bool tall = c.M > c.N, by8 = c.M % 8 == 0 && c.N % 8 == 0;
-    const int64_t fit = kTurnBytes / (count * (int64_t)sizeof(T));
-    const int64_t turn = fit < 1 ? 1 : fit < c.B ? fit : c.B;
-    for (int64_t b = 0; b < c.B; b += turn) {
-        const unsigned n = (unsigned)(c.B - b < turn ? c.B - b : turn);
-        const T *g = (const T *)c.g + b * count;
-        float *part = partial + b * kMaxParts;
-        const int64_t at = b * L.m * L.x_pitch;
-        ortho_norm_kernel<<<dim3(parts, n), 256, 0, s>>>(g, count, part, done + b);
-        const int M = (int)c.M, N = (int)c.N;
-        if (by8 && !tall)
-            ortho_split8_kernel<T, true>
-                <<<dim3((unsigned)ceil_div(count, 8 * 256 * 4), 1, n), 256, 0, s>>>(g, M, N, part, parts, c.eps,
-                                                                                    hi + at, lo + at);
-        else if (by8)
-            ortho_split8_kernel<T, false>
-                <<<dim3((unsigned)ceil_div(N, 64), (unsigned)ceil_div(M, 64), n), 256, 0, s>>>(g, M, N, part, parts,
-                                                                                               c.eps, hi + at, lo + at);
-        else
-            ortho_split_kernel<<<dim3((unsigned)ceil_div(N, 32), (unsigned)ceil_div(M, 32), n), 256, 0, s>>>(
-                g, M, N, part, parts, c.eps, tall, L.x_pitch, hi + at, lo + at);
-        const cudaError_t e = cudaPeekAtLastError();
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    const unsigned B = (unsigned)c.B;
+    const T *g = (const T *)c.g;
+    const int M = (int)c.M, N = (int)c.N;
+    ortho_norm_kernel<<<dim3(parts, B), 256, 0, s>>>(g, count, partial, done);
+    if (by8 && !tall)
+        ortho_split8_kernel<T, true><<<dim3((unsigned)ceil_div(count, 8 * 256 * 4), 1, B), 256, 0, s>>>(
+            g, M, N, partial, parts, c.eps, hi, lo);
+    else if (by8)
+        ortho_split8_kernel<T, false><<<dim3((unsigned)ceil_div(N, 64), (unsigned)ceil_div(M, 64), B), 256, 0, s>>>(
+            g, M, N, partial, parts, c.eps, hi, lo);
+    else
+        ortho_split_kernel<<<dim3((unsigned)ceil_div(N, 32), (unsigned)ceil_div(M, 32), B), 256, 0, s>>>(
+            g, M, N, partial, parts, c.eps, tall, L.x_pitch, hi, lo);
+    return cudaPeekAtLastError();
 }
 
 }  // namespace

@@ -353,7 +353,8 @@ def test_routed_mxfp8_tokens_are_their_values(T):
 
 
 @pytest.mark.parametrize("T,H,I,E,k", [(1, 256, 128, 8, 2), (3, 320, 192, 5, 3), (40, 384, 192, 12, 3),
-                                       (33, 128, 64, 3, 1), (90, 256, 128, 4, 2), (12, 64, 64, 40, 32)])
+                                       (33, 128, 64, 3, 1), (90, 256, 128, 4, 2), (12, 64, 64, 40, 32),
+                                       (150, 192, 64, 2, 2), (300, 64, 128, 3, 1)])
 @pytest.mark.parametrize("drop", [False, True])
 def test_routed_backward(T, H, I, E, k, drop):
     x, wgu, wd = layer(T, H, I, E, seed=20)
