@@ -226,7 +226,7 @@ int moe_ffn_forward_routed_train(const void *x_bf16, const int32_t *topk_idx,
  * of which the products read the high one; A and b A + c A A are rounded to
  * FP16.  Relative error in the 2-norm for the usual coefficients: up to 2e-3
  * before out's rounding to BF16, and 1.7e-3 from that.
- * A matrix of zeros gives zeros; a NaN or an infinity spreads over its whole
+ * A matrix of zeros gives zeros (NaN with eps == 0); a NaN or an infinity spreads over its whole
  * matrix and no other.  Squares are summed in FP32: entries below about
  * 1e-19 count as zero in the norm.
  * Limits: M, N in 1..32768, steps in 1..32, B >= 0 (0 enqueues nothing),

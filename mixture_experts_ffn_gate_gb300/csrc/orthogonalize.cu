@@ -82,7 +82,11 @@ constexpr int A_BYTES = 128 * BK * 2;     // one CTA's left operand of a stage
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
 constexpr int BLOCK = 32 * 64 * 2;        // one staged 32 x 64 FP16 block
-constexpr int kSlots = 4;                 // tiles that the producer and the epilogue can be apart, and one more
+// The producer says of a tile that its operands are complete on one of kSlots
+// barriers.  It can be ahead of the epilogue by the tiles in the ring (one per
+// stage where K is a single step) and the two accumulators; a barrier must not
+// come round again before the epilogue has waited for it.
+constexpr int kSlots = 16;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 enum : int { kGram = 0, kPoly = 1, kApply = 2, kLast = 3 };  // kLast: the last step's apply, into the output
@@ -97,6 +101,7 @@ struct Cfg {
     static constexpr int STAGING = kEpiWarps * 2 * BLOCK;
     static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + STAGING + 512;
     static_assert(SMEM <= 227 * 1024, "shared memory");
+    static_assert(STAGES + 2 < kSlots, "a ready barrier would come round too soon");
 };
 
 // The tensor maps over X (two hi buffers, used in turn, and lo), A and Bm:
@@ -901,6 +906,286 @@ __global__ void __launch_bounds__(256) ortho_split_kernel(const T *__restrict__ 
     }
 }
 
+// ---------------------------------------------------------------- small matrices
+// m, n <= 256: one pair of CTAs keeps a matrix in shared memory through all
+// its steps, one launch, no workspace.  CTA r holds rows 128 r .. of X
+// (K-major, the left and, as its half of N, the right operand of gram) and of
+// A, then Bm in its place (left and right operand of poly, left of apply; A is
+// symmetric), and columns 128 r .. of X (MN-major, the right operand of
+// apply), of which the other CTA writes its rows' share through the cluster.
+// lo stays in registers: thread (row, a quarter of its columns) in the epilogue of
+// every product.  Rows and columns past the matrix are zeros.  The general
+// kernel's tiles go through L2 between products, 4.4 us each; here a product
+// takes 3.4 us (1.3 us of MMAs, 0.9 to 2.2 us of epilogue, the rest signals).
+// Measured, us there and here: 8 x 256 x 256 86, 64; 76 x 256 x 256 120, 67;
+// 300 x 256 x 256 328, 266; 1 x 72 x 71 68, 52; 300 x 128 x 128 212, 191
+// (600 x 64 x 64, the one that is slower here, 271, 324).
+constexpr int kSmall = 256;
+constexpr int kSmallWarps = 16;                 // of the epilogue (eight took 1.3 to 4 us for a product's)
+constexpr int kSmallThreads = 32 * (kSmallWarps + 1);  // and the MMA issuer
+constexpr int kTile = 128 * BK * 2;             // 128 rows of 64 FP16
+constexpr int kRows = 4 * kTile;                // 128 rows of 256
+constexpr int kSmallSmem = 1024 + 3 * kRows + 256;
+static_assert(kSmallSmem <= 227 * 1024, "shared memory");
+
+struct SmallArgs {
+    const void *g;
+    int M, N, steps;
+    float eps, gram, pb, pc, xa, xc, out_scale;  // as in OrthoArgs
+    __nv_bfloat16 *out;
+};
+
+__device__ __forceinline__ void st_cluster(uint32_t addr, const uint4 &v)
+{
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w)
+                 : "memory");
+}
+
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const SmallArgs args)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *const xr = smem, *const ar = xr + kRows, *const xc = ar + kRows;
+    uint64_t *go = reinterpret_cast<uint64_t *>(xc + kRows);  // operands of the next product written, by 32 warps
+    uint64_t *done = go + 1;                                  // a product's MMAs have completed
+    float *sums = reinterpret_cast<float *>(done + 1);        // a warp's sum of squares; then, first, the CTA's
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sums + kSmallWarps + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int b = blockIdx.x / 2;
+    const bool tall = args.M > args.N;
+    const int m = tall ? args.N : args.M, n = tall ? args.M : args.N;
+    const T *g = (const T *)args.g + (int64_t)b * args.M * args.N;
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(go, 2 * kSmallWarps);
+        ptx::mbar_init(done, 1);
+        *abort_flag = 0;
+        ptx::fence_barrier_init();
+    }
+    __syncwarp();
+    if (warp == kSmallWarps) pair_tmem_alloc(tmem_slot, kSmall);
+    // the sum of squares, half of the elements per CTA
+    {
+        const int count = args.M * args.N;
+        float s = 0.0f;
+        for (int i = (int)rank * kSmallThreads + threadIdx.x; i < count; i += 2 * kSmallThreads) {
+            const float v = (float)g[i];
+            s = fmaf(v, v, s);
+        }
+        s = warp_sum(s);
+        if (lane == 0) sums[warp] = s;
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    float mine = 0.0f;
+    for (int w = 0; w <= kSmallWarps; ++w) mine += sums[w];
+    __syncthreads();
+    if (threadIdx.x == 0) sums[0] = mine;
+    cluster_sync();  // barriers initialised, TMEM allocated, both sums written
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    float other;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other) : "r"(map_to(ptx::smem_u32(sums), rank ^ 1)));
+    const float f = (float)(1 << kXBits) / (sqrtf(rank == 0 ? mine + other : other + mine) + args.eps);
+
+    const int products = 3 * args.steps;
+    if (warp == kSmallWarps) {
+        // ---------------------------------------------------- MMA issuer, for both CTAs
+        if (lane == 0 && rank == 0) {
+            const uint32_t xr_a = ptx::smem_u32(xr), ar_a = ptx::smem_u32(ar), xc_a = ptx::smem_u32(xc);
+            for (int p = 0; p < products; ++p) {
+                const int kind = p % 3;
+                uint32_t ok = 0;
+                const uint64_t t0 = ptx::globaltimer_ns();
+                do {  // the other CTA's stores to its shared memory are read by the MMAs
+                    asm volatile(
+                        "{\n\t.reg .pred q;\n\t"
+                        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 q, [%1], %2, %3;\n\t"
+                        "selp.u32 %0, 1, 0, q;\n\t}"
+                        : "=r"(ok)
+                        : "r"(ptx::smem_u32(go)), "r"((uint32_t)(p & 1)), "n"(ptx::kSuspendNs)
+                        : "memory");
+                } while (!ok && !*abort_flag && ptx::globaltimer_ns() - t0 < kWaitNs);
+                if (!ok) {
+                    if (!*abort_flag) raise(FAULT_GEMM_MMA);
+                    *abort_flag = 1;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const int blocks = ((kind == kGram ? n : m) + BK - 1) / BK;
+                const uint32_t idesc = idesc_f16(kSmall, false, kind == 2);
+                const uint32_t left = kind == kGram ? xr_a : ar_a;
+                for (int kb = 0; kb < blocks; ++kb) {
+                    const uint64_t ld = ptx::sw128_desc(left + kb * kTile);
+                    const uint64_t rd = kind == 2 ? ptx::sw128_desc_mn(xc_a + kb * 64 * 128, kRows / 2)
+                                                  : ptx::sw128_desc(left + kb * kTile);
+                    const uint64_t r_step = kind == 2 ? 2048 >> 4 : 32 >> 4;
+#pragma unroll
+                    for (int k = 0; k < BK / 16; ++k) pair_mma(tmem, ld + k * (32 >> 4), rd + k * r_step, idesc, (kb | k) != 0);
+                }
+                pair_commit(done);
+            }
+            // (the epilogues wait for every product's MMAs)
+        }
+    } else {
+        // ---------------------------------------------------- epilogue
+        const int q = warp & 3, part = warp >> 2;
+        const int r = 32 * q + lane, row = 128 * (int)rank + r;  // this thread's row, in the CTA and the matrix
+        // this thread's 16-byte piece of columns c .. c + 7 (c a multiple of 8)
+        // in 128 rows of 256, and of X's columns for CTA c / 128
+        auto piece = [&](uint8_t *rows, int c) {
+            return reinterpret_cast<uint4 *>(rows + (c / 64) * kTile + r * 128 + (((c / 8 % 8) ^ (r & 7)) << 4));
+        };
+        const bool own = (uint32_t)(part >> 1) == rank;  // this thread's columns are this CTA's
+        const uint32_t xc_other = map_to(ptx::smem_u32(xc), rank ^ 1);
+        auto put_x = [&](int c, const uint4 &v) {
+            *piece(xr, c) = v;
+            const uint32_t at = (part & 1) * (kRows / 2) + row * 128 + (((c / 8 % 8) ^ (row & 7)) << 4);
+            if (own)
+                *reinterpret_cast<uint4 *>(xc + at) = v;
+            else
+                st_cluster(xc_other + at, v);
+        };
+        auto publish = [&] {
+            ptx::tc_fence_before();
+            asm volatile("fence.proxy.async;" ::: "memory");  // this thread's stores, the other CTA's memory too
+            __syncwarp();
+            if (lane == 0)
+                asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                                 map_to(ptx::smem_u32(go), 0))
+                             : "memory");
+        };
+        uint32_t lo[2][16];  // 64 columns' low parts
+        // X = f G: this row's columns 64 part ..
+#pragma unroll
+        for (int c4 = 0; c4 < 2; ++c4)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int c = 64 * part + 32 * c4 + 8 * j;
+                float v[8];
+                if (!tall && args.N % 8 == 0) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+                    if (row < m && c < n) load8(g + (int64_t)row * n + c, v);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[e] = row < m && c + e < n ? (float)(tall ? g[(int64_t)(c + e) * m + row]
+                                                                  : g[(int64_t)row * n + c + e])
+                                                    : 0.0f;
+                }
+                uint32_t hi[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v0 = v[2 * e] * f, v1 = v[2 * e + 1] * f;
+                    hi[e] = half_pair(v0, v1);
+                    const float2 h = half_unpair(hi[e]);
+                    lo[c4][4 * j + e] = half_pair((v0 - h.x) * kLoScale, (v1 - h.y) * kLoScale);
+                }
+                put_x(c, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+                *piece(ar, c) = make_uint4(0, 0, 0, 0);  // what gram leaves out past m
+            }
+        publish();
+        for (int p = 0; p < products; ++p) {
+            const int kind = p % 3;
+            bool ok = wait_bar(done, p & 1, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) {
+                if (lane == 0) {
+                    if (!*abort_flag) raise(FAULT_GEMM_EPILOGUE);
+                    *abort_flag = 1;
+                }
+                break;
+            }
+            ptx::tc_fence_after();
+            const bool last = p + 1 == products;
+#pragma unroll
+            for (int c4 = 0; c4 < 2; ++c4) {
+                const int c0 = 64 * part + 32 * c4;
+                if (c0 >= (kind == 2 ? n : m)) continue;  // zeros, as they were
+                uint32_t acc[32];
+                ptx::tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + c0, acc);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int c = c0 + 8 * j;
+                    uint32_t o[4];
+                    if (kind == kGram) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[e] = half_pair(__uint_as_float(acc[8 * j + 2 * e]) * args.gram,
+                                             __uint_as_float(acc[8 * j + 2 * e + 1]) * args.gram);
+                        *piece(ar, c) = make_uint4(o[0], o[1], o[2], o[3]);
+                    } else if (kind == kPoly) {
+                        const uint4 a = *piece(ar, c);
+                        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 y = half_unpair(w[e]);
+                            o[e] = half_pair(fmaf(args.pc, __uint_as_float(acc[8 * j + 2 * e]), args.pb * y.x),
+                                             fmaf(args.pc, __uint_as_float(acc[8 * j + 2 * e + 1]), args.pb * y.y));
+                        }
+                        *piece(ar, c) = make_uint4(o[0], o[1], o[2], o[3]);
+                    } else {
+                        const uint4 a = *piece(xr, c);
+                        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 y = half_unpair(w[e]), z = half_unpair(lo[c4][4 * j + e]);
+                            v[2 * e] = fmaf(args.xc, __uint_as_float(acc[8 * j + 2 * e]), args.xa * fmaf(z.x, kLoInv, y.x));
+                            v[2 * e + 1] =
+                                fmaf(args.xc, __uint_as_float(acc[8 * j + 2 * e + 1]), args.xa * fmaf(z.y, kLoInv, y.y));
+                        }
+                        if (!last) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                o[e] = half_pair(v[2 * e], v[2 * e + 1]);
+                                const float2 h = half_unpair(o[e]);
+                                lo[c4][4 * j + e] = half_pair((v[2 * e] - h.x) * kLoScale, (v[2 * e + 1] - h.y) * kLoScale);
+                            }
+                            put_x(c, make_uint4(o[0], o[1], o[2], o[3]));
+                        } else if (row < m) {
+                            __nv_bfloat16 *out = args.out + (int64_t)b * m * n;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[e] *= args.out_scale;
+                            if (!tall && n % 8 == 0) {
+                                if (c < n) {
+                                    uint32_t z[4];
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+                                        z[e] = *reinterpret_cast<const uint32_t *>(&t);
+                                    }
+                                    *reinterpret_cast<uint4 *>(out + (int64_t)row * n + c) =
+                                        make_uint4(z[0], z[1], z[2], z[3]);
+                                }
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    if (c + e < n)
+                                        out[tall ? (int64_t)(c + e) * m + row : (int64_t)row * n + c + e] =
+                                            __float2bfloat16_rn(v[e]);
+                            }
+                        }
+                    }
+                }
+            }
+            if (!last) publish();
+        }
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    cluster_sync();  // neither CTA uses TMEM, or the other's memory, any more
+    ptx::tc_fence_after();
+    if (warp == kSmallWarps) pair_tmem_dealloc(tmem, kSmall);
+    cluster_sync();
+}
+
 // ---------------------------------------------------------------- host
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                               const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -1075,6 +1360,11 @@ cudaError_t ortho_init_device(int *pairs)
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(ortho_kernel<128, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  Cfg<128, 128>::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(ortho_small_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(ortho_small_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kSmallSmem);
     if (e != cudaSuccess) return e;
     // the pairs of CTAs that the device can hold at once
     cudaLaunchConfig_t cfg = {};
@@ -1092,6 +1382,17 @@ cudaError_t ortho_init_device(int *pairs)
 
 cudaError_t launch_orthogonalize(const OrthoCall &c, void *workspace, int pairs, cudaStream_t s)
 {
+    if (c.M <= kSmall && c.N <= kSmall) {
+        auto pow2 = [](int p) { return ldexpf(1.0f, p); };
+        const SmallArgs a{c.g, (int)c.M, (int)c.N, c.steps, c.eps, pow2(kABits - 2 * kXBits),
+                          c.b * pow2(kBBits - kABits), c.c * pow2(kBBits - 2 * kABits), c.a, pow2(-kBBits),
+                          c.out_scale * pow2(-kXBits), (__nv_bfloat16 *)c.out};
+        if (c.g_f32)
+            ortho_small_kernel<float><<<2 * (unsigned)c.B, kSmallThreads, kSmallSmem, s>>>(a);
+        else
+            ortho_small_kernel<__nv_bfloat16><<<2 * (unsigned)c.B, kSmallThreads, kSmallSmem, s>>>(a);
+        return cudaPeekAtLastError();
+    }
     const Region L = layout(c.B, c.M, c.N);
     char *ws = (char *)workspace;
     auto *partial = (float *)(ws + L.partial);

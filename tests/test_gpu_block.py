@@ -434,7 +434,8 @@ USUAL = (3.4445, -4.7750, 2.0315)
 
 @pytest.mark.parametrize("B,M,N", [(1, 1, 1), (2, 1, 40), (3, 5, 3), (1, 64, 64), (2, 65, 129), (3, 129, 65), (1, 256, 256),
                                    (2, 257, 300), (1, 300, 1000), (5, 31, 257), (1, 513, 512), (2, 768, 192),
-                                   (20, 48, 80), (1, 1100, 700), (70, 260, 300)])
+                                   (20, 48, 80), (1, 1100, 700), (70, 260, 300), (90, 200, 256), (200, 40, 300),
+                                   (300, 264, 8), (160, 130, 257), (1, 256, 257)])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_orthogonalize(B, M, N, dtype):
     g = randn(B, M, N, seed=M + N, std=1e-3, dtype=dtype)
