@@ -945,6 +945,8 @@ int moe_ffn_forward_routed(const void *x, const void *x_scale, const int32_t *to
     const moe::FusedMx mx{w_gate_up, w_gate_up_scale, w_down, w_down_scale};
     const bool mxw = w_gate_up_scale != nullptr;
     if (mxw && opts && opts->path == MOE_PATH_DECODE && T > kMxMaxTokens) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (opts && opts->path == MOE_PATH_GROUPED && !moe::gemm_supported((int)H, (int)I, (int)E))
+        return MOE_ERR_UNSUPPORTED_SHAPE;
     if (x_scale) {
         DeviceInfo *dev = nullptr;
         st = device_setup(&dev);

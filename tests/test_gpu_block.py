@@ -479,6 +479,30 @@ def test_orthogonalize_special_matrices():
     assert mb.moe_orthogonalize(g[:0]).shape == (0, 70, 90)
 
 
+@pytest.mark.parametrize("B,M,N", [(3, 300, 520), (2, 700, 300), (100, 30, 400), (5, 200, 100)])
+def test_orthogonalize_repeats_streams_graphs(B, M, N):
+    """The tiled products (one launch whose blocks wait on one another) and the small matrices."""
+    g, ws = randn(B, M, N, seed=1), mb.new_orthogonalize_workspace(B, M, N)
+    want = mb.moe_orthogonalize(g, workspace=ws)
+    for _ in range(5):
+        assert torch.equal(mb.moe_orthogonalize(g, workspace=ws), want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        again = mb.moe_orthogonalize(g, workspace=ws)
+    side.synchronize()
+    assert torch.equal(again, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = mb.moe_orthogonalize(g, workspace=ws)
+    g.copy_(randn(B, M, N, seed=2))
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    fresh = mb.moe_orthogonalize(g)
+    assert torch.equal(captured, fresh) and not torch.equal(fresh, want)
+
+
 # ------------------------------------------------------------------ streams, graphs, repeats
 def all_operators(s):
     """One call of each operator on the tensors of `s`, outputs allocated here."""
