@@ -511,7 +511,7 @@ __device__ __forceinline__ void down_rows_mx_na(int na, const uint8_t *const *ro
     }
 }
 
-// The router projection's inputs for the ROUTER instantiation: W_r [E][H]
+// The router projection's inputs for the kFromRouter instantiation: W_r [E][H]
 // BF16, the bias [E] (nullable), the tagged logit words [T*E] (16 bytes
 // each) and the caller's logits output (nullable).
 struct RouterArgs {
@@ -531,8 +531,10 @@ __device__ __forceinline__ unsigned long long mix64(unsigned long long z)
     return z ^ (z >> 31);
 }
 
-// ROUTER: the call passes the router weights instead of logits.  Before it
-// routes, CTA b computes the logits o = b, b + grid, ... of the T*E -- the
+// SOURCE says where the routing comes from, as a template parameter: a test
+// of the pointer in the kernel cost the one-token call 0.15 us of 18.3.
+// kFromRouter: the call passes the router weights instead of logits.  Before
+// it routes, CTA b computes the logits o = b, b + grid, ... of the T*E -- the
 // (logit, 256-element slice) pairs go round-robin over its warps
 // (router_slice_warp), one thread per logit then adds the slices in order
 // (router_logit_sum), the same arithmetic as the router kernel -- and
@@ -552,7 +554,9 @@ __device__ __forceinline__ unsigned long long mix64(unsigned long long z)
 // polls copy b % kLogitReplicas, so the grid's polls spread over that many
 // times more L2 lines (every CTA polls every logit, so one copy would draw
 // all of them to the same few lines).
-template <int NT, bool ROUTER, bool MX>
+enum : int { kFromLogits = 0, kFromRouter = 1, kGiven = 2 };
+
+template <int NT, int SOURCE, bool MX>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_fused_kernel(const uint16_t *__restrict__ x, const float *__restrict__ logits,
                         const uint16_t *__restrict__ wgu, const uint16_t *__restrict__ wd, int T, int H, int I, int E,
@@ -563,6 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float *__restrict__ out, int32_t *__restrict__ exchange_out, uint64_t wait_ns,
                         int mode, RouterArgs ra, MxArgs mx, Routing rt)
 {
+    constexpr bool ROUTER = SOURCE == kFromRouter, GIVEN = SOURCE == kGiven;
     static_assert(!(ROUTER && MX), "the router projection is built for BF16 weights only");
     extern __shared__ __align__(128) uint8_t sm[];
     const int A = T * k;
@@ -597,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The tokens' logits and x rows, which every CTA reads first, fetched
     // into L2 while the previous launch drains (whole 16-byte pieces only)
     if ((mode & kPrefetchInputs) && threadIdx.x == 0 && blockIdx.x < 2) {
-        const uint32_t n = blockIdx.x == 0 ? (ROUTER || rt.idx ? 0u : (uint32_t)(T * E * 4) & ~15u)
+        const uint32_t n = blockIdx.x == 0 ? (ROUTER || GIVEN ? 0u : (uint32_t)(T * E * 4) & ~15u)
                                            : (uint32_t)(T * H * 2);
         if (n) ptx::bulk_prefetch_l2(blockIdx.x == 0 ? (const void *)logits : (const void *)x, n);
     }
@@ -692,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int e;
         float wt;
         if (t == 0 && lane == 0) MOE_TL(56);
-        if (!ROUTER && rt.idx)  // the caller's routing
+        if constexpr (GIVEN)
             take_routing_warp(rt.idx + (int64_t)t * k, rt.w + (int64_t)t * k, E, k, e, wt);
         else
             route_token_warp<ROUTER>(logits + (int64_t)t * E, E, k, reinterpret_cast<float *>(sm) + (size_t)t * E, e,
@@ -1314,6 +1319,14 @@ size_t decode_fused_tag_words(int k, int I)
     return (size_t)a * I;
 }
 
+template <int SOURCE, bool MX>
+static auto pick_nt(int nt)
+{
+    return nt == 1   ? decode_fused_kernel<1, SOURCE, MX>
+           : nt == 2 ? decode_fused_kernel<2, SOURCE, MX>
+                     : decode_fused_kernel<4, SOURCE, MX>;
+}
+
 cudaError_t launch_decode_fused(const void *x, const float *logits, const void *wgu, const void *wd, int T, int H,
                                 int I, int E, int k, int n_sm, float *act, unsigned long long *act_tag,
                                 unsigned long long tag_cap, unsigned long long *flags, int32_t *idx_out, float *w_out,
@@ -1345,15 +1358,11 @@ cudaError_t launch_decode_fused(const void *x, const float *logits, const void *
     if (mxw)
         ma = MxArgs{(const uint8_t *)mxw->gq, (const uint8_t *)mxw->gs, (const uint8_t *)mxw->dq,
                     (const uint8_t *)mxw->ds, mx_scale_bytes(H), mx_scale_bytes(I)};
-    auto kern = router ? (p.nt == 1   ? decode_fused_kernel<1, true, false>
-                          : p.nt == 2 ? decode_fused_kernel<2, true, false>
-                                      : decode_fused_kernel<4, true, false>)
-                : mxw  ? (p.nt == 1   ? decode_fused_kernel<1, false, true>
-                          : p.nt == 2 ? decode_fused_kernel<2, false, true>
-                                      : decode_fused_kernel<4, false, true>)
-                       : (p.nt == 1   ? decode_fused_kernel<1, false, false>
-                          : p.nt == 2 ? decode_fused_kernel<2, false, false>
-                                      : decode_fused_kernel<4, false, false>);
+    auto kern = router              ? pick_nt<kFromRouter, false>(p.nt)
+                : mxw && routing    ? pick_nt<kGiven, true>(p.nt)
+                : mxw               ? pick_nt<kFromLogits, true>(p.nt)
+                : routing           ? pick_nt<kGiven, false>(p.nt)
+                                    : pick_nt<kFromLogits, false>(p.nt);
     return cudaLaunchKernelEx(&cfg, kern, (const uint16_t *)x, logits, (const uint16_t *)wgu, (const uint16_t *)wd, T,
                               H, I, E, k, p.slots, p.slot_bytes, p.rpc, p.rps, p.nh_max, p.act_in_smem, act, act_tag,
                               tag_cap, flags, epoch_salt(), idx_out, w_out, out, exchange_out, (uint64_t)wait_ns,
@@ -1388,15 +1397,12 @@ namespace moe {
 
 cudaError_t decode_fused_init_device()
 {
-    for (const void *kern :
-         {(const void *)decode_fused_kernel<1, false, false>, (const void *)decode_fused_kernel<2, false, false>,
-          (const void *)decode_fused_kernel<4, false, false>, (const void *)decode_fused_kernel<1, true, false>,
-          (const void *)decode_fused_kernel<2, true, false>, (const void *)decode_fused_kernel<4, true, false>,
-          (const void *)decode_fused_kernel<1, false, true>, (const void *)decode_fused_kernel<2, false, true>,
-          (const void *)decode_fused_kernel<4, false, true>}) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemCap);
-        if (e != cudaSuccess) return e;
-    }
+    for (int nt : {1, 2, 4})
+        for (auto kern : {pick_nt<kFromLogits, false>(nt), pick_nt<kFromRouter, false>(nt),
+                          pick_nt<kGiven, false>(nt), pick_nt<kFromLogits, true>(nt), pick_nt<kGiven, true>(nt)}) {
+            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemCap);
+            if (e != cudaSuccess) return e;
+        }
     return cudaSuccess;
 }
 

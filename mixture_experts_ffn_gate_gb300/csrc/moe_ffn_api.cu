@@ -442,7 +442,7 @@ int run_backward(const void *x, const float *logits, const void *wgu, const void
     MOE_TRY(stg.done(moe::launch_bwd_dx(ws + L.dgu_hi, ws + L.dgu_lo, wgu, chunks, nchunks, offs, rows, H, I, E, z,
                                         ctas, stream, dgu_lo2)));
     MOE_TRY(stg.done(moe::launch_combine(z, nullptr, pos, T, H, k, dx, dev->n_sm, stream)));
-    MOE_TRY(stg.done(moe::launch_zero_untouched(counts, E, H, I, dwgu, dwd, dev->n_sm, stream)));
+    MOE_TRY(stg.done(moe::launch_zero_untouched(counts, E, H, I, dwgu, dwd, stream)));
     MOE_TRY(stg.done(moe::launch_wgrad_down(ws + L.ds_hi, ws + L.ds_lo, ws + L.wa_hi, ws + L.wa_lo, offs, counts,
                                             rows, H, I, E, dwd, ctas, stream, ds_lo2, wa_lo2)));
     MOE_TRY(stg.done(moe::launch_wgrad_gate_up(ws + L.dgu_hi, ws + L.dgu_lo, ws + L.xs, offs, counts, rows, H, I, E,
