@@ -426,6 +426,71 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint16_t *__restric
     }
 }
 
+// ---------------------------------------------------------------- SwiGLU backward
+// Three BF16 terms of four FP32 values.
+__device__ __forceinline__ void store_terms4(void *hi, void *lo, void *lo2, int64_t at, const float (&v)[4])
+{
+    __align__(8) __nv_bfloat16 t[3][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        t[0][j] = __float2bfloat16_rn(v[j]);
+        const float r = v[j] - __bfloat162float(t[0][j]);
+        t[1][j] = __float2bfloat16_rn(r);
+        t[2][j] = __float2bfloat16_rn(r - __bfloat162float(t[1][j]));
+    }
+    reinterpret_cast<uint2 *>(hi)[at / 4] = *reinterpret_cast<const uint2 *>(t[0]);
+    reinterpret_cast<uint2 *>(lo)[at / 4] = *reinterpret_cast<const uint2 *>(t[1]);
+    reinterpret_cast<uint2 *>(lo2)[at / 4] = *reinterpret_cast<const uint2 *>(t[2]);
+}
+
+// Four neurons of one (padded) sorted row per thread, from q = W_down^T dout:
+//   s = sigmoid(g), a = g s u, da = w q,
+//   dg = da u s (1 + g (1 - s)), du = da g s,
+// in three terms each (dgu rows: dg at i, du at I + i; wa = w a), zeros in the
+// experts' pad rows; and a . q summed over 32 neurons into dwp.  A kernel of
+// its own: in the q product's epilogue, whose warps also add up the segments,
+// its loads and nine stores per value took 63 us that nothing overlapped
+// (512 tokens, H = 2048, I = 768, E = 128: q 145 us, so 80 + 21).
+__global__ void __launch_bounds__(256) bwd_swiglu_kernel(const float *__restrict__ q, const float *__restrict__ g,
+                                                         const float *__restrict__ u, const float *__restrict__ w_s,
+                                                         const int32_t *__restrict__ perm,
+                                                         const int32_t *__restrict__ offs, int E, int I,
+                                                         const BwdTerms o, float *__restrict__ dwp)
+{
+    const int quads = I / 4;
+    const int64_t n = (int64_t)__ldg(offs + E) * quads;  // a multiple of 16: eight lanes share 32 neurons of a row
+    for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < n; c += (int64_t)gridDim.x * 256) {
+        const int r = (int)(c / quads), i = 4 * (int)(c - (int64_t)r * quads);
+        float dg[4] = {0.f, 0.f, 0.f, 0.f}, du[4] = {0.f, 0.f, 0.f, 0.f}, wa[4] = {0.f, 0.f, 0.f, 0.f}, p = 0.0f;
+        if (__ldg(perm + r) >= 0) {
+            const float4 q4 = __ldg(reinterpret_cast<const float4 *>(q) + c);
+            const float4 g4 = __ldg(reinterpret_cast<const float4 *>(g) + c);
+            const float4 u4 = __ldg(reinterpret_cast<const float4 *>(u) + c);
+            const float w = __ldg(w_s + r);
+            const float qv[4] = {q4.x, q4.y, q4.z, q4.w}, gv[4] = {g4.x, g4.y, g4.z, g4.w},
+                        uv[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float sg = 1.0f / (1.0f + expf(-gv[j]));
+                const float silu = gv[j] * sg;
+                const float a = silu * uv[j];
+                const float da = w * qv[j];
+                dg[j] = da * uv[j] * (sg * (1.0f + gv[j] * (1.0f - sg)));
+                du[j] = da * silu;
+                wa[j] = w * a;
+                p += a * qv[j];
+            }
+        }
+        store_terms4(o.dgu_hi, o.dgu_lo, o.dgu_lo2, (int64_t)r * 2 * I + i, dg);
+        store_terms4(o.dgu_hi, o.dgu_lo, o.dgu_lo2, (int64_t)r * 2 * I + I + i, du);
+        store_terms4(o.wa_hi, o.wa_lo, o.wa_lo2, (int64_t)r * I + i, wa);
+        const unsigned eight = 0xffu << (threadIdx.x & 24);
+#pragma unroll
+        for (int d = 4; d >= 1; d >>= 1) p += __shfl_xor_sync(eight, p, d);
+        if ((threadIdx.x & 7) == 0) dwp[(int64_t)r * (I / 32) + i / 32] = p;
+    }
+}
+
 // ---------------------------------------------------------------- zeros
 // The weight gradients of the experts no row selects are zero.  One block
 // per expert (blockIdx.y) and about 1 MB of its gradients: where counts[e] is
@@ -601,6 +666,16 @@ cudaError_t launch_bwd_prep(const void *x, const float *dout, const float *w, co
     bwd_prep_kernel<<<grid, 256, 0, s>>>((const uint16_t *)x, dout, w, perm, offs, E, H, k, (uint16_t *)xs,
                                          (__nv_bfloat16 *)ds_hi, (__nv_bfloat16 *)ds_lo, (__nv_bfloat16 *)ds_lo2,
                                          w_s);
+    return cudaPeekAtLastError();
+}
+
+cudaError_t launch_bwd_swiglu(const float *q, const float *g, const float *u, const float *w_s, const int32_t *perm,
+                              const int32_t *offs, int n_rows_max, int E, int I, const BwdTerms &o, float *dwp,
+                              int n_sm, cudaStream_t s)
+{
+    const int64_t blocks = ceil_div((int64_t)n_rows_max * (I / 4), (int64_t)256);
+    const int grid = (int)(blocks < 8 * n_sm ? blocks : 8 * n_sm);
+    bwd_swiglu_kernel<<<grid, 256, 0, s>>>(q, g, u, w_s, perm, offs, E, I, o, dwp);
     return cudaPeekAtLastError();
 }
 

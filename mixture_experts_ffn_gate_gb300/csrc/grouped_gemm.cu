@@ -175,7 +175,6 @@ struct BwdQArgs {
     const float *g, *u, *w_s;
     __nv_bfloat16 *dgu_hi, *dgu_lo, *wa_hi, *wa_lo;
     float *dwp;
-    __nv_bfloat16 *dgu_lo2, *wa_lo2;  // SEG
 };
 
 struct GemmArgs {
@@ -224,17 +223,6 @@ __device__ __forceinline__ void store_pair(__nv_bfloat16 *hi, __nv_bfloat16 *lo,
     const __nv_bfloat16 h = __float2bfloat16_rn(v);
     hi[at] = h;
     lo[at] = __float2bfloat16_rn(v - __bfloat162float(h));
-}
-
-// Three BF16 terms of an FP32 value.
-__device__ __forceinline__ void store_terms(__nv_bfloat16 *hi, __nv_bfloat16 *lo, __nv_bfloat16 *lo2, int at, float v)
-{
-    const __nv_bfloat16 h = __float2bfloat16_rn(v);
-    const float r = v - __bfloat162float(h);
-    const __nv_bfloat16 l = __float2bfloat16_rn(r);
-    hi[at] = h;
-    lo[at] = l;
-    lo2[at] = __float2bfloat16_rn(r - __bfloat162float(l));
 }
 
 // After this, lane l holds the sum over the warp's 32 lanes of v[l] (a
@@ -313,69 +301,6 @@ __device__ __forceinline__ void bwd_q_columns(const uint32_t (&r)[32], int ncols
     }
     const float sum = warp_column_sums(prod, lane);
     if (lane < ncols && c0 + lane < n) b.dwp[(int64_t)(p0 + c0 + lane) * (I / 32) + grp] = sum;
-}
-
-// The same with three terms per value (SEG), eight columns at a time: the
-// warp also holds the item's 64 sums, and with all 32 columns' operands in
-// registers beside them the loads went one after the other (q took 170 us
-// instead of 145 at 512 tokens, H = 2048, I = 768, E = 128).  The next
-// eight columns' loads are issued before this one's stores.
-__device__ __forceinline__ void bwd_q_columns_terms(const uint32_t (&r)[32], int p0, int n, int c0, int i, int grp,
-                                                    const GemmArgs &args, int lane)
-{
-    const int I = args.I, npad = pad16(n);
-    const BwdQArgs &b = args.q;
-    // the block's first row; the rest are 32-bit offsets from it
-    const int64_t at = (int64_t)(p0 + c0) * I + i, at2 = at + (int64_t)(p0 + c0) * I;
-    const float *const g0 = b.g + at, *const u0 = b.u + at, *const w0 = b.w_s + p0 + c0;
-    __nv_bfloat16 *const d_hi = b.dgu_hi + at2, *const d_lo = b.dgu_lo + at2, *const d_lo2 = b.dgu_lo2 + at2;
-    __nv_bfloat16 *const a_hi = b.wa_hi + at, *const a_lo = b.wa_lo + at, *const a_lo2 = b.wa_lo2 + at;
-    float gv[2][8], uv[2][8], wv[2][8];
-    auto load = [&](int h, int buf) {
-#pragma unroll
-        for (int jj = 0; jj < 8; ++jj) {
-            const int j = 8 * h + jj;
-            const bool live = c0 + j < n;
-            gv[buf][jj] = live ? __ldg(g0 + j * I) : 0.0f;
-            uv[buf][jj] = live ? __ldg(u0 + j * I) : 0.0f;
-            wv[buf][jj] = live ? __ldg(w0 + j) : 0.0f;
-        }
-    };
-    load(0, 0);
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-        if (c0 + 8 * h >= npad) break;
-        if (h < 3) load(h + 1, (h + 1) & 1);
-        float prod[8];
-#pragma unroll
-        for (int jj = 0; jj < 8; ++jj) {
-            const int col = c0 + 8 * h + jj;
-            prod[jj] = 0.0f;
-            if (col < npad) {
-                float dg = 0.0f, du = 0.0f, wa = 0.0f;
-                if (col < n) {
-                    const float qv = __uint_as_float(r[8 * h + jj]);
-                    const float g = gv[h & 1][jj], u = uv[h & 1][jj], w = wv[h & 1][jj];
-                    const float sg = 1.0f / (1.0f + expf(-g));
-                    const float silu = g * sg;
-                    const float a = silu * u;
-                    const float da = w * qv;
-                    dg = da * u * (sg * (1.0f + g * (1.0f - sg)));
-                    du = da * silu;
-                    wa = w * a;
-                    prod[jj] = a * qv;
-                }
-                const int j = 8 * h + jj;
-                store_terms(d_hi, d_lo, d_lo2, j * 2 * I, dg);
-                store_terms(d_hi, d_lo, d_lo2, j * 2 * I + I, du);
-                store_terms(a_hi, a_lo, a_lo2, j * I, wa);
-            }
-        }
-        // the sum of column s ends in lanes 4 s ..
-        const float sum = warp_sum_split<8>(prod, lane);
-        const int col = c0 + 8 * h + (lane >> 2);
-        if ((lane & 3) == 0 && col < n) b.dwp[(int64_t)(p0 + col) * (I / 32) + grp] = sum;
-    }
 }
 
 template <int KIND, bool SEG = false>
@@ -766,11 +691,17 @@ __global__ void __launch_bounds__(Cfg<KIND, SEG>::THREADS, 1)
                                 for (int j = 0; j < 32; ++j)
                                     if (c0 + j < it.n) dst[(int64_t)(it.p0 + c0 + j) * args.I + neuron] = __uint_as_float(r[j]);
                             } else if constexpr (KIND == kBwdQ) {
-                if constexpr (SEG)
-                    bwd_q_columns_terms(r, it.p0, it.n, c0, tile * BM + 32 * q + lane, tile * 4 + q, args, lane);
-                else
+                if constexpr (SEG) {
+                    // q itself: bwd_swiglu_kernel takes it from there
+                    const int i = tile * BM + 32 * q + lane;
+                    float *dst = reinterpret_cast<float *>(args.out0);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (c0 + j < it.n) dst[(int64_t)(it.p0 + c0 + j) * args.I + i] = __uint_as_float(r[j]);
+                } else {
                     bwd_q_columns(r, it.n > SMALL_ROWS ? 32 : SMALL_ROWS, it.p0, it.n, c0, tile * BM + 32 * q + lane,
                                   tile * 4 + q, args, lane);
+                }
                             } else if constexpr (KIND == kGateUp || KIND == kGateUpMx || KIND == kGateUpSave) {
                                 const int neuron = tile * 64 + 16 * q + (lane & 15);
                                 __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(lane < 16 ? args.out0 : args.out1);
@@ -1194,17 +1125,26 @@ cudaError_t launch_gemm_gate_up_keep(const void *x, const int32_t *perm, int k, 
 
 cudaError_t launch_bwd_q(const void *ds_hi, const void *ds_lo, const void *wd, const int4 *chunks,
                          const int32_t *nchunks, const int32_t *offs, int n_rows, int H, int I, int E,
-                         const BwdQOut &o, int ctas, cudaStream_t s, const void *ds_lo2)
+                         const BwdQOut &o, int ctas, cudaStream_t s)
+{
+    CUtensorMap tA, tB[6];
+    cudaError_t e = make_mn_map(&tA, wd, I, H, E);
+    if (e == cudaSuccess) e = make_term_maps(tB, ds_hi, ds_lo, nullptr, n_rows, H);
+    if (e != cudaSuccess) return e;
+    const BwdQArgs q{o.g, o.u, o.w_s, (__nv_bfloat16 *)o.dgu_hi, (__nv_bfloat16 *)o.dgu_lo,
+                     (__nv_bfloat16 *)o.wa_hi, (__nv_bfloat16 *)o.wa_lo, o.dwp};
+    return launch_mn<kBwdQ, false>(tA, tB, chunks, nchunks, offs, n_rows, H, I, E, I, H, nullptr, q, ctas, s);
+}
+
+cudaError_t launch_bwd_q_sums(const void *ds_hi, const void *ds_lo, const void *ds_lo2, const void *wd,
+                              const int4 *chunks, const int32_t *nchunks, const int32_t *offs, int n_rows, int H,
+                              int I, int E, float *q, int ctas, cudaStream_t s)
 {
     CUtensorMap tA, tB[6];
     cudaError_t e = make_mn_map(&tA, wd, I, H, E);
     if (e == cudaSuccess) e = make_term_maps(tB, ds_hi, ds_lo, ds_lo2, n_rows, H);
     if (e != cudaSuccess) return e;
-    const BwdQArgs q{o.g, o.u, o.w_s, (__nv_bfloat16 *)o.dgu_hi, (__nv_bfloat16 *)o.dgu_lo,
-                     (__nv_bfloat16 *)o.wa_hi, (__nv_bfloat16 *)o.wa_lo, o.dwp,
-                     (__nv_bfloat16 *)o.dgu_lo2, (__nv_bfloat16 *)o.wa_lo2};
-    auto f = ds_lo2 ? launch_mn<kBwdQ, true> : launch_mn<kBwdQ, false>;
-    return f(tA, tB, chunks, nchunks, offs, n_rows, H, I, E, I, H, nullptr, q, ctas, s);
+    return launch_mn<kBwdQ, true>(tA, tB, chunks, nchunks, offs, n_rows, H, I, E, I, H, q, BwdQArgs{}, ctas, s);
 }
 
 cudaError_t launch_bwd_dx(const void *dgu_hi, const void *dgu_lo, const void *wgu, const int4 *chunks,

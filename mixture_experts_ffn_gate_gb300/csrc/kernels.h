@@ -155,11 +155,14 @@ struct BwdQOut {
     const float *g, *u, *w_s;
     void *dgu_hi, *dgu_lo, *wa_hi, *wa_lo;
     float *dwp;
-    void *dgu_lo2, *wa_lo2;  // with ds_lo2
 };
 cudaError_t launch_bwd_q(const void *ds_hi, const void *ds_lo, const void *wd, const int4 *chunks,
                          const int32_t *nchunks, const int32_t *offs, int n_rows, int H, int I, int E,
-                         const BwdQOut &o, int ctas, cudaStream_t s, const void *ds_lo2 = nullptr);
+                         const BwdQOut &o, int ctas, cudaStream_t s);
+// q [rows][I] alone, of dout in three terms: launch_bwd_swiglu goes on from it
+cudaError_t launch_bwd_q_sums(const void *ds_hi, const void *ds_lo, const void *ds_lo2, const void *wd,
+                              const int4 *chunks, const int32_t *nchunks, const int32_t *offs, int n_rows, int H,
+                              int I, int E, float *q, int ctas, cudaStream_t s);
 // z [rows][H] = W_gate_up^T (dgu_hi + dgu_lo)
 cudaError_t launch_bwd_dx(const void *dgu_hi, const void *dgu_lo, const void *wgu, const int4 *chunks,
                           const int32_t *nchunks, const int32_t *offs, int n_rows, int H, int I, int E, float *z,
@@ -173,6 +176,14 @@ cudaError_t read_bwd_fault_word(uint32_t *flags, bool clear);
 cudaError_t launch_bwd_prep(const void *x, const float *dout, const float *w, const int32_t *perm,
                             const int32_t *offs, int n_rows_max, int E, int H, int k, void *xs, void *ds_hi,
                             void *ds_lo, float *w_s, int n_sm, cudaStream_t s, void *ds_lo2 = nullptr);
+// the SwiGLU backward from q, g, u [rows][I] and w_s: dgu [rows][2I] and wa
+// [rows][I] in three BF16 terms, dwp [rows][I/32] as launch_bwd_q's
+struct BwdTerms {
+    void *dgu_hi, *dgu_lo, *dgu_lo2, *wa_hi, *wa_lo, *wa_lo2;
+};
+cudaError_t launch_bwd_swiglu(const float *q, const float *g, const float *u, const float *w_s, const int32_t *perm,
+                              const int32_t *offs, int n_rows_max, int E, int I, const BwdTerms &o, float *dwp,
+                              int n_sm, cudaStream_t s);
 // dW_down [E][H][I] = sum_r ds[r] (x) wa[r] over each expert's rows
 cudaError_t launch_wgrad_down(const void *ds_hi, const void *ds_lo, const void *wa_hi, const void *wa_lo,
                               const int32_t *offs, const int32_t *counts, int n_rows, int H, int I, int E,

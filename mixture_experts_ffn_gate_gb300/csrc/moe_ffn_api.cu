@@ -341,8 +341,9 @@ int run_forward(const void *x, const float *logits, const void *wgu, const void 
 struct BwdLayout {
     size_t flags, idx, w, offs, perm, pos, uexp, ucount, chunks, nchunks, counts;
     size_t xs, ds_hi, ds_lo, w_s, g, u, dgu_hi, dgu_lo, wa_hi, wa_lo, dwp, z, total;
-    // the third terms of the calls that take the routing, after everything else
-    size_t ds_lo2, dgu_lo2, wa_lo2, routed_total;
+    // of the calls that take the routing, after everything else: the third
+    // terms, and q [rows][I] f32 (in z, which dx writes later, where it fits)
+    size_t ds_lo2, dgu_lo2, wa_lo2, q, routed_total;
     int64_t rows;
 };
 
@@ -385,6 +386,7 @@ BwdLayout make_bwd_layout(const Shape &s)
     L.ds_lo2 = take(R * (size_t)s.H * 2);
     L.dgu_lo2 = take(R * (size_t)s.I * 4);
     L.wa_lo2 = take(R * (size_t)s.I * 2);
+    L.q = s.I <= s.H ? L.z : take(R * (size_t)s.I * 4);
     L.routed_total = o;
     return L;
 }
@@ -435,10 +437,17 @@ int run_backward(const void *x, const float *logits, const void *wgu, const void
     if (recompute)
         MOE_TRY(stg.done(moe::launch_gemm_gate_up_raw(x, perm, k, wgu, chunks, nchunks, offs, rows, H, I, E, g, u,
                                                       ctas, stream, seg)));
-    const moe::BwdQOut qo{g, u, w_s, ws + L.dgu_hi, ws + L.dgu_lo, ws + L.wa_hi, ws + L.wa_lo, dwp,
-                          dgu_lo2, wa_lo2};
-    MOE_TRY(stg.done(moe::launch_bwd_q(ws + L.ds_hi, ws + L.ds_lo, wd, chunks, nchunks, offs, rows, H, I, E, qo, ctas,
-                                       stream, ds_lo2)));
+    if (seg) {
+        auto *q = (float *)(ws + L.q);
+        const moe::BwdTerms o{ws + L.dgu_hi, ws + L.dgu_lo, dgu_lo2, ws + L.wa_hi, ws + L.wa_lo, wa_lo2};
+        MOE_TRY(moe::launch_bwd_q_sums(ws + L.ds_hi, ws + L.ds_lo, ds_lo2, wd, chunks, nchunks, offs, rows, H, I, E, q,
+                                       ctas, stream));
+        MOE_TRY(stg.done(moe::launch_bwd_swiglu(q, g, u, w_s, perm, offs, rows, E, I, o, dwp, dev->n_sm, stream)));
+    } else {
+        const moe::BwdQOut qo{g, u, w_s, ws + L.dgu_hi, ws + L.dgu_lo, ws + L.wa_hi, ws + L.wa_lo, dwp};
+        MOE_TRY(stg.done(moe::launch_bwd_q(ws + L.ds_hi, ws + L.ds_lo, wd, chunks, nchunks, offs, rows, H, I, E, qo,
+                                           ctas, stream)));
+    }
     MOE_TRY(stg.done(moe::launch_bwd_dx(ws + L.dgu_hi, ws + L.dgu_lo, wgu, chunks, nchunks, offs, rows, H, I, E, z,
                                         ctas, stream, dgu_lo2)));
     MOE_TRY(stg.done(moe::launch_combine(z, nullptr, pos, T, H, k, dx, dev->n_sm, stream)));
