@@ -9,29 +9,43 @@
 //
 // One warp per token.  Lane q owns the PER consecutive experts q PER ..., as
 // 32-bit keys in the order of c, and sorts its (at most) 8 largest once (a
-// sorting network on key and index); the list waits in shared memory, its
-// head in registers.  A round of the selection is one warp maximum of the
-// heads (redux); on equal keys the lowest lane that has it holds the lowest
-// index, so the 32-bit keys decide (the router of the expert layer, whose
-// lanes own experts 32 apart, compares 64 bits), and that lane pops its list.
+// sorting network of minima and maxima on the keys alone); the list waits in
+// shared memory, its head in a register.  A round of the selection is one
+// warp maximum of the heads (redux); on equal keys the lowest lane that has
+// it holds the lowest index, and that lane moves on in its list.  Which
+// expert a chosen key belongs to is looked up afterwards, by lane j for round
+// j, among the owner's keys in shared memory: carrying the index through the
+// sort took twice its instructions.
 //
 // The bytes (4 E per token in, 8 k out) would take 2.6 us for 16384 tokens of
 // 256 experts at the copy rate; the instructions bound it (the scores' exp
-// and division, the sort, k rounds).
+// and reciprocal, the sort, k rounds).  Measured there with sigmoid scores, a
+// bias, 4 of 8 groups and k = 8: 15.2 us (13.9 without the counts); softmax scores without a
+// bias: 9.1.
 #include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
 #include "route_block.cuh"
+#include "sm100_ptx.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kGateWarps = 8;
+constexpr int kGradWarps = 8;
 // up to this many tokens run as one block, which owns the counts (no zeroing
 // before it, no atomics to global memory)
-constexpr int kGateOneBlock = kGateWarps;
+constexpr int kGateOneBlock = 8;
+
+// Warps per block and blocks per SM: what the registers of a lane's PER
+// experts let an SM hold, in few blocks, because each adds its counts to the
+// same E words at the end (16384 tokens, 256 experts: 15.2 us with 2 blocks
+// of 16 warps, 17.7 with 4 of 8).
+template <int PER>
+struct GateShape {
+    static constexpr int WARPS = PER <= 8 ? 16 : 8, BLOCKS = PER <= 8 || PER > 16 ? 2 : 3;
+};
 constexpr int kList = 8;  // sorted keys per lane
 
 struct GateArgs {
@@ -43,6 +57,7 @@ struct GateArgs {
     int32_t *idx;
     float *w;
     int32_t *counts;
+    bool wait_late;  // the launch before this one only zeroes counts
 };
 
 // logit_key in three instructions: adding +0 turns -0 into +0 and every NaN
@@ -53,20 +68,89 @@ __device__ __forceinline__ uint32_t gate_key(float f)
     return (uint32_t)(b ^ ((b >> 31) | (int)0x80000000));
 }
 
+// a >= b afterwards
+__device__ __forceinline__ void order_desc(uint32_t &a, uint32_t &b)
+{
+    const uint32_t hi = max(a, b);
+    b = min(a, b);
+    a = hi;
+}
+
+// 8 keys in descending order: 19 comparators, depth 6
+__device__ __forceinline__ void sort8_desc(uint32_t (&x)[8])
+{
+    constexpr int pairs[19][2] = {{0, 2}, {1, 3}, {4, 6}, {5, 7}, {0, 4}, {1, 5}, {2, 6}, {3, 7}, {0, 1}, {2, 3},
+                                  {4, 5}, {6, 7}, {2, 4}, {3, 5}, {1, 4}, {3, 6}, {1, 2}, {3, 4}, {5, 6}};
+#pragma unroll
+    for (int i = 0; i < 19; ++i) order_desc(x[pairs[i][0]], x[pairs[i][1]]);
+}
+
 // The 8 largest of two descending lists, into `list`: the larger of each
 // list[q], x[7 - q] pair form a bitonic sequence, sorted by half-cleaners.
-__device__ __forceinline__ void merge8_desc(unsigned long long (&list)[8], const unsigned long long (&x)[8])
+__device__ __forceinline__ void merge8_desc(uint32_t (&list)[8], const uint32_t (&x)[8])
 {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) list[q] = list[q] > x[7 - q] ? list[q] : x[7 - q];
+    for (int q = 0; q < 8; ++q) list[q] = max(list[q], x[7 - q]);
 #pragma unroll
     for (int d = 4; d >= 1; d >>= 1)
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-            if (!(q & d)) key_order(list[q], list[q + d]);
+            if (!(q & d)) order_desc(list[q], list[q + d]);
+}
+
+// N words to and from shared memory (16 bytes at a time where N allows)
+template <int N>
+__device__ __forceinline__ void put_words(uint32_t *dst, const uint32_t *v)
+{
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            *reinterpret_cast<uint4 *>(dst + i) = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) dst[i] = v[i];
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void get_words(uint32_t *v, const uint32_t *src)
+{
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(src + i);
+            v[i] = w.x, v[i + 1] = w.y, v[i + 2] = w.z, v[i + 3] = w.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = src[i];
+    }
 }
 
 __device__ __forceinline__ float sigmoid_of(float l) { return 1.0f / (1.0f + expf(-l)); }
+
+// The same bits for N values: the reciprocal of x = 1 + exp(-l) is the
+// hardware's approximation and one Newton step, r + r (1 - x r) in fused
+// multiply-adds, which rounds correctly for every significand (tested against
+// the division); no branch per value, as the division has.  Beyond 2^126 the
+// reciprocal is subnormal and takes the division.
+template <int N>
+__device__ __forceinline__ void sigmoids(const float (&l)[N], float (&s)[N])
+{
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float x = 1.0f + expf(-l[i]);
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+        s[i] = __fmaf_rn(r, __fmaf_rn(-x, r, 1.0f), r);
+        top = fmaxf(top, x);
+    }
+    if (top >= 0x1p126f) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = sigmoid_of(l[i]);
+    }
+}
 
 // exp(l - top), zero for a logit of -inf (also where top is -inf)
 __device__ __forceinline__ float exp_below(float l, float top)
@@ -122,29 +206,36 @@ __device__ __forceinline__ void top2_merge(uint32_t &m1, uint32_t &m2, uint32_t 
 }
 
 template <int PER>
-__global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
+__global__ void __launch_bounds__(32 * GateShape<PER>::WARPS, GateShape<PER>::BLOCKS) gate_kernel(const GateArgs a)
 {
-    constexpr bool AHEAD = PER <= 12;  // the next token's logits are loaded before this one's are used
+    constexpr int WARPS = GateShape<PER>::WARPS;
+    constexpr bool KEEP_BIAS = PER <= 12;  // the lane's biases stay in registers
+    constexpr int LIST = PER < kList ? PER : kList;
+    // words per lane: rows of 16-byte pieces start in different banks (of 8
+    // and 32 keys some meet, which leaves room for the warps)
+    constexpr int KEYS = PER == 16 ? PER + 4 : PER, ROW = 12;
+    static_assert(4 * 32 * WARPS * (KEYS + ROW) + 4 * 32 * PER <= 48 * 1024, "shared memory");
     extern __shared__ int32_t hist[];  // [E], with counts
-    __shared__ unsigned long long lists[kGateWarps][kList][32];
-    __shared__ unsigned long long chosen[kGateWarps][32];
+    __shared__ __align__(16) uint32_t keys[WARPS][32 * KEYS];  // by expert
+    __shared__ __align__(16) uint32_t lists[WARPS][32 * ROW];  // sorted, then a 0
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int E = a.E, k = a.k, e0 = lane * PER;
+    const unsigned lower = (1u << lane) - 1u;
+    uint32_t *const my_list = lists[warp] + lane * ROW, *const my_keys = keys[warp] + lane * KEYS;
+    my_list[LIST] = 0;
     if (a.counts) {
         for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
         __syncthreads();
     }
+    float bias[PER];
+    if (KEEP_BIAS)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) bias[i] = a.bias && e0 + i < E ? __ldg(a.bias + e0 + i) : 0.0f;
+    if (!a.wait_late) ptx::griddep_wait();
     const int64_t stride = (int64_t)gridDim.x * (blockDim.x >> 5);
-    int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
-    float l[PER];
-    if (AHEAD && t < a.T) load_logits<PER>(a.logits + t * E, E, l);
-    for (; t < a.T; t += stride) {
-        float ln[PER];
-        if (AHEAD) {
-            if (t + stride < a.T) load_logits<PER>(a.logits + (t + stride) * E, E, ln);
-        } else {
-            load_logits<PER>(a.logits + t * E, E, l);
-        }
+    for (int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp; t < a.T; t += stride) {
+        float l[PER];
+        load_logits<PER>(a.logits + t * E, E, l);
         // the row's maximum and sum, where the scores themselves are needed
         float top = 0.0f, total = 1.0f;
         if (!a.sigmoid && (a.bias || !a.renorm)) {
@@ -160,17 +251,23 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
         uint32_t key[PER];
         if (!a.bias) {
 #pragma unroll
-            for (int i = 0; i < PER; ++i) key[i] = e0 + i < E ? gate_key(l[i]) : 0u;
+            for (int i = 0; i < PER; ++i) key[i] = gate_key(l[i]);
         } else {
+            float c[PER];
+            if (a.sigmoid) {
+                sigmoids(l, c);
+            } else {
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                float s;
-                if (a.sigmoid)
-                    s = sigmoid_of(l[i]);
-                else
-                    s = total > 0.0f ? exp_below(l[i], top) / total : 0.0f;
-                key[i] = e0 + i < E ? gate_key(s + __ldg(a.bias + e0 + i)) : 0u;
+                for (int i = 0; i < PER; ++i) c[i] = total > 0.0f ? exp_below(l[i], top) / total : 0.0f;
             }
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                key[i] = gate_key(c[i] + (KEEP_BIAS ? bias[i] : e0 + i < E ? __ldg(a.bias + e0 + i) : 0.0f));
+        }
+        if (E < 32 * PER) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (e0 + i >= E) key[i] = 0;
         }
         // groups that are a power of two of neighbouring lanes are ranked
         // from the lanes' lists, others from the keys
@@ -178,12 +275,14 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
         const bool whole = lanes * PER == size && (lanes & (lanes - 1)) == 0;
         uint32_t kept = 0;
         auto keep_best = [&](uint32_t rank) {  // lane g holds the rank of group g
+            bool in = false;
+            rank = lane < a.groups ? rank : 0u;
             for (int r = 0; r < a.topk_groups; ++r) {
-                const uint32_t m = __reduce_max_sync(0xffffffffu, lane < a.groups ? rank : 0u);
-                const int g = __ffs(__ballot_sync(0xffffffffu, rank == m && lane < a.groups)) - 1;
-                kept |= 1u << g;
-                if (lane == g) rank = 0;
+                const uint32_t m = __reduce_max_sync(0xffffffffu, rank);
+                const unsigned b = __ballot_sync(0xffffffffu, rank == m);
+                if (rank == m && (b & lower) == 0) in = true, rank = 0;
             }
+            kept = __ballot_sync(0xffffffffu, in);
         };
         auto rank_of = [&](uint32_t m1, uint32_t m2) {
             return a.bias && size > 1 ? gate_key(key_logit(m1) + key_logit(m2)) : m1;
@@ -205,20 +304,15 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
             for (int i = 0; i < PER; ++i)
                 if (e0 + i < E && !(kept >> ((unsigned)(e0 + i) / (unsigned)size) & 1)) key[i] = 0;
         }
-        // the lane's list: (key, ~index), so that the lower index is the larger
-        unsigned long long list[kList];
+        put_words<PER>(my_keys, key);
+        uint32_t list[kList];
 #pragma unroll
         for (int c = 0; c < (PER + 7) / 8; ++c) {
-            unsigned long long x[8];
+            uint32_t x[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const int i = 8 * c + q;
-                x[q] = i < PER && key[i < PER ? i : 0]
-                           ? ((unsigned long long)key[i < PER ? i : 0] << 32) | (uint32_t)~(uint32_t)(e0 + i)
-                           : 0ull;
-            }
+            for (int q = 0; q < 8; ++q) x[q] = 8 * c + q < PER ? key[8 * c + q < PER ? 8 * c + q : 0] : 0u;
             if (PER == 2)
-                key_order(x[0], x[1]);
+                order_desc(x[0], x[1]);
             else if (PER > 2)
                 sort8_desc(x);
             if (c == 0) {
@@ -228,56 +322,76 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
                 merge8_desc(list, x);
             }
         }
-        unsigned long long head = list[0];
+        put_words<LIST>(my_list, list);
+        uint32_t head = list[0];
         if (a.groups > 1 && whole) {
-            uint32_t m1 = (uint32_t)(list[0] >> 32), m2 = (uint32_t)(list[1] >> 32);
+            uint32_t m1 = list[0], m2 = list[1];
             for (int o = 1; o < lanes; o <<= 1)
                 top2_merge(m1, m2, __shfl_xor_sync(0xffffffffu, m1, o), __shfl_xor_sync(0xffffffffu, m2, o));
             keep_best(__shfl_sync(0xffffffffu, rank_of(m1, m2), (lane * lanes) & 31));
             if (!(kept >> (lane / lanes) & 1)) head = 0;
         }
-#pragma unroll
-        for (int q = 1; q < (PER < kList ? PER : kList); ++q) lists[warp][q][lane] = list[q];
         // k rounds (the experts that stay are at least k, so no round comes to
-        // a head of 0)
-        int next = 1;
+        // a head of 0); lane r keeps round r's key and the lanes that had it
+        uint32_t won = 0, who = 1;
+        int at = 0;
         for (int r = 0; r < k; ++r) {
-            const uint32_t m = __reduce_max_sync(0xffffffffu, (uint32_t)(head >> 32));
-            const int owner = __ffs(__ballot_sync(0xffffffffu, (uint32_t)(head >> 32) == m)) - 1;
-            if (lane == owner) {
-                chosen[warp][r] = head;
-                if (next < (PER < kList ? PER : kList)) {
-                    head = lists[warp][next++][lane];
+            const uint32_t m = __reduce_max_sync(0xffffffffu, head);
+            const unsigned b = __ballot_sync(0xffffffffu, head == m);
+            if (lane == r) won = m, who = b;
+            if (head == m && (b & lower) == 0) {
+                ++at;
+                if (PER <= kList || at < LIST) {
+                    head = my_list[at];
                 } else {
-                    // the list is used up: the largest key below the last one
-                    const unsigned long long last = head;
-                    head = 0;
-                    if (PER > kList)
+                    // the list is used up: the key again if there are more of
+                    // it than the lane has given, else the largest below it
+                    int n = 0;
+                    uint32_t next = 0;
 #pragma unroll
-                        for (int i = 0; i < PER; ++i) {
-                            const unsigned long long x =
-                                ((unsigned long long)key[i] << 32) | (uint32_t)~(uint32_t)(e0 + i);
-                            if (key[i] && x < last && x > head) head = x;
-                        }
+                    for (int i = 0; i < PER; ++i) {
+                        n += key[i] >= head;
+                        if (key[i] < head) next = max(next, key[i]);
+                    }
+                    if (n <= at) head = next;
                 }
             }
         }
+        // the expert of lane j's key: the owner's first one that has it, or,
+        // where the rounds before gave equal keys of the same owner (they
+        // follow one another), the one after theirs
+        const int owner = __ffs(who) - 1;
+        const uint32_t won_before = __shfl_up_sync(0xffffffffu, won, 1);
+        const int owner_before = __shfl_up_sync(0xffffffffu, owner, 1);
+        const bool again = lane > 0 && lane < k && won_before == won && owner_before == owner;
+        const unsigned repeats = __ballot_sync(0xffffffffu, again);
+        const float first = key_logit(__shfl_sync(0xffffffffu, won, 0));
         __syncwarp();
         float s = 0.0f;
         int sel = 0;
         if (lane < k) {
-            const unsigned long long mine = chosen[warp][lane];
-            sel = (int)~(uint32_t)mine;
+            const uint32_t *row = keys[warp] + owner * KEYS;
+            uint32_t v[PER];
+            get_words<PER>(v, row);
+#pragma unroll
+            for (int i = PER - 1; i >= 0; --i)
+                if (v[i] == won) sel = i;
+            if (again) {
+                int skip = lane - (31 - __clz(~repeats & ((2u << lane) - 1u)));
+                for (int i = 0; i < PER; ++i)
+                    if (row[i] == won && skip-- == 0) sel = i;
+            }
+            sel += owner * PER;
             // without a bias the key is the logit's
-            const float lj = a.bias ? __ldg(a.logits + t * E + sel) : key_logit((uint32_t)(mine >> 32));
+            const float lj = a.bias ? __ldg(a.logits + t * E + sel) : key_logit(won);
             if (a.sigmoid)
                 s = sigmoid_of(lj);
             else if (a.renorm)
-                s = exp_below(lj, a.bias ? top : key_logit((uint32_t)(chosen[warp][0] >> 32)));
+                s = exp_below(lj, a.bias ? top : first);
             else
                 s = total > 0.0f || total != total ? exp_below(lj, top) / total : 0.0f;
         }
-        __syncwarp();  // the lists and choices are read before the next token's
+        __syncwarp();  // the keys are read before the next token's are written
         if (a.renorm) {
             const float sum = warp_sum(s);
             s = sum == 0.0f ? 0.0f : s / sum;
@@ -287,11 +401,9 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
             a.w[t * k + lane] = s * a.scale;
             if (a.counts) atomicAdd(hist + sel, 1);
         }
-        if (AHEAD)
-#pragma unroll
-            for (int i = 0; i < PER; ++i) l[i] = ln[i];
     }
     if (a.counts) {
+        if (a.wait_late) ptx::griddep_wait();  // the counts are zero
         __syncthreads();
         for (int e = threadIdx.x; e < E; e += blockDim.x) {
             if (gridDim.x == 1)
@@ -302,21 +414,32 @@ __global__ void __launch_bounds__(32 * kGateWarps) gate_kernel(const GateArgs a)
     }
 }
 
+// The counts before a launch of several blocks.  This kernel may be scheduled
+// while the work before it drains, and the gate's once that work is done: the
+// gate waits for this kernel only before it adds to the counts (a memset put
+// 4 us before the gate, this about 0.5).
+__global__ void __launch_bounds__(256) zero_counts_kernel(int32_t *counts, int E)
+{
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    for (int e = threadIdx.x; e < E; e += 256) counts[e] = 0;
+}
+
 // ---------------------------------------------------------------- gradient
 // One warp per token; lane j owns slot j.  Only softmax weights that are not
 // renormalised give every logit a gradient and need the whole row; the other
 // forms gather the k chosen logits.  Every row of dlogits is written whole
 // before the slots' lanes put theirs in.
 template <int PER>
-__global__ void __launch_bounds__(32 * kGateWarps) gate_grad_kernel(const float *__restrict__ logits,
+__global__ void __launch_bounds__(32 * kGradWarps) gate_grad_kernel(const float *__restrict__ logits,
                                                                     const int32_t *__restrict__ idx,
                                                                     const float *__restrict__ dw, int64_t T, int E,
                                                                     int k, bool sigmoid, bool renorm, float scale,
                                                                     float *__restrict__ dlogits)
 {
     const int lane = threadIdx.x & 31;
-    const int64_t stride = (int64_t)gridDim.x * kGateWarps;
-    for (int64_t t = (int64_t)blockIdx.x * kGateWarps + (threadIdx.x >> 5); t < T; t += stride) {
+    const int64_t stride = (int64_t)gridDim.x * kGradWarps;
+    for (int64_t t = (int64_t)blockIdx.x * kGradWarps + (threadIdx.x >> 5); t < T; t += stride) {
         const float *row = logits + t * E;
         float *out = dlogits + t * E;
         int e = -1;
@@ -395,33 +518,41 @@ cudaError_t with_per(int E, F f)
 
 cudaError_t launch_gate(const GateCall &c, int n_sm, cudaStream_t s)
 {
+    const bool several = c.T > kGateOneBlock, zero = several && c.counts;
     const GateArgs a{c.logits, c.bias,        c.T,         c.E,         c.k,       c.groups, c.E / c.groups,
-                     c.topk_groups, c.sigmoid, c.renorm, c.scale, c.idx, c.w, c.counts};
-    int grid = 1, warps = (int)c.T;
-    if (c.T > kGateOneBlock) {
-        warps = kGateWarps;
-        const int64_t blocks = ceil_div(c.T, kGateWarps);
-        grid = (int)(blocks < (int64_t)n_sm * 4 ? blocks : (int64_t)n_sm * 4);
-        if (c.counts) {
-            cudaError_t e = cudaMemsetAsync(c.counts, 0, (size_t)c.E * 4, s);
-            if (e != cudaSuccess) return e;
-        }
+                     c.topk_groups, c.sigmoid, c.renorm, c.scale, c.idx, c.w, c.counts, zero};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (zero) {
+        cfg.gridDim = dim3(1);
+        cfg.blockDim = dim3(256);
+        cudaError_t e = cudaLaunchKernelEx(&cfg, zero_counts_kernel, c.counts, c.E);
+        if (e != cudaSuccess) return e;
     }
-    const size_t smem = c.counts ? (size_t)c.E * 4 : 0;
+    cfg.dynamicSmemBytes = c.counts ? (size_t)c.E * 4 : 0;
     return with_per(c.E, [&](auto per) {
-        gate_kernel<decltype(per)::value><<<grid, 32 * warps, smem, s>>>(a);
-        return cudaPeekAtLastError();
+        constexpr int PER = decltype(per)::value;
+        using G = GateShape<PER>;
+        const int64_t blocks = ceil_div(c.T, G::WARPS), most = (int64_t)n_sm * G::BLOCKS;
+        cfg.gridDim = dim3(several ? (unsigned)(blocks < most ? blocks : most) : 1);
+        cfg.blockDim = dim3(32 * (several ? (unsigned)G::WARPS : (unsigned)c.T));
+        return cudaLaunchKernelEx(&cfg, gate_kernel<PER>, a);
     });
 }
 
 cudaError_t launch_gate_grad(const float *logits, const int32_t *idx, const float *dw, int64_t T, int E, int k,
                              bool sigmoid, bool renorm, float scale, float *dlogits, int n_sm, cudaStream_t s)
 {
-    const int64_t blocks = ceil_div(T, kGateWarps);
+    const int64_t blocks = ceil_div(T, kGradWarps);
     const int grid = (int)(blocks < (int64_t)n_sm * 8 ? blocks : (int64_t)n_sm * 8);
     return with_per(E, [&](auto per) {
         gate_grad_kernel<decltype(per)::value>
-            <<<grid, 32 * kGateWarps, 0, s>>>(logits, idx, dw, T, E, k, sigmoid, renorm, scale, dlogits);
+            <<<grid, 32 * kGradWarps, 0, s>>>(logits, idx, dw, T, E, k, sigmoid, renorm, scale, dlogits);
         return cudaPeekAtLastError();
     });
 }

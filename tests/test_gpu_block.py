@@ -211,6 +211,26 @@ def test_gate_choices_from_one_lane():
         check_gate(logits, k)
 
 
+@pytest.mark.parametrize("E", [20, 33, 100, 200, 384, 500, 1000])
+def test_gate_equal_logits_in_every_lane(E):
+    """Few distinct values: lists of equal keys that are used up, in every number of experts per lane."""
+    r = np.random.default_rng(E)
+    k = min(E, 32)
+    logits = r.choice(np.array([-2.0, 0.5, 1.5], np.float32), size=(40, E), p=[0.6, 0.3, 0.1])
+    logits[0] = 0.5
+    logits[1, : E // 2] = 1.5
+    check_gate(logits, k)
+    check_gate(logits, k - 1, kind="sigmoid", renormalize=False)
+
+
+def test_gate_saturated_sigmoid_scores_with_a_bias():
+    """exp(-l) up to infinity; the scores are 0 or 1 to 1e-6, the bias keeps the choices 1/128 apart."""
+    r = np.random.default_rng(12)
+    logits = r.choice(np.array([-np.inf, -200, -89, -88, -87.5, -87, -20, 20, 90, np.inf], np.float32), size=(70, 60))
+    bias = (r.permutation(60) / 128).astype(np.float32)
+    check_gate(logits, 12, bias, "sigmoid")
+
+
 def test_gate_masked_and_special_logits():
     logits = logits_of(6, 64, 10)
     logits[0] = -np.inf                     # nothing left: weights of zero, the lowest experts
