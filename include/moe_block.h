@@ -226,10 +226,11 @@ int moe_ffn_forward_routed_train(const void *x_bf16, const int32_t *topk_idx,
  * of which the products read the high one; A and b A + c A A are rounded to
  * FP16.  Relative error in the 2-norm for the usual coefficients: up to 2e-3
  * before out's rounding to BF16, and 1.7e-3 from that.
- * A matrix of zeros gives zeros (NaN with eps == 0); a NaN or an infinity spreads over its whole
- * matrix and no other.  Squares are summed in FP32: entries below about
+ * A matrix of zeros gives zeros (NaN with eps == 0); a NaN or an infinity
+ * spreads over its whole matrix and no other.  Squares are summed in FP32: entries below about
  * 1e-19 count as zero in the norm.
- * Limits: M, N in 1..32768, steps in 1..32, B >= 0 (0 enqueues nothing),
+ * Limits: M, N in 1..32768, steps in 1..32, B in 0..65535 (0 enqueues
+ * nothing), B * M * N <= 2^40, B * ceil(M / 128) * ceil(N / 128) <= 2^24,
  * |a|, |b|, |c| <= 16 and |b| * 1.6 + |c| * 2.56 <= 24 (the FP16 range of
  * b A + c A A), eps >= 0.  workspace: at least
  * moe_orthogonalize_workspace_bytes (0 for an invalid shape).
