@@ -20,8 +20,8 @@
 // The bytes (4 E per token in, 8 k out) would take 2.6 us for 16384 tokens of
 // 256 experts at the copy rate; the instructions bound it (the scores' exp
 // and reciprocal, the sort, k rounds).  Measured there with sigmoid scores, a
-// bias, 4 of 8 groups and k = 8: 15.2 us (13.9 without the counts); softmax scores without a
-// bias: 9.1.
+// bias, 4 of 8 groups and k = 8: 17.1 us (14.0 without the counts); softmax
+// scores without a bias: 9.3.
 #include <type_traits>
 
 #include "common.cuh"
@@ -40,8 +40,8 @@ constexpr int kGateOneBlock = 8;
 
 // Warps per block and blocks per SM: what the registers of a lane's PER
 // experts let an SM hold, in few blocks, because each adds its counts to the
-// same E words at the end (16384 tokens, 256 experts: 15.2 us with 2 blocks
-// of 16 warps, 17.7 with 4 of 8).
+// same E words at the end (16384 tokens, 256 experts: 2.5 us less with 2
+// blocks of 16 warps than with 4 of 8).
 template <int PER>
 struct GateShape {
     static constexpr int WARPS = PER <= 8 ? 16 : 8, BLOCKS = PER <= 8 || PER > 16 ? 2 : 3;
@@ -57,7 +57,6 @@ struct GateArgs {
     int32_t *idx;
     float *w;
     int32_t *counts;
-    bool wait_late;  // the launch before this one only zeroes counts
 };
 
 // logit_key in three instructions: adding +0 turns -0 into +0 and every NaN
@@ -168,14 +167,14 @@ __device__ __forceinline__ void load_logits(const float *row, int E, float (&l)[
 #pragma unroll
             for (int i = 0; i < PER; i += 4) {
                 float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-                if (e0 + i < E) v = ld_nc_f4(row + e0 + i);
+                if (e0 + i < E) v = *reinterpret_cast<const float4 *>(row + e0 + i);
                 l[i] = v.x, l[i + 1] = v.y, l[i + 2] = v.z, l[i + 3] = v.w;
             }
             return;
         }
     }
 #pragma unroll
-    for (int i = 0; i < PER; ++i) l[i] = e0 + i < E ? __ldg(row + e0 + i) : -INFINITY;
+    for (int i = 0; i < PER; ++i) l[i] = e0 + i < E ? row[e0 + i] : -INFINITY;
 }
 
 // Its counterpart: the lane's gradients of one token.
@@ -223,6 +222,9 @@ __global__ void __launch_bounds__(32 * GateShape<PER>::WARPS, GateShape<PER>::BL
     const unsigned lower = (1u << lane) - 1u;
     uint32_t *const my_list = lists[warp] + lane * ROW, *const my_keys = keys[warp] + lane * KEYS;
     my_list[LIST] = 0;
+    // what the kernel before this one wrote is there from here on (plain loads
+    // below: read-only ones may be moved before this)
+    ptx::griddep_wait();
     if (a.counts) {
         for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
         __syncthreads();
@@ -230,8 +232,7 @@ __global__ void __launch_bounds__(32 * GateShape<PER>::WARPS, GateShape<PER>::BL
     float bias[PER];
     if (KEEP_BIAS)
 #pragma unroll
-        for (int i = 0; i < PER; ++i) bias[i] = a.bias && e0 + i < E ? __ldg(a.bias + e0 + i) : 0.0f;
-    if (!a.wait_late) ptx::griddep_wait();
+        for (int i = 0; i < PER; ++i) bias[i] = a.bias && e0 + i < E ? a.bias[e0 + i] : 0.0f;
     const int64_t stride = (int64_t)gridDim.x * (blockDim.x >> 5);
     for (int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp; t < a.T; t += stride) {
         float l[PER];
@@ -262,7 +263,7 @@ __global__ void __launch_bounds__(32 * GateShape<PER>::WARPS, GateShape<PER>::BL
             }
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                key[i] = gate_key(c[i] + (KEEP_BIAS ? bias[i] : e0 + i < E ? __ldg(a.bias + e0 + i) : 0.0f));
+                key[i] = gate_key(c[i] + (KEEP_BIAS ? bias[i] : e0 + i < E ? a.bias[e0 + i] : 0.0f));
         }
         if (E < 32 * PER) {
 #pragma unroll
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(32 * GateShape<PER>::WARPS, GateShape<PER>::BL
             }
             sel += owner * PER;
             // without a bias the key is the logit's
-            const float lj = a.bias ? __ldg(a.logits + t * E + sel) : key_logit(won);
+            const float lj = a.bias ? a.logits[t * E + sel] : key_logit(won);
             if (a.sigmoid)
                 s = sigmoid_of(lj);
             else if (a.renorm)
@@ -403,7 +404,6 @@ __global__ void __launch_bounds__(32 * GateShape<PER>::WARPS, GateShape<PER>::BL
         }
     }
     if (a.counts) {
-        if (a.wait_late) ptx::griddep_wait();  // the counts are zero
         __syncthreads();
         for (int e = threadIdx.x; e < E; e += blockDim.x) {
             if (gridDim.x == 1)
@@ -414,14 +414,13 @@ __global__ void __launch_bounds__(32 * GateShape<PER>::WARPS, GateShape<PER>::BL
     }
 }
 
-// The counts before a launch of several blocks.  This kernel may be scheduled
-// while the work before it drains, and the gate's once that work is done: the
-// gate waits for this kernel only before it adds to the counts (a memset put
-// 4 us before the gate, this about 0.5).
+// The counts before a launch of several blocks.  Both launches are scheduled
+// while the work before them drains (a memset in this one's place put 4 us
+// before the gate, this about 2).
 __global__ void __launch_bounds__(256) zero_counts_kernel(int32_t *counts, int E)
 {
-    ptx::griddep_wait();
     ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
     for (int e = threadIdx.x; e < E; e += 256) counts[e] = 0;
 }
 
@@ -520,7 +519,7 @@ cudaError_t launch_gate(const GateCall &c, int n_sm, cudaStream_t s)
 {
     const bool several = c.T > kGateOneBlock, zero = several && c.counts;
     const GateArgs a{c.logits, c.bias,        c.T,         c.E,         c.k,       c.groups, c.E / c.groups,
-                     c.topk_groups, c.sigmoid, c.renorm, c.scale, c.idx, c.w, c.counts, zero};
+                     c.topk_groups, c.sigmoid, c.renorm, c.scale, c.idx, c.w, c.counts};
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;

@@ -153,12 +153,14 @@ __device__ __forceinline__ void take_routing_warp(const int32_t *__restrict__ id
                                                   int k, int &sel_j, float &w_j)
 {
     const int lane = threadIdx.x & 31;
-    const int e = lane < k ? __ldg(idx + lane) : -1;
+    // (volatile: the fused decode kernel may have started before the kernel
+    // that wrote them ended; a read-only load may be moved before its wait)
+    const int e = lane < k ? *(const volatile int32_t *)(idx + lane) : -1;
     const unsigned lower = (1u << lane) - 1u;
     const unsigned same = __match_any_sync(0xffffffffu, e);
     const bool used = lane < k && e >= 0 && e < E && (same & lower) == 0;
     sel_j = used ? e : 0;
-    w_j = used ? __ldg(w + lane) : 0.0f;
+    w_j = used ? *(const volatile float *)(w + lane) : 0.0f;
     const unsigned dropped = __ballot_sync(0xffffffffu, lane < k && !used);
     if (dropped) {
         // k <= E: there are at least as many free experts as dropped slots

@@ -231,6 +231,42 @@ def test_gate_saturated_sigmoid_scores_with_a_bias():
     check_gate(logits, 12, bias, "sigmoid")
 
 
+def test_gate_reads_what_the_kernel_before_it_writes():
+    """Logits and bias that come straight from a kernel that lets the next one start early."""
+    H, I, E, k = 1024, 512, 16, 4
+    r = np.random.default_rng(21)
+    wgu, wd = (dev(r.normal(size=s) * 0.2, BF16) for s in ((E, 2 * I, H), (E, H, I)))
+    idx, w = dev(np.arange(k)[None], torch.int32), dev(np.full((1, k), 0.25))
+    x, logits = torch.empty(1, H, dtype=BF16, device="cuda"), dev(r.normal(size=(1, H)))
+    ws, out = m.new_workspace(1, H, I, E, k), torch.empty(1, H, device="cuda")
+
+    def experts():
+        out.zero_()
+        mb.moe_ffn_forward_routed(x, idx, w, wgu, wd, out=out, workspace=ws)
+
+    def run(between):
+        experts()
+        between()
+        a = mb.moe_gate_forward(out, 16, score="sigmoid")
+        experts()
+        between()
+        return (*a[:2], *mb.moe_gate_forward(logits, 16, bias=out[0], score="sigmoid", counts=True))
+
+    x.zero_()
+    run(torch.cuda.synchronize)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(lambda: None)
+    for _ in range(20):
+        x.copy_(dev(r.normal(size=(1, H)), BF16))
+        want = run(torch.cuda.synchronize)
+        graph.replay()
+        torch.cuda.synchronize()
+        for g, t in zip(got, want):
+            assert torch.equal(g, t)
+
+
 def test_gate_masked_and_special_logits():
     logits = logits_of(6, 64, 10)
     logits[0] = -np.inf                     # nothing left: weights of zero, the lowest experts
