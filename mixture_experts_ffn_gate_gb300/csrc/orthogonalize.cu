@@ -972,9 +972,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) or
     {
         const int count = args.M * args.N;
         float s = 0.0f;
-        for (int i = (int)rank * kSmallThreads + threadIdx.x; i < count; i += 2 * kSmallThreads) {
-            const float v = (float)g[i];
-            s = fmaf(v, v, s);
+        const int first = (int)rank * kSmallThreads + threadIdx.x;
+        if (count % 8 == 0) {  // the matrix starts on 16 bytes: all of a thread's loads at once
+#pragma unroll
+            for (int i = 0; i < kSmall * kSmall / 8; i += 2 * kSmallThreads) {
+                if (i + first >= count / 8) continue;
+                float v[8];
+                load8(g + 8 * (i + first), v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s = fmaf(v[e], v[e], s);
+            }
+        } else {
+            for (int i = first; i < count; i += 2 * kSmallThreads) {
+                const float v = (float)g[i];
+                s = fmaf(v, v, s);
+            }
         }
         s = warp_sum(s);
         if (lane == 0) sums[warp] = s;
