@@ -684,53 +684,52 @@ __global__ void __launch_bounds__(Cfg<KIND, SEG>::THREADS, 1)
         // what becomes of 32 columns (sorted rows it.p0 + c0 + j) of the
         // warp's 32 weight rows of a tile
         auto emit = [&](const uint32_t (&r)[32], const Item &it, int tile, int c0) {
-                            if constexpr (KIND == kGateUpRaw) {
-                                const int neuron = tile * 64 + 16 * q + (lane & 15);
-                                float *dst = reinterpret_cast<float *>(lane < 16 ? args.out0 : args.out1);
-            #pragma unroll
-                                for (int j = 0; j < 32; ++j)
-                                    if (c0 + j < it.n) dst[(int64_t)(it.p0 + c0 + j) * args.I + neuron] = __uint_as_float(r[j]);
-                            } else if constexpr (KIND == kBwdQ) {
-                if constexpr (SEG) {
-                    // q itself: bwd_swiglu_kernel takes it from there
-                    const int i = tile * BM + 32 * q + lane;
-                    float *dst = reinterpret_cast<float *>(args.out0);
+            if constexpr (KIND == kGateUpRaw) {
+                const int neuron = tile * 64 + 16 * q + (lane & 15);
+                float *dst = reinterpret_cast<float *>(lane < 16 ? args.out0 : args.out1);
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (c0 + j < it.n) dst[(int64_t)(it.p0 + c0 + j) * args.I + neuron] = __uint_as_float(r[j]);
+            } else if constexpr (KIND == kBwdQ && SEG) {
+                // q itself: bwd_swiglu_kernel takes it from there
+                const int i = tile * BM + 32 * q + lane;
+                float *dst = reinterpret_cast<float *>(args.out0);
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (c0 + j < it.n) dst[(int64_t)(it.p0 + c0 + j) * args.I + i] = __uint_as_float(r[j]);
+            } else if constexpr (KIND == kBwdQ) {
+                bwd_q_columns(r, it.n > SMALL_ROWS ? 32 : SMALL_ROWS, it.p0, it.n, c0, tile * BM + 32 * q + lane,
+                              tile * 4 + q, args, lane);
+            } else if constexpr (KIND == kGateUp || KIND == kGateUpMx || KIND == kGateUpSave) {
+                const int neuron = tile * 64 + 16 * q + (lane & 15);
+                __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(lane < 16 ? args.out0 : args.out1);
+                float *keep = lane < 16 ? args.g_keep : args.u_keep;  // kGateUpSave: g (lanes 0-15), u
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const float v = __uint_as_float(r[j]);
+                    const float o = __shfl_xor_sync(0xffffffffu, v, 16);
+                    const float a = lane < 16 ? swiglu(v, o) : swiglu(o, v);
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(a);
+                    const __nv_bfloat16 lo = __float2bfloat16_rn(a - __bfloat162float(hi));
+                    if (c0 + j < it.n) {
+                        const int64_t at = (int64_t)(it.p0 + c0 + j) * args.I + neuron;
+                        dst[at] = lane < 16 ? hi : lo;
+                        if constexpr (KIND == kGateUpSave) keep[at] = v;
+                        if constexpr (SEG)
+                            if (lane < 16)
+                                args.act_lo2[at] =
+                                    __float2bfloat16_rn((a - __bfloat162float(hi)) - __bfloat162float(lo));
+                    }
+                }
+            } else {
+                const int h = tile * BM + 32 * q + lane;
+                float *z = reinterpret_cast<float *>(args.out0);
+                if (h < args.H) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (c0 + j < it.n) dst[(int64_t)(it.p0 + c0 + j) * args.I + i] = __uint_as_float(r[j]);
-                } else {
-                    bwd_q_columns(r, it.n > SMALL_ROWS ? 32 : SMALL_ROWS, it.p0, it.n, c0, tile * BM + 32 * q + lane,
-                                  tile * 4 + q, args, lane);
+                        if (c0 + j < it.n) z[(int64_t)(it.p0 + c0 + j) * args.H + h] = __uint_as_float(r[j]);
                 }
-                            } else if constexpr (KIND == kGateUp || KIND == kGateUpMx || KIND == kGateUpSave) {
-                                const int neuron = tile * 64 + 16 * q + (lane & 15);
-                                __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(lane < 16 ? args.out0 : args.out1);
-                                float *keep = lane < 16 ? args.g_keep : args.u_keep;   // kGateUpSave: g (lanes 0-15), u
-            #pragma unroll
-                                for (int j = 0; j < 32; ++j) {
-                                    const float v = __uint_as_float(r[j]);
-                                    const float o = __shfl_xor_sync(0xffffffffu, v, 16);
-                                    const float a = lane < 16 ? swiglu(v, o) : swiglu(o, v);
-                                    const __nv_bfloat16 hi = __float2bfloat16_rn(a);
-                                    const __nv_bfloat16 lo = __float2bfloat16_rn(a - __bfloat162float(hi));
-                                    if (c0 + j < it.n) {
-                                        const int64_t at = (int64_t)(it.p0 + c0 + j) * args.I + neuron;
-                                        dst[at] = lane < 16 ? hi : lo;
-                                        if constexpr (KIND == kGateUpSave) keep[at] = v;
-                                        if constexpr (SEG)
-                                            if (lane < 16)
-                                                args.act_lo2[at] = __float2bfloat16_rn((a - __bfloat162float(hi)) - __bfloat162float(lo));
-                                    }
-                                }
-                            } else {
-                                const int h = tile * BM + 32 * q + lane;
-                                float *z = reinterpret_cast<float *>(args.out0);
-                                if (h < args.H) {
-            #pragma unroll
-                                    for (int j = 0; j < 32; ++j)
-                                        if (c0 + j < it.n) z[(int64_t)(it.p0 + c0 + j) * args.H + h] = __uint_as_float(r[j]);
-                                }
-                            }
+            }
         };
         // a set of accumulators that the MMAs have filled
         auto wait_set = [&](int acc, uint32_t aph) {
@@ -799,46 +798,46 @@ __global__ void __launch_bounds__(Cfg<KIND, SEG>::THREADS, 1)
                 if (it.n > 32) emit(sum[1], it, tile, 32);
             }
         } else {
-        for (int i = blockIdx.x; i < total; i += gridDim.x, ++li) {
-            const Item it = nxt;
-            if (i + (int)gridDim.x < total) nxt = decode_item(i + gridDim.x, args);
-            const int acc = C::ACC_BUFS == 2 ? (li & 1) : 0;
-            const uint32_t aph = C::ACC_BUFS == 2 ? (li >> 1) & 1 : li & 1;
-            if (!wait_set(acc, aph)) break;
-            for (int t = 0; t < MT && it.m * MT + t < args.tiles; ++t) {
-            const int tile = it.m * MT + t;
-            // q: a warp whose 32 neurons lie past I has nothing to do
-            if (KIND == kBwdQ && tile * BM + 32 * q >= args.I) continue;
-            const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (acc * MT + t) * C::TILE_COLS;
-            for (int c0 = c_first; c0 < it.n; c0 += c_step) {
-                uint32_t r[32];
-                ptx::tmem_ld32(tbase + c0, r);
-                if (!GATE_UP) {
-                    // z = hi part + lo part: for a small chunk both sit in
-                    // these 32 columns (lo from column 16), else the lo part
-                    // is 64 columns on
-                    if (it.n > SMALL_ROWS) {
-                        uint32_t rl[32];
-                        ptx::tmem_ld32(tbase + NMAX + c0, rl);
-                        ptx::tmem_wait_ld();
+            for (int i = blockIdx.x; i < total; i += gridDim.x, ++li) {
+                const Item it = nxt;
+                if (i + (int)gridDim.x < total) nxt = decode_item(i + gridDim.x, args);
+                const int acc = C::ACC_BUFS == 2 ? (li & 1) : 0;
+                const uint32_t aph = C::ACC_BUFS == 2 ? (li >> 1) & 1 : li & 1;
+                if (!wait_set(acc, aph)) break;
+                for (int t = 0; t < MT && it.m * MT + t < args.tiles; ++t) {
+                    const int tile = it.m * MT + t;
+                    // q: a warp whose 32 neurons lie past I has nothing to do
+                    if (KIND == kBwdQ && tile * BM + 32 * q >= args.I) continue;
+                    const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (acc * MT + t) * C::TILE_COLS;
+                    for (int c0 = c_first; c0 < it.n; c0 += c_step) {
+                        uint32_t r[32];
+                        ptx::tmem_ld32(tbase + c0, r);
+                        if (!GATE_UP) {
+                            // z = hi part + lo part: for a small chunk both sit in
+                            // these 32 columns (lo from column 16), else the lo part
+                            // is 64 columns on
+                            if (it.n > SMALL_ROWS) {
+                                uint32_t rl[32];
+                                ptx::tmem_ld32(tbase + NMAX + c0, rl);
+                                ptx::tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(rl[j]));
-                    } else {
-                        ptx::tmem_wait_ld();
+                                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(rl[j]));
+                            } else {
+                                ptx::tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < SMALL_ROWS; ++j)
-                            r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(r[SMALL_ROWS + j]));
+                                for (int j = 0; j < SMALL_ROWS; ++j)
+                                    r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(r[SMALL_ROWS + j]));
+                            }
+                        } else {
+                            ptx::tmem_wait_ld();
+                        }
+                        emit(r, it, tile, c0);
                     }
-                } else {
-                    ptx::tmem_wait_ld();
                 }
-                emit(r, it, tile, c0);
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(tempty + acc);
             }
-            }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(tempty + acc);
-        }
         }
     }
 
