@@ -209,12 +209,11 @@ cudaError_t launch_dlogits(const float *dwp, const int32_t *pos, const int32_t *
 int device_info(int *n_sm, int *pairs);
 
 // rms_norm.cu.  x_f32, res_f32 ...: FP32, else BF16
-constexpr int kNormGradParts = 512;  // most blocks (rows of partial sums) of the gradient
 bool norm_supported(int64_t H);
-int norm_grad_parts(int64_t T);
+int norm_grad_parts(int64_t T, int64_t H);
 cudaError_t launch_norm(const void *x, bool x_f32, const void *residual, bool res_f32, const float *weight, float eps,
                         int64_t T, int H, void *h_out, void *y, void *codes, void *scales, int n_sm, cudaStream_t s);
-// partial: [norm_grad_parts(T)][H]
+// partial: [norm_grad_parts(T, H)][H]
 cudaError_t launch_norm_grad(const void *h, bool h_f32, const float *weight, const void *dy, bool dy_f32,
                              const void *dres, float eps, int64_t T, int H, void *dh, float *dweight, float *partial,
                              int n_sm, cudaStream_t s);

@@ -89,7 +89,7 @@ int moe_rms_norm_forward(const void *x, int x_type, const void *residual, int re
 size_t moe_rms_norm_backward_workspace_bytes(int64_t T, int64_t H)
 {
     if (check_norm(T, H, 0.0f) != MOE_OK) return 0;
-    const size_t bytes = (size_t)moe::norm_grad_parts(T) * (size_t)H * 4;
+    const size_t bytes = (size_t)moe::norm_grad_parts(T, H) * (size_t)H * 4;
     return bytes < 256 ? 256 : bytes;
 }
 

@@ -18,9 +18,9 @@ namespace moe {
 
 namespace {
 
-// Elements per thread.  kVec consecutive ones are one access (16 bytes of
-// BF16) where H is a multiple of 8, so that every row starts on 16 bytes;
-// other H take single elements, coalesced over the block.
+// Elements per thread.  VEC consecutive ones are one access: 8 (16 bytes of
+// BF16) where H is a multiple of 8, so that every row starts on 16 bytes, 4
+// where it is one of 4; other H take single elements, coalesced over the block.
 constexpr int kEpt = 16;
 constexpr int kNormMaxH = 16384;  // 1024 threads of kEpt elements
 static_assert(kNormMaxH == 1024 * kEpt, "one row per block");
@@ -32,6 +32,9 @@ __device__ __forceinline__ void load_row(const float *p, float (&v)[VEC])
         const float4 a = ld_nc_f4(p), b = ld_nc_f4(p + 4);
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
         v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else if constexpr (VEC == 4) {
+        const float4 a = ld_nc_f4(p);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
     } else {
         v[0] = __ldg(p);
     }
@@ -40,10 +43,14 @@ __device__ __forceinline__ void load_row(const float *p, float (&v)[VEC])
 template <int VEC>
 __device__ __forceinline__ void load_row(const __nv_bfloat16 *p, float (&v)[VEC])
 {
-    if constexpr (VEC == 8)
+    if constexpr (VEC == 8) {
         unpack8(ld_nc16(p), v);
-    else
+    } else if constexpr (VEC == 4) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
+        v[0] = bf16lo(w.x), v[1] = bf16hi(w.x), v[2] = bf16lo(w.y), v[3] = bf16hi(w.y);
+    } else {
         v[0] = __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(p)) << 16);
+    }
 }
 
 // The same through plain loads: for rows that the call may also write (an
@@ -55,6 +62,9 @@ __device__ __forceinline__ void load_row_rw(const float *p, float (&v)[VEC])
         const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
         v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else if constexpr (VEC == 4) {
+        const float4 a = *reinterpret_cast<const float4 *>(p);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
     } else {
         v[0] = *p;
     }
@@ -63,10 +73,14 @@ __device__ __forceinline__ void load_row_rw(const float *p, float (&v)[VEC])
 template <int VEC>
 __device__ __forceinline__ void load_row_rw(const __nv_bfloat16 *p, float (&v)[VEC])
 {
-    if constexpr (VEC == 8)
+    if constexpr (VEC == 8) {
         unpack8(*reinterpret_cast<const uint4 *>(p), v);
-    else
+    } else if constexpr (VEC == 4) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(p);
+        v[0] = bf16lo(w.x), v[1] = bf16hi(w.x), v[2] = bf16lo(w.y), v[3] = bf16hi(w.y);
+    } else {
         v[0] = __bfloat162float(*p);
+    }
 }
 
 template <int VEC>
@@ -75,6 +89,8 @@ __device__ __forceinline__ void store_row(float *p, const float (&v)[VEC])
     if constexpr (VEC == 8) {
         *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
         *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else if constexpr (VEC == 4) {
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
         *p = v[0];
     }
@@ -92,6 +108,8 @@ __device__ __forceinline__ void store_row(__nv_bfloat16 *p, const float (&v)[VEC
     if constexpr (VEC == 8)
         *reinterpret_cast<uint4 *>(p) = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]),
                                                    bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+    else if constexpr (VEC == 4)
+        *reinterpret_cast<uint2 *>(p) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
     else
         *p = __float2bfloat16_rn(v[0]);
 }
@@ -154,12 +172,21 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a)
                     load_row_rw<VEC>((const RT *)a.residual + row + i, r);
 #pragma unroll
                     for (int q = 0; q < VEC; ++q) h[c][q] += r[q];
-                    if (a.h_out) store_row<VEC>((RT *)a.h_out + row + i, h[c]);
                 }
 #pragma unroll
                 for (int q = 0; q < VEC; ++q) sq[0] = fmaf(h[c][q], h[c][q], sq[0]);
             }
         }
+        // after the row's loads, which the compiler may not move past a store
+        // that could be to the residual (4097 columns: 453 us with the stores
+        // between them, 279 so)
+        if constexpr (!std::is_void_v<RT>)
+            if (a.h_out)
+#pragma unroll
+                for (int c = 0; c < NV; ++c) {
+                    const int i = (c * (int)blockDim.x + (int)threadIdx.x) * VEC;
+                    if (i < H) store_row<VEC>((RT *)a.h_out + row + i, h[c]);
+                }
         block_sum(sq, part[turn]);
         // r, and what its roundings leave, r (1 - v r^2) / 2: one error for all
         // of a row's elements turns 422 8-bit codes of 10 x 8192 x 7168 away
@@ -224,7 +251,8 @@ struct NormGradArgs {
 // BF16 while it waits.
 template <typename T, int VEC>
 struct Raw {
-    static constexpr int kWords = VEC * (int)sizeof(T) > 4 ? VEC * (int)sizeof(T) / 4 : 1;
+    static_assert(VEC == 8 || VEC == 4);
+    static constexpr int kWords = VEC * (int)sizeof(T) / 4;
     uint32_t v[kWords];
     __device__ __forceinline__ void zero()
     {
@@ -242,15 +270,17 @@ struct Raw {
                 v[i] = w.x, v[i + 1] = w.y, v[i + 2] = w.z, v[i + 3] = w.w;
             }
         } else if constexpr (sizeof(T) == 4) {
-            v[0] = *reinterpret_cast<const uint32_t *>(p);
+            const uint4 w = NC ? ld_nc16(p) : *reinterpret_cast<const uint4 *>(p);
+            v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
         } else {
-            v[0] = (uint32_t)*reinterpret_cast<const uint16_t *>(p) << 16;
+            const uint2 w = *reinterpret_cast<const uint2 *>(p);
+            v[0] = w.x, v[1] = w.y;
         }
     }
     __device__ __forceinline__ float get(int q) const
     {
-        if constexpr (sizeof(T) == 4 || VEC == 1)
-            return __uint_as_float(v[sizeof(T) == 4 ? q : 0]);
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(v[q]);
         else
             return q & 1 ? bf16hi(v[q / 2]) : bf16lo(v[q / 2]);
     }
@@ -331,6 +361,70 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024, 1) norm_grad_kernel(const 
     }
 }
 
+// The same for any H, an element at a time.  Kept in registers a row would
+// spill (its 16-bit elements take a register each), so it is read again, from
+// L1, for the outputs.
+template <typename HT, typename GT>
+__global__ void __launch_bounds__(1024, 1) norm_grad_any_kernel(const NormGradArgs a)
+{
+    __shared__ float part[2][2][32];
+    const int H = a.H;
+    const HT *h = (const HT *)a.h, *dres = (const HT *)a.dres;
+    const GT *dy = (const GT *)a.dy;
+    float w[kEpt], dw[kEpt];
+#pragma unroll
+    for (int c = 0; c < kEpt; ++c) {
+        const int i = c * (int)blockDim.x + (int)threadIdx.x;
+        w[c] = i < H ? __ldg(a.weight + i) : 0.0f;
+        dw[c] = 0.0f;
+    }
+    int turn = 0;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
+        const int64_t row = t * H;
+        float s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < kEpt; ++c) {
+            const int i = c * (int)blockDim.x + (int)threadIdx.x;
+            if (i < H) {
+                float hv[1], g[1];
+                load_row<1>(h + row + i, hv);
+                load_row<1>(dy + row + i, g);
+                s[0] = fmaf(hv[0], hv[0], s[0]);
+                s[1] = fmaf(g[0] * w[c], hv[0], s[1]);
+            }
+        }
+        block_sum(s, part[turn]);
+        const float inv = 1.0f / sqrtf(fmaf(s[0], a.inv_h, a.eps));
+        const float m = s[1] * a.inv_h * inv * inv;
+#pragma unroll
+        for (int c0 = 0; c0 < kEpt; c0 += 4) {
+            float o[4][1];
+#pragma unroll
+            for (int c = c0; c < c0 + 4; ++c) {
+                const int i = c * (int)blockDim.x + (int)threadIdx.x;
+                if (i < H) {
+                    float hv[1], g[1], d[1] = {0.0f};
+                    load_row<1>(h + row + i, hv);
+                    load_row<1>(dy + row + i, g);
+                    if (dres) load_row_rw<1>(dres + row + i, d);
+                    dw[c] = fmaf(g[0], hv[0] * inv, dw[c]);
+                    o[c - c0][0] = fmaf(inv, g[0] * w[c] - hv[0] * m, d[0]);
+                }
+            }
+#pragma unroll
+            for (int c = c0; c < c0 + 4; ++c) {
+                const int i = c * (int)blockDim.x + (int)threadIdx.x;
+                if (i < H) store_row<1>((HT *)a.dh + row + i, o[c - c0]);
+            }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < kEpt; ++c) {
+        const int i = c * (int)blockDim.x + (int)threadIdx.x;
+        if (i < H) a.partial[(int64_t)blockIdx.x * H + i] = dw[c];
+    }
+}
+
 // dweight[c] = sum over the blocks' partial rows.  A block takes 32 columns;
 // its 32 warps take the rows in turn, then one warp adds the 32 sums in
 // order.
@@ -366,6 +460,8 @@ cudaError_t norm_launch(const NormArgs &a, bool mx, int grid, int threads, cudaS
         norm_kernel<XT, RT, 8, true><<<grid, threads, 0, s>>>(a);
     else if (a.H % 8 == 0)
         norm_kernel<XT, RT, 8, false><<<grid, threads, 0, s>>>(a);
+    else if (a.H % 4 == 0)
+        norm_kernel<XT, RT, 4, false><<<grid, threads, 0, s>>>(a);
     else
         norm_kernel<XT, RT, 1, false><<<grid, threads, 0, s>>>(a);
     return cudaPeekAtLastError();
@@ -379,11 +475,13 @@ cudaError_t norm_grad_launch(const NormGradArgs &a, int grid, int threads, cudaS
             norm_grad_kernel<HT, GT, 8, true><<<grid, threads, 0, s>>>(a);
         else
             norm_grad_kernel<HT, GT, 8, false><<<grid, threads, 0, s>>>(a);
-    } else {
+    } else if (a.H % 4 == 0) {
         if (threads <= 512)
-            norm_grad_kernel<HT, GT, 1, true><<<grid, threads, 0, s>>>(a);
+            norm_grad_kernel<HT, GT, 4, true><<<grid, threads, 0, s>>>(a);
         else
-            norm_grad_kernel<HT, GT, 1, false><<<grid, threads, 0, s>>>(a);
+            norm_grad_kernel<HT, GT, 4, false><<<grid, threads, 0, s>>>(a);
+    } else {
+        norm_grad_any_kernel<HT, GT><<<grid, threads, 0, s>>>(a);
     }
     return cudaPeekAtLastError();
 }
@@ -392,7 +490,13 @@ cudaError_t norm_grad_launch(const NormGradArgs &a, int grid, int threads, cudaS
 
 bool norm_supported(int64_t H) { return H >= 1 && H <= kNormMaxH; }
 
-int norm_grad_parts(int64_t T) { return (int)(T < kNormGradParts ? T : kNormGradParts); }
+// Rows of partial sums: enough blocks to fill the SMs where a row is short
+// (128 columns: 643 us with 512 blocks, 197 so), 8 MB of them at most
+int norm_grad_parts(int64_t T, int64_t H)
+{
+    const int64_t fit = (1 << 21) / H, most = fit < 512 ? 512 : fit > 4096 ? 4096 : fit;
+    return (int)(T < most ? T : most);
+}
 
 cudaError_t launch_norm(const void *x, bool x_f32, const void *residual, bool res_f32, const float *weight, float eps,
                         int64_t T, int H, void *h_out, void *y, void *codes, void *scales, int n_sm, cudaStream_t s)
@@ -419,8 +523,9 @@ cudaError_t launch_norm_grad(const void *h, bool h_f32, const float *weight, con
 {
     const NormGradArgs a{h, dy, dres, weight, eps, 1.0f / (float)H, T, H, dh, partial};
     const int threads = norm_threads(H);
-    const int per_sm = threads >= 512 ? 1 : 512 / threads;
-    int grid = norm_grad_parts(T);
+    const int full = H % 4 ? 1024 : 512;  // threads on an SM at a time
+    const int per_sm = threads >= full ? 1 : full / threads;
+    int grid = norm_grad_parts(T, H);
     if (grid > n_sm * per_sm) grid = n_sm * per_sm;
     cudaError_t e;
     if (h_f32)

@@ -72,6 +72,18 @@ def test_norm_forward(T, H, xt, rt):
     assert np.all(np.abs(ref.mx_values(codes, scales) / step - v) <= tol)
 
 
+@pytest.mark.parametrize("T,H", [(9, 12), (3, 1004), (4, 4100), (2, 16380), (2000, 100)])
+@pytest.mark.parametrize("xt,rt", [(BF16, None), (F32, BF16), (BF16, F32)])
+def test_norm_forward_of_other_widths(T, H, xt, rt):
+    """Rows of a multiple of four elements, not of eight; in place as well."""
+    test_norm_forward(T, H, xt, rt)
+    if rt is not None:
+        x, w, res = randn(T, H, seed=1, dtype=xt), randn(H, seed=2), randn(T, H, seed=3, dtype=rt)
+        want = mb.moe_rms_norm_forward(x, w, residual=res)
+        got = mb.moe_rms_norm_forward(x, w, residual=res, h=res)
+        assert torch.equal(got.y, want.y) and torch.equal(res, want.h)
+
+
 def test_norm_in_place_and_outputs_of_the_caller():
     x, res, w = randn(9, 256, seed=1), randn(9, 256, seed=2, dtype=BF16), randn(256, seed=3)
     want = mb.moe_rms_norm_forward(x, w, residual=res, mxfp8=True)
@@ -121,6 +133,13 @@ def test_norm_backward(T, H, ht, gt, with_res):
         into = dres.clone()
         dh2, dw2 = mb.moe_rms_norm_backward(h, w, dy, dres=into, eps=1e-5, dh=into)
         assert torch.equal(dh2, dh) and torch.equal(dw2, dw)
+
+
+@pytest.mark.parametrize("T,H", [(9, 12), (6, 1004), (4, 4100), (2, 16380), (5000, 100), (9000, 36), (2500, 37)])
+@pytest.mark.parametrize("ht,gt,with_res", [(BF16, F32, True), (F32, BF16, False), (F32, F32, True)])
+def test_norm_backward_of_other_widths(T, H, ht, gt, with_res):
+    """Rows of a multiple of four elements, not of eight; many short rows."""
+    test_norm_backward(T, H, ht, gt, with_res)
 
 
 def test_norm_backward_of_no_rows():
