@@ -18,7 +18,7 @@ namespace moe {
 
 namespace {
 
-// Elements per thread.  VEC consecutive ones are one access: 8 (16 bytes of
+// Elements per thread (of single ones, norm_ept).  VEC consecutive ones are one access: 8 (16 bytes of
 // BF16) where H is a multiple of 8, so that every row starts on 16 bytes, 4
 // where it is one of 4; other H take single elements, coalesced over the block.
 constexpr int kEpt = 16;
@@ -145,10 +145,10 @@ struct NormArgs {
 };
 
 // Forward.  XT, RT: types of x and of the residual (RT void: none).
-template <typename XT, typename RT, int VEC, bool MX>
-__global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a)
+template <typename XT, typename RT, int VEC, bool MX, int EPT = kEpt>
+__global__ void __launch_bounds__(1024, EPT == 4 ? 2 : 1) norm_kernel(const NormArgs a)
 {
-    constexpr int NV = kEpt / VEC;
+    constexpr int NV = EPT / VEC;
     __shared__ float part[2][1][32];
     const int H = a.H;
     float w[NV][VEC];
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(const NormArgs a)
         }
         // after the row's loads, which the compiler may not move past a store
         // that could be to the residual (4097 columns: 453 us with the stores
-        // between them, 279 so)
+        // between them, 277 so)
         if constexpr (!std::is_void_v<RT>)
             if (a.h_out)
 #pragma unroll
@@ -364,16 +364,16 @@ __global__ void __launch_bounds__(AHEAD ? 512 : 1024, 1) norm_grad_kernel(const 
 // The same for any H, an element at a time.  Kept in registers a row would
 // spill (its 16-bit elements take a register each), so it is read again, from
 // L1, for the outputs.
-template <typename HT, typename GT>
-__global__ void __launch_bounds__(1024, 1) norm_grad_any_kernel(const NormGradArgs a)
+template <typename HT, typename GT, int EPT>
+__global__ void __launch_bounds__(1024, EPT == 4 ? 2 : 1) norm_grad_any_kernel(const NormGradArgs a)
 {
     __shared__ float part[2][2][32];
     const int H = a.H;
     const HT *h = (const HT *)a.h, *dres = (const HT *)a.dres;
     const GT *dy = (const GT *)a.dy;
-    float w[kEpt], dw[kEpt];
+    float w[EPT], dw[EPT];
 #pragma unroll
-    for (int c = 0; c < kEpt; ++c) {
+    for (int c = 0; c < EPT; ++c) {
         const int i = c * (int)blockDim.x + (int)threadIdx.x;
         w[c] = i < H ? __ldg(a.weight + i) : 0.0f;
         dw[c] = 0.0f;
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(1024, 1) norm_grad_any_kernel(const NormGradAr
         const int64_t row = t * H;
         float s[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int c = 0; c < kEpt; ++c) {
+        for (int c = 0; c < EPT; ++c) {
             const int i = c * (int)blockDim.x + (int)threadIdx.x;
             if (i < H) {
                 float hv[1], g[1];
@@ -397,10 +397,11 @@ __global__ void __launch_bounds__(1024, 1) norm_grad_any_kernel(const NormGradAr
         const float inv = 1.0f / sqrtf(fmaf(s[0], a.inv_h, a.eps));
         const float m = s[1] * a.inv_h * inv * inv;
 #pragma unroll
-        for (int c0 = 0; c0 < kEpt; c0 += 4) {
-            float o[4][1];
+        for (int c0 = 0; c0 < EPT; c0 += (EPT < 8 ? EPT : 8)) {
+            constexpr int G = EPT < 8 ? EPT : 8;
+            float o[G][1];
 #pragma unroll
-            for (int c = c0; c < c0 + 4; ++c) {
+            for (int c = c0; c < c0 + G; ++c) {
                 const int i = c * (int)blockDim.x + (int)threadIdx.x;
                 if (i < H) {
                     float hv[1], g[1], d[1] = {0.0f};
@@ -412,14 +413,14 @@ __global__ void __launch_bounds__(1024, 1) norm_grad_any_kernel(const NormGradAr
                 }
             }
 #pragma unroll
-            for (int c = c0; c < c0 + 4; ++c) {
+            for (int c = c0; c < c0 + G; ++c) {
                 const int i = c * (int)blockDim.x + (int)threadIdx.x;
                 if (i < H) store_row<1>((HT *)a.dh + row + i, o[c - c0]);
             }
         }
     }
 #pragma unroll
-    for (int c = 0; c < kEpt; ++c) {
+    for (int c = 0; c < EPT; ++c) {
         const int i = c * (int)blockDim.x + (int)threadIdx.x;
         if (i < H) a.partial[(int64_t)blockIdx.x * H + i] = dw[c];
     }
@@ -447,9 +448,19 @@ __global__ void __launch_bounds__(1024) norm_dweight_kernel(const float *__restr
     }
 }
 
+// Single elements: as few per thread as a block of 1024 can hold the row with
+// (more threads, and more loads in flight), 8 only where their block fills an
+// SM (6.7e7 elements in rows of 1001, 3001, 4097 and 8191 with 4 / 8 / 16:
+// forward 156 / 158 / 203, 189 / 231 / 215, - / 276 / 277, - / 183 / 217 us,
+// gradient 256 / 370 / 542, 328 / 486 / 560, - / 655 / 572, - / 395 / 492).
+int norm_ept(int H)
+{
+    return H % 4 == 0 ? kEpt : H <= 4096 ? 4 : H > 6144 && H <= 8192 ? 8 : 16;
+}
+
 int norm_threads(int H)
 {
-    const int n = (H + kEpt - 1) / kEpt;
+    const int per = norm_ept(H), n = (H + per - 1) / per;
     return (n + 31) / 32 * 32;
 }
 
@@ -462,6 +473,10 @@ cudaError_t norm_launch(const NormArgs &a, bool mx, int grid, int threads, cudaS
         norm_kernel<XT, RT, 8, false><<<grid, threads, 0, s>>>(a);
     else if (a.H % 4 == 0)
         norm_kernel<XT, RT, 4, false><<<grid, threads, 0, s>>>(a);
+    else if (norm_ept(a.H) == 4)
+        norm_kernel<XT, RT, 1, false, 4><<<grid, threads, 0, s>>>(a);
+    else if (norm_ept(a.H) == 8)
+        norm_kernel<XT, RT, 1, false, 8><<<grid, threads, 0, s>>>(a);
     else
         norm_kernel<XT, RT, 1, false><<<grid, threads, 0, s>>>(a);
     return cudaPeekAtLastError();
@@ -480,8 +495,12 @@ cudaError_t norm_grad_launch(const NormGradArgs &a, int grid, int threads, cudaS
             norm_grad_kernel<HT, GT, 4, true><<<grid, threads, 0, s>>>(a);
         else
             norm_grad_kernel<HT, GT, 4, false><<<grid, threads, 0, s>>>(a);
+    } else if (norm_ept(a.H) == 4) {
+        norm_grad_any_kernel<HT, GT, 4><<<grid, threads, 0, s>>>(a);
+    } else if (norm_ept(a.H) == 8) {
+        norm_grad_any_kernel<HT, GT, 8><<<grid, threads, 0, s>>>(a);
     } else {
-        norm_grad_any_kernel<HT, GT><<<grid, threads, 0, s>>>(a);
+        norm_grad_any_kernel<HT, GT, kEpt><<<grid, threads, 0, s>>>(a);
     }
     return cudaPeekAtLastError();
 }
@@ -523,7 +542,7 @@ cudaError_t launch_norm_grad(const void *h, bool h_f32, const float *weight, con
 {
     const NormGradArgs a{h, dy, dres, weight, eps, 1.0f / (float)H, T, H, dh, partial};
     const int threads = norm_threads(H);
-    const int full = H % 4 ? 1024 : 512;  // threads on an SM at a time
+    const int full = H % 4 == 0 ? 512 : norm_ept(H) == 4 ? 2048 : 1024;
     const int per_sm = threads >= full ? 1 : full / threads;
     int grid = norm_grad_parts(T, H);
     if (grid > n_sm * per_sm) grid = n_sm * per_sm;
