@@ -397,25 +397,16 @@ __global__ void __launch_bounds__(1024, EPT == 4 ? 2 : 1) norm_grad_any_kernel(c
         const float inv = 1.0f / sqrtf(fmaf(s[0], a.inv_h, a.eps));
         const float m = s[1] * a.inv_h * inv * inv;
 #pragma unroll
-        for (int c0 = 0; c0 < EPT; c0 += (EPT < 8 ? EPT : 8)) {
-            constexpr int G = EPT < 8 ? EPT : 8;
-            float o[G][1];
-#pragma unroll
-            for (int c = c0; c < c0 + G; ++c) {
-                const int i = c * (int)blockDim.x + (int)threadIdx.x;
-                if (i < H) {
-                    float hv[1], g[1], d[1] = {0.0f};
-                    load_row<1>(h + row + i, hv);
-                    load_row<1>(dy + row + i, g);
-                    if (dres) load_row_rw<1>(dres + row + i, d);
-                    dw[c] = fmaf(g[0], hv[0] * inv, dw[c]);
-                    o[c - c0][0] = fmaf(inv, g[0] * w[c] - hv[0] * m, d[0]);
-                }
-            }
-#pragma unroll
-            for (int c = c0; c < c0 + G; ++c) {
-                const int i = c * (int)blockDim.x + (int)threadIdx.x;
-                if (i < H) store_row<1>((HT *)a.dh + row + i, o[c - c0]);
+        for (int c = 0; c < EPT; ++c) {
+            const int i = c * (int)blockDim.x + (int)threadIdx.x;
+            if (i < H) {
+                float hv[1], g[1], o[1] = {0.0f};
+                load_row<1>(h + row + i, hv);
+                load_row<1>(dy + row + i, g);
+                if (dres) load_row_rw<1>(dres + row + i, o);
+                dw[c] = fmaf(g[0], hv[0] * inv, dw[c]);
+                o[0] = fmaf(inv, g[0] * w[c] - hv[0] * m, o[0]);
+                store_row<1>((HT *)a.dh + row + i, o);
             }
         }
     }
@@ -451,8 +442,8 @@ __global__ void __launch_bounds__(1024) norm_dweight_kernel(const float *__restr
 // Single elements: as few per thread as a block of 1024 can hold the row with
 // (more threads, and more loads in flight), 8 only where their block fills an
 // SM (6.7e7 elements in rows of 1001, 3001, 4097 and 8191 with 4 / 8 / 16:
-// forward 156 / 158 / 203, 189 / 231 / 215, - / 276 / 277, - / 183 / 217 us,
-// gradient 256 / 370 / 542, 328 / 486 / 560, - / 655 / 572, - / 395 / 492).
+// forward 156 / 158 / 203, 189 / 231 / 215, - / 276 / 277, - / 183 / 217 us;
+// gradient as chosen 233, 296, 437, about 400).
 int norm_ept(int H)
 {
     return H % 4 == 0 ? kEpt : H <= 4096 ? 4 : H > 6144 && H <= 8192 ? 8 : 16;
