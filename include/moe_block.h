@@ -163,8 +163,10 @@ int moe_gate_backward(const float *logits_f32, const int32_t *topk_idx,
  *   w_gate_up, w_down: BF16; or, with w_gate_up_scale and w_down_scale (both
  *            or none), MXFP8 as in moe_ffn_forward_mxfp8
  * A slot whose index is outside [0, E), or that repeats the index of an
- * earlier slot of its token, is dropped: an expert that the token does not
- * use takes its place with weight 0.  So -1 marks an unused slot.
+ * earlier slot of its token, is dropped: it adds nothing to any output, not
+ * even where its weight, or the weights of an expert that no slot uses, are
+ * infinite or NaN.  So -1 marks an unused slot.  (The fused decode kernel,
+ * up to four tokens, reads an unused expert's weights in its place.)
  * Arithmetic with BF16 weights: FP32 sums (on the grouped path in segments of
  * 256 products, added in order) and FP32 intermediates, which the tensor-core
  * products take as three BF16 terms (24 bits): closer to the definition than

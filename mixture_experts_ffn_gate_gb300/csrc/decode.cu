@@ -27,6 +27,7 @@
 // kernel's MX instantiation does.
 #include "common.cuh"
 #include "kernels.h"
+#include "route_block.cuh"
 
 namespace moe {
 
@@ -311,13 +312,17 @@ __global__ void __launch_bounds__(512) decode_down_kernel(const float *__restric
         }
     }
     __syncthreads();
-    // slot-ordered combine: out[t, h0+r] = sum_j w[t,j] * part[r][t,j]
+    // slot-ordered combine: out[t, h0+r] = sum_j w[t,j] * part[r][t,j], dropped
+    // slots (which have no partial sum) left out
     const int nt = t1 - t0;
     for (int q = threadIdx.x; q < DOWN_HW * nt; q += blockDim.x) {
         const int r = q / nt, tl = q - r * nt;
         const int t = t0 + tl;
         float o = 0.0f;
-        for (int j = 0; j < k; ++j) o = fmaf(__ldg(wts + (int64_t)t * k + j), part[r * span + tl * k + j], o);
+        for (int j = 0; j < k; ++j) {
+            const float w = __ldg(wts + (int64_t)t * k + j);
+            if (!is_dropped(w)) o = fmaf(w, part[r * span + tl * k + j], o);
+        }
         out[(int64_t)t * H + h0 + r] = o;
     }
 }

@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float wt;
         if (t == 0 && lane == 0) MOE_TL(56);
         if constexpr (GIVEN)
-            take_routing_warp(rt.idx + (int64_t)t * k, rt.w + (int64_t)t * k, E, k, e, wt);
+            take_routing_warp<true>(rt.idx + (int64_t)t * k, rt.w + (int64_t)t * k, E, k, e, wt);
         else
             route_token_warp<ROUTER>(logits + (int64_t)t * E, E, k, reinterpret_cast<float *>(sm) + (size_t)t * E, e,
                                      wt);
@@ -1208,7 +1208,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int v = ct; v < T * nh; v += n_ct) {
         const int t = v / nh, r = v - t * nh;
         float o = 0.0f;
-        for (int j = 0; j < k; ++j) o = fmaf(s_w[t * k + j], part[r * A + t * k + j], o);
+        for (int j = 0; j < k; ++j)
+            if (!GIVEN || !is_dropped(s_w[t * k + j])) o = fmaf(s_w[t * k + j], part[r * A + t * k + j], o);
         out[(size_t)t * H + h_lo + r] = o;
     }
 #ifdef MOE_FUSED_TIMELINE

@@ -553,17 +553,16 @@ __global__ void __launch_bounds__(256) dlogits_kernel(const float *__restrict__ 
 }
 
 // The routing weights' gradient where the caller passed the routing: the
-// same sums, 0 for a dropped slot (whose expert is not the caller's).
+// same sums, 0 for a dropped slot (which has no row).
 __global__ void __launch_bounds__(256) routed_dw_kernel(const float *__restrict__ dwp, const int32_t *__restrict__ pos,
-                                                        const int32_t *__restrict__ idx_in,
-                                                        const int32_t *__restrict__ idx, int64_t slots, int groups,
-                                                        float *__restrict__ dw)
+                                                        int64_t slots, int groups, float *__restrict__ dw)
 {
     const int64_t a = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (a >= slots) return;
     float v = 0.0f;
-    if (__ldg(idx_in + a) == __ldg(idx + a)) {
-        const float *p = dwp + (int64_t)__ldg(pos + a) * groups;
+    const int r = __ldg(pos + a);
+    if (r >= 0) {
+        const float *p = dwp + (int64_t)r * groups;
         for (int g = 0; g < groups; ++g) v += __ldg(p + g);
     }
     dw[a] = v;
@@ -705,11 +704,10 @@ cudaError_t launch_zero_untouched(const int32_t *counts, int E, int H, int I, fl
     return cudaPeekAtLastError();
 }
 
-cudaError_t launch_routed_dw(const float *dwp, const int32_t *pos, const int32_t *idx_in, const int32_t *idx, int T,
-                             int k, int I, float *dw, cudaStream_t s)
+cudaError_t launch_routed_dw(const float *dwp, const int32_t *pos, int T, int k, int I, float *dw, cudaStream_t s)
 {
     const int64_t slots = (int64_t)T * k;
-    routed_dw_kernel<<<(unsigned)ceil_div(slots, 256), 256, 0, s>>>(dwp, pos, idx_in, idx, slots, I / 32, dw);
+    routed_dw_kernel<<<(unsigned)ceil_div(slots, 256), 256, 0, s>>>(dwp, pos, slots, I / 32, dw);
     return cudaPeekAtLastError();
 }
 

@@ -233,16 +233,15 @@ cudaError_t launch_gate(const GateCall &c, int n_sm, cudaStream_t s);
 cudaError_t launch_gate_grad(const float *logits, const int32_t *idx, const float *dw, int64_t T, int E, int k,
                              bool sigmoid, bool renorm, float scale, float *dlogits, int n_sm, cudaStream_t s);
 
-// routing.cu: the caller's routing as the layer's own (dropped slots
-// replaced, route_block.cuh); tag_size, tag_cap as for launch_router
+// routing.cu: the caller's routing as the layer's own (dropped slots marked,
+// take_routing_warp); tag_size, tag_cap as for launch_router
 cudaError_t launch_take_routing(const int32_t *idx_in, const float *w_in, int T, int E, int k, int32_t *idx, float *w,
                                 unsigned long long *tag_size, unsigned long long tag_cap, cudaStream_t s);
 // MXFP8 rows [T, H] (codes, scales) widened to BF16
 cudaError_t launch_mx_widen(const void *codes, const void *scales, int T, int H, void *x, int n_sm, cudaStream_t s);
-// grouped_bwd.cu: dw [T, k] from the q GEMM's partial sums; 0 where idx_in
-// differs from the routing that ran (a dropped slot)
-cudaError_t launch_routed_dw(const float *dwp, const int32_t *pos, const int32_t *idx_in, const int32_t *idx, int T,
-                             int k, int I, float *dw, cudaStream_t s);
+// grouped_bwd.cu: dw [T, k] from the q GEMM's partial sums; 0 for a slot
+// without a row (dropped)
+cudaError_t launch_routed_dw(const float *dwp, const int32_t *pos, int T, int k, int I, float *dw, cudaStream_t s);
 
 // orthogonalize.cu
 struct OrthoCall {

@@ -456,7 +456,7 @@ int run_backward(const void *x, const float *logits, const void *wgu, const void
                                             rows, H, I, E, dwd, ctas, stream, ds_lo2, wa_lo2)));
     MOE_TRY(stg.done(moe::launch_wgrad_gate_up(ws + L.dgu_hi, ws + L.dgu_lo, ws + L.xs, offs, counts, rows, H, I, E,
                                                dwgu, ctas, stream, dgu_lo2)));
-    MOE_TRY(stg.done(routing ? moe::launch_routed_dw(dwp, pos, routing->idx, idx, T, k, I, dlogits, stream)
+    MOE_TRY(stg.done(routing ? moe::launch_routed_dw(dwp, pos, T, k, I, dlogits, stream)
                              : moe::launch_dlogits(dwp, pos, idx, w, T, E, k, I, dlogits, stream)));
     if (opts) {
         opts->n_stages = stg.n;

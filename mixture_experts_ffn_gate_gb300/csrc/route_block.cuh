@@ -144,11 +144,18 @@ __device__ __forceinline__ void route_token_warp(const float *__restrict__ l, in
     w_j = lane < k ? ex / s : 0.0f;
 }
 
+// The weight of a dropped slot in the layer's kernels: -0, which neither the
+// router's softmax nor take_routing_warp gives to a slot in use.
+__device__ __forceinline__ bool is_dropped(float w) { return __float_as_uint(w) == 0x80000000u; }
+
 // A routing that the caller passes, for one token by one warp: lane j < k
-// gets slot j's expert and weight.  The layer's kernels need k distinct
-// experts in [0, E): a slot whose index is outside, or repeats an earlier
-// slot's, is dropped, i.e. takes the lowest expert that no other slot has,
-// with weight 0.
+// gets slot j's expert and weight.  A slot whose index is outside [0, E), or
+// repeats an earlier slot's, is dropped: it gets the weight of is_dropped,
+// which the sums over a token's slots leave out (its product may be infinite
+// or NaN), and the expert -1, which the sort leaves out.  The fused decode
+// kernel needs k distinct experts in [0, E): with STAND_IN a dropped slot
+// gets the lowest expert that no other slot has.
+template <bool STAND_IN>
 __device__ __forceinline__ void take_routing_warp(const int32_t *__restrict__ idx, const float *__restrict__ w, int E,
                                                   int k, int &sel_j, float &w_j)
 {
@@ -159,18 +166,21 @@ __device__ __forceinline__ void take_routing_warp(const int32_t *__restrict__ id
     const unsigned lower = (1u << lane) - 1u;
     const unsigned same = __match_any_sync(0xffffffffu, e);
     const bool used = lane < k && e >= 0 && e < E && (same & lower) == 0;
-    sel_j = used ? e : 0;
-    w_j = used ? *(const volatile float *)(w + lane) : 0.0f;
-    const unsigned dropped = __ballot_sync(0xffffffffu, lane < k && !used);
-    if (dropped) {
-        // k <= E: there are at least as many free experts as dropped slots
-        int next = 0;
-        const int want = __popc(dropped), place = __popc(dropped & lower);
-        for (int c = 0; c < E && next < want; ++c)
-            if (!__any_sync(0xffffffffu, used && e == c)) {
-                if ((dropped >> lane & 1) && place == next) sel_j = c;
-                ++next;
-            }
+    sel_j = used ? e : -1;
+    // + 0: a caller's -0 is a weight like +0
+    w_j = used ? __fadd_rn(*(const volatile float *)(w + lane), 0.0f) : -0.0f;
+    if constexpr (STAND_IN) {
+        const unsigned dropped = __ballot_sync(0xffffffffu, lane < k && !used);
+        if (dropped) {
+            // k <= E: there are at least as many free experts as dropped slots
+            int next = 0;
+            const int want = __popc(dropped), place = __popc(dropped & lower);
+            for (int c = 0; c < E && next < want; ++c)
+                if (!__any_sync(0xffffffffu, used && e == c)) {
+                    if ((dropped >> lane & 1) && place == next) sel_j = c;
+                    ++next;
+                }
+        }
     }
 }
 

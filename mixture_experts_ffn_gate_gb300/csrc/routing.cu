@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps) take_routing_kernel(const i
     if (t >= T) return;
     int e;
     float wt;
-    take_routing_warp(idx_in + (int64_t)t * k, w_in + (int64_t)t * k, E, k, e, wt);
+    take_routing_warp<false>(idx_in + (int64_t)t * k, w_in + (int64_t)t * k, E, k, e, wt);
     if (j < k) {
         idx[(int64_t)t * k + j] = e;
         w[(int64_t)t * k + j] = wt;
@@ -126,7 +126,8 @@ __global__ void __launch_bounds__(32 * kRouterWarps) router_gemv_kernel(const ui
 // i.e. the assignments of each expert end up in ascending a = token order.
 // With pad > 1 every expert's segment is rounded up to a multiple of pad
 // rows (offs are the padded offsets, the pad rows' perm is -1) and counts[e]
-// (nullable) gets the expert's number of assignments.
+// (nullable) gets the expert's number of assignments.  An assignment whose
+// expert is -1 (a dropped slot) takes no row; its pos is -1.
 constexpr int SORT_THREADS = 1024;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
 
@@ -173,7 +174,10 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_kernel(const int32_t *__res
     __syncthreads();
     const int per = (n_assign + SORT_WARPS - 1) / SORT_WARPS;
     const int a_begin = min(n_assign, warp * per), a_end = min(n_assign, a_begin + per);
-    for (int a = a_begin + lane; a < a_end; a += 32) atomicAdd(&hist[warp * E + idx[a]], 1);
+    for (int a = a_begin + lane; a < a_end; a += 32) {
+        const int ea = idx[a];
+        if (ea >= 0) atomicAdd(&hist[warp * E + ea], 1);
+    }
     __syncthreads();
 
     // E <= SORT_THREADS: thread e owns expert e
@@ -218,8 +222,8 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_kernel(const int32_t *__res
     const unsigned lt = (1u << lane) - 1u;
     for (int base = a_begin; base < a_end; base += 32) {
         const int a = base + lane;
-        const bool valid = a < a_end;
-        const int ea = valid ? idx[a] : -1;
+        const int ea = a < a_end ? idx[a] : -1;
+        const bool valid = ea >= 0;
         const unsigned same = __match_any_sync(0xffffffffu, ea);
         const int rank = __popc(same & lt);
         int p = 0;
@@ -227,6 +231,8 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_kernel(const int32_t *__res
             p = hist[warp * E + ea] + rank;
             perm[p] = a;
             pos[a] = p;
+        } else if (a < a_end) {
+            pos[a] = -1;
         }
         __syncwarp();
         if (valid && rank == 0) hist[warp * E + ea] += __popc(same);
@@ -235,8 +241,9 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_kernel(const int32_t *__res
 }
 
 // ---------------------------------------------------------------- combine
-// out[t, h] = sum_{j ascending} w[t,j] * z[pos[t*k+j], h]   (FP32, fixed order);
-// with w null the rows are summed unweighted (the backward pass's dx)
+// out[t, h] = sum_{j ascending} w[t,j] * z[pos[t*k+j], h]   (FP32, fixed order)
+// over the slots that have a row (pos >= 0); with w null the rows are summed
+// unweighted (the backward pass's dx)
 constexpr int kCombineBatch = 8;   // slots whose rows one thread loads together
 
 __global__ void combine_kernel(const float *__restrict__ z, const float *__restrict__ w,
@@ -256,16 +263,20 @@ __global__ void combine_kernel(const float *__restrict__ z, const float *__restr
         if (k <= kCombineBatch) {
             // every slot's row load in flight at once; the sum keeps slot order
             float4 v[kCombineBatch];
+            int p[kCombineBatch];
+#pragma unroll
+            for (int j = 0; j < kCombineBatch; ++j) p[j] = j < k ? __ldg(pos + (int64_t)t * k + j) : -1;
 #pragma unroll
             for (int j = 0; j < kCombineBatch; ++j)
-                if (j < k) v[j] = ld_nc_f4(z + (int64_t)__ldg(pos + (int64_t)t * k + j) * H + 4 * c);
+                if (p[j] >= 0) v[j] = ld_nc_f4(z + (int64_t)p[j] * H + 4 * c);
 #pragma unroll
             for (int j = 0; j < kCombineBatch; ++j)
-                if (j < k) add(w ? __ldg(w + (int64_t)t * k + j) : 1.0f, v[j]);
+                if (p[j] >= 0) add(w ? __ldg(w + (int64_t)t * k + j) : 1.0f, v[j]);
         } else {
-            for (int j = 0; j < k; ++j)
-                add(w ? __ldg(w + (int64_t)t * k + j) : 1.0f,
-                    ld_nc_f4(z + (int64_t)__ldg(pos + (int64_t)t * k + j) * H + 4 * c));
+            for (int j = 0; j < k; ++j) {
+                const int p = __ldg(pos + (int64_t)t * k + j);
+                if (p >= 0) add(w ? __ldg(w + (int64_t)t * k + j) : 1.0f, ld_nc_f4(z + (int64_t)p * H + 4 * c));
+            }
         }
         reinterpret_cast<float4 *>(out)[i] = acc;
     }

@@ -1,0 +1,128 @@
+"""The block's operators where they are easily wrong: slots without an
+expert beside experts that are not numbers.  Values against the same calls
+without the disturbance, bit for bit, and against the 64-bit definitions."""
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_ffn_gate_gb300 import moe_block as mb
+from mixture_experts_ffn_gate_gb300 import moe_ffn as m
+from tests import block_ref as ref
+from tests.test_gpu_block import dev, f64, layer, randn
+
+pytestmark = pytest.mark.gpu
+
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(autouse=True)
+def _no_faults():
+    m.moe_ffn_device_faults(clear=True)
+    yield
+    assert m.moe_ffn_device_faults(clear=True) == 0, "a kernel's bounded wait gave up"
+
+
+# ------------------------------------------------------------------ dropped slots
+UNUSED = 4  # the experts that no slot uses are the lowest
+
+
+def masked_routing(T, E, k, seed=0):
+    """A routing over the experts from UNUSED on, a third of its slots dropped
+    (the first token's all): (idx, w, which are dropped)."""
+    r = np.random.default_rng(seed)
+    idx = np.stack([UNUSED + r.permutation(E - UNUSED)[:k] for _ in range(T)]).astype(np.int64)
+    w = r.normal(size=(T, k)).astype(np.float32)
+    for t in range(T):
+        for j in range(1, k):
+            if r.random() < 0.4:
+                idx[t, j] = [-1, E, idx[t, 0], -7][r.integers(4)]
+    idx[0] = -1
+    if T > 1:
+        idx[1] = [UNUSED] + [UNUSED] * (k - 1)
+    dropped = np.array([[not 0 <= idx[t, j] < E or idx[t, j] in idx[t, :j] for j in range(k)] for t in range(T)])
+    return idx, w, dropped
+
+
+def options(path):
+    o = m.moe_ffn_opts()
+    o.path = path
+    return o
+
+
+@pytest.mark.parametrize("T,path", [(1, m.MOE_PATH_AUTO), (2, m.MOE_PATH_AUTO), (4, m.MOE_PATH_AUTO),
+                                    (9, m.MOE_PATH_DECODE), (2, m.MOE_PATH_GROUPED), (30, m.MOE_PATH_GROUPED),
+                                    (90, m.MOE_PATH_AUTO)])
+@pytest.mark.parametrize("k", [3, 9])
+def test_dropped_slots_add_nothing(T, path, k):
+    """Neither through their weights nor through an expert that stands in for them."""
+    H, I, E = 256, 128, 16
+    x, wgu, wd = layer(T, H, I, E, seed=40)
+    idx, w, dropped = masked_routing(T, E, k, seed=T + k)
+    clean = np.where(dropped, np.float32(0), w)
+    args = dev(idx, torch.int32), dev(clean)
+    want = mb.moe_ffn_forward_routed(x, *args, wgu, wd, opts=options(path))
+    exact = ref.experts(f64(x), idx, clean.astype(np.float64), f64(wgu), f64(wd))
+    assert ref.rel(f64(want), exact) <= 1e-5  # the two sides' own check: test_gpu_block.py has the tolerance
+    gu_bad, d_bad = wgu.clone(), wd.clone()
+    gu_bad[0], d_bad[1], d_bad[2], gu_bad[3] = NAN, INF, -INF, INF
+    w_bad = np.where(dropped, np.float32([NAN, INF, -INF])[np.arange(T * k).reshape(T, k) % 3], w)
+    got = mb.moe_ffn_forward_routed(x, args[0], dev(w_bad), gu_bad, d_bad, opts=options(path))
+    assert torch.equal(got, want) and not got[0].any()
+
+
+@pytest.mark.parametrize("T", [1, 3, 7, 30])
+def test_dropped_slots_add_nothing_with_mxfp8_weights(T):
+    from mixture_experts_ffn_gate_gb300 import synth
+    from tests import gpu_util as gu
+    wl = gu.custom(T, 256, 128, 16, 3, name="dropped_mx")
+    gq, gs, dq, ds = (t.cuda() for t in synth.make_weights_mxfp8(wl))
+    x, _ = (t.cuda() for t in synth.make_tokens(wl, T))
+    idx, w, dropped = masked_routing(T, 16, 3, seed=T)
+    idx = dev(idx, torch.int32)
+    want = mb.moe_ffn_forward_routed(x, idx, dev(np.where(dropped, np.float32(0), w)), gq, dq, w_gate_up_scale=gs,
+                                     w_down_scale=ds)
+    gq_bad = gq.clone()
+    gq_bad[:UNUSED] = 0x7f  # the code of NaN
+    got = mb.moe_ffn_forward_routed(x, idx, dev(np.where(dropped, np.float32(NAN), w)), gq_bad, dq,
+                                    w_gate_up_scale=gs, w_down_scale=ds)
+    assert torch.equal(got, want) and torch.isfinite(got).all()
+
+
+@pytest.mark.parametrize("T,k", [(1, 3), (5, 9), (40, 3), (300, 2)])
+def test_dropped_slots_have_no_gradient(T, k):
+    H, I, E = 192, 128, 16
+    x, wgu, wd = layer(T, H, I, E, seed=50)
+    idx, w, dropped = masked_routing(T, E, k, seed=T + k)
+    dout, clean = randn(T, H, seed=60), np.where(dropped, np.float32(0), w)
+    ti = dev(idx, torch.int32)
+    want = mb.moe_ffn_backward_routed(x, ti, dev(clean), wgu, wd, dout)
+    exact = ref.experts_grad(f64(x), idx, clean.astype(np.float64), f64(wgu), f64(wd), f64(dout))
+    for g, r in zip((want[0], want[2], want[3]), (exact[0], exact[2], exact[3])):
+        assert ref.rel(f64(g), r) <= 1e-5
+    # experts and a token that no slot reaches, and the weights of dropped slots
+    gu_bad, d_bad, x_bad, dout_bad = wgu.clone(), wd.clone(), x.clone(), dout.clone()
+    gu_bad[0], d_bad[1], gu_bad[2], x_bad[0], dout_bad[0] = NAN, INF, -INF, INF, INF
+    args = x_bad, ti, dev(np.where(dropped, np.float32(NAN), w)), gu_bad, d_bad
+    state = m.new_train_state(T, H, I, E, k)
+    out = mb.moe_ffn_forward_routed_train(*args, state)
+    assert torch.isfinite(out).all() and not out[0].any()
+    for got in (mb.moe_ffn_backward_routed(*args, dout_bad), mb.moe_ffn_backward_routed(*args, dout_bad, state=state)):
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        assert not got[0][0].any() and not f64(got[1])[dropped].any()
+        assert not got[2][:UNUSED].any() and not got[3][:UNUSED].any()
+
+
+def test_a_weight_of_minus_zero_is_a_weight():
+    """Its slot is in use: the weight has a gradient and the output no change."""
+    x, wgu, wd = layer(6, 256, 128, 8, seed=70)
+    idx = dev(np.random.default_rng(1).permuted(np.tile(np.arange(8), (6, 1)), axis=1)[:, :3], torch.int32)
+    w, dout = randn(6, 3, seed=71), randn(6, 256, seed=72)
+    w[:, 1] = 0.0
+    minus = w.clone()
+    minus[:, 1] = -0.0
+    for o in (None, options(m.MOE_PATH_DECODE)):
+        a, b = (mb.moe_ffn_forward_routed(x, idx, v, wgu, wd, opts=o) for v in (w, minus))
+        assert torch.equal(a, b)
+    a, b = (mb.moe_ffn_backward_routed(x, idx, v, wgu, wd, dout) for v in (w, minus))
+    assert all(torch.equal(p, q) for p, q in zip(a, b)) and b[1][:, 1].all()
