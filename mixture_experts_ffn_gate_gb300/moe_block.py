@@ -15,7 +15,7 @@ from typing import NamedTuple
 import torch
 
 from . import moe_ffn as _m
-from .moe_ffn import MOE_ERR_UNSUPPORTED_SHAPE, MoeFfnError, mx_scale_bytes
+from .moe_ffn import MOE_ERR_UNSUPPORTED_SHAPE, MoeFfnError, _empty, mx_scale_bytes
 
 MOE_BF16 = 0
 MOE_F32 = 1
@@ -89,10 +89,10 @@ def _check(status, what):
         raise MoeFfnError(status, what)
 
 
-def _workspace(n, device, what):
+def _workspace(n, device, stream, what):
     if n == 0:
         raise MoeFfnError(MOE_ERR_UNSUPPORTED_SHAPE, what)
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    return _empty((n,), torch.uint8, device, stream)
 
 
 def _size(t):
@@ -122,7 +122,7 @@ def moe_rms_norm_forward(x, weight, residual=None, eps: float = 1e-6, bf16: bool
         rt = _type(residual, "residual")
         _is(residual, (T, H), residual.dtype, "residual")
         if h is None:
-            h = torch.empty_like(residual)
+            h = _empty((T, H), residual.dtype, dev, stream)
         else:
             _is(h, (T, H), residual.dtype, "h")
     elif h is not None:
@@ -130,13 +130,13 @@ def moe_rms_norm_forward(x, weight, residual=None, eps: float = 1e-6, bf16: bool
     if y is not None:
         _is(y, (T, H), torch.bfloat16, "y")
     elif bf16:
-        y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        y = _empty((T, H), torch.bfloat16, dev, stream)
     if codes is not None or scales is not None or mxfp8:
         Sh = mx_scale_bytes(H)
         if codes is None:
-            codes = torch.empty((T, H), dtype=torch.uint8, device=dev)
+            codes = _empty((T, H), torch.uint8, dev, stream)
         if scales is None:
-            scales = torch.empty((T, Sh), dtype=torch.uint8, device=dev)
+            scales = _empty((T, Sh), torch.uint8, dev, stream)
         _is(codes, (T, H), torch.uint8, "codes")
         _is(scales, (T, Sh), torch.uint8, "scales")
     p = _ptr
@@ -149,8 +149,8 @@ def moe_rms_norm_backward_workspace_bytes(T, H) -> int:
     return int(_m.lib().moe_rms_norm_backward_workspace_bytes(T, H))
 
 
-def new_rms_norm_backward_workspace(T, H, device="cuda"):
-    return _workspace(moe_rms_norm_backward_workspace_bytes(T, H), device, "workspace size")
+def new_rms_norm_backward_workspace(T, H, device="cuda", stream=None):
+    return _workspace(moe_rms_norm_backward_workspace_bytes(T, H), device, stream, "workspace size")
 
 
 def moe_rms_norm_backward(h, weight, dy, dres=None, eps: float = 1e-6, dh=None, dweight=None, workspace=None,
@@ -166,15 +166,15 @@ def moe_rms_norm_backward(h, weight, dy, dres=None, eps: float = 1e-6, dh=None, 
     if dres is not None:
         _is(dres, (T, H), h.dtype, "dres")
     if dh is None:
-        dh = torch.empty_like(h)
+        dh = _empty((T, H), h.dtype, h.device, stream)
     else:
         _is(dh, (T, H), h.dtype, "dh")
     if dweight is None:
-        dweight = torch.empty((H,), dtype=torch.float32, device=h.device)
+        dweight = _empty((H,), torch.float32, h.device, stream)
     else:
         _is(dweight, (H,), torch.float32, "dweight")
     if workspace is None:
-        workspace = new_rms_norm_backward_workspace(T, H, device=h.device)
+        workspace = new_rms_norm_backward_workspace(T, H, device=h.device, stream=stream)
     p = _ptr
     _check(_lib().moe_rms_norm_backward(p(h), ht, p(weight), p(dy), gt, p(dres), eps, T, H, p(dh), p(dweight),
                                         p(workspace), _size(workspace), _stream(stream, h.device)),
@@ -210,15 +210,15 @@ def moe_gate_forward(logits, k: int, bias=None, score: str = "softmax", groups: 
         _is(bias, (E,), torch.float32, "bias")
     dev = logits.device
     if topk_idx is None:
-        topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+        topk_idx = _empty((T, k), torch.int32, dev, stream)
     else:
         _is(topk_idx, (T, k), torch.int32, "topk_idx")
     if topk_w is None:
-        topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+        topk_w = _empty((T, k), torch.float32, dev, stream)
     else:
         _is(topk_w, (T, k), torch.float32, "topk_w")
     if counts is True:
-        counts = torch.empty((E,), dtype=torch.int32, device=dev)
+        counts = _empty((E,), torch.int32, dev, stream)
     elif counts is not None:
         _is(counts, (E,), torch.int32, "counts")
     o = _gate_opts(score, renormalize, scale, groups, topk_groups)
@@ -239,7 +239,7 @@ def moe_gate_backward(logits, topk_idx, dtopk_w, score: str = "softmax", renorma
     _is(topk_idx, (T, k), torch.int32, "topk_idx")
     _is(dtopk_w, (T, k), torch.float32, "dtopk_w")
     if dlogits is None:
-        dlogits = torch.empty_like(logits)
+        dlogits = _empty((T, E), torch.float32, logits.device, stream)
     else:
         _is(dlogits, (T, E), torch.float32, "dlogits")
     o = _gate_opts(score, renormalize, scale)
@@ -279,9 +279,9 @@ def _experts(x, w_gate_up, w_down, dtype=torch.bfloat16):
     return T, H, I, E
 
 
-def _new(t, shape, name, device):
+def _new(t, shape, name, device, stream):
     if t is None:
-        return torch.empty(shape, dtype=torch.float32, device=device)
+        return _empty(shape, torch.float32, device, stream)
     _is(t, shape, torch.float32, name)
     return t
 
@@ -304,9 +304,9 @@ def moe_ffn_forward_routed(x, topk_idx, topk_w, w_gate_up, w_down, x_scale=None,
     if w_down_scale is not None:
         _is(w_gate_up_scale, (E, 2 * I, mx_scale_bytes(H)), torch.uint8, "w_gate_up_scale")
         _is(w_down_scale, (E, H, mx_scale_bytes(I)), torch.uint8, "w_down_scale")
-    out = _new(out, (T, H), "out", x.device)
+    out = _new(out, (T, H), "out", x.device, stream)
     if workspace is None:
-        workspace = new_routed_workspace(T, H, I, E, k, device=x.device)
+        workspace = new_routed_workspace(T, H, I, E, k, device=x.device, stream=stream)
     p = _ptr
     _check(_lib().moe_ffn_forward_routed(
         p(x), p(x_scale), p(topk_idx), p(topk_w), p(w_gate_up), p(w_gate_up_scale), p(w_down), p(w_down_scale), T, H,
@@ -322,7 +322,7 @@ def moe_ffn_forward_routed_train(x, topk_idx, topk_w, w_gate_up, w_down, state, 
     T, H, I, E = _experts(x, w_gate_up, w_down)
     k = _routing(topk_idx, topk_w, T)
     _is(x, (T, H), torch.bfloat16, "x")
-    out = _new(out, (T, H), "out", x.device)
+    out = _new(out, (T, H), "out", x.device, stream)
     p = _ptr
     _check(_lib().moe_ffn_forward_routed_train(
         p(x), p(topk_idx), p(topk_w), p(w_gate_up), p(w_down), T, H, I, E, k, p(out), p(state), _size(state),
@@ -342,15 +342,15 @@ def moe_ffn_backward_routed(x, topk_idx, topk_w, w_gate_up, w_down, dout, dx=Non
     _is(x, (T, H), torch.bfloat16, "x")
     _is(dout, (T, H), torch.float32, "dout")
     dev = x.device
-    dx = _new(dx, (T, H), "dx", dev)
-    dtopk_w = _new(dtopk_w, (T, k), "dtopk_w", dev)
-    dw_gate_up = _new(dw_gate_up, (E, 2 * I, H), "dw_gate_up", dev)
-    dw_down = _new(dw_down, (E, H, I), "dw_down", dev)
+    dx = _new(dx, (T, H), "dx", dev, stream)
+    dtopk_w = _new(dtopk_w, (T, k), "dtopk_w", dev, stream)
+    dw_gate_up = _new(dw_gate_up, (E, 2 * I, H), "dw_gate_up", dev, stream)
+    dw_down = _new(dw_down, (E, H, I), "dw_down", dev, stream)
     if state is not None and workspace is not None:
         raise ValueError("pass a workspace or a state, not both")
     ws = state if state is not None else workspace
     if ws is None:
-        ws = _m.new_backward_workspace(T, H, I, E, k, device=dev)
+        ws = _m.new_backward_workspace(T, H, I, E, k, device=dev, stream=stream)
     p = _ptr
     _check(_lib().moe_ffn_backward_routed(
         p(x), p(topk_idx), p(topk_w), p(w_gate_up), p(w_down), p(dout), T, H, I, E, k, p(dx), p(dtopk_w),
@@ -364,8 +364,8 @@ def moe_orthogonalize_workspace_bytes(B, M, N) -> int:
     return int(_m.lib().moe_orthogonalize_workspace_bytes(B, M, N))
 
 
-def new_orthogonalize_workspace(B, M, N, device="cuda"):
-    return _workspace(moe_orthogonalize_workspace_bytes(B, M, N), device, "workspace size")
+def new_orthogonalize_workspace(B, M, N, device="cuda", stream=None):
+    return _workspace(moe_orthogonalize_workspace_bytes(B, M, N), device, stream, "workspace size")
 
 
 def moe_orthogonalize(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,
@@ -377,11 +377,11 @@ def moe_orthogonalize(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
     gt = _type(g, "g")
     _is(g, (B, M, N), g.dtype, "g")
     if out is None:
-        out = torch.empty((B, M, N), dtype=torch.bfloat16, device=g.device)
+        out = _empty((B, M, N), torch.bfloat16, g.device, stream)
     else:
         _is(out, (B, M, N), torch.bfloat16, "out")
     if workspace is None:
-        workspace = new_orthogonalize_workspace(B, M, N, device=g.device) if B else g.new_empty(0)
+        workspace = new_orthogonalize_workspace(B, M, N, device=g.device, stream=stream) if B else g.new_empty(0)
     a, b, c = coefficients
     p = _ptr
     _check(_lib().moe_orthogonalize(p(g), gt, B, M, N, steps, a, b, c, eps, out_scale, p(out), p(workspace),

@@ -7,6 +7,7 @@ fallback: if the library is not built, ``lib()`` raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -148,6 +149,44 @@ def _stream(stream):
     return int(stream)
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _on(stream, device):
+    """The context of torch work in the order of a call on `stream`."""
+    if stream is None or _stream(stream) == torch.cuda.current_stream(device).cuda_stream:
+        return _HERE
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream=None):
+    """A tensor that a call on `stream` writes.  It is allocated on that
+    stream: what used its memory before, and what uses it after it is
+    dropped, is ordered with the call.  Released, it also waits for the
+    current stream's work of that moment, which may read it."""
+    here = _on(stream, device)
+    if here is _HERE:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with here:
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _state_buffer(n, device, stream, what):
+    """n bytes with the fused decode kernel's state zeroed: torch's caching
+    allocator may hand out memory that served as another workspace and then
+    held other data."""
+    if n == 0:
+        raise MoeFfnError(MOE_ERR_UNSUPPORTED_SHAPE, what)
+    ws = _empty((n,), torch.uint8, device, stream)
+    with _on(stream, device):
+        ws[:MOE_FFN_WORKSPACE_STATE_BYTES].zero_()
+    return ws
+
+
 def _check(status, what):
     if status != MOE_OK:
         raise MoeFfnError(status, what)
@@ -205,7 +244,7 @@ def moe_ffn_forward(x, logits, w_gate_up, w_down, k: int, out=None, stream=None)
                     (w_gate_up, torch.bfloat16, "w_gate_up"), (w_down, torch.bfloat16, "w_down")):
         _dev(t, d, n)
     if out is None:
-        out = torch.empty((T, H), dtype=torch.float32, device=x.device)
+        out = _empty((T, H), torch.float32, x.device, stream)
     _dev(out, torch.float32, "out")
     _check(lib().moe_ffn_forward(_ptr(x), _ptr(logits), _ptr(w_gate_up), _ptr(w_down),
                                  T, H, I, E, k, _ptr(out), _stream(stream)), "moe_ffn_forward")
@@ -223,7 +262,7 @@ def moe_ffn_forward_noalloc(x, logits, w_gate_up, w_down, k: int, out=None, stre
                     (w_gate_up, torch.bfloat16, "w_gate_up"), (w_down, torch.bfloat16, "w_down")):
         _dev(t, d, n)
     if out is None:
-        out = torch.empty((T, H), dtype=torch.float32, device=x.device)
+        out = _empty((T, H), torch.float32, x.device, stream)
     _dev(out, torch.float32, "out")
     _check(lib().moe_ffn_forward_noalloc(_ptr(x), _ptr(logits), _ptr(w_gate_up), _ptr(w_down),
                                          T, H, I, E, k, _ptr(out), _stream(stream)),
@@ -231,18 +270,13 @@ def moe_ffn_forward_noalloc(x, logits, w_gate_up, w_down, k: int, out=None, stre
     return out
 
 
-def new_workspace(T, H, I, E, k, device="cuda", host=False):
-    """A workspace tensor big enough for this shape (256-byte aligned),
-    moe_block.moe_ffn_forward_routed's too unless it is for the host entry.
-
-    Its state bytes are zeroed: torch's caching allocator may hand out
-    memory that served as another workspace and then held other data."""
+def new_workspace(T, H, I, E, k, device="cuda", host=False, stream=None):
+    """A workspace tensor big enough for this shape (256-byte aligned), its
+    state bytes zeroed; moe_block.moe_ffn_forward_routed's too unless it is
+    for the host entry.  ``stream``: the one that the calls run on (default:
+    torch's current stream)."""
     n = moe_ffn_host_workspace_bytes(T, H, I, E, k) if host else lib().moe_ffn_routed_workspace_bytes(T, H, I, E, k)
-    if n == 0:
-        raise MoeFfnError(MOE_ERR_UNSUPPORTED_SHAPE, "workspace size")
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
-    ws[:MOE_FFN_WORKSPACE_STATE_BYTES].zero_()
-    return ws
+    return _state_buffer(n, device, stream, "workspace size")
 
 
 def moe_ffn_forward_ex(x, logits, w_gate_up, w_down, k: int, out=None, workspace=None,
@@ -255,9 +289,9 @@ def moe_ffn_forward_ex(x, logits, w_gate_up, w_down, k: int, out=None, workspace
                     (w_gate_up, torch.bfloat16, "w_gate_up"), (w_down, torch.bfloat16, "w_down")):
         _dev(t, d, n)
     if out is None:
-        out = torch.empty((T, H), dtype=torch.float32, device=x.device)
+        out = _empty((T, H), torch.float32, x.device, stream)
     if workspace is None:
-        workspace = new_workspace(T, H, I, E, k, device=x.device)
+        workspace = new_workspace(T, H, I, E, k, device=x.device, stream=stream)
     if topk_idx is not None:
         _dev(topk_idx, torch.int32, "topk_idx")
     if topk_w is not None:
@@ -274,14 +308,9 @@ def moe_ffn_router_workspace_bytes(T, H, I, E, k) -> int:
     return int(lib().moe_ffn_router_workspace_bytes(T, H, I, E, k))
 
 
-def new_router_workspace(T, H, I, E, k, device="cuda"):
+def new_router_workspace(T, H, I, E, k, device="cuda", stream=None):
     """A workspace for moe_ffn_forward_router (state bytes zeroed)."""
-    n = moe_ffn_router_workspace_bytes(T, H, I, E, k)
-    if n == 0:
-        raise MoeFfnError(MOE_ERR_UNSUPPORTED_SHAPE, "workspace size")
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
-    ws[:MOE_FFN_WORKSPACE_STATE_BYTES].zero_()
-    return ws
+    return _state_buffer(moe_ffn_router_workspace_bytes(T, H, I, E, k), device, stream, "workspace size")
 
 
 def moe_ffn_forward_router(x, w_router, router_bias, w_gate_up, w_down, k: int, out=None,
@@ -306,9 +335,9 @@ def moe_ffn_forward_router(x, w_router, router_bias, w_gate_up, w_down, k: int, 
         if t is not None:
             _dev(t, d, n)
     if out is None:
-        out = torch.empty((T, H), dtype=torch.float32, device=x.device)
+        out = _empty((T, H), torch.float32, x.device, stream)
     if workspace is None:
-        workspace = new_router_workspace(T, H, I, E, k, device=x.device)
+        workspace = new_router_workspace(T, H, I, E, k, device=x.device, stream=stream)
     _check(lib().moe_ffn_forward_router(
         _ptr(x), _ptr(w_router), _ptr(router_bias), _ptr(w_gate_up), _ptr(w_down), T, H, I, E, k,
         _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(logits),
@@ -347,9 +376,9 @@ def moe_ffn_forward_mxfp8(x, logits, w_gate_up_q, w_gate_up_s, w_down_q, w_down_
         if t is not None:
             _dev(t, d, n)
     if out is None:
-        out = torch.empty((T, H), dtype=torch.float32, device=x.device)
+        out = _empty((T, H), torch.float32, x.device, stream)
     if workspace is None:
-        workspace = new_workspace(T, H, I, E, k, device=x.device)
+        workspace = new_workspace(T, H, I, E, k, device=x.device, stream=stream)
     _check(lib().moe_ffn_forward_mxfp8(
         _ptr(x), _ptr(logits), _ptr(w_gate_up_q), _ptr(w_gate_up_s), _ptr(w_down_q), _ptr(w_down_s),
         T, H, I, E, k, _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -380,15 +409,11 @@ def moe_ffn_backward_workspace_bytes(T, H, I, E, k) -> int:
     return int(lib().moe_ffn_backward_workspace_bytes(T, H, I, E, k))
 
 
-def new_backward_workspace(T, H, I, E, k, device="cuda"):
+def new_backward_workspace(T, H, I, E, k, device="cuda", stream=None):
     """A workspace for moe_ffn_backward and moe_block.moe_ffn_backward_routed
     (state bytes zeroed, so that forward calls may share it)."""
-    n = lib().moe_ffn_routed_backward_workspace_bytes(T, H, I, E, k)
-    if n == 0:
-        raise MoeFfnError(MOE_ERR_UNSUPPORTED_SHAPE, "workspace size")
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
-    ws[:MOE_FFN_WORKSPACE_STATE_BYTES].zero_()
-    return ws
+    return _state_buffer(lib().moe_ffn_routed_backward_workspace_bytes(T, H, I, E, k), device, stream,
+                         "workspace size")
 
 
 def moe_ffn_backward(x, logits, w_gate_up, w_down, dout, k: int, dx=None, dlogits=None, dw_gate_up=None,
@@ -405,13 +430,13 @@ def moe_ffn_backward(x, logits, w_gate_up, w_down, dout, k: int, dx=None, dlogit
         raise ValueError(f"dout must be [{T}, {H}], got {tuple(dout.shape)}")
     dev = x.device
     if dx is None:
-        dx = torch.empty((T, H), dtype=torch.float32, device=dev)
+        dx = _empty((T, H), torch.float32, dev, stream)
     if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=torch.float32, device=dev)
+        dlogits = _empty((T, E), torch.float32, dev, stream)
     if dw_gate_up is None:
-        dw_gate_up = torch.empty((E, 2 * I, H), dtype=torch.float32, device=dev)
+        dw_gate_up = _empty((E, 2 * I, H), torch.float32, dev, stream)
     if dw_down is None:
-        dw_down = torch.empty((E, H, I), dtype=torch.float32, device=dev)
+        dw_down = _empty((E, H, I), torch.float32, dev, stream)
     for t, shape, n in ((dx, (T, H), "dx"), (dlogits, (T, E), "dlogits"), (dw_gate_up, (E, 2 * I, H), "dw_gate_up"),
                         (dw_down, (E, H, I), "dw_down")):
         _dev(t, torch.float32, n)
@@ -429,15 +454,10 @@ def moe_ffn_train_state_bytes(T, H, I, E, k) -> int:
     return int(lib().moe_ffn_train_state_bytes(T, H, I, E, k))
 
 
-def new_train_state(T, H, I, E, k, device="cuda"):
+def new_train_state(T, H, I, E, k, device="cuda", stream=None):
     """A state buffer for the training pair (moe_ffn_forward_train, then
     moe_ffn_backward_train; or moe_block's routed pair)."""
-    n = lib().moe_ffn_routed_backward_workspace_bytes(T, H, I, E, k)
-    if n == 0:
-        raise MoeFfnError(MOE_ERR_UNSUPPORTED_SHAPE, "state size")
-    st = torch.empty(n, dtype=torch.uint8, device=device)
-    st[:MOE_FFN_WORKSPACE_STATE_BYTES].zero_()
-    return st
+    return _state_buffer(lib().moe_ffn_routed_backward_workspace_bytes(T, H, I, E, k), device, stream, "state size")
 
 
 def moe_ffn_forward_train(x, logits, w_gate_up, w_down, k: int, state, out=None,
@@ -450,7 +470,7 @@ def moe_ffn_forward_train(x, logits, w_gate_up, w_down, k: int, state, out=None,
                     (state, torch.uint8, "state")):
         _dev(t, d, n)
     if out is None:
-        out = torch.empty((T, H), dtype=torch.float32, device=x.device)
+        out = _empty((T, H), torch.float32, x.device, stream)
     _dev(out, torch.float32, "out")
     if tuple(out.shape) != (T, H):
         raise ValueError(f"out must be [{T}, {H}], got {tuple(out.shape)}")
@@ -475,13 +495,13 @@ def moe_ffn_backward_train(x, logits, w_gate_up, w_down, dout, k: int, state, dx
         raise ValueError(f"dout must be [{T}, {H}], got {tuple(dout.shape)}")
     dev = x.device
     if dx is None:
-        dx = torch.empty((T, H), dtype=torch.float32, device=dev)
+        dx = _empty((T, H), torch.float32, dev, stream)
     if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=torch.float32, device=dev)
+        dlogits = _empty((T, E), torch.float32, dev, stream)
     if dw_gate_up is None:
-        dw_gate_up = torch.empty((E, 2 * I, H), dtype=torch.float32, device=dev)
+        dw_gate_up = _empty((E, 2 * I, H), torch.float32, dev, stream)
     if dw_down is None:
-        dw_down = torch.empty((E, H, I), dtype=torch.float32, device=dev)
+        dw_down = _empty((E, H, I), torch.float32, dev, stream)
     for t, shape, n in ((dx, (T, H), "dx"), (dlogits, (T, E), "dlogits"), (dw_gate_up, (E, 2 * I, H), "dw_gate_up"),
                         (dw_down, (E, H, I), "dw_down")):
         _dev(t, torch.float32, n)

@@ -1,5 +1,5 @@
 """The block's operators where they are easily wrong: slots without an
-expert beside experts that are not numbers.  Values against the same calls
+expert beside experts that are not numbers, calls on other streams.  Values against the same calls
 without the disturbance, bit for bit, and against the 64-bit definitions."""
 import numpy as np
 import pytest
@@ -126,3 +126,43 @@ def test_a_weight_of_minus_zero_is_a_weight():
         assert torch.equal(a, b)
     a, b = (mb.moe_ffn_backward_routed(x, idx, v, wgu, wd, dout) for v in (w, minus))
     assert all(torch.equal(p, q) for p, q in zip(a, b)) and b[1][:, 1].all()
+
+
+# ------------------------------------------------------------------ streams
+def stream_calls(T=12):
+    """The calls that make a workspace of their own."""
+    H, I, E, k = 512, 256, 16, 4
+    x, wgu, wd = layer(T, H, I, E, seed=80)
+    r = np.random.default_rng(2)
+    idx = dev(np.stack([r.permutation(E)[:k] for _ in range(T)]), torch.int32)
+    w, dout, logits, nw = randn(T, k, seed=81), randn(T, H, seed=82), randn(T, E, seed=83), randn(H, seed=84)
+    wr, batch = randn(E, H, seed=85, dtype=torch.bfloat16), randn(3, 300, 400, seed=86)
+    return {
+        "norm_backward": lambda **s: mb.moe_rms_norm_backward(x, nw, dout, **s),
+        "routed": lambda **s: (mb.moe_ffn_forward_routed(x, idx, w, wgu, wd, **s),),
+        "routed_decode": lambda **s: (mb.moe_ffn_forward_routed(x[:2], idx[:2], w[:2], wgu, wd, **s),),
+        "routed_backward": lambda **s: mb.moe_ffn_backward_routed(x, idx, w, wgu, wd, dout, **s),
+        "orthogonalize": lambda **s: (mb.moe_orthogonalize(batch, **s),),
+        "forward_ex": lambda **s: (m.moe_ffn_forward_ex(x, logits, wgu, wd, k, **s),),
+        "router": lambda **s: (m.moe_ffn_forward_router(x[:2], wr, None, wgu, wd, k, **s),),
+    }
+
+
+@pytest.mark.parametrize("name", ["norm_backward", "routed", "routed_decode", "routed_backward", "orthogonalize",
+                                  "forward_ex", "router"])
+@pytest.mark.parametrize("by_handle", [False, True])
+def test_calls_on_another_stream_keep_their_workspace(name, by_handle):
+    """The call waits on its stream while the current one takes and fills all
+    the memory that torch has given back."""
+    call = stream_calls()[name]
+    want = [t.clone() for t in call()]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+    got = call(stream=side.cuda_stream if by_handle else side)
+    waste = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (1 << 12, 1 << 16, 1 << 20, 1 << 22) * 8]
+    side.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    del waste
