@@ -9,6 +9,7 @@ training steps of a small block on synthetic data, and prints the loss.
 """
 from __future__ import annotations
 
+import collections
 import dataclasses
 import math
 
@@ -44,14 +45,26 @@ class MoeBlock:
         self.norm_weight, self.w_router, self.balance_bias = norm_weight, w_router, balance_bias
         self.w_gate_up, self.w_down, self.gate, self.eps = w_gate_up, w_down, gate, eps
         self.E, self.H, self.I = w_down.shape
-        self._buffers: dict = {}
+        self._serving: collections.OrderedDict = collections.OrderedDict()
 
-    def _buffer(self, name, T, make):
-        """A workspace kept between steps of the same number of tokens."""
-        key = (name, T)
-        if key not in self._buffers:
-            self._buffers[key] = make()
-        return self._buffers[key]
+    # Serving workspaces that are kept: the fused decode kernel is quicker on
+    # one that it has used before.
+    KEPT = 8
+
+    def _serving_workspace(self, T, device):
+        """The workspace of the serving steps of T tokens on the current
+        stream; of those least recently used only KEPT stay.  A step that is
+        being captured has its own, which lives as long as its graph."""
+        if torch.cuda.is_current_stream_capturing():
+            return mb.new_routed_workspace(*self._shape(T), device=device)
+        key = (T, torch.cuda.current_stream(device).cuda_stream)
+        ws = self._serving.pop(key, None)
+        if ws is None:
+            ws = mb.new_routed_workspace(*self._shape(T), device=device)
+        self._serving[key] = ws
+        if len(self._serving) > self.KEPT:
+            self._serving.popitem(last=False)
+        return ws
 
     def _shape(self, T):
         return T, self.H, self.I, self.E, self.gate.k
@@ -71,18 +84,20 @@ class MoeBlock:
         T = x.shape[0]
         n = mb.moe_rms_norm_forward(x, self.norm_weight, residual=residual, eps=self.eps, mxfp8=mxfp8_tokens)
         _, choice = self.choose(n.y)
-        ws = self._buffer("serve", T, lambda: mb.new_routed_workspace(*self._shape(T), device=x.device))
+        ws = self._serving_workspace(T, x.device)
         tokens = dict(x=n.codes, x_scale=n.scales) if mxfp8_tokens else dict(x=n.y)
         out = mb.moe_ffn_forward_routed(topk_idx=choice.topk_idx, topk_w=choice.topk_w, w_gate_up=self.w_gate_up,
                                         w_down=self.w_down, workspace=ws, **tokens)
         return out, n.h, choice.counts
 
     def train_forward(self, x, residual):
-        """The forward pass of a training step: (out, new stream, saved)."""
+        """The forward pass of a training step: (out, new stream, saved).
+        `saved` holds this call's own state (g and u of every assignment), so
+        any number of forward calls may come before their backward calls."""
         T = x.shape[0]
         n = mb.moe_rms_norm_forward(x, self.norm_weight, residual=residual, eps=self.eps)
         logits, choice = self.choose(n.y)
-        state = self._buffer("state", T, lambda: m.new_train_state(*self._shape(T), device=x.device))
+        state = m.new_train_state(*self._shape(T), device=x.device)
         out = mb.moe_ffn_forward_routed_train(n.y, choice.topk_idx, choice.topk_w, self.w_gate_up, self.w_down, state)
         return out, n.h, (n.y, n.h, logits, choice, state)
 
@@ -91,13 +106,11 @@ class MoeBlock:
         reaches the new stream besides): a dict; "x" is that of both x and the
         residual."""
         y, h, logits, choice, state = saved
-        T = y.shape[0]
         dy, dw, dw_gate_up, dw_down = mb.moe_ffn_backward_routed(y, choice.topk_idx, choice.topk_w, self.w_gate_up,
                                                                  self.w_down, dout, state=state)
         dlogits = mb.moe_gate_backward(logits, choice.topk_idx, dw, **self.gate.backward_args())
         dy = torch.addmm(dy, dlogits, self.w_router)
-        ws = self._buffer("norm", T, lambda: mb.new_rms_norm_backward_workspace(T, self.H, device=y.device))
-        dx, dnorm = mb.moe_rms_norm_backward(h, self.norm_weight, dy, dres=dstream, eps=self.eps, workspace=ws)
+        dx, dnorm = mb.moe_rms_norm_backward(h, self.norm_weight, dy, dres=dstream, eps=self.eps)
         return dict(x=dx, norm_weight=dnorm, w_router=torch.matmul(dlogits.t(), y.float()), w_gate_up=dw_gate_up,
                     w_down=dw_down, loads=choice.counts)
 
@@ -106,9 +119,8 @@ class MoeBlock:
         the others by the gradients, and the balance bias against the loads."""
         for name in ("w_gate_up", "w_down"):
             g, w = grads[name], getattr(self, name)
-            B, M, N = g.shape
-            ws = self._buffer(name, 0, lambda: mb.new_orthogonalize_workspace(B, M, N, device=g.device))
-            step = mb.moe_orthogonalize(g, out_scale=-experts_lr * math.sqrt(max(1.0, M / N)), workspace=ws)
+            _, M, N = g.shape
+            step = mb.moe_orthogonalize(g, out_scale=-experts_lr * math.sqrt(max(1.0, M / N)))
             w.add_(step)
         self.norm_weight.add_(grads["norm_weight"], alpha=-lr)
         self.w_router.add_(grads["w_router"], alpha=-lr)
