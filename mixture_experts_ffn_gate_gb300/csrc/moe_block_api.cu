@@ -59,6 +59,39 @@ bool ortho_shape(int64_t B, int64_t M, int64_t N)
            B * ((M + 127) / 128) * ((N + 127) / 128) <= ((int64_t)1 << 24);
 }
 
+// Whether what the steps store in FP16 stays in its range, whatever the
+// matrix: X's singular values lie in [0, top], top = 1 at the start and then
+// the largest |s (a + b s^2 + c s^4)| there, one part in a hundred more for
+// the roundings; A = X X^T is stored times 2^14 (an entry overflows where top
+// reaches 2), b A + c A A times 2^11 (at 32).  The last step's X is not
+// stored in FP16.
+bool ortho_in_range(double a, double b, double c, int steps)
+{
+    double top = 1.0;
+    for (int i = 0; i < steps; ++i) {
+        if (!(top <= 1.9)) return false;
+        const double end = top * top;
+        auto poly = [&](double t) { return fabs(b * t + c * t * t); };  // of t = s^2
+        double most = poly(end);
+        if (c != 0.0 && -b / (2.0 * c) > 0.0 && -b / (2.0 * c) < end) most = fmax(most, poly(-b / (2.0 * c)));
+        if (!(most <= 30.0)) return false;
+        auto value = [&](double t) { return fabs(sqrt(t) * (a + b * t + c * t * t)); };
+        most = value(end);
+        auto at = [&](double t) {  // an extremum, a root of a + 3 b t + 5 c t^2
+            if (t > 0.0 && t < end) most = fmax(most, value(t));
+        };
+        const double root = 9.0 * b * b - 20.0 * a * c;
+        if (c != 0.0 && root >= 0.0) {
+            at((-3.0 * b - sqrt(root)) / (10.0 * c));
+            at((-3.0 * b + sqrt(root)) / (10.0 * c));
+        } else if (c == 0.0 && b != 0.0) {
+            at(-a / (3.0 * b));
+        }
+        top = 1.01 * most;
+    }
+    return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -175,7 +208,7 @@ int moe_orthogonalize(const void *g, int g_type, int64_t B, int64_t M, int64_t N
     if (!ortho_shape(B, M, N) || steps > 32) return MOE_ERR_UNSUPPORTED_SHAPE;
     // NaN coefficients fail these too
     if (!(fabsf(a) <= 16.0f && fabsf(b) <= 16.0f && fabsf(c) <= 16.0f)) return MOE_ERR_INVALID_ARG;
-    if (fabsf(b) * 1.6f + fabsf(c) * 2.56f > 24.0f) return MOE_ERR_INVALID_ARG;
+    if (!ortho_in_range(a, b, c, steps)) return MOE_ERR_INVALID_ARG;
     if (B == 0) return MOE_OK;
     if (!g || !out_bf16 || !aligned16(g) || !aligned16(out_bf16)) return MOE_ERR_INVALID_ARG;
     if (!workspace || ((uintptr_t)workspace & 255)) return MOE_ERR_INVALID_ARG;

@@ -372,7 +372,8 @@ def moe_orthogonalize(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
                       out_scale: float = 1.0, out=None, workspace=None, stream=None):
     """bf16 [B,M,N]: each matrix of g (bf16 or f32 [B,M,N]) divided by its
     Frobenius norm plus eps and put through ``steps`` of X = a X + (b A +
-    c A A) X, A = X X^T; times out_scale."""
+    c A A) X, A = X X^T; times out_scale.  Coefficients that could take a
+    singular value beyond 1.9 before the last step are refused."""
     B, M, N = g.shape
     gt = _type(g, "g")
     _is(g, (B, M, N), g.dtype, "g")

@@ -1,5 +1,6 @@
 """The binding's and the C entries' own part of the block's operators, on the
-host: where a call on a stream allocates, with a stand-in for the library."""
+host: where a call on a stream allocates, with a stand-in for the library;
+the coefficients that the orthogonalisation takes."""
 import contextlib
 
 import pytest
@@ -116,3 +117,68 @@ def test_the_current_stream_is_the_default(monkeypatch, stream):
     watch = Watch(monkeypatch)
     call(stream=stream)
     assert watch.made and all(s == "current" for s, _ in watch.made) and not watch.kept
+
+
+# ------------------------------------------------------------------ the orthogonalisation's coefficients
+USUAL = (3.4445, -4.7750, 2.0315)
+
+
+def largest(coefficients, steps, slack=1.0, points=2001):
+    """The largest singular value that a product reads, and the largest
+    eigenvalue of b A + c A A, by trying many singular values of [0, 1];
+    `slack`: how much each step may raise the largest one besides."""
+    a, b, c = coefficients
+    grid, end, top, poly = torch.linspace(0, 1, points, dtype=torch.float64), 1.0, 0.0, 0.0
+    for _ in range(steps):
+        s = grid * end
+        t = s * s
+        top, poly = max(top, end), max(poly, (b * t + c * t * t).abs().max().item())
+        end = slack * (s * (a + b * t + c * t * t)).abs().max().item()
+    return top, poly
+
+
+@pytest.fixture(scope="module")
+def L():
+    from mixture_experts_ffn_gate_gb300 import _build
+    _build.build()
+    return m.lib()
+
+
+def accepted(L, coefficients, steps):
+    """B = 0: nothing is enqueued, and every check of the numbers runs."""
+    status = L.moe_orthogonalize(None, 1, 0, 64, 96, steps, *coefficients, 1e-7, 1.0, None, None, 0, None)
+    assert status in (m.MOE_OK, m.MOE_ERR_INVALID_ARG)
+    return status == m.MOE_OK
+
+
+@pytest.mark.parametrize("coefficients,steps,want", [
+    (USUAL, 1, True), (USUAL, 5, True), (USUAL, 32, True), ((1.5, -0.5, 0.0), 32, True), ((2.0, -1.5, 0.5), 32, True),
+    ((1.875, -1.25, 0.375), 32, True), ((4.0, -8.0, 4.2), 5, True), ((0.0, 0.0, 0.0), 32, True),
+    ((16.0, 0.0, 0.0), 1, True), ((16.0, 0.0, 0.0), 2, False),       # the last step's X may be any size
+    ((3.0, -0.5, 0.0), 1, True), ((3.0, -0.5, 0.0), 2, False),       # 1, then 2.5: A is 6.25
+    ((2.0, 0.0, 0.0), 2, False), ((1.8, 0.0, 0.0), 2, True), ((1.8, 0.0, 0.0), 3, False),
+    ((-1.8, 0.0, 0.0), 2, True), ((-2.5, 0.0, 0.0), 2, False), ((1.2, 0.0, 0.0), 3, True), ((1.2, 0.0, 0.0), 6, False),
+    ((0.0, 16.0, 16.0), 1, False), ((0.0, 14.0, 14.0), 1, True), ((0.0, 16.0, -16.0), 1, True),
+    ((0.0, -12.0, 16.0), 2, False), ((3.4445, -4.7750, 5.0), 5, False), ((float("nan"), 0.0, 0.0), 1, False)])
+def test_coefficients_that_leave_the_range_are_refused(L, coefficients, steps, want):
+    assert accepted(L, coefficients, steps) is want
+
+
+def test_accepted_coefficients_stay_in_range(L):
+    """No accepted set takes any singular value out of FP16's range, and every
+    refused one would with the roundings' part in a hundred per step."""
+    g = torch.Generator().manual_seed(0)
+    sets = torch.rand(1000, 3, generator=g, dtype=torch.float64) * torch.tensor([8.0, 12.0, 8.0]) - \
+        torch.tensor([4.0, 9.0, 1.0])
+    seen = {True: 0, False: 0}
+    for coefficients in sets.float().double().tolist():
+        for steps in (1, 2, 5):
+            ok = accepted(L, coefficients, steps)
+            seen[ok] += 1
+            if ok:
+                top, poly = largest(coefficients, steps)
+                assert top < 2.0 and poly < 32.0, (coefficients, steps)
+            else:  # the grid misses an extremum by 1e-5 of it
+                top, poly = largest(coefficients, steps, 1.01 * (1 + 1e-4))
+                assert top > 1.9 or poly > 30.0 * (1 - 1e-4), (coefficients, steps)
+    assert min(seen.values()) > 100

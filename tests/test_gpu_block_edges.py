@@ -166,3 +166,24 @@ def test_calls_on_another_stream_keep_their_workspace(name, by_handle):
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     del waste
+
+
+# ------------------------------------------------------------------ the orthogonalisation's range
+@pytest.mark.parametrize("M,N", [(1, 200), (60, 40), (300, 500), (2, 1000)])
+@pytest.mark.parametrize("coefficients,steps", [((1.8, 0.0, 0.0), 2), ((-1.8, 0.0, 0.0), 2), ((3.0, -0.5, 0.0), 1),
+                                                ((3.4445, -4.7750, 2.0315), 10), ((16.0, 0.0, 0.0), 1),
+                                                ((0.0, 14.0, 14.0), 1)])
+def test_matrices_of_one_row_stay_finite(M, N, coefficients, steps):
+    """All of the weight in one row (a singular value of 1 in one entry of A),
+    with coefficients near the limits."""
+    g = torch.zeros(2, M, N)
+    g[0, M // 2] = randn(N, seed=M).cpu()
+    g[1] = torch.outer(randn(M, seed=N).cpu(), randn(N, seed=N + 1).cpu())
+    out = f64(mb.moe_orthogonalize(g.cuda(), steps=steps, coefficients=coefficients))
+    assert np.isfinite(out).all()
+    if abs(coefficients[0]) ** steps > 500:
+        return  # the tolerance is of five steps of slope 3.4 at zero, which raise the roundings 485 times
+    for b in range(2):
+        want = ref.orthogonalize(f64(g[b]), steps, coefficients, 1e-7)
+        # FP16 roundings of X, A and b A + c A A, as in test_gpu_block.py, and BF16's of each element
+        assert ref.rel(out[b], want) <= 2.7e-3 + 2.0 ** -8
