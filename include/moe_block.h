@@ -114,7 +114,8 @@ typedef struct moe_gate_opts {
  *   topk_groups groups of highest rank stay, the lower index winning ties.
  *   The k experts of largest c among those that stay are chosen in
  *   descending order, the lower index winning ties (-0.0 == +0.0; a NaN
- *   ranks above every number).
+ *   ranks above every number).  A NaN or +inf among a row's logits makes all
+ *   of its softmax scores NaN, so with a bias its first k experts are chosen.
  *   w[j] = scale * s[idx_j]                            renormalize == 0
  *   w[j] = scale * s[idx_j] / sum over m of s[idx_m]   renormalize != 0
  *   A sum of zero gives weights of zero: a sigmoid row of logits that are all

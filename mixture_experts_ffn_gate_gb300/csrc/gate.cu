@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(32 * GateShape<PER>::WARPS, GateShape<PER>::BL
                 sigmoids(l, c);
             } else {
 #pragma unroll
-                for (int i = 0; i < PER; ++i) c[i] = total > 0.0f ? exp_below(l[i], top) / total : 0.0f;
+                for (int i = 0; i < PER; ++i) c[i] = total == 0.0f ? 0.0f : exp_below(l[i], top) / total;
             }
 #pragma unroll
             for (int i = 0; i < PER; ++i)
@@ -388,9 +388,9 @@ __global__ void __launch_bounds__(32 * GateShape<PER>::WARPS, GateShape<PER>::BL
             if (a.sigmoid)
                 s = sigmoid_of(lj);
             else if (a.renorm)
-                s = exp_below(lj, a.bias ? top : first);
+                s = total != total ? total : exp_below(lj, a.bias ? top : first);
             else
-                s = total > 0.0f || total != total ? exp_below(lj, top) / total : 0.0f;
+                s = total == 0.0f ? 0.0f : exp_below(lj, top) / total;
         }
         __syncwarp();  // the keys are read before the next token's are written
         if (a.renorm) {

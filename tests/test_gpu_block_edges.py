@@ -187,3 +187,24 @@ def test_matrices_of_one_row_stay_finite(M, N, coefficients, steps):
         want = ref.orthogonalize(f64(g[b]), steps, coefficients, 1e-7)
         # FP16 roundings of X, A and b A + c A A, as in test_gpu_block.py, and BF16's of each element
         assert ref.rel(out[b], want) <= 2.7e-3 + 2.0 ** -8
+
+
+# ------------------------------------------------------------------ the gate
+@pytest.mark.parametrize("E,groups,kept", [(24, 1, 1), (64, 8, 3), (384, 1, 1), (512, 4, 2), (1000, 1, 1)])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_gate_rows_without_softmax_scores(E, groups, kept, renormalize, bad):
+    """All of the row's scores are NaN, which tie above every number: the
+    bias has no say, the lowest experts are chosen."""
+    k, r = 6, np.random.default_rng(E)
+    logits, bias = r.normal(size=(5, E)).astype(np.float32), r.normal(size=E).astype(np.float32)
+    clean = mb.moe_gate_forward(dev(logits), k, bias=dev(bias), groups=groups, topk_groups=kept,
+                                renormalize=renormalize)
+    logits[1, E - 3] = logits[3, 0] = bad
+    out = mb.moe_gate_forward(dev(logits), k, bias=dev(bias), groups=groups, topk_groups=kept,
+                              renormalize=renormalize)
+    for t in range(5):
+        if t in (1, 3):
+            assert out.topk_idx[t].tolist() == list(range(k)) and torch.isnan(out.topk_w[t]).all()
+        else:
+            assert torch.equal(out.topk_idx[t], clean.topk_idx[t]) and torch.equal(out.topk_w[t], clean.topk_w[t])
