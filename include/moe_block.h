@@ -231,9 +231,9 @@ int moe_ffn_forward_routed_train(const void *x_bf16, const int32_t *topk_idx,
  * steps: up to 2e-3 before out's rounding to BF16, and 1.7e-3 from that.
  * Every further step raises what the roundings left beside small singular
  * values by a (ten steps on a 60 x 40 matrix of rank one: 1.5e-2).
- * A matrix of zeros gives zeros (NaN with eps == 0); a NaN or an infinity
- * spreads over its whole matrix and no other.  Squares are summed in FP32: entries below about
- * 1e-19 count as zero in the norm.
+ * A matrix of zeros gives zeros (NaN with eps < 1e-35); a NaN, an infinity or
+ * a norm beyond FP32's range makes its whole matrix NaN and no other.
+ * Entries below about 1e-28 count as zero in the norm.
  * Limits: M, N in 1..32768, steps in 1..32, B in 0..65535 (0 enqueues
  * nothing), B * M * N <= 2^40, B * ceil(M / 128) * ceil(N / 128) <= 2^24,
  * |a|, |b|, |c| <= 16, eps >= 0.  Coefficients and steps that can take a

@@ -751,21 +751,54 @@ __device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8])
     unpack8(__ldg(reinterpret_cast<const uint4 *>(p)), v);
 }
 
-// partial[b][p]: the sum of squares of a slice of matrix b.
+// Squares of FP32 values leave FP32's range, so there are two sums: of the
+// values times 2^30, which says the norm from 2^-93 times one element (1e-28)
+// up to 2^34, and of the values times 2^-80, for what is larger (an element
+// that matters there is at least 2^19: 2^30 elements at most).  The factors
+// are powers of two, so the norm has the bits of a plain sum in range.
+struct Squares {
+    float near, far;
+    __device__ __forceinline__ void add(float v)
+    {
+        const float a = v * 0x1p30f, b = v * 0x1p-80f;
+        near = fmaf(a, a, near);
+        far = fmaf(b, b, far);
+    }
+    __device__ __forceinline__ void add(const Squares &o)
+    {
+        near += o.near;
+        far += o.far;
+    }
+    // 2^kXBits / (norm + eps); NaN where the norm is no finite FP32 number
+    __device__ __forceinline__ float factor(float eps) const
+    {
+        const float norm = near < INFINITY ? sqrtf(near) * 0x1p-30f : sqrtf(far) * 0x1p80f;
+        return (float)(1 << kXBits) / (norm + eps) + (norm - norm);
+    }
+};
+
+__device__ __forceinline__ Squares warp_sum(const Squares &s)
+{
+    float v[2] = {s.near, s.far};
+    warp_sum_n(v);
+    return Squares{v[0], v[1]};
+}
+
+// partial[b][p]: the sums of squares of a slice of matrix b.
 template <typename T>
 __global__ void __launch_bounds__(256) ortho_norm_kernel(const T *__restrict__ g, int64_t count,
-                                                         float *__restrict__ partial, uint32_t *__restrict__ done)
+                                                         Squares *__restrict__ partial, uint32_t *__restrict__ done)
 {
-    __shared__ float sums[8];
+    __shared__ Squares sums[8];
     const int b = blockIdx.y;
     const T *p = g + (int64_t)b * count;
-    float s[8] = {};
+    Squares s[8] = {};
     const int64_t stride = (int64_t)gridDim.x * 256, start = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (count % 8 == 0) {
         const int64_t n = count / 8;
         auto add = [&](const float(&v)[8]) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) s[q] = fmaf(v[q], v[q], s[q]);
+            for (int q = 0; q < 8; ++q) s[q].add(v[q]);
         };
         int64_t i = start;
         for (; i + 3 * stride < n; i += 4 * stride) {  // four loads in flight
@@ -781,31 +814,33 @@ __global__ void __launch_bounds__(256) ortho_norm_kernel(const T *__restrict__ g
             add(v);
         }
     } else {
-        for (int64_t i = start; i < count; i += stride) {
-            const float v = (float)p[i];
-            s[0] = fmaf(v, v, s[0]);
-        }
+        for (int64_t i = start; i < count; i += stride) s[0].add((float)p[i]);
     }
-    const float t = warp_sum(((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7])));
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2)
+#pragma unroll
+        for (int q = 0; q < 8; q += 2 * d) s[q].add(s[q + d]);
+    const Squares t = warp_sum(s[0]);
     if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = t;
     __syncthreads();
     if (threadIdx.x == 0) {
-        float v = 0.0f;
+        Squares v{};
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v += sums[q];
+        for (int q = 0; q < 8; ++q) v.add(sums[q]);
         partial[b * kMaxParts + blockIdx.x] = v;
         if (blockIdx.x == 0) done[b] = 0;  // for the products that follow
     }
 }
 
 // 2^kXBits / (||G|| + eps) of a matrix from its partial sums.  Whole warp.
-__device__ __forceinline__ float input_factor(const float *partial, int parts, float eps)
+__device__ __forceinline__ float input_factor(const Squares *partial, int parts, float eps)
 {
     const int lane = threadIdx.x & 31;
-    float s = lane < parts ? __ldg(partial + lane) : 0.0f;
-    if (lane + 32 < parts) s += __ldg(partial + lane + 32);
+    Squares s{};
+    if (lane < parts) s.add(partial[lane]);
+    if (lane + 32 < parts) s.add(partial[lane + 32]);
     static_assert(kMaxParts == 64, "two partial sums per lane");
-    return (float)(1 << kXBits) / (sqrtf(warp_sum(s)) + eps);
+    return warp_sum(s).factor(eps);
 }
 
 __device__ __forceinline__ void split8(const float (&v)[8], __half *hi, __half *lo)
@@ -826,7 +861,7 @@ __device__ __forceinline__ void split8(const float (&v)[8], __half *hi, __half *
 // through shared memory.
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(256) ortho_split8_kernel(const T *__restrict__ g, int M, int N,
-                                                           const float *__restrict__ partial, int parts, float eps,
+                                                           const Squares *__restrict__ partial, int parts, float eps,
                                                            __half *__restrict__ hi, __half *__restrict__ lo)
 {
     const int b = blockIdx.z;
@@ -872,7 +907,7 @@ __global__ void __launch_bounds__(256) ortho_split8_kernel(const T *__restrict__
 // The same for any M and N, in 32 x 32 tiles (X's rows have `pitch` elements).
 template <typename T>
 __global__ void __launch_bounds__(256) ortho_split_kernel(const T *__restrict__ g, int M, int N,
-                                                          const float *__restrict__ partial, int parts, float eps,
+                                                          const Squares *__restrict__ partial, int parts, float eps,
                                                           bool tall, int64_t pitch, __half *__restrict__ hi,
                                                           __half *__restrict__ lo)
 {
@@ -950,7 +985,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) or
     uint8_t *const xr = smem, *const ar = xr + kRows, *const xc = ar + kRows;
     uint64_t *go = reinterpret_cast<uint64_t *>(xc + kRows);  // operands of the next product written, by 32 warps
     uint64_t *done = go + 1;                                  // a product's MMAs have completed
-    float *sums = reinterpret_cast<float *>(done + 1);        // a warp's sum of squares; then, first, the CTA's
+    Squares *sums = reinterpret_cast<Squares *>(done + 1);    // a warp's sums of squares; then, first, the CTA's
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sums + kSmallWarps + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -971,7 +1006,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) or
     // the sum of squares, half of the elements per CTA
     {
         const int count = args.M * args.N;
-        float s = 0.0f;
+        Squares s{};
         const int first = (int)rank * kSmallThreads + threadIdx.x;
         if (count % 8 == 0) {  // the matrix starts on 16 bytes: all of a thread's loads at once
 #pragma unroll
@@ -980,29 +1015,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kSmallThreads, 1) or
                 float v[8];
                 load8(g + 8 * (i + first), v);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s = fmaf(v[e], v[e], s);
+                for (int e = 0; e < 8; ++e) s.add(v[e]);
             }
         } else {
-            for (int i = first; i < count; i += 2 * kSmallThreads) {
-                const float v = (float)g[i];
-                s = fmaf(v, v, s);
-            }
+            for (int i = first; i < count; i += 2 * kSmallThreads) s.add((float)g[i]);
         }
         s = warp_sum(s);
         if (lane == 0) sums[warp] = s;
     }
     ptx::tc_fence_before();
     __syncthreads();
-    float mine = 0.0f;
-    for (int w = 0; w <= kSmallWarps; ++w) mine += sums[w];
+    Squares mine{};
+    for (int w = 0; w <= kSmallWarps; ++w) mine.add(sums[w]);
     __syncthreads();
     if (threadIdx.x == 0) sums[0] = mine;
     cluster_sync();  // barriers initialised, TMEM allocated, both sums written
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    float other;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other) : "r"(map_to(ptx::smem_u32(sums), rank ^ 1)));
-    const float f = (float)(1 << kXBits) / (sqrtf(rank == 0 ? mine + other : other + mine) + args.eps);
+    Squares all;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                 : "=f"(all.near), "=f"(all.far)
+                 : "r"(map_to(ptx::smem_u32(sums), rank ^ 1)));
+    all.add(mine);
+    const float f = all.factor(args.eps);
 
     const int products = 3 * args.steps;
     if (warp == kSmallWarps) {
@@ -1252,7 +1287,7 @@ Region layout(int64_t B, int64_t M, int64_t N)
         o += (bytes + 255) & ~size_t(255);
         return at;
     };
-    L.partial = take((size_t)B * kMaxParts * 4);
+    L.partial = take((size_t)B * kMaxParts * sizeof(Squares));
     L.done = take((size_t)B * 4);
     const size_t x = (size_t)(B * L.m * L.x_pitch) * 2, a = (size_t)(B * L.m * L.a_pitch) * 2;
     L.hi[0] = take(x);
@@ -1335,7 +1370,7 @@ cudaError_t run_steps(const OrthoCall &c, char *ws, const Region &L, int pairs, 
 }
 
 template <typename T>
-cudaError_t launch_input(const OrthoCall &c, const Region &L, float *partial, uint32_t *done, __half *hi, __half *lo,
+cudaError_t launch_input(const OrthoCall &c, const Region &L, Squares *partial, uint32_t *done, __half *hi, __half *lo,
                          cudaStream_t s)
 {
     const int64_t count = c.M * c.N;
@@ -1407,7 +1442,7 @@ cudaError_t launch_orthogonalize(const OrthoCall &c, void *workspace, int pairs,
     }
     const Region L = layout(c.B, c.M, c.N);
     char *ws = (char *)workspace;
-    auto *partial = (float *)(ws + L.partial);
+    auto *partial = (Squares *)(ws + L.partial);
     auto *hi = (__half *)(ws + L.hi[0]);
     auto *lo = (__half *)(ws + L.lo);
     auto *done = (uint32_t *)(ws + L.done);

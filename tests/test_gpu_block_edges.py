@@ -208,3 +208,22 @@ def test_gate_rows_without_softmax_scores(E, groups, kept, renormalize, bad):
             assert out.topk_idx[t].tolist() == list(range(k)) and torch.isnan(out.topk_w[t]).all()
         else:
             assert torch.equal(out.topk_idx[t], clean.topk_idx[t]) and torch.equal(out.topk_w[t], clean.topk_w[t])
+
+
+# ------------------------------------------------------------------ the orthogonalisation's norm
+@pytest.mark.parametrize("M,N", [(70, 90), (71, 33), (256, 256), (300, 520), (520, 300), (301, 77)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_orthogonalize_does_not_see_the_scale(M, N, dtype):
+    """A power of two on the whole matrix changes no bit, also where the
+    squares leave FP32's range at either end."""
+    g = randn(2, M, N, seed=M, dtype=dtype)
+    want = mb.moe_orthogonalize(g, eps=0.0)
+    assert torch.isfinite(want).all() and want.any()
+    for p in (-80, -70, -20, 20, 60, 64, 100):
+        assert torch.equal(mb.moe_orthogonalize(g * 2.0 ** p, eps=0.0), want), p
+    mixed = torch.stack([g[0] * 2.0 ** 90, g[1]])
+    assert torch.equal(mb.moe_orthogonalize(mixed, eps=0.0), want)
+    # a norm that no FP32 number holds is no silent zero
+    beyond = torch.stack([torch.full((M, N), 3e38, dtype=dtype, device="cuda"), g[1]])
+    out = mb.moe_orthogonalize(beyond, eps=0.0)
+    assert torch.isnan(out[0]).all() and torch.equal(out[1], want[1])
