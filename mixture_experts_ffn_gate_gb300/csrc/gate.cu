@@ -20,7 +20,7 @@
 // The bytes (4 E per token in, 8 k out) would take 2.6 us for 16384 tokens of
 // 256 experts at the copy rate; the instructions bound it (the scores' exp
 // and reciprocal, the sort, k rounds).  Measured there with sigmoid scores, a
-// bias, 4 of 8 groups and k = 8: 17.1 us (14.0 without the counts); softmax
+// bias, 4 of 8 groups and k = 8: 18.4 us (15.3 without the counts); softmax
 // scores without a bias: 9.3.
 #include <type_traits>
 
@@ -126,30 +126,7 @@ __device__ __forceinline__ void get_words(uint32_t *v, const uint32_t *src)
     }
 }
 
-__device__ __forceinline__ float sigmoid_of(float l) { return 1.0f / (1.0f + expf(-l)); }
-
-// The same bits for N values: the reciprocal of x = 1 + exp(-l) is the
-// hardware's approximation and one Newton step, r + r (1 - x r) in fused
-// multiply-adds, which rounds correctly for every significand (tested against
-// the division); no branch per value, as the division has.  Beyond 2^126 the
-// reciprocal is subnormal and takes the division.
-template <int N>
-__device__ __forceinline__ void sigmoids(const float (&l)[N], float (&s)[N])
-{
-    float top = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const float x = 1.0f + expf(-l[i]);
-        float r;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-        s[i] = __fmaf_rn(r, __fmaf_rn(-x, r, 1.0f), r);
-        top = fmaxf(top, x);
-    }
-    if (top >= 0x1p126f) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) s[i] = sigmoid_of(l[i]);
-    }
-}
+__device__ __forceinline__ float sigmoid_of(float l) { return __frcp_rn(1.0f + expf(-l)); }
 
 // exp(l - top), zero for a logit of -inf (also where top is -inf)
 __device__ __forceinline__ float exp_below(float l, float top)
@@ -256,7 +233,8 @@ __global__ void __launch_bounds__(32 * GateShape<PER>::WARPS, GateShape<PER>::BL
         } else {
             float c[PER];
             if (a.sigmoid) {
-                sigmoids(l, c);
+#pragma unroll
+                for (int i = 0; i < PER; ++i) c[i] = sigmoid_of(l[i]);
             } else {
 #pragma unroll
                 for (int i = 0; i < PER; ++i) c[i] = total == 0.0f ? 0.0f : exp_below(l[i], top) / total;

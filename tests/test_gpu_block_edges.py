@@ -210,6 +210,26 @@ def test_gate_rows_without_softmax_scores(E, groups, kept, renormalize, bad):
             assert torch.equal(out.topk_idx[t], clean.topk_idx[t]) and torch.equal(out.topk_w[t], clean.topk_w[t])
 
 
+@pytest.mark.parametrize("E", [32, 24, 20])
+def test_gate_chooses_by_the_scores_that_it_returns(E):
+    """With a bias of zero the choice is the order of the returned sigmoid
+    scores, bit for bit: logits so close that neighbours' scores are equal or
+    one unit apart."""
+    r = np.random.default_rng(E)
+    base = np.concatenate([r.uniform(-20, 20, 3000), r.uniform(-88.7, -86, 500), r.uniform(-104, -88.7, 200),
+                           r.uniform(-2, 2, 1000)]).astype(np.float32)
+    step = np.spacing(np.abs(base)) * r.integers(1, 5, size=base.shape)
+    logits = (base[:, None] + step[:, None] * r.permuted(np.tile(np.arange(E), (len(base), 1)), axis=1))
+    logits = dev(logits.astype(np.float32))
+    out = mb.moe_gate_forward(logits, E, bias=torch.zeros(E).cuda(), score="sigmoid", renormalize=False)
+    w, idx = out.topk_w.cpu().numpy(), out.topk_idx.cpu().numpy()
+    assert np.all((w[:, :-1] > w[:, 1:]) | ((w[:, :-1] == w[:, 1:]) & (idx[:, :-1] < idx[:, 1:])))
+    assert np.array_equal(np.sort(idx, axis=1), np.tile(np.arange(E), (len(base), 1)))
+    s = 1 / (1 + np.exp(-f64(logits)))
+    # expf and two roundings
+    assert np.all(np.abs(w - np.take_along_axis(s, idx, 1)) <= s.max(axis=1, keepdims=True) * 2.0 ** -20 + 1e-38)
+
+
 # ------------------------------------------------------------------ the orthogonalisation's norm
 @pytest.mark.parametrize("M,N", [(70, 90), (71, 33), (256, 256), (300, 520), (520, 300), (301, 77)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
