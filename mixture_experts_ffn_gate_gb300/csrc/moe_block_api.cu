@@ -216,6 +216,7 @@ int moe_orthogonalize(const void *g, int g_type, int64_t B, int64_t M, int64_t N
     int n_sm, pairs;
     const int st = moe::device_info(&n_sm, &pairs);
     if (st != MOE_OK) return st;
+    if (pairs < 1) return MOE_ERR_CUDA;
     const moe::OrthoCall call{g, g_type == MOE_F32, B, M, N, steps, a, b, c, eps, out_scale, out_bf16};
     return moe::launch_orthogonalize(call, workspace, pairs, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -145,7 +145,7 @@ struct DeviceInfo {
     bool ready = false;
     unsigned long long ctx = 0;
     int n_sm = 0;
-    int pairs = 0;  // pairs of CTAs that the orthogonalisation's products hold at once
+    int pairs = 0;  // pairs of CTAs that the orthogonalisation's products hold at once, 0: it cannot run
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mutex;
@@ -165,7 +165,11 @@ int device_setup(DeviceInfo **info)
         if (moe::decode_fused_init_device() != cudaSuccess) return MOE_ERR_CUDA;
         if (moe::gemm_init_device() != cudaSuccess) return MOE_ERR_CUDA;
         if (moe::bwd_init_device() != cudaSuccess) return MOE_ERR_CUDA;
-        if (moe::ortho_init_device(&d.pairs) != cudaSuccess || d.pairs < 1) return MOE_ERR_CUDA;
+        // (where no pair fits, that operator alone is refused)
+        if (moe::ortho_init_device(&d.pairs) != cudaSuccess) {
+            d.pairs = 0;
+            (void)cudaGetLastError();  // the launches look at it
+        }
         // the attribute calls above created the context if there was none
         d.ctx = moe::current_context_id();
         d.ready = true;
