@@ -270,13 +270,15 @@ def moe_ffn_forward_noalloc(x, logits, w_gate_up, w_down, k: int, out=None, stre
     return out
 
 
-def new_workspace(T, H, I, E, k, device="cuda", host=False, stream=None):
+def new_workspace(T, H, I, E, k, device="cuda", host=False, stream=None, routed=True):
     """A workspace tensor big enough for this shape (256-byte aligned), its
     state bytes zeroed; moe_block.moe_ffn_forward_routed's too unless it is
-    for the host entry.  ``stream``: the one that the calls run on (default:
-    torch's current stream)."""
-    n = moe_ffn_host_workspace_bytes(T, H, I, E, k) if host else lib().moe_ffn_routed_workspace_bytes(T, H, I, E, k)
-    return _state_buffer(n, device, stream, "workspace size")
+    for the host entry or ``routed`` is false (which saves 2 T (k I + H)
+    bytes).  ``stream``: the one that the calls run on (default: torch's
+    current stream)."""
+    size = (moe_ffn_host_workspace_bytes if host
+            else lib().moe_ffn_routed_workspace_bytes if routed else moe_ffn_workspace_bytes)
+    return _state_buffer(size(T, H, I, E, k), device, stream, "workspace size")
 
 
 def moe_ffn_forward_ex(x, logits, w_gate_up, w_down, k: int, out=None, workspace=None,
@@ -291,7 +293,7 @@ def moe_ffn_forward_ex(x, logits, w_gate_up, w_down, k: int, out=None, workspace
     if out is None:
         out = _empty((T, H), torch.float32, x.device, stream)
     if workspace is None:
-        workspace = new_workspace(T, H, I, E, k, device=x.device, stream=stream)
+        workspace = new_workspace(T, H, I, E, k, device=x.device, stream=stream, routed=False)
     if topk_idx is not None:
         _dev(topk_idx, torch.int32, "topk_idx")
     if topk_w is not None:
@@ -378,7 +380,7 @@ def moe_ffn_forward_mxfp8(x, logits, w_gate_up_q, w_gate_up_s, w_down_q, w_down_
     if out is None:
         out = _empty((T, H), torch.float32, x.device, stream)
     if workspace is None:
-        workspace = new_workspace(T, H, I, E, k, device=x.device, stream=stream)
+        workspace = new_workspace(T, H, I, E, k, device=x.device, stream=stream, routed=False)
     _check(lib().moe_ffn_forward_mxfp8(
         _ptr(x), _ptr(logits), _ptr(w_gate_up_q), _ptr(w_gate_up_s), _ptr(w_down_q), _ptr(w_down_s),
         T, H, I, E, k, _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -409,11 +411,12 @@ def moe_ffn_backward_workspace_bytes(T, H, I, E, k) -> int:
     return int(lib().moe_ffn_backward_workspace_bytes(T, H, I, E, k))
 
 
-def new_backward_workspace(T, H, I, E, k, device="cuda", stream=None):
-    """A workspace for moe_ffn_backward and moe_block.moe_ffn_backward_routed
-    (state bytes zeroed, so that forward calls may share it)."""
-    return _state_buffer(lib().moe_ffn_routed_backward_workspace_bytes(T, H, I, E, k), device, stream,
-                         "workspace size")
+def new_backward_workspace(T, H, I, E, k, device="cuda", stream=None, routed=True):
+    """A workspace for moe_ffn_backward and, unless ``routed`` is false,
+    moe_block.moe_ffn_backward_routed (a quarter more; state bytes zeroed, so
+    that forward calls may share it)."""
+    size = lib().moe_ffn_routed_backward_workspace_bytes if routed else moe_ffn_backward_workspace_bytes
+    return _state_buffer(size(T, H, I, E, k), device, stream, "workspace size")
 
 
 def moe_ffn_backward(x, logits, w_gate_up, w_down, dout, k: int, dx=None, dlogits=None, dw_gate_up=None,
@@ -454,10 +457,12 @@ def moe_ffn_train_state_bytes(T, H, I, E, k) -> int:
     return int(lib().moe_ffn_train_state_bytes(T, H, I, E, k))
 
 
-def new_train_state(T, H, I, E, k, device="cuda", stream=None):
+def new_train_state(T, H, I, E, k, device="cuda", stream=None, routed=True):
     """A state buffer for the training pair (moe_ffn_forward_train, then
-    moe_ffn_backward_train; or moe_block's routed pair)."""
-    return _state_buffer(lib().moe_ffn_routed_backward_workspace_bytes(T, H, I, E, k), device, stream, "state size")
+    moe_ffn_backward_train) and, unless ``routed`` is false, for moe_block's
+    routed pair (a quarter more)."""
+    size = lib().moe_ffn_routed_backward_workspace_bytes if routed else moe_ffn_train_state_bytes
+    return _state_buffer(size(T, H, I, E, k), device, stream, "state size")
 
 
 def moe_ffn_forward_train(x, logits, w_gate_up, w_down, k: int, state, out=None,

@@ -182,3 +182,28 @@ def test_accepted_coefficients_stay_in_range(L):
                 top, poly = largest(coefficients, steps, 1.01 * (1 + 1e-4))
                 assert top > 1.9 or poly > 30.0 * (1 - 1e-4), (coefficients, steps)
     assert min(seen.values()) > 100
+
+
+# ------------------------------------------------------------------ workspace sizes
+SHAPE = (2048, 6144, 2048, 256, 8)
+
+
+@pytest.mark.parametrize("make,plain,routed", [
+    ("new_workspace", "moe_ffn_workspace_bytes", "moe_ffn_routed_workspace_bytes"),
+    ("new_backward_workspace", "moe_ffn_backward_workspace_bytes", "moe_ffn_routed_backward_workspace_bytes"),
+    ("new_train_state", "moe_ffn_train_state_bytes", "moe_ffn_routed_backward_workspace_bytes")])
+def test_a_workspace_for_the_layer_alone_is_no_larger(L, make, plain, routed):
+    meta = getattr(m, make)(*SHAPE, device="meta", routed=False)
+    assert meta.numel() == getattr(L, plain)(*SHAPE)
+    assert getattr(m, make)(*SHAPE, device="meta").numel() == getattr(L, routed)(*SHAPE) > meta.numel()
+
+
+@pytest.mark.parametrize("name", ["forward_ex", "mxfp8"])
+def test_the_layers_own_workspace_is_the_layers(monkeypatch, name):
+    """Without one of the caller's, a call with logits makes no room for a given routing."""
+    call = calls()[name]
+    watch = Watch(monkeypatch)
+    monkeypatch.setattr(m, "_lib", type("Sizes", (Library,), {"moe_ffn_routed_workspace_bytes":
+                                                              lambda self, *a: 1 << 20})())
+    call(stream=5)
+    assert [t.numel() for _, t in watch.made if t.dtype is torch.uint8] == [1 << 16]
