@@ -95,7 +95,10 @@ def _workspace(n, device, stream, what):
     return _empty((n,), torch.uint8, device, stream)
 
 
-def _size(t):
+def _size(t, name="workspace"):
+    """The bytes of a workspace or state of the caller's."""
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
     return t.numel() * t.element_size()
 
 
@@ -325,7 +328,7 @@ def moe_ffn_forward_routed_train(x, topk_idx, topk_w, w_gate_up, w_down, state, 
     out = _new(out, (T, H), "out", x.device, stream)
     p = _ptr
     _check(_lib().moe_ffn_forward_routed_train(
-        p(x), p(topk_idx), p(topk_w), p(w_gate_up), p(w_down), T, H, I, E, k, p(out), p(state), _size(state),
+        p(x), p(topk_idx), p(topk_w), p(w_gate_up), p(w_down), T, H, I, E, k, p(out), p(state), _size(state, "state"),
         None if opts is None else ctypes.byref(opts), _stream(stream, x.device)), "moe_ffn_forward_routed_train")
     return out
 
@@ -354,7 +357,7 @@ def moe_ffn_backward_routed(x, topk_idx, topk_w, w_gate_up, w_down, dout, dx=Non
     p = _ptr
     _check(_lib().moe_ffn_backward_routed(
         p(x), p(topk_idx), p(topk_w), p(w_gate_up), p(w_down), p(dout), T, H, I, E, k, p(dx), p(dtopk_w),
-        p(dw_gate_up), p(dw_down), p(ws), _size(ws), int(state is not None),
+        p(dw_gate_up), p(dw_down), p(ws), _size(ws, "workspace" if state is None else "state"), int(state is not None),
         None if opts is None else ctypes.byref(opts), _stream(stream, x.device)), "moe_ffn_backward_routed")
     return dx, dtopk_w, dw_gate_up, dw_down
 

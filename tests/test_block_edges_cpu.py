@@ -49,6 +49,7 @@ class Watch:
         patch(m, "_lib", Library())
         patch(m, "_dev", lambda *a: None)
         patch(mb, "_is", lambda *a: None)
+        patch(mb, "_size", lambda t, name=None: t.numel() * t.element_size())
         patch(torch, "empty", lambda *a, **kw: made(empty(*a, **kw)))
         patch(torch, "empty_like", lambda *a, **kw: made(like(*a, **kw)))
         patch(torch.Tensor, "zero_", zeroed)
@@ -207,3 +208,17 @@ def test_the_layers_own_workspace_is_the_layers(monkeypatch, name):
                                                               lambda self, *a: 1 << 20})())
     call(stream=5)
     assert [t.numel() for _, t in watch.made if t.dtype is torch.uint8] == [1 << 16]
+
+
+# ------------------------------------------------------------------ the caller's buffers
+@pytest.mark.parametrize("name,buffer", [("norm_backward", "workspace"), ("routed", "workspace"),
+                                         ("routed_backward", "workspace"), ("routed_backward", "state"),
+                                         ("routed_train", None), ("orthogonalize", "workspace")])
+def test_a_workspace_in_host_memory_is_refused(monkeypatch, name, buffer):
+    """Its address is the kernels' to write to."""
+    call = calls()[name]
+    monkeypatch.setattr(m, "_lib", Library())
+    monkeypatch.setattr(mb, "_is", lambda *a: None)
+    monkeypatch.setattr(mb, "_stream", lambda s, device: 0)
+    with pytest.raises(ValueError, match="CUDA"):
+        call(**({buffer: torch.zeros(1 << 20, dtype=torch.uint8)} if buffer else {}))
