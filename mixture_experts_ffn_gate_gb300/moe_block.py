@@ -15,7 +15,7 @@ from typing import NamedTuple
 import torch
 
 from . import moe_ffn as _m
-from .moe_ffn import MOE_ERR_UNSUPPORTED_SHAPE, MoeFfnError, _empty, mx_scale_bytes
+from .moe_ffn import MOE_ERR_UNSUPPORTED_SHAPE, MoeFfnError, _empty_on, mx_scale_bytes
 
 MOE_BF16 = 0
 MOE_F32 = 1
@@ -92,7 +92,7 @@ def _check(status, what):
 def _workspace(n, device, stream, what):
     if n == 0:
         raise MoeFfnError(MOE_ERR_UNSUPPORTED_SHAPE, what)
-    return _empty((n,), torch.uint8, device, stream)
+    return (torch.empty if stream is None else _empty_on(stream))((n,), dtype=torch.uint8, device=device)
 
 
 def _size(t, name="workspace"):
@@ -119,13 +119,13 @@ def moe_rms_norm_forward(x, weight, residual=None, eps: float = 1e-6, bf16: bool
     T, H = x.shape
     _is(x, (T, H), x.dtype, "x")
     _is(weight, (H,), torch.float32, "weight")
-    dev = x.device
+    dev, empty = x.device, torch.empty if stream is None else _empty_on(stream)
     xt, rt = _type(x, "x"), 0
     if residual is not None:
         rt = _type(residual, "residual")
         _is(residual, (T, H), residual.dtype, "residual")
         if h is None:
-            h = _empty((T, H), residual.dtype, dev, stream)
+            h = empty((T, H), dtype=residual.dtype, device=dev)
         else:
             _is(h, (T, H), residual.dtype, "h")
     elif h is not None:
@@ -133,13 +133,13 @@ def moe_rms_norm_forward(x, weight, residual=None, eps: float = 1e-6, bf16: bool
     if y is not None:
         _is(y, (T, H), torch.bfloat16, "y")
     elif bf16:
-        y = _empty((T, H), torch.bfloat16, dev, stream)
+        y = empty((T, H), dtype=torch.bfloat16, device=dev)
     if codes is not None or scales is not None or mxfp8:
         Sh = mx_scale_bytes(H)
         if codes is None:
-            codes = _empty((T, H), torch.uint8, dev, stream)
+            codes = empty((T, H), dtype=torch.uint8, device=dev)
         if scales is None:
-            scales = _empty((T, Sh), torch.uint8, dev, stream)
+            scales = empty((T, Sh), dtype=torch.uint8, device=dev)
         _is(codes, (T, H), torch.uint8, "codes")
         _is(scales, (T, Sh), torch.uint8, "scales")
     p = _ptr
@@ -168,12 +168,13 @@ def moe_rms_norm_backward(h, weight, dy, dres=None, eps: float = 1e-6, dh=None, 
     _is(weight, (H,), torch.float32, "weight")
     if dres is not None:
         _is(dres, (T, H), h.dtype, "dres")
+    empty = torch.empty if stream is None else _empty_on(stream)
     if dh is None:
-        dh = _empty((T, H), h.dtype, h.device, stream)
+        dh = empty((T, H), dtype=h.dtype, device=h.device)
     else:
         _is(dh, (T, H), h.dtype, "dh")
     if dweight is None:
-        dweight = _empty((H,), torch.float32, h.device, stream)
+        dweight = empty((H,), dtype=torch.float32, device=h.device)
     else:
         _is(dweight, (H,), torch.float32, "dweight")
     if workspace is None:
@@ -211,17 +212,17 @@ def moe_gate_forward(logits, k: int, bias=None, score: str = "softmax", groups: 
     _is(logits, (T, E), torch.float32, "logits")
     if bias is not None:
         _is(bias, (E,), torch.float32, "bias")
-    dev = logits.device
+    dev, empty = logits.device, torch.empty if stream is None else _empty_on(stream)
     if topk_idx is None:
-        topk_idx = _empty((T, k), torch.int32, dev, stream)
+        topk_idx = empty((T, k), dtype=torch.int32, device=dev)
     else:
         _is(topk_idx, (T, k), torch.int32, "topk_idx")
     if topk_w is None:
-        topk_w = _empty((T, k), torch.float32, dev, stream)
+        topk_w = empty((T, k), dtype=torch.float32, device=dev)
     else:
         _is(topk_w, (T, k), torch.float32, "topk_w")
     if counts is True:
-        counts = _empty((E,), torch.int32, dev, stream)
+        counts = empty((E,), dtype=torch.int32, device=dev)
     elif counts is not None:
         _is(counts, (E,), torch.int32, "counts")
     o = _gate_opts(score, renormalize, scale, groups, topk_groups)
@@ -242,7 +243,8 @@ def moe_gate_backward(logits, topk_idx, dtopk_w, score: str = "softmax", renorma
     _is(topk_idx, (T, k), torch.int32, "topk_idx")
     _is(dtopk_w, (T, k), torch.float32, "dtopk_w")
     if dlogits is None:
-        dlogits = _empty((T, E), torch.float32, logits.device, stream)
+        empty = torch.empty if stream is None else _empty_on(stream)
+        dlogits = empty((T, E), dtype=torch.float32, device=logits.device)
     else:
         _is(dlogits, (T, E), torch.float32, "dlogits")
     o = _gate_opts(score, renormalize, scale)
@@ -284,7 +286,7 @@ def _experts(x, w_gate_up, w_down, dtype=torch.bfloat16):
 
 def _new(t, shape, name, device, stream):
     if t is None:
-        return _empty(shape, torch.float32, device, stream)
+        return (torch.empty if stream is None else _empty_on(stream))(shape, dtype=torch.float32, device=device)
     _is(t, shape, torch.float32, name)
     return t
 
@@ -381,7 +383,8 @@ def moe_orthogonalize(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
     gt = _type(g, "g")
     _is(g, (B, M, N), g.dtype, "g")
     if out is None:
-        out = _empty((B, M, N), torch.bfloat16, g.device, stream)
+        empty = torch.empty if stream is None else _empty_on(stream)
+        out = empty((B, M, N), dtype=torch.bfloat16, device=g.device)
     else:
         _is(out, (B, M, N), torch.bfloat16, "out")
     if workspace is None:

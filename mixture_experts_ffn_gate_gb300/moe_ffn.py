@@ -161,18 +161,20 @@ def _on(stream, device):
     return torch.cuda.stream(stream)
 
 
-def _empty(shape, dtype, device, stream=None):
-    """A tensor that a call on `stream` writes.  It is allocated on that
-    stream: what used its memory before, and what uses it after it is
-    dropped, is ordered with the call.  Released, it also waits for the
-    current stream's work of that moment, which may read it."""
-    here = _on(stream, device)
-    if here is _HERE:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with here:
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(device))
-    return t
+def _empty_on(stream):
+    """torch.empty for the tensors that a call on `stream` writes.  They are
+    allocated on that stream: what used their memory before, and what uses it
+    after they are dropped, is ordered with the call.  Released, they also
+    wait for the current stream's work of that moment, which may read them."""
+    def empty(shape, dtype, device):
+        here = _on(stream, device)
+        if here is _HERE:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with here:
+            t = torch.empty(shape, dtype=dtype, device=device)
+        t.record_stream(torch.cuda.current_stream(device))
+        return t
+    return empty
 
 
 def _state_buffer(n, device, stream, what):
@@ -181,7 +183,7 @@ def _state_buffer(n, device, stream, what):
     held other data."""
     if n == 0:
         raise MoeFfnError(MOE_ERR_UNSUPPORTED_SHAPE, what)
-    ws = _empty((n,), torch.uint8, device, stream)
+    ws = (torch.empty if stream is None else _empty_on(stream))((n,), dtype=torch.uint8, device=device)
     with _on(stream, device):
         ws[:MOE_FFN_WORKSPACE_STATE_BYTES].zero_()
     return ws
@@ -243,8 +245,9 @@ def moe_ffn_forward(x, logits, w_gate_up, w_down, k: int, out=None, stream=None)
     for t, d, n in ((x, torch.bfloat16, "x"), (logits, torch.float32, "logits"),
                     (w_gate_up, torch.bfloat16, "w_gate_up"), (w_down, torch.bfloat16, "w_down")):
         _dev(t, d, n)
+    empty = torch.empty if stream is None else _empty_on(stream)
     if out is None:
-        out = _empty((T, H), torch.float32, x.device, stream)
+        out = empty((T, H), dtype=torch.float32, device=x.device)
     _dev(out, torch.float32, "out")
     _check(lib().moe_ffn_forward(_ptr(x), _ptr(logits), _ptr(w_gate_up), _ptr(w_down),
                                  T, H, I, E, k, _ptr(out), _stream(stream)), "moe_ffn_forward")
@@ -261,8 +264,9 @@ def moe_ffn_forward_noalloc(x, logits, w_gate_up, w_down, k: int, out=None, stre
     for t, d, n in ((x, torch.bfloat16, "x"), (logits, torch.float32, "logits"),
                     (w_gate_up, torch.bfloat16, "w_gate_up"), (w_down, torch.bfloat16, "w_down")):
         _dev(t, d, n)
+    empty = torch.empty if stream is None else _empty_on(stream)
     if out is None:
-        out = _empty((T, H), torch.float32, x.device, stream)
+        out = empty((T, H), dtype=torch.float32, device=x.device)
     _dev(out, torch.float32, "out")
     _check(lib().moe_ffn_forward_noalloc(_ptr(x), _ptr(logits), _ptr(w_gate_up), _ptr(w_down),
                                          T, H, I, E, k, _ptr(out), _stream(stream)),
@@ -290,8 +294,9 @@ def moe_ffn_forward_ex(x, logits, w_gate_up, w_down, k: int, out=None, workspace
     for t, d, n in ((x, torch.bfloat16, "x"), (logits, torch.float32, "logits"),
                     (w_gate_up, torch.bfloat16, "w_gate_up"), (w_down, torch.bfloat16, "w_down")):
         _dev(t, d, n)
+    empty = torch.empty if stream is None else _empty_on(stream)
     if out is None:
-        out = _empty((T, H), torch.float32, x.device, stream)
+        out = empty((T, H), dtype=torch.float32, device=x.device)
     if workspace is None:
         workspace = new_workspace(T, H, I, E, k, device=x.device, stream=stream, routed=False)
     if topk_idx is not None:
@@ -336,8 +341,9 @@ def moe_ffn_forward_router(x, w_router, router_bias, w_gate_up, w_down, k: int, 
                     (topk_w, torch.float32, "topk_w")):
         if t is not None:
             _dev(t, d, n)
+    empty = torch.empty if stream is None else _empty_on(stream)
     if out is None:
-        out = _empty((T, H), torch.float32, x.device, stream)
+        out = empty((T, H), dtype=torch.float32, device=x.device)
     if workspace is None:
         workspace = new_router_workspace(T, H, I, E, k, device=x.device, stream=stream)
     _check(lib().moe_ffn_forward_router(
@@ -377,8 +383,9 @@ def moe_ffn_forward_mxfp8(x, logits, w_gate_up_q, w_gate_up_s, w_down_q, w_down_
     for t, d, n in ((topk_idx, torch.int32, "topk_idx"), (topk_w, torch.float32, "topk_w")):
         if t is not None:
             _dev(t, d, n)
+    empty = torch.empty if stream is None else _empty_on(stream)
     if out is None:
-        out = _empty((T, H), torch.float32, x.device, stream)
+        out = empty((T, H), dtype=torch.float32, device=x.device)
     if workspace is None:
         workspace = new_workspace(T, H, I, E, k, device=x.device, stream=stream, routed=False)
     _check(lib().moe_ffn_forward_mxfp8(
@@ -431,15 +438,15 @@ def moe_ffn_backward(x, logits, w_gate_up, w_down, dout, k: int, dx=None, dlogit
         _dev(t, d, n)
     if tuple(dout.shape) != (T, H):
         raise ValueError(f"dout must be [{T}, {H}], got {tuple(dout.shape)}")
-    dev = x.device
+    dev, empty = x.device, torch.empty if stream is None else _empty_on(stream)
     if dx is None:
-        dx = _empty((T, H), torch.float32, dev, stream)
+        dx = empty((T, H), dtype=torch.float32, device=dev)
     if dlogits is None:
-        dlogits = _empty((T, E), torch.float32, dev, stream)
+        dlogits = empty((T, E), dtype=torch.float32, device=dev)
     if dw_gate_up is None:
-        dw_gate_up = _empty((E, 2 * I, H), torch.float32, dev, stream)
+        dw_gate_up = empty((E, 2 * I, H), dtype=torch.float32, device=dev)
     if dw_down is None:
-        dw_down = _empty((E, H, I), torch.float32, dev, stream)
+        dw_down = empty((E, H, I), dtype=torch.float32, device=dev)
     for t, shape, n in ((dx, (T, H), "dx"), (dlogits, (T, E), "dlogits"), (dw_gate_up, (E, 2 * I, H), "dw_gate_up"),
                         (dw_down, (E, H, I), "dw_down")):
         _dev(t, torch.float32, n)
@@ -474,8 +481,9 @@ def moe_ffn_forward_train(x, logits, w_gate_up, w_down, k: int, state, out=None,
                     (w_gate_up, torch.bfloat16, "w_gate_up"), (w_down, torch.bfloat16, "w_down"),
                     (state, torch.uint8, "state")):
         _dev(t, d, n)
+    empty = torch.empty if stream is None else _empty_on(stream)
     if out is None:
-        out = _empty((T, H), torch.float32, x.device, stream)
+        out = empty((T, H), dtype=torch.float32, device=x.device)
     _dev(out, torch.float32, "out")
     if tuple(out.shape) != (T, H):
         raise ValueError(f"out must be [{T}, {H}], got {tuple(out.shape)}")
@@ -498,15 +506,15 @@ def moe_ffn_backward_train(x, logits, w_gate_up, w_down, dout, k: int, state, dx
         _dev(t, d, n)
     if tuple(dout.shape) != (T, H):
         raise ValueError(f"dout must be [{T}, {H}], got {tuple(dout.shape)}")
-    dev = x.device
+    dev, empty = x.device, torch.empty if stream is None else _empty_on(stream)
     if dx is None:
-        dx = _empty((T, H), torch.float32, dev, stream)
+        dx = empty((T, H), dtype=torch.float32, device=dev)
     if dlogits is None:
-        dlogits = _empty((T, E), torch.float32, dev, stream)
+        dlogits = empty((T, E), dtype=torch.float32, device=dev)
     if dw_gate_up is None:
-        dw_gate_up = _empty((E, 2 * I, H), torch.float32, dev, stream)
+        dw_gate_up = empty((E, 2 * I, H), dtype=torch.float32, device=dev)
     if dw_down is None:
-        dw_down = _empty((E, H, I), torch.float32, dev, stream)
+        dw_down = empty((E, H, I), dtype=torch.float32, device=dev)
     for t, shape, n in ((dx, (T, H), "dx"), (dlogits, (T, E), "dlogits"), (dw_gate_up, (E, 2 * I, H), "dw_gate_up"),
                         (dw_down, (E, H, I), "dw_down")):
         _dev(t, torch.float32, n)
