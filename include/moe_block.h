@@ -45,15 +45,17 @@ enum { MOE_BF16 = 0, MOE_F32 = 1 };
  *   y_e4m3, y_scale  nullable (both or none): y in MXFP8, the layout of
  *              moe_ffn.h's MXFP8 tensors: codes [T,H] and E8M0 scales
  *              [T, MOE_FFN_MX_SCALE_BYTES(H)], one per 32 elements of a row
- *              (2^(floor(log2 amax) - 8), 1 for a block of zeros; the pad
- *              bytes are written as zeros), elements rounded to nearest,
+ *              (2^(floor(log2 amax) - 8), at least 2^-126, 1 for a block of
+ *              zeros; the pad bytes are written as zeros), elements rounded to nearest,
  *              ties to even, from the FP32 y and clamped to +-448.  A block
  *              that holds a NaN or an infinity gets the scale 255 (NaN), its
  *              codes then say nothing.
  * The norm is taken of the FP32 h, before h_out is rounded.  Limits: H in
  * 1..16384 (H % 32 == 0 for MXFP8), T * H < 2^40, eps >= 0.  At least one of
  * y_bf16 and y_e4m3 is asked for.  A row of zeros with eps == 0 gives NaN, as
- * the formula does.
+ * the formula does.  Squares are summed in FP32: elements below about 1e-22
+ * count as zero in the mean, and a row whose sum of squares is beyond FP32's
+ * range (one element of 1.8e19) gives y = 0.
  */
 int moe_rms_norm_forward(const void *x, int x_type, const void *residual, int res_type,
                          const float *weight_f32, float eps, int64_t T, int64_t H,
@@ -61,7 +63,9 @@ int moe_rms_norm_forward(const void *x, int x_type, const void *residual, int re
                          cudaStream_t stream);
 
 /*
- * Its gradients, from h (what the norm was taken of) and dy = dL/dy:
+ * Its gradients at h, from dy = dL/dy.  (The forward call's h_out is h rounded
+ * to the stream's type: with a BF16 stream these are the gradients at the
+ * rounded h, within BF16's rounding of those at the h of the norm.)
  *   n  = h / sqrt(mean(h^2) + eps),   g = dy * weight
  *   dh = (g - n * mean(g * n)) / sqrt(mean(h^2) + eps) + dres
  *   dweight = sum over the rows of dy * n

@@ -104,7 +104,7 @@ class MoeBlock:
     def train_backward(self, saved, dout, dstream):
         """Its gradients for dout f32 [T,H] and dstream (the gradient that
         reaches the new stream besides): a dict; "x" is that of both x and the
-        residual."""
+        residual.  The norm's are taken at the new stream, h as it is kept."""
         y, h, logits, choice, state = saved
         dy, dw, dw_gate_up, dw_down = mb.moe_ffn_backward_routed(y, choice.topk_idx, choice.topk_w, self.w_gate_up,
                                                                  self.w_down, dout, state=state)

@@ -952,7 +952,7 @@ __global__ void __launch_bounds__(256) ortho_split_kernel(const T *__restrict__ 
 // every product.  Rows and columns past the matrix are zeros.  The general
 // kernel's tiles go through L2 between products, 4.4 us each; here a product
 // takes 3.4 us (1.3 us of MMAs, 0.9 to 2.2 us of epilogue, the rest signals).
-// Measured, us there and here: 8 x 256 x 256 86, 64; 76 x 256 x 256 120, 67;
+// Measured, us there and here: 8 x 256 x 256 86, 65; 76 x 256 x 256 120, 67;
 // 300 x 256 x 256 328, 266; 1 x 72 x 71 68, 52; 300 x 128 x 128 212, 191
 // (600 x 64 x 64, the one that is slower here, 271, 324).
 constexpr int kSmall = 256;
@@ -1455,8 +1455,10 @@ cudaError_t launch_orthogonalize(const OrthoCall &c, void *workspace, int pairs,
     // fill the last wave.  Measured, us for 256 / 256, 128 / 256, 128 / 128
     // (symmetric products / apply): 1 x 1536 x 2048 220, 197, 225 (42 and 96
     // tiles of 128 for 76 pairs); 1 x 1000 x 1000 204, 176, 156 (20, 32);
-    // 2 x 1536 x 2048 249, 253, 277 (84, 192); 40 x 256 x 256 113, 105, 95
-    // (80, 80); 6 x 768 x 2048 218, 204, 231 (72, 288)
+    // 2 x 1536 x 2048 249, 253, 277 (84, 192); 6 x 768 x 2048 218, 204, 231
+    // (72, 288).  A batch's 13 / 12, without and with it, where it decides:
+    // 40 x 256 x 300 126, 112 and 20 x 384 x 1000 197, 183 (80 symmetric
+    // tiles); 13 x 256 x 768 104, 98 (78 of apply), 10 x 300 x 500 112, 109 (80)
     auto fit = [&](int64_t tiles) { return c.B == 1 ? tiles <= pairs : 12 * c.B * tiles <= 13 * pairs; };
     const bool sym128 = fit(sym_tiles(L.m, 128));
     const bool x128 = fit(ceil_div(L.m, 256) * ceil_div(L.n, 128));
