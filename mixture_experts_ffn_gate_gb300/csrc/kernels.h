@@ -45,7 +45,7 @@ cudaError_t launch_sort(const int32_t *idx, int n_assign, int E, int chunk_max, 
                         cudaStream_t s, int pad = 1, int32_t *counts = nullptr);
 // w (nullable): without it the rows are summed unweighted
 cudaError_t launch_combine(const float *z, const float *w, const int32_t *pos, int T, int H, int k, float *out,
-                           int n_sm, cudaStream_t s);
+                           int n_sm, cudaStream_t s, bool drops = false);
 
 // decode.cu
 cudaError_t decode_init_device();

@@ -325,7 +325,7 @@ int run_forward(const void *x, const float *logits, const void *wgu, const void 
             MOE_TRY(stg.done(moe::launch_gemm_down(act_hi, act_lo, wd, chunks, nchunks, offs, n_assign, H, I, E, z,
                                                    gemm_ctas, stream, routing ? ws + L.act_lo2 : nullptr)));
         }
-        MOE_TRY(stg.done(moe::launch_combine(z, w, pos, T, H, k, out, dev->n_sm, stream)));
+        MOE_TRY(stg.done(moe::launch_combine(z, w, pos, T, H, k, out, dev->n_sm, stream, routing != nullptr)));
     }
     if (opts) {
         opts->n_stages = stg.n;
@@ -454,7 +454,7 @@ int run_backward(const void *x, const float *logits, const void *wgu, const void
     }
     MOE_TRY(stg.done(moe::launch_bwd_dx(ws + L.dgu_hi, ws + L.dgu_lo, wgu, chunks, nchunks, offs, rows, H, I, E, z,
                                         ctas, stream, dgu_lo2)));
-    MOE_TRY(stg.done(moe::launch_combine(z, nullptr, pos, T, H, k, dx, dev->n_sm, stream)));
+    MOE_TRY(stg.done(moe::launch_combine(z, nullptr, pos, T, H, k, dx, dev->n_sm, stream, seg)));
     MOE_TRY(stg.done(moe::launch_zero_untouched(counts, E, H, I, dwgu, dwd, stream)));
     MOE_TRY(stg.done(moe::launch_wgrad_down(ws + L.ds_hi, ws + L.ds_lo, ws + L.wa_hi, ws + L.wa_lo, offs, counts,
                                             rows, H, I, E, dwd, ctas, stream, ds_lo2, wa_lo2)));
@@ -508,7 +508,7 @@ int run_forward_train(const void *x, const float *logits, const void *wgu, const
                                                    (float *)(ws + L.u), ctas, stream, act_lo2)));
     MOE_TRY(stg.done(moe::launch_gemm_down(ws + L.wa_hi, ws + L.wa_lo, wd, chunks, nchunks, offs, rows, H, I, E, z,
                                            ctas, stream, act_lo2)));
-    MOE_TRY(stg.done(moe::launch_combine(z, w, pos, T, H, k, out, dev->n_sm, stream)));
+    MOE_TRY(stg.done(moe::launch_combine(z, w, pos, T, H, k, out, dev->n_sm, stream, routing != nullptr)));
     if (opts) {
         opts->n_stages = stg.n;
         opts->path_taken = MOE_PATH_TRAIN_FORWARD;
