@@ -8,8 +8,11 @@
  * experts and chooses k of them for every token (moe_gate_forward); the
  * experts run for that routing (moe_ffn_forward_routed).  Training adds the
  * gradients of the three (moe_ffn_backward_routed, moe_gate_backward,
- * moe_rms_norm_backward) and the orthogonalised update of the experts'
- * weight matrices (moe_orthogonalize).
+ * moe_rms_norm_backward), the gate's load-balance loss with its gradient
+ * (moe_balance_loss_forward, moe_balance_loss_backward), the clipping of the
+ * gradients by their norm (moe_grad_norm) and the updates: orthogonalised for
+ * the experts' weight matrices (moe_orthogonalize), AdamW for many tensors of
+ * any kind (moe_adamw_step).
  *
  * Conventions: those of moe_ffn.h (row-major contiguous device tensors owned
  * by the caller, 16-byte aligned base pointers, 256-byte aligned workspaces,
@@ -252,6 +255,174 @@ size_t moe_orthogonalize_workspace_bytes(int64_t B, int64_t M, int64_t N);
 int moe_orthogonalize(const void *g, int g_type, int64_t B, int64_t M, int64_t N, int steps,
                       float a, float b, float c, float eps, float out_scale, void *out_bf16,
                       void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * The load-balance loss of the gate's logits, and what training watches of
+ * it: how many tokens chose each expert, and the experts' mean probabilities.
+ *   score  MOE_SCORE_SOFTMAX: s_te = softmax(l_t)_e over all E;
+ *          MOE_SCORE_SIGMOID: s_te = q_te / sum_e q_te, q = 1 / (1 + exp(-l))
+ *   coef, z_coef: the factors of the two losses (0: that part is left out)
+ */
+typedef struct moe_balance_opts {
+    int32_t score;
+    float coef;
+    float z_coef;
+    int32_t reserved[5]; /* must be zero */
+} moe_balance_opts;
+
+/*
+ * The tokens are S packed sequences: sequence i has the rows
+ * [seq_offsets[i], seq_offsets[i+1]), n_i of them, N in all.  Rows before the
+ * first sequence and behind the last belong to none: they have no part in
+ * anything and are not read, whatever they hold.  Without seq_offsets all T
+ * rows are one sequence (S == 1).
+ *   counts[i,e] = rows of sequence i among whose k slots e is (a slot outside
+ *                 [0, E), and a repeated one, counts for nothing)
+ *   prob[i,e]   = mean over its rows of s_te (0 for an empty sequence)
+ *   balance     = sum_i n_i / N * E * sum_e counts[i,e] / (k n_i) * prob[i,e]
+ *                 (1 where every expert is as likely and as loaded as any)
+ *   z           = sum_t logsumexp(l_t)^2 / N
+ *   loss_f32[0] = coef * balance + z_coef * z; [1] = balance; [2] = z (0 with
+ *                 z_coef == 0).  N == 0 gives zeros.
+ *   logits_f32 [T,E]; topk_idx int32 [T,k]; seq_offsets nullable int32 [S+1],
+ *   ascending, in 0..T (others give meaningless results, but no access out of
+ *   bounds); loss_f32 [3]; counts int32 [S,E]; prob_f32 [S,E]
+ * A row of logits that are all -inf, or of sigmoids whose sum is below 2^-126,
+ * has s = 0 and no z; a NaN among a row's logits, or a +inf with softmax or z,
+ * makes its sequence's prob and the losses NaN.
+ * Sums are FP32, in an order fixed by T, S, E and the device; the
+ * probabilities are as exact as expf and a reciprocal within one unit make
+ * them.  Limits: those of the gate (E <= 1024, k <= 32, T * E < 2^40,
+ * T * k < 2^30), S in 1..2^20, finite coefficients.  T == 0
+ * writes its outputs too.  workspace: at least
+ * moe_balance_loss_workspace_bytes (0 for an invalid shape); it needs no
+ * initial content.
+ */
+size_t moe_balance_loss_workspace_bytes(int64_t T, int64_t S, int64_t E);
+int moe_balance_loss_forward(const float *logits_f32, const int32_t *topk_idx,
+                             const int32_t *seq_offsets, int64_t T, int64_t S, int64_t E,
+                             int64_t k, const moe_balance_opts *opts, float *loss_f32,
+                             int32_t *counts, float *prob_f32, void *workspace,
+                             size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Its gradient at the logits, added to the one that reaches them besides
+ * (moe_gate_backward's):
+ *   dlogits = dloss * d loss_f32[0] / d logits + dlogits_in
+ * The counts are piecewise constant in the logits and have no gradient:
+ *   a_ie = coef * E * counts[i,e] / (k n_i N)
+ *   softmax: s_e (a_e - sum a s); sigmoid: (a_e - sum a s) q_e (1 - q_e) / sum q
+ *   z: 2 z_coef / N * logsumexp(l) * softmax(l)_e
+ * Scores are computed again from the logits.  Rows of no sequence take
+ * dlogits_in (0 without one), whatever their logits hold.
+ *   counts        the forward call's, or the caller's own (of a larger batch,
+ *                 scaled to this one's n_i)
+ *   dloss_f32     nullable [1], the gradient at loss_f32[0] (1 without it)
+ *   dlogits_in_f32 nullable [T,E]; dlogits_f32 [T,E] may be dlogits_in itself
+ * Same limits; T == 0 enqueues nothing.
+ */
+int moe_balance_loss_backward(const float *logits_f32, const int32_t *counts,
+                              const int32_t *seq_offsets, int64_t T, int64_t S, int64_t E,
+                              int64_t k, const moe_balance_opts *opts,
+                              const float *dloss_f32, const float *dlogits_in_f32,
+                              float *dlogits_f32, cudaStream_t stream);
+
+/* One of many tensors: n contiguous elements of a type, 16-byte aligned. */
+typedef struct moe_tensor {
+    const void *data;
+    int64_t n;
+    int32_t type;     /* MOE_BF16 or MOE_F32 */
+    int32_t reserved; /* must be zero */
+} moe_tensor;
+
+/*
+ * The norm of many gradients together, and the factor that clips it.
+ *   out_f32[0] = sqrt(sum over all elements of g^2)
+ *   out_f32[1] = max_norm / norm where norm > max_norm, else 1; NaN where the
+ *                norm is no finite FP32 number (moe_adamw_step then leaves its
+ *                step out)
+ *   grads     host array of `count` descriptors, read before the call returns
+ *   max_norm  > 0; infinity for the norm alone
+ * Squares are summed in FP32 per thread and in FP64 from there on, in an order
+ * fixed by the tensors' sizes and the device.  A sum beyond FP32's range is
+ * taken of the elements times 2^-64, so the norm holds up to FP32's largest;
+ * elements below about 1e-22 count as zero.  Limits: count <= 65536, sum of n
+ * <= 2^42.  Without elements the norm is 0 and the factor 1.  workspace: at
+ * least moe_grad_norm_workspace_bytes(count), no initial content.
+ */
+size_t moe_grad_norm_workspace_bytes(int64_t count);
+int moe_grad_norm(const moe_tensor *grads, int64_t count, float max_norm, float *out_f32,
+                  void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Elements that share a scale of an 8-bit state. */
+#define MOE_ADAMW_STATE_BLOCK 256
+
+/*
+ * A tensor of an AdamW step: n elements, contiguous, all updated in place.
+ *   w       w_type; with `master` (FP32, nullable) the master is the weight and
+ *           w takes its rounding
+ *   grad    grad_type, read
+ *   m, v    the moments: state_bits 32: FP32.  state_bits 8: E4M3 codes of
+ *           m / m_scale and of sqrt(v) / v_scale, one FP32 scale per
+ *           MOE_ADAMW_STATE_BLOCK elements (the last block may be shorter):
+ *           the block's largest magnitude / 448, at least 2^-126.  Codes are
+ *           rounded to nearest, ties to even, but a v above zero takes at
+ *           least the lowest code.  The step computes with the values before
+ *           they are rounded.  Zeros (of codes and scales) are the initial
+ *           state.  A NaN stays with its element, an infinity makes its block
+ *           NaN.
+ *   lr_factor, weight_decay: this tensor's own
+ * All pointers 16-byte aligned, the scales 4-byte.
+ */
+typedef struct moe_adamw_tensor {
+    void *w;
+    float *master;
+    const void *grad;
+    void *m;
+    void *v;
+    float *m_scale;
+    float *v_scale;
+    int64_t n;
+    int32_t w_type;
+    int32_t grad_type;
+    int32_t state_bits; /* 32 or 8 */
+    float lr_factor;
+    float weight_decay;
+    int32_t reserved; /* must be zero */
+} moe_adamw_tensor;
+
+typedef struct moe_adamw_opts {
+    double lr;    /* finite, >= 0 */
+    double beta1; /* 0 <= beta < 1 */
+    double beta2;
+    double eps;   /* >= 0 */
+    int64_t step; /* this step's number, from 1 (ignored with step_i32) */
+    int64_t reserved[3]; /* must be zero */
+} moe_adamw_opts;
+
+/*
+ * One AdamW step of many tensors:
+ *   g = grad_scale * grad;  lr_i = lr * lr_factor
+ *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   w = w - lr_i weight_decay w
+ *         - lr_i (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
+ *   tensors        host array of `count` descriptors, read before the call
+ *                  returns.  What is written (w, master, m, v, scales) must not
+ *                  overlap with anything else in the call; gradients may.
+ *   grad_scale_f32 nullable device [1] (moe_grad_norm's out_f32 + 1): the
+ *                  gradients' factor; where it is NaN or infinite the whole
+ *                  step is left out and nothing changes
+ *   lr_f32         nullable device [1]: in the place of opts->lr
+ *   step_i32       nullable device [1]: the number of steps taken so far; the
+ *                  call adds one, unless the step is left out.  With it (and
+ *                  lr_f32) a captured graph's replays are successive steps.
+ *   workspace      with step_i32: at least 256 bytes, else nullable
+ * Arithmetic in FP32 but for the corrections by the betas' powers (FP64).
+ * Limits: count <= 65536, sum of n <= 2^42.
+ */
+int moe_adamw_step(const moe_adamw_tensor *tensors, int64_t count, const moe_adamw_opts *opts,
+                   const float *grad_scale_f32, const float *lr_f32, int32_t *step_i32,
+                   void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,509 @@
+// adamw.cu -- the norm of many gradients with the factor that clips it, and
+// an AdamW step of many tensors with states in FP32 or in 8 bits.
+//
+//   norm = sqrt(sum g^2), factor = min(1, max / norm)
+//   g' = factor g;  m = b1 m + (1 - b1) g';  v = b2 v + (1 - b2) g'^2
+//   w = w (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
+//
+// The tensors' addresses and sizes travel in the kernel's parameters, up to
+// 256 (512) of them per launch, so a call copies nothing to the device first and
+// may be captured.  A block takes one chunk of one tensor, found by bisection
+// in the chunks' running count.  Both kernels read every byte once and write
+// every byte once, and DRAM bounds them.
+//
+// 8-bit states: E4M3 codes of m / scale and sqrt(v) / scale, with one FP32
+// scale per 256 elements, the largest magnitude / 448.  A floating code keeps
+// small elements to 2^-4 of their size next to large ones; the scale is FP32
+// and not a power of two because the largest element then is its own code
+// times the scale exactly: elements that get no gradient decay by the factor
+// b1 or b2 through it, where a rounded scale would hold them where they are.
+// sqrt(v) needs half of v's range, and one that is not zero takes at least
+// the lowest code, so that no m is divided by eps alone.
+#include <math.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "sm100_ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kSmallBatch = 16;   // tensors of a launch, in calls of few
+constexpr int kStepBatch = 256;   // and in others: 21 KB of parameters
+constexpr int kNormBatch = 512;   // 14 KB
+constexpr int kThreads = 256;
+constexpr int kBlock8 = 256;        // elements that share a scale: eight to a lane
+constexpr int kChunk = 4096;        // elements of a block of the step
+constexpr int kNormChunk = 16384;   // elements that a block of the norm takes at a time
+constexpr int kNormBlocks = 1024;   // its partial sums per launch, at most
+constexpr float kTop = 448.0f;      // the largest E4M3 value
+constexpr float kLowest = 0.001953125f;  // the smallest, 2^-9
+constexpr float kShrink = 5.421010862427522e-20f;  // 2^-64
+
+// The tensors of one launch; first[i] is the chunks before tensor i.
+template <typename Tensor, int CAP>
+struct Batch {
+    Tensor t[CAP];
+    uint32_t first[CAP + 1];
+    int count;
+};
+
+// Which tensor a chunk belongs to.
+template <typename B>
+__device__ __forceinline__ int find_tensor(const B &b, uint32_t chunk)
+{
+    int lo = 0, hi = b.count;  // first[lo] <= chunk < first[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (b.first[mid] <= chunk)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// ---------------------------------------------------------------- elements
+// N consecutive elements from `e` on, FP32 or BF16, zero from n on.
+template <int N>
+__device__ __forceinline__ void load_n(const float *p, int64_t e, int64_t n, float (&v)[N])
+{
+    if (e + N <= n) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const float4 q = *reinterpret_cast<const float4 *>(p + e + i);
+            v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = e + i < n ? p[e + i] : 0.0f;
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void load_n(const __nv_bfloat16 *p, int64_t e, int64_t n, float (&v)[N])
+{
+    if (e + N <= n) {
+        uint32_t w[N / 2];
+        if constexpr (N == 8) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(p + e);
+            w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+        } else {
+            const uint2 q = *reinterpret_cast<const uint2 *>(p + e);
+            w[0] = q.x, w[1] = q.y;
+        }
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) v[2 * i] = bf16lo(w[i]), v[2 * i + 1] = bf16hi(w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = e + i < n ? __bfloat162float(p[e + i]) : 0.0f;
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void store_n(float *p, int64_t e, int64_t n, const float (&v)[N])
+{
+    if (e + N <= n) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            *reinterpret_cast<float4 *>(p + e + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (e + i < n) p[e + i] = v[i];
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void store_n(__nv_bfloat16 *p, int64_t e, int64_t n, const float (&v)[N])
+{
+    if (e + N <= n) {
+        uint32_t w[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const __nv_bfloat162 q = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&q);
+        }
+        if constexpr (N == 8)
+            *reinterpret_cast<uint4 *>(p + e) = make_uint4(w[0], w[1], w[2], w[3]);
+        else
+            *reinterpret_cast<uint2 *>(p + e) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (e + i < n) p[e + i] = __float2bfloat16_rn(v[i]);
+    }
+}
+
+// Eight E4M3 codes from `e` on, as values without their scale.
+__device__ __forceinline__ void load_codes(const uint8_t *p, int64_t e, int64_t n, float (&v)[8])
+{
+    uint2 w = make_uint2(0u, 0u);
+    if (e + 8 <= n) {
+        w = *reinterpret_cast<const uint2 *>(p + e);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (e + i < n) (i < 4 ? w.x : w.y) |= (uint32_t)p[e + i] << (8 * (i & 3));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t two = ((i < 2 ? w.x : w.y) >> (16 * (i & 1))) & 0xffffu;
+        const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3)));
+        v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    }
+}
+
+__device__ __forceinline__ void store_codes(uint8_t *p, int64_t e, int64_t n, const float (&v)[8])
+{
+    uint2 w = make_uint2(0u, 0u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+        (i < 2 ? w.x : w.y) |= two << (16 * (i & 1));
+    }
+    if (e + 8 <= n) {
+        *reinterpret_cast<uint2 *>(p + e) = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (e + i < n) p[e + i] = (uint8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+    }
+}
+
+// ---------------------------------------------------------------- norm
+using NormBatch = Batch<TensorRef, kNormBatch>;
+using NormBatchSmall = Batch<TensorRef, kSmallBatch>;
+
+// A block's sums of squares of its chunks: of the elements and of the
+// elements times 2^-64, which holds where the first one is beyond FP32.
+template <typename B>
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ B b, double2 *partial)
+{
+    __shared__ double part[2][kThreads / 32];
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    float s[4] = {}, r[4] = {};
+    auto add = [&](const float (&v)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s[i] = fmaf(v[i], v[i], s[i]);
+            const float small = v[i] * kShrink;
+            r[i] = fmaf(small, small, r[i]);
+        }
+    };
+    const uint32_t chunks = b.first[b.count];
+    for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const int k = find_tensor(b, c);
+        const int64_t n = b.t[k].n, at = (int64_t)(c - b.first[k]) * kNormChunk;
+        const int64_t end = n < at + kNormChunk ? n : at + kNormChunk;
+        constexpr int FLIGHT = 4;
+        auto run = [&](const auto *p) {
+            for (int64_t e = at + threadIdx.x * 4; e < end; e += kThreads * 4 * FLIGHT) {
+                float v[FLIGHT][4];
+#pragma unroll
+                for (int u = 0; u < FLIGHT; ++u) load_n<4>(p, e + u * kThreads * 4, end, v[u]);
+#pragma unroll
+                for (int u = 0; u < FLIGHT; ++u) add(v[u]);
+            }
+        };
+        if (b.t[k].f32)
+            run((const float *)b.t[k].data);
+        else
+            run((const __nv_bfloat16 *)b.t[k].data);
+    }
+    double x = (double)((s[0] + s[1]) + (s[2] + s[3])), y = (double)((r[0] + r[1]) + (r[2] + r[3]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+        y += __shfl_xor_sync(0xffffffffu, y, o);
+    }
+    if ((threadIdx.x & 31) == 0) part[0][threadIdx.x >> 5] = x, part[1][threadIdx.x >> 5] = y;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        x = y = 0.0;
+        for (int w = 0; w < kThreads / 32; ++w) x += part[0][w], y += part[1][w];
+        partial[blockIdx.x] = make_double2(x, y);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads) norm_factor_kernel(const double2 *partial, int n, float max_norm,
+                                                               float *out)
+{
+    __shared__ double part[2][kThreads / 32];
+    ptx::griddep_wait();
+    double x = 0.0, y = 0.0;
+    for (int i = threadIdx.x; i < n; i += kThreads) x += partial[i].x, y += partial[i].y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+        y += __shfl_xor_sync(0xffffffffu, y, o);
+    }
+    if ((threadIdx.x & 31) == 0) part[0][threadIdx.x >> 5] = x, part[1][threadIdx.x >> 5] = y;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        x = y = 0.0;
+        for (int w = 0; w < kThreads / 32; ++w) x += part[0][w], y += part[1][w];
+        const float norm = (float)(isinf(x) ? sqrt(y) * 18446744073709551616.0 : sqrt(x));
+        out[0] = norm;
+        out[1] = !isfinite(norm) ? NAN : norm > max_norm ? max_norm / norm : 1.0f;
+    }
+}
+
+// ---------------------------------------------------------------- the step
+using StepBatch = Batch<AdamWTensor, kStepBatch>;
+using StepBatchSmall = Batch<AdamWTensor, kSmallBatch>;
+
+// What an element's update takes.
+struct Element {
+    float b1, a1, b2, a2;  // the betas and 1 - them
+    float g_scale, decay, step, root, eps;
+
+    // m, v and w after the step; returns sqrt(v).  The moments' products and
+    // sums are rounded one by one: an 8-bit code next to a tie goes by their
+    // last bit, which then is the formula's in FP32 and not a contraction's.
+    // The quotient's two units in the last place are small against w's.
+    __device__ __forceinline__ float operator()(float g, float &m, float &v, float &w) const
+    {
+        g = __fmul_rn(g, g_scale);
+        m = __fadd_rn(__fmul_rn(b1, m), __fmul_rn(a1, g));
+        v = __fadd_rn(__fmul_rn(b2, v), __fmul_rn(__fmul_rn(a2, g), g));
+        const float r = __fsqrt_rn(v);
+        w = fmaf(w, decay, -step * __fdividef(m, fmaf(r, root, eps)));
+        return r;
+    }
+};
+
+template <typename W, bool MASTER>
+__device__ __forceinline__ const auto *source(const AdamWTensor &t)
+{
+    if constexpr (MASTER)
+        return (const float *)t.master;
+    else
+        return (const W *)t.w;
+}
+
+// FP32 states: four elements per thread at a time.
+template <typename W, typename G, bool MASTER>
+__device__ __forceinline__ void step_chunk(const AdamWTensor &t, int64_t at, int64_t end, const Element &el)
+{
+    constexpr int FLIGHT = 2;
+    float *const ms = (float *)t.m, *const vs = (float *)t.v;
+    for (int64_t e = at + threadIdx.x * 4; e < end; e += kThreads * 4 * FLIGHT) {
+        float g[FLIGHT][4], m[FLIGHT][4], v[FLIGHT][4], w[FLIGHT][4];
+#pragma unroll
+        for (int u = 0; u < FLIGHT; ++u) {
+            const int64_t i = e + u * kThreads * 4;
+            load_n<4>((const G *)t.grad, i, end, g[u]);
+            load_n<4>(ms, i, end, m[u]);
+            load_n<4>(vs, i, end, v[u]);
+            load_n<4>(source<W, MASTER>(t), i, end, w[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < FLIGHT; ++u) {
+            const int64_t i = e + u * kThreads * 4;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) el(g[u][q], m[u][q], v[u][q], w[u][q]);
+            store_n<4>(ms, i, end, m[u]);
+            store_n<4>(vs, i, end, v[u]);
+            if (MASTER) store_n<4>((float *)t.master, i, end, w[u]);
+            store_n<4>((W *)t.w, i, end, w[u]);
+        }
+    }
+}
+
+// The scale of a warp's 256 values and what they are over it, rounded once:
+// with the rounded reciprocal y of the scale, q = x y, r = x - q scale (exact)
+// and q + r y is the rounded quotient (Markstein's division by a multiply and
+// a correction, IBM J. Res. Dev. 34, 1990).  x y alone is off by a unit now
+// and then, and takes other codes next to ties.
+__device__ __forceinline__ float scale_block(float (&x)[8], bool up)
+{
+    float top = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) top = fmaxf(top, fabsf(x[q]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float scale = fmaxf(__fmul_rn(top, 1.0f / kTop), 1.17549435e-38f), inv = __frcp_rn(scale);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float q = x[i] * inv, r = fmaf(-q, scale, x[i]);
+        x[i] = up && x[i] > 0.0f ? fmaxf(fmaf(r, inv, q), kLowest) : fmaf(r, inv, q);
+    }
+    return scale;
+}
+
+// 8-bit states: a warp takes 256 elements, a scale's block, eight to a lane.
+template <typename W, typename G, bool MASTER>
+__device__ __forceinline__ void step_chunk_8bit(const AdamWTensor &t, int64_t at, int64_t end, const Element &el)
+{
+    const int lane = threadIdx.x & 31;
+    for (int64_t block = at + (threadIdx.x >> 5) * kBlock8; block < end; block += kThreads / 32 * kBlock8) {
+        const int64_t e = block + lane * 8, s = block / kBlock8;
+        float g[8], m[8], v[8], w[8];
+        load_n<8>((const G *)t.grad, e, end, g);
+        load_codes((const uint8_t *)t.m, e, end, m);
+        load_codes((const uint8_t *)t.v, e, end, v);
+        load_n<8>(source<W, MASTER>(t), e, end, w);
+        const float m_scale = t.m_scale[s], v_scale = t.v_scale[s];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            m[q] *= m_scale;
+            v[q] *= v_scale;
+            v[q] *= v[q];
+            v[q] = el(g[q], m[q], v[q], w[q]);
+        }
+        if (MASTER) store_n<8>((float *)t.master, e, end, w);
+        store_n<8>((W *)t.w, e, end, w);
+        // elements past the tensor's end are zero and stay so: they raise no scale
+        const float m_new = scale_block(m, false), v_new = scale_block(v, true);
+        store_codes((uint8_t *)t.m, e, end, m);
+        store_codes((uint8_t *)t.v, e, end, v);
+        __syncwarp();  // every lane has read the scales
+        if (lane == 0) t.m_scale[s] = m_new, t.v_scale[s] = v_new;
+    }
+}
+
+template <typename W, typename G, bool MASTER>
+__device__ __forceinline__ void step_any(const AdamWTensor &t, int64_t at, int64_t end, const Element &el)
+{
+    if (t.bits8)
+        step_chunk_8bit<W, G, MASTER>(t, at, end, el);
+    else
+        step_chunk<W, G, MASTER>(t, at, end, el);
+}
+
+template <typename W, bool MASTER>
+__device__ __forceinline__ void step_grad(const AdamWTensor &t, int64_t at, int64_t end, const Element &el)
+{
+    if (t.grad_f32)
+        step_any<W, float, MASTER>(t, at, end, el);
+    else
+        step_any<W, __nv_bfloat16, MASTER>(t, at, end, el);
+}
+
+// A factor that is no number leaves everything as it is.
+template <typename B>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ B b, const AdamWScalars sc)
+{
+    ptx::griddep_wait();
+    const uint32_t chunk = blockIdx.x;
+    const float factor = sc.grad_scale ? *sc.grad_scale : 1.0f;
+    if (!isfinite(factor)) return;
+    const float2 corrections = sc.corrections ? *sc.corrections : sc.host;
+    const int k = find_tensor(b, chunk);
+    const AdamWTensor &t = b.t[k];
+    const int64_t at = (int64_t)(chunk - b.first[k]) * kChunk;
+    const int64_t end = t.n < at + kChunk ? t.n : at + kChunk;
+    const float lr = (sc.lr_at ? *sc.lr_at : sc.lr) * t.lr_factor;
+    const Element el{sc.beta1, sc.one_minus1, sc.beta2, sc.one_minus2, factor, fmaf(-lr, t.weight_decay, 1.0f),
+                     lr * corrections.x, corrections.y, sc.eps};
+    if (t.master)
+        t.w_f32 ? step_grad<float, true>(t, at, end, el) : step_grad<__nv_bfloat16, true>(t, at, end, el);
+    else
+        t.w_f32 ? step_grad<float, false>(t, at, end, el) : step_grad<__nv_bfloat16, false>(t, at, end, el);
+}
+
+// The step's number from device memory: one more than it says, unless the
+// step is left out; with it the corrections 1 / (1 - b1^t) and
+// 1 / sqrt(1 - b2^t).
+__global__ void adamw_count_kernel(int32_t *step, const float *grad_scale, double beta1, double beta2, float2 *out)
+{
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    if (grad_scale && !isfinite(*grad_scale)) return;
+    const int32_t t = *step + 1;
+    *step = t;
+    *out = make_float2((float)(1.0 / (1.0 - pow(beta1, (double)t))), (float)(1.0 / sqrt(1.0 - pow(beta2, (double)t))));
+}
+
+// Calls f with batches of the tensors that have elements, in their order.
+template <typename B, typename Tensor, typename F>
+cudaError_t in_batches(const Tensor *tensors, int count, int cap, int64_t chunk_size, F f)
+{
+    B b;
+    b.count = 0;
+    b.first[0] = 0;
+    for (int i = 0; i < count; ++i) {
+        const int64_t chunks = ceil_div(tensors[i].n, chunk_size);
+        if (chunks == 0) continue;
+        if (b.count == cap) {
+            const cudaError_t e = f(b);
+            if (e != cudaSuccess) return e;
+            b.count = 0;
+        }
+        b.t[b.count] = tensors[i];
+        b.first[b.count + 1] = b.first[b.count] + (uint32_t)chunks;
+        ++b.count;
+    }
+    return b.count ? f(b) : cudaSuccess;
+}
+
+cudaLaunchConfig_t early(cudaLaunchAttribute *attr, cudaStream_t s)
+{
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.blockDim = dim3(kThreads);
+    return cfg;
+}
+
+}  // namespace
+
+// kNormBlocks sums for each launch of kNormBatch tensors.
+size_t grad_norm_workspace_bytes(int64_t count)
+{
+    const int64_t launches = count < 1 ? 1 : ceil_div(count, (int64_t)kNormBatch);
+    return (size_t)(launches * kNormBlocks) * sizeof(double2);
+}
+
+cudaError_t launch_grad_norm(const TensorRef *grads, int count, float max_norm, float *out, void *workspace, int n_sm,
+                             cudaStream_t s)
+{
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t cfg = early(&attr, s);
+    double2 *const partial = (double2 *)workspace;
+    int used = 0;
+    auto launch = [&](const auto &b) {
+        using B = std::remove_cv_t<std::remove_reference_t<decltype(b)>>;
+        const uint32_t chunks = b.first[b.count], most = (uint32_t)(n_sm * 8 < kNormBlocks ? n_sm * 8 : kNormBlocks);
+        cfg.gridDim = dim3(chunks < most ? chunks : most);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, grad_norm_kernel<B>, b, partial + used);
+        used += (int)cfg.gridDim.x;
+        return e;
+    };
+    const cudaError_t e = count <= kSmallBatch
+                              ? in_batches<NormBatchSmall>(grads, count, kSmallBatch, kNormChunk, launch)
+                              : in_batches<NormBatch>(grads, count, kNormBatch, kNormChunk, launch);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(1);
+    return cudaLaunchKernelEx(&cfg, norm_factor_kernel, (const double2 *)partial, used, max_norm, out);
+}
+
+cudaError_t launch_adamw(const AdamWTensor *tensors, int count, AdamWScalars sc, double beta1, double beta2,
+                         int32_t *step, void *workspace, cudaStream_t s)
+{
+    cudaLaunchAttribute attr;
+    cudaLaunchConfig_t cfg = early(&attr, s);
+    if (step) {
+        cfg.gridDim = cfg.blockDim = dim3(1);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, adamw_count_kernel, step, sc.grad_scale, beta1, beta2,
+                                                 (float2 *)workspace);
+        if (e != cudaSuccess) return e;
+        cfg.blockDim = dim3(kThreads);
+        sc.corrections = (const float2 *)workspace;
+    }
+    auto launch = [&](const auto &b) {
+        using B = std::remove_cv_t<std::remove_reference_t<decltype(b)>>;
+        cfg.gridDim = dim3(b.first[b.count]);
+        return cudaLaunchKernelEx(&cfg, adamw_kernel<B>, b, (const AdamWScalars)sc);
+    };
+    return count <= kSmallBatch ? in_batches<StepBatchSmall>(tensors, count, kSmallBatch, kChunk, launch)
+                                : in_batches<StepBatch>(tensors, count, kStepBatch, kChunk, launch);
+}
+
+}  // namespace moe

@@ -1,0 +1,647 @@
+// balance.cu -- the gate's load-balance loss with the experts' counts and
+// mean probabilities, and its gradient.
+//
+//   s = softmax(l), or sigmoid(l) / sum sigmoid(l); sequence i has n_i rows,
+//   N = sum n_i, c_ie of them chose e, P_ie = mean of s_te over them
+//   balance = sum_i n_i / N * E * sum_e c_ie / (k n_i) P_ie
+//   z = sum_t lse_t^2 / N;  loss = coef balance + z_coef z
+//   dl_te from balance: with a_e = coef E c_ie / (k n_i N),
+//     softmax s_e (a_e - sum a s), sigmoid (a_e - sum a s) q_e (1 - q_e) / sum q
+//   and from z: 2 z_coef / N lse_t softmax(l)_e
+//
+// A row lives in `lpr` lanes of a warp (32, fewer for up to 64 experts, whose
+// rows share a warp), PER logits to a lane.  A block has a run of rows and
+// goes through the sequences that meet it.  Per sequence its lanes add the
+// probabilities in registers, its warps meet in shared memory, and the sums
+// go to the slot (block + sequence): along the rows either the block or the
+// sequence grows, so no two pairs share a slot, and there are blocks +
+// sequences of them.  A second, small kernel adds the slots in order.  No
+// sum depends on the order in which blocks run.
+#include "common.cuh"
+#include "kernels.h"
+#include "sm100_ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kMostChunks = 1024;  // blocks of the first kernel
+constexpr int kCached = 1024;      // offsets that a block keeps in shared memory
+// up to this many rows and sequences run as one block, which adds nothing up
+// afterwards: one launch less
+constexpr int kOneBlockRows = 64;
+
+// Blocks per SM and rows of a warp in flight, by what the registers hold.
+template <int PER>
+struct RowShape {
+    static constexpr int BLOCKS = PER <= 4 ? 5 : PER <= 8 ? 4 : PER <= 16 ? 3 : 2;
+    static constexpr int ROWS = PER <= 4 ? 4 : PER <= 8 ? 2 : 1;
+};
+
+struct BalanceArgs {
+    const float *logits;
+    const int32_t *idx, *offsets;  // offsets nullable: one sequence of all rows
+    int T, S, E, k, lpr, chunk;    // chunk: rows per block
+    bool sigmoid;
+    float coef, z_coef;
+    float *loss, *prob;
+    int32_t *counts;
+    // per slot: [E] sums, [E] counts, one sum of lse^2
+    float *sums, *zs;
+    int32_t *cnts;
+    float2 *parts;  // [S][tiles]: the loss's two sums
+    unsigned *ticket;
+};
+
+struct BalanceGradArgs {
+    const float *logits, *dloss, *base;  // dloss, base nullable
+    const int32_t *counts, *offsets;
+    int T, S, E, k, lpr, chunk;
+    bool sigmoid;
+    float coef, z_coef;
+    float *out;  // may be base
+};
+
+__device__ __forceinline__ int clamp_row(int v, int T) { return min(max(v, 0), T); }
+
+// The offsets where the block's lanes read them: its shared memory if they
+// fit.  Ends with a barrier.
+__device__ __forceinline__ const int32_t *cache_offsets(const int32_t *offsets, int S, int T, int32_t *kept)
+{
+    if (!offsets) {
+        if (threadIdx.x == 0) kept[0] = 0, kept[1] = T;
+    } else if (S < kCached) {
+        for (int i = threadIdx.x; i <= S; i += kThreads) kept[i] = offsets[i];
+    }
+    __syncthreads();
+    return offsets && S >= kCached ? offsets : kept;
+}
+
+// How many of off[1..S] are at most `row`: the sequence of that row where it
+// has one.  A warp halves the range 32-fold per step.
+__device__ __forceinline__ int find_sequence(const int32_t *off, int S, int row)
+{
+    const int lane = threadIdx.x & 31;
+    int lo = 0, len = S;
+    while (len > 0) {
+        const int step = (len + 31) / 32;
+        const int at = min((lane + 1) * step, len);
+        const int c = __popc(__ballot_sync(0xffffffffu, off[lo + at] <= row)) * step;
+        lo += min(c, len);
+        len = max(min(step, len - c) - 1, 0);
+    }
+    return lo;
+}
+
+// Whether softmax's terms of a row of -inf, or a sigmoid row's, have a sum to
+// divide by.
+__device__ __forceinline__ float inverse_of(float total) { return total < 1.17549435e-38f ? 0.0f : 1.0f / total; }
+
+// The lane's logits of a row, -inf past the last expert and without a row.
+// VEC (E % 4 == 0): 16 bytes at a time, neighbouring lanes side by side.
+template <int PER, bool VEC>
+__device__ __forceinline__ int expert_of(int i, int sub, int lpr)
+{
+    return VEC ? (i / 4) * 4 * lpr + 4 * sub + i % 4 : i * lpr + sub;
+}
+
+template <int PER, bool VEC>
+__device__ __forceinline__ void load_row(const float *row, bool valid, int E, int sub, int lpr, float fill,
+                                         float (&l)[PER])
+{
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < PER; i += 4) {
+            const int e = expert_of<PER, VEC>(i, sub, lpr);
+            float4 v = make_float4(fill, fill, fill, fill);
+            if (valid && e < E) v = *reinterpret_cast<const float4 *>(row + e);
+            l[i] = v.x, l[i + 1] = v.y, l[i + 2] = v.z, l[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = expert_of<PER, VEC>(i, sub, lpr);
+            l[i] = valid && e < E ? row[e] : fill;
+        }
+    }
+}
+
+template <int PER, bool VEC>
+__device__ __forceinline__ void store_row(float *row, int E, int sub, int lpr, const float (&l)[PER])
+{
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < PER; i += 4) {
+            const int e = expert_of<PER, VEC>(i, sub, lpr);
+            if (e < E) *reinterpret_cast<float4 *>(row + e) = make_float4(l[i], l[i + 1], l[i + 2], l[i + 3]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = expert_of<PER, VEC>(i, sub, lpr);
+            if (e < E) row[e] = l[i];
+        }
+    }
+}
+
+// Sums (maxima) over the lanes of a row, for ROWS rows at once.
+template <int ROWS>
+__device__ __forceinline__ void row_sum(float (&v)[ROWS], int lpr)
+{
+    for (int o = lpr >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < ROWS; ++u) v[u] += __shfl_xor_sync(0xffffffffu, v[u], o);
+}
+
+template <int ROWS>
+__device__ __forceinline__ void row_max(float (&v)[ROWS], int lpr)
+{
+    for (int o = lpr >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < ROWS; ++u) v[u] = fmaxf(v[u], __shfl_xor_sync(0xffffffffu, v[u], o));
+}
+
+// exp(l - max l) of each row, with the sums and maxima.  A row of -inf gets
+// zeros; a NaN or +inf makes its row's sum NaN.
+template <int PER, int ROWS>
+__device__ __forceinline__ void exponentials(const float (&l)[ROWS][PER], int lpr, float (&e)[ROWS][PER],
+                                             float (&top)[ROWS], float (&total)[ROWS])
+{
+#pragma unroll
+    for (int u = 0; u < ROWS; ++u) {
+        top[u] = l[u][0];
+#pragma unroll
+        for (int i = 1; i < PER; ++i) top[u] = fmaxf(top[u], l[u][i]);
+    }
+    row_max(top, lpr);
+#pragma unroll
+    for (int u = 0; u < ROWS; ++u) {
+        if (top[u] == -INFINITY) top[u] = 0.0f;
+        total[u] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            e[u][i] = expf(l[u][i] - top[u]);
+            total[u] += e[u][i];
+        }
+    }
+    row_sum(total, lpr);
+}
+
+// 1 / (1 + exp(-l)) with the sums.  The reciprocal is the hardware's (one
+// unit in the last place), which gives zero below 2^-126.
+template <int PER, int ROWS>
+__device__ __forceinline__ void sigmoids(const float (&l)[ROWS][PER], int lpr, float (&q)[ROWS][PER],
+                                         float (&total)[ROWS])
+{
+#pragma unroll
+    for (int u = 0; u < ROWS; ++u) {
+        total[u] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            q[u][i] = __fdividef(1.0f, 1.0f + expf(-l[u][i]));
+            total[u] += q[u][i];
+        }
+    }
+    row_sum(total, lpr);
+}
+
+// log of the sum of exponentials; 0 for a row of -inf, which has none.
+__device__ __forceinline__ float lse_of(float top, float total) { return total == 0.0f ? 0.0f : top + logf(total); }
+
+// The distinct experts of the rows [lo, hi), one row per thread.
+__device__ __forceinline__ void count_rows(const int32_t *idx, int lo, int hi, int k, int E, int32_t *hist)
+{
+    for (int t = lo + (int)threadIdx.x; t < hi; t += kThreads) {
+        const int32_t *row = idx + (int64_t)t * k;
+        for (int j = 0; j < k; ++j) {
+            const int e = row[j];
+            bool fresh = e >= 0 && e < E;
+            for (int m = 0; m < j; ++m) fresh = fresh && row[m] != e;
+            if (fresh) atomicAdd(hist + e, 1);
+        }
+    }
+}
+
+// A sum over the block, the same for every thread, in an order fixed by the
+// threads alone.  `part`: a word per warp.
+__device__ __forceinline__ float sum_of_block(float v, float *part, int warps)
+{
+    v = warp_sum(v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float s = 0.0f;
+    for (int w = 0; w < warps; ++w) s += part[w];
+    return s;
+}
+
+template <int PER, bool VEC>
+__global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_kernel(const BalanceArgs a)
+{
+    constexpr int ROWS = RowShape<PER>::ROWS;
+    __shared__ float warp_sums[kWarps][32 * PER];
+    __shared__ int32_t hist[32 * PER];
+    __shared__ int32_t kept[kCached];
+    __shared__ float part[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int E = a.E, T = a.T, S = a.S;
+    const int lpr = PER > 4 ? 32 : a.lpr;
+    const int sub = lane & (lpr - 1), group = lane / lpr, rows_per_warp = 32 / lpr;
+    const bool alone = gridDim.x == 1;
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
+    if (!alone && blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
+    const int32_t *off = cache_offsets(a.offsets, S, T, kept);
+    float balance = 0.0f, z_total = 0.0f;  // alone: this thread's part of the two sums
+    if (alone) {
+        for (int i = threadIdx.x; i < S * E; i += kThreads) a.prob[i] = 0.0f, a.counts[i] = 0;
+        __syncthreads();
+    }
+    int row = blockIdx.x * a.chunk;
+    const int end = (int)min((int64_t)T, (int64_t)row + a.chunk);
+    while (row < end) {
+        const int i = find_sequence(off, S, row);
+        if (i >= S) break;  // rows behind the last sequence
+        const int lo = max(row, clamp_row(off[i], T)), hi = min(end, clamp_row(off[i + 1], T));
+        row = max(row + 1, hi);
+        if (lo >= hi) continue;
+        for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
+        __syncthreads();
+        count_rows(a.idx, lo, hi, a.k, E, hist);
+        float sum[PER], z = 0.0f;
+#pragma unroll
+        for (int q = 0; q < PER; ++q) sum[q] = 0.0f;
+        for (int at = lo + warp * rows_per_warp; at < hi; at += kWarps * rows_per_warp * ROWS) {
+            float l[ROWS][PER], p[ROWS][PER], top[ROWS], total[ROWS];
+#pragma unroll
+            for (int u = 0; u < ROWS; ++u) {
+                const int t = at + u * kWarps * rows_per_warp + group;
+                load_row<PER, VEC>(a.logits + (int64_t)t * E, t < hi, E, sub, lpr, -INFINITY, l[u]);
+            }
+            if (!a.sigmoid || a.z_coef != 0.0f) {
+                exponentials<PER, ROWS>(l, lpr, p, top, total);
+                if (a.z_coef != 0.0f) {
+#pragma unroll
+                    for (int u = 0; u < ROWS; ++u) {
+                        const float lse = lse_of(top[u], total[u]);
+                        if (sub == 0) z = fmaf(lse, lse, z);
+                    }
+                }
+            }
+            if (a.sigmoid) sigmoids<PER, ROWS>(l, lpr, p, total);
+#pragma unroll
+            for (int u = 0; u < ROWS; ++u) {
+                const float inv = inverse_of(total[u]);
+#pragma unroll
+                for (int q = 0; q < PER; ++q) sum[q] = fmaf(p[u][q], inv, sum[q]);
+            }
+        }
+        for (int o = lpr; o < 32; o <<= 1)
+#pragma unroll
+            for (int q = 0; q < PER; ++q) sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], o);
+        if (group == 0) {
+#pragma unroll
+            for (int q = 0; q < PER; ++q) {
+                const int e = expert_of<PER, VEC>(q, sub, lpr);
+                if (e < E) warp_sums[warp][e] = sum[q];
+            }
+        }
+        z = a.z_coef != 0.0f ? sum_of_block(z, part, kWarps) : 0.0f;
+        __syncthreads();
+        const int64_t slot = (int64_t)blockIdx.x + i;
+        const float inv_n = 1.0f / (float)(hi - lo);
+        for (int e = threadIdx.x; e < E; e += kThreads) {
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) s += warp_sums[w][e];
+            if (alone) {
+                s *= inv_n;
+                a.prob[i * E + e] = s;
+                a.counts[i * E + e] = hist[e];
+                balance = fmaf((float)hist[e], s, balance);
+            } else {
+                a.sums[slot * E + e] = s;
+                a.cnts[slot * E + e] = hist[e];
+            }
+        }
+        if (alone)
+            z_total += z;
+        else if (threadIdx.x == 0)
+            a.zs[slot] = z;
+        __syncthreads();  // the sums and counts are read before the next sequence's
+    }
+    if (alone) {
+        balance = sum_of_block(balance, part, kWarps);
+        if (threadIdx.x == 0) {
+            const int n = max(clamp_row(off[S], T) - clamp_row(off[0], T), 0);
+            balance = n ? balance * (float)E / ((float)a.k * (float)n) : 0.0f;
+            z_total = n ? z_total / (float)n : 0.0f;
+            a.loss[0] = a.coef * balance + a.z_coef * z_total;
+            a.loss[1] = balance;
+            a.loss[2] = z_total;
+        }
+    }
+}
+
+// The slots' sums: a block of 32 experts by blockDim.y for one sequence after
+// another; the block that ends last adds the loss's parts, in their order.
+__global__ void __launch_bounds__(1024) balance_sum_kernel(const BalanceArgs a)
+{
+    __shared__ float sums[32][33], part[32];
+    __shared__ int32_t cnts[32][33];
+    __shared__ bool last;
+    const int lane = threadIdx.x & 31, y = threadIdx.x >> 5, depth = blockDim.x >> 5;
+    const int T = a.T, S = a.S, E = a.E, e = blockIdx.x * 32 + lane;
+    ptx::griddep_wait();
+    auto offset = [&](int i) { return a.offsets ? clamp_row(a.offsets[i], T) : i ? T : 0; };
+    const float rows = (float)max(offset(S) - offset(0), 0);
+    for (int i = blockIdx.y; i < S; i += gridDim.y) {
+        const int lo = offset(i), hi = offset(i + 1), n = max(hi - lo, 0);
+        float s = 0.0f, z = 0.0f;
+        int32_t c = 0;
+        if (n > 0) {
+            const int first = lo / a.chunk, end = (hi - 1) / a.chunk;
+            if (e < E)
+                for (int b = first + y; b <= end; b += depth) {
+                    const int64_t slot = (int64_t)b + i;
+                    s += a.sums[slot * E + e];
+                    c += a.cnts[slot * E + e];
+                }
+            if (blockIdx.x == 0 && a.z_coef != 0.0f)
+                for (int b = first + (int)threadIdx.x; b <= end; b += blockDim.x) z += a.zs[(int64_t)b + i];
+        }
+        sums[y][lane] = s;
+        cnts[y][lane] = c;
+        if (blockIdx.x == 0 && a.z_coef != 0.0f)
+            z = sum_of_block(z, part, depth);  // has barriers
+        else
+            __syncthreads();
+        if (y == 0) {
+            s = 0.0f;
+            c = 0;
+            for (int w = 0; w < depth; ++w) s += sums[w][lane], c += cnts[w][lane];
+            s = n > 0 ? s / (float)n : 0.0f;
+            if (e < E) {
+                a.prob[(int64_t)i * E + e] = s;
+                a.counts[(int64_t)i * E + e] = c;
+            }
+            const float term = warp_sum((float)c * s);
+            if (lane == 0) a.parts[(int64_t)i * gridDim.x + blockIdx.x] = make_float2(term, z);
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        __threadfence();
+        last = atomicAdd(a.ticket, 1u) == gridDim.x * gridDim.y - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    float balance = 0.0f, z = 0.0f;
+    for (int64_t j = threadIdx.x; j < (int64_t)S * gridDim.x; j += blockDim.x) {
+        const float2 v = __ldcg(a.parts + j);
+        balance += v.x;
+        z += v.y;
+    }
+    balance = sum_of_block(balance, part, depth);
+    z = sum_of_block(z, part, depth);
+    if (threadIdx.x == 0) {
+        balance = rows > 0.0f ? balance * (float)E / ((float)a.k * rows) : 0.0f;
+        z = rows > 0.0f ? z / rows : 0.0f;
+        a.loss[0] = a.coef * balance + a.z_coef * z;
+        a.loss[1] = balance;
+        a.loss[2] = z;
+    }
+}
+
+// ---------------------------------------------------------------- gradient
+// The scores are computed again from the logits.  Rows of no sequence take
+// the gradient that comes in, or zero, whatever their logits hold.
+template <int PER, bool VEC>
+__global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_grad_kernel(const BalanceGradArgs a)
+{
+    constexpr int ROWS = RowShape<PER>::ROWS;
+    __shared__ int32_t kept[kCached];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int E = a.E, T = a.T, S = a.S;
+    const int lpr = PER > 4 ? 32 : a.lpr;
+    const int sub = lane & (lpr - 1), group = lane / lpr, rows_per_warp = 32 / lpr;
+    ptx::griddep_wait();
+    const int32_t *off = cache_offsets(a.offsets, S, T, kept);
+    const float up = a.dloss ? *a.dloss : 1.0f;
+    const float per_row = 1.0f / (float)max(clamp_row(off[S], T) - clamp_row(off[0], T), 1);
+    const float scale = up * a.coef * (float)E / (float)a.k * per_row;
+    const float z_scale = 2.0f * up * a.z_coef * per_row;
+    auto pass = [&](int from, int to) {  // rows of no sequence
+        for (int at = from + warp * rows_per_warp; at < to; at += kWarps * rows_per_warp) {
+            const int t = at + group;
+            if (t >= to) continue;
+            float v[PER];
+            load_row<PER, VEC>(a.base + (int64_t)t * E, a.base != nullptr, E, sub, lpr, 0.0f, v);
+            store_row<PER, VEC>(a.out + (int64_t)t * E, E, sub, lpr, v);
+        }
+    };
+    int row = blockIdx.x * a.chunk;
+    const int end = (int)min((int64_t)T, (int64_t)row + a.chunk);
+    while (row < end) {
+        const int i = find_sequence(off, S, row);
+        const int lo = i < S ? min(end, max(row, clamp_row(off[i], T))) : end;
+        const int hi = i < S ? max(lo, min(end, clamp_row(off[i + 1], T))) : end;
+        if (row < lo) pass(row, lo);
+        row = max(row + 1, hi);
+        if (lo >= hi) continue;
+        float share[PER];  // a_e of the sequence
+        const float inv_n = scale / (float)(clamp_row(off[i + 1], T) - clamp_row(off[i], T));
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+            const int e = expert_of<PER, VEC>(q, sub, lpr);
+            share[q] = e < E ? (float)a.counts[(int64_t)i * E + e] * inv_n : 0.0f;
+        }
+        for (int at = lo + warp * rows_per_warp; at < hi; at += kWarps * rows_per_warp * ROWS) {
+            float l[ROWS][PER], p[ROWS][PER], top[ROWS], total[ROWS], mean[ROWS], lse[ROWS];
+#pragma unroll
+            for (int u = 0; u < ROWS; ++u) {
+                const int t = at + u * kWarps * rows_per_warp + group;
+                load_row<PER, VEC>(a.logits + (int64_t)t * E, t < hi, E, sub, lpr, -INFINITY, l[u]);
+                lse[u] = 0.0f;
+            }
+            float d[ROWS][PER];
+            const bool soft = !a.sigmoid || a.z_coef != 0.0f;
+            if (soft) {
+                exponentials<PER, ROWS>(l, lpr, p, top, total);
+#pragma unroll
+                for (int u = 0; u < ROWS; ++u) {
+                    const float inv = inverse_of(total[u]);
+                    if (a.z_coef != 0.0f) lse[u] = z_scale * lse_of(top[u], total[u]);
+#pragma unroll
+                    for (int q = 0; q < PER; ++q) {
+                        p[u][q] *= inv;
+                        d[u][q] = lse[u] * p[u][q];
+                    }
+                }
+            }
+            if (a.sigmoid) {
+                sigmoids<PER, ROWS>(l, lpr, p, total);
+#pragma unroll
+                for (int u = 0; u < ROWS; ++u) {
+                    mean[u] = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < PER; ++q) mean[u] = fmaf(share[q], p[u][q], mean[u]);
+                }
+                row_sum(mean, lpr);
+#pragma unroll
+                for (int u = 0; u < ROWS; ++u) {
+                    const float inv = inverse_of(total[u]);
+                    mean[u] *= inv;
+#pragma unroll
+                    for (int q = 0; q < PER; ++q) {
+                        const float g = (share[q] - mean[u]) * inv * (p[u][q] * (1.0f - p[u][q]));
+                        d[u][q] = soft ? d[u][q] + g : g;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < ROWS; ++u) {
+                    mean[u] = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < PER; ++q) mean[u] = fmaf(share[q], p[u][q], mean[u]);
+                }
+                row_sum(mean, lpr);
+#pragma unroll
+                for (int u = 0; u < ROWS; ++u)
+#pragma unroll
+                    for (int q = 0; q < PER; ++q) d[u][q] = fmaf(p[u][q], share[q] - mean[u], d[u][q]);
+            }
+#pragma unroll
+            for (int u = 0; u < ROWS; ++u) {
+                const int t = at + u * kWarps * rows_per_warp + group;
+                if (t >= hi) continue;
+                if (a.base) {
+                    float b[PER];
+                    load_row<PER, VEC>(a.base + (int64_t)t * E, true, E, sub, lpr, 0.0f, b);
+#pragma unroll
+                    for (int q = 0; q < PER; ++q) d[u][q] += b[q];
+                }
+                store_row<PER, VEC>(a.out + (int64_t)t * E, E, sub, lpr, d[u]);
+            }
+        }
+    }
+}
+
+// Logits per lane and lanes per row.
+int lanes_per_row(int E)
+{
+    int lpr = 1;
+    while (lpr < 32 && 4 * lpr < E) lpr <<= 1;
+    return lpr;
+}
+
+template <bool VEC, typename F>
+cudaError_t with_row_vec(int E, F f)
+{
+    const int per = (E + 31) / 32;
+    if (per <= 4) return f(std::integral_constant<int, 4>(), std::integral_constant<bool, VEC>());
+    if (per <= 8) return f(std::integral_constant<int, 8>(), std::integral_constant<bool, VEC>());
+    if (per <= 12) return f(std::integral_constant<int, 12>(), std::integral_constant<bool, VEC>());
+    if (per <= 16) return f(std::integral_constant<int, 16>(), std::integral_constant<bool, VEC>());
+    if (per <= 24) return f(std::integral_constant<int, 24>(), std::integral_constant<bool, VEC>());
+    return f(std::integral_constant<int, 32>(), std::integral_constant<bool, VEC>());
+}
+
+template <typename F>
+cudaError_t with_row(int E, F f)
+{
+    return E % 4 == 0 ? with_row_vec<true>(E, f) : with_row_vec<false>(E, f);
+}
+
+int most_chunks(int64_t T)
+{
+    const int64_t c = ceil_div(T, kWarps);
+    return (int)(c < 1 ? 1 : c < kMostChunks ? c : kMostChunks);
+}
+
+// The workspace's parts, each on 256 bytes.
+struct Places {
+    size_t sums, cnts, zs, parts, bytes;
+};
+
+Places places(int64_t T, int64_t S, int64_t E)
+{
+    const int64_t slots = most_chunks(T) + S;
+    Places p;
+    p.sums = 256;  // the ticket before them
+    p.cnts = p.sums + round_up(slots * E * 4, 256);
+    p.zs = p.cnts + round_up(slots * E * 4, 256);
+    p.parts = p.zs + round_up(slots * 4, 256);
+    p.bytes = p.parts + round_up(S * ceil_div(E, 32) * 8, 256);
+    return p;
+}
+
+}  // namespace
+
+size_t balance_workspace_bytes(int64_t T, int64_t S, int64_t E) { return places(T, S, E).bytes; }
+
+cudaError_t launch_balance(const BalanceCall &c, void *workspace, int n_sm, cudaStream_t s)
+{
+    const Places p = places(c.T, c.S, c.E);
+    char *ws = (char *)workspace;
+    BalanceArgs a{c.logits, c.idx, c.offsets, (int)c.T, c.S, c.E, c.k, lanes_per_row(c.E), 0, c.sigmoid, c.coef,
+                  c.z_coef, c.loss, c.prob, c.counts, (float *)(ws + p.sums), (float *)(ws + p.zs),
+                  (int32_t *)(ws + p.cnts), (float2 *)(ws + p.parts), (unsigned *)ws};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const bool alone = c.T <= kOneBlockRows && c.S <= kOneBlockRows;
+    int blocks = 1;
+    cudaError_t e = with_row(c.E, [&](auto per, auto vec) {
+        constexpr int PER = decltype(per)::value;
+        constexpr bool VEC = decltype(vec)::value;
+        if (!alone) {
+            blocks = most_chunks(c.T);
+            if (blocks > n_sm * RowShape<PER>::BLOCKS) blocks = n_sm * RowShape<PER>::BLOCKS;
+            if (blocks < 2) blocks = 2;  // one is the block that ends the call by itself
+        }
+        a.chunk = (int)ceil_div(c.T, blocks);
+        if (a.chunk < 1) a.chunk = 1;
+        cfg.gridDim = dim3((unsigned)blocks);
+        cfg.blockDim = dim3(kThreads);
+        return cudaLaunchKernelEx(&cfg, balance_kernel<PER, VEC>, (const BalanceArgs)a);
+    });
+    if (e != cudaSuccess || alone) return e;
+    // as many warps per tile as a sequence has slots, about
+    int depth = 1;
+    while (depth < 32 && depth * c.S < blocks + c.S) depth <<= 1;
+    cfg.gridDim = dim3((unsigned)ceil_div(c.E, 32), (unsigned)(c.S < 32768 ? c.S : 32768));
+    cfg.blockDim = dim3(32 * depth);
+    return cudaLaunchKernelEx(&cfg, balance_sum_kernel, (const BalanceArgs)a);
+}
+
+cudaError_t launch_balance_grad(const BalanceGradCall &c, int n_sm, cudaStream_t s)
+{
+    BalanceGradArgs a{c.logits, c.dloss, c.base, c.counts, c.offsets, (int)c.T, c.S, c.E, c.k, lanes_per_row(c.E), 0,
+                      c.sigmoid, c.coef, c.z_coef, c.out};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cfg.blockDim = dim3(kThreads);
+    return with_row(c.E, [&](auto per, auto vec) {
+        constexpr int PER = decltype(per)::value;
+        constexpr bool VEC = decltype(vec)::value;
+        const int64_t rows = kWarps * (PER > 4 ? 1 : 32 / a.lpr), fit = ceil_div(c.T, rows);
+        const int64_t most = (int64_t)n_sm * RowShape<PER>::BLOCKS, blocks = fit < most ? fit : most;
+        a.chunk = (int)ceil_div(c.T, blocks);
+        cfg.gridDim = dim3((unsigned)blocks);
+        return cudaLaunchKernelEx(&cfg, balance_grad_kernel<PER, VEC>, (const BalanceGradArgs)a);
+    });
+}
+
+}  // namespace moe

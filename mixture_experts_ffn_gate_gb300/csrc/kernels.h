@@ -257,4 +257,58 @@ cudaError_t read_ortho_fault_word(uint32_t *flags, bool clear);
 size_t ortho_workspace_bytes(int64_t B, int64_t M, int64_t N);
 cudaError_t launch_orthogonalize(const OrthoCall &c, void *workspace, int pairs, cudaStream_t s);
 
+// balance.cu
+struct BalanceCall {
+    const float *logits;
+    const int32_t *idx, *offsets;  // offsets nullable
+    int64_t T;
+    int S, E, k;
+    bool sigmoid;
+    float coef, z_coef;
+    float *loss, *prob;
+    int32_t *counts;
+};
+struct BalanceGradCall {
+    const float *logits, *dloss, *base;  // dloss, base nullable
+    const int32_t *counts, *offsets;     // offsets nullable
+    int64_t T;
+    int S, E, k;
+    bool sigmoid;
+    float coef, z_coef;
+    float *out;
+};
+size_t balance_workspace_bytes(int64_t T, int64_t S, int64_t E);
+cudaError_t launch_balance(const BalanceCall &c, void *workspace, int n_sm, cudaStream_t s);
+cudaError_t launch_balance_grad(const BalanceGradCall &c, int n_sm, cudaStream_t s);
+
+// adamw.cu
+struct TensorRef {
+    const void *data;
+    int64_t n;
+    bool f32;  // else BF16
+};
+struct AdamWTensor {
+    void *w;
+    float *master;  // nullable
+    const void *grad;
+    void *m, *v;
+    float *m_scale, *v_scale;  // 8-bit states
+    int64_t n;
+    float lr_factor, weight_decay;
+    bool w_f32, grad_f32, bits8;
+};
+struct AdamWScalars {
+    float beta1, one_minus1, beta2, one_minus2, eps, lr;
+    float2 host;                // 1 / (1 - b1^t), 1 / sqrt(1 - b2^t)
+    const float2 *corrections;  // nullable: these, in device memory
+    const float *grad_scale, *lr_at;  // nullable
+};
+size_t grad_norm_workspace_bytes(int64_t count);
+cudaError_t launch_grad_norm(const TensorRef *grads, int count, float max_norm, float *out, void *workspace, int n_sm,
+                             cudaStream_t s);
+// step nullable: the number of steps so far, in device memory; with it the
+// workspace holds a float2
+cudaError_t launch_adamw(const AdamWTensor *tensors, int count, AdamWScalars sc, double beta1, double beta2,
+                         int32_t *step, void *workspace, cudaStream_t s);
+
 }  // namespace moe

@@ -2,6 +2,8 @@
 // points (moe_ffn_api.cu): argument checks and launches.  Host code only.
 #include <math.h>
 
+#include <vector>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "moe_block.h"
@@ -90,6 +92,66 @@ bool ortho_in_range(double a, double b, double c, int steps)
         top = 1.01 * most;
     }
     return true;
+}
+
+// The balance loss's limits: the gate's, and the sequences'.
+bool balance_shape(int64_t T, int64_t S, int64_t E)
+{
+    return T >= 0 && S >= 1 && E >= 1 && E <= 1024 && T < ((int64_t)1 << 30) && T <= ((int64_t)1 << 40) / E &&
+           S <= (1 << 20);
+}
+
+int check_balance(int64_t T, int64_t S, int64_t E, int64_t k, const int32_t *offsets, const moe_balance_opts *o)
+{
+    if (T < 0 || S < 1 || E < 1 || k < 1 || k > E || !o) return MOE_ERR_INVALID_ARG;
+    for (int32_t r : o->reserved)
+        if (r != 0) return MOE_ERR_INVALID_ARG;
+    if (o->score != MOE_SCORE_SOFTMAX && o->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+    if (!isfinite(o->coef) || !isfinite(o->z_coef)) return MOE_ERR_INVALID_ARG;
+    if (!offsets && S != 1) return MOE_ERR_INVALID_ARG;
+    if (!balance_shape(T, S, E) || k > 32 || T > ((int64_t)1 << 30) / k) return MOE_ERR_UNSUPPORTED_SHAPE;
+    return aligned16(offsets) ? MOE_OK : MOE_ERR_INVALID_ARG;
+}
+
+constexpr int64_t kMostTensors = 65536, kMostElements = (int64_t)1 << 42;
+
+// The running number of elements of a list of tensors.
+int add_elements(int64_t n, int64_t *total)
+{
+    if (n < 0) return MOE_ERR_INVALID_ARG;
+    if (n > kMostElements || (*total += n) > kMostElements) return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+bool misses(const void *p, uintptr_t mask) { return !p || ((uintptr_t)p & mask); }
+
+int check_adamw_tensor(const moe_adamw_tensor &t, moe::AdamWTensor *out)
+{
+    if (t.reserved != 0 || !is_type(t.w_type) || !is_type(t.grad_type)) return MOE_ERR_INVALID_ARG;
+    if (t.state_bits != 32 && t.state_bits != 8) return MOE_ERR_INVALID_ARG;
+    if (!isfinite(t.lr_factor) || !isfinite(t.weight_decay)) return MOE_ERR_INVALID_ARG;
+    const bool bits8 = t.state_bits == 8;
+    if (t.n > 0) {
+        if (misses(t.w, 15) || misses(t.grad, 15) || misses(t.m, 15) || misses(t.v, 15)) return MOE_ERR_INVALID_ARG;
+        if (t.master && !aligned16(t.master)) return MOE_ERR_INVALID_ARG;
+        if (bits8 && (misses(t.m_scale, 3) || misses(t.v_scale, 3))) return MOE_ERR_INVALID_ARG;
+    }
+    *out = moe::AdamWTensor{t.w,         t.master, t.grad,      t.m,
+                            t.v,         t.m_scale, t.v_scale,  t.n,
+                            t.lr_factor, t.weight_decay, t.w_type == MOE_F32, t.grad_type == MOE_F32,
+                            bits8};
+    return MOE_OK;
+}
+
+// A list of `count` elements; an empty one where there is no memory for it.
+template <typename T>
+std::vector<T> list_of(int64_t count)
+{
+    try {
+        return std::vector<T>((size_t)count);
+    } catch (...) {
+        return {};
+    }
 }
 
 }  // namespace
@@ -219,6 +281,126 @@ int moe_orthogonalize(const void *g, int g_type, int64_t B, int64_t M, int64_t N
     if (pairs < 1) return MOE_ERR_CUDA;
     const moe::OrthoCall call{g, g_type == MOE_F32, B, M, N, steps, a, b, c, eps, out_scale, out_bf16};
     return moe::launch_orthogonalize(call, workspace, pairs, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+size_t moe_balance_loss_workspace_bytes(int64_t T, int64_t S, int64_t E)
+{
+    return balance_shape(T, S, E) ? moe::balance_workspace_bytes(T, S, E) : 0;
+}
+
+int moe_balance_loss_forward(const float *logits_f32, const int32_t *topk_idx, const int32_t *seq_offsets, int64_t T,
+                             int64_t S, int64_t E, int64_t k, const moe_balance_opts *opts, float *loss_f32,
+                             int32_t *counts, float *prob_f32, void *workspace, size_t workspace_bytes,
+                             cudaStream_t stream)
+{
+    int st = check_balance(T, S, E, k, seq_offsets, opts);
+    if (st != MOE_OK) return st;
+    if (!loss_f32 || !counts || !prob_f32 || (T > 0 && (!logits_f32 || !topk_idx))) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(logits_f32) || !aligned16(topk_idx) || !aligned16(loss_f32) || !aligned16(counts) ||
+        !aligned16(prob_f32))
+        return MOE_ERR_INVALID_ARG;
+    if (!workspace || ((uintptr_t)workspace & 255)) return MOE_ERR_INVALID_ARG;
+    if (workspace_bytes < moe::balance_workspace_bytes(T, S, E)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    int n_sm, pairs;
+    st = moe::device_info(&n_sm, &pairs);
+    if (st != MOE_OK) return st;
+    const moe::BalanceCall c{logits_f32, topk_idx, seq_offsets, T, (int)S, (int)E, (int)k,
+                             opts->score == MOE_SCORE_SIGMOID, opts->coef, opts->z_coef, loss_f32, prob_f32, counts};
+    return moe::launch_balance(c, workspace, n_sm, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int moe_balance_loss_backward(const float *logits_f32, const int32_t *counts, const int32_t *seq_offsets, int64_t T,
+                              int64_t S, int64_t E, int64_t k, const moe_balance_opts *opts, const float *dloss_f32,
+                              const float *dlogits_in_f32, float *dlogits_f32, cudaStream_t stream)
+{
+    int st = check_balance(T, S, E, k, seq_offsets, opts);
+    if (st != MOE_OK) return st;
+    if (T == 0) return MOE_OK;
+    if (!logits_f32 || !counts || !dlogits_f32) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(logits_f32) || !aligned16(counts) || !aligned16(dlogits_in_f32) || !aligned16(dlogits_f32) ||
+        ((uintptr_t)dloss_f32 & 3))
+        return MOE_ERR_INVALID_ARG;
+    int n_sm, pairs;
+    st = moe::device_info(&n_sm, &pairs);
+    if (st != MOE_OK) return st;
+    const moe::BalanceGradCall c{logits_f32, dloss_f32, dlogits_in_f32, counts, seq_offsets, T, (int)S, (int)E, (int)k,
+                                 opts->score == MOE_SCORE_SIGMOID, opts->coef, opts->z_coef, dlogits_f32};
+    return moe::launch_balance_grad(c, n_sm, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+size_t moe_grad_norm_workspace_bytes(int64_t count)
+{
+    return count < 0 || count > kMostTensors ? 0 : moe::grad_norm_workspace_bytes(count);
+}
+
+int moe_grad_norm(const moe_tensor *grads, int64_t count, float max_norm, float *out_f32, void *workspace,
+                  size_t workspace_bytes, cudaStream_t stream)
+{
+    if (count < 0 || (count > 0 && !grads) || !(max_norm > 0.0f)) return MOE_ERR_INVALID_ARG;
+    if (count > kMostTensors) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (misses(out_f32, 3) || misses(workspace, 255)) return MOE_ERR_INVALID_ARG;
+    if (workspace_bytes < moe::grad_norm_workspace_bytes(count)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    auto refs = list_of<moe::TensorRef>(count);
+    if ((int64_t)refs.size() != count) return MOE_ERR_NO_MEMORY;
+    int64_t total = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        const moe_tensor &g = grads[i];
+        if (g.reserved != 0 || !is_type(g.type) || (g.n > 0 && misses(g.data, 15))) return MOE_ERR_INVALID_ARG;
+        const int st = add_elements(g.n, &total);
+        if (st != MOE_OK) return st;
+        refs[(size_t)i] = moe::TensorRef{g.data, g.n, g.type == MOE_F32};
+    }
+    int n_sm, pairs;
+    const int st = moe::device_info(&n_sm, &pairs);
+    if (st != MOE_OK) return st;
+    return moe::launch_grad_norm(refs.data(), (int)count, max_norm, out_f32, workspace, n_sm, stream) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+}
+
+int moe_adamw_step(const moe_adamw_tensor *tensors, int64_t count, const moe_adamw_opts *opts,
+                   const float *grad_scale_f32, const float *lr_f32, int32_t *step_i32, void *workspace,
+                   size_t workspace_bytes, cudaStream_t stream)
+{
+    if (count < 0 || (count > 0 && !tensors) || !opts) return MOE_ERR_INVALID_ARG;
+    if (count > kMostTensors) return MOE_ERR_UNSUPPORTED_SHAPE;
+    const moe_adamw_opts &o = *opts;
+    for (int64_t r : o.reserved)
+        if (r != 0) return MOE_ERR_INVALID_ARG;
+    // NaN fails these too
+    if (!(o.lr >= 0.0) || isinf((float)o.lr) || !(o.eps >= 0.0) || isinf((float)o.eps)) return MOE_ERR_INVALID_ARG;
+    if (!(o.beta1 >= 0.0 && o.beta1 < 1.0 && o.beta2 >= 0.0 && o.beta2 < 1.0)) return MOE_ERR_INVALID_ARG;
+    if (!step_i32 && o.step < 1) return MOE_ERR_INVALID_ARG;
+    if (((uintptr_t)grad_scale_f32 & 3) || ((uintptr_t)lr_f32 & 3) || ((uintptr_t)step_i32 & 3))
+        return MOE_ERR_INVALID_ARG;
+    if (step_i32 && misses(workspace, 255)) return MOE_ERR_INVALID_ARG;
+    if (step_i32 && workspace_bytes < 256) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    auto list = list_of<moe::AdamWTensor>(count);
+    if ((int64_t)list.size() != count) return MOE_ERR_NO_MEMORY;
+    int64_t total = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        int st = check_adamw_tensor(tensors[i], &list[(size_t)i]);
+        if (st == MOE_OK) st = add_elements(tensors[i].n, &total);
+        if (st != MOE_OK) return st;
+    }
+    int n_sm, pairs;
+    const int st = moe::device_info(&n_sm, &pairs);
+    if (st != MOE_OK) return st;
+    const double t = (double)o.step;
+    const moe::AdamWScalars sc{(float)o.beta1,
+                               (float)(1.0 - o.beta1),
+                               (float)o.beta2,
+                               (float)(1.0 - o.beta2),
+                               (float)o.eps,
+                               (float)o.lr,
+                               make_float2((float)(1.0 / (1.0 - pow(o.beta1, t))),
+                                           (float)(1.0 / sqrt(1.0 - pow(o.beta2, t)))),
+                               nullptr,
+                               grad_scale_f32,
+                               lr_f32};
+    return moe::launch_adamw(list.data(), (int)count, sc, o.beta1, o.beta2, step_i32, workspace, stream) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -1,6 +1,7 @@
 """ctypes binding of the block's operators in libmoeffn.so (C ABI in
 include/moe_block.h): norm, gate, the experts for a routing that is passed in,
-their gradients, and the orthogonalised update.
+their gradients, the load-balance loss, the gradients' norm, and the
+orthogonalised and AdamW updates.
 
 As in ``moe_ffn``: argument marshalling only, C names, torch tensors for
 device buffers, the stream defaults to torch's current stream, and no CPU
@@ -10,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 from typing import NamedTuple
 
 import torch
@@ -32,10 +34,35 @@ class moe_gate_opts(ctypes.Structure):
                 ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32 * 3)]
 
 
+class moe_balance_opts(ctypes.Structure):
+    """Mirror of ``struct moe_balance_opts``."""
+    _fields_ = [("score", ctypes.c_int32), ("coef", ctypes.c_float), ("z_coef", ctypes.c_float),
+                ("reserved", ctypes.c_int32 * 5)]
+
+
+class moe_tensor(ctypes.Structure):
+    """Mirror of ``struct moe_tensor``."""
+    _fields_ = [("data", ctypes.c_void_p), ("n", ctypes.c_int64), ("type", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class moe_adamw_tensor(ctypes.Structure):
+    """Mirror of ``struct moe_adamw_tensor``."""
+    _fields_ = ([(f, ctypes.c_void_p) for f in ("w", "master", "grad", "m", "v", "m_scale", "v_scale")]
+                + [("n", ctypes.c_int64)] + [(f, ctypes.c_int32) for f in ("w_type", "grad_type", "state_bits")]
+                + [("lr_factor", ctypes.c_float), ("weight_decay", ctypes.c_float), ("reserved", ctypes.c_int32)])
+
+
+class moe_adamw_opts(ctypes.Structure):
+    """Mirror of ``struct moe_adamw_opts``."""
+    _fields_ = ([(f, ctypes.c_double) for f in ("lr", "beta1", "beta2", "eps")]
+                + [("step", ctypes.c_int64), ("reserved", ctypes.c_int64 * 3)])
+
+
 def declare(L):
     """The argument types of moe_block.h's functions (``moe_ffn.lib`` calls it once)."""
     vp, i64, i32, f32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
-    opts, gate = ctypes.POINTER(_m.moe_ffn_opts), ctypes.POINTER(moe_gate_opts)
+    opts, gate, balance = (ctypes.POINTER(c) for c in (_m.moe_ffn_opts, moe_gate_opts, moe_balance_opts))
     for name, args in (
             ("moe_rms_norm_forward", [vp, i32, vp, i32, vp, f32, i64, i64, vp, vp, vp, vp, vp]),
             ("moe_rms_norm_backward", [vp, i32, vp, vp, i32, vp, f32, i64, i64, vp, vp, vp, sz, vp]),
@@ -44,12 +71,18 @@ def declare(L):
             ("moe_ffn_forward_routed", [vp] * 8 + [i64] * 5 + [vp, vp, sz, opts, vp]),
             ("moe_ffn_backward_routed", [vp] * 6 + [i64] * 5 + [vp] * 5 + [sz, i32, opts, vp]),
             ("moe_ffn_forward_routed_train", [vp] * 5 + [i64] * 5 + [vp, vp, sz, opts, vp]),
-            ("moe_orthogonalize", [vp, i32, i64, i64, i64, i32, f32, f32, f32, f32, f32, vp, vp, sz, vp])):
+            ("moe_orthogonalize", [vp, i32, i64, i64, i64, i32, f32, f32, f32, f32, f32, vp, vp, sz, vp]),
+            ("moe_balance_loss_forward", [vp] * 3 + [i64] * 4 + [balance, vp, vp, vp, vp, sz, vp]),
+            ("moe_balance_loss_backward", [vp] * 3 + [i64] * 4 + [balance, vp, vp, vp, vp]),
+            ("moe_grad_norm", [ctypes.POINTER(moe_tensor), i64, f32, vp, vp, sz, vp]),
+            ("moe_adamw_step", [ctypes.POINTER(moe_adamw_tensor), i64, ctypes.POINTER(moe_adamw_opts), vp, vp, vp, vp,
+                                sz, vp])):
         f = getattr(L, name)
         f.argtypes, f.restype = args, i32
     for name, n in (("moe_rms_norm_backward_workspace_bytes", 2), ("moe_ffn_routed_workspace_bytes", 5),
                     ("moe_ffn_routed_backward_workspace_bytes", 5),
-                    ("moe_orthogonalize_workspace_bytes", 3)):
+                    ("moe_orthogonalize_workspace_bytes", 3), ("moe_balance_loss_workspace_bytes", 3),
+                    ("moe_grad_norm_workspace_bytes", 1)):
         f = getattr(L, name)
         f.argtypes, f.restype = [i64] * n, sz
 
@@ -100,6 +133,12 @@ def _size(t, name="workspace"):
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
     return t.numel() * t.element_size()
+
+
+def _here(device):
+    """The current device is the tensors': the library runs on the current one."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
 
 
 # ------------------------------------------------------------------ norm
@@ -394,3 +433,293 @@ def moe_orthogonalize(g, steps: int = 5, coefficients=(3.4445, -4.7750, 2.0315),
     _check(_lib().moe_orthogonalize(p(g), gt, B, M, N, steps, a, b, c, eps, out_scale, p(out), p(workspace),
                                     _size(workspace), _stream(stream, g.device)), "moe_orthogonalize")
     return out
+
+
+# ------------------------------------------------------------------ load-balance loss
+class BalanceOutput(NamedTuple):
+    loss: torch.Tensor      # f32 [3]: coef * balance + z_coef * z, balance, z
+    counts: torch.Tensor    # int32 [S, E]: tokens of a sequence that chose an expert
+    prob: torch.Tensor      # f32 [S, E]: the sequence's mean probabilities
+
+
+def moe_balance_loss_workspace_bytes(T, S, E) -> int:
+    return int(_m.lib().moe_balance_loss_workspace_bytes(T, S, E))
+
+
+def new_balance_workspace(T, E, S=1, device="cuda", stream=None):
+    """For T tokens, E experts and S sequences."""
+    return _workspace(moe_balance_loss_workspace_bytes(T, S, E), device, stream, "workspace size")
+
+
+@functools.lru_cache(maxsize=64)
+def _balance_opts(score, coef, z_coef):
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    return ctypes.byref(moe_balance_opts(_SCORES[score], coef, z_coef))
+
+
+def _sequences(seq_offsets, device):
+    if seq_offsets is None:
+        return 1
+    if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
+        raise ValueError(f"seq_offsets must be [sequences + 1], got {tuple(seq_offsets.shape)}")
+    _is(seq_offsets, tuple(seq_offsets.shape), torch.int32, "seq_offsets")
+    _same_device(seq_offsets, device, "seq_offsets")
+    return seq_offsets.shape[0] - 1
+
+
+def _same_device(t, device, name):
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def moe_balance_loss_forward(logits, topk_idx, score: str = "softmax", coef: float = 1e-2, z_coef: float = 0.0,
+                             seq_offsets=None, loss=None, counts=None, prob=None, workspace=None,
+                             stream=None) -> BalanceOutput:
+    """The load-balance loss of logits f32 [T,E] for the gate's choice
+    topk_idx int32 [T,k], with each expert's count and mean probability:
+    balance = sum_i n_i / N * E * sum_e counts / (k n_i) * prob over the
+    sequences of seq_offsets (int32 [S+1], nullable: all tokens are one),
+    z = the mean of logsumexp(logits)^2."""
+    T, E = logits.shape
+    k = topk_idx.shape[1]
+    _is(logits, (T, E), torch.float32, "logits")
+    _is(topk_idx, (T, k), torch.int32, "topk_idx")
+    dev, empty = logits.device, torch.empty if stream is None else _empty_on(stream)
+    _here(dev)
+    _same_device(topk_idx, dev, "topk_idx")
+    S = _sequences(seq_offsets, dev)
+    if loss is None:
+        loss = empty((3,), dtype=torch.float32, device=dev)
+    else:
+        _is(loss, (3,), torch.float32, "loss")
+    if counts is None:
+        counts = empty((S, E), dtype=torch.int32, device=dev)
+    else:
+        _is(counts, (S, E), torch.int32, "counts")
+    if prob is None:
+        prob = empty((S, E), dtype=torch.float32, device=dev)
+    else:
+        _is(prob, (S, E), torch.float32, "prob")
+    if workspace is None:
+        workspace = new_balance_workspace(T, E, S, device=dev, stream=stream)
+    p = _ptr
+    _check(_lib().moe_balance_loss_forward(p(logits), p(topk_idx), p(seq_offsets), T, S, E, k,
+                                           _balance_opts(score, coef, z_coef), p(loss), p(counts), p(prob),
+                                           p(workspace), _size(workspace), _stream(stream, dev)),
+           "moe_balance_loss_forward")
+    return BalanceOutput(loss, counts, prob)
+
+
+def moe_balance_loss_backward(logits, counts, k: int, score: str = "softmax", coef: float = 1e-2, z_coef: float = 0.0,
+                              seq_offsets=None, dloss=None, dlogits_in=None, dlogits=None, stream=None):
+    """dlogits f32 [T,E] = dloss * d loss[0] / d logits + dlogits_in, for
+    the counts int32 [S,E] of moe_balance_loss_forward and the same score,
+    coefficients and sequences.  dloss f32 [1] (nullable: 1); dlogits_in f32
+    [T,E] (nullable), which ``dlogits`` may be itself."""
+    T, E = logits.shape
+    _is(logits, (T, E), torch.float32, "logits")
+    dev = logits.device
+    _here(dev)
+    S = _sequences(seq_offsets, dev)
+    _is(counts, (S, E), torch.int32, "counts")
+    _same_device(counts, dev, "counts")
+    if dloss is not None:
+        _is(dloss, (1,), torch.float32, "dloss")
+        _same_device(dloss, dev, "dloss")
+    if dlogits_in is not None:
+        _is(dlogits_in, (T, E), torch.float32, "dlogits_in")
+        _same_device(dlogits_in, dev, "dlogits_in")
+    if dlogits is None:
+        empty = torch.empty if stream is None else _empty_on(stream)
+        dlogits = empty((T, E), dtype=torch.float32, device=dev)
+    else:
+        _is(dlogits, (T, E), torch.float32, "dlogits")
+    p = _ptr
+    _check(_lib().moe_balance_loss_backward(p(logits), p(counts), p(seq_offsets), T, S, E, k,
+                                            _balance_opts(score, coef, z_coef), p(dloss), p(dlogits_in), p(dlogits),
+                                            _stream(stream, dev)), "moe_balance_loss_backward")
+    return dlogits
+
+
+# ------------------------------------------------------------------ clipping and AdamW
+STATE_BLOCK = 256   # elements that share a scale of an 8-bit state
+
+
+def _all_on(tensors, what):
+    """The one device of a list's tensors, None of an empty one."""
+    devices = {t.device for t in tensors}
+    if len(devices) > 1:
+        raise ValueError(f"{what} are on several devices: {sorted(map(str, devices))}")
+    return devices.pop() if devices else None
+
+
+class GradList:
+    """The gradients of a step, bf16 or f32, as moe_grad_norm takes them: made
+    once for tensors that stay where they are."""
+
+    def __init__(self, grads):
+        self.grads = list(grads)
+        for i, g in enumerate(self.grads):
+            _is(g, tuple(g.shape), g.dtype, f"grads[{i}]")
+        self.device = _all_on(self.grads, "grads")
+        self.array = (moe_tensor * len(self.grads))(
+            *(moe_tensor(g.data_ptr(), g.numel(), _type(g, "a gradient")) for g in self.grads))
+
+
+def moe_grad_norm_workspace_bytes(count) -> int:
+    return int(_m.lib().moe_grad_norm_workspace_bytes(count))
+
+
+def new_grad_norm_workspace(count, device="cuda", stream=None):
+    """For ``count`` gradients."""
+    return _workspace(moe_grad_norm_workspace_bytes(count), device, stream, "workspace size")
+
+
+def moe_grad_norm(grads, max_norm: float = math.inf, out=None, workspace=None, stream=None):
+    """f32 [2]: the norm of all gradients together, and the factor that clips
+    it to max_norm (1 where it is not above; NaN where the norm is no finite
+    number).  ``grads``: a list of tensors, a GradList or an AdamWPlan."""
+    if isinstance(grads, AdamWPlan):
+        grads = grads.grad_list()
+    elif not isinstance(grads, GradList):
+        grads = GradList(grads)
+    n, dev = len(grads.grads), grads.device
+    if dev is None:
+        dev = torch.device("cuda", torch.cuda.current_device()) if out is None else out.device
+    _here(dev)
+    if out is None:
+        out = (torch.empty if stream is None else _empty_on(stream))((2,), dtype=torch.float32, device=dev)
+    else:
+        _is(out, (2,), torch.float32, "out")
+        _same_device(out, dev, "out")
+    if workspace is None:
+        workspace = new_grad_norm_workspace(n, device=dev, stream=stream)
+    _check(_lib().moe_grad_norm(grads.array, n, max_norm, out.data_ptr(), workspace.data_ptr(), _size(workspace),
+                                _stream(stream, dev)), "moe_grad_norm")
+    return out
+
+
+class AdamWState(NamedTuple):
+    """The moments of a weight: f32 tensors of its shape; or E4M3 tensors
+    (torch.float8_e4m3fn) with f32 scales [ceil(elements / STATE_BLOCK)], of
+    which v's stand for sqrt(v)."""
+    m: torch.Tensor
+    v: torch.Tensor
+    m_scale: torch.Tensor | None = None
+    v_scale: torch.Tensor | None = None
+
+
+def new_adamw_state(weight, bits: int = 32) -> AdamWState:
+    """The state of a weight before its first step, in 32 or in 8 bits."""
+    if bits not in (8, 32):
+        raise ValueError(f"bits must be 8 or 32, got {bits}")
+    shape, dev = tuple(weight.shape), weight.device
+    if bits == 32:
+        return AdamWState(*(torch.zeros(shape, dtype=torch.float32, device=dev) for _ in range(2)))
+    blocks = -(-weight.numel() // STATE_BLOCK)
+    return AdamWState(*(torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn) for _ in range(2)),
+                      *(torch.zeros(blocks, dtype=torch.float32, device=dev) for _ in range(2)))
+
+
+class AdamWPlan:
+    """The tensors of an AdamW step, checked once: weights (bf16 or f32,
+    updated in place), their states, FP32 masters (nullable, per weight) of
+    which the weights are the rounding, and each weight's weight_decay and
+    lr_factor (one number or a list).  Gradients (bf16 or f32, the weights'
+    shapes) are given here or by set_grads; a captured step reads the ones
+    that it was captured with."""
+
+    def __init__(self, weights, states, masters=None, weight_decay=0.0, lr_factor=1.0, grads=None):
+        self.weights, self.states = list(weights), [AdamWState(*s) for s in states]
+        n = len(self.weights)
+        self.masters = [None] * n if masters is None else list(masters)
+        decay, factor = ([x] * n if isinstance(x, (int, float)) else list(x) for x in (weight_decay, lr_factor))
+        for name, x in (("states", self.states), ("masters", self.masters), ("weight_decay", decay),
+                        ("lr_factor", factor)):
+            if len(x) != n:
+                raise ValueError(f"{name}: {len(x)} for {n} weights")
+        self.array = (moe_adamw_tensor * n)()
+        written = []
+        for i, (w, s, master) in enumerate(zip(self.weights, self.states, self.masters)):
+            shape = tuple(w.shape)
+            _is(w, shape, w.dtype, f"weights[{i}]")
+            bits8 = s.m_scale is not None or s.v_scale is not None
+            kind = torch.float8_e4m3fn if bits8 else torch.float32
+            blocks = (-(-w.numel() // STATE_BLOCK),)
+            parts = [("m", s.m, shape, kind), ("v", s.v, shape, kind)]
+            if bits8:
+                if s.m_scale is None or s.v_scale is None:
+                    raise ValueError(f"states[{i}]: m_scale and v_scale go together")
+                parts += [("m_scale", s.m_scale, blocks, torch.float32), ("v_scale", s.v_scale, blocks, torch.float32)]
+            if master is not None:
+                parts.append(("master", master, shape, torch.float32))
+            d = self.array[i]
+            for name, t, size, dtype in parts:
+                _is(t, size, dtype, f"{name} of weights[{i}]")
+                setattr(d, name, t.data_ptr())
+            d.w, d.n, d.w_type, d.state_bits = w.data_ptr(), w.numel(), _type(w, f"weights[{i}]"), 8 if bits8 else 32
+            d.weight_decay, d.lr_factor = decay[i], factor[i]
+            written += [w] + [t for _, t, _, _ in parts]
+        self.device = _all_on(written, "weights and states")
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in written if t.numel())
+        if any(b[0] < a[1] for a, b in zip(spans, spans[1:])):
+            raise ValueError("weights, masters and states must not overlap: each is updated once")
+        self.grads = self._grad_list = None
+        if grads is not None:
+            self.set_grads(grads)
+
+    def set_grads(self, grads):
+        """The gradients of the steps from here on."""
+        grads = list(grads)
+        if len(grads) != len(self.weights):
+            raise ValueError(f"grads: {len(grads)} for {len(self.weights)} weights")
+        for i, (g, w) in enumerate(zip(grads, self.weights)):
+            _is(g, tuple(w.shape), g.dtype, f"grads[{i}]")
+            _type(g, f"grads[{i}]")
+            _same_device(g, self.device, f"grads[{i}]")
+        for d, g in zip(self.array, grads):
+            d.grad, d.grad_type = g.data_ptr(), _TYPES[g.dtype]
+        self.grads, self._grad_list = grads, None
+
+    def grad_list(self) -> GradList:
+        if self.grads is None:
+            raise ValueError("the plan has no gradients yet")
+        if self._grad_list is None:
+            self._grad_list = GradList(self.grads)
+        return self._grad_list
+
+
+def moe_adamw_step(plan: AdamWPlan, step, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, grad_scale=None,
+                   workspace=None, stream=None) -> None:
+    """One AdamW step of the plan's weights, in place.  ``step``: its number,
+    from 1; or an int32 CUDA tensor [1] with the steps taken so far, to which
+    the call adds one.  ``lr``: a number or an f32 CUDA tensor [1].
+    ``grad_scale`` f32 [1] (nullable; moe_grad_norm's [1:]): the gradients'
+    factor; where it is NaN or infinite nothing changes.  With tensors for
+    step and lr a captured step's replays go on counting."""
+    if plan.grads is None and plan.weights:
+        raise ValueError("the plan has no gradients yet")
+    dev = plan.device
+    if dev is None:
+        return
+    _here(dev)
+    counter = lr_at = None
+    if isinstance(step, torch.Tensor):
+        _is(step, (1,), torch.int32, "step")
+        counter, step = step, 0
+    if isinstance(lr, torch.Tensor):
+        _is(lr, (1,), torch.float32, "lr")
+        lr_at, lr = lr, 0.0
+    if grad_scale is not None:
+        _is(grad_scale, (1,), torch.float32, "grad_scale")
+    for name, t in (("step", counter), ("lr", lr_at), ("grad_scale", grad_scale)):
+        if t is not None:
+            _same_device(t, dev, name)
+    if counter is not None and workspace is None:
+        workspace = _workspace(256, dev, stream, "workspace size")
+    o = moe_adamw_opts(lr, betas[0], betas[1], eps, step)
+    p = _ptr
+    _check(_lib().moe_adamw_step(plan.array, len(plan.weights), ctypes.byref(o), p(grad_scale), p(lr_at), p(counter),
+                                 p(workspace), 0 if workspace is None else _size(workspace), _stream(stream, dev)),
+           "moe_adamw_step")
