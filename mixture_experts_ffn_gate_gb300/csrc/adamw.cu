@@ -21,6 +21,8 @@
 // the lowest code, so that no m is divided by eps alone.
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "sm100_ptx.cuh"
@@ -35,7 +37,8 @@ constexpr int kNormBatch = 512;   // 14 KB
 constexpr int kThreads = 256;
 constexpr int kBlock8 = 256;        // elements that share a scale: eight to a lane
 constexpr int kChunk = 4096;        // elements of a block of the step
-constexpr int kNormChunk = 16384;   // elements that a block of the norm takes at a time
+constexpr int kNormChunk = 4096;    // elements that a block of the norm takes at a time
+constexpr int kNormPerSm = 6;       // its blocks that an SM holds
 constexpr int kNormBlocks = 1024;   // its partial sums per launch, at most
 constexpr float kTop = 448.0f;      // the largest E4M3 value
 constexpr float kLowest = 0.001953125f;  // the smallest, 2^-9
@@ -65,46 +68,73 @@ __device__ __forceinline__ int find_tensor(const B &b, uint32_t chunk)
 }
 
 // ---------------------------------------------------------------- elements
-// N consecutive elements from `e` on, FP32 or BF16, zero from n on.
-template <int N>
-__device__ __forceinline__ void load_n(const float *p, int64_t e, int64_t n, float (&v)[N])
-{
-    if (e + N <= n) {
-#pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const float4 q = *reinterpret_cast<const float4 *>(p + e + i);
-            v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = e + i < n ? p[e + i] : 0.0f;
-    }
-}
+// N consecutive elements from `e` on as they are kept, FP32 or BF16, zero
+// from n on; FULL: there are N.
+template <typename T, int N>
+struct Raw;
 
 template <int N>
-__device__ __forceinline__ void load_n(const __nv_bfloat16 *p, int64_t e, int64_t n, float (&v)[N])
-{
-    if (e + N <= n) {
-        uint32_t w[N / 2];
-        if constexpr (N == 8) {
-            const uint4 q = *reinterpret_cast<const uint4 *>(p + e);
-            w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+struct Raw<float, N> {
+    float4 q[N / 4];
+
+    template <bool FULL>
+    __device__ __forceinline__ void load(const float *p, int e, int n)
+    {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            if (FULL || e + N <= n) {
+                q[i] = *reinterpret_cast<const float4 *>(p + e + 4 * i);
+            } else {
+                const int at = e + 4 * i;
+                q[i].x = at < n ? p[at] : 0.0f;
+                q[i].y = at + 1 < n ? p[at + 1] : 0.0f;
+                q[i].z = at + 2 < n ? p[at + 2] : 0.0f;
+                q[i].w = at + 3 < n ? p[at + 3] : 0.0f;
+            }
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[N]) const
+    {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) v[4 * i] = q[i].x, v[4 * i + 1] = q[i].y, v[4 * i + 2] = q[i].z, v[4 * i + 3] = q[i].w;
+    }
+};
+
+template <int N>
+struct Raw<__nv_bfloat16, N> {
+    uint32_t q[N / 2];
+
+    template <bool FULL>
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, int e, int n)
+    {
+        if (FULL || e + N <= n) {
+            if constexpr (N == 8) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(p + e);
+                q[0] = x.x, q[1] = x.y, q[2] = x.z, q[3] = x.w;
+            } else {
+                const uint2 x = *reinterpret_cast<const uint2 *>(p + e);
+                q[0] = x.x, q[1] = x.y;
+            }
         } else {
-            const uint2 q = *reinterpret_cast<const uint2 *>(p + e);
-            w[0] = q.x, w[1] = q.y;
+            const uint16_t *const bits = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                const int at = e + 2 * i;
+                q[i] = (at < n ? bits[at] : 0u) | (at + 1 < n ? (uint32_t)bits[at + 1] << 16 : 0u);
+            }
         }
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) v[2 * i] = bf16lo(w[i]), v[2 * i + 1] = bf16hi(w[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = e + i < n ? __bfloat162float(p[e + i]) : 0.0f;
     }
-}
+    __device__ __forceinline__ void get(float (&v)[N]) const
+    {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) v[2 * i] = bf16lo(q[i]), v[2 * i + 1] = bf16hi(q[i]);
+    }
+};
 
-template <int N>
-__device__ __forceinline__ void store_n(float *p, int64_t e, int64_t n, const float (&v)[N])
+template <int N, bool FULL>
+__device__ __forceinline__ void store_n(float *p, int e, int n, const float (&v)[N])
 {
-    if (e + N <= n) {
+    if (FULL || e + N <= n) {
 #pragma unroll
         for (int i = 0; i < N; i += 4)
             *reinterpret_cast<float4 *>(p + e + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
@@ -115,10 +145,10 @@ __device__ __forceinline__ void store_n(float *p, int64_t e, int64_t n, const fl
     }
 }
 
-template <int N>
-__device__ __forceinline__ void store_n(__nv_bfloat16 *p, int64_t e, int64_t n, const float (&v)[N])
+template <int N, bool FULL>
+__device__ __forceinline__ void store_n(__nv_bfloat16 *p, int e, int n, const float (&v)[N])
 {
-    if (e + N <= n) {
+    if (FULL || e + N <= n) {
         uint32_t w[N / 2];
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
@@ -136,17 +166,23 @@ __device__ __forceinline__ void store_n(__nv_bfloat16 *p, int64_t e, int64_t n, 
     }
 }
 
-// Eight E4M3 codes from `e` on, as values without their scale.
-__device__ __forceinline__ void load_codes(const uint8_t *p, int64_t e, int64_t n, float (&v)[8])
+// Eight E4M3 codes from `e` on, and their values without a scale.
+template <bool FULL>
+__device__ __forceinline__ uint2 load_codes(const uint8_t *p, int e, int n)
 {
     uint2 w = make_uint2(0u, 0u);
-    if (e + 8 <= n) {
+    if (FULL || e + 8 <= n) {
         w = *reinterpret_cast<const uint2 *>(p + e);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (e + i < n) (i < 4 ? w.x : w.y) |= (uint32_t)p[e + i] << (8 * (i & 3));
     }
+    return w;
+}
+
+__device__ __forceinline__ void unpack_codes(const uint2 &w, float (&v)[8])
+{
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t two = ((i < 2 ? w.x : w.y) >> (16 * (i & 1))) & 0xffffu;
@@ -155,7 +191,8 @@ __device__ __forceinline__ void load_codes(const uint8_t *p, int64_t e, int64_t 
     }
 }
 
-__device__ __forceinline__ void store_codes(uint8_t *p, int64_t e, int64_t n, const float (&v)[8])
+template <bool FULL>
+__device__ __forceinline__ void store_codes(uint8_t *p, int e, int n, const float (&v)[8])
 {
     uint2 w = make_uint2(0u, 0u);
 #pragma unroll
@@ -163,7 +200,7 @@ __device__ __forceinline__ void store_codes(uint8_t *p, int64_t e, int64_t n, co
         const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
         (i < 2 ? w.x : w.y) |= two << (16 * (i & 1));
     }
-    if (e + 8 <= n) {
+    if (FULL || e + 8 <= n) {
         *reinterpret_cast<uint2 *>(p + e) = w;
     } else {
 #pragma unroll
@@ -179,7 +216,7 @@ using NormBatchSmall = Batch<TensorRef, kSmallBatch>;
 // A block's sums of squares of its chunks: of the elements and of the
 // elements times 2^-64, which holds where the first one is beyond FP32.
 template <typename B>
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ B b, double2 *partial)
+__global__ void __launch_bounds__(kThreads, kNormPerSm) grad_norm_kernel(const __grid_constant__ B b, double2 *partial)
 {
     __shared__ double part[2][kThreads / 32];
     ptx::griddep_launch_dependents();
@@ -193,25 +230,33 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
             r[i] = fmaf(small, small, r[i]);
         }
     };
+    auto pass = [&](auto *p, int n, auto full) {
+        constexpr bool FULL = decltype(full)::value;
+        constexpr int FLIGHT = kNormChunk / (kThreads * 4);
+        Raw<std::remove_const_t<std::remove_pointer_t<decltype(p)>>, 4> raw[FLIGHT];
+#pragma unroll
+        for (int u = 0; u < FLIGHT; ++u) raw[u].template load<FULL>(p, (u * kThreads + threadIdx.x) * 4, n);
+#pragma unroll
+        for (int u = 0; u < FLIGHT; ++u) {
+            float v[4];
+            raw[u].get(v);
+            add(v);
+        }
+    };
+    auto run = [&](const auto *p, int64_t left) {
+        if (left >= kNormChunk)
+            pass(p, kNormChunk, std::true_type());
+        else
+            pass(p, (int)left, std::false_type());
+    };
     const uint32_t chunks = b.first[b.count];
     for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
         const int k = find_tensor(b, c);
-        const int64_t n = b.t[k].n, at = (int64_t)(c - b.first[k]) * kNormChunk;
-        const int64_t end = n < at + kNormChunk ? n : at + kNormChunk;
-        constexpr int FLIGHT = 4;
-        auto run = [&](const auto *p) {
-            for (int64_t e = at + threadIdx.x * 4; e < end; e += kThreads * 4 * FLIGHT) {
-                float v[FLIGHT][4];
-#pragma unroll
-                for (int u = 0; u < FLIGHT; ++u) load_n<4>(p, e + u * kThreads * 4, end, v[u]);
-#pragma unroll
-                for (int u = 0; u < FLIGHT; ++u) add(v[u]);
-            }
-        };
+        const int64_t at = (int64_t)(c - b.first[k]) * kNormChunk, left = b.t[k].n - at;
         if (b.t[k].f32)
-            run((const float *)b.t[k].data);
+            run((const float *)b.t[k].data + at, left);
         else
-            run((const __nv_bfloat16 *)b.t[k].data);
+            run((const __nv_bfloat16 *)b.t[k].data + at, left);
     }
     double x = (double)((s[0] + s[1]) + (s[2] + s[3])), y = (double)((r[0] + r[1]) + (r[2] + r[3]));
 #pragma unroll
@@ -275,40 +320,56 @@ struct Element {
     }
 };
 
-template <typename W, bool MASTER>
-__device__ __forceinline__ const auto *source(const AdamWTensor &t)
+// A chunk of a tensor: n elements from each address on.
+template <typename W, typename G>
+struct Chunk {
+    W *w;
+    float *master;
+    const G *grad;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    int n;
+};
+
+template <bool MASTER, typename W, typename G>
+__device__ __forceinline__ const auto *source(const Chunk<W, G> &c)
 {
     if constexpr (MASTER)
-        return (const float *)t.master;
+        return (const float *)c.master;
     else
-        return (const W *)t.w;
+        return (const W *)c.w;
 }
 
 // FP32 states: four elements per thread at a time.
-template <typename W, typename G, bool MASTER>
-__device__ __forceinline__ void step_chunk(const AdamWTensor &t, int64_t at, int64_t end, const Element &el)
+template <bool MASTER, bool FULL, typename W, typename G>
+__device__ __forceinline__ void step_chunk(const Chunk<W, G> &c, const Element &el)
 {
     constexpr int FLIGHT = 2;
-    float *const ms = (float *)t.m, *const vs = (float *)t.v;
-    for (int64_t e = at + threadIdx.x * 4; e < end; e += kThreads * 4 * FLIGHT) {
-        float g[FLIGHT][4], m[FLIGHT][4], v[FLIGHT][4], w[FLIGHT][4];
+    float *const ms = (float *)c.m, *const vs = (float *)c.v;
+    const int n = FULL ? kChunk : c.n;
+    for (int e = threadIdx.x * 4; e < n; e += kThreads * 4 * FLIGHT) {
+        Raw<G, 4> rg[FLIGHT];
+        Raw<std::remove_const_t<std::remove_pointer_t<decltype(source<MASTER>(c))>>, 4> rw[FLIGHT];
+        Raw<float, 4> rm[FLIGHT], rv[FLIGHT];
 #pragma unroll
         for (int u = 0; u < FLIGHT; ++u) {
-            const int64_t i = e + u * kThreads * 4;
-            load_n<4>((const G *)t.grad, i, end, g[u]);
-            load_n<4>(ms, i, end, m[u]);
-            load_n<4>(vs, i, end, v[u]);
-            load_n<4>(source<W, MASTER>(t), i, end, w[u]);
+            const int i = e + u * kThreads * 4;
+            rg[u].template load<FULL>(c.grad, i, n);
+            rm[u].template load<FULL>(ms, i, n);
+            rv[u].template load<FULL>(vs, i, n);
+            rw[u].template load<FULL>(source<MASTER>(c), i, n);
         }
 #pragma unroll
         for (int u = 0; u < FLIGHT; ++u) {
-            const int64_t i = e + u * kThreads * 4;
+            const int i = e + u * kThreads * 4;
+            float g[4], m[4], v[4], w[4];
+            rg[u].get(g), rm[u].get(m), rv[u].get(v), rw[u].get(w);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) el(g[u][q], m[u][q], v[u][q], w[u][q]);
-            store_n<4>(ms, i, end, m[u]);
-            store_n<4>(vs, i, end, v[u]);
-            if (MASTER) store_n<4>((float *)t.master, i, end, w[u]);
-            store_n<4>((W *)t.w, i, end, w[u]);
+            for (int q = 0; q < 4; ++q) el(g[q], m[q], v[q], w[q]);
+            store_n<4, FULL>(ms, i, n, m);
+            store_n<4, FULL>(vs, i, n, v);
+            if (MASTER) store_n<4, FULL>(c.master, i, n, w);
+            store_n<4, FULL>(c.w, i, n, w);
         }
     }
 }
@@ -335,18 +396,38 @@ __device__ __forceinline__ float scale_block(float (&x)[8], bool up)
 }
 
 // 8-bit states: a warp takes 256 elements, a scale's block, eight to a lane.
-template <typename W, typename G, bool MASTER>
-__device__ __forceinline__ void step_chunk_8bit(const AdamWTensor &t, int64_t at, int64_t end, const Element &el)
+template <bool MASTER, bool FULL, typename W, typename G>
+__device__ __forceinline__ void step_chunk_8bit(const Chunk<W, G> &c, const Element &el)
 {
-    const int lane = threadIdx.x & 31;
-    for (int64_t block = at + (threadIdx.x >> 5) * kBlock8; block < end; block += kThreads / 32 * kBlock8) {
-        const int64_t e = block + lane * 8, s = block / kBlock8;
+    const int lane = threadIdx.x & 31, n = FULL ? kChunk : c.n;
+    uint8_t *const ms = (uint8_t *)c.m, *const vs = (uint8_t *)c.v;
+    constexpr int WARPS = kThreads / 32, FLIGHT = kChunk / kBlock8 / WARPS;
+    // all that the warp reads of the chunk, as it is kept
+    Raw<G, 8> rg[FLIGHT];
+    Raw<std::remove_const_t<std::remove_pointer_t<decltype(source<MASTER>(c))>>, 8> rw[FLIGHT];
+    uint2 rm[FLIGHT], rv[FLIGHT];
+    float m_scales[FLIGHT], v_scales[FLIGHT];
+#pragma unroll
+    for (int u = 0; u < FLIGHT; ++u) {
+        const int s = (threadIdx.x >> 5) + u * WARPS, e = s * kBlock8 + lane * 8;
+        rg[u].template load<FULL>(c.grad, e, n);
+        rm[u] = load_codes<FULL>(ms, e, n);
+        rv[u] = load_codes<FULL>(vs, e, n);
+        rw[u].template load<FULL>(source<MASTER>(c), e, n);
+        const bool in = FULL || s * kBlock8 < n;
+        m_scales[u] = in ? c.m_scale[s] : 0.0f;
+        v_scales[u] = in ? c.v_scale[s] : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < FLIGHT; ++u) {
+        const int s = (threadIdx.x >> 5) + u * WARPS, e = s * kBlock8 + lane * 8;
+        if (!FULL && s * kBlock8 >= n) break;
         float g[8], m[8], v[8], w[8];
-        load_n<8>((const G *)t.grad, e, end, g);
-        load_codes((const uint8_t *)t.m, e, end, m);
-        load_codes((const uint8_t *)t.v, e, end, v);
-        load_n<8>(source<W, MASTER>(t), e, end, w);
-        const float m_scale = t.m_scale[s], v_scale = t.v_scale[s];
+        rg[u].get(g);
+        rw[u].get(w);
+        unpack_codes(rm[u], m);
+        unpack_codes(rv[u], v);
+        const float m_scale = m_scales[u], v_scale = v_scales[u];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             m[q] *= m_scale;
@@ -354,38 +435,43 @@ __device__ __forceinline__ void step_chunk_8bit(const AdamWTensor &t, int64_t at
             v[q] *= v[q];
             v[q] = el(g[q], m[q], v[q], w[q]);
         }
-        if (MASTER) store_n<8>((float *)t.master, e, end, w);
-        store_n<8>((W *)t.w, e, end, w);
+        if (MASTER) store_n<8, FULL>(c.master, e, n, w);
+        store_n<8, FULL>(c.w, e, n, w);
         // elements past the tensor's end are zero and stay so: they raise no scale
         const float m_new = scale_block(m, false), v_new = scale_block(v, true);
-        store_codes((uint8_t *)t.m, e, end, m);
-        store_codes((uint8_t *)t.v, e, end, v);
-        __syncwarp();  // every lane has read the scales
-        if (lane == 0) t.m_scale[s] = m_new, t.v_scale[s] = v_new;
+        store_codes<FULL>(ms, e, n, m);
+        store_codes<FULL>(vs, e, n, v);
+        if (lane == 0) c.m_scale[s] = m_new, c.v_scale[s] = v_new;
     }
 }
 
-template <typename W, typename G, bool MASTER>
-__device__ __forceinline__ void step_any(const AdamWTensor &t, int64_t at, int64_t end, const Element &el)
+template <bool BITS8, bool MASTER, typename W, typename G>
+__device__ __forceinline__ void step_any(const AdamWTensor &t, int64_t at, const Element &el)
 {
-    if (t.bits8)
-        step_chunk_8bit<W, G, MASTER>(t, at, end, el);
-    else
-        step_chunk<W, G, MASTER>(t, at, end, el);
+    const int64_t left = t.n - at;
+    Chunk<W, G> c{(W *)t.w + at, MASTER ? t.master + at : nullptr, (const G *)t.grad + at, nullptr, nullptr, nullptr, nullptr,
+                  (int)(left < kChunk ? left : kChunk)};
+    if constexpr (BITS8) {
+        c.m = (uint8_t *)t.m + at, c.v = (uint8_t *)t.v + at;
+        c.m_scale = t.m_scale + at / kBlock8, c.v_scale = t.v_scale + at / kBlock8;
+        c.n == kChunk ? step_chunk_8bit<MASTER, true>(c, el) : step_chunk_8bit<MASTER, false>(c, el);
+    } else {
+        c.m = (float *)t.m + at, c.v = (float *)t.v + at;
+        c.n == kChunk ? step_chunk<MASTER, true>(c, el) : step_chunk<MASTER, false>(c, el);
+    }
 }
 
-template <typename W, bool MASTER>
-__device__ __forceinline__ void step_grad(const AdamWTensor &t, int64_t at, int64_t end, const Element &el)
+template <bool BITS8, bool MASTER, typename W>
+__device__ __forceinline__ void step_grad(const AdamWTensor &t, int64_t at, const Element &el)
 {
-    if (t.grad_f32)
-        step_any<W, float, MASTER>(t, at, end, el);
-    else
-        step_any<W, __nv_bfloat16, MASTER>(t, at, end, el);
+    t.grad_f32 ? step_any<BITS8, MASTER, W, float>(t, at, el) : step_any<BITS8, MASTER, W, __nv_bfloat16>(t, at, el);
 }
 
-// A factor that is no number leaves everything as it is.
-template <typename B>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ B b, const AdamWScalars sc)
+// The tensors of a launch have states of one kind: the two kinds need
+// different numbers of registers.  A factor that is no number leaves
+// everything as it is.
+template <bool BITS8, typename B>
+__global__ void __launch_bounds__(kThreads, BITS8 ? 3 : 4) adamw_kernel(const __grid_constant__ B b, const AdamWScalars sc)
 {
     ptx::griddep_wait();
     const uint32_t chunk = blockIdx.x;
@@ -395,14 +481,13 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     const int k = find_tensor(b, chunk);
     const AdamWTensor &t = b.t[k];
     const int64_t at = (int64_t)(chunk - b.first[k]) * kChunk;
-    const int64_t end = t.n < at + kChunk ? t.n : at + kChunk;
     const float lr = (sc.lr_at ? *sc.lr_at : sc.lr) * t.lr_factor;
     const Element el{sc.beta1, sc.one_minus1, sc.beta2, sc.one_minus2, factor, fmaf(-lr, t.weight_decay, 1.0f),
                      lr * corrections.x, corrections.y, sc.eps};
     if (t.master)
-        t.w_f32 ? step_grad<float, true>(t, at, end, el) : step_grad<__nv_bfloat16, true>(t, at, end, el);
+        t.w_f32 ? step_grad<BITS8, true, float>(t, at, el) : step_grad<BITS8, true, __nv_bfloat16>(t, at, el);
     else
-        t.w_f32 ? step_grad<float, false>(t, at, end, el) : step_grad<__nv_bfloat16, false>(t, at, end, el);
+        t.w_f32 ? step_grad<BITS8, false, float>(t, at, el) : step_grad<BITS8, false, __nv_bfloat16>(t, at, el);
 }
 
 // The step's number from device memory: one more than it says, unless the
@@ -418,16 +503,17 @@ __global__ void adamw_count_kernel(int32_t *step, const float *grad_scale, doubl
     *out = make_float2((float)(1.0 / (1.0 - pow(beta1, (double)t))), (float)(1.0 / sqrt(1.0 - pow(beta2, (double)t))));
 }
 
-// Calls f with batches of the tensors that have elements, in their order.
-template <typename B, typename Tensor, typename F>
-cudaError_t in_batches(const Tensor *tensors, int count, int cap, int64_t chunk_size, F f)
+// Calls f with batches of the tensors that have elements and that `take`
+// accepts, in their order.
+template <typename B, typename Tensor, typename P, typename F>
+cudaError_t in_batches(const Tensor *tensors, int count, int cap, int64_t chunk_size, P take, F f)
 {
     B b;
     b.count = 0;
     b.first[0] = 0;
     for (int i = 0; i < count; ++i) {
         const int64_t chunks = ceil_div(tensors[i].n, chunk_size);
-        if (chunks == 0) continue;
+        if (chunks == 0 || !take(tensors[i])) continue;
         if (b.count == cap) {
             const cudaError_t e = f(b);
             if (e != cudaSuccess) return e;
@@ -470,15 +556,16 @@ cudaError_t launch_grad_norm(const TensorRef *grads, int count, float max_norm, 
     int used = 0;
     auto launch = [&](const auto &b) {
         using B = std::remove_cv_t<std::remove_reference_t<decltype(b)>>;
-        const uint32_t chunks = b.first[b.count], most = (uint32_t)(n_sm * 8 < kNormBlocks ? n_sm * 8 : kNormBlocks);
+        const uint32_t chunks = b.first[b.count], most = (uint32_t)(n_sm * kNormPerSm < kNormBlocks ? n_sm * kNormPerSm : kNormBlocks);
         cfg.gridDim = dim3(chunks < most ? chunks : most);
         const cudaError_t e = cudaLaunchKernelEx(&cfg, grad_norm_kernel<B>, b, partial + used);
         used += (int)cfg.gridDim.x;
         return e;
     };
+    auto all = [](const TensorRef &) { return true; };
     const cudaError_t e = count <= kSmallBatch
-                              ? in_batches<NormBatchSmall>(grads, count, kSmallBatch, kNormChunk, launch)
-                              : in_batches<NormBatch>(grads, count, kNormBatch, kNormChunk, launch);
+                              ? in_batches<NormBatchSmall>(grads, count, kSmallBatch, kNormChunk, all, launch)
+                              : in_batches<NormBatch>(grads, count, kNormBatch, kNormChunk, all, launch);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(1);
     return cudaLaunchKernelEx(&cfg, norm_factor_kernel, (const double2 *)partial, used, max_norm, out);
@@ -497,13 +584,19 @@ cudaError_t launch_adamw(const AdamWTensor *tensors, int count, AdamWScalars sc,
         cfg.blockDim = dim3(kThreads);
         sc.corrections = (const float2 *)workspace;
     }
-    auto launch = [&](const auto &b) {
-        using B = std::remove_cv_t<std::remove_reference_t<decltype(b)>>;
-        cfg.gridDim = dim3(b.first[b.count]);
-        return cudaLaunchKernelEx(&cfg, adamw_kernel<B>, b, (const AdamWScalars)sc);
+    auto launch = [&](auto bits8) {
+        constexpr bool BITS8 = decltype(bits8)::value;
+        auto take = [](const AdamWTensor &x) { return x.bits8 == BITS8; };
+        auto one = [&](const auto &b) {
+            using B = std::remove_cv_t<std::remove_reference_t<decltype(b)>>;
+            cfg.gridDim = dim3(b.first[b.count]);
+            return cudaLaunchKernelEx(&cfg, adamw_kernel<BITS8, B>, b, (const AdamWScalars)sc);
+        };
+        return count <= kSmallBatch ? in_batches<StepBatchSmall>(tensors, count, kSmallBatch, kChunk, take, one)
+                                    : in_batches<StepBatch>(tensors, count, kStepBatch, kChunk, take, one);
     };
-    return count <= kSmallBatch ? in_batches<StepBatchSmall>(tensors, count, kSmallBatch, kChunk, launch)
-                                : in_batches<StepBatch>(tensors, count, kStepBatch, kChunk, launch);
+    const cudaError_t e = launch(std::false_type());
+    return e == cudaSuccess ? launch(std::true_type()) : e;
 }
 
 }  // namespace moe

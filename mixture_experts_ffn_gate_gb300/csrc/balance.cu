@@ -17,6 +17,8 @@
 // sequence grows, so no two pairs share a slot, and there are blocks +
 // sequences of them.  A second, small kernel adds the slots in order.  No
 // sum depends on the order in which blocks run.
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "sm100_ptx.cuh"
@@ -27,6 +29,7 @@ namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kMostChunks = 1024;  // blocks of the first kernel
+constexpr int kLeastRows = 32;     // and their rows, where there are several
 constexpr int kCached = 1024;      // offsets that a block keeps in shared memory
 // up to this many rows and sequences run as one block, which adds nothing up
 // afterwards: one launch less
@@ -35,15 +38,17 @@ constexpr int kOneBlockRows = 64;
 // Blocks per SM and rows of a warp in flight, by what the registers hold.
 template <int PER>
 struct RowShape {
-    static constexpr int BLOCKS = PER <= 4 ? 5 : PER <= 8 ? 4 : PER <= 16 ? 3 : 2;
+    static constexpr int BLOCKS = PER <= 8 ? 4 : PER <= 16 ? 3 : 2;
     static constexpr int ROWS = PER <= 4 ? 4 : PER <= 8 ? 2 : 1;
 };
+
+// Instances by what a row needs: one set of exponentials or two.
+enum Kind { kSoftmax, kSigmoid, kSigmoidAndZ };
 
 struct BalanceArgs {
     const float *logits;
     const int32_t *idx, *offsets;  // offsets nullable: one sequence of all rows
-    int T, S, E, k, lpr, chunk;    // chunk: rows per block
-    bool sigmoid;
+    int T, S, E, k, kp, lpr, chunk;  // kp: k as a power of two; chunk: rows per block
     float coef, z_coef;
     float *loss, *prob;
     int32_t *counts;
@@ -58,7 +63,6 @@ struct BalanceGradArgs {
     const float *logits, *dloss, *base;  // dloss, base nullable
     const int32_t *counts, *offsets;
     int T, S, E, k, lpr, chunk;
-    bool sigmoid;
     float coef, z_coef;
     float *out;  // may be base
 };
@@ -206,19 +210,37 @@ __device__ __forceinline__ void sigmoids(const float (&l)[ROWS][PER], int lpr, f
     row_sum(total, lpr);
 }
 
+template <int PER, int ROWS>
+__device__ __forceinline__ void copy_rows(const float (&from)[ROWS][PER], float (&to)[ROWS][PER])
+{
+#pragma unroll
+    for (int u = 0; u < ROWS; ++u)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) to[u][i] = from[u][i];
+}
+
 // log of the sum of exponentials; 0 for a row of -inf, which has none.
 __device__ __forceinline__ float lse_of(float top, float total) { return total == 0.0f ? 0.0f : top + logf(total); }
 
-// The distinct experts of the rows [lo, hi), one row per thread.
-__device__ __forceinline__ void count_rows(const int32_t *idx, int lo, int hi, int k, int E, int32_t *hist)
+// The distinct experts of the rows [lo, hi): a warp takes as many rows at a
+// time as their slots (kp of them, a power of two) fit its lanes.
+__device__ __forceinline__ void count_rows(const int32_t *idx, int lo, int hi, int k, int kp, int E, int32_t *hist)
 {
-    for (int t = lo + (int)threadIdx.x; t < hi; t += kThreads) {
-        const int32_t *row = idx + (int64_t)t * k;
-        for (int j = 0; j < k; ++j) {
-            const int e = row[j];
-            bool fresh = e >= 0 && e < E;
-            for (int m = 0; m < j; ++m) fresh = fresh && row[m] != e;
-            if (fresh) atomicAdd(hist + e, 1);
+    constexpr int FLIGHT = 4;
+    const int lane = threadIdx.x & 31, rows = 32 / kp, mine = lane / kp, j = lane & (kp - 1);
+    for (int at = lo + (int)(threadIdx.x >> 5) * rows; at < hi; at += kWarps * rows * FLIGHT) {
+        int e[FLIGHT];
+#pragma unroll
+        for (int u = 0; u < FLIGHT; ++u) {
+            const int t = at + u * kWarps * rows + mine;
+            e[u] = t < hi && j < k ? idx[(int64_t)t * k + j] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < FLIGHT; ++u) {
+            const bool valid = e[u] >= 0 && e[u] < E;
+            // equal keys: the same expert in the same row
+            const unsigned same = __match_any_sync(0xffffffffu, valid ? mine * 1024 + e[u] : -1);
+            if (valid && (same & ((1u << lane) - 1u)) == 0) atomicAdd(hist + e[u], 1);
         }
     }
 }
@@ -236,7 +258,7 @@ __device__ __forceinline__ float sum_of_block(float v, float *part, int warps)
     return s;
 }
 
-template <int PER, bool VEC>
+template <int PER, bool VEC, Kind KIND>
 __global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_kernel(const BalanceArgs a)
 {
     constexpr int ROWS = RowShape<PER>::ROWS;
@@ -268,34 +290,44 @@ __global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_kerne
         if (lo >= hi) continue;
         for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
         __syncthreads();
-        count_rows(a.idx, lo, hi, a.k, E, hist);
+        count_rows(a.idx, lo, hi, a.k, a.kp, E, hist);
         float sum[PER], z = 0.0f;
 #pragma unroll
         for (int q = 0; q < PER; ++q) sum[q] = 0.0f;
-        for (int at = lo + warp * rows_per_warp; at < hi; at += kWarps * rows_per_warp * ROWS) {
-            float l[ROWS][PER], p[ROWS][PER], top[ROWS], total[ROWS];
+        const int step = kWarps * rows_per_warp;
+        auto fetch = [&](int at, float (&l)[ROWS][PER]) {
 #pragma unroll
             for (int u = 0; u < ROWS; ++u) {
-                const int t = at + u * kWarps * rows_per_warp + group;
+                const int t = at + u * step + group;
                 load_row<PER, VEC>(a.logits + (int64_t)t * E, t < hi, E, sub, lpr, -INFINITY, l[u]);
             }
-            if (!a.sigmoid || a.z_coef != 0.0f) {
-                exponentials<PER, ROWS>(l, lpr, p, top, total);
-                if (a.z_coef != 0.0f) {
+        };
+        float l[ROWS][PER], next[ROWS][PER];
+        int at = lo + warp * rows_per_warp;
+        fetch(at, l);
+        for (; at < hi; at += step * ROWS) {
+            float top[ROWS], total[ROWS];
+            fetch(at + step * ROWS, next);
+            if constexpr (KIND != kSigmoid) {
+                float e[ROWS][PER];
+                exponentials<PER, ROWS>(l, lpr, e, top, total);
+                if (KIND == kSigmoidAndZ || a.z_coef != 0.0f) {
 #pragma unroll
                     for (int u = 0; u < ROWS; ++u) {
                         const float lse = lse_of(top[u], total[u]);
                         if (sub == 0) z = fmaf(lse, lse, z);
                     }
                 }
+                if constexpr (KIND == kSoftmax) copy_rows(e, l);
             }
-            if (a.sigmoid) sigmoids<PER, ROWS>(l, lpr, p, total);
+            if constexpr (KIND != kSoftmax) sigmoids<PER, ROWS>(l, lpr, l, total);
 #pragma unroll
             for (int u = 0; u < ROWS; ++u) {
                 const float inv = inverse_of(total[u]);
 #pragma unroll
-                for (int q = 0; q < PER; ++q) sum[q] = fmaf(p[u][q], inv, sum[q]);
+                for (int q = 0; q < PER; ++q) sum[q] = fmaf(l[u][q], inv, sum[q]);
             }
+            copy_rows(next, l);
         }
         for (int o = lpr; o < 32; o <<= 1)
 #pragma unroll
@@ -363,10 +395,18 @@ __global__ void __launch_bounds__(1024) balance_sum_kernel(const BalanceArgs a)
         if (n > 0) {
             const int first = lo / a.chunk, end = (hi - 1) / a.chunk;
             if (e < E)
-                for (int b = first + y; b <= end; b += depth) {
-                    const int64_t slot = (int64_t)b + i;
-                    s += a.sums[slot * E + e];
-                    c += a.cnts[slot * E + e];
+                for (int b = first + y; b <= end; b += depth * 4) {
+                    float v[4];
+                    int32_t n4[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int64_t slot = (int64_t)b + u * depth + i;
+                        const bool in = b + u * depth <= end;
+                        v[u] = in ? a.sums[slot * E + e] : 0.0f;
+                        n4[u] = in ? a.cnts[slot * E + e] : 0;
+                    }
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) s += v[u], c += n4[u];
                 }
             if (blockIdx.x == 0 && a.z_coef != 0.0f)
                 for (int b = first + (int)threadIdx.x; b <= end; b += blockDim.x) z += a.zs[(int64_t)b + i];
@@ -418,7 +458,7 @@ __global__ void __launch_bounds__(1024) balance_sum_kernel(const BalanceArgs a)
 // ---------------------------------------------------------------- gradient
 // The scores are computed again from the logits.  Rows of no sequence take
 // the gradient that comes in, or zero, whatever their logits hold.
-template <int PER, bool VEC>
+template <int PER, bool VEC, Kind KIND>
 __global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_grad_kernel(const BalanceGradArgs a)
 {
     constexpr int ROWS = RowShape<PER>::ROWS;
@@ -467,8 +507,7 @@ __global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_grad_
                 lse[u] = 0.0f;
             }
             float d[ROWS][PER];
-            const bool soft = !a.sigmoid || a.z_coef != 0.0f;
-            if (soft) {
+            if constexpr (KIND != kSigmoid) {
                 exponentials<PER, ROWS>(l, lpr, p, top, total);
 #pragma unroll
                 for (int u = 0; u < ROWS; ++u) {
@@ -481,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_grad_
                     }
                 }
             }
-            if (a.sigmoid) {
+            if constexpr (KIND != kSoftmax) {
                 sigmoids<PER, ROWS>(l, lpr, p, total);
 #pragma unroll
                 for (int u = 0; u < ROWS; ++u) {
@@ -497,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_grad_
 #pragma unroll
                     for (int q = 0; q < PER; ++q) {
                         const float g = (share[q] - mean[u]) * inv * (p[u][q] * (1.0f - p[u][q]));
-                        d[u][q] = soft ? d[u][q] + g : g;
+                        d[u][q] = KIND == kSigmoidAndZ ? d[u][q] + g : g;
                     }
                 }
             } else {
@@ -537,27 +576,36 @@ int lanes_per_row(int E)
     return lpr;
 }
 
-template <bool VEC, typename F>
-cudaError_t with_row_vec(int E, F f)
+// f(PER, VEC, KIND) for E experts.
+template <bool VEC, Kind KIND, typename F>
+cudaError_t with_per(int E, F f)
 {
+    std::integral_constant<bool, VEC> vec;
+    std::integral_constant<Kind, KIND> kind;
     const int per = (E + 31) / 32;
-    if (per <= 4) return f(std::integral_constant<int, 4>(), std::integral_constant<bool, VEC>());
-    if (per <= 8) return f(std::integral_constant<int, 8>(), std::integral_constant<bool, VEC>());
-    if (per <= 12) return f(std::integral_constant<int, 12>(), std::integral_constant<bool, VEC>());
-    if (per <= 16) return f(std::integral_constant<int, 16>(), std::integral_constant<bool, VEC>());
-    if (per <= 24) return f(std::integral_constant<int, 24>(), std::integral_constant<bool, VEC>());
-    return f(std::integral_constant<int, 32>(), std::integral_constant<bool, VEC>());
+    if (per <= 4) return f(std::integral_constant<int, 4>(), vec, kind);
+    if (per <= 8) return f(std::integral_constant<int, 8>(), vec, kind);
+    if (per <= 12) return f(std::integral_constant<int, 12>(), vec, kind);
+    if (per <= 16) return f(std::integral_constant<int, 16>(), vec, kind);
+    if (per <= 24) return f(std::integral_constant<int, 24>(), vec, kind);
+    return f(std::integral_constant<int, 32>(), vec, kind);
+}
+
+template <Kind KIND, typename F>
+cudaError_t with_vec(int E, F f)
+{
+    return E % 4 == 0 ? with_per<true, KIND>(E, f) : with_per<false, KIND>(E, f);
 }
 
 template <typename F>
-cudaError_t with_row(int E, F f)
+cudaError_t with_row(int E, bool sigmoid, bool z, F f)
 {
-    return E % 4 == 0 ? with_row_vec<true>(E, f) : with_row_vec<false>(E, f);
+    return !sigmoid ? with_vec<kSoftmax>(E, f) : z ? with_vec<kSigmoidAndZ>(E, f) : with_vec<kSigmoid>(E, f);
 }
 
 int most_chunks(int64_t T)
 {
-    const int64_t c = ceil_div(T, kWarps);
+    const int64_t c = ceil_div(T, kLeastRows);
     return (int)(c < 1 ? 1 : c < kMostChunks ? c : kMostChunks);
 }
 
@@ -586,8 +634,8 @@ cudaError_t launch_balance(const BalanceCall &c, void *workspace, int n_sm, cuda
 {
     const Places p = places(c.T, c.S, c.E);
     char *ws = (char *)workspace;
-    BalanceArgs a{c.logits, c.idx, c.offsets, (int)c.T, c.S, c.E, c.k, lanes_per_row(c.E), 0, c.sigmoid, c.coef,
-                  c.z_coef, c.loss, c.prob, c.counts, (float *)(ws + p.sums), (float *)(ws + p.zs),
+    BalanceArgs a{c.logits, c.idx, c.offsets, (int)c.T, c.S, c.E, c.k, pow2_ceil(c.k), lanes_per_row(c.E), 0,
+                  c.coef, c.z_coef, c.loss, c.prob, c.counts, (float *)(ws + p.sums), (float *)(ws + p.zs),
                   (int32_t *)(ws + p.cnts), (float2 *)(ws + p.parts), (unsigned *)ws};
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -598,7 +646,7 @@ cudaError_t launch_balance(const BalanceCall &c, void *workspace, int n_sm, cuda
     cfg.numAttrs = 1;
     const bool alone = c.T <= kOneBlockRows && c.S <= kOneBlockRows;
     int blocks = 1;
-    cudaError_t e = with_row(c.E, [&](auto per, auto vec) {
+    cudaError_t e = with_row(c.E, c.sigmoid, c.z_coef != 0.0f, [&](auto per, auto vec, auto kind) {
         constexpr int PER = decltype(per)::value;
         constexpr bool VEC = decltype(vec)::value;
         if (!alone) {
@@ -610,12 +658,12 @@ cudaError_t launch_balance(const BalanceCall &c, void *workspace, int n_sm, cuda
         if (a.chunk < 1) a.chunk = 1;
         cfg.gridDim = dim3((unsigned)blocks);
         cfg.blockDim = dim3(kThreads);
-        return cudaLaunchKernelEx(&cfg, balance_kernel<PER, VEC>, (const BalanceArgs)a);
+        return cudaLaunchKernelEx(&cfg, balance_kernel<PER, VEC, decltype(kind)::value>, (const BalanceArgs)a);
     });
     if (e != cudaSuccess || alone) return e;
-    // as many warps per tile as a sequence has slots, about
+    // a warp takes about four of a sequence's slots
     int depth = 1;
-    while (depth < 32 && depth * c.S < blocks + c.S) depth <<= 1;
+    while (depth < 32 && 4 * depth * c.S < blocks + c.S) depth <<= 1;
     cfg.gridDim = dim3((unsigned)ceil_div(c.E, 32), (unsigned)(c.S < 32768 ? c.S : 32768));
     cfg.blockDim = dim3(32 * depth);
     return cudaLaunchKernelEx(&cfg, balance_sum_kernel, (const BalanceArgs)a);
@@ -624,7 +672,7 @@ cudaError_t launch_balance(const BalanceCall &c, void *workspace, int n_sm, cuda
 cudaError_t launch_balance_grad(const BalanceGradCall &c, int n_sm, cudaStream_t s)
 {
     BalanceGradArgs a{c.logits, c.dloss, c.base, c.counts, c.offsets, (int)c.T, c.S, c.E, c.k, lanes_per_row(c.E), 0,
-                      c.sigmoid, c.coef, c.z_coef, c.out};
+                      c.coef, c.z_coef, c.out};
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -633,14 +681,14 @@ cudaError_t launch_balance_grad(const BalanceGradCall &c, int n_sm, cudaStream_t
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     cfg.blockDim = dim3(kThreads);
-    return with_row(c.E, [&](auto per, auto vec) {
+    return with_row(c.E, c.sigmoid, c.z_coef != 0.0f, [&](auto per, auto vec, auto kind) {
         constexpr int PER = decltype(per)::value;
         constexpr bool VEC = decltype(vec)::value;
         const int64_t rows = kWarps * (PER > 4 ? 1 : 32 / a.lpr), fit = ceil_div(c.T, rows);
         const int64_t most = (int64_t)n_sm * RowShape<PER>::BLOCKS, blocks = fit < most ? fit : most;
         a.chunk = (int)ceil_div(c.T, blocks);
         cfg.gridDim = dim3((unsigned)blocks);
-        return cudaLaunchKernelEx(&cfg, balance_grad_kernel<PER, VEC>, (const BalanceGradArgs)a);
+        return cudaLaunchKernelEx(&cfg, balance_grad_kernel<PER, VEC, decltype(kind)::value>, (const BalanceGradArgs)a);
     });
 }
 
