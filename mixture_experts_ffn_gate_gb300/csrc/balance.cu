@@ -98,9 +98,30 @@ __device__ __forceinline__ int find_sequence(const int32_t *off, int S, int row)
     return lo;
 }
 
+// 2^x and 1 / x by the hardware's approximations (2^x within about two units
+// in the last place, 1 / x one; both flush results below 2^-126).  With expf
+// and a rounded reciprocal the instructions bound the loss (131072 x 256,
+// sigmoid: 195 a row, 42 us).  exp(l) = 2^(l log2 e) costs |l| more roundings
+// of 2^-24 than expf, which is in the tests' bounds.
+__device__ __forceinline__ float power_of_2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float reciprocal(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+constexpr float kLog2E = 1.4426950408889634f;
+
 // Whether softmax's terms of a row of -inf, or a sigmoid row's, have a sum to
 // divide by.
-__device__ __forceinline__ float inverse_of(float total) { return total < 1.17549435e-38f ? 0.0f : 1.0f / total; }
+__device__ __forceinline__ float inverse_of(float total) { return total < 1.17549435e-38f ? 0.0f : reciprocal(total); }
 
 // The lane's logits of a row, -inf past the last expert and without a row.
 // VEC (E % 4 == 0): 16 bytes at a time, neighbouring lanes side by side.
@@ -185,15 +206,14 @@ __device__ __forceinline__ void exponentials(const float (&l)[ROWS][PER], int lp
         total[u] = 0.0f;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            e[u][i] = expf(l[u][i] - top[u]);
+            e[u][i] = power_of_2((l[u][i] - top[u]) * kLog2E);
             total[u] += e[u][i];
         }
     }
     row_sum(total, lpr);
 }
 
-// 1 / (1 + exp(-l)) with the sums.  The reciprocal is the hardware's (one
-// unit in the last place), which gives zero below 2^-126.
+// 1 / (1 + exp(-l)) with the sums.
 template <int PER, int ROWS>
 __device__ __forceinline__ void sigmoids(const float (&l)[ROWS][PER], int lpr, float (&q)[ROWS][PER],
                                          float (&total)[ROWS])
@@ -203,7 +223,7 @@ __device__ __forceinline__ void sigmoids(const float (&l)[ROWS][PER], int lpr, f
         total[u] = 0.0f;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            q[u][i] = __fdividef(1.0f, 1.0f + expf(-l[u][i]));
+            q[u][i] = reciprocal(1.0f + power_of_2(-kLog2E * l[u][i]));
             total[u] += q[u][i];
         }
     }
@@ -222,27 +242,21 @@ __device__ __forceinline__ void copy_rows(const float (&from)[ROWS][PER], float 
 // log of the sum of exponentials; 0 for a row of -inf, which has none.
 __device__ __forceinline__ float lse_of(float top, float total) { return total == 0.0f ? 0.0f : top + logf(total); }
 
-// The distinct experts of the rows [lo, hi): a warp takes as many rows at a
-// time as their slots (kp of them, a power of two) fit its lanes.
-__device__ __forceinline__ void count_rows(const int32_t *idx, int lo, int hi, int k, int kp, int E, int32_t *hist)
+// A lane's slot among those of the rows [at, end): kp slots (k, as a power
+// of two) to a row.  -1 where there is none.
+__device__ __forceinline__ int load_slot(const int32_t *idx, int at, int end, int lane, int k, int kp)
 {
-    constexpr int FLIGHT = 4;
-    const int lane = threadIdx.x & 31, rows = 32 / kp, mine = lane / kp, j = lane & (kp - 1);
-    for (int at = lo + (int)(threadIdx.x >> 5) * rows; at < hi; at += kWarps * rows * FLIGHT) {
-        int e[FLIGHT];
-#pragma unroll
-        for (int u = 0; u < FLIGHT; ++u) {
-            const int t = at + u * kWarps * rows + mine;
-            e[u] = t < hi && j < k ? idx[(int64_t)t * k + j] : -1;
-        }
-#pragma unroll
-        for (int u = 0; u < FLIGHT; ++u) {
-            const bool valid = e[u] >= 0 && e[u] < E;
-            // equal keys: the same expert in the same row
-            const unsigned same = __match_any_sync(0xffffffffu, valid ? mine * 1024 + e[u] : -1);
-            if (valid && (same & ((1u << lane) - 1u)) == 0) atomicAdd(hist + e[u], 1);
-        }
-    }
+    const int t = at + lane / kp, j = lane & (kp - 1);
+    return t < end && j < k ? idx[(int64_t)t * k + j] : -1;
+}
+
+// Adds the slots of a warp's rows to the counts, a row's equal ones once.
+__device__ __forceinline__ void count_slots(int e, int E, int lane, int kp, int32_t *hist)
+{
+    const bool valid = e >= 0 && e < E;
+    // equal keys: the same expert in the same row
+    const unsigned same = __match_any_sync(0xffffffffu, valid ? (lane / kp) * 1024 + e : -1);
+    if (valid && (same & ((1u << lane) - 1u)) == 0) atomicAdd(hist + e, 1);
 }
 
 // A sum over the block, the same for every thread, in an order fixed by the
@@ -269,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_kerne
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int E = a.E, T = a.T, S = a.S;
     const int lpr = PER > 4 ? 32 : a.lpr;
-    const int sub = lane & (lpr - 1), group = lane / lpr, rows_per_warp = 32 / lpr;
+    const int sub = lane & (lpr - 1), group = lane / lpr, rows_per_warp = PER > 4 ? 1 : 32 / lpr;
     const bool alone = gridDim.x == 1;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
@@ -288,26 +302,33 @@ __global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_kerne
         const int lo = max(row, clamp_row(off[i], T)), hi = min(end, clamp_row(off[i + 1], T));
         row = max(row + 1, hi);
         if (lo >= hi) continue;
+        // a warp takes `own` rows at a time, its next ones (and their first
+        // slots) on their way while it works
+        const int own = ROWS * rows_per_warp, step = kWarps * own;
+        int at = lo + warp * own;
+        auto fetch = [&](int at, float (&l)[ROWS][PER]) {
+            const float *row = a.logits + (int64_t)(at + group) * E;
+#pragma unroll
+            for (int u = 0; u < ROWS; ++u)
+                load_row<PER, VEC>(row + (int64_t)(u * rows_per_warp) * E, at + u * rows_per_warp + group < hi, E, sub,
+                                   lpr, -INFINITY, l[u]);
+        };
+        float l[ROWS][PER], next[ROWS][PER];
+        fetch(at, l);
+        int slot = load_slot(a.idx, at, min(at + own, hi), lane, a.k, a.kp), next_slot;
         for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
         __syncthreads();
-        count_rows(a.idx, lo, hi, a.k, a.kp, E, hist);
         float sum[PER], z = 0.0f;
 #pragma unroll
         for (int q = 0; q < PER; ++q) sum[q] = 0.0f;
-        const int step = kWarps * rows_per_warp;
-        auto fetch = [&](int at, float (&l)[ROWS][PER]) {
-#pragma unroll
-            for (int u = 0; u < ROWS; ++u) {
-                const int t = at + u * step + group;
-                load_row<PER, VEC>(a.logits + (int64_t)t * E, t < hi, E, sub, lpr, -INFINITY, l[u]);
-            }
-        };
-        float l[ROWS][PER], next[ROWS][PER];
-        int at = lo + warp * rows_per_warp;
-        fetch(at, l);
-        for (; at < hi; at += step * ROWS) {
+        for (; at < hi; at += step) {
             float top[ROWS], total[ROWS];
-            fetch(at + step * ROWS, next);
+            fetch(at + step, next);
+            next_slot = load_slot(a.idx, at + step, min(at + step + own, hi), lane, a.k, a.kp);
+            count_slots(slot, E, lane, a.kp, hist);
+            for (int r = 32 / a.kp; r < own; r += 32 / a.kp)  // more rows than a warp has lanes for their slots
+                count_slots(load_slot(a.idx, at + r, min(at + own, hi), lane, a.k, a.kp), E, lane, a.kp, hist);
+            slot = next_slot;
             if constexpr (KIND != kSigmoid) {
                 float e[ROWS][PER];
                 exponentials<PER, ROWS>(l, lpr, e, top, total);
@@ -341,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_kerne
         }
         z = a.z_coef != 0.0f ? sum_of_block(z, part, kWarps) : 0.0f;
         __syncthreads();
-        const int64_t slot = (int64_t)blockIdx.x + i;
+        const int64_t place = (int64_t)blockIdx.x + i;
         const float inv_n = 1.0f / (float)(hi - lo);
         for (int e = threadIdx.x; e < E; e += kThreads) {
             float s = 0.0f;
@@ -353,14 +374,14 @@ __global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_kerne
                 a.counts[i * E + e] = hist[e];
                 balance = fmaf((float)hist[e], s, balance);
             } else {
-                a.sums[slot * E + e] = s;
-                a.cnts[slot * E + e] = hist[e];
+                a.sums[place * E + e] = s;
+                a.cnts[place * E + e] = hist[e];
             }
         }
         if (alone)
             z_total += z;
         else if (threadIdx.x == 0)
-            a.zs[slot] = z;
+            a.zs[place] = z;
         __syncthreads();  // the sums and counts are read before the next sequence's
     }
     if (alone) {
@@ -380,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_kerne
 // another; the block that ends last adds the loss's parts, in their order.
 __global__ void __launch_bounds__(1024) balance_sum_kernel(const BalanceArgs a)
 {
-    __shared__ float sums[32][33], part[32];
+    __shared__ float sums[32][33], part[32], terms[32];
     __shared__ int32_t cnts[32][33];
     __shared__ bool last;
     const int lane = threadIdx.x & 31, y = threadIdx.x >> 5, depth = blockDim.x >> 5;
@@ -417,19 +438,25 @@ __global__ void __launch_bounds__(1024) balance_sum_kernel(const BalanceArgs a)
             z = sum_of_block(z, part, depth);  // has barriers
         else
             __syncthreads();
-        if (y == 0) {
-            s = 0.0f;
-            c = 0;
-            for (int w = 0; w < depth; ++w) s += sums[w][lane], c += cnts[w][lane];
+        // a warp adds up 32 / depth experts, lane w what warp w had
+        const int per_warp = 32 / depth;
+        float term = 0.0f;
+        for (int j = y * per_warp; j < (y + 1) * per_warp; ++j) {
+            s = warp_sum(lane < depth ? sums[lane][j] : 0.0f);
+            c = __reduce_add_sync(0xffffffffu, lane < depth ? cnts[lane][j] : 0);
             s = n > 0 ? s / (float)n : 0.0f;
-            if (e < E) {
-                a.prob[(int64_t)i * E + e] = s;
-                a.counts[(int64_t)i * E + e] = c;
+            if (lane == 0 && blockIdx.x * 32 + j < E) {
+                a.prob[(int64_t)i * E + blockIdx.x * 32 + j] = s;
+                a.counts[(int64_t)i * E + blockIdx.x * 32 + j] = c;
             }
-            const float term = warp_sum((float)c * s);
+            term = fmaf((float)c, s, term);
+        }
+        if (lane == 0) terms[y] = term;
+        __syncthreads();
+        if (y == 0) {
+            term = warp_sum(lane < depth ? terms[lane] : 0.0f);
             if (lane == 0) a.parts[(int64_t)i * gridDim.x + blockIdx.x] = make_float2(term, z);
         }
-        __syncthreads();
     }
     if (threadIdx.x == 0) {
         __threadfence();

@@ -128,6 +128,21 @@ def test_masked_experts_and_rows_without_any(kind, T):
     assert (got[3] == 0).all() and (got[:, 5:9] == 0).all()
 
 
+@pytest.mark.parametrize("value", [np.finfo(np.float32).min, -1e30, 0.0, 1e30, np.finfo(np.float32).max])
+@pytest.mark.parametrize("T", [5, 100])
+def test_rows_of_one_number_are_even(value, T):
+    """Also where its exponential, or its product with a constant, is beyond FP32."""
+    logits = np.full((T, 20), value, np.float32)
+    idx = np.arange(T * 4, dtype=np.int32).reshape(T, 4) % 20
+    r = mb.moe_balance_loss_forward(cuda(logits), cuda(idx), coef=0.5)
+    assert np.allclose(r.prob.cpu().numpy(), 0.05, rtol=1e-6)
+    assert abs(r.loss[1].item() - 1) <= 1e-5 and abs(r.loss[0].item() - 0.5) <= 1e-5
+    skewed = torch.arange(20, device="cuda", dtype=torch.int32)[None]
+    d = mb.moe_balance_loss_backward(cuda(logits), skewed, 4, coef=0.5)
+    want, bound = ref.balance_grad(logits, skewed.cpu().numpy(), 4, "softmax", 0.5, 0.0)
+    assert (np.abs(d.cpu().double().numpy() - want) <= 48 * U * np.abs(want) + 48 * U * 0.5 * 20 / (4 * T * T)).all()
+
+
 @pytest.mark.parametrize("T", [40, 400])
 def test_rows_of_no_sequence_are_not_read(T):
     """NaN and infinities before the first sequence and behind the last."""
