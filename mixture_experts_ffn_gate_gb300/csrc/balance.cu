@@ -27,20 +27,30 @@ namespace moe {
 
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kMostChunks = 1024;  // blocks of the first kernel
-constexpr int kLeastRows = 32;     // and their rows, where there are several
+constexpr int kMostChunks = 512;   // blocks of the first kernel
+constexpr int kLeastRows = 64;     // and their rows, where there are several
 constexpr int kCached = 1024;      // offsets that a block keeps in shared memory
 // up to this many rows and sequences run as one block, which adds nothing up
 // afterwards: one launch less
 constexpr int kOneBlockRows = 64;
 
-// Blocks per SM and rows of a warp in flight, by what the registers hold.
+// Warps per block and rows of a warp in flight, by what the registers hold
+// with two blocks on an SM.  Few large blocks: every one adds a slot that the
+// second kernel reads (131072 x 256: 34.4 us with four blocks of 8 warps).
+constexpr int kPerSm = 2;
+
 template <int PER>
 struct RowShape {
-    static constexpr int BLOCKS = PER <= 8 ? 4 : PER <= 16 ? 3 : 2;
+    static constexpr int WARPS = PER <= 8 ? 16 : PER <= 16 ? 12 : 8, THREADS = 32 * WARPS;
     static constexpr int ROWS = PER <= 4 ? 4 : PER <= 8 ? 2 : 1;
 };
+
+// The gradient's blocks add nothing up and are smaller (131072 x 256: 64.0 us;
+// with the loss's shape 66.8).
+constexpr int kGradWarps = 8;
+
+template <int PER>
+constexpr int kGradPerSm = PER <= 8 ? 4 : PER <= 16 ? 3 : 2;
 
 // Instances by what a row needs: one set of exponentials or two.
 enum Kind { kSoftmax, kSigmoid, kSigmoidAndZ };
@@ -76,7 +86,7 @@ __device__ __forceinline__ const int32_t *cache_offsets(const int32_t *offsets, 
     if (!offsets) {
         if (threadIdx.x == 0) kept[0] = 0, kept[1] = T;
     } else if (S < kCached) {
-        for (int i = threadIdx.x; i <= S; i += kThreads) kept[i] = offsets[i];
+        for (int i = threadIdx.x; i <= S; i += blockDim.x) kept[i] = offsets[i];
     }
     __syncthreads();
     return offsets && S >= kCached ? offsets : kept;
@@ -273,25 +283,24 @@ __device__ __forceinline__ float sum_of_block(float v, float *part, int warps)
 }
 
 template <int PER, bool VEC, Kind KIND>
-__global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_kernel(const BalanceArgs a)
+__global__ void __launch_bounds__(RowShape<PER>::THREADS, kPerSm) balance_kernel(const BalanceArgs a)
 {
-    constexpr int ROWS = RowShape<PER>::ROWS;
-    __shared__ float warp_sums[kWarps][32 * PER];
+    constexpr int ROWS = RowShape<PER>::ROWS, WARPS = RowShape<PER>::WARPS, THREADS = 32 * WARPS;
+    __shared__ float warp_sums[WARPS][32 * PER];
     __shared__ int32_t hist[32 * PER];
     __shared__ int32_t kept[kCached];
-    __shared__ float part[kWarps];
+    __shared__ float part[WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int E = a.E, T = a.T, S = a.S;
     const int lpr = PER > 4 ? 32 : a.lpr;
     const int sub = lane & (lpr - 1), group = lane / lpr, rows_per_warp = PER > 4 ? 1 : 32 / lpr;
     const bool alone = gridDim.x == 1;
-    ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     if (!alone && blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
     const int32_t *off = cache_offsets(a.offsets, S, T, kept);
     float balance = 0.0f, z_total = 0.0f;  // alone: this thread's part of the two sums
     if (alone) {
-        for (int i = threadIdx.x; i < S * E; i += kThreads) a.prob[i] = 0.0f, a.counts[i] = 0;
+        for (int i = threadIdx.x; i < S * E; i += THREADS) a.prob[i] = 0.0f, a.counts[i] = 0;
         __syncthreads();
     }
     int row = blockIdx.x * a.chunk;
@@ -304,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_kerne
         if (lo >= hi) continue;
         // a warp takes `own` rows at a time, its next ones (and their first
         // slots) on their way while it works
-        const int own = ROWS * rows_per_warp, step = kWarps * own;
+        const int own = ROWS * rows_per_warp, step = WARPS * own;
         int at = lo + warp * own;
         auto fetch = [&](int at, float (&l)[ROWS][PER]) {
             const float *row = a.logits + (int64_t)(at + group) * E;
@@ -316,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_kerne
         float l[ROWS][PER], next[ROWS][PER];
         fetch(at, l);
         int slot = load_slot(a.idx, at, min(at + own, hi), lane, a.k, a.kp), next_slot;
-        for (int e = threadIdx.x; e < E; e += kThreads) hist[e] = 0;
+        for (int e = threadIdx.x; e < E; e += THREADS) hist[e] = 0;
         __syncthreads();
         float sum[PER], z = 0.0f;
 #pragma unroll
@@ -360,14 +369,14 @@ __global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_kerne
                 if (e < E) warp_sums[warp][e] = sum[q];
             }
         }
-        z = a.z_coef != 0.0f ? sum_of_block(z, part, kWarps) : 0.0f;
+        z = a.z_coef != 0.0f ? sum_of_block(z, part, WARPS) : 0.0f;
         __syncthreads();
         const int64_t place = (int64_t)blockIdx.x + i;
         const float inv_n = 1.0f / (float)(hi - lo);
-        for (int e = threadIdx.x; e < E; e += kThreads) {
+        for (int e = threadIdx.x; e < E; e += THREADS) {
             float s = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) s += warp_sums[w][e];
+            for (int w = 0; w < WARPS; ++w) s += warp_sums[w][e];
             if (alone) {
                 s *= inv_n;
                 a.prob[i * E + e] = s;
@@ -385,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_kerne
         __syncthreads();  // the sums and counts are read before the next sequence's
     }
     if (alone) {
-        balance = sum_of_block(balance, part, kWarps);
+        balance = sum_of_block(balance, part, WARPS);
         if (threadIdx.x == 0) {
             const int n = max(clamp_row(off[S], T) - clamp_row(off[0], T), 0);
             balance = n ? balance * (float)E / ((float)a.k * (float)n) : 0.0f;
@@ -397,10 +406,18 @@ __global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_kerne
     }
 }
 
+__device__ __forceinline__ unsigned add_acq_rel(unsigned *at, unsigned v)
+{
+    unsigned old;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(old) : "l"(at), "r"(v) : "memory");
+    return old;
+}
+
 // The slots' sums: a block of 32 experts by blockDim.y for one sequence after
 // another; the block that ends last adds the loss's parts, in their order.
 __global__ void __launch_bounds__(1024) balance_sum_kernel(const BalanceArgs a)
 {
+    constexpr int FLIGHT = 10;
     __shared__ float sums[32][33], part[32], terms[32];
     __shared__ int32_t cnts[32][33];
     __shared__ bool last;
@@ -416,18 +433,18 @@ __global__ void __launch_bounds__(1024) balance_sum_kernel(const BalanceArgs a)
         if (n > 0) {
             const int first = lo / a.chunk, end = (hi - 1) / a.chunk;
             if (e < E)
-                for (int b = first + y; b <= end; b += depth * 4) {
-                    float v[4];
-                    int32_t n4[4];
+                for (int b = first + y; b <= end; b += depth * FLIGHT) {
+                    float v[FLIGHT];
+                    int32_t many[FLIGHT];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
+                    for (int u = 0; u < FLIGHT; ++u) {
                         const int64_t slot = (int64_t)b + u * depth + i;
                         const bool in = b + u * depth <= end;
                         v[u] = in ? a.sums[slot * E + e] : 0.0f;
-                        n4[u] = in ? a.cnts[slot * E + e] : 0;
+                        many[u] = in ? a.cnts[slot * E + e] : 0;
                     }
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) s += v[u], c += n4[u];
+                    for (int u = 0; u < FLIGHT; ++u) s += v[u], c += many[u];
                 }
             if (blockIdx.x == 0 && a.z_coef != 0.0f)
                 for (int b = first + (int)threadIdx.x; b <= end; b += blockDim.x) z += a.zs[(int64_t)b + i];
@@ -458,21 +475,25 @@ __global__ void __launch_bounds__(1024) balance_sum_kernel(const BalanceArgs a)
             if (lane == 0) a.parts[(int64_t)i * gridDim.x + blockIdx.x] = make_float2(term, z);
         }
     }
-    if (threadIdx.x == 0) {
-        __threadfence();
-        last = atomicAdd(a.ticket, 1u) == gridDim.x * gridDim.y - 1;
-    }
+    // thread 0 wrote the block's parts, and its addition to the ticket releases
+    // them to the block whose addition is the last
+    if (threadIdx.x == 0) last = add_acq_rel(a.ticket, 1u) == gridDim.x * gridDim.y - 1;
     __syncthreads();
     if (!last) return;
-    __threadfence();
     float balance = 0.0f, z = 0.0f;
     for (int64_t j = threadIdx.x; j < (int64_t)S * gridDim.x; j += blockDim.x) {
         const float2 v = __ldcg(a.parts + j);
         balance += v.x;
         z += v.y;
     }
-    balance = sum_of_block(balance, part, depth);
-    z = sum_of_block(z, part, depth);
+    balance = warp_sum(balance);
+    z = warp_sum(z);
+    if (lane == 0) terms[y] = balance, part[y] = z;
+    __syncthreads();
+    if (y == 0) {
+        balance = warp_sum(lane < depth ? terms[lane] : 0.0f);
+        z = warp_sum(lane < depth ? part[lane] : 0.0f);
+    }
     if (threadIdx.x == 0) {
         balance = rows > 0.0f ? balance * (float)E / ((float)a.k * rows) : 0.0f;
         z = rows > 0.0f ? z / rows : 0.0f;
@@ -486,9 +507,9 @@ __global__ void __launch_bounds__(1024) balance_sum_kernel(const BalanceArgs a)
 // The scores are computed again from the logits.  Rows of no sequence take
 // the gradient that comes in, or zero, whatever their logits hold.
 template <int PER, bool VEC, Kind KIND>
-__global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_grad_kernel(const BalanceGradArgs a)
+__global__ void __launch_bounds__(32 * kGradWarps, kGradPerSm<PER>) balance_grad_kernel(const BalanceGradArgs a)
 {
-    constexpr int ROWS = RowShape<PER>::ROWS;
+    constexpr int ROWS = RowShape<PER>::ROWS, WARPS = kGradWarps;
     __shared__ int32_t kept[kCached];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int E = a.E, T = a.T, S = a.S;
@@ -501,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_grad_
     const float scale = up * a.coef * (float)E / (float)a.k * per_row;
     const float z_scale = 2.0f * up * a.z_coef * per_row;
     auto pass = [&](int from, int to) {  // rows of no sequence
-        for (int at = from + warp * rows_per_warp; at < to; at += kWarps * rows_per_warp) {
+        for (int at = from + warp * rows_per_warp; at < to; at += WARPS * rows_per_warp) {
             const int t = at + group;
             if (t >= to) continue;
             float v[PER];
@@ -525,11 +546,11 @@ __global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_grad_
             const int e = expert_of<PER, VEC>(q, sub, lpr);
             share[q] = e < E ? (float)a.counts[(int64_t)i * E + e] * inv_n : 0.0f;
         }
-        for (int at = lo + warp * rows_per_warp; at < hi; at += kWarps * rows_per_warp * ROWS) {
+        for (int at = lo + warp * rows_per_warp; at < hi; at += WARPS * rows_per_warp * ROWS) {
             float l[ROWS][PER], p[ROWS][PER], top[ROWS], total[ROWS], mean[ROWS], lse[ROWS];
 #pragma unroll
             for (int u = 0; u < ROWS; ++u) {
-                const int t = at + u * kWarps * rows_per_warp + group;
+                const int t = at + u * WARPS * rows_per_warp + group;
                 load_row<PER, VEC>(a.logits + (int64_t)t * E, t < hi, E, sub, lpr, -INFINITY, l[u]);
                 lse[u] = 0.0f;
             }
@@ -581,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, RowShape<PER>::BLOCKS) balance_grad_
             }
 #pragma unroll
             for (int u = 0; u < ROWS; ++u) {
-                const int t = at + u * kWarps * rows_per_warp + group;
+                const int t = at + u * WARPS * rows_per_warp + group;
                 if (t >= hi) continue;
                 if (a.base) {
                     float b[PER];
@@ -678,17 +699,17 @@ cudaError_t launch_balance(const BalanceCall &c, void *workspace, int n_sm, cuda
         constexpr bool VEC = decltype(vec)::value;
         if (!alone) {
             blocks = most_chunks(c.T);
-            if (blocks > n_sm * RowShape<PER>::BLOCKS) blocks = n_sm * RowShape<PER>::BLOCKS;
+            if (blocks > n_sm * kPerSm) blocks = n_sm * kPerSm;
             if (blocks < 2) blocks = 2;  // one is the block that ends the call by itself
         }
         a.chunk = (int)ceil_div(c.T, blocks);
         if (a.chunk < 1) a.chunk = 1;
         cfg.gridDim = dim3((unsigned)blocks);
-        cfg.blockDim = dim3(kThreads);
+        cfg.blockDim = dim3(RowShape<PER>::THREADS);
         return cudaLaunchKernelEx(&cfg, balance_kernel<PER, VEC, decltype(kind)::value>, (const BalanceArgs)a);
     });
     if (e != cudaSuccess || alone) return e;
-    // a warp takes about four of a sequence's slots
+    // a warp takes a few of a sequence's slots, all at once
     int depth = 1;
     while (depth < 32 && 4 * depth * c.S < blocks + c.S) depth <<= 1;
     cfg.gridDim = dim3((unsigned)ceil_div(c.E, 32), (unsigned)(c.S < 32768 ? c.S : 32768));
@@ -707,13 +728,13 @@ cudaError_t launch_balance_grad(const BalanceGradCall &c, int n_sm, cudaStream_t
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    cfg.blockDim = dim3(kThreads);
     return with_row(c.E, c.sigmoid, c.z_coef != 0.0f, [&](auto per, auto vec, auto kind) {
         constexpr int PER = decltype(per)::value;
         constexpr bool VEC = decltype(vec)::value;
-        const int64_t rows = kWarps * (PER > 4 ? 1 : 32 / a.lpr), fit = ceil_div(c.T, rows);
-        const int64_t most = (int64_t)n_sm * RowShape<PER>::BLOCKS, blocks = fit < most ? fit : most;
+        const int64_t rows = kGradWarps * (PER > 4 ? 1 : 32 / a.lpr), fit = ceil_div(c.T, rows);
+        const int64_t most = (int64_t)n_sm * kGradPerSm<PER>, blocks = fit < most ? fit : most;
         a.chunk = (int)ceil_div(c.T, blocks);
+        cfg.blockDim = dim3(32 * kGradWarps);
         cfg.gridDim = dim3((unsigned)blocks);
         return cudaLaunchKernelEx(&cfg, balance_grad_kernel<PER, VEC, decltype(kind)::value>, (const BalanceGradArgs)a);
     });

@@ -135,9 +135,12 @@ def _size(t, name="workspace"):
     return t.numel() * t.element_size()
 
 
-def _here(device):
-    """The current device is the tensors': the library runs on the current one."""
-    if device.index != torch.cuda.current_device():
+def _here(device, *others):
+    """The tensors are on one device, and it is the current one, where the library runs."""
+    for t in others:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {t.device} and on {device}")
+    if device.index != torch._C._cuda_getDevice():
         raise ValueError(f"tensors on {device}, but the current device is cuda:{torch.cuda.current_device()}")
 
 
@@ -458,19 +461,11 @@ def _balance_opts(score, coef, z_coef):
     return ctypes.byref(moe_balance_opts(_SCORES[score], coef, z_coef))
 
 
-def _sequences(seq_offsets, device):
-    if seq_offsets is None:
-        return 1
+def _sequences(seq_offsets):
     if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
         raise ValueError(f"seq_offsets must be [sequences + 1], got {tuple(seq_offsets.shape)}")
-    _is(seq_offsets, tuple(seq_offsets.shape), torch.int32, "seq_offsets")
-    _same_device(seq_offsets, device, "seq_offsets")
+    _is(seq_offsets, seq_offsets.shape, torch.int32, "seq_offsets")
     return seq_offsets.shape[0] - 1
-
-
-def _same_device(t, device, name):
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
 def moe_balance_loss_forward(logits, topk_idx, score: str = "softmax", coef: float = 1e-2, z_coef: float = 0.0,
@@ -485,10 +480,9 @@ def moe_balance_loss_forward(logits, topk_idx, score: str = "softmax", coef: flo
     k = topk_idx.shape[1]
     _is(logits, (T, E), torch.float32, "logits")
     _is(topk_idx, (T, k), torch.int32, "topk_idx")
+    S = 1 if seq_offsets is None else _sequences(seq_offsets)
     dev, empty = logits.device, torch.empty if stream is None else _empty_on(stream)
-    _here(dev)
-    _same_device(topk_idx, dev, "topk_idx")
-    S = _sequences(seq_offsets, dev)
+    _here(dev, topk_idx, seq_offsets, loss, counts, prob, workspace)
     if loss is None:
         loss = empty((3,), dtype=torch.float32, device=dev)
     else:
@@ -503,11 +497,11 @@ def moe_balance_loss_forward(logits, topk_idx, score: str = "softmax", coef: flo
         _is(prob, (S, E), torch.float32, "prob")
     if workspace is None:
         workspace = new_balance_workspace(T, E, S, device=dev, stream=stream)
-    p = _ptr
-    _check(_lib().moe_balance_loss_forward(p(logits), p(topk_idx), p(seq_offsets), T, S, E, k,
-                                           _balance_opts(score, coef, z_coef), p(loss), p(counts), p(prob),
-                                           p(workspace), _size(workspace), _stream(stream, dev)),
-           "moe_balance_loss_forward")
+    status = _lib().moe_balance_loss_forward(
+        logits.data_ptr(), topk_idx.data_ptr(), _ptr(seq_offsets), T, S, E, k, _balance_opts(score, coef, z_coef),
+        loss.data_ptr(), counts.data_ptr(), prob.data_ptr(), workspace.data_ptr(), _size(workspace),
+        _stream(stream, dev))
+    _check(status, "moe_balance_loss_forward")
     return BalanceOutput(loss, counts, prob)
 
 
@@ -519,26 +513,23 @@ def moe_balance_loss_backward(logits, counts, k: int, score: str = "softmax", co
     [T,E] (nullable), which ``dlogits`` may be itself."""
     T, E = logits.shape
     _is(logits, (T, E), torch.float32, "logits")
+    S = 1 if seq_offsets is None else _sequences(seq_offsets)
     dev = logits.device
-    _here(dev)
-    S = _sequences(seq_offsets, dev)
+    _here(dev, counts, seq_offsets, dloss, dlogits_in, dlogits)
     _is(counts, (S, E), torch.int32, "counts")
-    _same_device(counts, dev, "counts")
     if dloss is not None:
         _is(dloss, (1,), torch.float32, "dloss")
-        _same_device(dloss, dev, "dloss")
     if dlogits_in is not None:
         _is(dlogits_in, (T, E), torch.float32, "dlogits_in")
-        _same_device(dlogits_in, dev, "dlogits_in")
     if dlogits is None:
         empty = torch.empty if stream is None else _empty_on(stream)
         dlogits = empty((T, E), dtype=torch.float32, device=dev)
     else:
         _is(dlogits, (T, E), torch.float32, "dlogits")
-    p = _ptr
-    _check(_lib().moe_balance_loss_backward(p(logits), p(counts), p(seq_offsets), T, S, E, k,
-                                            _balance_opts(score, coef, z_coef), p(dloss), p(dlogits_in), p(dlogits),
-                                            _stream(stream, dev)), "moe_balance_loss_backward")
+    status = _lib().moe_balance_loss_backward(
+        logits.data_ptr(), counts.data_ptr(), _ptr(seq_offsets), T, S, E, k, _balance_opts(score, coef, z_coef),
+        _ptr(dloss), _ptr(dlogits_in), dlogits.data_ptr(), _stream(stream, dev))
+    _check(status, "moe_balance_loss_backward")
     return dlogits
 
 
@@ -587,12 +578,11 @@ def moe_grad_norm(grads, max_norm: float = math.inf, out=None, workspace=None, s
     n, dev = len(grads.grads), grads.device
     if dev is None:
         dev = torch.device("cuda", torch.cuda.current_device()) if out is None else out.device
-    _here(dev)
+    _here(dev, out, workspace)
     if out is None:
         out = (torch.empty if stream is None else _empty_on(stream))((2,), dtype=torch.float32, device=dev)
     else:
         _is(out, (2,), torch.float32, "out")
-        _same_device(out, dev, "out")
     if workspace is None:
         workspace = new_grad_norm_workspace(n, device=dev, stream=stream)
     _check(_lib().moe_grad_norm(grads.array, n, max_norm, out.data_ptr(), workspace.data_ptr(), _size(workspace),
@@ -677,7 +667,8 @@ class AdamWPlan:
         for i, (g, w) in enumerate(zip(grads, self.weights)):
             _is(g, tuple(w.shape), g.dtype, f"grads[{i}]")
             _type(g, f"grads[{i}]")
-            _same_device(g, self.device, f"grads[{i}]")
+            if g.device != self.device:
+                raise ValueError(f"grads[{i}] is on {g.device}, not on {self.device}")
         for d, g in zip(self.array, grads):
             d.grad, d.grad_type = g.data_ptr(), _TYPES[g.dtype]
         self.grads, self._grad_list = grads, None
@@ -703,7 +694,6 @@ def moe_adamw_step(plan: AdamWPlan, step, lr=1e-3, betas=(0.9, 0.999), eps: floa
     dev = plan.device
     if dev is None:
         return
-    _here(dev)
     counter = lr_at = None
     if isinstance(step, torch.Tensor):
         _is(step, (1,), torch.int32, "step")
@@ -713,9 +703,7 @@ def moe_adamw_step(plan: AdamWPlan, step, lr=1e-3, betas=(0.9, 0.999), eps: floa
         lr_at, lr = lr, 0.0
     if grad_scale is not None:
         _is(grad_scale, (1,), torch.float32, "grad_scale")
-    for name, t in (("step", counter), ("lr", lr_at), ("grad_scale", grad_scale)):
-        if t is not None:
-            _same_device(t, dev, name)
+    _here(dev, counter, lr_at, grad_scale, workspace)
     if counter is not None and workspace is None:
         workspace = _workspace(256, dev, stream, "workspace size")
     o = moe_adamw_opts(lr, betas[0], betas[1], eps, step)
