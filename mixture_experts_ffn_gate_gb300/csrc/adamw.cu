@@ -37,6 +37,7 @@ constexpr int kNormBatch = 512;   // 14 KB
 constexpr int kThreads = 256;
 constexpr int kBlock8 = 256;        // elements that share a scale: eight to a lane
 constexpr int kChunk = 4096;        // elements of a block of the step
+constexpr int kStepPerSm = 4;       // its blocks that an SM holds
 constexpr int kNormChunk = 4096;    // elements that a block of the norm takes at a time
 constexpr int kNormPerSm = 6;       // its blocks that an SM holds
 constexpr int kNormBlocks = 1024;   // its partial sums per launch, at most
@@ -300,6 +301,13 @@ __global__ void __launch_bounds__(kThreads) norm_factor_kernel(const double2 *pa
 using StepBatch = Batch<AdamWTensor, kStepBatch>;
 using StepBatchSmall = Batch<AdamWTensor, kSmallBatch>;
 
+__device__ __forceinline__ float reciprocal(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // What an element's update takes.
 struct Element {
     float b1, a1, b2, a2;  // the betas and 1 - them
@@ -308,14 +316,16 @@ struct Element {
     // m, v and w after the step; returns sqrt(v).  The moments' products and
     // sums are rounded one by one: an 8-bit code next to a tie goes by their
     // last bit, which then is the formula's in FP32 and not a contraction's.
-    // The quotient's two units in the last place are small against w's.
+    // The reciprocal's unit in the last place is small against w's (it is zero
+    // where sqrt(v) is beyond 2^126, which takes gradients whose square is
+    // infinite).
     __device__ __forceinline__ float operator()(float g, float &m, float &v, float &w) const
     {
         g = __fmul_rn(g, g_scale);
         m = __fadd_rn(__fmul_rn(b1, m), __fmul_rn(a1, g));
         v = __fadd_rn(__fmul_rn(b2, v), __fmul_rn(__fmul_rn(a2, g), g));
         const float r = __fsqrt_rn(v);
-        w = fmaf(w, decay, -step * __fdividef(m, fmaf(r, root, eps)));
+        w = fmaf(w, decay, -step * (m * reciprocal(fmaf(r, root, eps))));
         return r;
     }
 };
@@ -384,8 +394,8 @@ __device__ __forceinline__ float scale_block(float (&x)[8], bool up)
     float top = 0.0f;
 #pragma unroll
     for (int q = 0; q < 8; ++q) top = fmaxf(top, fabsf(x[q]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // numbers from zero on are ordered as their bits are
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
     const float scale = fmaxf(__fmul_rn(top, 1.0f / kTop), 1.17549435e-38f), inv = __frcp_rn(scale);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -445,13 +455,13 @@ __device__ __forceinline__ void step_chunk_8bit(const Chunk<W, G> &c, const Elem
     }
 }
 
-template <bool BITS8, bool MASTER, typename W, typename G>
+template <bool MASTER, typename W, typename G>
 __device__ __forceinline__ void step_any(const AdamWTensor &t, int64_t at, const Element &el)
 {
     const int64_t left = t.n - at;
     Chunk<W, G> c{(W *)t.w + at, MASTER ? t.master + at : nullptr, (const G *)t.grad + at, nullptr, nullptr, nullptr, nullptr,
                   (int)(left < kChunk ? left : kChunk)};
-    if constexpr (BITS8) {
+    if (t.bits8) {
         c.m = (uint8_t *)t.m + at, c.v = (uint8_t *)t.v + at;
         c.m_scale = t.m_scale + at / kBlock8, c.v_scale = t.v_scale + at / kBlock8;
         c.n == kChunk ? step_chunk_8bit<MASTER, true>(c, el) : step_chunk_8bit<MASTER, false>(c, el);
@@ -461,17 +471,15 @@ __device__ __forceinline__ void step_any(const AdamWTensor &t, int64_t at, const
     }
 }
 
-template <bool BITS8, bool MASTER, typename W>
+template <bool MASTER, typename W>
 __device__ __forceinline__ void step_grad(const AdamWTensor &t, int64_t at, const Element &el)
 {
-    t.grad_f32 ? step_any<BITS8, MASTER, W, float>(t, at, el) : step_any<BITS8, MASTER, W, __nv_bfloat16>(t, at, el);
+    t.grad_f32 ? step_any<MASTER, W, float>(t, at, el) : step_any<MASTER, W, __nv_bfloat16>(t, at, el);
 }
 
-// The tensors of a launch have states of one kind: the two kinds need
-// different numbers of registers.  A factor that is no number leaves
-// everything as it is.
-template <bool BITS8, typename B>
-__global__ void __launch_bounds__(kThreads, BITS8 ? 3 : 4) adamw_kernel(const __grid_constant__ B b, const AdamWScalars sc)
+// A factor that is no number leaves everything as it is.
+template <typename B>
+__global__ void __launch_bounds__(kThreads, kStepPerSm) adamw_kernel(const __grid_constant__ B b, const AdamWScalars sc)
 {
     ptx::griddep_wait();
     const uint32_t chunk = blockIdx.x;
@@ -485,9 +493,9 @@ __global__ void __launch_bounds__(kThreads, BITS8 ? 3 : 4) adamw_kernel(const __
     const Element el{sc.beta1, sc.one_minus1, sc.beta2, sc.one_minus2, factor, fmaf(-lr, t.weight_decay, 1.0f),
                      lr * corrections.x, corrections.y, sc.eps};
     if (t.master)
-        t.w_f32 ? step_grad<BITS8, true, float>(t, at, el) : step_grad<BITS8, true, __nv_bfloat16>(t, at, el);
+        t.w_f32 ? step_grad<true, float>(t, at, el) : step_grad<true, __nv_bfloat16>(t, at, el);
     else
-        t.w_f32 ? step_grad<BITS8, false, float>(t, at, el) : step_grad<BITS8, false, __nv_bfloat16>(t, at, el);
+        t.w_f32 ? step_grad<false, float>(t, at, el) : step_grad<false, __nv_bfloat16>(t, at, el);
 }
 
 // The step's number from device memory: one more than it says, unless the
@@ -503,17 +511,16 @@ __global__ void adamw_count_kernel(int32_t *step, const float *grad_scale, doubl
     *out = make_float2((float)(1.0 / (1.0 - pow(beta1, (double)t))), (float)(1.0 / sqrt(1.0 - pow(beta2, (double)t))));
 }
 
-// Calls f with batches of the tensors that have elements and that `take`
-// accepts, in their order.
-template <typename B, typename Tensor, typename P, typename F>
-cudaError_t in_batches(const Tensor *tensors, int count, int cap, int64_t chunk_size, P take, F f)
+// Calls f with batches of the tensors that have elements, in their order.
+template <typename B, typename Tensor, typename F>
+cudaError_t in_batches(const Tensor *tensors, int count, int cap, int64_t chunk_size, F f)
 {
     B b;
     b.count = 0;
     b.first[0] = 0;
     for (int i = 0; i < count; ++i) {
         const int64_t chunks = ceil_div(tensors[i].n, chunk_size);
-        if (chunks == 0 || !take(tensors[i])) continue;
+        if (chunks == 0) continue;
         if (b.count == cap) {
             const cudaError_t e = f(b);
             if (e != cudaSuccess) return e;
@@ -562,10 +569,9 @@ cudaError_t launch_grad_norm(const TensorRef *grads, int count, float max_norm, 
         used += (int)cfg.gridDim.x;
         return e;
     };
-    auto all = [](const TensorRef &) { return true; };
     const cudaError_t e = count <= kSmallBatch
-                              ? in_batches<NormBatchSmall>(grads, count, kSmallBatch, kNormChunk, all, launch)
-                              : in_batches<NormBatch>(grads, count, kNormBatch, kNormChunk, all, launch);
+                              ? in_batches<NormBatchSmall>(grads, count, kSmallBatch, kNormChunk, launch)
+                              : in_batches<NormBatch>(grads, count, kNormBatch, kNormChunk, launch);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(1);
     return cudaLaunchKernelEx(&cfg, norm_factor_kernel, (const double2 *)partial, used, max_norm, out);
@@ -584,19 +590,13 @@ cudaError_t launch_adamw(const AdamWTensor *tensors, int count, AdamWScalars sc,
         cfg.blockDim = dim3(kThreads);
         sc.corrections = (const float2 *)workspace;
     }
-    auto launch = [&](auto bits8) {
-        constexpr bool BITS8 = decltype(bits8)::value;
-        auto take = [](const AdamWTensor &x) { return x.bits8 == BITS8; };
-        auto one = [&](const auto &b) {
-            using B = std::remove_cv_t<std::remove_reference_t<decltype(b)>>;
-            cfg.gridDim = dim3(b.first[b.count]);
-            return cudaLaunchKernelEx(&cfg, adamw_kernel<BITS8, B>, b, (const AdamWScalars)sc);
-        };
-        return count <= kSmallBatch ? in_batches<StepBatchSmall>(tensors, count, kSmallBatch, kChunk, take, one)
-                                    : in_batches<StepBatch>(tensors, count, kStepBatch, kChunk, take, one);
+    auto launch = [&](const auto &b) {
+        using B = std::remove_cv_t<std::remove_reference_t<decltype(b)>>;
+        cfg.gridDim = dim3(b.first[b.count]);
+        return cudaLaunchKernelEx(&cfg, adamw_kernel<B>, b, (const AdamWScalars)sc);
     };
-    const cudaError_t e = launch(std::false_type());
-    return e == cudaSuccess ? launch(std::true_type()) : e;
+    return count <= kSmallBatch ? in_batches<StepBatchSmall>(tensors, count, kSmallBatch, kChunk, launch)
+                                : in_batches<StepBatch>(tensors, count, kStepBatch, kChunk, launch);
 }
 
 }  // namespace moe

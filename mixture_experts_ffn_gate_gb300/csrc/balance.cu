@@ -17,6 +17,13 @@
 // sequence grows, so no two pairs share a slot, and there are blocks +
 // sequences of them.  A second, small kernel adds the slots in order.  No
 // sum depends on the order in which blocks run.
+//
+// DRAM bounds a large call's first kernel (131072 x 256, 37 sequences: 26 us,
+// floor at the copy rate 20.4) and latency the second (6 us: the slots, their
+// sum, the release to the block that ends last): 32 us in all.  Without the
+// hardware's exponentials the first kernel's instructions took longer than its
+// bytes; with the slots counted before the rows instead of between them it
+// waited for them (40 us).  8191 x 128: 10.2 us, of which the second kernel 5.5.
 #include <type_traits>
 
 #include "common.cuh"
@@ -45,12 +52,15 @@ struct RowShape {
     static constexpr int ROWS = PER <= 4 ? 4 : PER <= 8 ? 2 : 1;
 };
 
-// The gradient's blocks add nothing up and are smaller (131072 x 256: 64.0 us;
-// with the loss's shape 66.8).
+// The gradient's blocks add nothing up and are smaller; a warp has fewer rows
+// in flight, for each brings the incoming gradient along.
 constexpr int kGradWarps = 8;
 
 template <int PER>
-constexpr int kGradPerSm = PER <= 8 ? 4 : PER <= 16 ? 3 : 2;
+struct GradShape {
+    static constexpr int PER_SM = PER <= 8 ? 5 : PER <= 16 ? 3 : 2;
+    static constexpr int ROWS = PER <= 4 ? 2 : 1;
+};
 
 // Instances by what a row needs: one set of exponentials or two.
 enum Kind { kSoftmax, kSigmoid, kSigmoidAndZ };
@@ -505,11 +515,16 @@ __global__ void __launch_bounds__(1024) balance_sum_kernel(const BalanceArgs a)
 
 // ---------------------------------------------------------------- gradient
 // The scores are computed again from the logits.  Rows of no sequence take
-// the gradient that comes in, or zero, whatever their logits hold.
+// the gradient that comes in, or zero, whatever their logits hold.  Bound by
+// DRAM: 131072 x 256 with 37 sequences and an incoming gradient 64.7 us (floor
+// at the copy rate 59.3), without one 45.1 (39.5); 100000 x 128, softmax and
+// z, 27.9 (22.6).  The incoming gradient loaded with the logits instead of
+// after them, and one row of a warp in flight instead of two: 34.7 to 27.9,
+// 65.7 to 64.7.
 template <int PER, bool VEC, Kind KIND>
-__global__ void __launch_bounds__(32 * kGradWarps, kGradPerSm<PER>) balance_grad_kernel(const BalanceGradArgs a)
+__global__ void __launch_bounds__(32 * kGradWarps, GradShape<PER>::PER_SM) balance_grad_kernel(const BalanceGradArgs a)
 {
-    constexpr int ROWS = RowShape<PER>::ROWS, WARPS = kGradWarps;
+    constexpr int ROWS = GradShape<PER>::ROWS, WARPS = kGradWarps;
     __shared__ int32_t kept[kCached];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int E = a.E, T = a.T, S = a.S;
@@ -547,11 +562,12 @@ __global__ void __launch_bounds__(32 * kGradWarps, kGradPerSm<PER>) balance_grad
             share[q] = e < E ? (float)a.counts[(int64_t)i * E + e] * inv_n : 0.0f;
         }
         for (int at = lo + warp * rows_per_warp; at < hi; at += WARPS * rows_per_warp * ROWS) {
-            float l[ROWS][PER], p[ROWS][PER], top[ROWS], total[ROWS], mean[ROWS], lse[ROWS];
+            float l[ROWS][PER], p[ROWS][PER], top[ROWS], total[ROWS], mean[ROWS], lse[ROWS], base[ROWS][PER];
 #pragma unroll
             for (int u = 0; u < ROWS; ++u) {
                 const int t = at + u * WARPS * rows_per_warp + group;
                 load_row<PER, VEC>(a.logits + (int64_t)t * E, t < hi, E, sub, lpr, -INFINITY, l[u]);
+                load_row<PER, VEC>(a.base + (int64_t)t * E, a.base != nullptr && t < hi, E, sub, lpr, 0.0f, base[u]);
                 lse[u] = 0.0f;
             }
             float d[ROWS][PER];
@@ -604,12 +620,8 @@ __global__ void __launch_bounds__(32 * kGradWarps, kGradPerSm<PER>) balance_grad
             for (int u = 0; u < ROWS; ++u) {
                 const int t = at + u * WARPS * rows_per_warp + group;
                 if (t >= hi) continue;
-                if (a.base) {
-                    float b[PER];
-                    load_row<PER, VEC>(a.base + (int64_t)t * E, true, E, sub, lpr, 0.0f, b);
 #pragma unroll
-                    for (int q = 0; q < PER; ++q) d[u][q] += b[q];
-                }
+                for (int q = 0; q < PER; ++q) d[u][q] += base[u][q];
                 store_row<PER, VEC>(a.out + (int64_t)t * E, E, sub, lpr, d[u]);
             }
         }
@@ -732,7 +744,7 @@ cudaError_t launch_balance_grad(const BalanceGradCall &c, int n_sm, cudaStream_t
         constexpr int PER = decltype(per)::value;
         constexpr bool VEC = decltype(vec)::value;
         const int64_t rows = kGradWarps * (PER > 4 ? 1 : 32 / a.lpr), fit = ceil_div(c.T, rows);
-        const int64_t most = (int64_t)n_sm * kGradPerSm<PER>, blocks = fit < most ? fit : most;
+        const int64_t most = (int64_t)n_sm * GradShape<PER>::PER_SM, blocks = fit < most ? fit : most;
         a.chunk = (int)ceil_div(c.T, blocks);
         cfg.blockDim = dim3(32 * kGradWarps);
         cfg.gridDim = dim3((unsigned)blocks);
