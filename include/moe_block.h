@@ -343,8 +343,8 @@ typedef struct moe_tensor {
  *                step out)
  *   grads     host array of `count` descriptors, read before the call returns
  *   max_norm  > 0; infinity for the norm alone
- * Squares are summed in FP32 per thread and in FP64 from there on, in an order
- * fixed by the tensors' sizes and the device.  A sum beyond FP32's range is
+ * Squares are summed in FP32 within a block and in FP64 over the blocks, in an
+ * order fixed by the tensors' sizes and the device.  A sum beyond FP32's range is
  * taken of the elements times 2^-64, so the norm holds up to FP32's largest;
  * elements below about 1e-22 count as zero.  Limits: count <= 65536, sum of n
  * <= 2^42.  Without elements the norm is 0 and the factor 1.  workspace: at

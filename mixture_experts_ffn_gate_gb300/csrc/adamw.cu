@@ -38,9 +38,9 @@ constexpr int kThreads = 256;
 constexpr int kBlock8 = 256;        // elements that share a scale: eight to a lane
 constexpr int kChunk = 4096;        // elements of a block of the step
 constexpr int kStepPerSm = 4;       // its blocks that an SM holds
-constexpr int kNormChunk = 4096;    // elements that a block of the norm takes at a time
-constexpr int kNormPerSm = 6;       // its blocks that an SM holds
-constexpr int kNormBlocks = 1024;   // its partial sums per launch, at most
+constexpr int kNormChunk = 8192;    // elements that a block of the norm takes at a time
+constexpr int kNormPerSm = 3;       // its blocks that an SM holds
+constexpr int kNormBlocks = 512;    // its partial sums per launch, at most
 constexpr float kTop = 448.0f;      // the largest E4M3 value
 constexpr float kLowest = 0.001953125f;  // the smallest, 2^-9
 constexpr float kShrink = 5.421010862427522e-20f;  // 2^-64
@@ -217,9 +217,9 @@ using NormBatchSmall = Batch<TensorRef, kSmallBatch>;
 // A block's sums of squares of its chunks: of the elements and of the
 // elements times 2^-64, which holds where the first one is beyond FP32.
 template <typename B>
-__global__ void __launch_bounds__(kThreads, kNormPerSm) grad_norm_kernel(const __grid_constant__ B b, double2 *partial)
+__global__ void __launch_bounds__(kThreads, kNormPerSm) grad_norm_kernel(const __grid_constant__ B b, float2 *partial)
 {
-    __shared__ double part[2][kThreads / 32];
+    __shared__ float2 part[kThreads / 32];
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
     float s[4] = {}, r[4] = {};
@@ -259,38 +259,39 @@ __global__ void __launch_bounds__(kThreads, kNormPerSm) grad_norm_kernel(const _
         else
             run((const __nv_bfloat16 *)b.t[k].data + at, left);
     }
-    double x = (double)((s[0] + s[1]) + (s[2] + s[3])), y = (double)((r[0] + r[1]) + (r[2] + r[3]));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        x += __shfl_xor_sync(0xffffffffu, x, o);
-        y += __shfl_xor_sync(0xffffffffu, y, o);
-    }
-    if ((threadIdx.x & 31) == 0) part[0][threadIdx.x >> 5] = x, part[1][threadIdx.x >> 5] = y;
+    const float x = warp_sum((s[0] + s[1]) + (s[2] + s[3])), y = warp_sum((r[0] + r[1]) + (r[2] + r[3]));
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) part[warp] = make_float2(x, y);
     __syncthreads();
-    if (threadIdx.x == 0) {
-        x = y = 0.0;
-        for (int w = 0; w < kThreads / 32; ++w) x += part[0][w], y += part[1][w];
-        partial[blockIdx.x] = make_double2(x, y);
+    if (warp == 0) {
+        const float2 v = lane < kThreads / 32 ? part[lane] : make_float2(0.0f, 0.0f);
+        const float2 sums = make_float2(warp_sum(v.x), warp_sum(v.y));
+        if (lane == 0) partial[blockIdx.x] = sums;
     }
 }
 
-__global__ void __launch_bounds__(kThreads) norm_factor_kernel(const double2 *partial, int n, float max_norm,
+__device__ __forceinline__ double warp_sum64(double v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+__global__ void __launch_bounds__(kThreads) norm_factor_kernel(const float2 *partial, int n, float max_norm,
                                                                float *out)
 {
-    __shared__ double part[2][kThreads / 32];
+    __shared__ double2 part[kThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     ptx::griddep_wait();
     double x = 0.0, y = 0.0;
-    for (int i = threadIdx.x; i < n; i += kThreads) x += partial[i].x, y += partial[i].y;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        x += __shfl_xor_sync(0xffffffffu, x, o);
-        y += __shfl_xor_sync(0xffffffffu, y, o);
-    }
-    if ((threadIdx.x & 31) == 0) part[0][threadIdx.x >> 5] = x, part[1][threadIdx.x >> 5] = y;
+    for (int i = threadIdx.x; i < n; i += kThreads) x += (double)partial[i].x, y += (double)partial[i].y;
+    x = warp_sum64(x), y = warp_sum64(y);
+    if (lane == 0) part[warp] = make_double2(x, y);
     __syncthreads();
-    if (threadIdx.x == 0) {
-        x = y = 0.0;
-        for (int w = 0; w < kThreads / 32; ++w) x += part[0][w], y += part[1][w];
+    if (warp > 0) return;
+    x = warp_sum64(lane < kThreads / 32 ? part[lane].x : 0.0);
+    y = warp_sum64(lane < kThreads / 32 ? part[lane].y : 0.0);
+    if (lane == 0) {
         const float norm = (float)(isinf(x) ? sqrt(y) * 18446744073709551616.0 : sqrt(x));
         out[0] = norm;
         out[1] = !isfinite(norm) ? NAN : norm > max_norm ? max_norm / norm : 1.0f;
@@ -551,7 +552,7 @@ cudaLaunchConfig_t early(cudaLaunchAttribute *attr, cudaStream_t s)
 size_t grad_norm_workspace_bytes(int64_t count)
 {
     const int64_t launches = count < 1 ? 1 : ceil_div(count, (int64_t)kNormBatch);
-    return (size_t)(launches * kNormBlocks) * sizeof(double2);
+    return (size_t)(launches * kNormBlocks) * sizeof(float2);
 }
 
 cudaError_t launch_grad_norm(const TensorRef *grads, int count, float max_norm, float *out, void *workspace, int n_sm,
@@ -559,7 +560,7 @@ cudaError_t launch_grad_norm(const TensorRef *grads, int count, float max_norm, 
 {
     cudaLaunchAttribute attr;
     cudaLaunchConfig_t cfg = early(&attr, s);
-    double2 *const partial = (double2 *)workspace;
+    float2 *const partial = (float2 *)workspace;
     int used = 0;
     auto launch = [&](const auto &b) {
         using B = std::remove_cv_t<std::remove_reference_t<decltype(b)>>;
@@ -574,7 +575,7 @@ cudaError_t launch_grad_norm(const TensorRef *grads, int count, float max_norm, 
                               : in_batches<NormBatch>(grads, count, kNormBatch, kNormChunk, launch);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(1);
-    return cudaLaunchKernelEx(&cfg, norm_factor_kernel, (const double2 *)partial, used, max_norm, out);
+    return cudaLaunchKernelEx(&cfg, norm_factor_kernel, (const float2 *)partial, used, max_norm, out);
 }
 
 cudaError_t launch_adamw(const AdamWTensor *tensors, int count, AdamWScalars sc, double beta1, double beta2,

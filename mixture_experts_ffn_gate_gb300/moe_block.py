@@ -660,7 +660,11 @@ class AdamWPlan:
             self.set_grads(grads)
 
     def set_grads(self, grads):
-        """The gradients of the steps from here on."""
+        """The gradients of the steps from here on, which the plan keeps; None
+        lets go of them."""
+        if grads is None:
+            self.grads = self._grad_list = None
+            return
         grads = list(grads)
         if len(grads) != len(self.weights):
             raise ValueError(f"grads: {len(grads)} for {len(self.weights)} weights")

@@ -260,3 +260,50 @@ def test_a_plan_refuses_what_does_not_fit(on_host):
 def test_an_empty_plan_does_nothing(mb):
     plan = mb.AdamWPlan([], [], grads=[])
     assert mb.moe_adamw_step(plan, 1) is None
+
+
+# ------------------------------------------------------------------ streams
+def test_calls_on_a_stream_allocate_there(monkeypatch, on_host):
+    """What a call makes for itself is allocated on the stream that the call
+    runs on, and its outputs also wait for the current stream's readers."""
+    from mixture_experts_ffn_gate_gb300 import moe_ffn as m
+    from tests.test_block_edges_cpu import Watch
+    mb = on_host
+    l, idx, w = torch.zeros(4, 8), torch.zeros(4, 2).int(), torch.zeros(64)
+    counts, off = torch.zeros(3, 8).int(), torch.zeros(4).int()
+    plan = mb.AdamWPlan([w], [mb.new_adamw_state(w)], grads=[w.clone()])
+    calls = [lambda **s: mb.moe_balance_loss_forward(l, idx, seq_offsets=off, **s),
+             lambda **s: [mb.moe_balance_loss_backward(l, counts, 2, seq_offsets=off, **s)],
+             lambda **s: [mb.moe_grad_norm(plan, **s)],
+             lambda **s: [mb.moe_adamw_step(plan, torch.zeros(1).int(), **s)]]
+    for call in calls:
+        with monkeypatch.context() as patch:
+            watch = Watch(patch)
+            patch.setattr(mb, "_here", lambda *a: None)
+            out = [t for t in call(stream=5) if t is not None]
+            assert watch.made and all(s == 5 for s, _ in watch.made)
+            for t in out:
+                assert any(t is kept and s.cuda_stream == 7 for s, kept in watch.kept)
+            assert m._lib is not None
+
+
+def test_tensors_of_other_devices_are_refused(monkeypatch, mb):
+    class On:
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    mb._here(On(0).device, On(0), None)
+    with pytest.raises(ValueError, match="current device"):
+        mb._here(On(1).device, On(1))
+    with pytest.raises(ValueError, match="on cuda:1 and on cuda:0"):
+        mb._here(On(0).device, On(1))
+
+
+def test_a_plan_lets_go_of_its_gradients(on_host):
+    mb, w = on_host, torch.zeros(16)
+    plan = mb.AdamWPlan([w], [mb.new_adamw_state(w)], grads=[w.clone()])
+    plan.set_grads(None)
+    assert plan.grads is None
+    with pytest.raises(ValueError, match="no gradients"):
+        mb.moe_adamw_step(plan, 1)
