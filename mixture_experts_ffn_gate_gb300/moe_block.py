@@ -9,6 +9,7 @@ fallback.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import functools
 import math
@@ -545,6 +546,10 @@ def _all_on(tensors, what):
     return devices.pop() if devices else None
 
 
+def _span(t):
+    return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+
+
 class GradList:
     """The gradients of a step, bf16 or f32, as moe_grad_norm takes them: made
     once for tensors that stay where they are."""
@@ -618,7 +623,9 @@ class AdamWPlan:
     which the weights are the rounding, and each weight's weight_decay and
     lr_factor (one number or a list).  Gradients (bf16 or f32, the weights'
     shapes) are given here or by set_grads; a captured step reads the ones
-    that it was captured with."""
+    that it was captured with.  The tensors keep their memory for as long as
+    the plan is used: a step whose weights have other memory (``w.data = ...``)
+    is refused, and takes a new plan."""
 
     def __init__(self, weights, states, masters=None, weight_decay=0.0, lr_factor=1.0, grads=None):
         self.weights, self.states = list(weights), [AdamWState(*s) for s in states]
@@ -652,8 +659,9 @@ class AdamWPlan:
             d.weight_decay, d.lr_factor = decay[i], factor[i]
             written += [w] + [t for _, t, _, _ in parts]
         self.device = _all_on(written, "weights and states")
-        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in written if t.numel())
-        if any(b[0] < a[1] for a, b in zip(spans, spans[1:])):
+        self._addresses = [w.data_ptr() for w in self.weights]
+        self._spans = sorted(_span(t) for t in written if t.numel())
+        if any(b[0] < a[1] for a, b in zip(self._spans, self._spans[1:])):
             raise ValueError("weights, masters and states must not overlap: each is updated once")
         self.grads = self._grad_list = None
         if grads is not None:
@@ -673,6 +681,10 @@ class AdamWPlan:
             _type(g, f"grads[{i}]")
             if g.device != self.device:
                 raise ValueError(f"grads[{i}] is on {g.device}, not on {self.device}")
+            start, end = _span(g)
+            at = bisect.bisect_left(self._spans, (end,))  # the spans from here on start behind it
+            if start < end and at and self._spans[at - 1][1] > start:
+                raise ValueError(f"grads[{i}] overlaps with a weight, master or state")
         for d, g in zip(self.array, grads):
             d.grad, d.grad_type = g.data_ptr(), _TYPES[g.dtype]
         self.grads, self._grad_list = grads, None
@@ -698,6 +710,8 @@ def moe_adamw_step(plan: AdamWPlan, step, lr=1e-3, betas=(0.9, 0.999), eps: floa
     dev = plan.device
     if dev is None:
         return
+    if [w.data_ptr() for w in plan.weights] != plan._addresses:
+        raise ValueError("a weight's memory is no longer the one that the plan was made for")
     counter = lr_at = None
     if isinstance(step, torch.Tensor):
         _is(step, (1,), torch.int32, "step")

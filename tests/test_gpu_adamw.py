@@ -378,6 +378,21 @@ def test_refusals_on_the_device():
     with pytest.raises(mb.MoeFfnError):  # an address that is no multiple of 16
         mb.moe_grad_norm([big[1:]])
     with pytest.raises(mb.MoeFfnError):
-        mb.moe_adamw_step(mb.AdamWPlan([big[1:]], [mb.new_adamw_state(big[1:])], grads=[big[1:]]), 1)
+        mb.moe_adamw_step(mb.AdamWPlan([big[1:]], [mb.new_adamw_state(big[1:])], grads=[torch.zeros_like(big[1:])]), 1)
     with pytest.raises(ValueError):
         mb.AdamWPlan([big[::2]], [mb.new_adamw_state(big[::2])])
+
+
+def test_more_than_32_bits_of_elements():
+    """The last elements of a tensor of 2^31 + 1000, 8-bit states, and its norm."""
+    n = (1 << 31) + 1000
+    w = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    g = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    s = mb.new_adamw_state(w, 8)
+    g[-1], g[-257], g[5] = 3.0, -4.0, 12.0
+    plan = mb.AdamWPlan([w], [s], grads=[g])
+    assert f64(mb.moe_grad_norm(plan, max_norm=INF))[0] == 13.0
+    mb.moe_adamw_step(plan, 1, lr=0.5, betas=(0.5, 0.5))
+    assert w[-1] == -0.5 and w[-257] == 0.5 and w[5] == -0.5
+    assert int((w != 0).sum()) == 3 and int((s.m.view(torch.uint8) != 0).sum()) == 3
+    assert s.m_scale[-1].item() * 448 == pytest.approx(1.5, rel=1e-6)

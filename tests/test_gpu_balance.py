@@ -292,3 +292,25 @@ def test_refusals_on_the_device():
         mb.moe_balance_loss_backward(l, c, 5)
     with pytest.raises(mb.MoeFfnError):
         mb.moe_balance_loss_forward(l, idx, coef=math.nan)
+
+
+def test_more_than_32_bits_of_logits():
+    """2^31 logits and some: the last rows' part in the counts, the loss and the gradient."""
+    E = 1024
+    T = (1 << 31) // E + 500
+    l = torch.zeros(T, E, device="cuda")
+    l[-1, 5] = 20.0
+    idx = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    idx[-3:] = 1000
+    off = torch.tensor([0, T - 2, T], dtype=torch.int32, device="cuda")
+    r = mb.moe_balance_loss_forward(l, idx, coef=1.0, seq_offsets=off)
+    assert r.counts[0, 0] == T - 3 and r.counts[0, 1000] == 1 and r.counts[1, 1000] == 2
+    p = torch.softmax(l[-1].double(), 0)
+    want = (p + 1 / E) / 2
+    assert ((r.prob[1].double() - want).abs() <= 200 * U * want).all()
+    d = mb.moe_balance_loss_backward(l, r.counts, 1, coef=1.0, seq_offsets=off)
+    a = torch.zeros(E, dtype=torch.float64, device="cuda")
+    a[1000] = E / T
+    want = p * (a - (a * p).sum())
+    assert ((d[-1].double() - want).abs() <= 200 * U * (p * (a + (a * p).sum()))).all()
+    assert torch.isfinite(d[:: 1 << 16]).all()

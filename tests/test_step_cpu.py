@@ -307,3 +307,20 @@ def test_a_plan_lets_go_of_its_gradients(on_host):
     assert plan.grads is None
     with pytest.raises(ValueError, match="no gradients"):
         mb.moe_adamw_step(plan, 1)
+
+
+def test_a_plan_refuses_gradients_that_it_would_write_to_and_moved_weights(on_host):
+    mb = on_host
+    both = torch.zeros(1024)
+    w, s = both[256:512], mb.new_adamw_state(both[256:512])
+    plan = mb.AdamWPlan([w], [s])
+    plan.set_grads([both[512:768]])
+    plan.set_grads([both[:256]])
+    for g in (w, both[500:756], both[1:257], s.m, s.v):
+        with pytest.raises(ValueError, match="overlaps"):
+            plan.set_grads([g])
+    free = torch.zeros(256)
+    plan = mb.AdamWPlan([free], [mb.new_adamw_state(free)], grads=[torch.zeros(256)])
+    free.data = torch.zeros(256)
+    with pytest.raises(ValueError, match="no longer"):
+        mb.moe_adamw_step(plan, 1)
