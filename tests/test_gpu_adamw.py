@@ -396,3 +396,31 @@ def test_more_than_32_bits_of_elements():
     assert w[-1] == -0.5 and w[-257] == 0.5 and w[5] == -0.5
     assert int((w != 0).sum()) == 3 and int((s.m.view(torch.uint8) != 0).sum()) == 3
     assert s.m_scale[-1].item() * 448 == pytest.approx(1.5, rel=1e-6)
+
+
+@pytest.mark.parametrize("g", ["f32", "bf16"])
+@pytest.mark.parametrize("factor", [None, 0.37])
+def test_codes_are_those_of_the_formula_in_fp32(g, factor):
+    """Operation by operation in torch, each rounded once; the quotient by the
+    scale is the rounded one (torch's division)."""
+    n = 1 << 22
+    w, s, _, grad = make(n, "f32", g, False, 8)
+    top = 1.0 / 448.0
+
+    def quantised(x, up):
+        blocks = x.view(-1, 256)
+        scale = (blocks.abs().amax(1) * torch.tensor(top, device="cuda")).clamp_min(2.0 ** -126)
+        q = blocks / scale[:, None]
+        if up:
+            q = torch.where(blocks > 0, q.clamp_min(2.0 ** -9), q)
+        return q.clamp(-448, 448).to(torch.float8_e4m3fn).view(-1).view(torch.uint8), scale
+    gf = grad.float() if factor is None else grad.float() * torch.tensor(factor, device="cuda")
+    m = s.m.float() * s.m_scale.repeat_interleave(256)
+    v = (s.v.float() * s.v_scale.repeat_interleave(256)).square()
+    b1, a1, b2, a2 = (torch.tensor(x, dtype=torch.float32, device="cuda") for x in (0.9, 1 - 0.9, 0.95, 1 - 0.95))
+    want = [*quantised(b1 * m + a1 * gf, False), *quantised((b2 * v + (a2 * gf) * gf).sqrt(), True)]
+    plan = mb.AdamWPlan([w], [s], grads=[grad])
+    mb.moe_adamw_step(plan, 9, grad_scale=None if factor is None else torch.tensor([factor], device="cuda"), **HOW)
+    got = [s.m.view(torch.uint8), s.m_scale, s.v.view(torch.uint8), s.v_scale]
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
