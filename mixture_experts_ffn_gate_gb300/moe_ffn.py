@@ -43,7 +43,8 @@ EXPORTED = ["moe_ffn_forward", "moe_ffn_workspace_bytes", "moe_ffn_forward_ex",
             "moe_rms_norm_forward", "moe_rms_norm_backward_workspace_bytes", "moe_rms_norm_backward",
             "moe_gate_forward", "moe_gate_backward", "moe_ffn_routed_workspace_bytes", "moe_ffn_forward_routed",
             "moe_ffn_routed_backward_workspace_bytes", "moe_ffn_backward_routed", "moe_ffn_forward_routed_train", "moe_orthogonalize_workspace_bytes",
-            "moe_orthogonalize"]
+            "moe_orthogonalize", "moe_balance_loss_workspace_bytes", "moe_balance_loss_forward",
+            "moe_balance_loss_backward", "moe_grad_norm_workspace_bytes", "moe_grad_norm", "moe_adamw_step"]
 
 # Size of the library's fixed scratch array used by moe_ffn_forward_noalloc.
 MOE_FFN_NOALLOC_SCRATCH_BYTES = 16 << 20
