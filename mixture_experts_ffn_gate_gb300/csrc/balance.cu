@@ -37,9 +37,13 @@ namespace {
 constexpr int kMostChunks = 512;   // blocks of the first kernel
 constexpr int kLeastRows = 64;     // and their rows, where there are several
 constexpr int kCached = 1024;      // offsets that a block keeps in shared memory
-// up to this many rows and sequences run as one block, which adds nothing up
-// afterwards: one launch less
-constexpr int kOneBlockRows = 64;
+// A call whose rows take one block's warps up to so many turns, in up to so
+// many sequences, runs as one block, which ends it by itself.  One block and
+// two kernels, us: 256 x 128 6.7 and 7.0, 512 x 128 10.5 and 7.4; 128 x 256 5.7
+// and 7.6, 256 x 256 8.4 and 7.6; 32 x 1000 6.4 and 8.3, 64 x 1000 9.6 and 9.8;
+// 256 x 16 4.6 and 7.4, 1024 x 16 8.6 and 7.6; 64 x 16 in two sequences 6.9 and
+// 9.6, in four 10.5 and 10.7, in eight 17 and 13.  One launch less on the host.
+constexpr int kOneBlockTurns = 4, kOneBlockRows = 512, kOneBlockSequences = 3;
 
 // Warps per block and rows of a warp in flight, by what the registers hold
 // with two blocks on an SM.  Few large blocks: every one adds a slot that the
@@ -345,8 +349,16 @@ __global__ void __launch_bounds__(RowShape<PER>::THREADS, kPerSm) balance_kernel
             fetch(at + step, next);
             next_slot = load_slot(a.idx, at + step, min(at + step + own, hi), lane, a.k, a.kp);
             count_slots(slot, E, lane, a.kp, hist);
-            for (int r = 32 / a.kp; r < own; r += 32 / a.kp)  // more rows than a warp has lanes for their slots
-                count_slots(load_slot(a.idx, at + r, min(at + own, hi), lane, a.k, a.kp), E, lane, a.kp, hist);
+            // more rows than a warp has lanes for their slots
+            const int at_once = 32 / a.kp;
+            for (int r = at_once; r < own; r += 4 * at_once) {
+                int more[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    more[u] = load_slot(a.idx, at + r + u * at_once, min(at + own, hi), lane, a.k, a.kp);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) count_slots(more[u], E, lane, a.kp, hist);
+            }
             slot = next_slot;
             if constexpr (KIND != kSigmoid) {
                 float e[ROWS][PER];
@@ -379,7 +391,10 @@ __global__ void __launch_bounds__(RowShape<PER>::THREADS, kPerSm) balance_kernel
                 if (e < E) warp_sums[warp][e] = sum[q];
             }
         }
-        z = a.z_coef != 0.0f ? sum_of_block(z, part, WARPS) : 0.0f;
+        if (a.z_coef != 0.0f) {
+            z = warp_sum(z);
+            if (lane == 0) part[warp] = z;
+        }
         __syncthreads();
         const int64_t place = (int64_t)blockIdx.x + i;
         const float inv_n = 1.0f / (float)(hi - lo);
@@ -397,10 +412,13 @@ __global__ void __launch_bounds__(RowShape<PER>::THREADS, kPerSm) balance_kernel
                 a.cnts[place * E + e] = hist[e];
             }
         }
-        if (alone)
-            z_total += z;
-        else if (threadIdx.x == 0)
-            a.zs[place] = z;
+        if (a.z_coef != 0.0f && warp == 0) {
+            z = warp_sum(lane < WARPS ? part[lane] : 0.0f);
+            if (alone)
+                z_total += z;
+            else if (lane == 0)
+                a.zs[place] = z;
+        }
         __syncthreads();  // the sums and counts are read before the next sequence's
     }
     if (alone) {
@@ -442,6 +460,8 @@ __global__ void __launch_bounds__(1024) balance_sum_kernel(const BalanceArgs a)
         int32_t c = 0;
         if (n > 0) {
             const int first = lo / a.chunk, end = (hi - 1) / a.chunk;
+            if (blockIdx.x == 0 && a.z_coef != 0.0f)
+                for (int b = first + (int)threadIdx.x; b <= end; b += blockDim.x) z += a.zs[(int64_t)b + i];
             if (e < E)
                 for (int b = first + y; b <= end; b += depth * FLIGHT) {
                     float v[FLIGHT];
@@ -456,34 +476,27 @@ __global__ void __launch_bounds__(1024) balance_sum_kernel(const BalanceArgs a)
 #pragma unroll
                     for (int u = 0; u < FLIGHT; ++u) s += v[u], c += many[u];
                 }
-            if (blockIdx.x == 0 && a.z_coef != 0.0f)
-                for (int b = first + (int)threadIdx.x; b <= end; b += blockDim.x) z += a.zs[(int64_t)b + i];
         }
         sums[y][lane] = s;
         cnts[y][lane] = c;
-        if (blockIdx.x == 0 && a.z_coef != 0.0f)
-            z = sum_of_block(z, part, depth);  // has barriers
-        else
-            __syncthreads();
-        // a warp adds up 32 / depth experts, lane w what warp w had
-        const int per_warp = 32 / depth;
-        float term = 0.0f;
-        for (int j = y * per_warp; j < (y + 1) * per_warp; ++j) {
-            s = warp_sum(lane < depth ? sums[lane][j] : 0.0f);
-            c = __reduce_add_sync(0xffffffffu, lane < depth ? cnts[lane][j] : 0);
-            s = n > 0 ? s / (float)n : 0.0f;
-            if (lane == 0 && blockIdx.x * 32 + j < E) {
-                a.prob[(int64_t)i * E + blockIdx.x * 32 + j] = s;
-                a.counts[(int64_t)i * E + blockIdx.x * 32 + j] = c;
-            }
-            term = fmaf((float)c, s, term);
-        }
-        if (lane == 0) terms[y] = term;
+        z = warp_sum(z);
+        if (lane == 0) part[y] = z;
         __syncthreads();
         if (y == 0) {
-            term = warp_sum(lane < depth ? terms[lane] : 0.0f);
+            s = 0.0f;
+            c = 0;
+#pragma unroll 8
+            for (int w = 0; w < depth; ++w) s += sums[w][lane], c += cnts[w][lane];
+            s = n > 0 ? s / (float)n : 0.0f;
+            if (e < E) {
+                a.prob[(int64_t)i * E + e] = s;
+                a.counts[(int64_t)i * E + e] = c;
+            }
+            const float term = warp_sum((float)c * s);
+            z = warp_sum(lane < depth ? part[lane] : 0.0f);
             if (lane == 0) a.parts[(int64_t)i * gridDim.x + blockIdx.x] = make_float2(term, z);
         }
+        __syncthreads();
     }
     // thread 0 wrote the block's parts, and its addition to the ticket releases
     // them to the block whose addition is the last
@@ -663,9 +676,12 @@ cudaError_t with_row(int E, bool sigmoid, bool z, F f)
     return !sigmoid ? with_vec<kSoftmax>(E, f) : z ? with_vec<kSigmoidAndZ>(E, f) : with_vec<kSigmoid>(E, f);
 }
 
-int most_chunks(int64_t T)
+// Blocks of the first kernel: of kLeastRows rows, or as many as there are
+// sequences (a block goes through the sequences of its rows one by one).
+int most_chunks(int64_t T, int64_t S)
 {
-    const int64_t c = ceil_div(T, kLeastRows);
+    int64_t c = ceil_div(T, kLeastRows);
+    if (c < S) c = S < T ? S : T;
     return (int)(c < 1 ? 1 : c < kMostChunks ? c : kMostChunks);
 }
 
@@ -676,7 +692,7 @@ struct Places {
 
 Places places(int64_t T, int64_t S, int64_t E)
 {
-    const int64_t slots = most_chunks(T) + S;
+    const int64_t slots = most_chunks(T, S) + S;
     Places p;
     p.sums = 256;  // the ticket before them
     p.cnts = p.sums + round_up(slots * E * 4, 256);
@@ -704,13 +720,15 @@ cudaError_t launch_balance(const BalanceCall &c, void *workspace, int n_sm, cuda
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const bool alone = c.T <= kOneBlockRows && c.S <= kOneBlockRows;
+    bool alone = false;
     int blocks = 1;
     cudaError_t e = with_row(c.E, c.sigmoid, c.z_coef != 0.0f, [&](auto per, auto vec, auto kind) {
         constexpr int PER = decltype(per)::value;
         constexpr bool VEC = decltype(vec)::value;
+        const int turn = RowShape<PER>::WARPS * RowShape<PER>::ROWS * (PER > 4 ? 1 : 32 / a.lpr);
+        alone = c.S <= kOneBlockSequences && c.T <= kOneBlockRows && c.T <= (int64_t)turn * kOneBlockTurns;
         if (!alone) {
-            blocks = most_chunks(c.T);
+            blocks = most_chunks(c.T, c.S);
             if (blocks > n_sm * kPerSm) blocks = n_sm * kPerSm;
             if (blocks < 2) blocks = 2;  // one is the block that ends the call by itself
         }
