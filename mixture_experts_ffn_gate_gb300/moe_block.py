@@ -546,21 +546,30 @@ def _all_on(tensors, what):
     return devices.pop() if devices else None
 
 
+def _addresses(tensors):
+    return list(map(torch.Tensor.data_ptr, tensors))
+
+
 def _span(t):
     return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
 
 
 class GradList:
     """The gradients of a step, bf16 or f32, as moe_grad_norm takes them: made
-    once for tensors that stay where they are."""
+    once for tensors that keep their memory (others are refused then)."""
 
     def __init__(self, grads):
         self.grads = list(grads)
         for i, g in enumerate(self.grads):
             _is(g, tuple(g.shape), g.dtype, f"grads[{i}]")
         self.device = _all_on(self.grads, "grads")
+        self.addresses = _addresses(self.grads)
         self.array = (moe_tensor * len(self.grads))(
-            *(moe_tensor(g.data_ptr(), g.numel(), _type(g, "a gradient")) for g in self.grads))
+            *(moe_tensor(a, g.numel(), _type(g, "a gradient")) for a, g in zip(self.addresses, self.grads)))
+
+    def check(self):
+        if _addresses(self.grads) != self.addresses:
+            raise ValueError("a gradient's memory is no longer the one that it was given with")
 
 
 def moe_grad_norm_workspace_bytes(count) -> int:
@@ -578,7 +587,9 @@ def moe_grad_norm(grads, max_norm: float = math.inf, out=None, workspace=None, s
     number).  ``grads``: a list of tensors, a GradList or an AdamWPlan."""
     if isinstance(grads, AdamWPlan):
         grads = grads.grad_list()
-    elif not isinstance(grads, GradList):
+    if isinstance(grads, GradList):
+        grads.check()
+    else:
         grads = GradList(grads)
     n, dev = len(grads.grads), grads.device
     if dev is None:
@@ -624,8 +635,8 @@ class AdamWPlan:
     lr_factor (one number or a list).  Gradients (bf16 or f32, the weights'
     shapes) are given here or by set_grads; a captured step reads the ones
     that it was captured with.  The tensors keep their memory for as long as
-    the plan is used: a step whose weights have other memory (``w.data = ...``)
-    is refused, and takes a new plan."""
+    the plan is used: a step whose weights or gradients have other memory
+    (``w.data = ...``) is refused, and takes a new plan or set_grads."""
 
     def __init__(self, weights, states, masters=None, weight_decay=0.0, lr_factor=1.0, grads=None):
         self.weights, self.states = list(weights), [AdamWState(*s) for s in states]
@@ -659,7 +670,7 @@ class AdamWPlan:
             d.weight_decay, d.lr_factor = decay[i], factor[i]
             written += [w] + [t for _, t, _, _ in parts]
         self.device = _all_on(written, "weights and states")
-        self._addresses = [w.data_ptr() for w in self.weights]
+        self._weights_at = _addresses(self.weights)
         self._spans = sorted(_span(t) for t in written if t.numel())
         if any(b[0] < a[1] for a, b in zip(self._spans, self._spans[1:])):
             raise ValueError("weights, masters and states must not overlap: each is updated once")
@@ -674,6 +685,7 @@ class AdamWPlan:
             self.grads = self._grad_list = None
             return
         grads = list(grads)
+        addresses = []
         if len(grads) != len(self.weights):
             raise ValueError(f"grads: {len(grads)} for {len(self.weights)} weights")
         for i, (g, w) in enumerate(zip(grads, self.weights)):
@@ -685,9 +697,11 @@ class AdamWPlan:
             at = bisect.bisect_left(self._spans, (end,))  # the spans from here on start behind it
             if start < end and at and self._spans[at - 1][1] > start:
                 raise ValueError(f"grads[{i}] overlaps with a weight, master or state")
-        for d, g in zip(self.array, grads):
-            d.grad, d.grad_type = g.data_ptr(), _TYPES[g.dtype]
+            addresses.append(start)
+        for d, g, start in zip(self.array, grads, addresses):
+            d.grad, d.grad_type = start, _TYPES[g.dtype]
         self.grads, self._grad_list = grads, None
+        self._tensors, self._addresses = self.weights + grads, self._weights_at + addresses
 
     def grad_list(self) -> GradList:
         if self.grads is None:
@@ -710,8 +724,8 @@ def moe_adamw_step(plan: AdamWPlan, step, lr=1e-3, betas=(0.9, 0.999), eps: floa
     dev = plan.device
     if dev is None:
         return
-    if [w.data_ptr() for w in plan.weights] != plan._addresses:
-        raise ValueError("a weight's memory is no longer the one that the plan was made for")
+    if _addresses(plan._tensors) != plan._addresses:
+        raise ValueError("a weight's or gradient's memory is no longer the one that the plan was made for")
     counter = lr_at = None
     if isinstance(step, torch.Tensor):
         _is(step, (1,), torch.int32, "step")

@@ -321,6 +321,13 @@ def test_a_plan_refuses_gradients_that_it_would_write_to_and_moved_weights(on_ho
             plan.set_grads([g])
     free = torch.zeros(256)
     plan = mb.AdamWPlan([free], [mb.new_adamw_state(free)], grads=[torch.zeros(256)])
+    for t in (free, plan.grads[0]):
+        kept = t.data
+        t.data = torch.zeros(256)
+        with pytest.raises(ValueError, match="no longer"):
+            mb.moe_adamw_step(plan, 1)
+        t.data = kept
+    listed = mb.GradList([free])
     free.data = torch.zeros(256)
     with pytest.raises(ValueError, match="no longer"):
-        mb.moe_adamw_step(plan, 1)
+        mb.moe_grad_norm(listed)
