@@ -538,12 +538,11 @@ def moe_balance_loss_backward(logits, counts, k: int, score: str = "softmax", co
 STATE_BLOCK = 256   # elements that share a scale of an 8-bit state
 
 
-def _all_on(tensors, what):
+def _one_device(devices, what):
     """The one device of a list's tensors, None of an empty one."""
-    devices = {t.device for t in tensors}
     if len(devices) > 1:
         raise ValueError(f"{what} are on several devices: {sorted(map(str, devices))}")
-    return devices.pop() if devices else None
+    return next(iter(devices), None)
 
 
 def _addresses(tensors):
@@ -561,8 +560,9 @@ class GradList:
     def __init__(self, grads):
         self.grads = list(grads)
         for i, g in enumerate(self.grads):
-            _is(g, tuple(g.shape), g.dtype, f"grads[{i}]")
-        self.device = _all_on(self.grads, "grads")
+            if not (g.is_cuda and g.is_contiguous()):
+                _is(g, g.shape, g.dtype, f"grads[{i}]")
+        self.device = _one_device({g.device for g in self.grads}, "grads")
         self.addresses = _addresses(self.grads)
         self.array = (moe_tensor * len(self.grads))(
             *(moe_tensor(a, g.numel(), _type(g, "a gradient")) for a, g in zip(self.addresses, self.grads)))
@@ -647,31 +647,32 @@ class AdamWPlan:
                         ("lr_factor", factor)):
             if len(x) != n:
                 raise ValueError(f"{name}: {len(x)} for {n} weights")
-        self.array = (moe_adamw_tensor * n)()
-        written = []
-        for i, (w, s, master) in enumerate(zip(self.weights, self.states, self.masters)):
-            shape = tuple(w.shape)
-            _is(w, shape, w.dtype, f"weights[{i}]")
-            bits8 = s.m_scale is not None or s.v_scale is not None
-            kind = torch.float8_e4m3fn if bits8 else torch.float32
-            blocks = (-(-w.numel() // STATE_BLOCK),)
-            parts = [("m", s.m, shape, kind), ("v", s.v, shape, kind)]
-            if bits8:
-                if s.m_scale is None or s.v_scale is None:
-                    raise ValueError(f"states[{i}]: m_scale and v_scale go together")
-                parts += [("m_scale", s.m_scale, blocks, torch.float32), ("v_scale", s.v_scale, blocks, torch.float32)]
-            if master is not None:
-                parts.append(("master", master, shape, torch.float32))
-            d = self.array[i]
-            for name, t, size, dtype in parts:
-                _is(t, size, dtype, f"{name} of weights[{i}]")
-                setattr(d, name, t.data_ptr())
-            d.w, d.n, d.w_type, d.state_bits = w.data_ptr(), w.numel(), _type(w, f"weights[{i}]"), 8 if bits8 else 32
-            d.weight_decay, d.lr_factor = decay[i], factor[i]
-            written += [w] + [t for _, t, _, _ in parts]
-        self.device = _all_on(written, "weights and states")
+        rows, devices, spans = [], set(), []
+
+        def written(t, shape, dtype, name):  # its address, after the checks
+            if not (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
+                _is(t, shape, dtype, f"{name}[{len(rows)}]")
+            at = t.data_ptr()
+            devices.add(t.device)
+            spans.append((at, at + t.numel() * t.element_size()))
+            return at
+
+        for w, s, master, d, f in zip(self.weights, self.states, self.masters, decay, factor):
+            shape, elements, bits8 = w.shape, w.numel(), s.m_scale is not None or s.v_scale is not None
+            if bits8 and (s.m_scale is None or s.v_scale is None):
+                raise ValueError(f"states[{len(rows)}]: m_scale and v_scale go together")
+            kind, blocks = torch.float8_e4m3fn if bits8 else torch.float32, (-(-elements // STATE_BLOCK),)
+            rows.append(moe_adamw_tensor(
+                written(w, shape, w.dtype, "weights"),
+                None if master is None else written(master, shape, torch.float32, "masters"), None,
+                written(s.m, shape, kind, "m of weights"), written(s.v, shape, kind, "v of weights"),
+                written(s.m_scale, blocks, torch.float32, "m_scale of weights") if bits8 else None,
+                written(s.v_scale, blocks, torch.float32, "v_scale of weights") if bits8 else None,
+                elements, _type(w, f"weights[{len(rows)}]"), 0, 8 if bits8 else 32, f, d))
+        self.array = (moe_adamw_tensor * n)(*rows)
+        self.device = _one_device(devices, "weights and states")
         self._weights_at = _addresses(self.weights)
-        self._spans = sorted(_span(t) for t in written if t.numel())
+        self._spans = sorted(s for s in spans if s[0] < s[1])
         if any(b[0] < a[1] for a, b in zip(self._spans, self._spans[1:])):
             raise ValueError("weights, masters and states must not overlap: each is updated once")
         self.grads = self._grad_list = None
@@ -689,8 +690,9 @@ class AdamWPlan:
         if len(grads) != len(self.weights):
             raise ValueError(f"grads: {len(grads)} for {len(self.weights)} weights")
         for i, (g, w) in enumerate(zip(grads, self.weights)):
-            _is(g, tuple(w.shape), g.dtype, f"grads[{i}]")
-            _type(g, f"grads[{i}]")
+            if not (g.dtype in _TYPES and g.shape == w.shape and g.is_cuda and g.is_contiguous()):
+                _is(g, w.shape, g.dtype, f"grads[{i}]")
+                _type(g, f"grads[{i}]")
             if g.device != self.device:
                 raise ValueError(f"grads[{i}] is on {g.device}, not on {self.device}")
             start, end = _span(g)
