@@ -23,7 +23,8 @@
 // sum, the release to the block that ends last): 32 us in all.  Without the
 // hardware's exponentials the first kernel's instructions took longer than its
 // bytes; with the slots counted before the rows instead of between them it
-// waited for them (40 us).  8191 x 128: 10.2 us, of which the second kernel 5.5.
+// waited for them (40 us).  8191 x 128 with z: 10.2 us, of which the second
+// kernel 5.5.
 #include <type_traits>
 
 #include "common.cuh"
@@ -443,7 +444,9 @@ __device__ __forceinline__ unsigned add_acq_rel(unsigned *at, unsigned v)
 
 // The slots' sums: a block of 32 experts by blockDim.y for one sequence after
 // another; the block that ends last adds the loss's parts, in their order.
-__global__ void __launch_bounds__(1024) balance_sum_kernel(const BalanceArgs a)
+// (All of a warp's slots are loaded at once, which takes 64 registers: with the
+// 32 that two blocks of 1024 threads would leave, 0.5 to 1.4 us more.)
+__global__ void __launch_bounds__(1024, 1) balance_sum_kernel(const BalanceArgs a)
 {
     constexpr int FLIGHT = 10;
     __shared__ float sums[32][33], part[32], terms[32];
