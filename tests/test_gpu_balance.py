@@ -91,6 +91,17 @@ def test_sequences(kind, T, E, S, first, behind):
     run(T, E, 4, kind, z_coef=0.02, offsets=offsets_of(T, S, T, first, behind), seed=S, base=True)
 
 
+@pytest.mark.parametrize("T,E,S", [(512, 16, 0), (513, 16, 0), (256, 128, 0), (257, 128, 3), (128, 256, 3), (128, 256, 4),
+                                   (129, 256, 0), (32, 1000, 0), (33, 1000, 2), (48, 500, 3), (49, 500, 0), (511, 7, 3)])
+def test_where_one_block_becomes_several(T, E, S):
+    for kind in ("softmax", "sigmoid"):
+        run(T, E, min(E, 8), kind, z_coef=0.02, offsets=offsets_of(T, S, E, 1, 2), seed=T, base=True)
+
+
+def test_more_sequences_than_the_grid_is_deep():
+    run(3000, 8, 2, "sigmoid", z_coef=0.1, offsets=offsets_of(3000, 40000, 3, 5, 11), base=True)
+
+
 def test_thousands_of_rows():
     run(20000, 12, 3, "softmax", z_coef=0.01, offsets=offsets_of(20000, 6, 1, 17, 29), spread=3.0)
 

@@ -89,6 +89,27 @@ def test_codes_are_torchs():
     assert ref.to_codes(ties)[0][:5].tolist() == [448.0, 16.0, 20.0, 0.0, 2.0 ** -8]
 
 
+def test_slots_of_blocks_and_sequences_are_distinct():
+    """A block of rows that meets a sequence adds to the slot block + sequence:
+    distinct for every pair, below the number of blocks and sequences together,
+    and a sequence's are those from its first row's block to its last one's."""
+    r = np.random.default_rng(3)
+    for _ in range(200):
+        T, S, chunk = int(r.integers(1, 300)), int(r.integers(1, 80)), int(r.integers(1, 40))
+        off = np.concatenate(([0], np.sort(r.integers(0, T + 1, S))))
+        blocks, pairs = -(-T // chunk), set()
+        for b in range(blocks):
+            for i in range(S):
+                if max(off[i], b * chunk) < min(off[i + 1], (b + 1) * chunk):
+                    pairs.add((b, i))
+        slots = [b + i for b, i in pairs]
+        assert len(set(slots)) == len(slots) and all(s < blocks + S for s in slots)
+        for i in range(S):
+            mine = sorted(b for b, j in pairs if j == i)
+            want = list(range(off[i] // chunk, (off[i + 1] - 1) // chunk + 1)) if off[i] < off[i + 1] else []
+            assert mine == want
+
+
 # ------------------------------------------------------------------ refusals of the C entries
 def balance_opts(mb, **f):
     o = mb.moe_balance_opts(0, 1e-2, 0.0)
