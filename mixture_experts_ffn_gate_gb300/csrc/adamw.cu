@@ -12,9 +12,9 @@
 // every byte once, and DRAM bounds them (us, and the floor at the copy rate):
 // the norm of 1.5e8 FP32 gradients 88.7 (88.9); the step of as many BF16
 // weights with FP32 masters and gradients, FP32 states 645 (667); with BF16
-// gradients and 8-bit states 350 (357).  Where a step with 8-bit states moves
+// gradients and 8-bit states 353 (357).  Where a step with 8-bit states moves
 // few bytes, its instructions come near (BF16 weights and gradients without
-// masters 275, 223): 64 an element at first, of which the block maxima by
+// masters 279, 223): 64 an element at first, of which the block maxima by
 // shuffles, a full division and the chunks' bounds are gone.  Many small
 // tensors leave chunks part empty (192 of 501 to 261522 elements: 53, 45).
 //
@@ -321,21 +321,23 @@ __device__ __forceinline__ float reciprocal(float x)
 // What an element's update takes.
 struct Element {
     float b1, a1, b2, a2;  // the betas and 1 - them
-    float g_scale, decay, step, root, eps;
+    float g_scale, minus_decay, minus_step, root, eps;
 
     // m, v and w after the step; returns sqrt(v).  The moments' products and
     // sums are rounded one by one: an 8-bit code next to a tie goes by their
     // last bit, which then is the formula's in FP32 and not a contraction's.
     // The reciprocal's unit in the last place is small against w's (it is zero
     // where sqrt(v) is beyond 2^126, which takes gradients whose square is
-    // infinite).
+    // infinite).  The decay is subtracted with the step, and w rounded once: a
+    // factor 1 - lr wd would be rounded to 2^-24, which is a tenth of an lr wd
+    // of 1e-6.
     __device__ __forceinline__ float operator()(float g, float &m, float &v, float &w) const
     {
         g = __fmul_rn(g, g_scale);
         m = __fadd_rn(__fmul_rn(b1, m), __fmul_rn(a1, g));
         v = __fadd_rn(__fmul_rn(b2, v), __fmul_rn(__fmul_rn(a2, g), g));
         const float r = __fsqrt_rn(v);
-        w = fmaf(w, decay, -step * (m * reciprocal(fmaf(r, root, eps))));
+        w += fmaf(minus_decay, w, minus_step * (m * reciprocal(fmaf(r, root, eps))));
         return r;
     }
 };
@@ -418,10 +420,10 @@ __device__ __forceinline__ float scale_block(float (&x)[8], bool up)
 
 // 8-bit states: a warp takes 256 elements, a scale's block, eight to a lane.
 // The loads of its two blocks of a chunk come before the first one's work: with
-// one block at a time and bounds on every access 519 us where this takes 350.
+// one block at a time and bounds on every access 519 us where this takes 353.
 // Four blocks per SM leave 64 registers, which cost spills where weights and
-// gradients are FP32 (368 us; with three blocks 356) and bring more elsewhere
-// (350; 366).
+// gradients are FP32 (371 us; with three blocks 356) and bring more elsewhere
+// (353; 366).
 template <bool MASTER, bool FULL, typename W, typename G>
 __device__ __forceinline__ void step_chunk_8bit(const Chunk<W, G> &c, const Element &el)
 {
@@ -506,8 +508,8 @@ __global__ void __launch_bounds__(kThreads, kStepPerSm) adamw_kernel(const __gri
     const AdamWTensor &t = b.t[k];
     const int64_t at = (int64_t)(chunk - b.first[k]) * kChunk;
     const float lr = (sc.lr_at ? *sc.lr_at : sc.lr) * t.lr_factor;
-    const Element el{sc.beta1, sc.one_minus1, sc.beta2, sc.one_minus2, factor, fmaf(-lr, t.weight_decay, 1.0f),
-                     lr * corrections.x, corrections.y, sc.eps};
+    const Element el{sc.beta1, sc.one_minus1, sc.beta2, sc.one_minus2, factor, -lr * t.weight_decay,
+                     -lr * corrections.x, corrections.y, sc.eps};
     if (t.master)
         t.w_f32 ? step_grad<true, float>(t, at, el) : step_grad<true, __nv_bfloat16>(t, at, el);
     else

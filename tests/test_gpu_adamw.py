@@ -424,3 +424,19 @@ def test_codes_are_those_of_the_formula_in_fp32(g, factor):
     got = [s.m.view(torch.uint8), s.m_scale, s.v.view(torch.uint8), s.v_scale]
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_small_decay_is_not_rounded_away(bits):
+    """lr * weight_decay of 2e-6 over 50 steps with gradients of zero: what is
+    lost is w's own rounding, at random (half a unit a step at most, its sum's
+    spread sqrt(50) of it), and not the factor's."""
+    n = 1 << 16
+    w = (1 + torch.rand(n, generator=torch.Generator().manual_seed(1))).cuda()
+    w0 = w.double()
+    plan = mb.AdamWPlan([w], [mb.new_adamw_state(w, bits)], weight_decay=0.1, grads=[torch.zeros(n, device="cuda")])
+    for step in range(1, 51):
+        mb.moe_adamw_step(plan, step, lr=2e-5)
+    lost = ((w.double() / w0 - (1 - 2e-6) ** 50) / 1e-4)
+    # the mean over 2^16 elements; a step rounds off at most 2^-24 of w, 3% of the decay, both ways
+    assert abs(lost.mean().item()) <= 3e-3
