@@ -360,7 +360,9 @@ int moe_grad_norm(const moe_tensor *grads, int64_t count, float max_norm, float 
 /*
  * A tensor of an AdamW step: n elements, contiguous, all updated in place.
  *   w       w_type; with `master` (FP32, nullable) the master is the weight and
- *           w takes its rounding
+ *           w takes its rounding.  A BF16 weight without one is rounded to
+ *           nearest after every step: steps below 2^-9 of it can leave it as
+ *           it is
  *   grad    grad_type, read
  *   m, v    the moments: state_bits 32: FP32.  state_bits 8: E4M3 codes of
  *           m / m_scale and of sqrt(v) / v_scale, one FP32 scale per
@@ -406,6 +408,7 @@ typedef struct moe_adamw_opts {
  *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
  *   w = w - lr_i weight_decay w
  *         - lr_i (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
+ * w is rounded once, after both subtractions.
  *   tensors        host array of `count` descriptors, read before the call
  *                  returns.  What is written (w, master, m, v, scales) must not
  *                  overlap with anything else in the call; gradients may.
