@@ -635,8 +635,9 @@ class AdamWPlan:
     lr_factor (one number or a list).  Gradients (bf16 or f32, the weights'
     shapes) are given here or by set_grads; a captured step reads the ones
     that it was captured with.  The tensors keep their memory for as long as
-    the plan is used: a step whose weights or gradients have other memory
-    (``w.data = ...``) is refused, and takes a new plan or set_grads."""
+    the plan is used: a step of which a weight, master, moment, scale or
+    gradient has other memory (``w.data = ...``) is refused, and takes a new
+    plan or set_grads."""
 
     def __init__(self, weights, states, masters=None, weight_decay=0.0, lr_factor=1.0, grads=None):
         self.weights, self.states = list(weights), [AdamWState(*s) for s in states]
@@ -648,6 +649,7 @@ class AdamWPlan:
             if len(x) != n:
                 raise ValueError(f"{name}: {len(x)} for {n} weights")
         rows, devices, spans = [], set(), []
+        self._written = []  # all that a step writes, with the addresses that its descriptors have
 
         def written(t, shape, dtype, name):  # its address, after the checks
             if not (t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous()):
@@ -655,6 +657,7 @@ class AdamWPlan:
             at = t.data_ptr()
             devices.add(t.device)
             spans.append((at, at + t.numel() * t.element_size()))
+            self._written.append(t)
             return at
 
         for w, s, master, d, f in zip(self.weights, self.states, self.masters, decay, factor):
@@ -671,7 +674,7 @@ class AdamWPlan:
                 elements, _type(w, f"weights[{len(rows)}]"), 0, 8 if bits8 else 32, f, d))
         self.array = (moe_adamw_tensor * n)(*rows)
         self.device = _one_device(devices, "weights and states")
-        self._weights_at = _addresses(self.weights)
+        self._written_at = [s[0] for s in spans]
         self._spans = sorted(s for s in spans if s[0] < s[1])
         if any(b[0] < a[1] for a, b in zip(self._spans, self._spans[1:])):
             raise ValueError("weights, masters and states must not overlap: each is updated once")
@@ -703,7 +706,7 @@ class AdamWPlan:
         for d, g, start in zip(self.array, grads, addresses):
             d.grad, d.grad_type = start, _TYPES[g.dtype]
         self.grads, self._grad_list = grads, None
-        self._tensors, self._addresses = self.weights + grads, self._weights_at + addresses
+        self._tensors, self._addresses = self._written + grads, self._written_at + addresses
 
     def grad_list(self) -> GradList:
         if self.grads is None:
@@ -727,7 +730,8 @@ def moe_adamw_step(plan: AdamWPlan, step, lr=1e-3, betas=(0.9, 0.999), eps: floa
     if dev is None:
         return
     if _addresses(plan._tensors) != plan._addresses:
-        raise ValueError("a weight's or gradient's memory is no longer the one that the plan was made for")
+        raise ValueError("a tensor's memory is no longer the one that the plan was made for: "
+                         "weights, masters, states and gradients keep theirs")
     counter = lr_at = None
     if isinstance(step, torch.Tensor):
         _is(step, (1,), torch.int32, "step")

@@ -1,0 +1,56 @@
+"""Edges of the training step's operators on the host: plans whose tensors moved,
+calls without tensors, arguments that are tensors."""
+import pytest
+import torch
+
+from mixture_experts_ffn_gate_gb300 import moe_block as mb
+
+pytestmark = pytest.mark.cpu
+
+
+@pytest.fixture()
+def on_host(monkeypatch):
+    """The plan's checks but for the device, on host tensors."""
+    def check(t, shape, dtype, name):
+        if t.dtype is not dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+            raise ValueError(name)
+    monkeypatch.setattr(mb, "_is", check)
+
+
+class Library:
+    """In the library's place: notes the calls that reach it, with every argument."""
+
+    def __init__(self, monkeypatch):
+        self.calls = []
+        monkeypatch.setattr(mb, "_lib", lambda: self)
+        monkeypatch.setattr(mb, "_here", lambda *a: None)
+        monkeypatch.setattr(mb, "_stream", lambda *a: None)
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("what", ["w", "master", "grad", "m", "v", "m_scale", "v_scale"])
+def test_a_step_refuses_every_tensor_whose_memory_has_changed(monkeypatch, on_host, bits, what):
+    """The plan's descriptors have the old memory, which is free by then."""
+    if bits == 32 and "scale" in what:
+        return
+    library = Library(monkeypatch)
+    w, master, g = torch.zeros(300).bfloat16(), torch.zeros(300), torch.zeros(300)
+    s = mb.new_adamw_state(w, bits)
+    plan = mb.AdamWPlan([torch.zeros(8).bfloat16(), w], [mb.new_adamw_state(torch.zeros(8)), s], masters=[None, master],
+                        grads=[torch.zeros(8), g])
+    t = dict(w=w, master=master, grad=g, **s._asdict())[what]
+    mb.moe_adamw_step(plan, 1)
+    kept = t.data
+    t.data = t.detach().clone()
+    with pytest.raises(ValueError, match="no longer"):
+        mb.moe_adamw_step(plan, 2)
+    assert len(library.calls) == 1
+    t.data = kept
+    mb.moe_adamw_step(plan, 2)
+    assert [name for name, _ in library.calls] == ["moe_adamw_step"] * 2
