@@ -236,8 +236,14 @@ class GateOutput(NamedTuple):
     counts: torch.Tensor | None     # int32 [E]
 
 
-@functools.lru_cache(maxsize=64)
+# The structs of a few settings are kept by the settings' values: a tensor among
+# them is read at every call, since a cache would take it by its identity.
 def _gate_opts(score, renormalize, scale, groups=1, topk_groups=1):
+    return _kept_gate_opts(score, bool(renormalize), float(scale), int(groups), int(topk_groups))
+
+
+@functools.lru_cache(maxsize=64)
+def _kept_gate_opts(score, renormalize, scale, groups, topk_groups):
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
     if scale == 0.0:
@@ -455,8 +461,12 @@ def new_balance_workspace(T, E, S=1, device="cuda", stream=None):
     return _workspace(moe_balance_loss_workspace_bytes(T, S, E), device, stream, "workspace size")
 
 
-@functools.lru_cache(maxsize=64)
 def _balance_opts(score, coef, z_coef):
+    return _kept_balance_opts(score, float(coef), float(z_coef))
+
+
+@functools.lru_cache(maxsize=64)
+def _kept_balance_opts(score, coef, z_coef):
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
     return ctypes.byref(moe_balance_opts(_SCORES[score], coef, z_coef))

@@ -54,3 +54,19 @@ def test_a_step_refuses_every_tensor_whose_memory_has_changed(monkeypatch, on_ho
     t.data = kept
     mb.moe_adamw_step(plan, 2)
     assert [name for name, _ in library.calls] == ["moe_adamw_step"] * 2
+
+
+def test_settings_that_are_tensors_are_read_at_every_call():
+    """A coefficient that is annealed in place: the struct that the library
+    gets has its value, not the first call's."""
+    x = torch.tensor(0.5)
+    for value in (0.5, 0.25, 2.0):
+        x.fill_(value)
+        for coef, z_coef in ((x, 0.0), (0.0, x)):
+            o = mb._balance_opts("sigmoid", coef, z_coef)._obj
+            assert (o.coef, o.z_coef) == (float(coef), float(z_coef))
+        assert mb._gate_opts("softmax", True, x)._obj.scale == value
+    groups = torch.tensor(2)
+    for value in (2, 4):
+        groups.fill_(value)
+        assert mb._gate_opts("softmax", True, 1.0, groups, 1)._obj.groups == value
