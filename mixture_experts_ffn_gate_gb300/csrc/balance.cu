@@ -255,6 +255,25 @@ __device__ __forceinline__ void sigmoids(const float (&l)[ROWS][PER], int lpr, f
     row_sum(total, lpr);
 }
 
+// For the gradient: of q = 1 / (1 + exp(-l)) and 1 - q the one that is not above
+// a half, negative where that is 1 - q.  A difference of q from one would
+// lose it for large logits (17% of it at 15, all of it from 17 on).
+template <int PER, int ROWS>
+__device__ __forceinline__ void small_sides(const float (&l)[ROWS][PER], float (&side)[ROWS][PER])
+{
+#pragma unroll
+    for (int u = 0; u < ROWS; ++u)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const float x = power_of_2(-kLog2E * fabsf(l[u][i]));  // q / (1 - q) or its inverse
+            side[u][i] = copysignf(x * reciprocal(1.0f + x), -l[u][i]);
+        }
+}
+
+// q of such a side, and q (1 - q).
+__device__ __forceinline__ float sigmoid_of(float side) { return signbit(side) ? 1.0f + side : side; }
+__device__ __forceinline__ float slope_of(float side) { return fmaf(-side, side, fabsf(side)); }
+
 template <int PER, int ROWS>
 __device__ __forceinline__ void copy_rows(const float (&from)[ROWS][PER], float (&to)[ROWS][PER])
 {
@@ -536,7 +555,9 @@ __global__ void __launch_bounds__(1024, 1) balance_sum_kernel(const BalanceArgs 
 // at the copy rate 59.3), without one 45.1 (39.5); 100000 x 128, softmax and
 // z, 27.9 (22.6).  The incoming gradient loaded with the logits instead of
 // after them, and one row of a warp in flight instead of two: 34.7 to 27.9,
-// 65.7 to 64.7.
+// 65.7 to 64.7.  The sigmoid's smaller side and its sign instead of q alone:
+// 131072 x 256 as before, 100000 x 128 with z 33.1 to 35.3, 32768 x 1000 with an
+// incoming gradient 64.8 to 68.5 (these two are bound by instructions).
 template <int PER, bool VEC, Kind KIND>
 __global__ void __launch_bounds__(32 * kGradWarps, GradShape<PER>::PER_SM) balance_grad_kernel(const BalanceGradArgs a)
 {
@@ -601,13 +622,18 @@ __global__ void __launch_bounds__(32 * kGradWarps, GradShape<PER>::PER_SM) balan
                 }
             }
             if constexpr (KIND != kSoftmax) {
-                sigmoids<PER, ROWS>(l, lpr, p, total);
+                small_sides<PER, ROWS>(l, p);
 #pragma unroll
                 for (int u = 0; u < ROWS; ++u) {
-                    mean[u] = 0.0f;
+                    mean[u] = total[u] = 0.0f;
 #pragma unroll
-                    for (int q = 0; q < PER; ++q) mean[u] = fmaf(share[q], p[u][q], mean[u]);
+                    for (int q = 0; q < PER; ++q) {
+                        const float s = sigmoid_of(p[u][q]);
+                        total[u] += s;
+                        mean[u] = fmaf(share[q], s, mean[u]);
+                    }
                 }
+                row_sum(total, lpr);
                 row_sum(mean, lpr);
 #pragma unroll
                 for (int u = 0; u < ROWS; ++u) {
@@ -615,7 +641,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, GradShape<PER>::PER_SM) balan
                     mean[u] *= inv;
 #pragma unroll
                     for (int q = 0; q < PER; ++q) {
-                        const float g = (share[q] - mean[u]) * inv * (p[u][q] * (1.0f - p[u][q]));
+                        const float g = (share[q] - mean[u]) * inv * slope_of(p[u][q]);
                         d[u][q] = KIND == kSigmoidAndZ ? d[u][q] + g : g;
                     }
                 }
