@@ -57,6 +57,10 @@ struct RowShape {
     static constexpr int ROWS = PER <= 4 ? 4 : PER <= 8 ? 2 : 1;
 };
 
+// Blocks and warps of the second kernel that an SM holds (10 KB of shared memory
+// a block, 64 registers a thread).
+constexpr int kSumBlocksPerSm = 20, kSumWarpsPerSm = 32;
+
 // The gradient's blocks add nothing up and are smaller; a warp has fewer rows
 // in flight, for each brings the incoming gradient along.
 constexpr int kGradWarps = 8;
@@ -80,7 +84,7 @@ struct BalanceArgs {
     // per slot: [E] sums, [E] counts, one sum of lse^2
     float *sums, *zs;
     int32_t *cnts;
-    float2 *parts;  // [S][tiles]: the loss's two sums
+    float2 *parts;  // [blocks of the second kernel]: the loss's two sums
     unsigned *ticket;
 };
 
@@ -461,10 +465,26 @@ __device__ __forceinline__ unsigned add_acq_rel(unsigned *at, unsigned v)
     return old;
 }
 
-// The slots' sums: a block of 32 experts by blockDim.y for one sequence after
-// another; the block that ends last adds the loss's parts, in their order.
-// (All of a warp's slots are loaded at once, which takes 64 registers: with the
-// 32 that two blocks of 1024 threads would leave, 0.5 to 1.4 us more.)
+// A sum that keeps what its additions round off (Kahan, Commun. ACM 8, 1965), so
+// that its error does not grow with their number.
+struct Sum {
+    float sum = 0.0f, lost = 0.0f;
+
+    __device__ __forceinline__ void add(float v)
+    {
+        const float y = v - lost, t = sum + y;
+        lost = isinf(t) ? 0.0f : (t - sum) - y;
+        sum = t;
+    }
+};
+
+// The slots' sums: a block of 32 experts by depth warps for one sequence after
+// another, whose parts of the loss it adds up; the block that ends last adds the
+// blocks' parts, in their order.  The blocks are at most as many as the device
+// holds at once, so no lane's sum there grows with the sequences (8191 x 256 in
+// 4096 of them: 150 us with a block for each and every part in one warp's sums,
+// 74 so).  All of a warp's slots are loaded at once, which takes 64 registers:
+// with the 32 that two blocks of 1024 threads would leave, 0.5 to 1.4 us more.
 __global__ void __launch_bounds__(1024, 1) balance_sum_kernel(const BalanceArgs a)
 {
     constexpr int FLIGHT = 10;
@@ -476,6 +496,7 @@ __global__ void __launch_bounds__(1024, 1) balance_sum_kernel(const BalanceArgs 
     ptx::griddep_wait();
     auto offset = [&](int i) { return a.offsets ? clamp_row(a.offsets[i], T) : i ? T : 0; };
     const float rows = (float)max(offset(S) - offset(0), 0);
+    Sum my_balance, my_z;  // thread 0's: the block's parts
     for (int i = blockIdx.y; i < S; i += gridDim.y) {
         const int lo = offset(i), hi = offset(i + 1), n = max(hi - lo, 0);
         float s = 0.0f, z = 0.0f;
@@ -516,23 +537,28 @@ __global__ void __launch_bounds__(1024, 1) balance_sum_kernel(const BalanceArgs 
             }
             const float term = warp_sum((float)c * s);
             z = warp_sum(lane < depth ? part[lane] : 0.0f);
-            if (lane == 0) a.parts[(int64_t)i * gridDim.x + blockIdx.x] = make_float2(term, z);
+            my_balance.add(term);
+            my_z.add(z);
         }
         __syncthreads();
     }
+    const int blocks = gridDim.x * gridDim.y;
+    if (threadIdx.x == 0) a.parts[blockIdx.y * gridDim.x + blockIdx.x] = make_float2(my_balance.sum, my_z.sum);
     // thread 0 wrote the block's parts, and its addition to the ticket releases
     // them to the block whose addition is the last
-    if (threadIdx.x == 0) last = add_acq_rel(a.ticket, 1u) == gridDim.x * gridDim.y - 1;
+    if (threadIdx.x == 0) last = add_acq_rel(a.ticket, 1u) == (unsigned)blocks - 1;
     __syncthreads();
     if (!last) return;
-    float balance = 0.0f, z = 0.0f;
-    for (int64_t j = threadIdx.x; j < (int64_t)S * gridDim.x; j += blockDim.x) {
-        const float2 v = __ldcg(a.parts + j);
-        balance += v.x;
-        z += v.y;
-    }
-    balance = warp_sum(balance);
-    z = warp_sum(z);
+    float b4[4] = {}, z4[4] = {};
+    for (int j = threadIdx.x; j < blocks; j += 4 * blockDim.x)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int at = j + u * blockDim.x;
+            const float2 v = at < blocks ? __ldcg(a.parts + at) : make_float2(0.0f, 0.0f);
+            b4[u] += v.x;
+            z4[u] += v.y;
+        }
+    float balance = warp_sum((b4[0] + b4[1]) + (b4[2] + b4[3])), z = warp_sum((z4[0] + z4[1]) + (z4[2] + z4[3]));
     if (lane == 0) terms[y] = balance, part[y] = z;
     __syncthreads();
     if (y == 0) {
@@ -771,7 +797,10 @@ cudaError_t launch_balance(const BalanceCall &c, void *workspace, int n_sm, cuda
     // a warp takes a few of a sequence's slots, all at once
     int depth = 1;
     while (depth < 32 && 4 * depth * c.S < blocks + c.S) depth <<= 1;
-    cfg.gridDim = dim3((unsigned)ceil_div(c.E, 32), (unsigned)(c.S < 32768 ? c.S : 32768));
+    const int64_t tiles = ceil_div(c.E, 32), per_sm = kSumWarpsPerSm / depth;
+    const int64_t resident = n_sm * (per_sm < kSumBlocksPerSm ? per_sm : kSumBlocksPerSm);
+    const int64_t most = resident > tiles ? resident / tiles : 1;
+    cfg.gridDim = dim3((unsigned)tiles, (unsigned)(c.S < most ? c.S : most));
     cfg.blockDim = dim3(32 * depth);
     return cudaLaunchKernelEx(&cfg, balance_sum_kernel, (const BalanceArgs)a);
 }
