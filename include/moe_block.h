@@ -368,7 +368,7 @@ int moe_grad_norm(const moe_tensor *grads, int64_t count, float max_norm, float 
  *           m / m_scale and of sqrt(v) / v_scale, one FP32 scale per
  *           MOE_ADAMW_STATE_BLOCK elements (the last block may be shorter):
  *           the block's largest magnitude / 448, at least 2^-126.  Codes are
- *           rounded to nearest, ties to even, but a v above zero takes at
+ *           rounded as state_rounding says, but a v above zero takes at
  *           least the lowest code.  The step computes with the values before
  *           they are rounded.  Zeros (of codes and scales) are the initial
  *           state.  A NaN stays with its element, an infinity makes its block
@@ -399,8 +399,28 @@ typedef struct moe_adamw_opts {
     double beta2;
     double eps;   /* >= 0 */
     int64_t step; /* this step's number, from 1 (ignored with step_i32) */
-    int64_t reserved[3]; /* must be zero */
+    int32_t state_rounding; /* MOE_ADAMW_ROUND_*, of 8-bit states' codes */
+    int32_t reserved[5]; /* must be zero */
 } moe_adamw_opts;
+
+/*
+ * How the codes of 8-bit states are rounded.
+ *   NEAREST  ties to even.  A code stays where it is while a step changes its
+ *            value by less than 3 to 6% of it: moments whose betas are close to 1
+ *            stop following their gradients (sqrt(v) 3.4 times too large, for
+ *            good, where gradients fall fourfold beside others that do not, with
+ *            beta2 = 0.999).  It bears betas up to 0.95, where sqrt(v) is off by
+ *            10% rms; a moment without any noise in its gradients can stop there too.
+ *   RANDOM   to one of the two codes next to the value, the nearer one the
+ *            likelier, so that the mean is the value whatever the betas (16% rms
+ *            at beta2 = 0.999).  What is drawn depends on the step's number, the
+ *            tensor's place in the list and the element's alone: the same step
+ *            gives the same bits again.
+ *   AUTO     NEAREST where both betas are at most 0.95, else RANDOM
+ */
+#define MOE_ADAMW_ROUND_AUTO 0
+#define MOE_ADAMW_ROUND_NEAREST 1
+#define MOE_ADAMW_ROUND_RANDOM 2
 
 /*
  * One AdamW step of many tensors:

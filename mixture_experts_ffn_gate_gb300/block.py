@@ -175,15 +175,16 @@ class MoeBlock:
 class BlockAdamW:
     """AdamW for a block, its gradients clipped by their common norm: the norm
     and router weights with 32-bit states, and the experts' with FP32 masters
-    and states in ``bits`` (8 or 32), or orthogonalised updates for them
-    (``bits`` None).  Weight decay is the matrices' alone.  Steps whose
-    gradients' norm is no finite number are left out (with orthogonalised
-    updates the experts' are not).  The step's number and the learning rate
-    are kept on the device, so a step may be captured into a CUDA graph."""
+    and states in ``bits`` (8 or 32; their ``rounding`` as moe_adamw_step's), or
+    orthogonalised updates for them (``bits`` None).  Weight decay is the
+    matrices' alone.  Steps whose gradients' norm is no finite number are left
+    out (with orthogonalised updates the experts' are not).  The step's number
+    and the learning rate are kept on the device, so a step may be captured into
+    a CUDA graph."""
 
     def __init__(self, block: MoeBlock, lr: float = 1e-3, betas=(0.9, 0.95), eps: float = 1e-8,
-                 weight_decay: float = 0.1, max_norm: float = 1.0, bits: int | None = 8):
-        self.block, self.betas, self.eps, self.max_norm = block, betas, eps, max_norm
+                 weight_decay: float = 0.1, max_norm: float = 1.0, bits: int | None = 8, rounding: str = "auto"):
+        self.block, self.betas, self.eps, self.max_norm, self.rounding = block, betas, eps, max_norm, rounding
         self.names = ["norm_weight", "w_router"] + (["w_gate_up", "w_down"] if bits else [])
         weights = [getattr(block, n) for n in self.names]
         self.plan = mb.AdamWPlan(
@@ -200,7 +201,8 @@ class BlockAdamW:
         self.plan.set_grads([grads[n] for n in self.names])
         clip = mb.moe_grad_norm([grads[n] for n in ("norm_weight", "w_router", "w_gate_up", "w_down")],
                                 max_norm=self.max_norm)
-        mb.moe_adamw_step(self.plan, self.step_count, lr=self.lr, betas=self.betas, eps=self.eps, grad_scale=clip[1:])
+        mb.moe_adamw_step(self.plan, self.step_count, lr=self.lr, betas=self.betas, eps=self.eps, grad_scale=clip[1:],
+                          rounding=self.rounding)
         self.plan.set_grads(None)
         if "w_down" not in self.names:
             self.block.update_experts(grads, experts_lr)

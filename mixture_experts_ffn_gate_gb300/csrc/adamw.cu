@@ -25,7 +25,11 @@
 // times the scale exactly: elements that get no gradient decay by the factor
 // b1 or b2 through it, where a rounded scale would hold them where they are.
 // sqrt(v) needs half of v's range, and one that is not zero takes at least
-// the lowest code, so that no m is divided by eps alone.
+// the lowest code, so that no m is divided by eps alone.  Codes are rounded to
+// nearest, or at random where the betas are so close to 1 that a step changes a
+// moment by less than half of its code's spacing and nearest would hold it where
+// it is.  The numbers drawn cost instructions: BF16 weights with masters and BF16
+// gradients 411 us (355 to nearest), without masters 381 (280), all FP32 424 (370).
 #include <math.h>
 
 #include <type_traits>
@@ -50,6 +54,7 @@ constexpr int kNormPerSm = 3;       // its blocks that an SM holds
 constexpr int kNormBlocks = 512;    // its partial sums per launch, at most
 constexpr float kTop = 448.0f;      // the largest E4M3 value
 constexpr float kLowest = 0.001953125f;  // the smallest, 2^-9
+constexpr float kNormal = 0.015625f;     // the smallest with a full mantissa, 2^-6
 constexpr float kShrink = 5.421010862427522e-20f;  // 2^-64
 
 // The tensors of one launch; first[i] is the chunks before tensor i.
@@ -397,6 +402,37 @@ __device__ __forceinline__ void step_chunk(const Chunk<W, G> &c, const Element &
     }
 }
 
+// Numbers drawn for a lane's elements, from the step, the tensor and the
+// element's place alone: a hash of those (multiplications by odd fractions of
+// square roots and the golden ratio, with shifts), then one linear congruential
+// step (Knuth, The Art of Computer Programming 2, 3.3.4) per number, whose upper
+// 20 bits are taken.
+struct Draws {
+    uint32_t x;
+
+    static __device__ __forceinline__ uint32_t mix(uint32_t h)
+    {
+        h = (h ^ (h >> 16)) * 0x9e3779b9u;
+        h = (h ^ (h >> 15)) * 0xbb67ae85u;
+        return h ^ (h >> 16);
+    }
+    __device__ __forceinline__ Draws(uint32_t key, int64_t block, int lane)
+        : x(mix(mix(key ^ (uint32_t)(block >> 32) * 0x6a09e667u) + (uint32_t)block * 32u + lane))
+    {
+    }
+    __device__ __forceinline__ uint32_t next() { return (x = x * 1664525u + 1013904223u) >> 12; }
+};
+
+// x, at most 448 and a rounding, as one of the two E4M3 numbers next to it, the
+// nearer one the likelier, so that its mean is x.  Their distance is 2^20 units of
+// x's last place, or 2^-9 below 2^-6; r: 20 bits.
+__device__ __forceinline__ float round_at_random(float x, uint32_t r)
+{
+    const float a = fabsf(x), up = a < kNormal ? kNormal : 0.0f, t = a + up;
+    const float q = __uint_as_float((__float_as_uint(t) + r) & 0xfff00000u) - up;
+    return copysignf(t <= kTop ? q : a, x);  // a NaN stays one
+}
+
 // The scale of a warp's 256 values and what they are over it, rounded once:
 // with the rounded reciprocal y of the scale, q = x y, r = x - q scale (exact)
 // and q + r y is the rounded quotient (Markstein's division by a multiply and
@@ -423,9 +459,10 @@ __device__ __forceinline__ float scale_block(float (&x)[8], bool up)
 // one block at a time and bounds on every access 519 us where this takes 353.
 // Four blocks per SM leave 64 registers, which cost spills where weights and
 // gradients are FP32 (371 us; with three blocks 356) and bring more elsewhere
-// (353; 366).
-template <bool MASTER, bool FULL, typename W, typename G>
-__device__ __forceinline__ void step_chunk_8bit(const Chunk<W, G> &c, const Element &el)
+// (353; 366).  RANDOM: codes are rounded at random, by the key and the place of
+// the chunk's first block.
+template <bool MASTER, bool FULL, bool RANDOM, typename W, typename G>
+__device__ __forceinline__ void step_chunk_8bit(const Chunk<W, G> &c, const Element &el, uint32_t key, int64_t place)
 {
     const int lane = threadIdx.x & 31, n = FULL ? kChunk : c.n;
     uint8_t *const ms = (uint8_t *)c.m, *const vs = (uint8_t *)c.v;
@@ -466,15 +503,24 @@ __device__ __forceinline__ void step_chunk_8bit(const Chunk<W, G> &c, const Elem
         if (MASTER) store_n<8, FULL>(c.master, e, n, w);
         store_n<8, FULL>(c.w, e, n, w);
         // elements past the tensor's end are zero and stay so: they raise no scale
-        const float m_new = scale_block(m, false), v_new = scale_block(v, true);
+        const float m_new = scale_block(m, false), v_new = scale_block(v, !RANDOM);
+        if constexpr (RANDOM) {
+            Draws draws(key, place + s, lane);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                m[q] = round_at_random(m[q], draws.next());
+                const float code = round_at_random(v[q], draws.next());
+                v[q] = v[q] > 0.0f ? fmaxf(code, kLowest) : code;
+            }
+        }
         store_codes<FULL>(ms, e, n, m);
         store_codes<FULL>(vs, e, n, v);
         if (lane == 0) c.m_scale[s] = m_new, c.v_scale[s] = v_new;
     }
 }
 
-template <bool MASTER, typename W, typename G>
-__device__ __forceinline__ void step_any(const AdamWTensor &t, int64_t at, const Element &el)
+template <bool RANDOM, bool MASTER, typename W, typename G>
+__device__ __forceinline__ void step_any(const AdamWTensor &t, int64_t at, const Element &el, uint32_t key)
 {
     const int64_t left = t.n - at;
     Chunk<W, G> c{(W *)t.w + at, MASTER ? t.master + at : nullptr, (const G *)t.grad + at, nullptr, nullptr, nullptr, nullptr,
@@ -482,21 +528,23 @@ __device__ __forceinline__ void step_any(const AdamWTensor &t, int64_t at, const
     if (t.bits8) {
         c.m = (uint8_t *)t.m + at, c.v = (uint8_t *)t.v + at;
         c.m_scale = t.m_scale + at / kBlock8, c.v_scale = t.v_scale + at / kBlock8;
-        c.n == kChunk ? step_chunk_8bit<MASTER, true>(c, el) : step_chunk_8bit<MASTER, false>(c, el);
+        c.n == kChunk ? step_chunk_8bit<MASTER, true, RANDOM>(c, el, key, at / kBlock8)
+                      : step_chunk_8bit<MASTER, false, RANDOM>(c, el, key, at / kBlock8);
     } else {
         c.m = (float *)t.m + at, c.v = (float *)t.v + at;
         c.n == kChunk ? step_chunk<MASTER, true>(c, el) : step_chunk<MASTER, false>(c, el);
     }
 }
 
-template <bool MASTER, typename W>
-__device__ __forceinline__ void step_grad(const AdamWTensor &t, int64_t at, const Element &el)
+template <bool RANDOM, bool MASTER, typename W>
+__device__ __forceinline__ void step_grad(const AdamWTensor &t, int64_t at, const Element &el, uint32_t key)
 {
-    t.grad_f32 ? step_any<MASTER, W, float>(t, at, el) : step_any<MASTER, W, __nv_bfloat16>(t, at, el);
+    t.grad_f32 ? step_any<RANDOM, MASTER, W, float>(t, at, el, key)
+               : step_any<RANDOM, MASTER, W, __nv_bfloat16>(t, at, el, key);
 }
 
 // A factor that is no number leaves everything as it is.
-template <typename B>
+template <typename B, bool RANDOM>
 __global__ void __launch_bounds__(kThreads, kStepPerSm) adamw_kernel(const __grid_constant__ B b, const AdamWScalars sc)
 {
     ptx::griddep_wait();
@@ -510,10 +558,13 @@ __global__ void __launch_bounds__(kThreads, kStepPerSm) adamw_kernel(const __gri
     const float lr = (sc.lr_at ? *sc.lr_at : sc.lr) * t.lr_factor;
     const Element el{sc.beta1, sc.one_minus1, sc.beta2, sc.one_minus2, factor, -lr * t.weight_decay,
                      -lr * corrections.x, corrections.y, sc.eps};
+    uint32_t key = 0;
+    if constexpr (RANDOM) key = Draws::mix(Draws::mix(sc.step_at ? (uint32_t)*sc.step_at : sc.step) + t.index);
     if (t.master)
-        t.w_f32 ? step_grad<true, float>(t, at, el) : step_grad<true, __nv_bfloat16>(t, at, el);
+        t.w_f32 ? step_grad<RANDOM, true, float>(t, at, el, key) : step_grad<RANDOM, true, __nv_bfloat16>(t, at, el, key);
     else
-        t.w_f32 ? step_grad<false, float>(t, at, el) : step_grad<false, __nv_bfloat16>(t, at, el);
+        t.w_f32 ? step_grad<RANDOM, false, float>(t, at, el, key)
+                : step_grad<RANDOM, false, __nv_bfloat16>(t, at, el, key);
 }
 
 // The step's number from device memory: one more than it says, unless the
@@ -596,7 +647,7 @@ cudaError_t launch_grad_norm(const TensorRef *grads, int count, float max_norm, 
 }
 
 cudaError_t launch_adamw(const AdamWTensor *tensors, int count, AdamWScalars sc, double beta1, double beta2,
-                         int32_t *step, void *workspace, cudaStream_t s)
+                         int32_t *step, bool random, void *workspace, cudaStream_t s)
 {
     cudaLaunchAttribute attr;
     cudaLaunchConfig_t cfg = early(&attr, s);
@@ -607,11 +658,12 @@ cudaError_t launch_adamw(const AdamWTensor *tensors, int count, AdamWScalars sc,
         if (e != cudaSuccess) return e;
         cfg.blockDim = dim3(kThreads);
         sc.corrections = (const float2 *)workspace;
+        sc.step_at = step;
     }
     auto launch = [&](const auto &b) {
         using B = std::remove_cv_t<std::remove_reference_t<decltype(b)>>;
         cfg.gridDim = dim3(b.first[b.count]);
-        return cudaLaunchKernelEx(&cfg, adamw_kernel<B>, b, (const AdamWScalars)sc);
+        return cudaLaunchKernelEx(&cfg, random ? adamw_kernel<B, true> : adamw_kernel<B, false>, b, (const AdamWScalars)sc);
     };
     return count <= kSmallBatch ? in_batches<StepBatchSmall>(tensors, count, kSmallBatch, kChunk, launch)
                                 : in_batches<StepBatch>(tensors, count, kStepBatch, kChunk, launch);

@@ -296,19 +296,22 @@ struct AdamWTensor {
     int64_t n;
     float lr_factor, weight_decay;
     bool w_f32, grad_f32, bits8;
+    uint32_t index;  // its place in the call's list
 };
 struct AdamWScalars {
     float beta1, one_minus1, beta2, one_minus2, eps, lr;
     float2 host;                // 1 / (1 - b1^t), 1 / sqrt(1 - b2^t)
     const float2 *corrections;  // nullable: these, in device memory
     const float *grad_scale, *lr_at;  // nullable
+    uint32_t step;                    // this step's number
+    const int32_t *step_at;           // nullable: it, in device memory
 };
 size_t grad_norm_workspace_bytes(int64_t count);
 cudaError_t launch_grad_norm(const TensorRef *grads, int count, float max_norm, float *out, void *workspace, int n_sm,
                              cudaStream_t s);
 // step nullable: the number of steps so far, in device memory; with it the
-// workspace holds a float2
+// workspace holds a float2.  random: 8-bit codes are rounded at random
 cudaError_t launch_adamw(const AdamWTensor *tensors, int count, AdamWScalars sc, double beta1, double beta2,
-                         int32_t *step, void *workspace, cudaStream_t s);
+                         int32_t *step, bool random, void *workspace, cudaStream_t s);
 
 }  // namespace moe

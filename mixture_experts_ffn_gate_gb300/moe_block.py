@@ -26,6 +26,7 @@ MOE_SCORE_SOFTMAX = 0
 MOE_SCORE_SIGMOID = 1
 
 _TYPES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
+_ROUNDINGS = {"auto": 0, "nearest": 1, "random": 2}   # MOE_ADAMW_ROUND_*
 _SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 
 
@@ -57,7 +58,7 @@ class moe_adamw_tensor(ctypes.Structure):
 class moe_adamw_opts(ctypes.Structure):
     """Mirror of ``struct moe_adamw_opts``."""
     _fields_ = ([(f, ctypes.c_double) for f in ("lr", "beta1", "beta2", "eps")]
-                + [("step", ctypes.c_int64), ("reserved", ctypes.c_int64 * 3)])
+                + [("step", ctypes.c_int64), ("state_rounding", ctypes.c_int32), ("reserved", ctypes.c_int32 * 5)])
 
 
 def declare(L):
@@ -727,13 +728,17 @@ class AdamWPlan:
 
 
 def moe_adamw_step(plan: AdamWPlan, step, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, grad_scale=None,
-                   workspace=None, stream=None) -> None:
+                   workspace=None, stream=None, rounding: str = "auto") -> None:
     """One AdamW step of the plan's weights, in place.  ``step``: its number,
     from 1; or an int32 CUDA tensor [1] with the steps taken so far, to which
     the call adds one.  ``lr``: a number or an f32 CUDA tensor [1].
     ``grad_scale`` f32 [1] (nullable; moe_grad_norm's [1:]): the gradients'
     factor; where it is NaN or infinite nothing changes.  With tensors for
-    step and lr a captured step's replays go on counting."""
+    step and lr a captured step's replays go on counting.  ``rounding`` of
+    8-bit states: "nearest", which follows the gradients with betas up to 0.95;
+    "random", which does with any; "auto", the one or the other by the betas."""
+    if rounding not in _ROUNDINGS:
+        raise ValueError(f"rounding must be one of {sorted(_ROUNDINGS)}, got {rounding!r}")
     if plan.grads is None and plan.weights:
         raise ValueError("the plan has no gradients yet")
     dev = plan.device
@@ -754,7 +759,7 @@ def moe_adamw_step(plan: AdamWPlan, step, lr=1e-3, betas=(0.9, 0.999), eps: floa
     _here(dev, counter, lr_at, grad_scale, workspace)
     if counter is not None and workspace is None:
         workspace = _workspace(256, dev, stream, "workspace size")
-    o = moe_adamw_opts(lr, betas[0], betas[1], eps, step)
+    o = moe_adamw_opts(lr, betas[0], betas[1], eps, step, _ROUNDINGS[rounding])
     p = _ptr
     _check(_lib().moe_adamw_step(plan.array, len(plan.weights), ctypes.byref(o), p(grad_scale), p(lr_at), p(counter),
                                  p(workspace), 0 if workspace is None else _size(workspace), _stream(stream, dev)),

@@ -108,3 +108,201 @@ def test_losses_of_many_sequences(kind, T, E, S, even):
     z = (2 * lse.abs() * (rel + 4 * U * lse.abs())).max().item() + 400 * U * lse.square().max().item()
     assert abs(got[2] - want[2]) <= z
     assert abs(got[0] - want[0]) <= 0.5 * (rel + 400 * U) * want[1] + 0.25 * z + 4 * U * want[0]
+
+
+# ------------------------------------------------------------------ 8-bit states
+def moment(codes, scale):
+    return codes.float().double() * scale.double().repeat_interleave(256)[: codes.numel()].view(codes.shape)
+
+
+def follow(betas, phases, rounding=None, blocks=40):
+    """sqrt(v) and m of 8-bit states over those of 32-bit ones after each of
+    the phases (steps, factors of the gradients), every second element apart."""
+    n = blocks * 256
+    w8, w32 = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    s8, s32, g = mb.new_adamw_state(w8, 8), mb.new_adamw_state(w32, 32), torch.empty(n, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    plans = [mb.AdamWPlan([w], [s], grads=[g]) for w, s in ((w8, s8), (w32, s32))]
+    t, out = 0, []
+    how = {} if rounding is None else dict(rounding=rounding)
+    for steps, even, odd in phases:
+        factor = torch.tensor([even, odd], device="cuda").repeat(n // 2)
+        for _ in range(steps):
+            t += 1
+            g.copy_(torch.randn(n, generator=gen, device="cuda") * factor)
+            for plan in plans:
+                mb.moe_adamw_step(plan, t, lr=1e-3, betas=betas, **how)
+        r = (moment(s8.v, s8.v_scale) / s32.v.double().sqrt()).cpu().numpy()
+        d = (moment(s8.m, s8.m_scale) - s32.m.double()).cpu().numpy()
+        out.append([(r[i::2], d[i::2] / np.sqrt(np.mean(s32.m.cpu().numpy()[i::2] ** 2.0))) for i in (0, 1)])
+    return out
+
+
+@pytest.mark.parametrize("betas,steps", [((0.9, 0.95), 300), ((0.9, 0.99), 1500), ((0.9, 0.999), 6000),
+                                         ((0.99, 0.999), 6000)])
+def test_8_bit_second_moments_follow_their_gradients(betas, steps):
+    """As 32-bit ones do: steady gradients, then half of the elements' fall
+    fourfold, then the others' rise fourfold (six time constants of v each, after
+    which 1/400 of the old v is left: a tenth of the new one's, 5% of its root).
+    A code moves by its spacing (9% of the value on average) with a chance of
+    what sqrt(v) changes over it, (1 - beta2) / 2 times about 1 for Gaussian
+    gradients, and is drawn back by 1 - beta2 of its distance: a variance of
+    0.09 / 4 of the square, 15% rms, 17% with the last step's rounding and the
+    old v.  Rounded to nearest, up to a beta2 of 0.95, it is off by half a
+    spacing more where gradients fell: 15% at the median, 25% rms."""
+    nearest = betas[1] <= 0.95
+    for phase, both in enumerate(follow(betas, [(steps, 1.0, 1.0), (steps, 0.25, 1.0), (steps, 0.25, 4.0)])):
+        for r, _ in both:
+            assert abs(np.median(r) - 1) <= (0.2 if nearest else 0.07), (phase, np.median(r))
+            assert np.sqrt(np.mean((r - 1) ** 2)) <= (0.35 if nearest else 0.25), phase
+
+
+def test_8_bit_first_moments_follow_at_betas_close_to_one():
+    """Unbiased: m's error over m's size averages to nothing (10240 elements of
+    30% rms: 0.3%), and is a fraction of it."""
+    for both in follow((0.99, 0.999), [(1500, 1.0, 1.0), (1500, 0.1, 1.0)]):
+        for _, d in both:
+            assert abs(d.mean()) <= 0.03 and np.sqrt(np.mean(d ** 2)) <= 0.6
+
+
+def test_gradients_of_zero_beside_others_let_the_second_moment_decay():
+    """sqrt(v) of elements without gradients, in blocks whose scale stays: after
+    three time constants its mean is exp(-1.5) of what it was (10240 elements of
+    40% rms at most: 0.4%; the sum of their roundings is unbiased)."""
+    n = 80 * 256
+    w, g = torch.zeros(n, device="cuda"), torch.ones(n, device="cuda")
+    s = mb.new_adamw_state(w, 8)
+    plan = mb.AdamWPlan([w], [s], grads=[g])
+    mb.moe_adamw_step(plan, 1, betas=(0.9, 0.0))   # v = 1
+    before = moment(s.v, s.v_scale)[::2].mean().item()
+    g[::2] = 0.0
+    for t in range(2, 302):
+        mb.moe_adamw_step(plan, t, betas=(0.9, 0.99))
+    r = moment(s.v, s.v_scale)[::2].mean().item() / before
+    assert abs(r / 0.99 ** 150 - 1) <= 0.03
+
+
+def codes_in_fp32(w, s, g, b1, b2):
+    """The quotients that a step's codes are the rounding of, operation by
+    operation in FP32, for m and sqrt(v)."""
+    b1, a1, b2, a2, top = (torch.tensor(x, dtype=torch.float32, device="cuda") for x in (b1, 1 - b1, b2, 1 - b2, 1 / 448))
+    m = s.m.float() * s.m_scale.repeat_interleave(256)
+    v = (s.v.float() * s.v_scale.repeat_interleave(256)).square()
+    out = []
+    for x in (b1 * m + a1 * g, (b2 * v + (a2 * g) * g).sqrt()):
+        scale = (x.view(-1, 256).abs().amax(1) * top).clamp_min(2.0 ** -126)
+        out.append(((x.view(-1, 256) / scale[:, None]).clamp(-448, 448).view(-1), scale))
+    return out
+
+
+def neighbours(q):
+    """The E4M3 numbers below and above |q|, equal where |q| is one."""
+    a = q.double().abs()
+    gap = torch.exp2(torch.floor(torch.log2(a.clamp_min(2.0 ** -6))) - 3)
+    lo = torch.floor(a / gap) * gap
+    return lo, torch.where(a == lo, lo, lo + gap)
+
+
+@pytest.mark.parametrize("b1,b2,rounding", [(0.9, 0.999, "auto"), (0.96, 0.9, "auto"), (0.9, 0.95, "random")])
+def test_random_rounding_is_to_a_neighbour_and_unbiased(b1, b2, rounding):
+    n = 1 << 21
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    w, g = torch.zeros(n, device="cuda"), torch.randn(n, generator=gen, device="cuda")
+    g *= torch.exp2(torch.randint(-12, 1, (n,), generator=gen, device="cuda").float())
+    s = mb.new_adamw_state(w, 8)
+    plan = mb.AdamWPlan([w], [s], grads=[g])
+    mb.moe_adamw_step(plan, 1, betas=(0.5, 0.5), rounding="nearest")
+    g.copy_(torch.randn(n, generator=gen, device="cuda") * 0.3)
+    state = [t.clone() for t in s]
+    want = codes_in_fp32(w, s, g, b1, b2)
+    mb.moe_adamw_step(plan, 7, betas=(b1, b2), rounding=rounding)
+    ups = []
+    for (q, scale), got, got_scale in zip(want, (s.m, s.v), (s.m_scale, s.v_scale)):
+        assert torch.equal(scale, got_scale)
+        code = got.float().double()
+        lo, hi = neighbours(q)
+        if got is s.v:
+            lo, hi = (torch.where(q > 0, x.clamp_min(2.0 ** -9), x) for x in (lo, hi))
+        assert ((code.abs() == lo) | (code.abs() == hi)).all()
+        assert (torch.sign(code) == torch.sign(q.double()))[code != 0].all()
+        inside = hi > lo
+        f = ((q.double().abs() - lo) / (hi - lo))[inside]
+        up = (code.abs() == hi)[inside]
+        ups.append((inside, up.double() - f, (code.abs() == hi).double()))
+        # a coin of chance f, 2^20 values to it: six standard deviations in all and in tenths
+        for part in [torch.ones_like(up)] + [(f >= k / 10) & (f < (k + 1) / 10) for k in range(10)]:
+            count = int(part.sum())
+            assert count > 1000
+            spread = (f[part] * (1 - f[part])).sum().sqrt().item()
+            assert abs((up.double() - f)[part].sum().item()) <= 6 * spread + count * 2.0 ** -20
+    # m's and sqrt(v)'s coins are two: their product's mean is nothing
+    a, b = (torch.zeros(n, dtype=torch.float64, device="cuda").masked_scatter_(i, d) for i, d, _ in ups)
+    assert abs((a * b).sum().item()) <= 6 * (a * b).square().sum().sqrt().item()
+    # the same step again: the same bits; another step, another tensor in the list: others
+    first = [t.clone() for t in s]
+
+    def again(step, front=0):
+        for t, x in zip(s, state):
+            t.copy_(x)
+        empty = [torch.zeros(0, device="cuda") for _ in range(front)]
+        p = mb.AdamWPlan(empty + [w], [mb.new_adamw_state(t, 8) for t in empty] + [s], grads=[t.clone() for t in empty] + [g])
+        mb.moe_adamw_step(p, step, betas=(b1, b2), rounding=rounding)
+        return [torch.equal(t.view(torch.uint8), x.view(torch.uint8)) for t, x in zip(s, first)]
+    assert all(again(7)) and all(again(torch.tensor([6], dtype=torch.int32, device="cuda")))
+    for other in (again(8), again(7, front=1)):
+        assert other == [False, False, True, True]
+
+
+@pytest.mark.parametrize("n", [1, 7, 255, 257, 4097, 70001])
+def test_random_rounding_of_odd_sizes_extremes_and_nan(n):
+    w, g = torch.ones(n, device="cuda"), torch.randn(n, generator=torch.Generator().manual_seed(n)).cuda()
+    g[::3] = 0.0
+    s = mb.new_adamw_state(w, 8)
+    plan = mb.AdamWPlan([w], [s], grads=[g])
+    for t in range(1, 4):
+        mb.moe_adamw_step(plan, t)
+    assert all(torch.isfinite(t.float()).all() for t in (w, *s))
+    assert (s.m.float()[::3] == 0).all() and (s.v.float()[::3] == 0).all() and (w[::3] == 1).all()
+    # what is not zero has a code; the largest element's is the largest
+    assert (s.v.float()[g != 0] > 0).all()
+    if n > 1:
+        assert s.v.float()[:256].max() == 448
+    g[n // 2] = float("nan")
+    mb.moe_adamw_step(plan, 4)
+    for t in (w, s.m.float(), s.v.float()):
+        assert torch.isnan(t[n // 2]) and int(torch.isnan(t).sum()) == 1
+
+
+def test_nearest_rounding_of_any_betas():
+    n = 1 << 16
+    w, g = torch.zeros(n, device="cuda"), torch.randn(n, device="cuda")
+    s = mb.new_adamw_state(w, 8)
+    plan = mb.AdamWPlan([w], [s], grads=[g])
+    mb.moe_adamw_step(plan, 1, betas=(0.5, 0.5))
+    g.normal_()
+    want = codes_in_fp32(w, s, g, 0.9, 0.999)
+    mb.moe_adamw_step(plan, 2, betas=(0.9, 0.999), rounding="nearest")
+    for (q, _), got in zip(want, (s.m, s.v)):
+        code = q.to(torch.float8_e4m3fn).float()
+        if got is s.v:
+            code = torch.where(q > 0, code.clamp_min(2.0 ** -9), code)
+        assert torch.equal(got.float(), code)
+
+
+def test_a_captured_step_draws_anew():
+    """With the step's number on the device: replays equal the steps one by one."""
+    runs = []
+    for captured in (True, False):
+        gen = torch.Generator(device="cuda").manual_seed(0)
+        w, g = torch.zeros(5000, device="cuda"), torch.randn(5000, generator=gen, device="cuda")
+        s, step = mb.new_adamw_state(w, 8), torch.zeros(1, dtype=torch.int32, device="cuda")
+        plan = mb.AdamWPlan([w], [s], grads=[g])
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                mb.moe_adamw_step(plan, step)
+        for _ in range(5):
+            graph.replay() if captured else mb.moe_adamw_step(plan, step)
+            g.mul_(0.9)
+        runs.append([w, *(t.view(torch.uint8) for t in s)])
+    assert all(torch.equal(a, b) for a, b in zip(*runs))

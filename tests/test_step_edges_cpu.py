@@ -1,5 +1,7 @@
 """Edges of the training step's operators on the host: plans whose tensors moved,
 calls without tensors, arguments that are tensors."""
+import ctypes
+
 import pytest
 import torch
 
@@ -70,3 +72,20 @@ def test_settings_that_are_tensors_are_read_at_every_call():
     for value in (2, 4):
         groups.fill_(value)
         assert mb._gate_opts("softmax", True, 1.0, groups, 1)._obj.groups == value
+
+
+def test_the_rounding_of_8_bit_states(monkeypatch, on_host):
+    """By the betas unless it is given; others are refused, by the library too."""
+    from mixture_experts_ffn_gate_gb300 import _build, moe_ffn
+    _build.build()
+    for bad in (-1, 3):
+        o = mb.moe_adamw_opts(1e-3, 0.9, 0.99, 1e-8, 1, bad)
+        assert moe_ffn.lib().moe_adamw_step(None, 0, ctypes.byref(o), None, None, None, None, 0, None) == 1
+    library = Library(monkeypatch)
+    w = torch.zeros(300)
+    plan = mb.AdamWPlan([w], [mb.new_adamw_state(w, 8)], grads=[torch.zeros(300)])
+    for rounding, code in (("auto", 0), ("nearest", 1), ("random", 2)):
+        mb.moe_adamw_step(plan, 1, rounding=rounding)
+        assert library.calls[-1][1][2]._obj.state_rounding == code
+    with pytest.raises(ValueError, match="rounding"):
+        mb.moe_adamw_step(plan, 1, rounding="up")
