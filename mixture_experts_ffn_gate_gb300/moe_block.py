@@ -9,6 +9,7 @@ fallback.
 """
 from __future__ import annotations
 
+import array
 import bisect
 import ctypes
 import functools
@@ -17,6 +18,7 @@ from typing import NamedTuple
 
 import torch
 
+from . import _build
 from . import moe_ffn as _m
 from .moe_ffn import MOE_ERR_UNSUPPORTED_SHAPE, MoeFfnError, _empty_on, mx_scale_bytes
 
@@ -560,6 +562,20 @@ def _addresses(tensors):
     return list(map(torch.Tensor.data_ptr, tensors))
 
 
+def _same_memory(tensors, addresses):
+    """Whether the tensors of a list have the addresses packed in bytes."""
+    return _pack(_addresses(tensors)) == addresses
+
+
+def _pack(addresses):
+    return array.array("Q", addresses).tobytes()
+
+
+_tensors = _build.load_tensors()
+if _tensors is not None:
+    _same_memory = _tensors.same_memory
+
+
 def _span(t):
     return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
 
@@ -574,12 +590,13 @@ class GradList:
             if not (g.is_cuda and g.is_contiguous()):
                 _is(g, g.shape, g.dtype, f"grads[{i}]")
         self.device = _one_device({g.device for g in self.grads}, "grads")
-        self.addresses = _addresses(self.grads)
+        addresses = _addresses(self.grads)
+        self.addresses = _pack(addresses)
         self.array = (moe_tensor * len(self.grads))(
-            *(moe_tensor(a, g.numel(), _type(g, "a gradient")) for a, g in zip(self.addresses, self.grads)))
+            *(moe_tensor(a, g.numel(), _type(g, "a gradient")) for a, g in zip(addresses, self.grads)))
 
     def check(self):
-        if _addresses(self.grads) != self.addresses:
+        if not _same_memory(self.grads, self.addresses):
             raise ValueError("a gradient's memory is no longer the one that it was given with")
 
 
@@ -717,7 +734,7 @@ class AdamWPlan:
         for d, g, start in zip(self.array, grads, addresses):
             d.grad, d.grad_type = start, _TYPES[g.dtype]
         self.grads, self._grad_list = grads, None
-        self._tensors, self._addresses = self._written + grads, self._written_at + addresses
+        self._tensors, self._addresses = self._written + grads, _pack(self._written_at + addresses)
 
     def grad_list(self) -> GradList:
         if self.grads is None:
@@ -744,7 +761,7 @@ def moe_adamw_step(plan: AdamWPlan, step, lr=1e-3, betas=(0.9, 0.999), eps: floa
     dev = plan.device
     if dev is None:
         return
-    if _addresses(plan._tensors) != plan._addresses:
+    if not _same_memory(plan._tensors, plan._addresses):
         raise ValueError("a tensor's memory is no longer the one that the plan was made for: "
                          "weights, masters, states and gradients keep theirs")
     counter = lr_at = None

@@ -89,3 +89,22 @@ def test_the_rounding_of_8_bit_states(monkeypatch, on_host):
         assert library.calls[-1][1][2]._obj.state_rounding == code
     with pytest.raises(ValueError, match="rounding"):
         mb.moe_adamw_step(plan, 1, rounding="up")
+
+
+def test_addresses_are_compared_natively_as_in_python():
+    """The built module and the plain comparison, which is what there is without it."""
+    from mixture_experts_ffn_gate_gb300 import _build
+    _build.build_tensors()
+    native = _build.load_tensors().same_memory
+    ts = [torch.zeros(n) for n in (3, 0, 5)] + [torch.zeros(8)[2:], torch.nn.Parameter(torch.zeros(4))]
+    plain = lambda tensors, addresses: mb._pack(mb._addresses(tensors)) == addresses
+    at = mb._pack(mb._addresses(ts))
+    for same in (native, plain, mb._same_memory):
+        assert same(ts, at) and same([], b"") and not same(ts, at[:8] + at[:8] + at[16:])
+        kept, ts[2].data = ts[2].data, torch.zeros(5)
+        assert not same(ts, at)
+        ts[2].data = kept
+        assert same(ts, at)
+    for bad in ((tuple(ts), at), (ts, list(at)), (ts, at[:-8]), ([1], at[:8])):
+        with pytest.raises((TypeError, ValueError)):
+            native(*bad)
