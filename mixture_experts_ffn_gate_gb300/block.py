@@ -157,19 +157,27 @@ class MoeBlock:
         self.w_router.add_(grads["w_router"], alpha=-lr)
         self.update_bias(grads, balance_rate)
 
-    def update_experts(self, grads, lr: float):
-        """The experts' matrices by their orthogonalised gradients."""
+    def update_experts(self, grads, lr: float, factor=None):
+        """The experts' matrices by their orthogonalised gradients.  Where
+        ``factor`` (f32 [1], nullable) is no finite number they stay as they are."""
         for name in ("w_gate_up", "w_down"):
             g, w = grads[name], getattr(self, name)
             _, M, N = g.shape
             step = mb.moe_orthogonalize(g, out_scale=-lr * math.sqrt(max(1.0, M / N)))
-            w.add_(step)
+            w.add_(step if factor is None else _unless_finite(factor, step))
 
-    def update_bias(self, grads, rate: float):
-        """The balance bias against the loads."""
+    def update_bias(self, grads, rate: float, factor=None):
+        """The balance bias against the loads; ``factor`` as in update_experts."""
         if self.balance_bias is not None and rate:
             loads = grads["loads"].float()
-            self.balance_bias.add_(torch.sign(loads.mean() - loads), alpha=rate)
+            step = torch.sign(loads.mean() - loads).mul_(rate)
+            self.balance_bias.add_(step if factor is None else _unless_finite(factor, step))
+
+
+def _unless_finite(factor, step):
+    """The step, or where the factor f32 [1] is no finite number -0.0, which
+    added to any number leaves it: decided on the device."""
+    return step.masked_fill_(~torch.isfinite(factor), -0.0)
 
 
 class BlockAdamW:
@@ -177,10 +185,10 @@ class BlockAdamW:
     and router weights with 32-bit states, and the experts' with FP32 masters
     and states in ``bits`` (8 or 32; their ``rounding`` as moe_adamw_step's), or
     orthogonalised updates for them (``bits`` None).  Weight decay is the
-    matrices' alone.  Steps whose gradients' norm is no finite number are left
-    out (with orthogonalised updates the experts' are not).  The step's number
-    and the learning rate are kept on the device, so a step may be captured into
-    a CUDA graph."""
+    matrices' alone.  A step whose gradients' norm is no finite number is left
+    out: weights, states, balance bias and the step's number stay as they are.
+    That number and the learning rate are kept on the device, so a step may be
+    captured into a CUDA graph."""
 
     def __init__(self, block: MoeBlock, lr: float = 1e-3, betas=(0.9, 0.95), eps: float = 1e-8,
                  weight_decay: float = 0.1, max_norm: float = 1.0, bits: int | None = 8, rounding: str = "auto"):
@@ -205,8 +213,8 @@ class BlockAdamW:
                           rounding=self.rounding)
         self.plan.set_grads(None)
         if "w_down" not in self.names:
-            self.block.update_experts(grads, experts_lr)
-        self.block.update_bias(grads, balance_rate)
+            self.block.update_experts(grads, experts_lr, clip[1:])
+        self.block.update_bias(grads, balance_rate, clip[1:])
         return clip
 
 

@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+from mixture_experts_ffn_gate_gb300 import block as b
 from mixture_experts_ffn_gate_gb300 import moe_block as mb
 from tests import step_ref as ref
 from tests.block_ref import U
@@ -306,3 +307,68 @@ def test_a_captured_step_draws_anew():
             g.mul_(0.9)
         runs.append([w, *(t.view(torch.uint8) for t in s)])
     assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
+# ------------------------------------------------------------------ the block's step
+NAMES = ("norm_weight", "w_router", "w_gate_up", "w_down")
+
+
+def block_step(bits):
+    block = b.synthetic_block(balance=b.BalanceSettings())
+    opt = b.BlockAdamW(block, lr=1e-2, bits=bits)
+    g = torch.Generator().manual_seed(1)
+    x, stream, dout = (torch.randn(20, 256, generator=g).cuda() for _ in range(3))
+    _, h, saved = block.train_forward(x, stream.bfloat16())
+    return block, opt, block.train_backward(saved, dout, torch.zeros_like(h))
+
+
+def all_of(block, opt):
+    states = [t for s in opt.plan.states for t in s if t is not None]
+    masters = [t for t in opt.plan.masters if t is not None]
+    return [t.clone().view(torch.uint8) for t in
+            [getattr(block, n) for n in NAMES] + [block.balance_bias, opt.step_count] + masters + states]
+
+
+@pytest.mark.parametrize("bits", [8, 32, None])
+@pytest.mark.parametrize("where", NAMES)
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_step_that_is_left_out_changes_nothing_of_the_block(bits, where, value):
+    """The experts with orthogonalised updates and the balance bias among the
+    rest; a step after it takes all of them along."""
+    block, opt, grads = block_step(bits)
+    block.balance_bias.normal_()
+    block.balance_bias[3] = -0.0
+    block.w_down.view(-1)[:2] = torch.tensor([0.0, -0.0])
+    before = all_of(block, opt)
+    good = grads[where].clone()
+    grads[where].view(-1)[7] = value
+    clip = opt.step(grads, balance_rate=1e-3)
+    assert not torch.isfinite(clip[1])
+    assert all(torch.equal(x, y) for x, y in zip(all_of(block, opt), before))
+    grads[where].copy_(good)
+    opt.step(grads, balance_rate=1e-3)
+    after = all_of(block, opt)
+    assert not any(torch.equal(x, y) for x, y in zip(after[:6], before[:6]))
+    assert all(torch.isfinite(getattr(block, n)).all() for n in NAMES)
+
+
+def test_a_captured_step_is_left_out_on_the_device():
+    runs = []
+    _, opt, grads = block_step(None)
+    opt.step(grads)
+    for captured in (True, False):
+        block, opt, grads = block_step(None)
+        step = lambda: opt.step(grads, balance_rate=1e-3)
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                step()
+        for i in range(4):
+            kept = grads["w_down"].view(-1)[5].clone()
+            if i % 2:
+                grads["w_down"].view(-1)[5] = float("nan")
+            graph.replay() if captured else step()
+            grads["w_down"].view(-1)[5] = kept
+        assert opt.step_count.item() == 2
+        runs.append(all_of(block, opt))
+    assert all(torch.equal(x, y) for x, y in zip(*runs))
