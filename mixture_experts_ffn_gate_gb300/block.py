@@ -205,7 +205,12 @@ class BlockAdamW:
 
     def step(self, grads, experts_lr: float = 2e-2, balance_rate: float = 0.0):
         """One step for train_backward's gradients; returns the gradients'
-        norm and factor, f32 [2]."""
+        norm and factor, f32 [2].  It is of the weights that the block had at
+        first: one that has another tensor in its place since is refused."""
+        for n, w in zip(self.names, self.plan.weights):
+            if getattr(self.block, n) is not w:
+                raise ValueError(f"the block's {n} is no longer the tensor that is optimised: copy into it, "
+                                 "or make a new BlockAdamW")
         self.plan.set_grads([grads[n] for n in self.names])
         clip = mb.moe_grad_norm([grads[n] for n in ("norm_weight", "w_router", "w_gate_up", "w_down")],
                                 max_norm=self.max_norm)

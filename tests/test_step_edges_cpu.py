@@ -108,3 +108,28 @@ def test_addresses_are_compared_natively_as_in_python():
     for bad in ((tuple(ts), at), (ts, list(at)), (ts, at[:-8]), ([1], at[:8])):
         with pytest.raises((TypeError, ValueError)):
             native(*bad)
+
+
+@pytest.mark.parametrize("bits", [8, None])
+def test_a_block_whose_weight_is_another_tensor_is_refused(monkeypatch, on_host, bits):
+    """Its step would go on with the tensor that the block no longer reads."""
+    from mixture_experts_ffn_gate_gb300 import block as b
+    library = Library(monkeypatch)
+    block = b.MoeBlock(torch.ones(8), torch.zeros(4, 8), None, torch.zeros(4, 6, 8).bfloat16(),
+                       torch.zeros(4, 8, 3).bfloat16(), b.GateSettings(k=2))
+    monkeypatch.setattr(block, "update_experts", lambda *a: None)
+    monkeypatch.setattr(mb, "new_grad_norm_workspace", lambda *a, **k: torch.zeros(256, dtype=torch.uint8))
+    monkeypatch.setattr(mb, "_size", lambda t: t.numel())
+    opt = b.BlockAdamW(block, bits=bits)
+    names = ("norm_weight", "w_router", "w_gate_up", "w_down")
+    grads = {n: torch.zeros(getattr(block, n).shape) for n in names}
+    opt.step(grads)
+    assert [name for name, _ in library.calls] == ["moe_grad_norm", "moe_adamw_step"]
+    for n in names if bits else names[:2]:
+        kept = getattr(block, n)
+        setattr(block, n, kept.clone())
+        with pytest.raises(ValueError, match="no longer"):
+            opt.step(grads)
+        setattr(block, n, kept)
+    assert len(library.calls) == 2
+    opt.step(grads)
