@@ -394,6 +394,7 @@ int moe_adamw_step(const moe_adamw_tensor *tensors, int64_t count, const moe_ada
         if (st == MOE_OK) st = add_elements(tensors[i].n, &total);
         if (st != MOE_OK) return st;
     }
+    if (count == 0 && !step_i32) return MOE_OK;
     int n_sm, pairs;
     const int st = moe::device_info(&n_sm, &pairs);
     if (st != MOE_OK) return st;

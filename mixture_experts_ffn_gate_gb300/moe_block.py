@@ -748,7 +748,7 @@ def moe_adamw_step(plan: AdamWPlan, step, lr=1e-3, betas=(0.9, 0.999), eps: floa
                    workspace=None, stream=None, rounding: str = "auto") -> None:
     """One AdamW step of the plan's weights, in place.  ``step``: its number,
     from 1; or an int32 CUDA tensor [1] with the steps taken so far, to which
-    the call adds one.  ``lr``: a number or an f32 CUDA tensor [1].
+    the call adds one (a plan without weights does too).  ``lr``: a number or an f32 CUDA tensor [1].
     ``grad_scale`` f32 [1] (nullable; moe_grad_norm's [1:]): the gradients'
     factor; where it is NaN or infinite nothing changes.  With tensors for
     step and lr a captured step's replays go on counting.  ``rounding`` of
@@ -758,10 +758,7 @@ def moe_adamw_step(plan: AdamWPlan, step, lr=1e-3, betas=(0.9, 0.999), eps: floa
         raise ValueError(f"rounding must be one of {sorted(_ROUNDINGS)}, got {rounding!r}")
     if plan.grads is None and plan.weights:
         raise ValueError("the plan has no gradients yet")
-    dev = plan.device
-    if dev is None:
-        return
-    if not _same_memory(plan._tensors, plan._addresses):
+    if plan.weights and not _same_memory(plan._tensors, plan._addresses):
         raise ValueError("a tensor's memory is no longer the one that the plan was made for: "
                          "weights, masters, states and gradients keep theirs")
     counter = lr_at = None
@@ -773,11 +770,15 @@ def moe_adamw_step(plan: AdamWPlan, step, lr=1e-3, betas=(0.9, 0.999), eps: floa
         lr_at, lr = lr, 0.0
     if grad_scale is not None:
         _is(grad_scale, (1,), torch.float32, "grad_scale")
-    _here(dev, counter, lr_at, grad_scale, workspace)
+    dev = plan.device
+    if dev is None:  # no weights: the device that counts, where there is one
+        dev = next((t.device for t in (counter, lr_at, grad_scale) if t is not None), None)
+    if dev is not None:
+        _here(dev, counter, lr_at, grad_scale, workspace)
     if counter is not None and workspace is None:
         workspace = _workspace(256, dev, stream, "workspace size")
     o = moe_adamw_opts(lr, betas[0], betas[1], eps, step, _ROUNDINGS[rounding])
     p = _ptr
     _check(_lib().moe_adamw_step(plan.array, len(plan.weights), ctypes.byref(o), p(grad_scale), p(lr_at), p(counter),
-                                 p(workspace), 0 if workspace is None else _size(workspace), _stream(stream, dev)),
-           "moe_adamw_step")
+                                 p(workspace), 0 if workspace is None else _size(workspace),
+                                 None if dev is None else _stream(stream, dev)), "moe_adamw_step")

@@ -372,3 +372,17 @@ def test_a_captured_step_is_left_out_on_the_device():
         assert opt.step_count.item() == 2
         runs.append(all_of(block, opt))
     assert all(torch.equal(x, y) for x, y in zip(*runs))
+
+
+def test_a_plan_without_weights_counts():
+    """Unless the step is left out: the counter of plans of which one is empty."""
+    w, step = torch.zeros(64, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    none = mb.AdamWPlan([], [], grads=[])
+    some = mb.AdamWPlan([w], [mb.new_adamw_state(w)], grads=[torch.ones(64, device="cuda")])
+    for t, plan in enumerate((none, some, none, none), 1):
+        mb.moe_adamw_step(plan, step)
+        assert step.item() == t
+    mb.moe_adamw_step(none, step, grad_scale=torch.tensor([float("nan")], device="cuda"))
+    assert step.item() == 4
+    mb.moe_adamw_step(none, 5, lr=torch.ones(1, device="cuda"))
+    assert step.item() == 4

@@ -133,3 +133,24 @@ def test_a_block_whose_weight_is_another_tensor_is_refused(monkeypatch, on_host,
         setattr(block, n, kept)
     assert len(library.calls) == 2
     opt.step(grads)
+
+
+def test_an_empty_plan_checks_its_arguments_and_counts(monkeypatch):
+    """As the library does: bad numbers are refused, a counter reaches it."""
+    from mixture_experts_ffn_gate_gb300 import _build
+    _build.build()
+    plan = mb.AdamWPlan([], [], grads=[])
+    assert mb.moe_adamw_step(plan, 1) is None
+    for bad in (dict(step=0), dict(lr=float("nan")), dict(betas=(0.9, 1.0)), dict(eps=-1.0)):
+        with pytest.raises(mb.MoeFfnError):
+            mb.moe_adamw_step(plan, **{**dict(step=1), **bad})
+    with pytest.raises(ValueError):
+        mb.moe_adamw_step(plan, torch.zeros(1))
+    library = Library(monkeypatch)
+    monkeypatch.setattr(mb, "_is", lambda *a: None)
+    monkeypatch.setattr(mb, "_size", lambda t: t.numel())
+    monkeypatch.setattr(mb, "_workspace", lambda n, *a: torch.zeros(n, dtype=torch.uint8))
+    counter = torch.zeros(1, dtype=torch.int32)
+    mb.moe_adamw_step(plan, counter)
+    (name, args), = library.calls
+    assert name == "moe_adamw_step" and args[1] == 0 and args[5] == counter.data_ptr() and args[7] == 256
