@@ -397,7 +397,7 @@ typedef struct moe_adamw_opts {
     double lr;    /* finite, >= 0 */
     double beta1; /* 0 <= beta < 1 */
     double beta2;
-    double eps;   /* >= 0 */
+    double eps;   /* >= 0; 0 gives NaN where v is 0, 2^-158 is the least above it */
     int64_t step; /* this step's number, from 1 (ignored with step_i32) */
     int32_t state_rounding; /* MOE_ADAMW_ROUND_*, of 8-bit states' codes */
     int32_t reserved[5]; /* must be zero */

@@ -333,7 +333,8 @@ struct Element {
     // last bit, which then is the formula's in FP32 and not a contraction's.
     // The reciprocal's unit in the last place is small against w's (it is zero
     // where sqrt(v) is beyond 2^126, which takes gradients whose square is
-    // infinite).  The decay is subtracted with the step, and w rounded once: a
+    // infinite; below 2^-126, where it would be infinite, no denominator comes:
+    // sqrt(v) is zero or above 2^-75, and eps is scaled).  The decay is subtracted with the step, and w rounded once: a
     // factor 1 - lr wd would be rounded to 2^-24, which is a tenth of an lr wd
     // of 1e-6.
     __device__ __forceinline__ float operator()(float g, float &m, float &v, float &w) const
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, kStepPerSm) adamw_kernel(const __gri
     const int64_t at = (int64_t)(chunk - b.first[k]) * kChunk;
     const float lr = (sc.lr_at ? *sc.lr_at : sc.lr) * t.lr_factor;
     const Element el{sc.beta1, sc.one_minus1, sc.beta2, sc.one_minus2, factor, -lr * t.weight_decay,
-                     -lr * corrections.x, corrections.y, sc.eps};
+                     -lr * corrections.x * sc.den_scale, corrections.y * sc.den_scale, sc.eps};
     uint32_t key = 0;
     if constexpr (RANDOM) key = Draws::mix(Draws::mix(sc.step_at ? (uint32_t)*sc.step_at : sc.step) + t.index);
     if (t.master)

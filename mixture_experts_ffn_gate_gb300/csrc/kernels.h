@@ -300,6 +300,7 @@ struct AdamWTensor {
 };
 struct AdamWScalars {
     float beta1, one_minus1, beta2, one_minus2, eps, lr;
+    float den_scale;            // a power of two that eps, and the quotient's other parts, are taken times
     float2 host;                // 1 / (1 - b1^t), 1 / sqrt(1 - b2^t)
     const float2 *corrections;  // nullable: these, in device memory
     const float *grad_scale, *lr_at;  // nullable

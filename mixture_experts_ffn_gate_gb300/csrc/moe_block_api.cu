@@ -1,5 +1,6 @@
 // moe_block_api.cu -- the C ABI of moe_block.h but for the experts' entry
 // points (moe_ffn_api.cu): argument checks and launches.  Host code only.
+#include <float.h>
 #include <math.h>
 
 #include <vector>
@@ -399,12 +400,18 @@ int moe_adamw_step(const moe_adamw_tensor *tensors, int64_t count, const moe_ada
     const int st = moe::device_info(&n_sm, &pairs);
     if (st != MOE_OK) return st;
     const double t = (double)o.step;
+    // an eps below FP32's normal numbers, alone in a denominator, would count as
+    // zero: numerator and denominator are taken times 2^32, at least 2^-126
+    const bool tiny = o.eps > 0.0 && o.eps < FLT_MIN;
+    const double den_scale = tiny ? 4294967296.0 : 1.0;
+    const double eps = tiny && o.eps * den_scale < FLT_MIN ? FLT_MIN : o.eps * den_scale;
     const moe::AdamWScalars sc{(float)o.beta1,
                                (float)(1.0 - o.beta1),
                                (float)o.beta2,
                                (float)(1.0 - o.beta2),
-                               (float)o.eps,
+                               (float)eps,
                                (float)o.lr,
+                               (float)den_scale,
                                make_float2((float)(1.0 / (1.0 - pow(o.beta1, t))),
                                            (float)(1.0 / sqrt(1.0 - pow(o.beta2, t)))),
                                nullptr,

@@ -386,3 +386,25 @@ def test_a_plan_without_weights_counts():
     assert step.item() == 4
     mb.moe_adamw_step(none, 5, lr=torch.ones(1, device="cuda"))
     assert step.item() == 4
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-38, 1e-39, 1e-44, 1e-46, 1e-60, 0.0])
+@pytest.mark.parametrize("on_device", [False, True])
+def test_an_eps_below_the_normal_numbers_is_above_zero(bits, eps, on_device):
+    """Where v is 0 it is the denominator, and m / eps is 0 with m; with eps 0
+    that is 0 / 0.  Elsewhere it does not count: a first step is lr times the
+    gradient's sign, off by the step's 16 roundings and those of w; and 1 / b
+    and 1 / sqrt(b) of the betas' complements, in FP64."""
+    n = 1000
+    w, g = torch.ones(n, device="cuda"), torch.randn(n, generator=torch.Generator().manual_seed(2)).cuda()
+    g[::2] = 0.0
+    s = mb.new_adamw_state(w, bits)
+    step = torch.zeros(1, dtype=torch.int32, device="cuda") if on_device else 1
+    mb.moe_adamw_step(mb.AdamWPlan([w], [s], grads=[g]), step, lr=0.125, eps=eps)
+    if eps:
+        assert (w[::2] == 1).all()
+    else:
+        assert torch.isnan(w[::2]).all()
+    want = 1 - 0.125 * torch.sign(g[1::2])
+    assert (w[1::2] - want).abs().max().item() <= (0.125 * 24 + 3 * 1.125) * U
