@@ -290,9 +290,9 @@ typedef struct moe_balance_opts {
  * A row of logits that are all -inf, or of sigmoids whose sum is below 2^-126,
  * has s = 0 and no z; a NaN among a row's logits, or a +inf with softmax or z,
  * makes its sequence's prob and the losses NaN.
- * Sums are FP32, in an order fixed by T, S, E and the device; the
- * probabilities are as exact as expf and a reciprocal within one unit make
- * them.  Limits: those of the gate (E <= 1024, k <= 32, T * E < 2^40,
+ * Sums are FP32, in an order fixed by T, S, E and the device; exponentials are
+ * within three units in the last place of their FP32 argument's, and a fortieth
+ * of a unit more for each whole number in it, reciprocals within one.  Limits: those of the gate (E <= 1024, k <= 32, T * E < 2^40,
  * T * k < 2^30), S in 1..2^20, finite coefficients.  T == 0
  * writes its outputs too.  workspace: at least
  * moe_balance_loss_workspace_bytes (0 for an invalid shape); it needs no

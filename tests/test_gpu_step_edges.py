@@ -59,6 +59,37 @@ def test_sigmoid_gradient_next_to_extreme_logits(value, q):
     assert ((got - want).abs() <= 200 * U * s * rest * (a + (a * s).sum()) + 1e-37).all()
 
 
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [24, 200])
+def test_probabilities_of_far_logits(kind, E):
+    """Their error does not grow with the logits.  2^y is off by two units in the
+    last place (4 U), c's product and 1 + x by U, a reciprocal by 2 U: 8 U, and
+    |l| / 20 U for ln 2's rounding; the sum over the row 13 additions, its
+    reciprocal 2 U, the product and the mean of one row 2 U: 33 U.  The largest
+    softmax logit is 0, so the differences are exact."""
+    r = np.random.default_rng(E)
+    T = 300
+    logits = r.uniform(-85, 0 if kind == "softmax" else 85, size=(T, E)).astype(np.float32)
+    logits[:, 0] = 0.0
+    idx = np.zeros((T, 1), np.int32)
+    got = mb.moe_balance_loss_forward(torch.from_numpy(logits).cuda(), torch.from_numpy(idx).cuda(), score=kind,
+                                      seq_offsets=torch.arange(T + 1, dtype=torch.int32, device="cuda"))
+    l = logits.astype(np.float64)
+    q = np.exp(l) if kind == "softmax" else 1 / (1 + np.exp(-l))
+    s = q / q.sum(1, keepdims=True)
+    bound = (34 + np.abs(l) / 20) * U * s
+    assert (np.abs(got.prob.cpu().double().numpy() - s) <= bound).all()
+    # the gradient: s again, a's products 6 U, the mean under s 50 U of its own
+    counts = r.integers(0, T, size=(1, E)).astype(np.int32)
+    d = mb.moe_balance_loss_backward(torch.from_numpy(logits).cuda(), torch.from_numpy(counts).cuda(), 1, score=kind,
+                                     coef=float(T)).cpu().double().numpy()
+    a = E * counts / float(T)
+    mean = (a * s).sum(1, keepdims=True)
+    rest = 1.0 if kind == "softmax" else 1 / (1 + np.exp(l))
+    want = s * rest * (a - mean)
+    assert (np.abs(d - want) <= (96 + np.abs(l) / 10) * U * s * rest * (a + mean) + 2.0 ** -126).all()
+
+
 def loss_in_64_bits(logits, idx, offsets, kind, coef, z_coef):
     """(loss [3], prob [S,E]) of ascending offsets from 0 to T, on the device."""
     T, E = logits.shape
