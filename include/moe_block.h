@@ -287,15 +287,17 @@ typedef struct moe_balance_opts {
  *   logits_f32 [T,E]; topk_idx int32 [T,k]; seq_offsets nullable int32 [S+1],
  *   ascending, in 0..T (others give meaningless results, but no access out of
  *   bounds); loss_f32 [3]; counts int32 [S,E]; prob_f32 [S,E]
- * A row of logits that are all -inf, or of sigmoids whose sum is below 2^-126,
- * has s = 0 and no z; a NaN among a row's logits, or a +inf with softmax or z,
- * makes its sequence's prob and the losses NaN.
+ * A row of logits that are all -inf has s = 0 and no z.  A sigmoid below 2^-126
+ * (logits below -87.3) counts as zero, and so does, in the gradient, its 1 - q
+ * there (above 87.3); a row of nothing else has s = 0 (and its z, where its logits
+ * are finite).  A NaN among a row's logits, or a +inf with softmax or z, makes its
+ * sequence's prob and the losses NaN.
  * Sums are FP32, in an order fixed by T, S, E and the device; exponentials are
  * within three units in the last place of their FP32 argument's, and a fortieth
- * of a unit more for each whole number in it, reciprocals within one.  Limits: those of the gate (E <= 1024, k <= 32, T * E < 2^40,
- * T * k < 2^30), S in 1..2^20, finite coefficients.  T == 0
- * writes its outputs too.  workspace: at least
- * moe_balance_loss_workspace_bytes (0 for an invalid shape); it needs no
+ * of a unit more for each whole number in it, reciprocals within one.  Limits:
+ * those of the gate (E <= 1024, k <= 32, T * E < 2^40, T * k < 2^30), S in
+ * 1..2^20, finite coefficients.  T == 0 writes its outputs too.  workspace: at
+ * least moe_balance_loss_workspace_bytes (0 for an invalid shape); it needs no
  * initial content.
  */
 size_t moe_balance_loss_workspace_bytes(int64_t T, int64_t S, int64_t E);
@@ -346,9 +348,10 @@ typedef struct moe_tensor {
  * Squares are summed in FP32 within a block and in FP64 over the blocks, in an
  * order fixed by the tensors' sizes and the device.  A sum beyond FP32's range is
  * taken of the elements times 2^-64, so the norm holds up to FP32's largest;
- * elements below about 1e-22 count as zero.  Limits: count <= 65536, sum of n
- * <= 2^42.  Without elements the norm is 0 and the factor 1.  workspace: at
- * least moe_grad_norm_workspace_bytes(count), no initial content.
+ * elements below about 1e-19 lose bits of their squares, and below 1e-22 count as
+ * zero.  Limits: count <= 65536, sum of n <= 2^42.  Without elements the norm is 0
+ * and the factor 1.  workspace: at least moe_grad_norm_workspace_bytes(count), no
+ * initial content.
  */
 size_t moe_grad_norm_workspace_bytes(int64_t count);
 int moe_grad_norm(const moe_tensor *grads, int64_t count, float max_norm, float *out_f32,
@@ -361,13 +364,14 @@ int moe_grad_norm(const moe_tensor *grads, int64_t count, float max_norm, float 
  * A tensor of an AdamW step: n elements, contiguous, all updated in place.
  *   w       w_type; with `master` (FP32, nullable) the master is the weight and
  *           w takes its rounding.  A BF16 weight without one is rounded to
- *           nearest after every step: steps below 2^-9 of it can leave it as
- *           it is
+ *           nearest after every step: steps below 2^-8 of it can leave it as
+ *           it is (half a spacing is 2^-9 to 2^-8 of it)
  *   grad    grad_type, read
  *   m, v    the moments: state_bits 32: FP32.  state_bits 8: E4M3 codes of
  *           m / m_scale and of sqrt(v) / v_scale, one FP32 scale per
  *           MOE_ADAMW_STATE_BLOCK elements (the last block may be shorter):
- *           the block's largest magnitude / 448, at least 2^-126.  Codes are
+ *           the block's largest magnitude times the rounded 1 / 448, at least
+ *           2^-126.  Codes are
  *           rounded as state_rounding says, but a v above zero takes at
  *           least the lowest code.  The step computes with the values before
  *           they are rounded.  Zeros (of codes and scales) are the initial

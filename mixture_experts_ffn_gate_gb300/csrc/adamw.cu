@@ -3,7 +3,7 @@
 //
 //   norm = sqrt(sum g^2), factor = min(1, max / norm)
 //   g' = factor g;  m = b1 m + (1 - b1) g';  v = b2 v + (1 - b2) g'^2
-//   w = w (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
+//   w = w - (lr wd w + lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps))
 //
 // The tensors' addresses and sizes travel in the kernel's parameters, up to
 // 256 (512) of them per launch, so a call copies nothing to the device first and
@@ -19,11 +19,11 @@
 // tensors leave chunks part empty (192 of 501 to 261522 elements: 53, 45).
 //
 // 8-bit states: E4M3 codes of m / scale and sqrt(v) / scale, with one FP32
-// scale per 256 elements, the largest magnitude / 448.  A floating code keeps
-// small elements to 2^-4 of their size next to large ones; the scale is FP32
-// and not a power of two because the largest element then is its own code
-// times the scale exactly: elements that get no gradient decay by the factor
-// b1 or b2 through it, where a rounded scale would hold them where they are.
+// scale per 256 elements, the largest magnitude times the rounded 1 / 448.  A
+// floating code keeps small elements to 2^-4 of their size next to large ones.
+// The scale is FP32 and not a power of two because it then follows the largest
+// element, whose code stays 448, to a rounding: a block without gradients decays
+// by the factor b1 or b2 through it, where a rounded scale would hold it.
 // sqrt(v) needs half of v's range, and one that is not zero takes at least
 // the lowest code, so that no m is divided by eps alone.  Codes are rounded to
 // nearest, or at random where the betas are so close to 1 that a step changes a

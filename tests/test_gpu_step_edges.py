@@ -90,6 +90,41 @@ def test_probabilities_of_far_logits(kind, E):
     assert (np.abs(d - want) <= (96 + np.abs(l) / 10) * U * s * rest * (a + mean) + 2.0 ** -126).all()
 
 
+@pytest.mark.parametrize("T", [20, 400])
+def test_rows_of_sigmoids_below_the_normal_numbers(T):
+    """Each counts as zero, so a row of nothing else has no probability and no
+    gradient of the balance, but the z of its finite logits."""
+    r = np.random.default_rng(T)
+    logits = r.normal(size=(T, 40)).astype(np.float32)
+    logits[3], logits[5], logits[7] = -88.0, -88.0, -float("inf")
+    logits[5, 11] = 0.0
+    idx = np.argsort(-logits, axis=1, kind="stable")[:, :4].astype(np.int32)
+    how = dict(score="sigmoid", coef=0.5, z_coef=0.25)
+    got = mb.moe_balance_loss_forward(torch.from_numpy(logits).cuda(), torch.from_numpy(idx).cuda(), **how)
+    l = logits.astype(np.float64)
+    q = np.where(l < -87.5, 0.0, 1 / (1 + np.exp(-l.clip(-500))))
+    total = q.sum(1, keepdims=True)
+    s = np.divide(q, total, out=np.zeros_like(q), where=total > 0)
+    prob = s.mean(0)
+    rel = (ref.row_error(logits[0], 40) + (T / 8 + 100) * U)
+    assert (np.abs(got.prob.cpu().double().numpy()[0] - prob) <= rel * prob).all()
+    top = l.max(1, keepdims=True, initial=-1e300)
+    e = np.where(np.isfinite(l), np.exp(l - top), 0.0)
+    lse = np.where(np.isfinite(top[:, 0]) & (e.sum(1) > 0), top[:, 0] + np.log(np.maximum(e.sum(1), 1e-300)), 0.0)
+    assert lse[7] == 0 and abs(lse[3] + 88 - np.log(40)) < 1e-9
+    z = (lse ** 2).mean()
+    # a logarithm's error, twice over in the square, of lse up to 88
+    assert abs(got.loss[2].item() - z) <= (2 * 88 * (rel + 4 * U * 88) + rel * 88 * 88) * 2 / T + rel * z
+    counts = np.bincount(idx.ravel(), minlength=40)[None]
+    assert np.array_equal(got.counts.cpu().numpy(), counts)
+    d = mb.moe_balance_loss_backward(torch.from_numpy(logits).cuda(), got.counts, 4, **how).cpu().double().numpy()
+    want = 2 * 0.25 / T * lse[:, None] * np.divide(e, e.sum(1, keepdims=True), out=np.zeros_like(e),
+                                                   where=e.sum(1, keepdims=True) > 0)
+    assert (d[7] == 0).all()
+    assert (np.abs(d[3] - want[3]) <= 2 * (ref.row_error(logits[3], 40) + 4 * U) * np.abs(want[3])).all()
+    assert np.isfinite(d).all() and (np.abs(d[5, 12:] - want[5, 12:]) <= 1e-30).all()
+
+
 def loss_in_64_bits(logits, idx, offsets, kind, coef, z_coef):
     """(loss [3], prob [S,E]) of ascending offsets from 0 to T, on the device."""
     T, E = logits.shape
