@@ -14,6 +14,7 @@ import bisect
 import ctypes
 import functools
 import math
+import operator
 from typing import NamedTuple
 
 import torch
@@ -242,7 +243,7 @@ class GateOutput(NamedTuple):
 # The structs of a few settings are kept by the settings' values: a tensor among
 # them is read at every call, since a cache would take it by its identity.
 def _gate_opts(score, renormalize, scale, groups=1, topk_groups=1):
-    return _kept_gate_opts(score, bool(renormalize), float(scale), int(groups), int(topk_groups))
+    return _kept_gate_opts(score, bool(renormalize), float(scale), operator.index(groups), operator.index(topk_groups))
 
 
 @functools.lru_cache(maxsize=64)

@@ -72,6 +72,9 @@ def test_settings_that_are_tensors_are_read_at_every_call():
     for value in (2, 4):
         groups.fill_(value)
         assert mb._gate_opts("softmax", True, 1.0, groups, 1)._obj.groups == value
+    for groups, topk_groups in ((2.5, 1), (2, 1.0), ("2", 1)):
+        with pytest.raises(TypeError):
+            mb._gate_opts("softmax", True, 1.0, groups, topk_groups)
 
 
 def test_the_rounding_of_8_bit_states(monkeypatch, on_host):
