@@ -442,7 +442,8 @@ typedef struct moe_adamw_opts {
  *   lr_f32         nullable device [1]: in the place of opts->lr
  *   step_i32       nullable device [1]: the number of steps taken so far; the
  *                  call adds one, unless the step is left out.  With it (and
- *                  lr_f32) a captured graph's replays are successive steps.
+ *                  lr_f32) a captured graph's replays are successive steps;
+ *                  without it they repeat one, what it draws for 8-bit states too.
  *   workspace      with step_i32: at least 256 bytes, else nullable
  * Arithmetic in FP32 but for the corrections by the betas' powers (FP64).
  * Limits: count <= 65536, sum of n <= 2^42.

@@ -390,10 +390,12 @@ int moe_adamw_step(const moe_adamw_tensor *tensors, int64_t count, const moe_ada
     auto list = list_of<moe::AdamWTensor>(count);
     if ((int64_t)list.size() != count) return MOE_ERR_NO_MEMORY;
     int64_t total = 0;
+    bool bits8 = false;
     for (int64_t i = 0; i < count; ++i) {
         int st = check_adamw_tensor(tensors[i], (uint32_t)i, &list[(size_t)i]);
         if (st == MOE_OK) st = add_elements(tensors[i].n, &total);
         if (st != MOE_OK) return st;
+        bits8 |= tensors[i].state_bits == 8;
     }
     if (count == 0 && !step_i32) return MOE_OK;
     int n_sm, pairs;
@@ -421,7 +423,8 @@ int moe_adamw_step(const moe_adamw_tensor *tensors, int64_t count, const moe_ada
                                nullptr};
     const bool random = o.state_rounding == MOE_ADAMW_ROUND_AUTO ? o.beta1 > kMostNearest || o.beta2 > kMostNearest
                                                                  : o.state_rounding == MOE_ADAMW_ROUND_RANDOM;
-    return moe::launch_adamw(list.data(), (int)count, sc, o.beta1, o.beta2, step_i32, random, workspace, stream) == cudaSuccess
+    return moe::launch_adamw(list.data(), (int)count, sc, o.beta1, o.beta2, step_i32, random && bits8, workspace, stream) ==
+                   cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
 }
