@@ -49,6 +49,10 @@ constexpr int kOneBlockTurns = 4, kOneBlockRows = 512, kOneBlockSequences = 3;
 // Warps per block and rows of a warp in flight, by what the registers hold
 // with two blocks on an SM.  Few large blocks: every one adds a slot that the
 // second kernel reads (131072 x 256: 34.4 us with four blocks of 8 warps).
+// Softmax, us, as it is, with fewer warps, with more: 256 experts 30.6, 33.7 (8
+// warps), 31.0 (12); 512 30.4, 33.1 (8), 32.6 (16); 1000 29.8, 34.6 (4), 46.8 (12).
+// Half the rows in flight: 128 experts 38.8 (35.0), 256 35.2 (30.6), but 64 29.9
+// (33.3); twice as many: 256 49, 512 40, 1000 53.
 constexpr int kPerSm = 2;
 
 template <int PER>
@@ -62,7 +66,10 @@ struct RowShape {
 constexpr int kSumBlocksPerSm = 20, kSumWarpsPerSm = 32;
 
 // The gradient's blocks add nothing up and are smaller; a warp has fewer rows
-// in flight, for each brings the incoming gradient along.
+// in flight, for each brings the incoming gradient along.  Blocks per SM, one
+// less and one more (softmax, us, the logits' bytes alike): 256 experts 65, 63.6
+// and 72; 384 65.8, 65.5 and 67; 768 59.4, 66 and 70; 1000 63, 66 and 84; sigmoid at
+// 512 66.1, 78 and 67.
 constexpr int kGradWarps = 8;
 
 template <int PER>
@@ -137,18 +144,18 @@ __device__ __forceinline__ float reciprocal(float x)
 }
 
 // exp(x), x <= 88: 2^y by the hardware (two units in the last place, zero below
-// 2^-126), y = x log2 e rounded, times 1 + c for what the rounding took: c =
-// x - y ln 2 is below 1e-5, and exact but for y times the rounding of ln 2, 2e-9.
+// 2^-126), y = x log2 e rounded down, times 1 + c for what the rounding took: c =
+// x - y ln 2 is in [0, 1e-5], exact but for y times the rounding of ln 2, 2e-9.
 // In all within three units and |x| / 40 of one, where without c it is |x|; a NaN
-// of a NaN.  It costs the loss nothing where DRAM bounds it (131072 x 256, sigmoid
-// or softmax, 31.0 and 31.3 us, 30.4 and 30.1 without c; sigmoid and z 45.8, 39.6);
-// with ln 2 in two parts 31.6, 32.1 and 47.9.
+// of a NaN.  Saturation makes c of an infinity, which is none, zero.
+// 131072 x 256: sigmoid 30.7 us, softmax 30.9, sigmoid and z 43.8; without c 30.4,
+// 30.1 and 39.6; with ln 2 in two parts and a clamp of x instead 31.6, 32.1, 47.9.
 __device__ __forceinline__ float exp_to_88(float x)
 {
     constexpr float log2e = 1.4426950408889634f, ln2 = 0.6931471805599453f;
-    float e;
-    asm("max.NaN.f32 %0, %0, 0fC3000000;" : "+f"(x));  // -128: an infinity has no c
-    const float y = x * log2e, c = fmaf(-y, ln2, x);
+    const float y = __fmul_rd(x, log2e);
+    float e, c;
+    asm("fma.rn.sat.f32 %0, %1, %2, %3;" : "=f"(c) : "f"(-y), "f"(ln2), "f"(x));
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y));
     return fmaf(e, c, e);
 }
@@ -265,25 +272,6 @@ __device__ __forceinline__ void sigmoids(const float (&l)[ROWS][PER], int lpr, f
     }
     row_sum(total, lpr);
 }
-
-// For the gradient: of q = 1 / (1 + exp(-l)) and 1 - q the one that is not above
-// a half, negative where that is 1 - q.  A difference of q from one would
-// lose it for large logits (17% of it at 15, all of it from 17 on).
-template <int PER, int ROWS>
-__device__ __forceinline__ void small_sides(const float (&l)[ROWS][PER], float (&side)[ROWS][PER])
-{
-#pragma unroll
-    for (int u = 0; u < ROWS; ++u)
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const float x = exp_to_88(-fabsf(l[u][i]));  // q / (1 - q) or its inverse
-            side[u][i] = copysignf(x * reciprocal(1.0f + x), -l[u][i]);
-        }
-}
-
-// q of such a side, and q (1 - q).
-__device__ __forceinline__ float sigmoid_of(float side) { return signbit(side) ? 1.0f + side : side; }
-__device__ __forceinline__ float slope_of(float side) { return fmaf(-side, side, fabsf(side)); }
 
 template <int PER, int ROWS>
 __device__ __forceinline__ void copy_rows(const float (&from)[ROWS][PER], float (&to)[ROWS][PER])
@@ -584,17 +572,24 @@ __global__ void __launch_bounds__(1024, 1) balance_sum_kernel(const BalanceArgs 
 // ---------------------------------------------------------------- gradient
 // The scores are computed again from the logits.  Rows of no sequence take
 // the gradient that comes in, or zero, whatever their logits hold.  Bound by
-// DRAM: 131072 x 256 with 37 sequences and an incoming gradient 64.7 us (floor
-// at the copy rate 59.3), without one 45.1 (39.5); 100000 x 128, softmax and
-// z, 27.9 (22.6).  The incoming gradient loaded with the logits instead of
-// after them, and one row of a warp in flight instead of two: 34.7 to 27.9,
-// 65.7 to 64.7.  The sigmoid's smaller side and its sign instead of q alone:
-// 131072 x 256 as before, 100000 x 128 with z 33.1 to 35.3, 32768 x 1000 with an
-// incoming gradient 64.8 to 68.5 (these two are bound by instructions).
+// DRAM: 131072 x 256 with 37 sequences and an incoming gradient 62.5 us (floor
+// at the copy rate 59.3), without one 44.7 (39.5); 100000 x 128, softmax and
+// z, 25.7 (22.6).  One row of a warp in flight from 129 experts on, two below:
+// two of 256 logits 73.7 where one takes 62.4, one of 128 54.8 (50.0).  Sigmoid
+// and z, three exponentials and reciprocals a logit, is bound by instructions:
+// 200000 x 128 60 (45), 32768 x 1000 75 (58).
+//
+// Wide rows fill the registers, and the compiler then loads them bit by bit as
+// it works.  The warp's barrier after the loads keeps them together (32768 x
+// 1000, softmax: 70.8 to 62.9).  For sigmoids, whose work on one logit waits for
+// no other, it did not; there the incoming gradient is loaded at the end, from
+// L2, where its row is fetched to meanwhile (40000 x 768: 86 to 60.5).  With z the
+// next row's logits are fetched there (67.5 to 61.3).
 template <int PER, bool VEC, Kind KIND>
 __global__ void __launch_bounds__(32 * kGradWarps, GradShape<PER>::PER_SM) balance_grad_kernel(const BalanceGradArgs a)
 {
     constexpr int ROWS = GradShape<PER>::ROWS, WARPS = kGradWarps;
+    constexpr bool LATE = PER > 8 && KIND == kSigmoid;  // the incoming gradient is loaded at the end
     __shared__ int32_t kept[kCached];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int E = a.E, T = a.T, S = a.S;
@@ -614,6 +609,9 @@ __global__ void __launch_bounds__(32 * kGradWarps, GradShape<PER>::PER_SM) balan
             load_row<PER, VEC>(a.base + (int64_t)t * E, a.base != nullptr, E, sub, lpr, 0.0f, v);
             store_row<PER, VEC>(a.out + (int64_t)t * E, E, sub, lpr, v);
         }
+    };
+    auto fetch = [&](const float *row) {  // of a warp's row, to L2: a lane for each 128 bytes
+        if (lane * 32 < E) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + lane * 32));
     };
     int row = blockIdx.x * a.chunk;
     const int end = (int)min((int64_t)T, (int64_t)row + a.chunk);
@@ -637,9 +635,13 @@ __global__ void __launch_bounds__(32 * kGradWarps, GradShape<PER>::PER_SM) balan
             for (int u = 0; u < ROWS; ++u) {
                 const int t = at + u * WARPS * rows_per_warp + group;
                 load_row<PER, VEC>(a.logits + (int64_t)t * E, t < hi, E, sub, lpr, -INFINITY, l[u]);
-                load_row<PER, VEC>(a.base + (int64_t)t * E, a.base != nullptr && t < hi, E, sub, lpr, 0.0f, base[u]);
+                if (!LATE)
+                    load_row<PER, VEC>(a.base + (int64_t)t * E, a.base != nullptr && t < hi, E, sub, lpr, 0.0f, base[u]);
                 lse[u] = 0.0f;
             }
+            if (PER > 8 && KIND == kSigmoidAndZ && at + WARPS < hi) fetch(a.logits + (int64_t)(at + WARPS) * E);
+            if (LATE && a.base != nullptr) fetch(a.base + (int64_t)at * E);
+            __syncwarp();
             float d[ROWS][PER];
             if constexpr (KIND != kSigmoid) {
                 exponentials<PER, ROWS>(l, lpr, p, top, total);
@@ -650,20 +652,25 @@ __global__ void __launch_bounds__(32 * kGradWarps, GradShape<PER>::PER_SM) balan
 #pragma unroll
                     for (int q = 0; q < PER; ++q) {
                         p[u][q] *= inv;
-                        d[u][q] = lse[u] * p[u][q];
+                        // with the sigmoids still to come the incoming gradient joins here
+                        d[u][q] = KIND == kSigmoidAndZ ? fmaf(lse[u], p[u][q], base[u][q]) : lse[u] * p[u][q];
                     }
                 }
             }
             if constexpr (KIND != kSoftmax) {
-                small_sides<PER, ROWS>(l, p);
+                // p: q (1 - q), of x = exp(-|l|), which is q / (1 - q) or its
+                // inverse.  A difference of q from one would lose it for large
+                // logits (17% of it at 15, all of it from 17 on).
 #pragma unroll
                 for (int u = 0; u < ROWS; ++u) {
                     mean[u] = total[u] = 0.0f;
 #pragma unroll
                     for (int q = 0; q < PER; ++q) {
-                        const float s = sigmoid_of(p[u][q]);
+                        const float x = exp_to_88(-fabsf(l[u][q])), r = reciprocal(1.0f + x), xr = x * r;
+                        const float s = l[u][q] < 0.0f ? xr : r;
                         total[u] += s;
                         mean[u] = fmaf(share[q], s, mean[u]);
+                        p[u][q] = xr * r;
                     }
                 }
                 row_sum(total, lpr);
@@ -674,7 +681,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, GradShape<PER>::PER_SM) balan
                     mean[u] *= inv;
 #pragma unroll
                     for (int q = 0; q < PER; ++q) {
-                        const float g = (share[q] - mean[u]) * inv * slope_of(p[u][q]);
+                        const float g = (share[q] - mean[u]) * inv * p[u][q];
                         d[u][q] = KIND == kSigmoidAndZ ? d[u][q] + g : g;
                     }
                 }
@@ -695,8 +702,10 @@ __global__ void __launch_bounds__(32 * kGradWarps, GradShape<PER>::PER_SM) balan
             for (int u = 0; u < ROWS; ++u) {
                 const int t = at + u * WARPS * rows_per_warp + group;
                 if (t >= hi) continue;
+                if (LATE) load_row<PER, VEC>(a.base + (int64_t)t * E, a.base != nullptr, E, sub, lpr, 0.0f, base[u]);
 #pragma unroll
-                for (int q = 0; q < PER; ++q) d[u][q] += base[u][q];
+                for (int q = 0; q < PER; ++q)
+                    if (KIND != kSigmoidAndZ) d[u][q] += base[u][q];
                 store_row<PER, VEC>(a.out + (int64_t)t * E, E, sub, lpr, d[u]);
             }
         }
