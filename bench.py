@@ -28,7 +28,7 @@ of the layer the metric names (the 2048-hidden decode layer at T=2, the
 4096-hidden one at T=1/4/16/64, the 7168-hidden one at T=1/8/32 and the
 T=2048 training-size forward) is measured the same way, W warm-up and K
 timed steps each over its own layers' weights drawn on the GPU, and reported
-in the line's "supplementary" array: us per call, tokens/s, the whole
+in the details' "supplementary" array: us per call, tokens/s, the whole
 call's HBM fraction, the dominant kernel's roofline and the TFLOP/s against
 dense BF16 peak and against min(peak, HBM peak x flop/byte).  Two of the
 rows ("entry": moe_ffn_forward_router) run the 2048-hidden decode layer at
@@ -43,6 +43,10 @@ every call), with its own byte model (backward_bytes) and 16 H I T k flops.
 One row ("entry": moe_ffn_forward_train + moe_ffn_backward_train) runs a
 training step of that layer: the forward pass keeping g and u, then the
 backward pass reading them (byte model train_bytes, 18 H I T k flops).
+
+stdout has one JSON line, the headline's figures, kept short enough for what
+reads only the end of a program's output; stderr has another before it with the
+details (rooflines, cold calls, stages, baseline, the other configurations).
 
 --impl reference times the FP64 CPU oracle on this machine's host cores on a
 bounded sample of the same workload (it is the slow baseline, not a target).
@@ -117,6 +121,29 @@ def parse():
                    help="expert weight format of the headline line (mxfp8: moe_ffn_forward_mxfp8, "
                         "one to four tokens; no e2e or CPU-baseline figures)")
     return p.parse_args()
+
+
+# What the line on stdout has, of at most LINE_CHARS: a record of a run that
+# keeps the last 1500 characters of its output still has all of it.
+LINE_KEYS = ("metric", "value", "unit", "n_gpus", "steps", "warmup", "ms_per_step", "higher_is_better", "scaling",
+             "vs_baseline", "dtype", "data", "config", "e2e", "gpu_launches", "clocks")
+LINE_CHARS = 1400
+
+
+def split_line(line):
+    """(the line on stdout, the details)."""
+    short = {k: line[k] for k in LINE_KEYS if k in line}
+    short["config"] = {k: v for k, v in line["config"].items() if k != "timing"}
+    details = {k: v for k, v in line.items() if k not in LINE_KEYS}
+    if "timing" in line["config"]:
+        details["timing"] = line["config"]["timing"]
+    return short, details
+
+
+def print_line(line):
+    short, details = split_line(line)
+    print(json.dumps({"details": details}), file=sys.stderr, flush=True)
+    print(json.dumps(short), flush=True)
 
 
 def rank_calls(rank, W, K):
@@ -416,7 +443,7 @@ def cpu_model():
 
 # Every other configuration the metric names, measured by the same command
 # after the headline line: a short timed run each (weights drawn on the GPU,
-# no oracle timing), reported in the line's "supplementary" array.
+# no oracle timing), reported in the details' "supplementary" array.
 SUPPLEMENTARY = [
     ("decode_h2048_i768_e128_k8", (2,)),
     ("decode_h2048_i768_e128_k8+router", (1, 2)),
@@ -937,7 +964,7 @@ def main():
         del run, layers, wgu, wd, flush
         torch.cuda.empty_cache()
         line["supplementary"] = supplementary_rows(args, dev, peaks, skip=(wl.name, T))
-    print(json.dumps(line), flush=True)
+    print_line(line)
     if world > 1:
         dist.destroy_process_group()
 
