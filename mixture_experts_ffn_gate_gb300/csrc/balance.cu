@@ -23,8 +23,8 @@
 // sum, the release to the block that ends last): 32 us in all.  Without the
 // hardware's exponentials the first kernel's instructions took longer than its
 // bytes; with the slots counted before the rows instead of between them it
-// waited for them (40 us).  8191 x 128 with z: 10.2 us, of which the second
-// kernel 5.5.
+// waited for them (40 us).  8191 x 128 with z: 9.8 us, of which the second
+// kernel about 5.
 #include <type_traits>
 
 #include "common.cuh"
