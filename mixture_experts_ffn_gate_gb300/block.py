@@ -164,18 +164,18 @@ class MoeBlock:
             g, w = grads[name], getattr(self, name)
             _, M, N = g.shape
             step = mb.moe_orthogonalize(g, out_scale=-lr * math.sqrt(max(1.0, M / N)))
-            w.add_(step if factor is None else _unless_finite(factor, step))
+            w.add_(step if factor is None else _if_finite(factor, step))
 
     def update_bias(self, grads, rate: float, factor=None):
         """The balance bias against the loads; ``factor`` as in update_experts."""
         if self.balance_bias is not None and rate:
             loads = grads["loads"].float()
             step = torch.sign(loads.mean() - loads).mul_(rate)
-            self.balance_bias.add_(step if factor is None else _unless_finite(factor, step))
+            self.balance_bias.add_(step if factor is None else _if_finite(factor, step))
 
 
-def _unless_finite(factor, step):
-    """The step, or where the factor f32 [1] is no finite number -0.0, which
+def _if_finite(factor, step):
+    """The step if the factor f32 [1] is a finite number, else -0.0, which
     added to any number leaves it: decided on the device."""
     return step.masked_fill_(~torch.isfinite(factor), -0.0)
 
